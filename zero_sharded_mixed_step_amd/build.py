@@ -1,4 +1,5 @@
-"""Build libzero_step.so (the HIP kernels and the C ABI) for gfx950, in-tree.
+"""Build libzero_step.so (the HIP kernels and the C ABI) and libzero_ops.so (the
+training operators) for gfx950, in-tree.
 
 Floating-point flags are part of the contract: no contraction of a*b+c into
 fma unless written, IEEE-correct binary32 division and square root, denormals
@@ -28,6 +29,12 @@ FLAGS = [
 PATTERNS_LIB = os.path.join(HERE, "libzs_patterns.so")
 PATTERNS_SOURCES = [os.path.join(HERE, "csrc", "zs_patterns.hip")]
 
+# The training operators (include/zero_ops.h).
+OPS_LIB = os.path.join(HERE, "libzero_ops.so")
+OPS_SOURCES = [os.path.join(HERE, "csrc", f)
+               for f in ("zo_abi.hip", "zo_norm.hip", "zo_attn_fwd.hip", "zo_attn_bwd.hip",
+                         "zo_distill.hip")]
+
 
 def _compile(sources, out, defines, verbose):
     """Compiles `sources` into `out`, and writes the compiler's per-kernel
@@ -56,11 +63,18 @@ RESOURCES = ".resources.txt"
 
 
 def build(verbose: bool = False, out: str = LIB, defines=(), patterns: bool = True) -> str:
-    """libzero_step.so (and, unless patterns=False, libzs_patterns.so)."""
+    """libzero_step.so and libzero_ops.so (and, unless patterns=False,
+    libzs_patterns.so)."""
     _compile(SOURCES, out, defines, verbose)
+    build_ops(verbose)
     if patterns:
         _compile(PATTERNS_SOURCES, PATTERNS_LIB, (), verbose)
     return out
+
+
+def build_ops(verbose: bool = False) -> str:
+    """libzero_ops.so alone."""
+    return _compile(OPS_SOURCES, OPS_LIB, (), verbose)
 
 
 if __name__ == "__main__":

@@ -1,0 +1,417 @@
+// zo_attn_fwd.hip -- attention, forward: one pass over the keys with the
+// running maximum and sum of the softmax.
+//
+// A workgroup owns 128 queries of one head, 32 to a wave, whose q fragments
+// stay in registers; tiles of 64 keys and values are staged in shared memory
+// (the next tile's global loads are in flight while this one is used).  Per
+// tile a wave forms S^T = K Q^T, updates its statistics and adds V^T P^T to
+// the output accumulators.
+#include "zo_attn.h"
+#include "zo_internal.h"
+
+namespace zo {
+
+template <int D, bool CAP, bool BIAS, bool SPLIT>
+__global__ __launch_bounds__(kAttnThreads) void attn_fwd_kernel(const AttnParams p) {
+  constexpr int P = kPitch<D>;
+  constexpr int kRows = 32 * kWaves;
+  extern __shared__ __align__(16) char smem[];
+  bf16* kt = reinterpret_cast<bf16*>(smem);           // [2][kTile][P]
+  bf16* vt = kt + 2 * kTile * P;                      // [2][kTile][P]
+  int* hull = reinterpret_cast<int*>(vt + 2 * kTile * P);   // [kWaves][2]
+  float* bias = reinterpret_cast<float*>(hull + 2 * kWaves);
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5;
+  const int bh = blockIdx.x, b = bh / p.Hq, h = bh % p.Hq;
+  const int hk = h / p.group;
+  const int tile = gridDim.y - 1 - blockIdx.y;        // the longest rows of a causal mask first
+  const int i0 = tile * kRows + wave * 32;
+  const int i = i0 + (lane & 31);
+
+  const int2 rng = key_range(p, b, i);
+  const int2 wh = wave_hull(rng);
+  if (lane == 0) {
+    hull[2 * wave] = wh.x;
+    hull[2 * wave + 1] = wh.y;
+  }
+  if constexpr (BIAS) stage_bias(p, h, bias, tid);
+
+  bf16x8 qf[D / 16];
+  {
+    const bf16* q = p.q + b * p.qs.b + static_cast<int64_t>(min(i, p.Tq - 1)) * p.qs.t + h * p.qs.h;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) qf[c] = load8(q + 16 * c + 8 * half);
+  }
+  __syncthreads();
+  int first = 0x7FFFFFFF, last = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    first = min(first, hull[2 * w]);
+    last = max(last, hull[2 * w + 1]);
+  }
+  if (first > last) first = last;
+  int k0 = first & ~(kTile - 1), kend = last;
+  if constexpr (SPLIT) {
+    k0 = max(k0, static_cast<int>(blockIdx.z) * p.tiles_per_split * kTile);
+    kend = min(kend, (static_cast<int>(blockIdx.z) + 1) * p.tiles_per_split * kTile);
+  }
+
+  const bf16* kg = p.k + b * p.ks.b + hk * p.ks.h;
+  const bf16* vg = p.v + b * p.vs.b + hk * p.vs.h;
+  const float c2 = CAP ? p.cap * kLog2e : 0.f;
+  const float a = CAP ? 2.f * p.scale * kLog2e / p.cap : p.scale * kLog2e;
+
+  f32x16 acc[D / 32];
+#pragma unroll
+  for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[t][r] = 0.f;
+  float m = kLowest, l = 0.f;
+
+  Stage<D> sk, sv;
+  if (k0 < kend) {
+    sk.load(kg, p.ks.t, k0, first, last, tid);
+    sv.load(vg, p.vs.t, k0, first, last, tid);
+    sk.store(kt, tid);
+    sv.store(vt, tid);
+  }
+  __syncthreads();
+  int buf = 0;
+  for (; k0 < kend; k0 += kTile, buf ^= 1) {
+    const bool more = k0 + kTile < kend;
+    if (more) {
+      sk.load(kg, p.ks.t, k0 + kTile, first, last, tid);
+      sv.load(vg, p.vs.t, k0 + kTile, first, last, tid);
+    }
+    const bf16* kb = kt + buf * kTile * P;
+    const bf16* vb = vt + buf * kTile * P;
+    if (wh.x < k0 + kTile && wh.y > k0) {             // a row of this wave sees some of the tile
+      float s[2][16];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        f32x16 x;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x[r] = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) x = mfma(frag_rows<P>(kb, 32 * t, 16 * c, lane), qf[c], x);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[t][r] = score2<CAP>(x[r], a, c2);
+      }
+      if constexpr (BIAS) {
+        const int d0 = k0 - (i0 + p.off);             // distances span d0 - 31 .. d0 + 63
+        if (d0 + kTile - 1 <= -p.reach || d0 - 31 >= p.reach) {
+          const float c = bias[d0 <= -p.reach ? 0 : 2 * p.reach];
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[t][r] += c;
+        } else {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const int d = k0 + 32 * t + result_row(r, lane) - (i + p.off);
+              s[t][r] += bias[min(max(d, -p.reach), p.reach) + p.reach];
+            }
+        }
+      }
+      uint32_t keep[4] = {0xFFu, 0xFFu, 0xFFu, 0xFFu};  // per 16 keys
+      if (!__all(rng.x <= k0 && rng.y >= k0 + kTile)) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) keep[g] = 0;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int j = k0 + 32 * t + result_row(r, lane);
+            const bool seen = j >= rng.x && j < rng.y;
+            s[t][r] = seen ? s[t][r] : -kInf;
+            keep[2 * t + (r >> 3)] |= any_in_half(seen, lane) << (r & 7);
+          }
+      }
+      float mx = s[0][0];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[t][r]);
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      const float mn = fmaxf(m, mx);
+      if (__any(mn > m)) {
+        const float f = exp2_hw(m - mn);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[t][r] *= f;
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          s[t][r] = exp2_hw(s[t][r] - m);
+          l += s[t][r];
+        }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const bf16x8 pf = to_frag(&s[g >> 1][8 * (g & 1)]);
+#pragma unroll
+        for (int t = 0; t < D / 32; ++t) {
+          bf16x8 vf = frag_cols<P>(vb, 16 * g, 32 * t, lane);
+          if (keep[g] != 0xFFu) vf = keep_frag(vf, keep[g]);
+          acc[t] = mfma(vf, pf, acc[t]);
+        }
+      }
+    }
+    if (more) {
+      sk.store(kt + (buf ^ 1) * kTile * P, tid);
+      sv.store(vt + (buf ^ 1) * kTile * P, tid);
+    }
+    __syncthreads();
+  }
+
+  l += __shfl_xor(l, 32);
+  if (i >= p.Tq) return;
+  const int64_t row = static_cast<int64_t>(bh) * p.Tq + i;
+  if constexpr (SPLIT) {
+    const int64_t rows = static_cast<int64_t>(p.B) * p.Hq * p.Tq;
+    float* out = p.osplit + (blockIdx.z * rows + row) * D;
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; r += 4) {
+        const f32x4 x = {acc[t][r], acc[t][r + 1], acc[t][r + 2], acc[t][r + 3]};
+        *reinterpret_cast<f32x4*>(out + 32 * t + result_row(r, lane)) = x;
+      }
+    if (half == 0) {
+      float* st = p.osplit + p.splits * rows * D + 2 * (blockIdx.z * rows + row);
+      st[0] = m;
+      st[1] = l;
+    }
+  } else {
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);     // NaN stays NaN
+    bf16* o = p.o + b * p.os.b + static_cast<int64_t>(i) * p.os.t + h * p.os.h;
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; r += 4) {
+        bf16x4 x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = static_cast<bf16>(acc[t][r + e] * inv);
+        *reinterpret_cast<bf16x4*>(o + 32 * t + result_row(r, lane)) = x;
+      }
+    if (half == 0) p.lse[row] = l == 0.f ? -kInf : (m + log2_hw(l)) * kLn2;
+  }
+}
+
+// Joins the parts of split rows: a wave to a row.
+template <int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(const AttnParams p) {
+  const int64_t rows = static_cast<int64_t>(p.B) * p.Hq * p.Tq;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (row >= rows) return;
+  const float* st = p.osplit + p.splits * rows * D;
+  float m = kLowest;
+  for (int z = 0; z < p.splits; ++z) m = fmaxf(m, st[2 * (z * rows + row)]);
+  float l = 0.f, x[(D + 63) / 64];
+#pragma unroll
+  for (int c = 0; c < (D + 63) / 64; ++c) x[c] = 0.f;
+  for (int z = 0; z < p.splits; ++z) {
+    const float f = exp2_hw(st[2 * (z * rows + row)] - m);
+    l += f * st[2 * (z * rows + row) + 1];
+#pragma unroll
+    for (int c = 0; c < (D + 63) / 64; ++c)
+      if (lane + 64 * c < D) x[c] += f * p.osplit[(z * rows + row) * D + lane + 64 * c];
+  }
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  const int64_t bh = row / p.Tq;
+  const int i = static_cast<int>(row % p.Tq);
+  bf16* o = p.o + (bh / p.Hq) * p.os.b + i * p.os.t + (bh % p.Hq) * p.os.h;
+#pragma unroll
+  for (int c = 0; c < (D + 63) / 64; ++c)
+    if (lane + 64 * c < D) o[lane + 64 * c] = static_cast<bf16>(x[c] * inv);
+  if (lane == 0) p.lse[row] = l == 0.f ? -kInf : (m + log2_hw(l)) * kLn2;
+}
+
+namespace {
+
+// Keys are split over workgroups where the query tiles alone leave compute
+// units idle.
+struct Split {
+  int n, tiles_each;
+};
+
+Split choose_split(int B, int Tq, int Tk, int Hq) {
+  const int64_t groups = static_cast<int64_t>(B) * Hq * ((Tq + 127) / 128);
+  const int tiles = (Tk + kTile - 1) / kTile;
+  int64_t n = 512 / (groups > 0 ? groups : 1);
+  if (n > tiles / 4) n = tiles / 4;        // at least 4 tiles to a part
+  if (n > 64) n = 64;
+  if (n < 2) return {1, tiles};
+  const int each = static_cast<int>((tiles + n - 1) / n);
+  return {(tiles + each - 1) / each, each};
+}
+
+template <int D, bool CAP, bool BIAS>
+hipError_t run_fwd(const AttnParams& p, hipStream_t s) {
+  const size_t lds = 4 * sizeof(bf16) * kTile * kPitch<D> + 2 * kWaves * sizeof(int) +
+                     (BIAS ? (2 * p.reach + 1) * sizeof(float) : 0);
+  const dim3 grid(p.B * p.Hq, (p.Tq + 127) / 128, p.splits);
+  if (p.splits > 1) {
+    const auto fn = attn_fwd_kernel<D, CAP, BIAS, true>;
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                                       hipFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(lds));
+    if (e != hipSuccess) return e;
+    fn<<<grid, kAttnThreads, lds, s>>>(p);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t rows = static_cast<int64_t>(p.B) * p.Hq * p.Tq;
+    attn_join_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 256, 0, s>>>(p);
+  } else {
+    const auto fn = attn_fwd_kernel<D, CAP, BIAS, false>;
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(lds));
+    if (e != hipSuccess) return e;
+    fn<<<grid, kAttnThreads, lds, s>>>(p);
+  }
+  return hipGetLastError();
+}
+
+template <int D>
+hipError_t pick_fwd(const AttnParams& p, hipStream_t s) {
+  if (p.cap > 0.f)
+    return p.table ? run_fwd<D, true, true>(p, s) : run_fwd<D, true, false>(p, s);
+  return p.table ? run_fwd<D, false, true>(p, s) : run_fwd<D, false, false>(p, s);
+}
+
+}  // namespace
+
+size_t attn_fwd_workspace(int B, int Tq, int Tk, int Hq, int Hk, int D) {
+  (void)Hk;
+  const Split sp = choose_split(B, Tq, Tk, Hq);
+  return sp.n > 1 ? static_cast<size_t>(sp.n) * B * Hq * Tq * (D + 2) * sizeof(float) : 0;
+}
+
+hipError_t launch_attn_fwd(const zero_attn_args& a, hipStream_t s) {
+  AttnParams p = attn_params(a);
+  const Split sp = choose_split(a.B, a.Tq, a.Tk, a.Hq);
+  p.splits = sp.n;
+  p.tiles_per_split = sp.tiles_each;
+  p.osplit = static_cast<float*>(a.workspace);
+  switch (a.D) {
+    case 32: return pick_fwd<32>(p, s);
+    case 64: return pick_fwd<64>(p, s);
+    case 96: return pick_fwd<96>(p, s);
+    default: return pick_fwd<128>(p, s);
+  }
+}
+
+AttnParams attn_params(const zero_attn_args& a) {
+  AttnParams p = {};
+  p.B = a.B;
+  p.Tq = a.Tq;
+  p.Tk = a.Tk;
+  p.Hq = a.Hq;
+  p.Hk = a.Hk;
+  p.group = a.Hq / a.Hk;
+  p.causal = a.causal;
+  p.off = a.Tk - a.Tq;
+  p.scale = static_cast<float>(a.scale);
+  p.cap = static_cast<float>(a.cap);
+  p.q = static_cast<const bf16*>(a.q);
+  p.k = static_cast<const bf16*>(a.k);
+  p.v = static_cast<const bf16*>(a.v);
+  p.ranges = a.ranges;
+  p.table = a.bias_table;
+  p.buckets = a.bias_buckets;
+  p.table_f32 = a.bias_dtype == ZERO_F32;
+  p.n_buckets = a.n_buckets;
+  p.reach = a.bias_table ? a.reach : 0;
+  p.o = static_cast<bf16*>(a.o);
+  p.lse = a.lse;
+  p.d_o = static_cast<const bf16*>(a.d_o);
+  p.dq = static_cast<bf16*>(a.dq);
+  p.dk = static_cast<bf16*>(a.dk);
+  p.dv = static_cast<bf16*>(a.dv);
+  p.dtable = a.dbias_table;
+  const auto st = [](const int64_t* x) { return Strides3{x[0], x[1], x[2]}; };
+  p.qs = st(a.q_stride);
+  p.ks = st(a.k_stride);
+  p.vs = st(a.v_stride);
+  p.os = st(a.o_stride);
+  p.dos = st(a.do_stride);
+  p.dqs = st(a.dq_stride);
+  p.dks = st(a.dk_stride);
+  p.dvs = st(a.dv_stride);
+  return p;
+}
+
+// Document runs of a batch row, found by a workgroup: every thread takes a
+// run of consecutive tokens; the start of the document that a segment's first
+// token continues, and the end of the one its last token begins or continues,
+// come from a scan over the segments.
+__global__ __launch_bounds__(1024) void attn_ranges_kernel(const int32_t* doc,
+                                                           const int32_t* prefix, int T,
+                                                           int causal, int2* ranges) {
+  __shared__ int last_start[1024], first_start[1024];
+  const int tid = threadIdx.x;
+  doc += static_cast<int64_t>(blockIdx.x) * T;
+  ranges += static_cast<int64_t>(blockIdx.x) * T;
+  if (prefix) prefix += static_cast<int64_t>(blockIdx.x) * T;
+  const int each = (T + 1023) / 1024;
+  const int lo = static_cast<int>(min(static_cast<int64_t>(tid) * each, static_cast<int64_t>(T)));
+  const int hi = min(lo + each, T);
+  int ls = -1, fs = T;                     // starts of documents inside [lo, hi)
+  for (int t = lo; t < hi; ++t)
+    if (t == 0 || doc[t] != doc[t - 1]) {
+      ls = t;
+      if (fs == T) fs = t;
+    }
+  last_start[tid] = ls;
+  first_start[tid] = fs;
+  __syncthreads();
+  for (int d = 1; d < 1024; d <<= 1) {     // running maximum from the left, minimum from the right
+    const int a = tid >= d ? last_start[tid - d] : -1;
+    const int b = tid + d < 1024 ? first_start[tid + d] : T;
+    __syncthreads();
+    last_start[tid] = max(last_start[tid], a);
+    first_start[tid] = min(first_start[tid], b);
+    __syncthreads();
+  }
+  int start = tid > 0 ? last_start[tid - 1] : 0;
+  const int after = tid < 1023 ? first_start[tid + 1] : T;   // first start beyond the segment
+  int end = -1;
+  for (int t = lo; t < hi; ++t) {
+    if (t == 0 || doc[t] != doc[t - 1]) {
+      start = t;
+      end = -1;
+    }
+    if (end < 0) {
+      end = t + 1;
+      while (end < hi && doc[end] == doc[t]) ++end;
+      if (end == hi) end = after;
+    }
+    int2 r = make_int2(start, end);
+    if (causal) {
+      int see = t + 1;
+      if (prefix) {
+        const int64_t reach = static_cast<int64_t>(start) + prefix[t];
+        if (reach > see) see = static_cast<int>(min(reach, static_cast<int64_t>(end)));
+      }
+      r.y = min(see, end);
+    }
+    if (doc[t] < 0) r = make_int2(0, 0);
+    ranges[t] = r;
+  }
+}
+
+hipError_t launch_attn_ranges(const int32_t* doc, const int32_t* prefix, int B, int T, int causal,
+                              int32_t* ranges, hipStream_t s) {
+  attn_ranges_kernel<<<B, 1024, 0, s>>>(doc, prefix, T, causal, reinterpret_cast<int2*>(ranges));
+  return hipGetLastError();
+}
+
+}  // namespace zo

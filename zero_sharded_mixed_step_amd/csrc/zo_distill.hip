@@ -1,0 +1,491 @@
+// zo_distill.hip -- the distillation loss against a teacher's top logits.
+//
+// Bound by memory: the logits are read once and their gradient is written
+// once.  A workgroup owns a row; the forward pass keeps it in registers
+// (packed as it came) between the maximum, the sums and the gradient, or, when
+// the row is too long for that, reads it again.  The backward pass needs no
+// row-wide sum, so a row is cut into pieces over workgroups.
+//
+// Rows may start at any element (an odd vocabulary makes every other row of a
+// bf16 matrix misaligned): a row is taken as 16-byte chunks counted from the
+// aligned address at or below its start, and its first and last chunk are
+// loaded and stored element by element.
+//
+// The teacher's K entries and everything of them is formed in binary64: the
+// tail's mass is a difference from 1.  The entries' positions are marked in a
+// bit map in shared memory, so that the sum outside them is a sum of its own and
+// no difference of large numbers.
+#include "zo_device.h"
+#include "zo_internal.h"
+
+namespace zo {
+
+struct DistillParams {
+  int64_t N, V;
+  int K, tail;
+  double inv_tau, tau;
+  double grad_scale;
+  const void* z;
+  const int32_t* idx;
+  const void* val;
+  const float* tlse;
+  const float* weight;
+  float *loss, *stats;
+  void* dz;
+  int64_t z_stride, dz_stride;
+  int seg;  // backward: chunks of a piece
+};
+
+template <typename E>
+struct Chunk;
+template <>
+struct Chunk<bf16> {
+  static constexpr int kN = 8;
+  u32x4 r;
+  __device__ __forceinline__ float get(int e) const {
+    return e & 1 ? __uint_as_float(r[e >> 1] & 0xFFFF0000u) : bf16_bits_to_f32(r[e >> 1]);
+  }
+  __device__ __forceinline__ void fill_lowest() {  // -inf
+    r = u32x4{0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u};
+  }
+  __device__ __forceinline__ void put_raw(int e, bf16 x) {
+    union {
+      bf16 b;
+      uint16_t u;
+    } c;
+    c.b = x;
+    const uint32_t bits = c.u;
+    r[e >> 1] = e & 1 ? (r[e >> 1] & 0x0000FFFFu) | (bits << 16) : (r[e >> 1] & 0xFFFF0000u) | bits;
+  }
+};
+template <>
+struct Chunk<float> {
+  static constexpr int kN = 4;
+  f32x4 r;
+  __device__ __forceinline__ float get(int e) const { return r[e]; }
+  __device__ __forceinline__ void fill_lowest() { r = f32x4{-kInf, -kInf, -kInf, -kInf}; }
+  __device__ __forceinline__ void put_raw(int e, float x) { r[e] = x; }
+};
+
+template <typename E>
+__device__ __forceinline__ float value(const void* p, int64_t at) {
+  return static_cast<float>(static_cast<const E*>(p)[at]);
+}
+
+// A row as aligned chunks: chunk c holds elements c * kN - shift .. + kN - 1.
+template <typename E>
+struct Row {
+  static constexpr int kN = Chunk<E>::kN;
+  E* p;       // element 0
+  int shift;
+  int64_t V;
+  __device__ __forceinline__ Row(const void* base, int64_t at, int64_t v)
+      : p(const_cast<E*>(static_cast<const E*>(base)) + at), V(v) {
+    shift = static_cast<int>((reinterpret_cast<uintptr_t>(p) / sizeof(E)) % kN);
+  }
+  __device__ __forceinline__ int chunks() const {
+    return static_cast<int>((V + shift + kN - 1) / kN);
+  }
+  __device__ __forceinline__ bool whole(int c) const {
+    const int64_t e0 = static_cast<int64_t>(c) * kN - shift;
+    return e0 >= 0 && e0 + kN <= V;
+  }
+  __device__ __forceinline__ Chunk<E> load(int c) const {
+    Chunk<E> x;
+    const int64_t e0 = static_cast<int64_t>(c) * kN - shift;
+    if (whole(c)) {
+      x.r = *reinterpret_cast<const decltype(x.r)*>(p + e0);
+    } else {
+      x.fill_lowest();
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+        if (e0 + e >= 0 && e0 + e < V) x.put_raw(e, p[e0 + e]);
+    }
+    return x;
+  }
+  // y as this row's elements that chunk c of a row shifted by `from` holds
+  __device__ __forceinline__ void store(int c, int from, const float y[kN]) const {
+    const int64_t e0 = static_cast<int64_t>(c) * kN - from;
+    if (from == shift && e0 >= 0 && e0 + kN <= V) {
+      Chunk<E> x;
+      if constexpr (sizeof(E) == 2) {
+        union {
+          bf16x8 b;
+          u32x4 u;
+        } v;
+#pragma unroll
+        for (int e = 0; e < kN; ++e) v.b[e] = static_cast<bf16>(y[e]);
+        x.r = v.u;
+      } else {
+#pragma unroll
+        for (int e = 0; e < kN; ++e) x.r[e] = y[e];
+      }
+      *reinterpret_cast<decltype(x.r)*>(p + e0) = x.r;
+    } else {
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+        if (e0 + e >= 0 && e0 + e < V) p[e0 + e] = static_cast<E>(y[e]);
+    }
+  }
+};
+
+// Between the passes over a held row: its values are unpacked again in the next
+// pass, not carried over as twice the registers.
+template <typename E, int CH>
+__device__ __forceinline__ void keep_packed(Chunk<E> (&held)[CH]) {
+#pragma unroll
+  for (int c = 0; c < CH; ++c) asm volatile("" : "+v"(held[c].r));
+}
+
+struct MaxOp {
+  template <typename X>
+  __device__ __forceinline__ X operator()(X a, X b) const {
+    return a > b || a != a ? a : b;      // a NaN stays
+  }
+};
+struct AddOp {
+  template <typename X>
+  __device__ __forceinline__ X operator()(X a, X b) const {
+    return a + b;
+  }
+};
+
+// Joins a value over the workgroup, in one fixed order; everyone gets it.
+template <int NT, typename X, typename Op>
+__device__ __forceinline__ X join(X x, Op op, double* scratch) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) x = op(x, __shfl_xor(x, d));
+  X* s = reinterpret_cast<X*>(scratch);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = x;
+  __syncthreads();
+  x = s[(threadIdx.x & 63) % (NT / 64)];
+#pragma unroll
+  for (int d = 1; d < NT / 64; d <<= 1) x = op(x, __shfl_xor(x, d));
+  return x;
+}
+
+// The teacher's side of a row, in shared memory: p[k], the student's logit
+// z[k] (of entries in [from, to)) and idx[k], -1 for an absent entry.
+struct Teacher {
+  float* p;
+  float* z;
+  int* idx;
+  double mass;   // sum of p
+  double cross;  // sum of p (log p - z / tau)
+  bool any;
+};
+
+template <typename E, int NT>
+__device__ __forceinline__ void load_teacher(const DistillParams& p, int64_t n, const E* z,
+                                             int64_t from, int64_t to, double* scratch,
+                                             Teacher& t) {
+  const int tid = threadIdx.x;
+  float mx = -kInf;
+  int any = 0;
+  for (int k = tid; k < p.K; k += NT) {
+    const int i = p.idx[n * p.K + k];
+    const bool ok = i >= 0 && i < p.V;
+    t.idx[k] = ok ? i : -1;
+    t.z[k] = ok && i >= from && i < to ? static_cast<float>(z[i]) : 0.f;
+    const float v = ok ? value<E>(p.val, n * p.K + k) : -kInf;
+    t.p[k] = v;
+    any |= ok;
+    mx = MaxOp()(mx, v);
+  }
+  t.any = __syncthreads_or(any) != 0;
+  double base;
+  if (p.tlse != nullptr) {
+    base = p.tlse[n];
+  } else {
+    mx = join<NT>(mx, MaxOp(), scratch);
+    const double m = static_cast<double>(mx) * p.inv_tau;
+    double s = 0.0;
+    for (int k = tid; k < p.K; k += NT)
+      if (t.idx[k] >= 0) s += exp(static_cast<double>(t.p[k]) * p.inv_tau - m);
+    s = join<NT>(s, AddOp(), scratch);
+    base = m + log(s);
+  }
+  double mass = 0.0, cross = 0.0;
+  for (int k = tid; k < p.K; k += NT) {
+    double pk = 0.0;
+    if (t.idx[k] >= 0) {
+      const double lp = static_cast<double>(t.p[k]) * p.inv_tau - base;
+      pk = exp(lp);
+      mass += pk;
+      if (pk != 0.0) cross += pk * (lp - static_cast<double>(t.z[k]) * p.inv_tau);
+    }
+    t.p[k] = static_cast<float>(pk);
+  }
+  t.mass = join<NT>(mass, AddOp(), scratch);
+  t.cross = join<NT>(cross, AddOp(), scratch);
+}
+
+__device__ __forceinline__ float prob(float z, float inv_tau, float lse) {
+  return exp2_hw(__builtin_fmaf(z, inv_tau, -lse) * kLog2e);
+}
+
+// Writes the gradient of the row's entries over what the row's pass wrote.
+template <typename E, int NT, typename Prob>
+__device__ __forceinline__ void store_entries(const DistillParams& p, const Row<E>& out,
+                                              const Teacher& t, float scale, int64_t from,
+                                              int64_t to, Prob prob_of) {
+  __syncthreads();                       // orders the workgroup's stores
+  for (int k = threadIdx.x; k < p.K; k += NT) {
+    const int i = t.idx[k];
+    if (i >= from && i < to)
+      out.p[i] = static_cast<E>(scale * (prob_of(t.z[k]) - t.p[k]));
+  }
+}
+
+// Forward: loss and statistics, and the gradient if asked for.  CH > 0: the
+// row stays in registers, CH chunks to a thread; CH = 0: it is read again.
+template <typename E, int NT, int CH>
+__global__ __launch_bounds__(NT, CH <= (sizeof(E) == 2 ? 8 : 4) ? 8 : 4) void distill_fwd_kernel(const DistillParams p) {
+  constexpr int kN = Chunk<E>::kN;
+  constexpr int kHeld = CH > 0 ? CH : 1;
+  extern __shared__ __align__(16) char smem[];
+  double* scratch = reinterpret_cast<double*>(smem);           // [NT / 64]
+  Teacher t;
+  t.p = reinterpret_cast<float*>(scratch + NT / 64);
+  t.z = t.p + p.K;
+  t.idx = reinterpret_cast<int*>(t.z + p.K);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(t.idx + p.K);   // with a tail
+
+  const int tid = threadIdx.x;
+  const int64_t n = blockIdx.x;
+  const Row<E> in(p.z, n * p.z_stride, p.V), out(p.dz, n * p.dz_stride, p.V);
+  const int chunks = in.chunks();
+  const float w = p.weight ? p.weight[n] : 1.f;
+  const float inv_tau = static_cast<float>(p.inv_tau);
+
+  if (p.tail)
+    for (int64_t i = tid; i < (p.V + kN) / 32 + 1; i += NT) bits[i] = 0;
+  load_teacher<E, NT>(p, n, in.p, 0, p.V, scratch, t);
+  if (p.tail)
+    for (int64_t i = tid; i < (p.V + kN) / 32 + 1; i += NT) bits[i] = 0;
+  load_teacher<E, NT>(p, n, in.p, 0, p.V, scratch, t);
+  Chunk<E> held[kHeld];
+  if constexpr (CH > 0) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      held[c].fill_lowest();
+      if (tid + c * NT < chunks) held[c] = in.load(tid + c * NT);
+    }
+  }
+  // a row without weight, or with nothing to be compared with: statistics only
+  const bool live = w != 0.f && (t.any || p.tail);
+  if (p.tail) {
+    for (int k = tid; k < p.K; k += NT)
+      if (t.idx[k] >= 0) {
+        const int64_t e = t.idx[k] + in.shift;
+        atomicOr(&bits[e >> 5], 1u << (e & 31));
+      }
+    __syncthreads();
+  }
+
+  // running maximum (streamed rows), sum and sum outside the entries
+  float m = -kInf, sum = 0.f, rest = 0.f;
+  const auto chunk_max = [&](const Chunk<E>& x, float a) {
+#pragma unroll
+    for (int e = 0; e < kN; ++e) a = fmaxf(a, x.get(e));
+    return a;
+  };
+  const float k2 = inv_tau * kLog2e;
+  const auto chunk_sum = [&](const Chunk<E>& x, int c, float mx) {
+    uint32_t marked = 0;
+    if (p.tail) {
+      const int64_t e = static_cast<int64_t>(c) * kN;
+      marked = (bits[e >> 5] >> (e & 31)) & ((1u << kN) - 1);
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < kN; ++e) s += exp2_hw((x.get(e) - mx) * k2);
+    sum += s;
+    rest += marked != 0 ? 0.f : s;
+    if (marked != 0) {
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+        if (!((marked >> e) & 1u)) rest += exp2_hw((x.get(e) - mx) * k2);
+    }
+  };
+  if constexpr (CH > 0) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) m = chunk_max(held[c], m);
+  } else {
+    for (int c = tid; c < chunks; c += NT) m = chunk_max(in.load(c), m);
+  }
+  m = join<NT>(m, MaxOp(), scratch);
+  if constexpr (CH > 0) keep_packed(held);
+  if (m == -kInf) m = 0.f;               // nothing but -inf: a sum of 0, not of NaN
+  if constexpr (CH > 0) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      if (tid + c * NT < chunks) chunk_sum(held[c], tid + c * NT, m);
+  } else {
+    for (int c = tid; c < chunks; c += NT) chunk_sum(in.load(c), c, m);
+  }
+  if constexpr (CH > 0) keep_packed(held);
+  const double total = join<NT>(static_cast<double>(sum), AddOp(), scratch);
+  double outside = 0.0, mass = 0.0, coef = 1.0;
+  if (p.tail) {
+    outside = join<NT>(static_cast<double>(rest), AddOp(), scratch);
+    mass = t.mass < 1.0 ? 1.0 - t.mass : 0.0;
+    if (mass > 0.0) coef = 1.0 - mass * (total / outside);
+  }
+  if (p.dz != nullptr) {
+    const float scale = static_cast<float>(p.grad_scale * p.tau * static_cast<double>(w));
+    if (live) {
+      const float inv = static_cast<float>(1.0 / total), other = static_cast<float>(coef) * scale;
+      const auto grad = [&](const Chunk<E>& x, int c) {
+        float y[kN];
+#pragma unroll
+        for (int e = 0; e < kN; ++e) y[e] = exp2_hw((x.get(e) - m) * k2) * inv * other;
+        out.store(c, in.shift, y);
+      };
+      if constexpr (CH > 0) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+          if (tid + c * NT < chunks) grad(held[c], tid + c * NT);
+      } else {
+        for (int c = tid; c < chunks; c += NT) grad(in.load(c), c);
+      }
+      store_entries<E, NT>(p, out, t, scale, 0, p.V, [&](float z) {
+        return exp2_hw((z - m) * k2) * inv;
+      });
+    } else {
+      const float zero[kN] = {};
+      for (int c = tid; c < chunks; c += NT) out.store(c, in.shift, zero);
+    }
+  }
+  // the logarithms come last: in binary64 they take registers that the held row
+  // leaves only now
+  if (tid == 0) {
+    const double base = static_cast<double>(m) * p.inv_tau;
+    const double lse = base + log(total);
+    double loss = t.cross + t.mass * lse;
+    if (mass > 0.0) loss += mass * (log(mass) - (base + log(outside)) + lse);
+    p.loss[n] = live ? static_cast<float>(loss * p.tau * p.tau * static_cast<double>(w)) : 0.f;
+    p.stats[2 * n] = static_cast<float>(lse);
+    p.stats[2 * n + 1] = static_cast<float>(coef);
+  }
+}
+
+// Backward from saved statistics: a piece of a row to a workgroup.
+template <typename E, int NT>
+__global__ __launch_bounds__(NT) void distill_bwd_kernel(const DistillParams p) {
+  constexpr int kN = Chunk<E>::kN;
+  extern __shared__ __align__(16) char smem[];
+  double* scratch = reinterpret_cast<double*>(smem);
+  Teacher t;
+  t.p = reinterpret_cast<float*>(scratch + NT / 64);
+  t.z = t.p + p.K;
+  t.idx = reinterpret_cast<int*>(t.z + p.K);
+
+  const int tid = threadIdx.x;
+  const int64_t n = blockIdx.y;
+  const Row<E> in(p.z, n * p.z_stride, p.V), out(p.dz, n * p.dz_stride, p.V);
+  const int c0 = blockIdx.x * p.seg, c1 = min(c0 + p.seg, in.chunks());
+  if (c0 >= c1) return;
+  const float w = p.weight ? p.weight[n] : 1.f;
+  const float inv_tau = static_cast<float>(p.inv_tau);
+  // (only this piece's logits are read: in place, others may be gradients already)
+  const int64_t from = max(static_cast<int64_t>(c0) * kN - in.shift, int64_t(0));
+  const int64_t to = static_cast<int64_t>(c1) * kN - in.shift;
+  if (w != 0.f) load_teacher<E, NT>(p, n, in.p, from, to, scratch, t);
+  if (w == 0.f || (!t.any && !p.tail)) {
+    const float zero[kN] = {};
+    for (int c = c0 + tid; c < c1; c += NT) out.store(c, in.shift, zero);
+    return;
+  }
+  const float lse = p.stats[2 * n];
+  const float scale = static_cast<float>(p.grad_scale * p.tau * static_cast<double>(w));
+  const float other = p.stats[2 * n + 1] * scale;
+  for (int c = c0 + tid; c < c1; c += NT) {
+    const Chunk<E> x = in.load(c);
+    float y[kN];
+#pragma unroll
+    for (int e = 0; e < kN; ++e) y[e] = other * prob(x.get(e), inv_tau, lse);
+    out.store(c, in.shift, y);
+  }
+  store_entries<E, NT>(p, out, t, scale, from, to,
+                       [&](float z) { return prob(z, inv_tau, lse); });
+}
+
+namespace {
+
+template <typename E, int NT, int CH>
+hipError_t run_fwd(const DistillParams& p, hipStream_t s) {
+  size_t lds = NT / 64 * sizeof(double) + 12 * static_cast<size_t>(p.K);
+  if (p.tail) lds += ((p.V + Chunk<E>::kN) / 32 + 1) * 4;
+  const auto fn = distill_fwd_kernel<E, NT, CH>;
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize,
+                                           static_cast<int>(lds));
+  if (e != hipSuccess) return e;
+  fn<<<static_cast<unsigned>(p.N), NT, lds, s>>>(p);
+  return hipGetLastError();
+}
+
+template <typename E>
+hipError_t pick_fwd(const DistillParams& p, hipStream_t s) {
+  const int64_t chunks = (p.V + Chunk<E>::kN - 1) / Chunk<E>::kN + 1;
+  if (chunks <= 256 * 2) return run_fwd<E, 256, 2>(p, s);
+  if (chunks <= 256 * 4) return run_fwd<E, 256, 4>(p, s);
+  if (chunks <= 1024 * 2) return run_fwd<E, 1024, 2>(p, s);
+  if (chunks <= 1024 * 4) return run_fwd<E, 1024, 4>(p, s);
+  if (chunks <= 1024 * 8) return run_fwd<E, 1024, 8>(p, s);
+  if (chunks <= 1024 * 16) return run_fwd<E, 1024, 16>(p, s);
+  return run_fwd<E, 1024, 0>(p, s);
+}
+
+template <typename E>
+hipError_t run_bwd(DistillParams p, hipStream_t s) {
+  constexpr int NT = 256;
+  const int chunks = static_cast<int>((p.V + Chunk<E>::kN - 1) / Chunk<E>::kN + 1);
+  p.seg = NT * 16;
+  const size_t lds = NT / 64 * sizeof(double) + 12 * static_cast<size_t>(p.K);
+  for (int64_t n0 = 0; n0 < p.N; n0 += 65535) {
+    DistillParams q = p;
+    const int64_t rows = p.N - n0 < 65535 ? p.N - n0 : 65535;
+    q.z = static_cast<const E*>(p.z) + n0 * p.z_stride;
+    q.dz = static_cast<E*>(p.dz) + n0 * p.dz_stride;
+    q.idx = p.idx + n0 * p.K;
+    q.val = static_cast<const E*>(p.val) + n0 * p.K;
+    q.tlse = p.tlse ? p.tlse + n0 : nullptr;
+    q.weight = p.weight ? p.weight + n0 : nullptr;
+    q.stats = p.stats + 2 * n0;
+    distill_bwd_kernel<E, NT>
+        <<<dim3((chunks + p.seg - 1) / p.seg, static_cast<unsigned>(rows)), NT, lds, s>>>(q);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_distill(const zero_distill_args& a, bool forward, hipStream_t s) {
+  DistillParams p = {};
+  p.N = a.N;
+  p.V = a.V;
+  p.K = a.K;
+  p.tail = a.teacher_lse != nullptr;
+  p.tau = a.temperature;
+  p.inv_tau = 1.0 / a.temperature;
+  p.grad_scale = a.grad_scale;
+  p.z = a.logits;
+  p.idx = a.teacher_idx;
+  p.val = a.teacher_val;
+  p.tlse = a.teacher_lse;
+  p.weight = a.row_weight;
+  p.loss = a.loss;
+  p.stats = a.stats;
+  p.dz = a.dlogits;
+  p.z_stride = a.logits_stride;
+  p.dz_stride = a.dlogits_stride;
+  if (forward) return a.dtype == ZERO_BF16 ? pick_fwd<bf16>(p, s) : pick_fwd<float>(p, s);
+  return a.dtype == ZERO_BF16 ? run_bwd<bf16>(p, s) : run_bwd<float>(p, s);
+}
+
+}  // namespace zo
