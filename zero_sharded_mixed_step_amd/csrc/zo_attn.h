@@ -27,12 +27,24 @@ constexpr int kAttnThreads = 256;
 constexpr int kWaves = 4;
 constexpr int kTile = 64;  // rows of a staged tile
 
-// Row pitch, in elements, of a staged tile of D columns: D + 16 is an odd
-// multiple of 8 banks of 4 bytes for every supported D, so the 8 rows that 16
-// lanes' 16-byte reads take at a time, and the 4 rows of a transposing read,
-// fall on different banks.
+// A staged tile is 64 rows of D bf16 without gaps (the direct loads to shared
+// memory write 64 lanes' 16 bytes one after another), and the 16-byte pieces of
+// row r are stored at piece ^ swizzle(r).  The 8 rows of consecutive lanes'
+// 16-byte reads, and the 4 rows of a transposing read, then fall on different
+// banks: with 256-byte rows all start on the same bank and the 4 x 32 bytes of a
+// transposing read need 4 different pairs of pieces; 128-byte rows alternate between
+// two halves of the banks, 64- and 192-byte rows repeat after 4.
 template <int D>
-constexpr int kPitch = D + 16;
+__device__ __forceinline__ constexpr int swizzle(int r) {
+  return D == 128 ? (r & 7) << 1 : D == 64 ? r & 6 : (r >> 2) & 1;
+}
+template <int D>
+constexpr int kTileBytes = kTile * D * 2;
+
+template <bool V>
+struct Bool {
+  static constexpr bool value = V;
+};
 
 struct Strides3 {
   int64_t b, t, h;
@@ -53,10 +65,13 @@ struct AttnParams {
   void* dtable;
   Strides3 qs, ks, vs, os, dos, dqs, dks, dvs;
   // workspace
-  float* lse2;      // [B][Hq][Tq]  lse * log2(e), +inf for a query without keys
-  float* delta;     // [B][Hq][Tq]  do . o
-  int2* qbounds;    // [B][tiles of 64 queries]  keys their queries see, as a hull
+  int tq64;         // Tq up to a multiple of 64: the rows below are padded to it
+  float* lse2;      // [B][Hq][tq64]  lse * log2(e), +inf for a query without keys
+  float* delta;     // [B][Hq][tq64]  do . o
+  int *qlo, *qhi;   // [B][tq64]      the keys a query sees; 0, 0 for none
   float* dpart;     // [B][Hq][query tiles][n_buckets]
+  float* kvpart;    // [2][parts][B][Hk][Tk][D]: dk and dv of parts of a group's heads
+  int parts;        // 1: no parts
   float* osplit;    // split forward: [splits][B * Hq * Tq][D] and, behind it, two statistics
   int splits, tiles_per_split;
 };
@@ -92,32 +107,62 @@ __device__ __forceinline__ bf16x8 load8(const bf16* p) {
   return *reinterpret_cast<const bf16x8*>(p);
 }
 
-// Operand fragment of a row-major tile in shared memory, contraction along
-// the row: rows row0 + l % 32, elements col0 + 8 (l / 32) .. + 7.
-template <int PITCH>
-__device__ __forceinline__ bf16x8 frag_rows(const bf16* tile, int row0, int col0, int lane) {
-  return load8(tile + (row0 + (lane & 31)) * PITCH + col0 + 8 * (lane >> 5));
+// Shared memory is addressed by its 32-bit offsets: a fragment's address is one
+// exclusive or away from the lane's place in the tile.
+#define ZO_LDS __attribute__((address_space(3)))
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((const ZO_LDS char*)static_cast<const char*>(p)));
 }
 
-// Operand fragment of the same tile, contraction along the column: columns
-// col0 + l % 32 and, of the 16 rows from row0, the 8 in the order in which a
-// score result holds them.  A transposing read hands each of 16 lanes a
-// column of the 4 x 16 block whose rows those lanes address by fours.
-template <int PITCH>
-__device__ __forceinline__ bf16x8 frag_cols(const bf16* tile, int row0, int col0, int lane) {
-  const int i = lane & 15;
-  const bf16* a = tile + (row0 + 4 * (lane >> 5) + (i >> 2)) * PITCH + col0 +
-                  16 * ((lane >> 4) & 1) + 4 * (i & 3);
-  using P = __attribute__((address_space(3))) s16x4*;
-  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(a));
-  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(a + 8 * PITCH));
+// A lane's place in the fragments of a staged tile.
+template <int D>
+struct FragAt {
+  uint32_t rows, cols;
+  __device__ __forceinline__ explicit FragAt(int lane) {
+    const int r = lane & 31, half = lane >> 5;
+    rows = r * 2 * D + ((half ^ swizzle<D>(r)) << 4);
+    const int i = lane & 15, c = 4 * half + (i >> 2), g = (lane >> 4) & 1;
+    cols = c * 2 * D + (((2 * g + ((i >> 1) & 1)) ^ swizzle<D>(c)) << 4) + 8 * (i & 1);
+  }
+  // The same in the tile at `tile` (aligned to 1 KiB, so that or-ing and adding
+  // agree).  Opaque to the compiler, which otherwise keeps every fragment's
+  // address in a register of its own across the loop, 40 of them.
+  __device__ __forceinline__ FragAt in(uint32_t tile) const {
+    FragAt f = *this;
+    f.rows += tile;
+    f.cols += tile;
+    asm volatile("" : "+v"(f.rows), "+v"(f.cols));
+    return f;
+  }
+};
+
+// Operand fragment, contraction along the row: rows 32 t + l % 32, elements
+// 16 c + 8 (l / 32) .. + 7.  (Swizzles repeat after 8 rows, and piece 2 c + half
+// is 2 c ^ half: moving along the row is one exclusive or, or for swizzles of
+// one bit a sum.)
+template <int D>
+__device__ __forceinline__ bf16x8 frag_rows(const FragAt<D>& at, int t, int c) {
+  const uint32_t x = (D == 64 || D == 128 ? at.rows ^ (c << 5) : at.rows + (c << 5)) + t * 64 * D;
+  return *reinterpret_cast<const ZO_LDS bf16x8*>(x);
+}
+
+// Operand fragment, contraction along the column: columns 32 t + l % 32 and, of
+// the 16 rows from 16 u, the 8 in the order in which a score result holds
+// them.  A transposing read hands each of 16 lanes a column of the 4 x 16
+// block whose rows those lanes address by fours.
+template <int D>
+__device__ __forceinline__ bf16x8 frag_cols(const FragAt<D>& at, int u, int t) {
+  const uint32_t x = (D == 64 || D == 128 ? at.cols ^ (t << 6) : at.cols + (t << 6)) + u * 32 * D;
+  using P = ZO_LDS s16x4*;
   union {
     s16x4 s[2];
     bf16x8 v;
-  } u;
-  u.s[0] = lo;
-  u.s[1] = hi;
-  return u.v;
+  } f;
+  f.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<P>(x));
+  f.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<P>(x + 16 * D));
+  return f.v;
 }
 
 __device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
@@ -162,60 +207,109 @@ __device__ __forceinline__ uint32_t any_in_half(bool f, int lane) {
   return half != 0 ? 1u : 0u;
 }
 
-// A 64-row tile of D columns: global loads of a thread's 16-byte pieces (rows
-// outside [first, last) read as 0) and their stores to shared memory.
+// Starts the loads of a tile of 64 rows, row0 .. + 63 of `base`, straight into
+// shared memory (no registers on the way).  Rows outside [first, last) are
+// replaced by a row inside: no owned row sees them.  wait_tile() ends them.
 template <int D>
-struct Stage {
-  static constexpr int kPieces = kTile * D / 8 / kAttnThreads;
-  u32x4 r[kPieces];
-
-  __device__ __forceinline__ void load(const bf16* base, int64_t stride, int row0, int first,
-                                       int last, int tid) {
+__device__ __forceinline__ void load_tile(uint32_t tile, const bf16* base, int64_t stride, int row0,
+                                          int first, int last, int wave, int lane) {
 #pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      const int c = tid + u * kAttnThreads;
-      const int row = row0 + c / (D / 8), col = (c % (D / 8)) * 8;
-      r[u] = u32x4{0, 0, 0, 0};
-      if (row >= first && row < last)
-        r[u] = *reinterpret_cast<const u32x4*>(base + row * stride + col);
-    }
+  for (int u = 0; u < D / 32; ++u) {
+    const int n = wave * (D / 32) + u;                 // of D / 8 loads of 64 pieces
+    const int piece = n * 64 + lane;
+    const int r = piece / (D / 8), c = (piece % (D / 8)) ^ swizzle<D>(r);
+    const int row = min(max(row0 + r, first), last - 1);
+    const bf16* src = base + row * stride + c * 8;
+    __builtin_amdgcn_global_load_lds(
+        (const __attribute__((address_space(1))) void*)src,
+        reinterpret_cast<ZO_LDS void*>(tile + n * 1024), 16, 0, 0);
   }
-  __device__ __forceinline__ void store(bf16* tile, int tid) const {
-#pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      const int c = tid + u * kAttnThreads;
-      const int row = c / (D / 8), col = (c % (D / 8)) * 8;
-      *reinterpret_cast<u32x4*>(tile + row * kPitch<D> + col) = r[u];
-    }
-  }
-};
+}
 
-// The head's bias by distance, times log2(e), into shared memory:
-// out[d + reach].  A finite bias stays finite.
+// The same for 64 words of a padded array, by one wave.
+__device__ __forceinline__ void load_words(uint32_t to, const void* from, int lane) {
+  __builtin_amdgcn_global_load_lds(
+      (const __attribute__((address_space(1))) void*)(static_cast<const uint32_t*>(from) + lane),
+      reinterpret_cast<ZO_LDS void*>(to), 4, 0, 0);
+}
+
+// The calling thread's tile loads are done; the workgroup's after the barrier.
+__device__ __forceinline__ void wait_tile() {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+}
+
+// The larger of a value and the other half wave's at the same lane.
+__device__ __forceinline__ float max_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                  false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// The distance bias in shared memory, times log2(e), at distance d + kSpan(reach):
+// it goes on past the reach by kOver at either end, so that in a tile with
+// any distance inside the reach no index has to be clipped.
+constexpr int kOver = 2 * kTile;
+__host__ __device__ constexpr int bias_span(int reach) { return reach + kOver; }
+__host__ __device__ constexpr int bias_entries(int reach) { return 2 * bias_span(reach) + 1; }
+
+__device__ __forceinline__ int bias_bucket(const AttnParams& p, int d) {
+  return min(max(p.buckets[min(max(d, -p.reach), p.reach) + p.reach], 0), p.n_buckets - 1);
+}
+
+// The head's bias into shared memory.  A finite bias stays finite.
 __device__ __forceinline__ void stage_bias(const AttnParams& p, int h, float* out, int tid) {
-  for (int d = tid; d <= 2 * p.reach; d += kAttnThreads) {
-    const int bucket = min(max(p.buckets[d], 0), p.n_buckets - 1);
-    const int64_t at = static_cast<int64_t>(bucket) * p.Hq + h;
+  const int span = bias_span(p.reach);
+  for (int d = tid - span; d <= span; d += kAttnThreads) {
+    const int64_t at = static_cast<int64_t>(bias_bucket(p, d)) * p.Hq + h;
     const float b = p.table_f32 ? static_cast<const float*>(p.table)[at]
                                 : static_cast<float>(static_cast<const bf16*>(p.table)[at]);
     const float x = b * kLog2e;
-    out[d] = __builtin_isinf(x) && !__builtin_isinf(b) ? __builtin_copysignf(-kLowest, b) : x;
+    out[d + span] =
+        __builtin_isinf(x) && !__builtin_isinf(b) ? __builtin_copysignf(-kLowest, b) : x;
   }
 }
 
-// A raw product q.k as a score in units of log2: x = scale q.k, capped.
-// `a` is scale * log2(e), or 2 scale log2(e) / cap with the cap, where
-// cap tanh(y) = cap - 2 cap / (exp(2 y) + 1); `c2` is then cap log2(e).
-template <bool CAP>
-__device__ __forceinline__ float score2(float x, float a, float c2) {
-  if constexpr (CAP) {
-    const float e = exp2_hw(x * a);
-    return __builtin_fmaf(rcp_hw(e + 1.f), -2.f * c2, c2);
-  } else {
-    return x * a;
-  }
+// Where a block of distances lies: all at or past one end of the reach (-1, 1),
+// where the bias is one number, or not (0).
+__device__ __forceinline__ int bias_side(int lowest, int highest, int reach) {
+  return highest <= -reach ? -1 : lowest >= reach ? 1 : 0;
 }
 
+// Factors of the scores.  Without a cap a score in units of log2 is x * a.
+// With one, cap tanh(y) = cap - 2 cap u, u = 1 / (exp(2 y) + 1): exp(2 y) is
+// exp2(x * a) and the score c2 - 2 c2 u.  A negative scale is taken to q, so a > 0:
+// the largest score is that of the largest x, and of the smallest u.  (A scale
+// of 0 becomes one that vanishes beside any score.)
+struct ScoreFactors {
+  float a, c2;
+  bool flip;
+  __device__ __forceinline__ ScoreFactors(const AttnParams& p, bool cap) {
+    const float s = fmaxf(fabsf(p.scale), 1e-30f) * kLog2e;
+    a = cap ? fmaxf(2.f * s / p.cap, 1e-30f) : s;
+    c2 = cap ? p.cap * kLog2e : 0.f;
+    flip = p.scale < 0.f;
+  }
+};
+
+// q's fragment times the sign of the scale.
+__device__ __forceinline__ bf16x8 signed_frag(bf16x8 f, bool flip) {
+  union {
+    bf16x8 v;
+    uint32_t u[4];
+  } x;
+  x.v = f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x.u[j] ^= flip ? 0x80008000u : 0u;
+  return x.v;
+}
+
+// Workgroup index along x to (batch, head): the 8 dies take workgroups in turn, so
+// eighths of the heads in a row go to one die, whose cache then serves the query
+// heads of a key head together.
+__device__ __forceinline__ int head_of_group(int x, int n) {
+  return n % 8 == 0 ? (x % 8) * (n / 8) + x / 8 : x;
+}
 
 AttnParams attn_params(const zero_attn_args& a);
 

@@ -11,22 +11,121 @@
 
 namespace zo {
 
+// One tile of 64 keys for a wave's 32 queries.  FULL: every query sees every key.
+template <int D, bool CAP, bool BIAS, bool FULL>
+__device__ __forceinline__ void attn_fwd_tile(const AttnParams& p, const FragAt<D>& kt,
+                                              const FragAt<D>& vt, const bf16x8 (&qf)[D / 16],
+                                              f32x16 (&acc)[D / 32], float& m, float& l, int2 rng,
+                                              int k0, int i0, const ScoreFactors& f,
+                                              const float* bias, int lane) {
+  float s[2][16];                        // x, or u with a cap, or with a bias the score
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    f32x16 x;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) x[r] = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) x = mfma(frag_rows<D>(kt, t, c), qf[c], x);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[t][r] = CAP ? rcp_hw(exp2_hw(x[r] * f.a) + 1.f) : x[r];
+  }
+  if constexpr (BIAS) {
+    const int d0 = k0 - (i0 + p.off);    // distances span d0 - 31 .. d0 + 63
+    const int side = bias_side(d0 - 31, d0 + kTile - 1, p.reach);
+    if (side != 0) {
+      const float c = bias[side < 0 ? 0 : 2 * bias_span(p.reach)];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          s[t][r] = CAP ? __builtin_fmaf(s[t][r], -2.f * f.c2, f.c2 + c)
+                        : __builtin_fmaf(s[t][r], f.a, c);
+    } else {
+      const float* row = bias + d0 - (lane & 31) + 4 * (lane >> 5) + bias_span(p.reach);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const float c = row[32 * t + 8 * (r >> 2) + (r & 3)];
+          s[t][r] = CAP ? __builtin_fmaf(s[t][r], -2.f * f.c2, f.c2 + c)
+                        : __builtin_fmaf(s[t][r], f.a, c);
+        }
+    }
+  }
+  constexpr bool kU = CAP && !BIAS;      // s holds u: the smallest is the largest score
+  uint32_t keep[4] = {0, 0, 0, 0};       // per 16 keys: those that some query sees
+  if constexpr (!FULL) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int j = k0 + 32 * t + result_row(r, lane);
+        const bool seen = j >= rng.x && j < rng.y;
+        s[t][r] = seen ? s[t][r] : (kU ? kInf : -kInf);
+        keep[2 * t + (r >> 3)] |= any_in_half(seen, lane) << (r & 7);
+      }
+  }
+  float mx = s[0][0];
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) mx = kU ? fminf(mx, s[t][r]) : fmaxf(mx, s[t][r]);
+  if constexpr (kU)
+    mx = __builtin_fmaf(mx, -2.f * f.c2, f.c2);
+  else if constexpr (!BIAS)
+    mx *= f.a;
+  mx = max_halves(mx);
+  // The reference of the exponentials moves only when it is 2^8 too low: p, its
+  // sum and the outputs carry the factor in their exponents, at no loss.
+  if (__any(mx > m + 8.f)) {
+    const float mn = fmaxf(m, mx), g = exp2_hw(m - mn);
+    m = mn;
+    l *= g;
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[t][r] *= g;
+  }
+  const float shift = kU ? f.c2 - m : -m;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    float e[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x = s[g >> 1][8 * (g & 1) + j];
+      if constexpr (BIAS)
+        e[j] = exp2_hw(x - m);
+      else
+        e[j] = exp2_hw(__builtin_fmaf(x, kU ? -2.f * f.c2 : f.a, shift));
+      l += e[j];
+    }
+    const bf16x8 pf = to_frag(e);
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t) {
+      bf16x8 vf = frag_cols<D>(vt, g, t);
+      if constexpr (!FULL) vf = keep_frag(vf, keep[g]);
+      acc[t] = mfma(vf, pf, acc[t]);
+    }
+  }
+}
+
 template <int D, bool CAP, bool BIAS, bool SPLIT>
-__global__ __launch_bounds__(kAttnThreads) void attn_fwd_kernel(const AttnParams p) {
-  constexpr int P = kPitch<D>;
+__global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnParams p) {
   constexpr int kRows = 32 * kWaves;
-  extern __shared__ __align__(16) char smem[];
-  bf16* kt = reinterpret_cast<bf16*>(smem);           // [2][kTile][P]
-  bf16* vt = kt + 2 * kTile * P;                      // [2][kTile][P]
-  int* hull = reinterpret_cast<int*>(vt + 2 * kTile * P);   // [kWaves][2]
+  extern __shared__ __align__(1024) char smem[];      // [2] tiles of K, of V
+  const uint32_t tiles = lds_address(smem);
+  int* hull = reinterpret_cast<int*>(smem + 4 * kTileBytes<D>);      // [kWaves][2]
   float* bias = reinterpret_cast<float*>(hull + 2 * kWaves);
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, half = lane >> 5;
-  const int bh = blockIdx.x, b = bh / p.Hq, h = bh % p.Hq;
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int bh = head_of_group(blockIdx.x, gridDim.x), b = bh / p.Hq, h = bh % p.Hq;
   const int hk = h / p.group;
   const int tile = gridDim.y - 1 - blockIdx.y;        // the longest rows of a causal mask first
   const int i0 = tile * kRows + wave * 32;
   const int i = i0 + (lane & 31);
+  const ScoreFactors f(p, CAP);
+  const FragAt<D> at(lane);
 
   const int2 rng = key_range(p, b, i);
   const int2 wh = wave_hull(rng);
@@ -35,13 +134,6 @@ __global__ __launch_bounds__(kAttnThreads) void attn_fwd_kernel(const AttnParams
     hull[2 * wave + 1] = wh.y;
   }
   if constexpr (BIAS) stage_bias(p, h, bias, tid);
-
-  bf16x8 qf[D / 16];
-  {
-    const bf16* q = p.q + b * p.qs.b + static_cast<int64_t>(min(i, p.Tq - 1)) * p.qs.t + h * p.qs.h;
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) qf[c] = load8(q + 16 * c + 8 * half);
-  }
   __syncthreads();
   int first = 0x7FFFFFFF, last = 0;
 #pragma unroll
@@ -49,7 +141,8 @@ __global__ __launch_bounds__(kAttnThreads) void attn_fwd_kernel(const AttnParams
     first = min(first, hull[2 * w]);
     last = max(last, hull[2 * w + 1]);
   }
-  if (first > last) first = last;
+  first = __builtin_amdgcn_readfirstlane(min(first, last));
+  last = __builtin_amdgcn_readfirstlane(last);
   int k0 = first & ~(kTile - 1), kend = last;
   if constexpr (SPLIT) {
     k0 = max(k0, static_cast<int>(blockIdx.z) * p.tiles_per_split * kTile);
@@ -58,116 +151,44 @@ __global__ __launch_bounds__(kAttnThreads) void attn_fwd_kernel(const AttnParams
 
   const bf16* kg = p.k + b * p.ks.b + hk * p.ks.h;
   const bf16* vg = p.v + b * p.vs.b + hk * p.vs.h;
-  const float c2 = CAP ? p.cap * kLog2e : 0.f;
-  const float a = CAP ? 2.f * p.scale * kLog2e / p.cap : p.scale * kLog2e;
-
+  const auto stage = [&](int buf, int row0) {
+    load_tile<D>(tiles + buf * kTileBytes<D>, kg, p.ks.t, row0, first, last, wave, lane);
+    load_tile<D>(tiles + (2 + buf) * kTileBytes<D>, vg, p.vs.t, row0, first, last, wave, lane);
+  };
+  if (k0 < kend) stage(0, k0);
+  bf16x8 qf[D / 16];
+  {
+    const bf16* q = p.q + b * p.qs.b + static_cast<int64_t>(min(i, p.Tq - 1)) * p.qs.t + h * p.qs.h;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) qf[c] = signed_frag(load8(q + 16 * c + 8 * half), f.flip);
+  }
   f32x16 acc[D / 32];
 #pragma unroll
   for (int t = 0; t < D / 32; ++t)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[t][r] = 0.f;
   float m = kLowest, l = 0.f;
-
-  Stage<D> sk, sv;
-  if (k0 < kend) {
-    sk.load(kg, p.ks.t, k0, first, last, tid);
-    sv.load(vg, p.vs.t, k0, first, last, tid);
-    sk.store(kt, tid);
-    sv.store(vt, tid);
-  }
-  __syncthreads();
+  wait_tile();
+  // The tiles that all of the wave's queries see whole are one run; the loops
+  // for it and for the others leave the accumulators where they are, which a
+  // branch inside one loop did not (64 register copies a tile).  Every wave goes
+  // through the same number of turns, each with its one barrier.
   int buf = 0;
-  for (; k0 < kend; k0 += kTile, buf ^= 1) {
-    const bool more = k0 + kTile < kend;
-    if (more) {
-      sk.load(kg, p.ks.t, k0 + kTile, first, last, tid);
-      sv.load(vg, p.vs.t, k0 + kTile, first, last, tid);
+  const auto turn = [&](auto full) {
+    if (k0 + kTile < kend) stage(buf ^ 1, k0 + kTile);
+    if (full.value || (wh.x < k0 + kTile && wh.y > k0)) {   // a query sees some of the tile
+      const FragAt<D> kt = at.in(tiles + buf * kTileBytes<D>);
+      const FragAt<D> vt = at.in(tiles + (2 + buf) * kTileBytes<D>);
+      attn_fwd_tile<D, CAP, BIAS, full.value>(p, kt, vt, qf, acc, m, l, rng, k0, i0, f, bias, lane);
     }
-    const bf16* kb = kt + buf * kTile * P;
-    const bf16* vb = vt + buf * kTile * P;
-    if (wh.x < k0 + kTile && wh.y > k0) {             // a row of this wave sees some of the tile
-      float s[2][16];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        f32x16 x;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) x[r] = 0.f;
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) x = mfma(frag_rows<P>(kb, 32 * t, 16 * c, lane), qf[c], x);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[t][r] = score2<CAP>(x[r], a, c2);
-      }
-      if constexpr (BIAS) {
-        const int d0 = k0 - (i0 + p.off);             // distances span d0 - 31 .. d0 + 63
-        if (d0 + kTile - 1 <= -p.reach || d0 - 31 >= p.reach) {
-          const float c = bias[d0 <= -p.reach ? 0 : 2 * p.reach];
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) s[t][r] += c;
-        } else {
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              const int d = k0 + 32 * t + result_row(r, lane) - (i + p.off);
-              s[t][r] += bias[min(max(d, -p.reach), p.reach) + p.reach];
-            }
-        }
-      }
-      uint32_t keep[4] = {0xFFu, 0xFFu, 0xFFu, 0xFFu};  // per 16 keys
-      if (!__all(rng.x <= k0 && rng.y >= k0 + kTile)) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) keep[g] = 0;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int j = k0 + 32 * t + result_row(r, lane);
-            const bool seen = j >= rng.x && j < rng.y;
-            s[t][r] = seen ? s[t][r] : -kInf;
-            keep[2 * t + (r >> 3)] |= any_in_half(seen, lane) << (r & 7);
-          }
-      }
-      float mx = s[0][0];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[t][r]);
-      mx = fmaxf(mx, __shfl_xor(mx, 32));
-      const float mn = fmaxf(m, mx);
-      if (__any(mn > m)) {
-        const float f = exp2_hw(m - mn);
-        m = mn;
-        l *= f;
-#pragma unroll
-        for (int t = 0; t < D / 32; ++t)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) acc[t][r] *= f;
-      }
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          s[t][r] = exp2_hw(s[t][r] - m);
-          l += s[t][r];
-        }
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const bf16x8 pf = to_frag(&s[g >> 1][8 * (g & 1)]);
-#pragma unroll
-        for (int t = 0; t < D / 32; ++t) {
-          bf16x8 vf = frag_cols<P>(vb, 16 * g, 32 * t, lane);
-          if (keep[g] != 0xFFu) vf = keep_frag(vf, keep[g]);
-          acc[t] = mfma(vf, pf, acc[t]);
-        }
-      }
-    }
-    if (more) {
-      sk.store(kt + (buf ^ 1) * kTile * P, tid);
-      sv.store(vt + (buf ^ 1) * kTile * P, tid);
-    }
-    __syncthreads();
+    wait_tile();
+    k0 += kTile;
+    buf ^= 1;
+  };
+  const auto sees_all = [&] { return __all(rng.x <= k0 && rng.y >= k0 + kTile) != 0; };
+  while (k0 < kend) {
+    while (k0 < kend && !sees_all()) turn(Bool<false>());
+    while (k0 < kend && sees_all()) turn(Bool<true>());
   }
 
   l += __shfl_xor(l, 32);
@@ -204,32 +225,45 @@ __global__ __launch_bounds__(kAttnThreads) void attn_fwd_kernel(const AttnParams
   }
 }
 
-// Joins the parts of split rows: a wave to a row.
+// Joins the parts of split rows: a wave to a row.  Lane z takes part z's
+// statistics, so that all of their loads are under way at once.
+constexpr int kMaxSplits = 64;
+
 template <int D>
-__global__ __launch_bounds__(256) void attn_join_kernel(const AttnParams p) {
+__global__ __launch_bounds__(64) void attn_join_kernel(const AttnParams p) {
+  constexpr int kN = (D + 63) / 64;
   const int64_t rows = static_cast<int64_t>(p.B) * p.Hq * p.Tq;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (row >= rows) return;
-  const float* st = p.osplit + p.splits * rows * D;
-  float m = kLowest;
-  for (int z = 0; z < p.splits; ++z) m = fmaxf(m, st[2 * (z * rows + row)]);
-  float l = 0.f, x[(D + 63) / 64];
+  const int64_t row = blockIdx.x;
+  const int lane = threadIdx.x;
+  const float* st = p.osplit + p.splits * rows * D + 2 * row;
+  float mine = kLowest, l = 0.f;
+  if (lane < p.splits) {
+    mine = st[2 * rows * lane];
+    l = st[2 * rows * lane + 1];
+  }
+  float m = mine;
 #pragma unroll
-  for (int c = 0; c < (D + 63) / 64; ++c) x[c] = 0.f;
+  for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+  const float f = exp2_hw(mine - m);
+  l *= f;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
+  float x[kN];
+#pragma unroll
+  for (int c = 0; c < kN; ++c) x[c] = 0.f;
+#pragma unroll 8
   for (int z = 0; z < p.splits; ++z) {
-    const float f = exp2_hw(st[2 * (z * rows + row)] - m);
-    l += f * st[2 * (z * rows + row) + 1];
+    const float fz = __shfl(f, z);
 #pragma unroll
-    for (int c = 0; c < (D + 63) / 64; ++c)
-      if (lane + 64 * c < D) x[c] += f * p.osplit[(z * rows + row) * D + lane + 64 * c];
+    for (int c = 0; c < kN; ++c)
+      if (lane + 64 * c < D) x[c] += fz * p.osplit[(z * rows + row) * D + lane + 64 * c];
   }
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
   const int64_t bh = row / p.Tq;
   const int i = static_cast<int>(row % p.Tq);
   bf16* o = p.o + (bh / p.Hq) * p.os.b + i * p.os.t + (bh % p.Hq) * p.os.h;
 #pragma unroll
-  for (int c = 0; c < (D + 63) / 64; ++c)
+  for (int c = 0; c < kN; ++c)
     if (lane + 64 * c < D) o[lane + 64 * c] = static_cast<bf16>(x[c] * inv);
   if (lane == 0) p.lse[row] = l == 0.f ? -kInf : (m + log2_hw(l)) * kLn2;
 }
@@ -247,7 +281,7 @@ Split choose_split(int B, int Tq, int Tk, int Hq) {
   const int tiles = (Tk + kTile - 1) / kTile;
   int64_t n = 512 / (groups > 0 ? groups : 1);
   if (n > tiles / 4) n = tiles / 4;        // at least 4 tiles to a part
-  if (n > 64) n = 64;
+  if (n > kMaxSplits) n = kMaxSplits;
   if (n < 2) return {1, tiles};
   const int each = static_cast<int>((tiles + n - 1) / n);
   return {(tiles + each - 1) / each, each};
@@ -255,8 +289,8 @@ Split choose_split(int B, int Tq, int Tk, int Hq) {
 
 template <int D, bool CAP, bool BIAS>
 hipError_t run_fwd(const AttnParams& p, hipStream_t s) {
-  const size_t lds = 4 * sizeof(bf16) * kTile * kPitch<D> + 2 * kWaves * sizeof(int) +
-                     (BIAS ? (2 * p.reach + 1) * sizeof(float) : 0);
+  const size_t lds = 4 * kTileBytes<D> + 2 * kWaves * sizeof(int) +
+                     (BIAS ? bias_entries(p.reach) * sizeof(float) : 0);
   const dim3 grid(p.B * p.Hq, (p.Tq + 127) / 128, p.splits);
   if (p.splits > 1) {
     const auto fn = attn_fwd_kernel<D, CAP, BIAS, true>;
@@ -268,7 +302,7 @@ hipError_t run_fwd(const AttnParams& p, hipStream_t s) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t rows = static_cast<int64_t>(p.B) * p.Hq * p.Tq;
-    attn_join_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 256, 0, s>>>(p);
+    attn_join_kernel<D><<<static_cast<unsigned>(rows), 64, 0, s>>>(p);
   } else {
     const auto fn = attn_fwd_kernel<D, CAP, BIAS, false>;
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
