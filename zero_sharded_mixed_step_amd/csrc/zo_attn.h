@@ -41,11 +41,6 @@ __device__ __forceinline__ constexpr int swizzle(int r) {
 template <int D>
 constexpr int kTileBytes = kTile * D * 2;
 
-template <bool V>
-struct Bool {
-  static constexpr bool value = V;
-};
-
 struct Strides3 {
   int64_t b, t, h;
 };
@@ -66,10 +61,10 @@ struct AttnParams {
   Strides3 qs, ks, vs, os, dos, dqs, dks, dvs;
   // workspace
   int tq64;         // Tq up to a multiple of 64: the rows below are padded to it
-  float* lse2;      // [B][Hq][tq64]  lse * log2(e), +inf for a query without keys
+  float* base;      // [B][Hq][tq64]  -lse * log2(e), plus cap * log2(e); -inf: no keys
   float* delta;     // [B][Hq][tq64]  do . o
   int *qlo, *qhi;   // [B][tq64]      the keys a query sees; 0, 0 for none
-  float* dpart;     // [B][Hq][query tiles][n_buckets]
+  float* dpart;     // [B][Hq][query tiles][bias_entries]: ds by distance
   float* kvpart;    // [2][parts][B][Hk][Tk][D]: dk and dv of parts of a group's heads
   int parts;        // 1: no parts
   float* osplit;    // split forward: [splits][B * Hq * Tq][D] and, behind it, two statistics
@@ -141,11 +136,11 @@ struct FragAt {
 // Operand fragment, contraction along the row: rows 32 t + l % 32, elements
 // 16 c + 8 (l / 32) .. + 7.  (Swizzles repeat after 8 rows, and piece 2 c + half
 // is 2 c ^ half: moving along the row is one exclusive or, or for swizzles of
-// one bit a sum.)
+// one bit a sum.  `beyond`: of a tile that lies so many bytes behind, a constant.)
 template <int D>
-__device__ __forceinline__ bf16x8 frag_rows(const FragAt<D>& at, int t, int c) {
-  const uint32_t x = (D == 64 || D == 128 ? at.rows ^ (c << 5) : at.rows + (c << 5)) + t * 64 * D;
-  return *reinterpret_cast<const ZO_LDS bf16x8*>(x);
+__device__ __forceinline__ bf16x8 frag_rows(const FragAt<D>& at, int t, int c, int beyond = 0) {
+  const uint32_t x = (D == 64 || D == 128 ? at.rows ^ (c << 5) : at.rows + (c << 5));
+  return *reinterpret_cast<const ZO_LDS bf16x8*>(x + (t * 64 * D + beyond));
 }
 
 // Operand fragment, contraction along the column: columns 32 t + l % 32 and, of
@@ -153,8 +148,9 @@ __device__ __forceinline__ bf16x8 frag_rows(const FragAt<D>& at, int t, int c) {
 // them.  A transposing read hands each of 16 lanes a column of the 4 x 16
 // block whose rows those lanes address by fours.
 template <int D>
-__device__ __forceinline__ bf16x8 frag_cols(const FragAt<D>& at, int u, int t) {
-  const uint32_t x = (D == 64 || D == 128 ? at.cols ^ (t << 6) : at.cols + (t << 6)) + u * 32 * D;
+__device__ __forceinline__ bf16x8 frag_cols(const FragAt<D>& at, int u, int t, int beyond = 0) {
+  const uint32_t x =
+      (D == 64 || D == 128 ? at.cols ^ (t << 6) : at.cols + (t << 6)) + (u * 32 * D + beyond);
   using P = ZO_LDS s16x4*;
   union {
     s16x4 s[2];
@@ -182,49 +178,63 @@ __device__ __forceinline__ bf16x8 to_frag(const float* x) {
   return f;
 }
 
-// Clears the fragment's elements whose bit in `keep` is 0: rows that no owned
-// row sees are weighted with 0, and whatever they hold (an uninitialised
-// padding row's NaN, say) must not reach the product.
-__device__ __forceinline__ bf16x8 keep_frag(bf16x8 f, uint32_t keep) {
-  union {
-    bf16x8 v;
-    uint32_t u[4];
-  } x;
-  x.v = f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t m = ((keep >> (2 * j)) & 1u ? 0x0000FFFFu : 0u) |
-                       ((keep >> (2 * j + 1)) & 1u ? 0xFFFF0000u : 0u);
-    x.u[j] &= m;
-  }
-  return x.v;
-}
-
-// Whether any lane of this lane's half wave has the flag set.
-__device__ __forceinline__ uint32_t any_in_half(bool f, int lane) {
-  const uint64_t m = __ballot(f);
-  const uint32_t half = lane >= 32 ? static_cast<uint32_t>(m >> 32) : static_cast<uint32_t>(m);
-  return half != 0 ? 1u : 0u;
-}
-
-// Starts the loads of a tile of 64 rows, row0 .. + 63 of `base`, straight into
-// shared memory (no registers on the way).  Rows outside [first, last) are
-// replaced by a row inside: no owned row sees them.  wait_tile() ends them.
+// Loads of tiles of 64 rows of D columns straight into shared memory (no
+// registers on the way); wait_tile() ends them.  A lane's offsets from a tile's
+// first row are formed once, and a tile inside [first, last) takes a uniform
+// base and these 32-bit offsets: forming 64-bit addresses a tile cost as much
+// as a quarter of the softmax (integer products run at a quarter of the rate).  At
+// the ends, rows outside are replaced by one inside (no owned row sees them),
+// and rows too far apart for the offsets go the same way.
 template <int D>
-__device__ __forceinline__ void load_tile(uint32_t tile, const bf16* base, int64_t stride, int row0,
-                                          int first, int last, int wave, int lane) {
+struct TileLoad {
+  static constexpr int kLoads = D / 32;                // of the workgroup's D / 8, 64 pieces each
+  // (8 rows further the swizzle is the same: loads that start there share a lane offset)
+  static constexpr int kOffs = D == 128 ? 2 : D == 64 ? 1 : kLoads;
+  const bf16* base;
+  int64_t stride;
+  int first, last;
+  bool near;
+  uint32_t off[kOffs];
+
+  __device__ __forceinline__ TileLoad(const bf16* b, int64_t s, int from, int to, int wave, int lane)
+      : base(b), stride(s), first(from), last(to) {
+    near = s >= 0 && s < (1 << 23);
 #pragma unroll
-  for (int u = 0; u < D / 32; ++u) {
-    const int n = wave * (D / 32) + u;                 // of D / 8 loads of 64 pieces
-    const int piece = n * 64 + lane;
-    const int r = piece / (D / 8), c = (piece % (D / 8)) ^ swizzle<D>(r);
-    const int row = min(max(row0 + r, first), last - 1);
-    const bf16* src = base + row * stride + c * 8;
-    __builtin_amdgcn_global_load_lds(
-        (const __attribute__((address_space(1))) void*)src,
-        reinterpret_cast<ZO_LDS void*>(tile + n * 1024), 16, 0, 0);
+    for (int u = 0; u < kOffs; ++u) {
+      const int piece = (wave * kLoads + u) * 64 + lane;
+      const int r = piece / (D / 8), c = (piece % (D / 8)) ^ swizzle<D>(r);
+      off[u] = static_cast<uint32_t>(r) * static_cast<uint32_t>(s) * 2u + c * 16u;
+    }
   }
-}
+
+  __device__ __forceinline__ void start(uint32_t tile, int row0, int wave, int lane) const {
+    using Global = const __attribute__((address_space(1))) void*;
+    using Shared = ZO_LDS void*;
+    const uint32_t to = tile + wave * (kLoads * 1024);
+    if (near && row0 >= first && row0 + kTile <= last) {
+      // (a buffer descriptor, because it takes a 32-bit offset a lane; its type is not
+      // known to the compiler's pass over the host's side)
+#ifdef __HIP_DEVICE_COMPILE__
+      const auto from = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<bf16*>(base + row0 * stride), 0, -1, 0x00020000);
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(from, reinterpret_cast<Shared>(to + u * 1024), 16,
+                                                 off[u % kOffs],
+                                                 static_cast<int>((u / kOffs) * 16 * stride), 0, 0);
+#endif
+    } else {
+#pragma unroll 1
+      for (int u = 0; u < kLoads; ++u) {
+        const int piece = (wave * kLoads + u) * 64 + lane;
+        const int r = piece / (D / 8), c = (piece % (D / 8)) ^ swizzle<D>(r);
+        const bf16* from = base + min(max(row0 + r, first), last - 1) * stride + c * 8;
+        __builtin_amdgcn_global_load_lds((Global)from, reinterpret_cast<Shared>(to + u * 1024), 16,
+                                         0, 0);
+      }
+    }
+  }
+};
 
 // The same for 64 words of a padded array, by one wave.
 __device__ __forceinline__ void load_words(uint32_t to, const void* from, int lane) {
@@ -257,16 +267,28 @@ __device__ __forceinline__ int bias_bucket(const AttnParams& p, int d) {
   return min(max(p.buckets[min(max(d, -p.reach), p.reach) + p.reach], 0), p.n_buckets - 1);
 }
 
-// The head's bias into shared memory.  A finite bias stays finite.
+// The head's bias into shared memory.  A finite bias stays finite.  (Each entry
+// is two loads, one after the other: four entries a thread are under way at once.)
 __device__ __forceinline__ void stage_bias(const AttnParams& p, int h, float* out, int tid) {
-  const int span = bias_span(p.reach);
-  for (int d = tid - span; d <= span; d += kAttnThreads) {
-    const int64_t at = static_cast<int64_t>(bias_bucket(p, d)) * p.Hq + h;
-    const float b = p.table_f32 ? static_cast<const float*>(p.table)[at]
-                                : static_cast<float>(static_cast<const bf16*>(p.table)[at]);
-    const float x = b * kLog2e;
-    out[d + span] =
-        __builtin_isinf(x) && !__builtin_isinf(b) ? __builtin_copysignf(-kLowest, b) : x;
+  constexpr int kAtOnce = 4;
+  const int span = bias_span(p.reach), n = bias_entries(p.reach);
+  for (int e0 = tid; e0 < n; e0 += kAtOnce * kAttnThreads) {
+    int64_t at[kAtOnce];
+    float b[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k)
+      at[k] = static_cast<int64_t>(bias_bucket(p, min(e0 + k * kAttnThreads, n - 1) - span)) * p.Hq + h;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k)
+      b[k] = p.table_f32 ? static_cast<const float*>(p.table)[at[k]]
+                         : static_cast<float>(static_cast<const bf16*>(p.table)[at[k]]);
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const float x = b[k] * kLog2e;
+      if (e0 + k * kAttnThreads < n)
+        out[e0 + k * kAttnThreads] =
+            __builtin_isinf(x) && !__builtin_isinf(b[k]) ? __builtin_copysignf(-kLowest, b[k]) : x;
+    }
   }
 }
 
@@ -309,6 +331,94 @@ __device__ __forceinline__ bf16x8 signed_frag(bf16x8 f, bool flip) {
 // heads of a key head together.
 __device__ __forceinline__ int head_of_group(int x, int n) {
   return n % 8 == 0 ? (x % 8) * (n / 8) + x / 8 : x;
+}
+
+// Writes zeros over the rows of two staged tiles whose bit in `rows` is 0, by
+// the whole workgroup.
+template <int D>
+__device__ __forceinline__ void clear_rows(uint32_t tile0, uint32_t tile1, uint64_t rows, int tid) {
+  for (int piece = tid; piece < kTile * D / 8; piece += kAttnThreads)
+    if (!((rows >> (piece / (D / 8))) & 1)) {
+      *reinterpret_cast<ZO_LDS u32x4*>(tile0 + piece * 16) = u32x4{0, 0, 0, 0};
+      *reinterpret_cast<ZO_LDS u32x4*>(tile1 + piece * 16) = u32x4{0, 0, 0, 0};
+    }
+}
+
+// Whether some key between the first and the last that a workgroup's 128
+// queries see is seen by none of them (padding between documents).  Such a key may
+// hold anything, a NaN too, and is cleared from the staged tile, since a weight of 0 does
+// not stop a NaN.  Keys in no gap are seen by a query of the workgroup, so what
+// they hold counts; without gaps nothing needs clearing.  A range's end that
+// lies in no other range, short of the last end, begins a gap.
+// Ranges whose ends do not step back, none empty, as of causal documents and
+// prefixes, are compared with their neighbours only.
+__device__ __forceinline__ bool has_gaps(const int2* ranges, int last, int tid) {
+  const int k = tid & 127;
+  const int2 r = ranges[k], next = ranges[k < 127 ? k + 1 : k];
+  const bool plain = r.y > r.x && next.x >= r.x && next.y >= r.y;
+  if (__syncthreads_and(plain)) return __syncthreads_or(next.x > r.y) != 0;
+  bool gap = false;
+  if (r.y > r.x && r.y < last) {
+    bool inside = false;
+    for (int i = 0; i < 128; ++i) inside |= ranges[i].x <= r.y && ranges[i].y > r.y;
+    gap = !inside;
+  }
+  return __syncthreads_or(gap) != 0;
+}
+
+// The keys k0 .. + 63 that some of the 128 queries see; `flags`: 2 words.
+__device__ __forceinline__ uint64_t seen_keys(const int2* ranges, int k0, uint32_t* flags, int tid) {
+  __syncthreads();
+  if (tid < 2) flags[tid] = 0;
+  __syncthreads();
+  const int j = k0 + (tid & 63);
+  bool seen = false;
+  for (int k = 32 * (tid >> 6); k < 32 * (tid >> 6) + 32; ++k)
+    seen |= j >= ranges[k].x && j < ranges[k].y;
+  if (seen) atomicOr(&flags[(tid & 63) >> 5], 1u << (tid & 31));
+  __syncthreads();
+  return flags[0] | static_cast<uint64_t>(flags[1]) << 32;
+}
+
+// Which tile the workgroup at place y of its batch row's launch order takes:
+// the one of rank y by decreasing cost (ties by index), so that the longest start first
+// and the last to start are short; documents give a tile's cost no order that its index
+// would tell.  cost(t) is an estimate; `scratch`: n + 1 words, n <= 256.
+template <typename Cost>
+__device__ __forceinline__ int tile_of_rank(int y, int n, int* scratch, int tid, Cost cost) {
+  if (tid < n) scratch[tid] = cost(tid);
+  __syncthreads();
+  if (tid < n) {
+    const int mine = scratch[tid];
+    int rank = 0;
+    for (int k = 0; k < n; ++k) rank += scratch[k] > mine || (scratch[k] == mine && k < tid);
+    if (rank == y) scratch[n] = tid;
+  }
+  __syncthreads();
+  const int t = scratch[n];
+  __syncthreads();
+  return t;
+}
+constexpr int kMinRanked = 16, kMaxRanked = 255;   // (a few tiles are not worth the ranking)
+
+// The same for a tile of 128 queries: its cost is the span of keys that four of its
+// queries see.  Without ranges, or where all workgroups run at once anyway (two to a
+// compute unit), the last tile first: the order of a causal mask.
+__device__ __forceinline__ int query_tile(const AttnParams& p, int b, int* scratch, int tid) {
+  const int n = gridDim.y, y = blockIdx.y;
+  if (!p.ranges || n < kMinRanked || n > kMaxRanked || gridDim.x * n <= 512) return n - 1 - y;
+  return tile_of_rank(y, n, scratch, tid, [&](int t) {
+    int lo = 0x7FFFFFFF, hi = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int2 r = key_range(p, b, min(128 * t + 42 * k, p.Tq - 1));
+      if (r.y > r.x) {
+        lo = min(lo, r.x);
+        hi = max(hi, r.y);
+      }
+    }
+    return max(hi - lo, 0);
+  });
 }
 
 AttnParams attn_params(const zero_attn_args& a);

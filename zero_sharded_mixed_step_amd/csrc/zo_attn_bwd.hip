@@ -4,8 +4,8 @@
 // lse in both: 7 matrix products instead of the 5 of a kernel that adds dq
 // through memory, for gradients that have one fixed order of summation.
 //
-// A first kernel leaves delta = do . o and the lse in units of log2 in the
-// workspace, and the ranges, clipped, all padded to whole tiles of 64 queries.
+// A first kernel leaves delta = do . o, minus the lse in units of log2 and the
+// ranges, clipped, in the workspace, all padded to whole tiles of 64 queries.
 #include "zo_attn.h"
 #include "zo_internal.h"
 
@@ -35,7 +35,7 @@ __global__ __launch_bounds__(256) void attn_bwd_prepare_kernel(const AttnParams 
     p.delta[row] = sum;
     float lse = -kInf;
     if (r.y > r.x) lse = p.lse[static_cast<int64_t>(bh) * p.Tq + i];
-    p.lse2[row] = lse != -kInf ? lse * kLog2e : kInf;
+    p.base[row] = lse != -kInf ? (p.cap > 0.f ? p.cap * kLog2e : 0.f) - lse * kLog2e : -kInf;
     if (h == 0) {
       p.qlo[static_cast<int64_t>(b) * p.tq64 + i] = r.x;
       p.qhi[static_cast<int64_t>(b) * p.tq64 + i] = r.y;
@@ -43,8 +43,8 @@ __global__ __launch_bounds__(256) void attn_bwd_prepare_kernel(const AttnParams 
   }
 }
 
-// One score's p, ds and dx, from the raw product x, dp, and base = bias - lse2 (plus c2
-// with a cap).  With a cap, u = (1 - tanh) / 2 and dx is a quarter of ds (1 -
+// One score's p, ds and dx, from the raw product x, dp, and base = bias - lse (in log2,
+// plus c2 with a cap).  With a cap, u = (1 - tanh) / 2 and dx is a quarter of ds (1 -
 // tanh^2) = 4 ds u (1 - u): the 4 goes into the gradients' final scale.
 template <bool CAP>
 __device__ __forceinline__ void grad_score(float x, float base, float dp, float delta,
@@ -64,17 +64,30 @@ __device__ __forceinline__ void grad_score(float x, float base, float dp, float 
 
 // ---------------------------------------------------------------- dk, dv ---
 
-// One tile of 64 queries for a wave's 32 keys.  FULL: every query sees every key.
-template <int D, bool CAP, bool BIAS, bool FULL>
+// The bits 0 .. n - 1 (n from below 0 to above 64).
+__device__ __forceinline__ uint64_t bits_below(int n) {
+  return n <= 0 ? 0 : n >= 64 ? ~uint64_t(0) : (uint64_t(1) << n) - 1;
+}
+
+// One tile of 64 queries, do's behind q's, for a wave's 32 keys.
+template <int D, bool CAP, bool BIAS>
 __device__ __forceinline__ void attn_dkv_tile(const AttnParams& p, const FragAt<D>& qt,
-                                              const FragAt<D>& gt, const float* stat,
+                                              uint32_t stat,
                                               const bf16x8 (&kf)[D / 16],
                                               const bf16x8 (&vf)[D / 16], f32x16 (&dk)[D / 32],
                                               f32x16 (&dv)[D / 32], int j, int jw, int i0,
                                               const ScoreFactors& f, const float* bias, int lane) {
+  constexpr int kG = 2 * kTileBytes<D>;  // from q's tile to do's
   const int half = lane >> 5;
-  const int* lo = reinterpret_cast<const int*>(stat) + 2 * kTile;
-  const int* hi = lo + kTile;
+  // the lane's places in the tile's words (opaque: one register each, not one a use)
+  uint32_t quads = stat + 16 * half, words = stat + 4 * (lane & 31);
+  asm volatile("" : "+v"(quads), "+v"(words));
+  const auto quad = [&](int array, int at) {   // words at + 4 half .. + 3 of an array
+    return *reinterpret_cast<const ZO_LDS f32x4*>(quads + 4 * (array * kTile + at));
+  };
+  const auto word = [&](int array, int at) {   // word at + l % 32
+    return *reinterpret_cast<const ZO_LDS int*>(words + 4 * (array * kTile + at));
+  };
 #pragma unroll
   for (int s = 0; s < 2; ++s) {          // 32 queries at a time
     f32x16 x, dp;
@@ -83,68 +96,84 @@ __device__ __forceinline__ void attn_dkv_tile(const AttnParams& p, const FragAt<
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) x = mfma(frag_rows<D>(qt, s, c), kf[c], x);
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) dp = mfma(frag_rows<D>(gt, s, c), vf[c], dp);
+    for (int c = 0; c < D / 16; ++c) dp = mfma(frag_rows<D>(qt, s, c, kG), vf[c], dp);
     const int d0 = jw - (i0 + 32 * s + p.off);         // distances span d0 - 31 .. d0 + 31
     const int side = BIAS ? bias_side(d0 - 31, d0 + 31, p.reach) : 1;
     const float* row = bias + d0 + (lane & 31) - 4 * half + bias_span(p.reach);
     const float end = BIAS ? bias[side < 0 ? 0 : 2 * bias_span(p.reach)] : 0.f;
-    float pr[16], dx[16];
-    uint32_t keep[2] = {0, 0};
+    const bool full = __all(word(2, 32 * s) <= jw && word(3, 32 * s) >= jw + 32);
+    bf16x8 pf[2], xf[2];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int at = 32 * s + 8 * g + 4 * half;
-      const f32x4 lse = *reinterpret_cast<const f32x4*>(stat + at);
-      const f32x4 del = *reinterpret_cast<const f32x4*>(stat + kTile + at);
+    for (int u = 0; u < 2; ++u) {
+      float pr[8], dx[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = 4 * g + e;
-        float base = (CAP ? f.c2 : 0.f) - lse[e];
-        if constexpr (BIAS) base += side != 0 ? end : row[-(8 * g + e)];
-        float ds;
-        grad_score<CAP>(x[r], base, dp[r], del[e], f, pr[r], ds, dx[r]);
-        if constexpr (!FULL) {
-          const bool seen = j >= lo[at + e] && j < hi[at + e];
-          pr[r] = seen ? pr[r] : 0.f;
-          dx[r] = seen ? dx[r] : 0.f;
-          keep[r >> 3] |= any_in_half(seen, lane) << (r & 7);
+      for (int g = 0; g < 2; ++g) {
+        const int at = 32 * s + 16 * u + 8 * g;
+        f32x4 base4 = quad(0, at);
+        const f32x4 del = quad(1, at);
+        if (!full) {
+          const f32x4 lo = quad(2, at), hi = quad(3, at);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (j < __float_as_int(lo[e]) || j >= __float_as_int(hi[e])) base4[e] = -kInf;  // p = 0
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int k = 4 * g + e, r = 8 * u + k;
+          float base = base4[e], ds;
+          if constexpr (BIAS) base += side != 0 ? end : row[-(16 * u + 8 * g + e)];
+          grad_score<CAP>(x[r], base, dp[r], del[e], f, pr[k], ds, dx[k]);
         }
       }
+      pf[u] = to_frag(pr);
+      xf[u] = to_frag(dx);
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const bf16x8 pf = to_frag(pr + 8 * u), xf = to_frag(dx + 8 * u);
 #pragma unroll
       for (int t = 0; t < D / 32; ++t) {
-        bf16x8 of = frag_cols<D>(gt, 2 * s + u, t);
-        if constexpr (!FULL) of = keep_frag(of, keep[u]);
-        dv[t] = mfma(of, pf, dv[t]);
-      }
-#pragma unroll
-      for (int t = 0; t < D / 32; ++t) {
-        bf16x8 qf = frag_cols<D>(qt, 2 * s + u, t);
-        if constexpr (!FULL) qf = keep_frag(qf, keep[u]);
-        dk[t] = mfma(qf, xf, dk[t]);
+        dv[t] = mfma(frag_cols<D>(qt, 2 * s + u, t, kG), pf[u], dv[t]);
+        dk[t] = mfma(frag_cols<D>(qt, 2 * s + u, t), xf[u], dk[t]);
       }
     }
   }
 }
 
+// Which tile of 128 keys a workgroup takes: the most often seen first (see query_tile),
+// by 256 queries spread over the row.
+__device__ __forceinline__ int key_tile(const AttnParams& p, int b, int* scratch, int tid) {
+  const int n = gridDim.y, y = blockIdx.y;
+  if (!p.ranges || n < kMinRanked || n > kMaxRanked || gridDim.x * n <= 512) return y;
+  int* part = scratch + kMaxRanked + 1;                // [kWaves][n]
+  const int64_t i = static_cast<int64_t>(b) * p.tq64 + static_cast<int64_t>(tid) * p.Tq / 256;
+  const int lo = p.qlo[i], hi = p.qhi[i];
+  for (int t = 0; t < n; ++t) {
+    const int seen = __popcll(__ballot(lo < 128 * t + 128 && hi > 128 * t));
+    if ((tid & 63) == 0) part[(tid >> 6) * n + t] = seen;
+  }
+  __syncthreads();
+  return tile_of_rank(y, n, scratch, tid, [&](int t) {
+    return part[t] + part[n + t] + part[2 * n + t] + part[3 * n + t];
+  });
+}
+
 // A workgroup owns 128 keys of one key head, 32 to a wave, and walks tiles of
 // 64 queries of the query heads that share it, or of a part of them.
 template <int D, bool CAP, bool BIAS>
-__global__ __launch_bounds__(kAttnThreads, D >= 96 ? 1 : 2) void attn_dkv_kernel(const AttnParams p) {
-  constexpr int kStat = 4 * kTile * 4;                 // lse2, delta, lo, hi of a tile
+__global__ __launch_bounds__(kAttnThreads, D > 64 ? 1 : 2) void attn_dkv_kernel(const AttnParams p) {
+  constexpr int kStat = 4 * kTile * 4;                 // base, delta, lo, hi of a tile
   extern __shared__ __align__(1024) char smem[];       // [2] tiles of q, of do
   const uint32_t tiles = lds_address(smem);
   char* stats = smem + 4 * kTileBytes<D>;              // [2] kStat
   int* span = reinterpret_cast<int*>(stats + 2 * kStat);             // [kWaves][2]
-  float* bias = reinterpret_cast<float*>(span + 2 * kWaves);
+  uint32_t* seen_by = reinterpret_cast<uint32_t*>(span + 2 * kWaves);       // [kWaves][4]
+  float* bias = reinterpret_cast<float*>(seen_by + 4 * kWaves);
 
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int bx = head_of_group(blockIdx.x, gridDim.x);
   const int part = bx % p.parts, bk = bx / p.parts, b = bk / p.Hk, hk = bk % p.Hk;
-  const int j0 = blockIdx.y * 128;                     // the workgroup's first key
+  const int j0 = key_tile(p, b, reinterpret_cast<int*>(smem), tid) * 128;   // its first key
   const int jw = j0 + wave * 32, j = jw + (lane & 31);
   const int* qlo = p.qlo + static_cast<int64_t>(b) * p.tq64;
   const int* qhi = p.qhi + static_cast<int64_t>(b) * p.tq64;
@@ -152,13 +181,16 @@ __global__ __launch_bounds__(kAttnThreads, D >= 96 ? 1 : 2) void attn_dkv_kernel
   const FragAt<D> at(lane);
   const int heads = p.group / p.parts, h0 = hk * p.group + part * heads;
 
-  // the tiles of queries that see any of the keys lie in [qa, qb)
+  // the tiles of queries that see any of the keys lie in [qa, qb); and the keys seen
   int qa = 0x7FFFFFFF, qb = 0;
+  uint64_t seen_lo = 0, seen_hi = 0;
   for (int i = tid; i < p.tq64; i += kAttnThreads) {
-    const int lo = qlo[i], hi = qhi[i];
-    if (lo < j0 + 128 && hi > j0 && hi > lo) {
+    const int lo = max(qlo[i] - j0, 0), hi = min(qhi[i] - j0, 128);
+    if (lo < hi) {
       qa = min(qa, i / kTile);
       qb = max(qb, i / kTile + 1);
+      seen_lo |= bits_below(hi) & ~bits_below(lo);
+      seen_hi |= bits_below(hi - 64) & ~bits_below(lo - 64);
     }
   }
 #pragma unroll
@@ -170,7 +202,15 @@ __global__ __launch_bounds__(kAttnThreads, D >= 96 ? 1 : 2) void attn_dkv_kernel
     span[2 * wave] = qa;
     span[2 * wave + 1] = qb;
   }
-  if constexpr (BIAS) stage_bias(p, h0, bias, tid);    // (a bias goes with one head a workgroup)
+  const uint32_t mine[4] = {static_cast<uint32_t>(seen_lo), static_cast<uint32_t>(seen_lo >> 32),
+                            static_cast<uint32_t>(seen_hi), static_cast<uint32_t>(seen_hi >> 32)};
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    uint32_t x = mine[w];
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) x |= __shfl_xor(x, d);
+    if (lane == 0) seen_by[4 * wave + w] = x;
+  }
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) {
@@ -181,16 +221,16 @@ __global__ __launch_bounds__(kAttnThreads, D >= 96 ? 1 : 2) void attn_dkv_kernel
   qa = __builtin_amdgcn_readfirstlane(min(qa, qb));
   const int turns = (qb - qa) * heads;
 
+  TileLoad<D> ql(p.q + b * p.qs.b + h0 * p.qs.h, p.qs.t, 0, p.Tq, wave, lane);
+  TileLoad<D> ol(p.d_o + b * p.dos.b + h0 * p.dos.h, p.dos.t, 0, p.Tq, wave, lane);
   int head = 0, qi = qa;                               // of the next tile to stage
   const auto stage = [&](int buf) {
     const int64_t bh = static_cast<int64_t>(b) * p.Hq + h0 + head;
-    const bf16* qg = p.q + b * p.qs.b + (h0 + head) * p.qs.h;
-    const bf16* og = p.d_o + b * p.dos.b + (h0 + head) * p.dos.h;
-    load_tile<D>(tiles + buf * kTileBytes<D>, qg, p.qs.t, qi * kTile, 0, p.Tq, wave, lane);
-    load_tile<D>(tiles + (2 + buf) * kTileBytes<D>, og, p.dos.t, qi * kTile, 0, p.Tq, wave, lane);
+    ql.start(tiles + buf * kTileBytes<D>, qi * kTile, wave, lane);
+    ol.start(tiles + (2 + buf) * kTileBytes<D>, qi * kTile, wave, lane);
     const uint32_t to = tiles + 4 * kTileBytes<D> + buf * kStat + wave * kTile * 4;
     const int i0 = qi * kTile;
-    const void* from = wave == 0   ? static_cast<const void*>(p.lse2 + bh * p.tq64 + i0)
+    const void* from = wave == 0   ? static_cast<const void*>(p.base + bh * p.tq64 + i0)
                        : wave == 1 ? static_cast<const void*>(p.delta + bh * p.tq64 + i0)
                        : wave == 2 ? static_cast<const void*>(qlo + i0)
                                    : static_cast<const void*>(qhi + i0);
@@ -198,6 +238,8 @@ __global__ __launch_bounds__(kAttnThreads, D >= 96 ? 1 : 2) void attn_dkv_kernel
     if (++qi == qb) {
       qi = qa;
       ++head;
+      ql.base += p.qs.h;
+      ol.base += p.dos.h;
     }
   };
   if (turns > 0) stage(0);
@@ -206,10 +248,16 @@ __global__ __launch_bounds__(kAttnThreads, D >= 96 ? 1 : 2) void attn_dkv_kernel
     const int64_t jj = min(j, p.Tk - 1);
     const bf16* k = p.k + b * p.ks.b + jj * p.ks.t + hk * p.ks.h;
     const bf16* v = p.v + b * p.vs.b + jj * p.vs.t + hk * p.vs.h;
+    // (a key that no query sees may hold anything)
+    const uint32_t any = seen_by[wave] | seen_by[4 + wave] | seen_by[8 + wave] | seen_by[12 + wave];
+    const bool seen = (any >> (lane & 31)) & 1;
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) {
-      kf[c] = signed_frag(load8(k + 16 * c + 8 * half), f.flip);
-      vf[c] = load8(v + 16 * c + 8 * half);
+      kf[c] = vf[c] = bf16x8{};
+      if (seen) {
+        kf[c] = signed_frag(load8(k + 16 * c + 8 * half), f.flip);
+        vf[c] = load8(v + 16 * c + 8 * half);
+      }
     }
   }
   f32x16 dk[D / 32], dv[D / 32];
@@ -217,37 +265,36 @@ __global__ __launch_bounds__(kAttnThreads, D >= 96 ? 1 : 2) void attn_dkv_kernel
   for (int t = 0; t < D / 32; ++t)
 #pragma unroll
     for (int r = 0; r < 16; ++r) dk[t][r] = dv[t][r] = 0.f;
+  if constexpr (BIAS) stage_bias(p, h0, bias, tid);    // (a bias goes with one head a workgroup)
   wait_tile();
 
   int n = 0, buf = 0, i0 = qa * kTile;                 // of the tile at hand
   const auto stat_of = [&] { return reinterpret_cast<const float*>(stats + buf * kStat); };
-  const auto turn = [&](auto full) {
+  const auto word = [&](int k) { return reinterpret_cast<const int*>(stat_of())[k * kTile + lane]; };
+  const auto turn = [&](auto work) {
     if (n + 1 < turns) stage(buf ^ 1);
-    const float* stat = stat_of();
-    bool some = full.value;
-    if constexpr (!full.value) {
-      const int lo = reinterpret_cast<const int*>(stat)[2 * kTile + lane];
-      const int hi = reinterpret_cast<const int*>(stat)[3 * kTile + lane];
-      some = __any(lo < jw + 32 && hi > jw && hi > lo) != 0;
+    // a query that sees nothing (padding) may hold anything: cleared, since a weight of 0
+    // does not stop a NaN
+    const uint64_t seeing = __ballot(word(3) > word(2));
+    if (~seeing != 0) {
+      clear_rows<D>(tiles + buf * kTileBytes<D>, tiles + (2 + buf) * kTileBytes<D>, seeing, tid);
+      __syncthreads();
     }
-    if (some) {
-      const FragAt<D> qt = at.in(tiles + buf * kTileBytes<D>);
-      const FragAt<D> gt = at.in(tiles + (2 + buf) * kTileBytes<D>);
-      attn_dkv_tile<D, CAP, BIAS, full.value>(p, qt, gt, stat, kf, vf, dk, dv, j, jw, i0, f, bias,
-                                              lane);
-    }
+    work();
     wait_tile();
     ++n;
     buf ^= 1;
     i0 = i0 + kTile == qb * kTile ? qa * kTile : i0 + kTile;
   };
-  const auto sees_all = [&] {
-    const int* stat = reinterpret_cast<const int*>(stat_of());
-    return __all(stat[2 * kTile + lane] <= jw && stat[3 * kTile + lane] >= jw + 32) != 0;
-  };
+  const auto seen = [&] { return __any(word(2) < jw + 32 && word(3) > jw) != 0; };
   while (n < turns) {
-    while (n < turns && !sees_all()) turn(Bool<false>());
-    while (n < turns && sees_all()) turn(Bool<true>());
+    while (n < turns && !seen()) turn([] {});
+    while (n < turns && seen())
+      turn([&] {
+        attn_dkv_tile<D, CAP, BIAS>(p, at.in(tiles + buf * kTileBytes<D>),
+                                    tiles + 4 * kTileBytes<D> + buf * kStat, kf, vf, dk, dv,
+                                    j, jw, i0, f, bias, lane);
+      });
   }
 
   if (j >= p.Tk) return;
@@ -317,13 +364,48 @@ __global__ __launch_bounds__(256) void attn_dkv_join_kernel(const AttnParams p, 
 
 // ------------------------------------------------ dq and the bias gradient ---
 
-// One tile of 64 keys for a wave's 32 queries.  `mine`: the half wave's sums of ds by
-// distance (nullptr: not wanted), at distance 0 - lane; `ends`: of the distances past the reach.
-template <int D, bool CAP, bool BIAS, bool FULL>
+// Adds a 32 x 32 block's ds, summed along its diagonals, to the wave's sums by
+// distance at `mine`, of which entry `at` is that of the diagonal through the
+// block's corner.  The block is written to shared memory with every row (key)
+// turned by its number, so that entry (j - i) mod 32 of row j is that of query i; lane
+// c + 32 h then sums column c over the rows at or below the main diagonal (h = 0:
+// distance c) or above it (h = 1: distance c - 32).  Adding each value to its
+// distance by an atomic in shared memory took ten times as long: those go a
+// lane at a time.
+constexpr int kDiagWords = 32 * 32;                    // of a wave, before its sums
+__device__ __forceinline__ void add_diagonals(const float (&ds)[16], uint32_t mine, int at,
+                                              int lane) {
+  using F = ZO_LDS float*;
+  const uint32_t block = mine - 4 * kDiagWords;
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int j = result_row(r, lane);
+    *reinterpret_cast<F>(block + 4 * (32 * j + ((j - lane) & 31))) = ds[r];
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  const int c = lane & 31;
+  const bool above = lane >= 32;
+  float sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const float x = *reinterpret_cast<F>(block + 4 * (32 * j + c));
+    sum += (j < c) == above ? x : 0.f;
+  }
+  const F to = reinterpret_cast<F>(mine + 4 * (at + c - (above ? 32 : 0)));
+  *to += sum;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// One tile of 64 keys for a wave's 32 queries.  `mine`: the wave's sums of ds by
+// distance, in shared memory; `ends`: of the distances past the reach.
+template <int D, bool CAP, bool BIAS>
 __device__ __forceinline__ void attn_dq_tile(const AttnParams& p, const FragAt<D>& kt,
                                              const FragAt<D>& vt, const bf16x8 (&qf)[D / 16],
                                              const bf16x8 (&of)[D / 16], f32x16 (&dq)[D / 32],
-                                             int2 rng, float lse2, float delta, int k0, int i0,
+                                             int2 rng, float base0, float delta, int k0, int i0,
                                              const ScoreFactors& f, const float* bias,
                                              uint32_t mine, float (&ends)[2], int lane) {
 #pragma unroll
@@ -339,28 +421,34 @@ __device__ __forceinline__ void attn_dq_tile(const AttnParams& p, const FragAt<D
     const int side = BIAS ? bias_side(d0 - 31, d0 + 31, p.reach) : 1;
     const int from = d0 - (lane & 31) + 4 * (lane >> 5) + bias_span(p.reach);
     const float end = BIAS ? bias[side < 0 ? 0 : 2 * bias_span(p.reach)] : 0.f;
-    const float base0 = (CAP ? f.c2 : 0.f) - lse2;
-    float dx[16], all = 0.f;
-    uint32_t keep[2] = {0, 0};
+    float base[16];
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      const int to = 8 * (r >> 2) + (r & 3);
-      float base = base0, pr, ds;
-      if constexpr (BIAS) base += side != 0 ? end : bias[from + to];
-      grad_score<CAP>(x[r], base, dp[r], delta, f, pr, ds, dx[r]);
-      if constexpr (!FULL) {
-        const int j = k0 + 32 * s + result_row(r, lane);
-        const bool seen = j >= rng.x && j < rng.y;
-        ds = seen ? ds : 0.f;
-        dx[r] = seen ? dx[r] : 0.f;
-        keep[r >> 3] |= any_in_half(seen, lane) << (r & 7);
+      base[r] = base0;
+      if constexpr (BIAS) base[r] += side != 0 ? end : bias[from + 8 * (r >> 2) + (r & 3)];
+    }
+    if (!__all(rng.x <= k0 + 32 * s && rng.y >= k0 + 32 * s + 32)) {
+      const uint32_t n = rng.y - rng.x;
+      const int first = k0 + 32 * s + 4 * (lane >> 5) - rng.x;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const uint32_t j = first + 8 * (r >> 2) + (r & 3);
+        base[r] = j < n ? base[r] : -kInf;               // p = 0
       }
-      if constexpr (BIAS) {
-        if (side != 0)
-          all += ds;
-        else
-          __builtin_amdgcn_ds_faddf(reinterpret_cast<ZO_LDS float*>(mine + 4 * (from + to)), ds, 0,
-                                    0, false);
+    }
+    float dx[16], ds[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      float pr;
+      grad_score<CAP>(x[r], base[r], dp[r], delta, f, pr, ds[r], dx[r]);
+    }
+    float all = 0.f;
+    if constexpr (BIAS) {
+      if (side != 0) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) all += ds[r];
+      } else {
+        add_diagonals(ds, mine, d0 + bias_span(p.reach), lane);
       }
     }
     if constexpr (BIAS) ends[0] += side < 0 ? all : 0.f;
@@ -370,35 +458,33 @@ __device__ __forceinline__ void attn_dq_tile(const AttnParams& p, const FragAt<D
       const bf16x8 xf = to_frag(dx + 8 * u);
 #pragma unroll
       for (int t = 0; t < D / 32; ++t) {
-        bf16x8 kf = frag_cols<D>(kt, 2 * s + u, t);
-        if constexpr (!FULL) kf = keep_frag(kf, keep[u]);
-        dq[t] = mfma(kf, xf, dq[t]);
+        dq[t] = mfma(frag_cols<D>(kt, 2 * s + u, t), xf, dq[t]);
       }
     }
   }
 }
 
 // A workgroup owns 128 queries of one head, 32 to a wave, and walks tiles of
-// 64 keys.  With the bias, sums of ds by distance are kept per half wave in
-// shared memory: the 32 lanes of a half wave hold 32 consecutive queries, so
-// at one key row their distances, and the addresses they add to, all differ,
-// and every address has one writer at a time, in program order.  Blocks that
-// lie past the reach share a bucket and are summed in two registers instead.
+// 64 keys.  With the bias, sums of ds by distance are kept per wave in shared
+// memory; blocks that lie past the reach share a bucket and are summed in two
+// registers instead.
 template <int D, bool CAP, bool BIAS>
-__global__ __launch_bounds__(kAttnThreads, 2) void attn_dq_kernel(const AttnParams p) {
+__global__ __launch_bounds__(kAttnThreads, D > 96 && BIAS ? 1 : 2) void attn_dq_kernel(const AttnParams p) {
   extern __shared__ __align__(1024) char smem[];       // [2] tiles of k, of v
   const uint32_t tiles = lds_address(smem);
-  int* hull = reinterpret_cast<int*>(smem + 4 * kTileBytes<D>);      // [kWaves][2]
+  int2* ranges = reinterpret_cast<int2*>(smem + 4 * kTileBytes<D>);  // [128]
+  int* hull = reinterpret_cast<int*>(ranges + 128);                  // [kWaves][2]
   float* past = reinterpret_cast<float*>(hull + 2 * kWaves);         // [kWaves][2]
   float* bias = past + 2 * kWaves;                                   // [entries]
   const int entries = BIAS ? bias_entries(p.reach) : 0;
-  float* hist = bias + entries;                                      // [8][entries]
+  const int hist_words = kDiagWords + entries;                       // a block, then the sums
+  float* hist = bias + entries;                                      // [kWaves][hist_words]
 
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int bh = head_of_group(blockIdx.x, gridDim.x), b = bh / p.Hq, h = bh % p.Hq;
   const int hk = h / p.group;
-  const int tile = gridDim.y - 1 - blockIdx.y;
+  const int tile = query_tile(p, b, reinterpret_cast<int*>(ranges), tid);
   const int i0 = tile * 128 + wave * 32;
   const int i = i0 + (lane & 31);
   const ScoreFactors f(p, CAP);
@@ -410,12 +496,12 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_dq_kernel(const AttnPara
     hull[2 * wave] = wh.x;
     hull[2 * wave + 1] = wh.y;
   }
+  if (lane < 32) ranges[wave * 32 + lane] = rng;
   float ends[2] = {0.f, 0.f};
   uint32_t mine = 0;
   if constexpr (BIAS) {
-    stage_bias(p, h, bias, tid);
-    for (int d = tid; d < 8 * entries; d += kAttnThreads) hist[d] = 0.f;
-    mine = lds_address(hist + (2 * wave + half) * entries);
+    for (int d = lane; d < entries; d += 64) hist[wave * hist_words + kDiagWords + d] = 0.f;
+    mine = lds_address(hist + wave * hist_words + kDiagWords);
   }
   __syncthreads();
   int first = 0x7FFFFFFF, last = 0;
@@ -427,11 +513,11 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_dq_kernel(const AttnPara
   first = __builtin_amdgcn_readfirstlane(min(first, last));
   last = __builtin_amdgcn_readfirstlane(last);
 
-  const bf16* kg = p.k + b * p.ks.b + hk * p.ks.h;
-  const bf16* vg = p.v + b * p.vs.b + hk * p.vs.h;
+  const TileLoad<D> kl(p.k + b * p.ks.b + hk * p.ks.h, p.ks.t, first, last, wave, lane);
+  const TileLoad<D> vl(p.v + b * p.vs.b + hk * p.vs.h, p.vs.t, first, last, wave, lane);
   const auto stage = [&](int buf, int row0) {
-    load_tile<D>(tiles + buf * kTileBytes<D>, kg, p.ks.t, row0, first, last, wave, lane);
-    load_tile<D>(tiles + (2 + buf) * kTileBytes<D>, vg, p.vs.t, row0, first, last, wave, lane);
+    kl.start(tiles + buf * kTileBytes<D>, row0, wave, lane);
+    vl.start(tiles + (2 + buf) * kTileBytes<D>, row0, wave, lane);
   };
   int k0 = first & ~(kTile - 1);
   if (k0 < last) stage(0, k0);
@@ -440,38 +526,49 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_dq_kernel(const AttnPara
     const int64_t ii = min(i, p.Tq - 1);
     const bf16* q = p.q + b * p.qs.b + ii * p.qs.t + h * p.qs.h;
     const bf16* o = p.d_o + b * p.dos.b + ii * p.dos.t + h * p.dos.h;
+    // (a query that sees nothing may hold anything)
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) {
-      qf[c] = signed_frag(load8(q + 16 * c + 8 * half), f.flip);
-      of[c] = load8(o + 16 * c + 8 * half);
+      qf[c] = of[c] = bf16x8{};
+      if (rng.y > rng.x) {
+        qf[c] = signed_frag(load8(q + 16 * c + 8 * half), f.flip);
+        of[c] = load8(o + 16 * c + 8 * half);
+      }
     }
   }
   const int64_t row = static_cast<int64_t>(bh) * p.tq64 + min(i, p.tq64 - 1);
-  const float lse2 = p.lse2[row], delta = p.delta[row];
+  const float base0 = p.base[row], delta = p.delta[row];
   f32x16 dq[D / 32];
 #pragma unroll
   for (int t = 0; t < D / 32; ++t)
 #pragma unroll
     for (int r = 0; r < 16; ++r) dq[t][r] = 0.f;
+  if constexpr (BIAS) stage_bias(p, h, bias, tid);
+  const bool gaps = p.ranges && has_gaps(ranges, last, tid);
   wait_tile();
 
   int buf = 0;
-  const auto turn = [&](auto full) {
+  const auto turn = [&](auto work) {
     if (k0 + kTile < last) stage(buf ^ 1, k0 + kTile);
-    if (full.value || (wh.x < k0 + kTile && wh.y > k0)) {
-      const FragAt<D> kt = at.in(tiles + buf * kTileBytes<D>);
-      const FragAt<D> vt = at.in(tiles + (2 + buf) * kTileBytes<D>);
-      attn_dq_tile<D, CAP, BIAS, full.value>(p, kt, vt, qf, of, dq, rng, lse2, delta, k0, i0, f,
-                                             bias, mine, ends, lane);
+    if (gaps) {
+      const uint64_t seen = seen_keys(ranges, k0, reinterpret_cast<uint32_t*>(hull), tid);
+      clear_rows<D>(tiles + buf * kTileBytes<D>, tiles + (2 + buf) * kTileBytes<D>, seen, tid);
+      __syncthreads();
     }
+    work();
     wait_tile();
     k0 += kTile;
     buf ^= 1;
   };
-  const auto sees_all = [&] { return __all(rng.x <= k0 && rng.y >= k0 + kTile) != 0; };
+  const auto sees = [&] { return wh.x < k0 + kTile && wh.y > k0; };
   while (k0 < last) {
-    while (k0 < last && !sees_all()) turn(Bool<false>());
-    while (k0 < last && sees_all()) turn(Bool<true>());
+    while (k0 < last && !sees()) turn([] {});
+    while (k0 < last && sees())
+      turn([&] {
+        attn_dq_tile<D, CAP, BIAS>(p, at.in(tiles + buf * kTileBytes<D>),
+                                   at.in(tiles + (2 + buf) * kTileBytes<D>), qf, of, dq, rng, base0,
+                                   delta, k0, i0, f, bias, mine, ends, lane);
+      });
   }
 
   if (i < p.Tq) {
@@ -499,50 +596,62 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_dq_kernel(const AttnPara
       past[2 * wave + 1] = ends[1];
     }
     __syncthreads();
-    for (int d = tid; d < entries; d += kAttnThreads) {    // by distance, in the bias' place
+    float* out = p.dpart + (static_cast<int64_t>(bh) * gridDim.y + tile) * entries;
+    for (int d = tid; d < entries; d += kAttnThreads) {
       float x = 0.f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) x += hist[w * entries + d];
+      for (int w = 0; w < kWaves; ++w) x += hist[w * hist_words + kDiagWords + d];
       if (d == 0) x += past[0] + past[2] + past[4] + past[6];
       if (d == entries - 1) x += past[1] + past[3] + past[5] + past[7];
-      bias[d] = x;
-      hist[d] = __int_as_float(bias_bucket(p, d - bias_span(p.reach)));   // (its own entry)
-    }
-    __syncthreads();
-    float* out = p.dpart + (static_cast<int64_t>(bh) * gridDim.y + tile) * p.n_buckets;
-    for (int bucket = wave; bucket < p.n_buckets; bucket += kWaves) {
-      float x = 0.f;
-      for (int d = lane; d < entries; d += 64)
-        x += __float_as_int(hist[d]) == bucket ? bias[d] : 0.f;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
-      if (lane == 0) out[bucket] = x;
+      out[d] = x;
     }
   }
 }
 
-// dbias_table[bucket][h]: the parts of all batch rows and query tiles, a
-// workgroup to an element.
-__global__ __launch_bounds__(256) void attn_dtable_kernel(const AttnParams p, int tiles) {
-  __shared__ float part[256];
-  const int h = blockIdx.x, bucket = blockIdx.y, tid = threadIdx.x;
-  float x = 0.f;
-  for (int64_t n = tid; n < static_cast<int64_t>(p.B) * tiles; n += 256) {
-    const int64_t b = n / tiles, t = n % tiles;
-    x += p.dpart[((b * p.Hq + h) * tiles + t) * p.n_buckets + bucket];
+// dbias_table[.][h]: the sums by distance of all batch rows and query tiles,
+// then by bucket; a workgroup to a head.
+__global__ __launch_bounds__(1024) void attn_dtable_kernel(const AttnParams p, int tiles) {
+  extern __shared__ float sums[];                      // [groups][entries], then bucket ids
+  const int h = blockIdx.x, tid = threadIdx.x, entries = bias_entries(p.reach);
+  // as many threads to a distance as there are for all of them
+  const int groups = max(1, 1024 / entries), rows = p.B * tiles;
+  int* bucket = reinterpret_cast<int*>(sums + groups * entries);
+  for (int d = tid; d < entries; d += 1024) bucket[d] = bias_bucket(p, d - bias_span(p.reach));
+  for (int k = tid; k < groups * entries; k += 1024) {
+    const int g = k / entries, d = k % entries;
+    float x = 0.f;
+    for (int n0 = g; n0 < rows; n0 += 8 * groups) {    // 8 loads under way at a time
+      float part[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int n = n0 + u * groups;
+        part[u] = 0.f;
+        if (n < rows) {
+          const int64_t b = n / tiles, t = n % tiles;
+          part[u] = p.dpart[((b * p.Hq + h) * tiles + t) * entries + d];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) x += part[u];
+    }
+    sums[k] = x;
   }
-  part[tid] = x;
   __syncthreads();
-  for (int w = 128; w > 0; w >>= 1) {
-    if (tid < w) part[tid] += part[tid + w];
-    __syncthreads();
-  }
-  if (tid == 0) {
-    const int64_t at = static_cast<int64_t>(bucket) * p.Hq + h;
-    if (p.table_f32)
-      static_cast<float*>(p.dtable)[at] = part[0];
-    else
-      static_cast<bf16*>(p.dtable)[at] = static_cast<bf16>(part[0]);
+  const int lane = tid & 63;
+  for (int k = tid >> 6; k < p.n_buckets; k += 16) {
+    float x = 0.f;
+    for (int d = lane; d < entries; d += 64)
+      if (bucket[d] == k)
+        for (int g = 0; g < groups; ++g) x += sums[g * entries + d];
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
+    if (lane == 0) {
+      const int64_t at = static_cast<int64_t>(k) * p.Hq + h;
+      if (p.table_f32)
+        static_cast<float*>(p.dtable)[at] = x;
+      else
+        static_cast<bf16*>(p.dtable)[at] = static_cast<bf16>(x);
+    }
   }
 }
 
@@ -582,7 +691,7 @@ hipError_t run_bwd(const AttnParams& p, hipStream_t s) {
   hipError_t e = hipSuccess;
   if (p.B > 0 && p.Tk > 0) {
     e = launch_lds(attn_dkv_kernel<D, CAP, BIAS>, dim3(p.B * p.Hk * p.parts, (p.Tk + 127) / 128),
-                   staged + 8 * kTile * 4 + 2 * kWaves * 4 + n * 4, p, s);
+                   staged + 8 * kTile * 4 + 2 * kWaves * 4 + 16 * kWaves + n * 4, p, s);
     if (e != hipSuccess) return e;
     if (p.parts > 1) {
       const int64_t pieces = static_cast<int64_t>(p.B) * p.Hk * p.Tk * D / 8;
@@ -593,10 +702,13 @@ hipError_t run_bwd(const AttnParams& p, hipStream_t s) {
   }
   if (p.B > 0 && p.Tq > 0)
     e = launch_lds(attn_dq_kernel<D, CAP, BIAS>, dim3(p.B * p.Hq, tiles),
-                   staged + 4 * kWaves * 4 + 9 * n * 4, p, s);
+                   staged + 128 * 8 + 4 * kWaves * 4 +
+                       (BIAS ? n + kWaves * (kDiagWords + n) : 0) * sizeof(float),
+                   p, s);
   if (e != hipSuccess) return e;
   if (BIAS && p.dtable) {
-    attn_dtable_kernel<<<dim3(p.Hq, p.n_buckets), 256, 0, s>>>(p, tiles);
+    const int groups = 1024 / static_cast<int>(n) > 1 ? 1024 / static_cast<int>(n) : 1;
+    attn_dtable_kernel<<<p.Hq, 1024, (groups + 1) * n * 4, s>>>(p, tiles);
     e = hipGetLastError();
   }
   return e;
@@ -610,7 +722,7 @@ hipError_t pick_bwd(const AttnParams& p, hipStream_t s) {
 }
 
 // The workspace, in order; returns its size.
-size_t lay_out(AttnParams& p, int D, int n_buckets, char* base) {
+size_t lay_out(AttnParams& p, int D, size_t entries, char* base) {
   size_t at = 0;
   const auto take = [&](size_t bytes) {
     char* x = base + at;
@@ -618,12 +730,12 @@ size_t lay_out(AttnParams& p, int D, int n_buckets, char* base) {
     return x;
   };
   const size_t rows = static_cast<size_t>(p.B) * p.tq64, parts = p.parts > 1 ? p.parts : 0;
-  p.lse2 = reinterpret_cast<float*>(take(rows * p.Hq * 4));
+  p.base = reinterpret_cast<float*>(take(rows * p.Hq * 4));
   p.delta = reinterpret_cast<float*>(take(rows * p.Hq * 4));
   p.qlo = reinterpret_cast<int*>(take(rows * 4));
   p.qhi = reinterpret_cast<int*>(take(rows * 4));
   p.dpart = reinterpret_cast<float*>(
-      take(static_cast<size_t>(p.B) * p.Hq * ((p.Tq + 127) / 128) * n_buckets * 4));
+      take(static_cast<size_t>(p.B) * p.Hq * ((p.Tq + 127) / 128) * entries * 4));
   p.kvpart = reinterpret_cast<float*>(take(2 * parts * p.B * p.Hk * p.Tk * D * 4));
   return at;
 }
@@ -639,14 +751,15 @@ size_t attn_bwd_workspace(int B, int Tq, int Tk, int Hq, int Hk, int D, int n_bu
   p.Hq = Hq;
   p.Hk = Hk;
   p.parts = choose_parts(B, Tk, Hq, Hk, n_buckets > 0);
-  return lay_out(p, D, n_buckets, nullptr);
+  // (for any reach up to the largest: the size goes by the buckets)
+  return lay_out(p, D, n_buckets > 0 ? bias_entries(ZERO_ATTN_MAX_REACH) : 0, nullptr);
 }
 
 hipError_t launch_attn_bwd(const zero_attn_args& a, hipStream_t s) {
   AttnParams p = attn_params(a);
   p.tq64 = up64(a.Tq);
   p.parts = choose_parts(a.B, a.Tk, a.Hq, a.Hk, a.bias_table != nullptr);
-  lay_out(p, a.D, a.bias_table ? a.n_buckets : 0, static_cast<char*>(a.workspace));
+  lay_out(p, a.D, a.bias_table ? bias_entries(p.reach) : 0, static_cast<char*>(a.workspace));
   if (a.B > 0 && a.Tq > 0) {
     attn_bwd_prepare_kernel<<<dim3(a.B * a.Hq, p.tq64 / 64), 256, 0, s>>>(p, a.D);
     const hipError_t e = hipGetLastError();

@@ -11,8 +11,8 @@
 
 namespace zo {
 
-// One tile of 64 keys for a wave's 32 queries.  FULL: every query sees every key.
-template <int D, bool CAP, bool BIAS, bool FULL>
+// One tile of 64 keys for a wave's 32 queries.
+template <int D, bool CAP, bool BIAS>
 __device__ __forceinline__ void attn_fwd_tile(const AttnParams& p, const FragAt<D>& kt,
                                               const FragAt<D>& vt, const bf16x8 (&qf)[D / 16],
                                               f32x16 (&acc)[D / 32], float& m, float& l, int2 rng,
@@ -53,16 +53,15 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnParams& p, const FragAt<
     }
   }
   constexpr bool kU = CAP && !BIAS;      // s holds u: the smallest is the largest score
-  uint32_t keep[4] = {0, 0, 0, 0};       // per 16 keys: those that some query sees
-  if constexpr (!FULL) {
+  if (!__all(rng.x <= k0 && rng.y >= k0 + kTile)) {    // not every query sees every key
+    const uint32_t n = rng.y - rng.x;
+    const int from = k0 + 4 * (lane >> 5) - rng.x;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const int j = k0 + 32 * t + result_row(r, lane);
-        const bool seen = j >= rng.x && j < rng.y;
-        s[t][r] = seen ? s[t][r] : (kU ? kInf : -kInf);
-        keep[2 * t + (r >> 3)] |= any_in_half(seen, lane) << (r & 7);
+        const uint32_t j = from + 32 * t + 8 * (r >> 2) + (r & 3);
+        s[t][r] = j < n ? s[t][r] : (kU ? kInf : -kInf);
       }
   }
   float mx = s[0][0];
@@ -102,9 +101,7 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnParams& p, const FragAt<
     const bf16x8 pf = to_frag(e);
 #pragma unroll
     for (int t = 0; t < D / 32; ++t) {
-      bf16x8 vf = frag_cols<D>(vt, g, t);
-      if constexpr (!FULL) vf = keep_frag(vf, keep[g]);
-      acc[t] = mfma(vf, pf, acc[t]);
+      acc[t] = mfma(frag_cols<D>(vt, g, t), pf, acc[t]);
     }
   }
 }
@@ -114,14 +111,15 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnPar
   constexpr int kRows = 32 * kWaves;
   extern __shared__ __align__(1024) char smem[];      // [2] tiles of K, of V
   const uint32_t tiles = lds_address(smem);
-  int* hull = reinterpret_cast<int*>(smem + 4 * kTileBytes<D>);      // [kWaves][2]
+  int2* ranges = reinterpret_cast<int2*>(smem + 4 * kTileBytes<D>);  // [kRows]
+  int* hull = reinterpret_cast<int*>(ranges + kRows);                // [kWaves][2]
   float* bias = reinterpret_cast<float*>(hull + 2 * kWaves);
 
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int bh = head_of_group(blockIdx.x, gridDim.x), b = bh / p.Hq, h = bh % p.Hq;
   const int hk = h / p.group;
-  const int tile = gridDim.y - 1 - blockIdx.y;        // the longest rows of a causal mask first
+  const int tile = query_tile(p, b, reinterpret_cast<int*>(ranges), tid);
   const int i0 = tile * kRows + wave * 32;
   const int i = i0 + (lane & 31);
   const ScoreFactors f(p, CAP);
@@ -133,7 +131,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnPar
     hull[2 * wave] = wh.x;
     hull[2 * wave + 1] = wh.y;
   }
-  if constexpr (BIAS) stage_bias(p, h, bias, tid);
+  if (lane < 32) ranges[wave * 32 + lane] = rng;
   __syncthreads();
   int first = 0x7FFFFFFF, last = 0;
 #pragma unroll
@@ -149,11 +147,11 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnPar
     kend = min(kend, (static_cast<int>(blockIdx.z) + 1) * p.tiles_per_split * kTile);
   }
 
-  const bf16* kg = p.k + b * p.ks.b + hk * p.ks.h;
-  const bf16* vg = p.v + b * p.vs.b + hk * p.vs.h;
+  const TileLoad<D> kl(p.k + b * p.ks.b + hk * p.ks.h, p.ks.t, first, last, wave, lane);
+  const TileLoad<D> vl(p.v + b * p.vs.b + hk * p.vs.h, p.vs.t, first, last, wave, lane);
   const auto stage = [&](int buf, int row0) {
-    load_tile<D>(tiles + buf * kTileBytes<D>, kg, p.ks.t, row0, first, last, wave, lane);
-    load_tile<D>(tiles + (2 + buf) * kTileBytes<D>, vg, p.vs.t, row0, first, last, wave, lane);
+    kl.start(tiles + buf * kTileBytes<D>, row0, wave, lane);
+    vl.start(tiles + (2 + buf) * kTileBytes<D>, row0, wave, lane);
   };
   if (k0 < kend) stage(0, k0);
   bf16x8 qf[D / 16];
@@ -168,27 +166,34 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnPar
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[t][r] = 0.f;
   float m = kLowest, l = 0.f;
+  if constexpr (BIAS) stage_bias(p, h, bias, tid);
+  const bool gaps = p.ranges && has_gaps(ranges, last, tid);
   wait_tile();
-  // The tiles that all of the wave's queries see whole are one run; the loops
-  // for it and for the others leave the accumulators where they are, which a
-  // branch inside one loop did not (64 register copies a tile).  Every wave goes
-  // through the same number of turns, each with its one barrier.
+  // Turns in which the wave has nothing to see have a loop of their own: a
+  // branch inside one loop copied the accumulators to other registers every turn.
+  // Every wave goes through the same number of turns, each with its barrier.
   int buf = 0;
-  const auto turn = [&](auto full) {
+  const auto turn = [&](auto work) {
     if (k0 + kTile < kend) stage(buf ^ 1, k0 + kTile);
-    if (full.value || (wh.x < k0 + kTile && wh.y > k0)) {   // a query sees some of the tile
-      const FragAt<D> kt = at.in(tiles + buf * kTileBytes<D>);
-      const FragAt<D> vt = at.in(tiles + (2 + buf) * kTileBytes<D>);
-      attn_fwd_tile<D, CAP, BIAS, full.value>(p, kt, vt, qf, acc, m, l, rng, k0, i0, f, bias, lane);
+    if (gaps) {
+      const uint64_t seen = seen_keys(ranges, k0, reinterpret_cast<uint32_t*>(hull), tid);
+      clear_rows<D>(tiles + buf * kTileBytes<D>, tiles + (2 + buf) * kTileBytes<D>, seen, tid);
+      __syncthreads();
     }
+    work();
     wait_tile();
     k0 += kTile;
     buf ^= 1;
   };
-  const auto sees_all = [&] { return __all(rng.x <= k0 && rng.y >= k0 + kTile) != 0; };
+  const auto sees = [&] { return wh.x < k0 + kTile && wh.y > k0; };
   while (k0 < kend) {
-    while (k0 < kend && !sees_all()) turn(Bool<false>());
-    while (k0 < kend && sees_all()) turn(Bool<true>());
+    while (k0 < kend && !sees()) turn([] {});
+    while (k0 < kend && sees())
+      turn([&] {
+        attn_fwd_tile<D, CAP, BIAS>(p, at.in(tiles + buf * kTileBytes<D>),
+                                    at.in(tiles + (2 + buf) * kTileBytes<D>), qf, acc, m, l, rng,
+                                    k0, i0, f, bias, lane);
+      });
   }
 
   l += __shfl_xor(l, 32);
@@ -251,12 +256,22 @@ __global__ __launch_bounds__(64) void attn_join_kernel(const AttnParams p) {
   float x[kN];
 #pragma unroll
   for (int c = 0; c < kN; ++c) x[c] = 0.f;
-#pragma unroll 8
-  for (int z = 0; z < p.splits; ++z) {
-    const float fz = __shfl(f, z);
+  for (int z0 = 0; z0 < p.splits; z0 += 8) {       // 8 loads under way at a time
+    float part[8][kN];
 #pragma unroll
-    for (int c = 0; c < kN; ++c)
-      if (lane + 64 * c < D) x[c] += fz * p.osplit[(z * rows + row) * D + lane + 64 * c];
+    for (int z = 0; z < 8; ++z)
+#pragma unroll
+      for (int c = 0; c < kN; ++c) {
+        part[z][c] = 0.f;
+        if (z0 + z < p.splits && lane + 64 * c < D)
+          part[z][c] = p.osplit[((z0 + z) * rows + row) * D + lane + 64 * c];
+      }
+#pragma unroll
+    for (int z = 0; z < 8; ++z) {
+      const float fz = __shfl(f, z0 + z);          // (of a part that is not there: times 0)
+#pragma unroll
+      for (int c = 0; c < kN; ++c) x[c] = __builtin_fmaf(fz, part[z][c], x[c]);
+    }
   }
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
   const int64_t bh = row / p.Tq;
@@ -289,7 +304,7 @@ Split choose_split(int B, int Tq, int Tk, int Hq) {
 
 template <int D, bool CAP, bool BIAS>
 hipError_t run_fwd(const AttnParams& p, hipStream_t s) {
-  const size_t lds = 4 * kTileBytes<D> + 2 * kWaves * sizeof(int) +
+  const size_t lds = 4 * kTileBytes<D> + 128 * sizeof(int2) + 2 * kWaves * sizeof(int) +
                      (BIAS ? bias_entries(p.reach) * sizeof(float) : 0);
   const dim3 grid(p.B * p.Hq, (p.Tq + 127) / 128, p.splits);
   if (p.splits > 1) {
