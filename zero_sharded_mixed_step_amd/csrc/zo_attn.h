@@ -178,8 +178,48 @@ __device__ __forceinline__ bf16x8 to_frag(const float* x) {
   return f;
 }
 
-// Loads of tiles of 64 rows of D columns straight into shared memory (no
-// registers on the way); wait_tile() ends them.  A lane's offsets from a tile's
+__device__ __forceinline__ uint32_t uniform(uint32_t x) {
+  return __builtin_amdgcn_readfirstlane(x);
+}
+
+// Direct loads to shared memory: 64 lanes' 16 (or 4) bytes each, one after the
+// other from the uniform address `to`, with no registers on the way.  They are
+// written as instructions because the compiler, which cannot tell the buffers
+// apart, waits for all of them before the next transposing read and so loses
+// what two buffers are for; nothing here returns a value, and wait_tile() holds the
+// only wait they need.  (m0, which nothing else here uses, takes the address.  The wait
+// states cover its write, and scalar registers that a vector instruction wrote just
+// before: inside the text no one else inserts them.)
+__device__ __forceinline__ void lds_load16(uint32_t to, u32x4 buffer, uint32_t lane_offset,
+                                           uint32_t offset) {
+#ifdef __HIP_DEVICE_COMPILE__
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(
+                   uniform(to)),
+               "v"(lane_offset), "s"(buffer), "s"(uniform(offset))
+               : "memory");
+#endif
+}
+__device__ __forceinline__ void lds_load16(uint32_t to, const void* from) {
+#ifdef __HIP_DEVICE_COMPILE__
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(uniform(to)), "v"(from)
+               : "memory");
+#endif
+}
+__device__ __forceinline__ void lds_load4(uint32_t to, const void* from) {
+#ifdef __HIP_DEVICE_COMPILE__
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, off" ::"s"(uniform(to)), "v"(from)
+               : "memory");
+#endif
+}
+
+// A descriptor of the memory from `base` on, for 32-bit offsets.
+__device__ __forceinline__ u32x4 buffer_at(const void* base) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  return u32x4{uniform(static_cast<uint32_t>(a)), uniform(static_cast<uint32_t>(a >> 32) & 0xFFFFu),
+               0xFFFFFFFFu, 0x00020000u};
+}
+
+// Loads of tiles of 64 rows of D columns.  A lane's offsets from a tile's
 // first row are formed once, and a tile inside [first, last) takes a uniform
 // base and these 32-bit offsets: forming 64-bit addresses a tile cost as much
 // as a quarter of the softmax (integer products run at a quarter of the rate).  At
@@ -208,44 +248,35 @@ struct TileLoad {
   }
 
   __device__ __forceinline__ void start(uint32_t tile, int row0, int wave, int lane) const {
-    using Global = const __attribute__((address_space(1))) void*;
-    using Shared = ZO_LDS void*;
     const uint32_t to = tile + wave * (kLoads * 1024);
     if (near && row0 >= first && row0 + kTile <= last) {
-      // (a buffer descriptor, because it takes a 32-bit offset a lane; its type is not
-      // known to the compiler's pass over the host's side)
-#ifdef __HIP_DEVICE_COMPILE__
-      const auto from = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<bf16*>(base + row0 * stride), 0, -1, 0x00020000);
+      const u32x4 from = buffer_at(base + row0 * stride);
 #pragma unroll
       for (int u = 0; u < kLoads; ++u)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(from, reinterpret_cast<Shared>(to + u * 1024), 16,
-                                                 off[u % kOffs],
-                                                 static_cast<int>((u / kOffs) * 16 * stride), 0, 0);
-#endif
+        lds_load16(to + u * 1024, from, off[u % kOffs],
+                   static_cast<uint32_t>((u / kOffs) * 16 * stride));
     } else {
 #pragma unroll 1
       for (int u = 0; u < kLoads; ++u) {
         const int piece = (wave * kLoads + u) * 64 + lane;
         const int r = piece / (D / 8), c = (piece % (D / 8)) ^ swizzle<D>(r);
-        const bf16* from = base + min(max(row0 + r, first), last - 1) * stride + c * 8;
-        __builtin_amdgcn_global_load_lds((Global)from, reinterpret_cast<Shared>(to + u * 1024), 16,
-                                         0, 0);
+        lds_load16(to + u * 1024, base + min(max(row0 + r, first), last - 1) * stride + c * 8);
       }
     }
   }
 };
 
-// The same for 64 words of a padded array, by one wave.
-__device__ __forceinline__ void load_words(uint32_t to, const void* from, int lane) {
-  __builtin_amdgcn_global_load_lds(
-      (const __attribute__((address_space(1))) void*)(static_cast<const uint32_t*>(from) + lane),
-      reinterpret_cast<ZO_LDS void*>(to), 4, 0, 0);
-}
+// Tiles of a pair of tensors under way or in use.  With three, a tile's loads have two
+// turns to arrive: a turn alone (1 to 2 us) does not cover the way to memory.
+// Where two workgroups share a compute unit, three of 128 columns do not fit.
+template <int D, bool ALONE>
+constexpr int kBuffers = D <= 96 || ALONE ? 3 : 2;
 
-// The calling thread's tile loads are done; the workgroup's after the barrier.
+// The calling wave's direct loads are done but for the last `LATER`; the
+// workgroup's after the barrier.  (Loads end in the order they were started in.)
+template <int LATER = 0>
 __device__ __forceinline__ void wait_tile() {
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LATER) : "memory");
   __syncthreads();
 }
 

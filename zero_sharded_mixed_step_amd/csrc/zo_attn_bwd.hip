@@ -69,6 +69,11 @@ __device__ __forceinline__ uint64_t bits_below(int n) {
   return n <= 0 ? 0 : n >= 64 ? ~uint64_t(0) : (uint64_t(1) << n) - 1;
 }
 
+// The registers of one wave a SIMD for 96 columns and more: k, v, dk and dv alone take
+// 144 or 192 of the 256 that two waves leave each.
+template <int D>
+constexpr bool kDkvAlone = D > 64;
+
 // One tile of 64 queries, do's behind q's, for a wave's 32 keys.
 template <int D, bool CAP, bool BIAS>
 __device__ __forceinline__ void attn_dkv_tile(const AttnParams& p, const FragAt<D>& qt,
@@ -77,7 +82,7 @@ __device__ __forceinline__ void attn_dkv_tile(const AttnParams& p, const FragAt<
                                               const bf16x8 (&vf)[D / 16], f32x16 (&dk)[D / 32],
                                               f32x16 (&dv)[D / 32], int j, int jw, int i0,
                                               const ScoreFactors& f, const float* bias, int lane) {
-  constexpr int kG = 2 * kTileBytes<D>;  // from q's tile to do's
+  constexpr int kG = kBuffers<D, kDkvAlone<D>> * kTileBytes<D>;  // from q's tile to do's
   const int half = lane >> 5;
   // the lane's places in the tile's words (opaque: one register each, not one a use)
   uint32_t quads = stat + 16 * half, words = stat + 4 * (lane & 31);
@@ -160,12 +165,14 @@ __device__ __forceinline__ int key_tile(const AttnParams& p, int b, int* scratch
 // A workgroup owns 128 keys of one key head, 32 to a wave, and walks tiles of
 // 64 queries of the query heads that share it, or of a part of them.
 template <int D, bool CAP, bool BIAS>
-__global__ __launch_bounds__(kAttnThreads, D > 64 ? 1 : 2) void attn_dkv_kernel(const AttnParams p) {
+__global__ __launch_bounds__(kAttnThreads, kDkvAlone<D> ? 1 : 2) void attn_dkv_kernel(const AttnParams p) {
+  constexpr int kBufs = kBuffers<D, kDkvAlone<D>>, kTiles = 2 * kBufs;
+  constexpr int kAhead = (kBufs - 2) * (2 * TileLoad<D>::kLoads + 1);
   constexpr int kStat = 4 * kTile * 4;                 // base, delta, lo, hi of a tile
-  extern __shared__ __align__(1024) char smem[];       // [2] tiles of q, of do
+  extern __shared__ __align__(1024) char smem[];       // [kBufs] tiles of q, of do
   const uint32_t tiles = lds_address(smem);
-  char* stats = smem + 4 * kTileBytes<D>;              // [2] kStat
-  int* span = reinterpret_cast<int*>(stats + 2 * kStat);             // [kWaves][2]
+  char* stats = smem + kTiles * kTileBytes<D>;         // [kBufs] kStat
+  int* span = reinterpret_cast<int*>(stats + kBufs * kStat);             // [kWaves][2]
   uint32_t* seen_by = reinterpret_cast<uint32_t*>(span + 2 * kWaves);       // [kWaves][4]
   float* bias = reinterpret_cast<float*>(seen_by + 4 * kWaves);
 
@@ -227,14 +234,14 @@ __global__ __launch_bounds__(kAttnThreads, D > 64 ? 1 : 2) void attn_dkv_kernel(
   const auto stage = [&](int buf) {
     const int64_t bh = static_cast<int64_t>(b) * p.Hq + h0 + head;
     ql.start(tiles + buf * kTileBytes<D>, qi * kTile, wave, lane);
-    ol.start(tiles + (2 + buf) * kTileBytes<D>, qi * kTile, wave, lane);
-    const uint32_t to = tiles + 4 * kTileBytes<D> + buf * kStat + wave * kTile * 4;
+    ol.start(tiles + (kBufs + buf) * kTileBytes<D>, qi * kTile, wave, lane);
+    const uint32_t to = tiles + kTiles * kTileBytes<D> + buf * kStat + wave * kTile * 4;
     const int i0 = qi * kTile;
     const void* from = wave == 0   ? static_cast<const void*>(p.base + bh * p.tq64 + i0)
                        : wave == 1 ? static_cast<const void*>(p.delta + bh * p.tq64 + i0)
                        : wave == 2 ? static_cast<const void*>(qlo + i0)
                                    : static_cast<const void*>(qhi + i0);
-    load_words(to, from, lane);
+    lds_load4(to, static_cast<const uint32_t*>(from) + lane);
     if (++qi == qb) {
       qi = qa;
       ++head;
@@ -242,7 +249,9 @@ __global__ __launch_bounds__(kAttnThreads, D > 64 ? 1 : 2) void attn_dkv_kernel(
       ol.base += p.dos.h;
     }
   };
-  if (turns > 0) stage(0);
+#pragma unroll
+  for (int k = 0; k < kBufs - 1; ++k)
+    if (k < turns) stage(k);
   bf16x8 kf[D / 16], vf[D / 16];
   {
     const int64_t jj = min(j, p.Tk - 1);
@@ -272,18 +281,22 @@ __global__ __launch_bounds__(kAttnThreads, D > 64 ? 1 : 2) void attn_dkv_kernel(
   const auto stat_of = [&] { return reinterpret_cast<const float*>(stats + buf * kStat); };
   const auto word = [&](int k) { return reinterpret_cast<const int*>(stat_of())[k * kTile + lane]; };
   const auto turn = [&](auto work) {
-    if (n + 1 < turns) stage(buf ^ 1);
+    const bool more = n + kBufs - 1 < turns;
+    if (more) stage((buf + kBufs - 1) % kBufs);
     // a query that sees nothing (padding) may hold anything: cleared, since a weight of 0
     // does not stop a NaN
     const uint64_t seeing = __ballot(word(3) > word(2));
     if (~seeing != 0) {
-      clear_rows<D>(tiles + buf * kTileBytes<D>, tiles + (2 + buf) * kTileBytes<D>, seeing, tid);
+      clear_rows<D>(tiles + buf * kTileBytes<D>, tiles + (kBufs + buf) * kTileBytes<D>, seeing, tid);
       __syncthreads();
     }
     work();
-    wait_tile();
+    if (more)
+      wait_tile<kAhead>();
+    else
+      wait_tile();
     ++n;
-    buf ^= 1;
+    buf = buf + 1 == kBufs ? 0 : buf + 1;
     i0 = i0 + kTile == qb * kTile ? qa * kTile : i0 + kTile;
   };
   const auto seen = [&] { return __any(word(2) < jw + 32 && word(3) > jw) != 0; };
@@ -292,7 +305,7 @@ __global__ __launch_bounds__(kAttnThreads, D > 64 ? 1 : 2) void attn_dkv_kernel(
     while (n < turns && seen())
       turn([&] {
         attn_dkv_tile<D, CAP, BIAS>(p, at.in(tiles + buf * kTileBytes<D>),
-                                    tiles + 4 * kTileBytes<D> + buf * kStat, kf, vf, dk, dv,
+                                    tiles + kTiles * kTileBytes<D> + buf * kStat, kf, vf, dk, dv,
                                     j, jw, i0, f, bias, lane);
       });
   }
@@ -468,11 +481,17 @@ __device__ __forceinline__ void attn_dq_tile(const AttnParams& p, const FragAt<D
 // 64 keys.  With the bias, sums of ds by distance are kept per wave in shared
 // memory; blocks that lie past the reach share a bucket and are summed in two
 // registers instead.
+template <int D, bool BIAS>
+constexpr bool kDqAlone = D > 96 && BIAS;
+
 template <int D, bool CAP, bool BIAS>
-__global__ __launch_bounds__(kAttnThreads, D > 96 && BIAS ? 1 : 2) void attn_dq_kernel(const AttnParams p) {
-  extern __shared__ __align__(1024) char smem[];       // [2] tiles of k, of v
+__global__ __launch_bounds__(kAttnThreads, (kDqAlone<D, BIAS> ? 1 : 2)) void attn_dq_kernel(
+    const AttnParams p) {
+  constexpr int kBufs = kBuffers<D, kDqAlone<D, BIAS>>, kTiles = 2 * kBufs;
+  constexpr int kAhead = (kBufs - 2) * 2 * TileLoad<D>::kLoads;
+  extern __shared__ __align__(1024) char smem[];       // [kBufs] tiles of k, of v
   const uint32_t tiles = lds_address(smem);
-  int2* ranges = reinterpret_cast<int2*>(smem + 4 * kTileBytes<D>);  // [128]
+  int2* ranges = reinterpret_cast<int2*>(smem + kTiles * kTileBytes<D>);  // [128]
   int* hull = reinterpret_cast<int*>(ranges + 128);                  // [kWaves][2]
   float* past = reinterpret_cast<float*>(hull + 2 * kWaves);         // [kWaves][2]
   float* bias = past + 2 * kWaves;                                   // [entries]
@@ -517,10 +536,12 @@ __global__ __launch_bounds__(kAttnThreads, D > 96 && BIAS ? 1 : 2) void attn_dq_
   const TileLoad<D> vl(p.v + b * p.vs.b + hk * p.vs.h, p.vs.t, first, last, wave, lane);
   const auto stage = [&](int buf, int row0) {
     kl.start(tiles + buf * kTileBytes<D>, row0, wave, lane);
-    vl.start(tiles + (2 + buf) * kTileBytes<D>, row0, wave, lane);
+    vl.start(tiles + (kBufs + buf) * kTileBytes<D>, row0, wave, lane);
   };
   int k0 = first & ~(kTile - 1);
-  if (k0 < last) stage(0, k0);
+#pragma unroll
+  for (int n = 0; n < kBufs - 1; ++n)
+    if (k0 + n * kTile < last) stage(n, k0 + n * kTile);
   bf16x8 qf[D / 16], of[D / 16];
   {
     const int64_t ii = min(i, p.Tq - 1);
@@ -549,16 +570,20 @@ __global__ __launch_bounds__(kAttnThreads, D > 96 && BIAS ? 1 : 2) void attn_dq_
 
   int buf = 0;
   const auto turn = [&](auto work) {
-    if (k0 + kTile < last) stage(buf ^ 1, k0 + kTile);
+    const int ahead = k0 + (kBufs - 1) * kTile;
+    if (ahead < last) stage((buf + kBufs - 1) % kBufs, ahead);
     if (gaps) {
       const uint64_t seen = seen_keys(ranges, k0, reinterpret_cast<uint32_t*>(hull), tid);
-      clear_rows<D>(tiles + buf * kTileBytes<D>, tiles + (2 + buf) * kTileBytes<D>, seen, tid);
+      clear_rows<D>(tiles + buf * kTileBytes<D>, tiles + (kBufs + buf) * kTileBytes<D>, seen, tid);
       __syncthreads();
     }
     work();
-    wait_tile();
+    if (ahead < last)
+      wait_tile<kAhead>();
+    else
+      wait_tile();
     k0 += kTile;
-    buf ^= 1;
+    buf = buf + 1 == kBufs ? 0 : buf + 1;
   };
   const auto sees = [&] { return wh.x < k0 + kTile && wh.y > k0; };
   while (k0 < last) {
@@ -566,7 +591,7 @@ __global__ __launch_bounds__(kAttnThreads, D > 96 && BIAS ? 1 : 2) void attn_dq_
     while (k0 < last && sees())
       turn([&] {
         attn_dq_tile<D, CAP, BIAS>(p, at.in(tiles + buf * kTileBytes<D>),
-                                   at.in(tiles + (2 + buf) * kTileBytes<D>), qf, of, dq, rng, base0,
+                                   at.in(tiles + (kBufs + buf) * kTileBytes<D>), qf, of, dq, rng, base0,
                                    delta, k0, i0, f, bias, mine, ends, lane);
       });
   }
@@ -687,11 +712,11 @@ template <int D, bool CAP, bool BIAS>
 hipError_t run_bwd(const AttnParams& p, hipStream_t s) {
   const size_t n = BIAS ? bias_entries(p.reach) : 0;
   const int tiles = (p.Tq + 127) / 128;
-  const size_t staged = 4 * kTileBytes<D>;
+  const size_t dkv_bufs = kBuffers<D, kDkvAlone<D>>, dq_bufs = kBuffers<D, kDqAlone<D, BIAS>>;
   hipError_t e = hipSuccess;
   if (p.B > 0 && p.Tk > 0) {
     e = launch_lds(attn_dkv_kernel<D, CAP, BIAS>, dim3(p.B * p.Hk * p.parts, (p.Tk + 127) / 128),
-                   staged + 8 * kTile * 4 + 2 * kWaves * 4 + 16 * kWaves + n * 4, p, s);
+                   dkv_bufs * (2 * kTileBytes<D> + 4 * kTile * 4) + 2 * kWaves * 4 + 16 * kWaves + n * 4, p, s);
     if (e != hipSuccess) return e;
     if (p.parts > 1) {
       const int64_t pieces = static_cast<int64_t>(p.B) * p.Hk * p.Tk * D / 8;
@@ -702,7 +727,7 @@ hipError_t run_bwd(const AttnParams& p, hipStream_t s) {
   }
   if (p.B > 0 && p.Tq > 0)
     e = launch_lds(attn_dq_kernel<D, CAP, BIAS>, dim3(p.B * p.Hq, tiles),
-                   staged + 128 * 8 + 4 * kWaves * 4 +
+                   dq_bufs * 2 * kTileBytes<D> + 128 * 8 + 4 * kWaves * 4 +
                        (BIAS ? n + kWaves * (kDiagWords + n) : 0) * sizeof(float),
                    p, s);
   if (e != hipSuccess) return e;

@@ -108,10 +108,11 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnParams& p, const FragAt<
 
 template <int D, bool CAP, bool BIAS, bool SPLIT>
 __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnParams p) {
-  constexpr int kRows = 32 * kWaves;
-  extern __shared__ __align__(1024) char smem[];      // [2] tiles of K, of V
+  constexpr int kRows = 32 * kWaves, kBufs = kBuffers<D, false>, kTiles = 2 * kBufs;
+  constexpr int kAhead = (kBufs - 2) * 2 * TileLoad<D>::kLoads;   // loads of later tiles than the next
+  extern __shared__ __align__(1024) char smem[];      // [kBufs] tiles of K, of V
   const uint32_t tiles = lds_address(smem);
-  int2* ranges = reinterpret_cast<int2*>(smem + 4 * kTileBytes<D>);  // [kRows]
+  int2* ranges = reinterpret_cast<int2*>(smem + kTiles * kTileBytes<D>);  // [kRows]
   int* hull = reinterpret_cast<int*>(ranges + kRows);                // [kWaves][2]
   float* bias = reinterpret_cast<float*>(hull + 2 * kWaves);
 
@@ -151,9 +152,11 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnPar
   const TileLoad<D> vl(p.v + b * p.vs.b + hk * p.vs.h, p.vs.t, first, last, wave, lane);
   const auto stage = [&](int buf, int row0) {
     kl.start(tiles + buf * kTileBytes<D>, row0, wave, lane);
-    vl.start(tiles + (2 + buf) * kTileBytes<D>, row0, wave, lane);
+    vl.start(tiles + (kBufs + buf) * kTileBytes<D>, row0, wave, lane);
   };
-  if (k0 < kend) stage(0, k0);
+#pragma unroll
+  for (int n = 0; n < kBufs - 1; ++n)
+    if (k0 + n * kTile < kend) stage(n, k0 + n * kTile);
   bf16x8 qf[D / 16];
   {
     const bf16* q = p.q + b * p.qs.b + static_cast<int64_t>(min(i, p.Tq - 1)) * p.qs.t + h * p.qs.h;
@@ -174,16 +177,20 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnPar
   // Every wave goes through the same number of turns, each with its barrier.
   int buf = 0;
   const auto turn = [&](auto work) {
-    if (k0 + kTile < kend) stage(buf ^ 1, k0 + kTile);
+    const int ahead = k0 + (kBufs - 1) * kTile;
+    if (ahead < kend) stage((buf + kBufs - 1) % kBufs, ahead);
     if (gaps) {
       const uint64_t seen = seen_keys(ranges, k0, reinterpret_cast<uint32_t*>(hull), tid);
-      clear_rows<D>(tiles + buf * kTileBytes<D>, tiles + (2 + buf) * kTileBytes<D>, seen, tid);
+      clear_rows<D>(tiles + buf * kTileBytes<D>, tiles + (kBufs + buf) * kTileBytes<D>, seen, tid);
       __syncthreads();
     }
     work();
-    wait_tile();
+    if (ahead < kend)
+      wait_tile<kAhead>();
+    else
+      wait_tile();
     k0 += kTile;
-    buf ^= 1;
+    buf = buf + 1 == kBufs ? 0 : buf + 1;
   };
   const auto sees = [&] { return wh.x < k0 + kTile && wh.y > k0; };
   while (k0 < kend) {
@@ -191,7 +198,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnPar
     while (k0 < kend && sees())
       turn([&] {
         attn_fwd_tile<D, CAP, BIAS>(p, at.in(tiles + buf * kTileBytes<D>),
-                                    at.in(tiles + (2 + buf) * kTileBytes<D>), qf, acc, m, l, rng,
+                                    at.in(tiles + (kBufs + buf) * kTileBytes<D>), qf, acc, m, l, rng,
                                     k0, i0, f, bias, lane);
       });
   }
@@ -304,7 +311,7 @@ Split choose_split(int B, int Tq, int Tk, int Hq) {
 
 template <int D, bool CAP, bool BIAS>
 hipError_t run_fwd(const AttnParams& p, hipStream_t s) {
-  const size_t lds = 4 * kTileBytes<D> + 128 * sizeof(int2) + 2 * kWaves * sizeof(int) +
+  const size_t lds = 2 * kBuffers<D, false> * kTileBytes<D> + 128 * sizeof(int2) + 2 * kWaves * sizeof(int) +
                      (BIAS ? bias_entries(p.reach) * sizeof(float) : 0);
   const dim3 grid(p.B * p.Hq, (p.Tq + 127) / 128, p.splits);
   if (p.splits > 1) {
