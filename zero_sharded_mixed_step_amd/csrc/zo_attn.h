@@ -87,15 +87,12 @@ __device__ __forceinline__ int2 key_range(const AttnParams& p, int b, int i) {
   return make_int2(lo, hi);
 }
 
-// Hull of the lanes' non-empty ranges over a wave ({INT_MAX, 0}: none).
+// Hull of the lanes' non-empty ranges over a wave ({INT_MAX, 0}: none).  Uniform,
+// and known to be: what decides a wave's loops has to live in scalar registers.
 __device__ __forceinline__ int2 wave_hull(int2 r) {
-  int lo = r.y > r.x ? r.x : 0x7FFFFFFF, hi = r.y;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    lo = min(lo, __shfl_xor(lo, d));
-    hi = max(hi, __shfl_xor(hi, d));
-  }
-  return make_int2(lo, hi);
+  const int lo = join_lanes<64>(r.y > r.x ? r.x : 0x7FFFFFFF, MinOp());
+  const int hi = join_lanes<64>(r.y, MaxOp());
+  return make_int2(uniform(lo), uniform(hi));
 }
 
 __device__ __forceinline__ bf16x8 load8(const bf16* p) {
@@ -176,10 +173,6 @@ __device__ __forceinline__ bf16x8 to_frag(const float* x) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) f[j] = static_cast<bf16>(x[j]);
   return f;
-}
-
-__device__ __forceinline__ uint32_t uniform(uint32_t x) {
-  return __builtin_amdgcn_readfirstlane(x);
 }
 
 // Direct loads to shared memory: 64 lanes' 16 (or 4) bytes each, one after the

@@ -28,8 +28,7 @@ __global__ __launch_bounds__(256) void attn_bwd_prepare_kernel(const AttnParams 
         sum = __builtin_fmaf(static_cast<float>(x[e]), static_cast<float>(y[e]), sum);
     }
   }
-  sum += __shfl_xor(sum, 1);
-  sum += __shfl_xor(sum, 2);
+  sum = join_lanes<4>(sum, AddOp());
   if (sub == 0) {
     const int64_t row = static_cast<int64_t>(bh) * p.tq64 + i;
     p.delta[row] = sum;
@@ -200,11 +199,8 @@ __global__ __launch_bounds__(kAttnThreads, kDkvAlone<D> ? 1 : 2) void attn_dkv_k
       seen_hi |= bits_below(hi - 64) & ~bits_below(lo - 64);
     }
   }
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    qa = min(qa, __shfl_xor(qa, d));
-    qb = max(qb, __shfl_xor(qb, d));
-  }
+  qa = join_lanes<64>(qa, MinOp());
+  qb = join_lanes<64>(qb, MaxOp());
   if (lane == 0) {
     span[2 * wave] = qa;
     span[2 * wave + 1] = qb;
@@ -213,9 +209,7 @@ __global__ __launch_bounds__(kAttnThreads, kDkvAlone<D> ? 1 : 2) void attn_dkv_k
                             static_cast<uint32_t>(seen_hi), static_cast<uint32_t>(seen_hi >> 32)};
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    uint32_t x = mine[w];
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) x |= __shfl_xor(x, d);
+    const uint32_t x = join_lanes<64>(mine[w], OrOp());
     if (lane == 0) seen_by[4 * wave + w] = x;
   }
   __syncthreads();
@@ -611,11 +605,8 @@ __global__ __launch_bounds__(kAttnThreads, (kDqAlone<D, BIAS> ? 1 : 2)) void att
   }
   if constexpr (BIAS) {
     if (p.dtable == nullptr) return;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      ends[0] += __shfl_xor(ends[0], d);
-      ends[1] += __shfl_xor(ends[1], d);
-    }
+    ends[0] = join_lanes<64>(ends[0], AddOp());
+    ends[1] = join_lanes<64>(ends[1], AddOp());
     if (lane == 0) {
       past[2 * wave] = ends[0];
       past[2 * wave + 1] = ends[1];
@@ -668,8 +659,7 @@ __global__ __launch_bounds__(1024) void attn_dtable_kernel(const AttnParams p, i
     for (int d = lane; d < entries; d += 64)
       if (bucket[d] == k)
         for (int g = 0; g < groups; ++g) x += sums[g * entries + d];
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
+    x = join_lanes<64>(x, AddOp());
     if (lane == 0) {
       const int64_t at = static_cast<int64_t>(k) * p.Hq + h;
       if (p.table_f32)

@@ -28,4 +28,56 @@ __device__ __forceinline__ float bf16_bits_to_f32(uint32_t low16) {
   return __uint_as_float(low16 << 16);
 }
 
+__device__ __forceinline__ uint32_t uniform(uint32_t x) {
+  return __builtin_amdgcn_readfirstlane(x);
+}
+
+// Joins a 32-bit value over groups of G consecutive lanes (all of them get the
+// result) by moves between registers: neighbours, pairs, mirrored halves of 8 and
+// of 16 lanes (the halves are uniform by then), then rows of 16 and halves of the
+// wave swapped.  A shuffle through the shared-memory crossbar takes some 100 cycles
+// where one of these takes 8.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_move(uint32_t x) {
+  return __builtin_amdgcn_update_dpp(x, x, CTRL, 0xF, 0xF, false);
+}
+template <int G, typename T, typename Op>
+__device__ __forceinline__ T join_lanes(T x, Op op) {
+  static_assert(sizeof(T) == 4 && G <= 64, "32-bit values");
+  const auto bits = [](T v) { return __builtin_bit_cast(uint32_t, v); };
+  const auto value = [](uint32_t v) { return __builtin_bit_cast(T, v); };
+  if constexpr (G >= 2) x = op(x, value(dpp_move<0xB1>(bits(x))));    // lanes 1 0 3 2
+  if constexpr (G >= 4) x = op(x, value(dpp_move<0x4E>(bits(x))));    // lanes 2 3 0 1
+  if constexpr (G >= 8) x = op(x, value(dpp_move<0x141>(bits(x))));   // 8 lanes mirrored
+  if constexpr (G >= 16) x = op(x, value(dpp_move<0x140>(bits(x))));  // 16 lanes mirrored
+  if constexpr (G >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(bits(x), bits(x), false, false);
+    x = op(value(r[0]), value(r[1]));
+  }
+  if constexpr (G >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(bits(x), bits(x), false, false);
+    x = op(value(r[0]), value(r[1]));
+  }
+  return x;
+}
+
+struct AddOp {
+  template <typename X>
+  __device__ __forceinline__ X operator()(X a, X b) const {
+    return a + b;
+  }
+};
+struct MaxOp {
+  __device__ __forceinline__ float operator()(float a, float b) const {
+    return a > b || a != a ? a : b;      // a NaN stays
+  }
+  __device__ __forceinline__ int operator()(int a, int b) const { return max(a, b); }
+};
+struct MinOp {
+  __device__ __forceinline__ int operator()(int a, int b) const { return min(a, b); }
+};
+struct OrOp {
+  __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return a | b; }
+};
+
 }  // namespace zo

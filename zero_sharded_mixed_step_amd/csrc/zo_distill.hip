@@ -137,32 +137,26 @@ __device__ __forceinline__ void keep_packed(Chunk<E> (&held)[CH]) {
   for (int c = 0; c < CH; ++c) asm volatile("" : "+v"(held[c].r));
 }
 
-struct MaxOp {
-  template <typename X>
-  __device__ __forceinline__ X operator()(X a, X b) const {
-    return a > b || a != a ? a : b;      // a NaN stays
-  }
-};
-struct AddOp {
-  template <typename X>
-  __device__ __forceinline__ X operator()(X a, X b) const {
-    return a + b;
-  }
-};
-
 // Joins a value over the workgroup, in one fixed order; everyone gets it.
+template <int G, typename X, typename Op>
+__device__ __forceinline__ X join_group(X x, Op op) {
+  if constexpr (sizeof(X) == 4) {
+    return join_lanes<G>(x, op);
+  } else {
+#pragma unroll
+    for (int d = 1; d < G; d <<= 1) x = op(x, __shfl_xor(x, d));
+    return x;
+  }
+}
 template <int NT, typename X, typename Op>
 __device__ __forceinline__ X join(X x, Op op, double* scratch) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) x = op(x, __shfl_xor(x, d));
+  x = join_group<64>(x, op);
   X* s = reinterpret_cast<X*>(scratch);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = x;
   __syncthreads();
   x = s[(threadIdx.x & 63) % (NT / 64)];
-#pragma unroll
-  for (int d = 1; d < NT / 64; d <<= 1) x = op(x, __shfl_xor(x, d));
-  return x;
+  return join_group<NT / 64>(x, op);
 }
 
 // The teacher's side of a row, in shared memory: p[k], the student's logit

@@ -143,9 +143,7 @@ __device__ __forceinline__ void make_turn(const NormParams& p, int64_t t, int la
 
 template <int G>
 __device__ __forceinline__ float sum_row(float x) {
-#pragma unroll
-  for (int d = 1; d < G; d <<= 1) x += __shfl_xor(x, d);
-  return x;
+  return join_lanes<G>(x, AddOp());
 }
 
 template <typename E>
