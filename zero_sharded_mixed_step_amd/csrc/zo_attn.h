@@ -65,6 +65,7 @@ struct AttnParams {
   float* delta;     // [B][Hq][tq64]  do . o
   int *qlo, *qhi;   // [B][tq64]      the keys a query sees; 0, 0 for none
   float* dpart;     // [B][Hq][query tiles][bias_entries]: ds by distance
+  float* dsum;      // [Hq][bias_entries]
   float* kvpart;    // [2][parts][B][Hk][Tk][D]: dk and dv of parts of a group's heads
   int parts;        // 1: no parts
   float* osplit;    // split forward: [splits][B * Hq * Tq][D] and, behind it, two statistics
@@ -291,30 +292,44 @@ __device__ __forceinline__ int bias_bucket(const AttnParams& p, int d) {
   return min(max(p.buckets[min(max(d, -p.reach), p.reach) + p.reach], 0), p.n_buckets - 1);
 }
 
-// The head's bias into shared memory.  A finite bias stays finite.  (Each entry
-// is two loads, one after the other: four entries a thread are under way at once.)
-__device__ __forceinline__ void stage_bias(const AttnParams& p, int h, float* out, int tid) {
-  constexpr int kAtOnce = 4;
-  const int span = bias_span(p.reach), n = bias_entries(p.reach);
-  for (int e0 = tid; e0 < n; e0 += kAtOnce * kAttnThreads) {
-    int64_t at[kAtOnce];
-    float b[kAtOnce];
-#pragma unroll
-    for (int k = 0; k < kAtOnce; ++k)
-      at[k] = static_cast<int64_t>(bias_bucket(p, min(e0 + k * kAttnThreads, n - 1) - span)) * p.Hq + h;
-#pragma unroll
-    for (int k = 0; k < kAtOnce; ++k)
-      b[k] = p.table_f32 ? static_cast<const float*>(p.table)[at[k]]
-                         : static_cast<float>(static_cast<const bf16*>(p.table)[at[k]]);
-#pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) {
-      const float x = b[k] * kLog2e;
-      if (e0 + k * kAttnThreads < n)
-        out[e0 + k * kAttnThreads] =
-            __builtin_isinf(x) && !__builtin_isinf(b[k]) ? __builtin_copysignf(-kLowest, b[k]) : x;
-    }
+// The head's bias into shared memory, in three steps with other work between
+// them: every entry is two loads, one after the other, and waiting for both in
+// one place took 2.4 us of each workgroup.  Four entries a thread go this way, what a
+// longer reach has beyond them (from 1025 entries on) at the end.  A finite bias stays
+// finite.
+struct BiasStage {
+  static constexpr int kAtOnce = 4;
+  int bucket[kAtOnce];
+  float b[kAtOnce];
+
+  static __device__ __forceinline__ float entry(const AttnParams& p, int h, int bucket) {
+    const int64_t at = static_cast<int64_t>(bucket) * p.Hq + h;
+    return p.table_f32 ? static_cast<const float*>(p.table)[at]
+                       : static_cast<float>(static_cast<const bf16*>(p.table)[at]);
   }
-}
+  static __device__ __forceinline__ float in_log2(float b) {
+    const float x = b * kLog2e;
+    return __builtin_isinf(x) && !__builtin_isinf(b) ? __builtin_copysignf(-kLowest, b) : x;
+  }
+
+  __device__ __forceinline__ void buckets(const AttnParams& p, int tid) {
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k)
+      bucket[k] = bias_bucket(p, tid + k * kAttnThreads - bias_span(p.reach));   // (clips)
+  }
+  __device__ __forceinline__ void values(const AttnParams& p, int h) {
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) b[k] = entry(p, h, bucket[k]);
+  }
+  __device__ __forceinline__ void store(const AttnParams& p, int h, float* out, int tid) const {
+    const int n = bias_entries(p.reach);
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k)
+      if (tid + k * kAttnThreads < n) out[tid + k * kAttnThreads] = in_log2(b[k]);
+    for (int e = tid + kAtOnce * kAttnThreads; e < n; e += kAttnThreads)
+      out[e] = in_log2(entry(p, h, bias_bucket(p, e - bias_span(p.reach))));
+  }
+};
 
 // Where a block of distances lies: all at or past one end of the reach (-1, 1),
 // where the bias is one number, or not (0).
@@ -381,13 +396,13 @@ __device__ __forceinline__ bool has_gaps(const int2* ranges, int last, int tid) 
   const int2 r = ranges[k], next = ranges[k < 127 ? k + 1 : k];
   const bool plain = r.y > r.x && next.x >= r.x && next.y >= r.y;
   if (__syncthreads_and(plain)) return __syncthreads_or(next.x > r.y) != 0;
-  bool gap = false;
-  if (r.y > r.x && r.y < last) {
-    bool inside = false;
-    for (int i = 0; i < 128; ++i) inside |= ranges[i].x <= r.y && ranges[i].y > r.y;
-    gap = !inside;
+  bool inside = false;
+#pragma unroll 16
+  for (int i = 0; i < 128; ++i) {        // (no early end: the reads follow one another)
+    const int2 o = ranges[i];
+    inside |= (o.x <= r.y) & (o.y > r.y);
   }
-  return __syncthreads_or(gap) != 0;
+  return __syncthreads_or((r.y > r.x) & (r.y < last) & !inside) != 0;
 }
 
 // The keys k0 .. + 63 that some of the 128 queries see; `flags`: 2 words.
@@ -397,8 +412,11 @@ __device__ __forceinline__ uint64_t seen_keys(const int2* ranges, int k0, uint32
   __syncthreads();
   const int j = k0 + (tid & 63);
   bool seen = false;
-  for (int k = 32 * (tid >> 6); k < 32 * (tid >> 6) + 32; ++k)
-    seen |= j >= ranges[k].x && j < ranges[k].y;
+#pragma unroll 8
+  for (int k = 0; k < 32; ++k) {
+    const int2 o = ranges[32 * (tid >> 6) + k];
+    seen |= (j >= o.x) & (j < o.y);
+  }
   if (seen) atomicOr(&flags[(tid & 63) >> 5], 1u << (tid & 31));
   __syncthreads();
   return flags[0] | static_cast<uint64_t>(flags[1]) << 32;

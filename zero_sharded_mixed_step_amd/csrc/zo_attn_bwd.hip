@@ -179,6 +179,8 @@ __global__ __launch_bounds__(kAttnThreads, kDkvAlone<D> ? 1 : 2) void attn_dkv_k
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int bx = head_of_group(blockIdx.x, gridDim.x);
   const int part = bx % p.parts, bk = bx / p.parts, b = bk / p.Hk, hk = bk % p.Hk;
+  BiasStage bs;                                        // (a bias goes with one head a workgroup)
+  if constexpr (BIAS) bs.buckets(p, tid);
   const int j0 = key_tile(p, b, reinterpret_cast<int*>(smem), tid) * 128;   // its first key
   const int jw = j0 + wave * 32, j = jw + (lane & 31);
   const int* qlo = p.qlo + static_cast<int64_t>(b) * p.tq64;
@@ -187,17 +189,27 @@ __global__ __launch_bounds__(kAttnThreads, kDkvAlone<D> ? 1 : 2) void attn_dkv_k
   const FragAt<D> at(lane);
   const int heads = p.group / p.parts, h0 = hk * p.group + part * heads;
 
+  if constexpr (BIAS) bs.values(p, h0);
   // the tiles of queries that see any of the keys lie in [qa, qb); and the keys seen
   int qa = 0x7FFFFFFF, qb = 0;
   uint64_t seen_lo = 0, seen_hi = 0;
-  for (int i = tid; i < p.tq64; i += kAttnThreads) {
-    const int lo = max(qlo[i] - j0, 0), hi = min(qhi[i] - j0, 128);
-    if (lo < hi) {
-      qa = min(qa, i / kTile);
-      qb = max(qb, i / kTile + 1);
-      seen_lo |= bits_below(hi) & ~bits_below(lo);
-      seen_hi |= bits_below(hi - 64) & ~bits_below(lo - 64);
+  for (int i0 = tid; i0 < p.tq64; i0 += 4 * kAttnThreads) {
+    int lo[4], hi[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k * kAttnThreads;
+      lo[k] = i < p.tq64 ? max(qlo[i] - j0, 0) : 0;
+      hi[k] = i < p.tq64 ? min(qhi[i] - j0, 128) : 0;
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (lo[k] < hi[k]) {
+        const int t = (i0 + k * kAttnThreads) / kTile;
+        qa = min(qa, t);
+        qb = max(qb, t + 1);
+        seen_lo |= bits_below(hi[k]) & ~bits_below(lo[k]);
+        seen_hi |= bits_below(hi[k] - 64) & ~bits_below(lo[k] - 64);
+      }
   }
   qa = join_lanes<64>(qa, MinOp());
   qb = join_lanes<64>(qb, MaxOp());
@@ -268,7 +280,7 @@ __global__ __launch_bounds__(kAttnThreads, kDkvAlone<D> ? 1 : 2) void attn_dkv_k
   for (int t = 0; t < D / 32; ++t)
 #pragma unroll
     for (int r = 0; r < 16; ++r) dk[t][r] = dv[t][r] = 0.f;
-  if constexpr (BIAS) stage_bias(p, h0, bias, tid);    // (a bias goes with one head a workgroup)
+  if constexpr (BIAS) bs.store(p, h0, bias, tid);
   wait_tile();
 
   int n = 0, buf = 0, i0 = qa * kTile;                 // of the tile at hand
@@ -497,6 +509,8 @@ __global__ __launch_bounds__(kAttnThreads, (kDqAlone<D, BIAS> ? 1 : 2)) void att
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int bh = head_of_group(blockIdx.x, gridDim.x), b = bh / p.Hq, h = bh % p.Hq;
   const int hk = h / p.group;
+  BiasStage bs;
+  if constexpr (BIAS) bs.buckets(p, tid);
   const int tile = query_tile(p, b, reinterpret_cast<int*>(ranges), tid);
   const int i0 = tile * 128 + wave * 32;
   const int i = i0 + (lane & 31);
@@ -510,6 +524,7 @@ __global__ __launch_bounds__(kAttnThreads, (kDqAlone<D, BIAS> ? 1 : 2)) void att
     hull[2 * wave + 1] = wh.y;
   }
   if (lane < 32) ranges[wave * 32 + lane] = rng;
+  if constexpr (BIAS) bs.values(p, h);
   float ends[2] = {0.f, 0.f};
   uint32_t mine = 0;
   if constexpr (BIAS) {
@@ -558,7 +573,7 @@ __global__ __launch_bounds__(kAttnThreads, (kDqAlone<D, BIAS> ? 1 : 2)) void att
   for (int t = 0; t < D / 32; ++t)
 #pragma unroll
     for (int r = 0; r < 16; ++r) dq[t][r] = 0.f;
-  if constexpr (BIAS) stage_bias(p, h, bias, tid);
+  if constexpr (BIAS) bs.store(p, h, bias, tid);
   const bool gaps = p.ranges && has_gaps(ranges, last, tid);
   wait_tile();
 
@@ -624,23 +639,20 @@ __global__ __launch_bounds__(kAttnThreads, (kDqAlone<D, BIAS> ? 1 : 2)) void att
   }
 }
 
-// dbias_table[.][h]: the sums by distance of all batch rows and query tiles,
-// then by bucket; a workgroup to a head.
-__global__ __launch_bounds__(1024) void attn_dtable_kernel(const AttnParams p, int tiles) {
-  extern __shared__ float sums[];                      // [groups][entries], then bucket ids
-  const int h = blockIdx.x, tid = threadIdx.x, entries = bias_entries(p.reach);
-  // as many threads to a distance as there are for all of them
-  const int groups = max(1, 1024 / entries), rows = p.B * tiles;
-  int* bucket = reinterpret_cast<int*>(sums + groups * entries);
-  for (int d = tid; d < entries; d += 1024) bucket[d] = bias_bucket(p, d - bias_span(p.reach));
-  for (int k = tid; k < groups * entries; k += 1024) {
-    const int g = k / entries, d = k % entries;
-    float x = 0.f;
-    for (int n0 = g; n0 < rows; n0 += 8 * groups) {    // 8 loads under way at a time
-      float part[8];
+// The sums by distance over all batch rows and query tiles: 64 distances of a head
+// to a workgroup, 16 threads to a distance.
+__global__ __launch_bounds__(1024) void attn_dsum_kernel(const AttnParams p, int tiles) {
+  __shared__ float sums[16][64];
+  const int entries = bias_entries(p.reach), rows = p.B * tiles;
+  const int h = blockIdx.x, lane = threadIdx.x & 63, g = threadIdx.x >> 6;
+  const int d = blockIdx.y * 64 + lane;
+  float x = 0.f;
+  if (d < entries)
+    for (int n0 = g; n0 < rows; n0 += 64) {            // 4 loads under way at a time
+      float part[4];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int n = n0 + u * groups;
+      for (int u = 0; u < 4; ++u) {
+        const int n = n0 + 16 * u;
         part[u] = 0.f;
         if (n < rows) {
           const int64_t b = n / tiles, t = n % tiles;
@@ -648,17 +660,32 @@ __global__ __launch_bounds__(1024) void attn_dtable_kernel(const AttnParams p, i
         }
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) x += part[u];
+      for (int u = 0; u < 4; ++u) x += part[u];
     }
-    sums[k] = x;
+  sums[g][lane] = x;
+  __syncthreads();
+  if (g == 0 && d < entries) {
+    x = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x += sums[k][lane];
+    p.dsum[static_cast<int64_t>(h) * entries + d] = x;
+  }
+}
+
+// dbias_table[.][h]: the sums by distance, by bucket; a wave to a bucket.
+__global__ __launch_bounds__(1024) void attn_dtable_kernel(const AttnParams p) {
+  extern __shared__ float sums[];                      // [entries], then bucket ids
+  const int h = blockIdx.x, tid = threadIdx.x, lane = tid & 63, entries = bias_entries(p.reach);
+  int* bucket = reinterpret_cast<int*>(sums + entries);
+  for (int d = tid; d < entries; d += 1024) {
+    sums[d] = p.dsum[static_cast<int64_t>(h) * entries + d];
+    bucket[d] = bias_bucket(p, d - bias_span(p.reach));
   }
   __syncthreads();
-  const int lane = tid & 63;
   for (int k = tid >> 6; k < p.n_buckets; k += 16) {
     float x = 0.f;
-    for (int d = lane; d < entries; d += 64)
-      if (bucket[d] == k)
-        for (int g = 0; g < groups; ++g) x += sums[g * entries + d];
+#pragma unroll 4
+    for (int d = lane; d < entries; d += 64) x += bucket[d] == k ? sums[d] : 0.f;
     x = join_lanes<64>(x, AddOp());
     if (lane == 0) {
       const int64_t at = static_cast<int64_t>(k) * p.Hq + h;
@@ -722,8 +749,10 @@ hipError_t run_bwd(const AttnParams& p, hipStream_t s) {
                    p, s);
   if (e != hipSuccess) return e;
   if (BIAS && p.dtable) {
-    const int groups = 1024 / static_cast<int>(n) > 1 ? 1024 / static_cast<int>(n) : 1;
-    attn_dtable_kernel<<<p.Hq, 1024, (groups + 1) * n * 4, s>>>(p, tiles);
+    attn_dsum_kernel<<<dim3(p.Hq, static_cast<unsigned>((n + 63) / 64)), 1024, 0, s>>>(p, tiles);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    attn_dtable_kernel<<<p.Hq, 1024, 2 * n * sizeof(float), s>>>(p);
     e = hipGetLastError();
   }
   return e;
@@ -751,6 +780,7 @@ size_t lay_out(AttnParams& p, int D, size_t entries, char* base) {
   p.qhi = reinterpret_cast<int*>(take(rows * 4));
   p.dpart = reinterpret_cast<float*>(
       take(static_cast<size_t>(p.B) * p.Hq * ((p.Tq + 127) / 128) * entries * 4));
+  p.dsum = reinterpret_cast<float*>(take(p.Hq * entries * 4));
   p.kvpart = reinterpret_cast<float*>(take(2 * parts * p.B * p.Hk * p.Tk * D * 4));
   return at;
 }

@@ -120,6 +120,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnPar
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int bh = head_of_group(blockIdx.x, gridDim.x), b = bh / p.Hq, h = bh % p.Hq;
   const int hk = h / p.group;
+  BiasStage bs;
+  if constexpr (BIAS) bs.buckets(p, tid);
   const int tile = query_tile(p, b, reinterpret_cast<int*>(ranges), tid);
   const int i0 = tile * kRows + wave * 32;
   const int i = i0 + (lane & 31);
@@ -133,6 +135,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnPar
     hull[2 * wave + 1] = wh.y;
   }
   if (lane < 32) ranges[wave * 32 + lane] = rng;
+  if constexpr (BIAS) bs.values(p, h);
   __syncthreads();
   int first = 0x7FFFFFFF, last = 0;
 #pragma unroll
@@ -169,7 +172,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnPar
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[t][r] = 0.f;
   float m = kLowest, l = 0.f;
-  if constexpr (BIAS) stage_bias(p, h, bias, tid);
+  if constexpr (BIAS) bs.store(p, h, bias, tid);
   const bool gaps = p.ranges && has_gaps(ranges, last, tid);
   wait_tile();
   // Turns in which the wave has nothing to see have a loop of their own: a
