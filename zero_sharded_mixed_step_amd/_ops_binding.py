@@ -78,51 +78,66 @@ def zero_ops_strerror(status: int) -> str:
     return ops_lib().zero_ops_strerror(int(status)).decode()
 
 
-def _call(fn, args, stream):
-    status = getattr(ops_lib(), fn)(args, _stream(stream))
+def _device():
+    """The current device, asked once a call (the checks and packing below are
+    what a small call costs: some 10 us of host time for 10 tensors)."""
+    if torch.cuda.is_initialized():
+        return torch._C._cuda_getDevice()
+    return torch.cuda.current_device() if torch.cuda.is_available() else -1
+
+
+def _call(fn, args, stream, dev):
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        s = _stream(stream)
+    status = getattr(ops_lib(), fn)(args, s)
     if status != 0:
         raise ZeroOpsError(status, fn)
 
 
-def _tensor(t, name, shape, dtypes):
-    """Address of a tensor on the current device with the given shape (None: any
-    size there), whose last dimension is contiguous."""
+def _tensor(t, name, shape, dtype, dev):
+    """Address and strides of a tensor on device `dev` with the given shape
+    and dtype, whose last dimension is contiguous."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}; the library launches on the current "
-                         f"device, cuda:{torch.cuda.current_device()}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(dtypes)}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, the call needs {shape}")
-    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+                         f"device, cuda:{dev}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, the call needs {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, the call needs {tuple(shape)}")
+    st = t.stride()
+    if st and st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t.data_ptr()
+    return t.data_ptr(), st
 
 
-def _flat(t, name, shape, dtypes):
-    """As _tensor, of a contiguous tensor; 0 for None."""
+def _flat(t, name, shape, dtype, dev):
+    """Address of a contiguous tensor; 0 for None."""
     if t is None:
         return 0
-    p = _tensor(t, name, shape, dtypes)
+    p, _ = _tensor(t, name, shape, dtype, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return p
 
 
-def _strides(t):
-    """Strides of all dimensions but the last (0 where the size is 1: a stride
-    that nothing uses need not be aligned)."""
-    return [0 if n == 1 else s for n, s in zip(t.shape[:-1], t.stride()[:-1])]
+def _used(shape, strides):
+    """Strides of all dimensions but the last, 0 where the size is 1: a stride
+    that nothing uses need not be aligned."""
+    if 1 in shape:
+        return tuple(0 if n == 1 else s for n, s in zip(shape[:-1], strides))
+    return strides[:-1]
 
 
-def _workspace(ws):
+def _workspace(ws, dev):
     if ws is None:
         return 0, 0
     if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA (HIP) tensor")
-    if ws.device.index != torch.cuda.current_device():
+    if ws.get_device() != dev:
         raise ValueError(f"workspace is on {ws.device}, not on the current device")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
@@ -139,6 +154,19 @@ def zero_qk_norm_rope_workspace_bytes(T: int, D: int) -> int:
     return ops_lib().zero_qk_norm_rope_workspace_bytes(int(T), int(D))
 
 
+_NO_STRIDE = (0, 0)
+
+
+def _heads(x, name, T, like, dtype, dev):
+    """Address and two strides of one tensor of rows of heads shaped as `like`."""
+    if like is None:
+        if x is not None:
+            raise ValueError(f"{name} without its input")
+        return 0, _NO_STRIDE
+    p, st = _tensor(x, name, like.shape, dtype, dev)
+    return p, _used(like.shape, st)
+
+
 def _norm_call(fn, q, k, outs, grads, wq, wk, dwq, dwk, eps, pos, inv_freq, interleaved,
                workspace, stream):
     x = q if q is not None else k
@@ -147,47 +175,37 @@ def _norm_call(fn, q, k, outs, grads, wq, wk, dwq, dwk, eps, pos, inv_freq, inte
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
         raise ValueError("q and k are (T, H, D) tensors")
     T, _, D = x.shape
-    code = _CODES.get(x.dtype)
+    dt = x.dtype
+    code = _CODES.get(dt)
     if code is None:
-        raise TypeError(f"q and k are float32 or bfloat16, not {x.dtype}")
-    dt = (x.dtype,)
-    ptrs, strides = {}, {}
-
-    def rows(name, t, like):
-        if like is None:
-            if t is not None:
-                raise ValueError(f"{name} without its input")
-            ptrs[name], strides[name] = 0, (0, 0)
-        else:
-            ptrs[name] = _tensor(t, name, (T, like.shape[1], D), dt)
-            strides[name] = _strides(t)
-
-    rows("q", q, q)
-    rows("k", k, k)
-    for n in ("yq", "yk", "dyq", "dyk", "dq", "dk"):
-        if n in outs or n in grads:
-            rows(n, outs.get(n, grads.get(n)), q if n[-1] == "q" else k)
-        else:
-            ptrs[n], strides[n] = 0, (0, 0)
-    pairs = 0
+        raise TypeError(f"q and k are float32 or bfloat16, not {dt}")
+    if k is not None and (k.dim() != 3 or k.shape[0] != T or k.shape[2] != D):
+        raise ValueError(f"k has shape {tuple(k.shape)}, the call needs ({T}, H, {D})")
+    dev = _device()
+    pq, sq = _heads(q, "q", T, q, dt, dev)
+    pk, sk = _heads(k, "k", T, k, dt, dev)
+    poq, soq = _heads(outs[0], "the output of q", T, q, dt, dev)
+    pok, sok = _heads(outs[1], "the output of k", T, k, dt, dev)
+    pairs = pos_p = freq_p = 0
     if inv_freq is not None:
         pairs = inv_freq.shape[0]
-        pos_p = _flat(pos, "pos", (T,), (torch.int32,))
-        freq_p = _flat(inv_freq, "inv_freq", (pairs,), (torch.float64,))
-        if not pos_p:
+        pos_p = _flat(pos, "pos", (T,), torch.int32, dev)
+        freq_p = _flat(inv_freq, "inv_freq", (pairs,), torch.float64, dev)
+        if pos is None:
             raise ValueError("inv_freq needs pos")
+    wqp, wkp = _flat(wq, "wq", (D,), dt, dev), _flat(wk, "wk", (D,), dt, dev)
+    head = (_NORM_ARGS.size, T, 0 if q is None else q.shape[1], 0 if k is None else k.shape[1], D,
+            2 * pairs, code, 1 if interleaved else 0, eps, pq, pk, wqp, wkp, pos_p, freq_p)
+    if grads is None:
+        args = _NORM_ARGS.pack(*head, poq, pok, 0, 0, 0, 0, 0, 0, *sq, *sk, *soq, *sok, 0, 0, 0, 0,
+                               0, 0, 0, 0, 0, 0)
     else:
-        pos_p = freq_p = 0
-    w = [_flat(t, n, (D,), dt) for n, t in
-         (("wq", wq), ("wk", wk), ("dwq", dwq), ("dwk", dwk))]
-    ws = _workspace(workspace)
-    args = _NORM_ARGS.pack(
-        _NORM_ARGS.size, T, 0 if q is None else q.shape[1], 0 if k is None else k.shape[1], D,
-        2 * pairs, code, 1 if interleaved else 0, float(eps), ptrs["q"], ptrs["k"], w[0], w[1],
-        pos_p, freq_p, ptrs["yq"], ptrs["yk"], ptrs["dyq"], ptrs["dyk"], ptrs["dq"], ptrs["dk"],
-        w[2], w[3], *strides["q"], *strides["k"], *strides["yq"], *strides["yk"],
-        *strides["dyq"], *strides["dyk"], *strides["dq"], *strides["dk"], *ws)
-    _call(fn, args, stream)
+        pgq, sgq = _heads(grads[0], "dyq", T, q, dt, dev)
+        pgk, sgk = _heads(grads[1], "dyk", T, k, dt, dev)
+        args = _NORM_ARGS.pack(*head, 0, 0, pgq, pgk, poq, pok, _flat(dwq, "dwq", (D,), dt, dev),
+                               _flat(dwk, "dwk", (D,), dt, dev), *sq, *sk, 0, 0, 0, 0, *sgq, *sgk,
+                               *soq, *sok, *_workspace(workspace, dev))
+    _call(fn, args, stream, dev)
 
 
 def zero_qk_norm_rope_fwd(q, k, yq, yk, *, wq=None, wk=None, eps=1e-6, pos=None, inv_freq=None,
@@ -196,7 +214,7 @@ def zero_qk_norm_rope_fwd(q, k, yq, yk, *, wq=None, wk=None, eps=1e-6, pos=None,
     wq and wk (D), and the rotation by pos (T, int32) times inv_freq (float64,
     half the rotated width): yq and yk.  q or k may be None, views of one
     projection's output are fine, and yq may be q."""
-    _norm_call("zero_qk_norm_rope_fwd", q, k, {"yq": yq, "yk": yk}, {}, wq, wk, None, None, eps,
+    _norm_call("zero_qk_norm_rope_fwd", q, k, (yq, yk), None, wq, wk, None, None, eps,
                pos, inv_freq, interleaved, None, stream)
 
 
@@ -206,8 +224,8 @@ def zero_qk_norm_rope_bwd(q, k, dyq, dyk, dq, dk, *, wq=None, wk=None, dwq=None,
     """Gradients of zero_qk_norm_rope_fwd from its inputs and dyq, dyk: dq, dk
     and, where given, dwq and dwk (which need a workspace of
     zero_qk_norm_rope_workspace_bytes(T, D) bytes)."""
-    _norm_call("zero_qk_norm_rope_bwd", q, k, {"dq": dq, "dk": dk}, {"dyq": dyq, "dyk": dyk}, wq,
-               wk, dwq, dwk, eps, pos, inv_freq, interleaved, workspace, stream)
+    _norm_call("zero_qk_norm_rope_bwd", q, k, (dq, dk), (dyq, dyk), wq, wk,
+               dwq, dwk, eps, pos, inv_freq, interleaved, workspace, stream)
 
 
 # -------------------------------------------------------------- attention ---
@@ -260,9 +278,9 @@ def zero_attn_ranges(doc, ranges, *, prefix=None, causal=True, stream=None) -> N
     if not isinstance(doc, torch.Tensor) or doc.dim() != 2:
         raise ValueError("doc is a (B, T) tensor")
     B, T = doc.shape
-    i32 = (torch.int32,)
-    p = (_flat(doc, "doc", (B, T), i32), _flat(prefix, "prefix", (B, T), i32),
-         _flat(ranges, "ranges", (B, T, 2), i32))
+    dev, i32 = _device(), torch.int32
+    p = (_flat(doc, "doc", (B, T), i32, dev), _flat(prefix, "prefix", (B, T), i32, dev),
+         _flat(ranges, "ranges", (B, T, 2), i32, dev))
     if ranges is None:
         raise TypeError("ranges must be a CUDA (HIP) tensor")
     status = ops_lib().zero_attn_ranges(p[0], p[1] or None, B, T, int(bool(causal)), p[2],
@@ -271,22 +289,23 @@ def zero_attn_ranges(doc, ranges, *, prefix=None, causal=True, stream=None) -> N
         raise ZeroOpsError(status, "zero_attn_ranges")
 
 
-_BF = (_BF16,)
-
-
 def _attn_call(fn, q, k, v, o, lse, do, dq, dk, dv, dtable, scale, cap, ranges, causal, table,
                buckets, workspace, stream):
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q is a (B, Tq, Hq, D) tensor")
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("k is a (B, Tk, Hk, D) tensor")
-    B, Tq, Hq, D = q.shape
-    Tk, Hk = k.shape[1], k.shape[2]
-    qs, ks = (B, Tq, Hq, D), (B, Tk, Hk, D)
-    bwd = do is not None
-    ptr = [_tensor(q, "q", qs, _BF), _tensor(k, "k", ks, _BF), _tensor(v, "v", ks, _BF),
-           _flat(ranges, "ranges", (B, Tq, 2), (torch.int32,))]
-    n_buckets = reach = code = 0
+    B, Tq, Hq, D = qs = q.shape
+    ks = k.shape
+    Tk, Hk = ks[1], ks[2]
+    if ks[0] != B or ks[3] != D:
+        raise ValueError(f"k has shape {tuple(ks)}, the call needs ({B}, Tk, Hk, {D})")
+    dev, bf, f32 = _device(), _BF16, torch.float32
+    q_, sq = _tensor(q, "q", qs, bf, dev)
+    k_, sk = _tensor(k, "k", ks, bf, dev)
+    v_, sv = _tensor(v, "v", ks, bf, dev)
+    o_, so = _tensor(o, "o", qs, bf, dev)
+    n_buckets = reach = code = table_ = buckets_ = 0
     if table is not None:
         n_buckets = table.shape[0]
         if buckets is None or buckets.dim() != 1 or buckets.shape[0] % 2 == 0:
@@ -295,27 +314,29 @@ def _attn_call(fn, q, k, v, o, lse, do, dq, dk, dv, dtable, scale, cap, ranges, 
         if table.dtype not in _CODES:
             raise TypeError(f"bias_table is float32 or bfloat16, not {table.dtype}")
         code = _CODES[table.dtype]
-        ptr += [_flat(table, "bias_table", (n_buckets, Hq), (table.dtype,)),
-                _flat(buckets, "bias_buckets", (2 * reach + 1,), (torch.int32,))]
+        table_ = _flat(table, "bias_table", (n_buckets, Hq), table.dtype, dev)
+        buckets_ = _flat(buckets, "bias_buckets", (2 * reach + 1,), torch.int32, dev)
     elif dtable is not None:
         raise ValueError("dbias_table without bias_table")
+    ptr = (q_, k_, v_, _flat(ranges, "ranges", (B, Tq, 2), torch.int32, dev), table_, buckets_, o_,
+           _flat(lse, "lse", (B, Hq, Tq), f32, dev))
+    strides = _used(qs, sq) + _used(ks, sk) + _used(ks, sv) + _used(qs, so)
+    if do is not None:
+        do_, sdo = _tensor(do, "do", qs, bf, dev)
+        dq_, sdq = _tensor(dq, "dq", qs, bf, dev)
+        dk_, sdk = _tensor(dk, "dk", ks, bf, dev)
+        dv_, sdv = _tensor(dv, "dv", ks, bf, dev)
+        ptr += (do_, dq_, dk_, dv_,
+                0 if dtable is None else
+                _flat(dtable, "dbias_table", (n_buckets, Hq), table.dtype, dev))
+        strides += _used(qs, sdo) + _used(qs, sdq) + _used(ks, sdk) + _used(ks, sdv)
     else:
-        ptr += [0, 0]
-    ptr += [_tensor(o, "o", qs, _BF), _flat(lse, "lse", (B, Hq, Tq), (torch.float32,))]
-    strides = _strides(q) + _strides(k) + _strides(v) + _strides(o)
-    if bwd:
-        ptr += [_tensor(do, "do", qs, _BF), _tensor(dq, "dq", qs, _BF), _tensor(dk, "dk", ks, _BF),
-                _tensor(dv, "dv", ks, _BF),
-                _flat(dtable, "dbias_table", (n_buckets, Hq), (table.dtype,))
-                if dtable is not None else 0]
-        strides += _strides(do) + _strides(dq) + _strides(dk) + _strides(dv)
-    else:
-        ptr += [0] * 5
-        strides += [0] * 12
+        ptr += (0, 0, 0, 0, 0)
+        strides += (0,) * 12
     args = _ATTN_ARGS.pack(_ATTN_ARGS.size, B, Tq, Tk, Hq, Hk, D, 1 if causal else 0, code,
                            n_buckets, reach, D ** -0.5 if scale is None else scale, cap, *ptr,
-                           *strides, *_workspace(workspace))
-    _call(fn, args, stream)
+                           *strides, *_workspace(workspace, dev))
+    _call(fn, args, stream, dev)
 
 
 def zero_attn_fwd(q, k, v, o, lse, *, scale=None, cap=0.0, ranges=None, causal=False,
@@ -354,16 +375,16 @@ def _distill_call(fn, z, idx, val, loss, stats, dz, temperature, tlse, weight, g
     code = _CODES.get(z.dtype)
     if code is None:
         raise TypeError(f"logits are float32 or bfloat16, not {z.dtype}")
-    dt, f32 = (z.dtype,), (torch.float32,)
+    dev, dt, f32 = _device(), z.dtype, torch.float32
+    z_, sz = _tensor(z, "logits", z.shape, dt, dev)
+    dz_, sdz = (0, (V, 1)) if dz is None else _tensor(dz, "dlogits", z.shape, dt, dev)
     args = _DISTILL_ARGS.pack(
-        _DISTILL_ARGS.size, N, V, K, code, temperature, grad_scale,
-        _tensor(z, "logits", (N, V), dt), _flat(idx, "teacher_idx", (N, K), (torch.int32,)),
-        _flat(val, "teacher_val", (N, K), dt), _flat(tlse, "teacher_lse", (N,), f32),
-        _flat(weight, "row_weight", (N,), f32), _flat(loss, "loss", (N,), f32),
-        _flat(stats, "stats", (N, 2), f32),
-        0 if dz is None else _tensor(dz, "dlogits", (N, V), dt), z.stride(0),
-        V if dz is None else dz.stride(0))
-    _call(fn, args, stream)
+        _DISTILL_ARGS.size, N, V, K, code, temperature, grad_scale, z_,
+        _flat(idx, "teacher_idx", (N, K), torch.int32, dev),
+        _flat(val, "teacher_val", (N, K), dt, dev), _flat(tlse, "teacher_lse", (N,), f32, dev),
+        _flat(weight, "row_weight", (N,), f32, dev), _flat(loss, "loss", (N,), f32, dev),
+        _flat(stats, "stats", (N, 2), f32, dev), dz_, sz[0], sdz[0])
+    _call(fn, args, stream, dev)
 
 
 def zero_distill_fwd(logits, teacher_idx, teacher_val, loss, stats, *, dlogits=None,

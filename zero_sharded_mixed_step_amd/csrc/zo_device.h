@@ -32,7 +32,7 @@ __device__ __forceinline__ uint32_t uniform(uint32_t x) {
   return __builtin_amdgcn_readfirstlane(x);
 }
 
-// Joins a 32-bit value over groups of G consecutive lanes (all of them get the
+// Joins a 32- or 64-bit value over groups of G consecutive lanes (all of them get the
 // result) by moves between registers: neighbours, pairs, mirrored halves of 8 and
 // of 16 lanes (the halves are uniform by then), then rows of 16 and halves of the
 // wave swapped.  A shuffle through the shared-memory crossbar takes some 100 cycles
@@ -41,23 +41,37 @@ template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_move(uint32_t x) {
   return __builtin_amdgcn_update_dpp(x, x, CTRL, 0xF, 0xF, false);
 }
+template <typename T, typename Move>
+__device__ __forceinline__ T move_words(T x, Move move) {
+  if constexpr (sizeof(T) == 4) {
+    return __builtin_bit_cast(T, move(__builtin_bit_cast(uint32_t, x)));
+  } else {
+    const uint64_t v = __builtin_bit_cast(uint64_t, x);
+    const uint64_t lo = move(static_cast<uint32_t>(v)), hi = move(static_cast<uint32_t>(v >> 32));
+    return __builtin_bit_cast(T, hi << 32 | lo);
+  }
+}
 template <int G, typename T, typename Op>
 __device__ __forceinline__ T join_lanes(T x, Op op) {
-  static_assert(sizeof(T) == 4 && G <= 64, "32-bit values");
-  const auto bits = [](T v) { return __builtin_bit_cast(uint32_t, v); };
-  const auto value = [](uint32_t v) { return __builtin_bit_cast(T, v); };
-  if constexpr (G >= 2) x = op(x, value(dpp_move<0xB1>(bits(x))));    // lanes 1 0 3 2
-  if constexpr (G >= 4) x = op(x, value(dpp_move<0x4E>(bits(x))));    // lanes 2 3 0 1
-  if constexpr (G >= 8) x = op(x, value(dpp_move<0x141>(bits(x))));   // 8 lanes mirrored
-  if constexpr (G >= 16) x = op(x, value(dpp_move<0x140>(bits(x))));  // 16 lanes mirrored
-  if constexpr (G >= 32) {
-    const auto r = __builtin_amdgcn_permlane16_swap(bits(x), bits(x), false, false);
-    x = op(value(r[0]), value(r[1]));
-  }
-  if constexpr (G >= 64) {
-    const auto r = __builtin_amdgcn_permlane32_swap(bits(x), bits(x), false, false);
-    x = op(value(r[0]), value(r[1]));
-  }
+  static_assert((sizeof(T) == 4 || sizeof(T) == 8) && G <= 64);
+  if constexpr (G >= 2) x = op(x, move_words(x, dpp_move<0xB1>));    // lanes 1 0 3 2
+  if constexpr (G >= 4) x = op(x, move_words(x, dpp_move<0x4E>));    // lanes 2 3 0 1
+  if constexpr (G >= 8) x = op(x, move_words(x, dpp_move<0x141>));   // 8 lanes mirrored
+  if constexpr (G >= 16) x = op(x, move_words(x, dpp_move<0x140>));  // 16 lanes mirrored
+  if constexpr (G >= 32)
+    x = op(move_words(x, [](uint32_t v) {
+             return __builtin_amdgcn_permlane16_swap(v, v, false, false)[0];
+           }),
+           move_words(x, [](uint32_t v) {
+             return __builtin_amdgcn_permlane16_swap(v, v, false, false)[1];
+           }));
+  if constexpr (G >= 64)
+    x = op(move_words(x, [](uint32_t v) {
+             return __builtin_amdgcn_permlane32_swap(v, v, false, false)[0];
+           }),
+           move_words(x, [](uint32_t v) {
+             return __builtin_amdgcn_permlane32_swap(v, v, false, false)[1];
+           }));
   return x;
 }
 

@@ -137,47 +137,23 @@ __device__ __forceinline__ void keep_packed(Chunk<E> (&held)[CH]) {
   for (int c = 0; c < CH; ++c) asm volatile("" : "+v"(held[c].r));
 }
 
-// Joins a value over the workgroup, in one fixed order; everyone gets it.
-template <int G, typename X, typename Op>
-__device__ __forceinline__ X join_group(X x, Op op) {
-  if constexpr (sizeof(X) == 4) {
-    return join_lanes<G>(x, op);
-  } else {
-#pragma unroll
-    for (int d = 1; d < G; d <<= 1) x = op(x, __shfl_xor(x, d));
-    return x;
-  }
-}
-template <int NT, typename X, typename Op>
-__device__ __forceinline__ X join(X x, Op op, double* scratch) {
-  x = join_group<64>(x, op);
-  X* s = reinterpret_cast<X*>(scratch);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = x;
-  __syncthreads();
-  x = s[(threadIdx.x & 63) % (NT / 64)];
-  return join_group<NT / 64>(x, op);
-}
-
 // The teacher's side of a row, in shared memory: p[k], the student's logit
-// z[k] (of entries in [from, to)) and idx[k], -1 for an absent entry.
+// z[k] (of entries in [from, to)) and idx[k], -1 for an absent entry; and what
+// the row needs of them.  All of it is one wave's work, wave-wide sums and no
+// barrier, so that the workgroup's others are at the row meanwhile.
 struct Teacher {
   float* p;
   float* z;
   int* idx;
-  double mass;   // sum of p
-  double cross;  // sum of p (log p - z / tau)
-  bool any;
+  double* sums;  // mass: sum of p; cross: sum of p (log p - z / tau); any entry
 };
 
-template <typename E, int NT>
+template <typename E>
 __device__ __forceinline__ void load_teacher(const DistillParams& p, int64_t n, const E* z,
-                                             int64_t from, int64_t to, double* scratch,
-                                             Teacher& t) {
-  const int tid = threadIdx.x;
+                                             int64_t from, int64_t to, int lane, const Teacher& t) {
   float mx = -kInf;
   int any = 0;
-  for (int k = tid; k < p.K; k += NT) {
+  for (int k = lane; k < p.K; k += 64) {
     const int i = p.idx[n * p.K + k];
     const bool ok = i >= 0 && i < p.V;
     t.idx[k] = ok ? i : -1;
@@ -187,21 +163,19 @@ __device__ __forceinline__ void load_teacher(const DistillParams& p, int64_t n, 
     any |= ok;
     mx = MaxOp()(mx, v);
   }
-  t.any = __syncthreads_or(any) != 0;
   double base;
   if (p.tlse != nullptr) {
     base = p.tlse[n];
   } else {
-    mx = join<NT>(mx, MaxOp(), scratch);
+    mx = join_lanes<64>(mx, MaxOp());
     const double m = static_cast<double>(mx) * p.inv_tau;
     double s = 0.0;
-    for (int k = tid; k < p.K; k += NT)
+    for (int k = lane; k < p.K; k += 64)
       if (t.idx[k] >= 0) s += exp(static_cast<double>(t.p[k]) * p.inv_tau - m);
-    s = join<NT>(s, AddOp(), scratch);
-    base = m + log(s);
+    base = m + log(join_lanes<64>(s, AddOp()));
   }
   double mass = 0.0, cross = 0.0;
-  for (int k = tid; k < p.K; k += NT) {
+  for (int k = lane; k < p.K; k += 64) {
     double pk = 0.0;
     if (t.idx[k] >= 0) {
       const double lp = static_cast<double>(t.p[k]) * p.inv_tau - base;
@@ -211,8 +185,14 @@ __device__ __forceinline__ void load_teacher(const DistillParams& p, int64_t n, 
     }
     t.p[k] = static_cast<float>(pk);
   }
-  t.mass = join<NT>(mass, AddOp(), scratch);
-  t.cross = join<NT>(cross, AddOp(), scratch);
+  mass = join_lanes<64>(mass, AddOp());
+  cross = join_lanes<64>(cross, AddOp());
+  any = __any(any) != 0;
+  if (lane == 0) {
+    t.sums[0] = mass;
+    t.sums[1] = cross;
+    t.sums[2] = any ? 1.0 : 0.0;
+  }
 }
 
 __device__ __forceinline__ float prob(float z, float inv_tau, float lse) {
@@ -232,33 +212,66 @@ __device__ __forceinline__ void store_entries(const DistillParams& p, const Row<
   }
 }
 
+// Shared memory of the kernels: the waves' parts of the maximum and of the two sums, the
+// teacher's, and the bit map.
+template <int NT>
+struct DistillShared {
+  double* sum;   // [2][waves]
+  float* top;    // [waves]
+  Teacher t;
+  uint32_t* bits;
+  __device__ __forceinline__ DistillShared(char* smem, int K) {
+    sum = reinterpret_cast<double*>(smem);
+    t.sums = sum + 2 * (NT / 64);
+    top = reinterpret_cast<float*>(t.sums + 4);
+    bits = reinterpret_cast<uint32_t*>(top + NT / 64);         // 16-byte aligned, as is smem
+    t.p = reinterpret_cast<float*>(bits);
+    t.z = t.p + K;
+    t.idx = reinterpret_cast<int*>(t.z + K);
+    bits += (3 * K + 3) & ~3;
+  }
+  static size_t bytes(int K, int64_t bit_words) {
+    return 2 * (NT / 64) * 8 + 4 * 8 + (NT / 64) * 4 + ((3 * K + 3) & ~3) * 4 + bit_words * 4;
+  }
+};
+
+__host__ __device__ constexpr int64_t bit_words(int64_t V, int n) { return ((V + n) / 128 + 1) * 4; }
+
 // Forward: loss and statistics, and the gradient if asked for.  CH > 0: the
 // row stays in registers, CH chunks to a thread; CH = 0: it is read again.
+// The workgroup's last wave first does the teacher's work and marks the
+// entries, while the others load the row; two barriers, of the maximum and of
+// the sums, come before the gradient.  64 registers a thread, two rows to a
+// compute unit, one loading while the other computes.
 template <typename E, int NT, int CH>
-__global__ __launch_bounds__(NT, CH <= (sizeof(E) == 2 ? 8 : 4) ? 8 : 4) void distill_fwd_kernel(const DistillParams p) {
-  constexpr int kN = Chunk<E>::kN;
+__global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void distill_fwd_kernel(
+    const DistillParams p) {
+  constexpr int kN = Chunk<E>::kN, kW = NT / 64;
   constexpr int kHeld = CH > 0 ? CH : 1;
   extern __shared__ __align__(16) char smem[];
-  double* scratch = reinterpret_cast<double*>(smem);           // [NT / 64]
-  Teacher t;
-  t.p = reinterpret_cast<float*>(scratch + NT / 64);
-  t.z = t.p + p.K;
-  t.idx = reinterpret_cast<int*>(t.z + p.K);
-  uint32_t* bits = reinterpret_cast<uint32_t*>(t.idx + p.K);   // with a tail
+  const DistillShared<NT> sh(smem, p.K);
+  const Teacher& t = sh.t;
+  uint32_t* bits = sh.bits;
 
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t n = blockIdx.x;
   const Row<E> in(p.z, n * p.z_stride, p.V), out(p.dz, n * p.dz_stride, p.V);
   const int chunks = in.chunks();
   const float w = p.weight ? p.weight[n] : 1.f;
-  const float inv_tau = static_cast<float>(p.inv_tau);
+  const float k2 = static_cast<float>(p.inv_tau * 1.4426950408889634);
 
-  if (p.tail)
-    for (int64_t i = tid; i < (p.V + kN) / 32 + 1; i += NT) bits[i] = 0;
-  load_teacher<E, NT>(p, n, in.p, 0, p.V, scratch, t);
-  if (p.tail)
-    for (int64_t i = tid; i < (p.V + kN) / 32 + 1; i += NT) bits[i] = 0;
-  load_teacher<E, NT>(p, n, in.p, 0, p.V, scratch, t);
+  if (wave == kW - 1) {
+    if (p.tail)
+      for (int64_t i = 4 * lane; i < bit_words(p.V, kN); i += 256)
+        *reinterpret_cast<u32x4*>(bits + i) = u32x4{0, 0, 0, 0};
+    load_teacher<E>(p, n, in.p, 0, p.V, lane, t);
+    if (p.tail)                            // (the wave's own writes: in order)
+      for (int k = lane; k < p.K; k += 64)
+        if (t.idx[k] >= 0) {
+          const int64_t e = t.idx[k] + in.shift;
+          atomicOr(&bits[e >> 5], 1u << (e & 31));
+        }
+  }
   Chunk<E> held[kHeld];
   if constexpr (CH > 0) {
 #pragma unroll
@@ -267,41 +280,12 @@ __global__ __launch_bounds__(NT, CH <= (sizeof(E) == 2 ? 8 : 4) ? 8 : 4) void di
       if (tid + c * NT < chunks) held[c] = in.load(tid + c * NT);
     }
   }
-  // a row without weight, or with nothing to be compared with: statistics only
-  const bool live = w != 0.f && (t.any || p.tail);
-  if (p.tail) {
-    for (int k = tid; k < p.K; k += NT)
-      if (t.idx[k] >= 0) {
-        const int64_t e = t.idx[k] + in.shift;
-        atomicOr(&bits[e >> 5], 1u << (e & 31));
-      }
-    __syncthreads();
-  }
 
-  // running maximum (streamed rows), sum and sum outside the entries
   float m = -kInf, sum = 0.f, rest = 0.f;
   const auto chunk_max = [&](const Chunk<E>& x, float a) {
 #pragma unroll
     for (int e = 0; e < kN; ++e) a = fmaxf(a, x.get(e));
     return a;
-  };
-  const float k2 = inv_tau * kLog2e;
-  const auto chunk_sum = [&](const Chunk<E>& x, int c, float mx) {
-    uint32_t marked = 0;
-    if (p.tail) {
-      const int64_t e = static_cast<int64_t>(c) * kN;
-      marked = (bits[e >> 5] >> (e & 31)) & ((1u << kN) - 1);
-    }
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < kN; ++e) s += exp2_hw((x.get(e) - mx) * k2);
-    sum += s;
-    rest += marked != 0 ? 0.f : s;
-    if (marked != 0) {
-#pragma unroll
-      for (int e = 0; e < kN; ++e)
-        if (!((marked >> e) & 1u)) rest += exp2_hw((x.get(e) - mx) * k2);
-    }
   };
   if constexpr (CH > 0) {
 #pragma unroll
@@ -309,32 +293,67 @@ __global__ __launch_bounds__(NT, CH <= (sizeof(E) == 2 ? 8 : 4) ? 8 : 4) void di
   } else {
     for (int c = tid; c < chunks; c += NT) m = chunk_max(in.load(c), m);
   }
-  m = join<NT>(m, MaxOp(), scratch);
-  if constexpr (CH > 0) keep_packed(held);
+  m = join_lanes<64>(m, MaxOp());
+  if (lane == 0) sh.top[wave] = m;
+  __syncthreads();
+  m = join_lanes<kW>(sh.top[lane % kW], MaxOp());
   if (m == -kInf) m = 0.f;               // nothing but -inf: a sum of 0, not of NaN
+  if constexpr (CH > 0) keep_packed(held);
+
+  // exp((z - m) / tau) = 2^(z k2 - m2), with m2 the rounded m k2: the same in
+  // every term, and what the logarithm of the sum is put together with again
+  const float m2 = m * k2;
+  const auto power = [&](float z) { return exp2_hw(__builtin_fmaf(z, k2, -m2)); };
+  const auto chunk_sum = [&](const Chunk<E>& x, int c) {
+    uint32_t marked = 0;
+    if (p.tail) {
+      const int64_t e = static_cast<int64_t>(c) * kN;
+      marked = (bits[e >> 5] >> (e & 31)) & ((1u << kN) - 1);
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < kN; ++e) s += power(x.get(e));
+    sum += s;
+    rest += marked != 0 ? 0.f : s;
+    if (marked != 0) {
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+        if (!((marked >> e) & 1u)) rest += power(x.get(e));
+    }
+  };
   if constexpr (CH > 0) {
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-      if (tid + c * NT < chunks) chunk_sum(held[c], tid + c * NT, m);
+      if (tid + c * NT < chunks) chunk_sum(held[c], tid + c * NT);
   } else {
-    for (int c = tid; c < chunks; c += NT) chunk_sum(in.load(c), c, m);
+    for (int c = tid; c < chunks; c += NT) chunk_sum(in.load(c), c);
   }
   if constexpr (CH > 0) keep_packed(held);
-  const double total = join<NT>(static_cast<double>(sum), AddOp(), scratch);
-  double outside = 0.0, mass = 0.0, coef = 1.0;
+  const double part = join_lanes<64>(static_cast<double>(sum), AddOp());
+  const double part_rest = join_lanes<64>(static_cast<double>(rest), AddOp());
+  if (lane == 0) {
+    sh.sum[wave] = part;
+    sh.sum[kW + wave] = part_rest;
+  }
+  __syncthreads();
+  const double total = join_lanes<kW>(sh.sum[lane % kW], AddOp());
+  const double outside = p.tail ? join_lanes<kW>(sh.sum[kW + lane % kW], AddOp()) : 0.0;
+  double mass = 0.0, coef = 1.0;
   if (p.tail) {
-    outside = join<NT>(static_cast<double>(rest), AddOp(), scratch);
-    mass = t.mass < 1.0 ? 1.0 - t.mass : 0.0;
+    mass = t.sums[0] < 1.0 ? 1.0 - t.sums[0] : 0.0;
     if (mass > 0.0) coef = 1.0 - mass * (total / outside);
   }
+  // a row without weight, or with nothing to be compared with: statistics only
+  const bool live = w != 0.f && (t.sums[2] != 0.0 || p.tail);
   if (p.dz != nullptr) {
     const float scale = static_cast<float>(p.grad_scale * p.tau * static_cast<double>(w));
     if (live) {
-      const float inv = static_cast<float>(1.0 / total), other = static_cast<float>(coef) * scale;
+      const float inv = static_cast<float>(1.0 / total);
+      const float other = static_cast<float>(coef) * scale * inv;
       const auto grad = [&](const Chunk<E>& x, int c) {
         float y[kN];
 #pragma unroll
-        for (int e = 0; e < kN; ++e) y[e] = exp2_hw((x.get(e) - m) * k2) * inv * other;
+        for (int e = 0; e < kN; ++e) y[e] = power(x.get(e)) * other;
         out.store(c, in.shift, y);
       };
       if constexpr (CH > 0) {
@@ -344,9 +363,7 @@ __global__ __launch_bounds__(NT, CH <= (sizeof(E) == 2 ? 8 : 4) ? 8 : 4) void di
       } else {
         for (int c = tid; c < chunks; c += NT) grad(in.load(c), c);
       }
-      store_entries<E, NT>(p, out, t, scale, 0, p.V, [&](float z) {
-        return exp2_hw((z - m) * k2) * inv;
-      });
+      store_entries<E, NT>(p, out, t, scale, 0, p.V, [&](float z) { return power(z) * inv; });
     } else {
       const float zero[kN] = {};
       for (int c = tid; c < chunks; c += NT) out.store(c, in.shift, zero);
@@ -355,9 +372,9 @@ __global__ __launch_bounds__(NT, CH <= (sizeof(E) == 2 ? 8 : 4) ? 8 : 4) void di
   // the logarithms come last: in binary64 they take registers that the held row
   // leaves only now
   if (tid == 0) {
-    const double base = static_cast<double>(m) * p.inv_tau;
+    const double base = static_cast<double>(m2) * 0.6931471805599453;
     const double lse = base + log(total);
-    double loss = t.cross + t.mass * lse;
+    double loss = t.sums[1] + t.sums[0] * lse;
     if (mass > 0.0) loss += mass * (log(mass) - (base + log(outside)) + lse);
     p.loss[n] = live ? static_cast<float>(loss * p.tau * p.tau * static_cast<double>(w)) : 0.f;
     p.stats[2 * n] = static_cast<float>(lse);
@@ -370,13 +387,10 @@ template <typename E, int NT>
 __global__ __launch_bounds__(NT) void distill_bwd_kernel(const DistillParams p) {
   constexpr int kN = Chunk<E>::kN;
   extern __shared__ __align__(16) char smem[];
-  double* scratch = reinterpret_cast<double*>(smem);
-  Teacher t;
-  t.p = reinterpret_cast<float*>(scratch + NT / 64);
-  t.z = t.p + p.K;
-  t.idx = reinterpret_cast<int*>(t.z + p.K);
+  const DistillShared<NT> sh(smem, p.K);
+  const Teacher& t = sh.t;
 
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63;
   const int64_t n = blockIdx.y;
   const Row<E> in(p.z, n * p.z_stride, p.V), out(p.dz, n * p.dz_stride, p.V);
   const int c0 = blockIdx.x * p.seg, c1 = min(c0 + p.seg, in.chunks());
@@ -386,32 +400,40 @@ __global__ __launch_bounds__(NT) void distill_bwd_kernel(const DistillParams p) 
   // (only this piece's logits are read: in place, others may be gradients already)
   const int64_t from = max(static_cast<int64_t>(c0) * kN - in.shift, int64_t(0));
   const int64_t to = static_cast<int64_t>(c1) * kN - in.shift;
-  if (w != 0.f) load_teacher<E, NT>(p, n, in.p, from, to, scratch, t);
-  if (w == 0.f || (!t.any && !p.tail)) {
-    const float zero[kN] = {};
-    for (int c = c0 + tid; c < c1; c += NT) out.store(c, in.shift, zero);
-    return;
-  }
+  if (tid >= NT - 64 && w != 0.f) load_teacher<E>(p, n, in.p, from, to, lane, t);
   const float lse = p.stats[2 * n];
   const float scale = static_cast<float>(p.grad_scale * p.tau * static_cast<double>(w));
   const float other = p.stats[2 * n + 1] * scale;
-  for (int c = c0 + tid; c < c1; c += NT) {
-    const Chunk<E> x = in.load(c);
-    float y[kN];
+  // without a tail a row may have no entry; in place, the entries' logits come first
+  if (w != 0.f && (!p.tail || p.z == p.dz)) __syncthreads();
+  const bool live = w != 0.f && (p.tail || t.sums[2] != 0.0);
+  constexpr int kAtOnce = 4;                           // loads under way, a thread
+  for (int cc = c0 + tid; cc < c1; cc += kAtOnce * NT) {
+    Chunk<E> x[kAtOnce];
 #pragma unroll
-    for (int e = 0; e < kN; ++e) y[e] = other * prob(x.get(e), inv_tau, lse);
-    out.store(c, in.shift, y);
+    for (int k = 0; k < kAtOnce; ++k) {
+      x[k].fill_lowest();
+      if (live && cc + k * NT < c1) x[k] = in.load(cc + k * NT);
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      float y[kN];
+#pragma unroll
+      for (int e = 0; e < kN; ++e) y[e] = live ? other * prob(x[k].get(e), inv_tau, lse) : 0.f;
+      if (cc + k * NT < c1) out.store(cc + k * NT, in.shift, y);
+    }
   }
-  store_entries<E, NT>(p, out, t, scale, from, to,
-                       [&](float z) { return prob(z, inv_tau, lse); });
+  if (live)
+    store_entries<E, NT>(p, out, t, scale, from, to,
+                         [&](float z) { return prob(z, inv_tau, lse); });
 }
 
 namespace {
 
 template <typename E, int NT, int CH>
 hipError_t run_fwd(const DistillParams& p, hipStream_t s) {
-  size_t lds = NT / 64 * sizeof(double) + 12 * static_cast<size_t>(p.K);
-  if (p.tail) lds += ((p.V + Chunk<E>::kN) / 32 + 1) * 4;
+  const size_t lds =
+      DistillShared<NT>::bytes(p.K, p.tail ? bit_words(p.V, Chunk<E>::kN) : 0);
   const auto fn = distill_fwd_kernel<E, NT, CH>;
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
                                            hipFuncAttributeMaxDynamicSharedMemorySize,
@@ -438,7 +460,7 @@ hipError_t run_bwd(DistillParams p, hipStream_t s) {
   constexpr int NT = 256;
   const int chunks = static_cast<int>((p.V + Chunk<E>::kN - 1) / Chunk<E>::kN + 1);
   p.seg = NT * 16;
-  const size_t lds = NT / 64 * sizeof(double) + 12 * static_cast<size_t>(p.K);
+  const size_t lds = DistillShared<NT>::bytes(p.K, 0);
   for (int64_t n0 = 0; n0 < p.N; n0 += 65535) {
     DistillParams q = p;
     const int64_t rows = p.N - n0 < 65535 ? p.N - n0 : 65535;
