@@ -32,7 +32,7 @@ struct NormParams {
   int64_t T;
   int D, rot, interleaved;
   float eps;
-  float* part;  // backward: [groups][2][D]
+  float* part;  // backward: [2][groups][D]
 };
 
 template <typename E>
@@ -79,25 +79,48 @@ struct Vec8<float> {
   }
 };
 
+// The value of the lane half a group of G away.
+template <int G>
+__device__ __forceinline__ float across(float x) {
+  const uint32_t v = __float_as_uint(x);
+  if constexpr (G == 4) return __uint_as_float(dpp_move<0x4E>(v));                     // 2 3 0 1
+  if constexpr (G == 8) return __uint_as_float(dpp_move<0x1B>(dpp_move<0x141>(v)));    // 8 mirrored, 4 mirrored
+  if constexpr (G == 16) return __uint_as_float(dpp_move<0x128>(v));                   // turned by 8
+  if constexpr (G == 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return __uint_as_float((threadIdx.x & 16) ? r[0] : r[1]);
+  }
+}
+
 // What a lane needs to turn its 8 values: cosines, signed sines (of its own
 // member of each pair), and where the other members are.
+enum class Partner { kInside, kAcross, kLane };  // in the lane; half the group away; lane_step away
 struct Turn {
   float c[8], s[8];
-  int lane_step;     // pairs half a rotation apart: the partner's lane, relative
-  bool interleaved;  // pairs inside the lane
+  int lane_step;
+  Partner partner;
 
   // out = x cos + partner * signed sin, with sign -1 for the way back
-  template <bool BACK>
+  template <bool BACK, int G>
   __device__ __forceinline__ void apply(const float x[8], float y[8], int lane) const {
+    float other[8];
+    if (partner == Partner::kInside) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float other = interleaved ? x[j ^ 1] : __shfl(x[j], lane + lane_step);
-      y[j] = __builtin_fmaf(BACK ? -s[j] : s[j], other, x[j] * c[j]);
+      for (int j = 0; j < 8; ++j) other[j] = x[j ^ 1];
+    } else if (partner == Partner::kAcross) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) other[j] = across<G>(x[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) other[j] = __shfl(x[j], lane + lane_step);
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = __builtin_fmaf(BACK ? -s[j] : s[j], other[j], x[j] * c[j]);
   }
 };
 
 // Sine and cosine of the token's angles, by the wave, then each lane's share.
+template <int G>
 __device__ __forceinline__ void make_turn(const NormParams& p, int64_t t, int lane, int chunk,
                                           float* cs, Turn& turn) {
   const int pairs = p.rot / 2;
@@ -113,7 +136,9 @@ __device__ __forceinline__ void make_turn(const NormParams& p, int64_t t, int la
   }
   __syncthreads();
   const int d0 = 8 * chunk;
-  turn.interleaved = p.interleaved || pairs == 0;
+  turn.partner = p.interleaved || pairs == 0 ? Partner::kInside
+                 : p.rot == 8 * G            ? Partner::kAcross
+                                             : Partner::kLane;
   turn.lane_step = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -159,14 +184,14 @@ __device__ __forceinline__ void load_weight(const void* w, int at, bool active, 
 
 template <typename E, int G>
 __global__ __launch_bounds__(kNormThreads) void norm_fwd_kernel(const NormParams p) {
-  constexpr int kHeads = 64 / G, kU = 2;  // heads at a time, times two in flight
+  constexpr int kHeads = 64 / G, kU = 4;  // heads at a time, times four in flight
   __shared__ float cs[kNormWaves][2 * kMaxPairs];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int chunk = lane % G, sub = lane / G;
   const bool active = 8 * chunk < p.D;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kNormWaves + wave;
   Turn turn;
-  make_turn(p, t, lane, chunk, cs[wave], turn);
+  make_turn<G>(p, t, lane, chunk, cs[wave], turn);
   if (t >= p.T) return;
   const float inv_d = 1.f / static_cast<float>(p.D);
 #pragma unroll
@@ -190,109 +215,114 @@ __global__ __launch_bounds__(kNormThreads) void norm_fwd_kernel(const NormParams
 #pragma unroll
         for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(x[j], x[j], sq);
         sq = sum_row<G>(sq);
-        const float r = 1.f / sqrtf(__builtin_fmaf(sq, inv_d, p.eps));
+        const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(sq, inv_d, p.eps));
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j];
-        turn.apply<false>(x, y, lane);
+        turn.template apply<false, G>(x, y, lane);
         if (h < a.H && active) Vec8<E>::store(a.y, t * a.y_t + h * a.y_h + 8 * chunk, y);
       }
     }
   }
 }
 
+// Queries and keys go to workgroups of their own (blockIdx.y): one weight and one
+// row of its gradient to keep.
 template <typename E, int G>
 __global__ __launch_bounds__(kNormThreads) void norm_bwd_kernel(const NormParams p) {
-  constexpr int kHeads = 64 / G;
+  constexpr int kHeads = 64 / G, kU = 2;
   __shared__ float cs[kNormWaves][2 * kMaxPairs];
-  __shared__ float fold[kNormWaves][2][8 * G];
+  __shared__ float fold[kNormWaves][8 * G];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int chunk = lane % G, sub = lane / G;
   const bool active = 8 * chunk < p.D;
   const float inv_d = 1.f / static_cast<float>(p.D);
-  float w[2][8], dw[2][8];
+  const NormHeads& a = p.t[blockIdx.y];
+  float w[8], dw[8];
+  load_weight<E>(a.w, 8 * chunk, active, w);
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    load_weight<E>(p.t[which].w, 8 * chunk, active, w[which]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dw[which][j] = 0.f;
-  }
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kNormWaves; t0 < p.T;
-       t0 += static_cast<int64_t>(gridDim.x) * kNormWaves) {
+  for (int j = 0; j < 8; ++j) dw[j] = 0.f;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kNormWaves;
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kNormWaves; t0 < p.T && a.H > 0; t0 += step) {
     const int64_t t = t0 + wave;
     Turn turn;
-    make_turn(p, t, lane, chunk, cs[wave], turn);
-    if (t < p.T) {
+    make_turn<G>(p, t, lane, chunk, cs[wave], turn);
+    for (int h0 = 0; h0 < a.H && t < p.T; h0 += kHeads * kU) {
+      Vec8<E> rx[kU], rg[kU];
 #pragma unroll
-      for (int which = 0; which < 2; ++which) {
-        const NormHeads& a = p.t[which];
-        for (int h0 = 0; h0 < a.H; h0 += kHeads) {
-          const int h = h0 + sub;
-          const bool on = h < a.H && active;
-          Vec8<E> rx{}, rg{};
-          if (on) {
-            rx.load(a.x, t * a.x_t + h * a.x_h + 8 * chunk);
-            rg.load(a.dy, t * a.dy_t + h * a.dy_h + 8 * chunk);
-          }
-          float x[8], g[8], u[8], sq = 0.f, ux = 0.f;
-          rx.get(x);
-          rg.get(u);
-          turn.apply<true>(u, g, lane);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            sq = __builtin_fmaf(x[j], x[j], sq);
-            u[j] = g[j] * w[which][j];
-            ux = __builtin_fmaf(u[j], x[j], ux);
-          }
-          sq = sum_row<G>(sq);
-          ux = sum_row<G>(ux);
-          const float r = 1.f / sqrtf(__builtin_fmaf(sq, inv_d, p.eps));
-          const float k = ux * inv_d * r * r;             // mean(u xhat) r
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (on) dw[which][j] = __builtin_fmaf(g[j], x[j] * r, dw[which][j]);
-            u[j] = r * __builtin_fmaf(-k, x[j], u[j]);
-          }
-          if (on) Vec8<E>::store(a.dx, t * a.dx_t + h * a.dx_h + 8 * chunk, u);
+      for (int v = 0; v < kU; ++v) {
+        const int h = h0 + v * kHeads + sub;
+        rx[v] = rg[v] = Vec8<E>{};
+        if (h < a.H && active) {
+          rx[v].load(a.x, t * a.x_t + h * a.x_h + 8 * chunk);
+          rg[v].load(a.dy, t * a.dy_t + h * a.dy_h + 8 * chunk);
         }
+      }
+#pragma unroll
+      for (int v = 0; v < kU; ++v) {
+        const int h = h0 + v * kHeads + sub;
+        const bool on = h < a.H && active;
+        float x[8], g[8], u[8], sq = 0.f, ux = 0.f;
+        rx[v].get(x);
+        rg[v].get(u);
+        turn.template apply<true, G>(u, g, lane);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          sq = __builtin_fmaf(x[j], x[j], sq);
+          u[j] = g[j] * w[j];
+          ux = __builtin_fmaf(u[j], x[j], ux);
+        }
+        sq = sum_row<G>(sq);
+        ux = sum_row<G>(ux);
+        const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(sq, inv_d, p.eps));
+        const float k = ux * inv_d * r * r;               // mean(u xhat) r
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (on) dw[j] = __builtin_fmaf(g[j], x[j] * r, dw[j]);
+          u[j] = r * __builtin_fmaf(-k, x[j], u[j]);
+        }
+        if (on) Vec8<E>::store(a.dx, t * a.dx_t + h * a.dx_h + 8 * chunk, u);
       }
     }
     __syncthreads();                                      // before the next token's angles
   }
   if (p.part == nullptr) return;
 #pragma unroll
-  for (int which = 0; which < 2; ++which)
+  for (int j = 0; j < 8; ++j) {
+    float x = dw[j];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float x = dw[which][j];
-#pragma unroll
-      for (int d = G; d < 64; d <<= 1) x += __shfl_xor(x, d);
-      if (sub == 0) fold[wave][which][8 * chunk + j] = x;
-    }
+    for (int d = G; d < 64; d <<= 1) x += __shfl_xor(x, d);
+    if (sub == 0) fold[wave][8 * chunk + j] = x;
+  }
   __syncthreads();
-  for (int k = threadIdx.x; k < 2 * p.D; k += kNormThreads) {
-    const int which = k >= p.D, d = k - which * p.D;
+  for (int d = threadIdx.x; d < p.D; d += kNormThreads) {
     float x = 0.f;
 #pragma unroll
-    for (int v = 0; v < kNormWaves; ++v) x += fold[v][which][d];
-    p.part[static_cast<int64_t>(blockIdx.x) * 2 * p.D + k] = x;
+    for (int v = 0; v < kNormWaves; ++v) x += fold[v][d];
+    p.part[(static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * p.D + d] = x;
   }
 }
 
-// dw: the workgroups' parts, 8 columns to a workgroup.
+// dw: the workgroups' parts, 8 columns of one weight to a workgroup (blockIdx.y:
+// which), 128 threads to a column.
 template <typename E>
-__global__ __launch_bounds__(256) void norm_fold_kernel(const float* part, int groups, int D,
-                                                        void* dwq, void* dwk) {
-  __shared__ float sum[32][9];
-  const int col = threadIdx.x % 8, r0 = threadIdx.x / 8, k = blockIdx.x * 8 + col;
+__global__ __launch_bounds__(1024) void norm_fold_kernel(const float* part, int groups, int D,
+                                                         void* dwq, void* dwk) {
+  __shared__ float sum[16][8];
+  const int lane = threadIdx.x & 63, col = lane % 8, d = blockIdx.x * 8 + col;
+  part += static_cast<int64_t>(blockIdx.y) * groups * D + d;
   float x = 0.f;
-  for (int r = r0; r < groups; r += 32) x += part[static_cast<int64_t>(r) * 2 * D + k];
-  sum[r0][col] = x;
+#pragma unroll 8
+  for (int r = threadIdx.x / 8; r < groups; r += 128) x += part[static_cast<int64_t>(r) * D];
+#pragma unroll
+  for (int k = 8; k < 64; k <<= 1) x += __shfl_xor(x, k);
+  if (lane < 8) sum[threadIdx.x / 64][col] = x;
   __syncthreads();
-  if (threadIdx.x < 8) {
+  void* out = blockIdx.y == 0 ? dwq : dwk;
+  if (threadIdx.x < 8 && out != nullptr) {
     x = 0.f;
-    for (int r = 0; r < 32; ++r) x += sum[r][col];
-    void* out = k < D ? dwq : dwk;
-    if (out != nullptr) static_cast<E*>(out)[k % D] = static_cast<E>(x);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) x += sum[r][col];
+    static_cast<E*>(out)[d] = static_cast<E>(x);
   }
 }
 
@@ -330,7 +360,7 @@ hipError_t run_norm(const NormParams& p, bool fwd, hipStream_t s) {
     const unsigned grid = static_cast<unsigned>((p.T + kNormWaves - 1) / kNormWaves);
     norm_fwd_kernel<E, G><<<grid, kNormThreads, 0, s>>>(p);
   } else if (p.T > 0) {
-    norm_bwd_kernel<E, G><<<bwd_groups(p.T), kNormThreads, 0, s>>>(p);
+    norm_bwd_kernel<E, G><<<dim3(bwd_groups(p.T), 2), kNormThreads, 0, s>>>(p);
   }
   return hipGetLastError();
 }
@@ -361,11 +391,11 @@ hipError_t launch_qk_norm_rope_bwd(const zero_qk_norm_rope_args& a, hipStream_t 
   const hipError_t e =
       a.dtype == ZERO_BF16 ? pick_norm<bf16>(p, false, s) : pick_norm<float>(p, false, s);
   if (e != hipSuccess || !weights) return e;
-  const unsigned grid = 2 * a.D / 8;
+  const dim3 grid(a.D / 8, 2);
   if (a.dtype == ZERO_BF16)
-    norm_fold_kernel<bf16><<<grid, 256, 0, s>>>(p.part, bwd_groups(a.T), a.D, a.dwq, a.dwk);
+    norm_fold_kernel<bf16><<<grid, 1024, 0, s>>>(p.part, bwd_groups(a.T), a.D, a.dwq, a.dwk);
   else
-    norm_fold_kernel<float><<<grid, 256, 0, s>>>(p.part, bwd_groups(a.T), a.D, a.dwq, a.dwk);
+    norm_fold_kernel<float><<<grid, 1024, 0, s>>>(p.part, bwd_groups(a.T), a.D, a.dwq, a.dwk);
   return hipGetLastError();
 }
 
