@@ -274,6 +274,14 @@ __device__ __forceinline__ void wait_tile() {
   __syncthreads();
 }
 
+// Has the compiler wait for a value's load here: at its first use, in the loop, the
+// wait would be there every turn and for all direct loads under way (a full trip to
+// memory a turn, which the buffers are there to hide).
+template <typename T>
+__device__ __forceinline__ void arrived(T& x) {
+  asm volatile("" : "+v"(x));
+}
+
 // The larger of a value and the other half wave's at the same lane.
 __device__ __forceinline__ float max_halves(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,

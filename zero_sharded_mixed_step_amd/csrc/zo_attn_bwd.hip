@@ -73,40 +73,81 @@ __device__ __forceinline__ uint64_t bits_below(int n) {
 template <int D>
 constexpr bool kDkvAlone = D > 64;
 
-// One tile of 64 queries, do's behind q's, for a wave's 32 keys.
+// One tile of 64 queries, do's behind q's, for a wave's 32 keys: two blocks of 32
+// queries, of 4 D / 16 matrix instructions and 16 scores a lane each.  A wave that has
+// its SIMD for itself overlaps the two by itself: the second block's scores are
+// multiplied while the first's are worked on, and the first's gradients while the
+// second's are.
 template <int D, bool CAP, bool BIAS>
-__device__ __forceinline__ void attn_dkv_tile(const AttnParams& p, const FragAt<D>& qt,
-                                              uint32_t stat,
-                                              const bf16x8 (&kf)[D / 16],
-                                              const bf16x8 (&vf)[D / 16], f32x16 (&dk)[D / 32],
-                                              f32x16 (&dv)[D / 32], int j, int jw, int i0,
-                                              const ScoreFactors& f, const float* bias, int lane) {
-  constexpr int kG = kBuffers<D, kDkvAlone<D>> * kTileBytes<D>;  // from q's tile to do's
-  const int half = lane >> 5;
-  // the lane's places in the tile's words (opaque: one register each, not one a use)
-  uint32_t quads = stat + 16 * half, words = stat + 4 * (lane & 31);
-  asm volatile("" : "+v"(quads), "+v"(words));
-  const auto quad = [&](int array, int at) {   // words at + 4 half .. + 3 of an array
+struct DkvTile {
+  static constexpr bool kOverlap = kDkvAlone<D>;
+  static constexpr int kG = kBuffers<D, kDkvAlone<D>> * kTileBytes<D>;  // from q's tile to do's
+  static constexpr int kC = D / 16, kT = D / 32;
+  const AttnParams& p;
+  const ScoreFactors& f;
+  const float* bias;
+  const bf16x8 (&kf)[kC], (&vf)[kC];
+  f32x16 (&dk)[kT], (&dv)[kT];
+  int j, jw, i0, lane;
+  FragAt<D> qt;
+  uint32_t quads, words;
+
+  struct Block {
+    f32x16 x, dp;                        // the raw scores; do . v
+    bf16x8 pf[2], xf[2];                 // p, dx as operands
+    bf16x8 q[kC], g[kC];                 // rows of q, do
+    bf16x8 qc[2 * kT], gc[2 * kT];       // columns of q, do
+  };
+
+  __device__ __forceinline__ f32x4 quad(int array, int at) const {  // words at + 4 half .. + 3
     return *reinterpret_cast<const ZO_LDS f32x4*>(quads + 4 * (array * kTile + at));
-  };
-  const auto word = [&](int array, int at) {   // word at + l % 32
+  }
+  __device__ __forceinline__ int word(int array, int at) const {    // word at + l % 32
     return *reinterpret_cast<const ZO_LDS int*>(words + 4 * (array * kTile + at));
-  };
+  }
+  __device__ __forceinline__ void rows(Block& k, int s) const {
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {          // 32 queries at a time
-    f32x16 x, dp;
+    for (int c = 0; c < kC; ++c) {
+      k.q[c] = frag_rows<D>(qt, s, c);
+      k.g[c] = frag_rows<D>(qt, s, c, kG);
+    }
+  }
+  __device__ __forceinline__ void cols(Block& k, int s) const {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) x[r] = dp[r] = 0.f;
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) x = mfma(frag_rows<D>(qt, s, c), kf[c], x);
+      for (int t = 0; t < kT; ++t) {
+        k.gc[u * kT + t] = frag_cols<D>(qt, 2 * s + u, t, kG);
+        k.qc[u * kT + t] = frag_cols<D>(qt, 2 * s + u, t);
+      }
+  }
+  __device__ __forceinline__ void multiply(Block& k) const {
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) dp = mfma(frag_rows<D>(qt, s, c, kG), vf[c], dp);
+    for (int r = 0; r < 16; ++r) k.x[r] = k.dp[r] = 0.f;
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+      k.x = mfma(k.q[c], kf[c], k.x);
+      k.dp = mfma(k.g[c], vf[c], k.dp);
+    }
+  }
+  __device__ __forceinline__ void add(const Block& k) const {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int t = 0; t < kT; ++t) {
+        dv[t] = mfma(k.gc[u * kT + t], k.pf[u], dv[t]);
+        dk[t] = mfma(k.qc[u * kT + t], k.xf[u], dk[t]);
+      }
+  }
+  __device__ __forceinline__ bool block_full(int s) const {
+    return __all(word(2, 32 * s) <= jw && word(3, 32 * s) >= jw + 32);
+  }
+  template <bool FULL>
+  __device__ __forceinline__ void scores(Block& k, int s) const {
     const int d0 = jw - (i0 + 32 * s + p.off);         // distances span d0 - 31 .. d0 + 31
     const int side = BIAS ? bias_side(d0 - 31, d0 + 31, p.reach) : 1;
-    const float* row = bias + d0 + (lane & 31) - 4 * half + bias_span(p.reach);
+    const float* row = bias + d0 + (lane & 31) - 4 * (lane >> 5) + bias_span(p.reach);
     const float end = BIAS ? bias[side < 0 ? 0 : 2 * bias_span(p.reach)] : 0.f;
-    const bool full = __all(word(2, 32 * s) <= jw && word(3, 32 * s) >= jw + 32);
-    bf16x8 pf[2], xf[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       float pr[8], dx[8];
@@ -115,7 +156,7 @@ __device__ __forceinline__ void attn_dkv_tile(const AttnParams& p, const FragAt<
         const int at = 32 * s + 16 * u + 8 * g;
         f32x4 base4 = quad(0, at);
         const f32x4 del = quad(1, at);
-        if (!full) {
+        if (!FULL) {
           const f32x4 lo = quad(2, at), hi = quad(3, at);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -123,25 +164,63 @@ __device__ __forceinline__ void attn_dkv_tile(const AttnParams& p, const FragAt<
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int k = 4 * g + e, r = 8 * u + k;
+          const int n = 4 * g + e, r = 8 * u + n;
           float base = base4[e], ds;
           if constexpr (BIAS) base += side != 0 ? end : row[-(16 * u + 8 * g + e)];
-          grad_score<CAP>(x[r], base, dp[r], del[e], f, pr[k], ds, dx[k]);
+          grad_score<CAP>(k.x[r], base, k.dp[r], del[e], f, pr[n], ds, dx[n]);
         }
       }
-      pf[u] = to_frag(pr);
-      xf[u] = to_frag(dx);
-    }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-#pragma unroll
-      for (int t = 0; t < D / 32; ++t) {
-        dv[t] = mfma(frag_cols<D>(qt, 2 * s + u, t, kG), pf[u], dv[t]);
-        dk[t] = mfma(frag_cols<D>(qt, 2 * s + u, t), xf[u], dk[t]);
-      }
+      k.pf[u] = to_frag(pr);
+      k.xf[u] = to_frag(dx);
     }
   }
-}
+  // (FIRST reads, then matrix instructions with what fits beside each)
+  template <int FIRST, int READS>
+  static __device__ __forceinline__ void interleave() {
+    __builtin_amdgcn_sched_group_barrier(0x100, FIRST, 0);
+#pragma unroll
+    for (int n = 0; n < 2 * kC; ++n) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+      __builtin_amdgcn_sched_group_barrier(0x402, 20, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  // Every query of the tile sees all of the wave's keys.
+  __device__ __forceinline__ void full() const {
+    Block a, b;
+    rows(a, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(a);
+    __builtin_amdgcn_sched_barrier(0);
+    rows(b, 1);
+    multiply(b);
+    scores<true>(a, 0);
+    interleave<4, 2>();
+    cols(a, 0);
+    add(a);
+    scores<true>(b, 1);
+    interleave<8, 3>();
+    cols(b, 1);
+    add(b);
+    interleave<8, 2>();
+  }
+  __device__ __forceinline__ void any() const {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      Block a;
+      rows(a, s);
+      multiply(a);
+      if (block_full(s))
+        scores<true>(a, s);
+      else
+        scores<false>(a, s);
+      cols(a, s);
+      add(a);
+    }
+  }
+};
 
 // Which tile of 128 keys a workgroup takes: the most often seen first (see query_tile),
 // by 256 queries spread over the row.
@@ -274,6 +353,11 @@ __global__ __launch_bounds__(kAttnThreads, kDkvAlone<D> ? 1 : 2) void attn_dkv_k
         vf[c] = load8(v + 16 * c + 8 * half);
       }
     }
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      arrived(kf[c]);
+      arrived(vf[c]);
+    }
   }
   f32x16 dk[D / 32], dv[D / 32];
 #pragma unroll
@@ -306,14 +390,21 @@ __global__ __launch_bounds__(kAttnThreads, kDkvAlone<D> ? 1 : 2) void attn_dkv_k
     i0 = i0 + kTile == qb * kTile ? qa * kTile : i0 + kTile;
   };
   const auto seen = [&] { return __any(word(2) < jw + 32 && word(3) > jw) != 0; };
+  const auto full = [&] { return __all(word(2) <= jw && word(3) >= jw + 32) != 0; };
+  using Tile = DkvTile<D, CAP, BIAS>;
+  const auto tile = [&] {
+    // the lane's places in the tile's words (opaque: one register each, not one a use)
+    const uint32_t stat = tiles + kTiles * kTileBytes<D> + buf * kStat;
+    uint32_t quads = stat + 16 * half, words = stat + 4 * (lane & 31);
+    asm volatile("" : "+v"(quads), "+v"(words));
+    return Tile{p, f, bias, kf, vf, dk, dv, j, jw, i0, lane, at.in(tiles + buf * kTileBytes<D>), quads,
+                words};
+  };
   while (n < turns) {
     while (n < turns && !seen()) turn([] {});
-    while (n < turns && seen())
-      turn([&] {
-        attn_dkv_tile<D, CAP, BIAS>(p, at.in(tiles + buf * kTileBytes<D>),
-                                    tiles + kTiles * kTileBytes<D> + buf * kStat, kf, vf, dk, dv,
-                                    j, jw, i0, f, bias, lane);
-      });
+    if constexpr (Tile::kOverlap)
+      while (n < turns && full()) turn([&] { tile().full(); });
+    while (n < turns && seen() && !(Tile::kOverlap && full())) turn([&] { tile().any(); });
   }
 
   if (j >= p.Tk) return;
@@ -565,9 +656,16 @@ __global__ __launch_bounds__(kAttnThreads, (kDqAlone<D, BIAS> ? 1 : 2)) void att
         of[c] = load8(o + 16 * c + 8 * half);
       }
     }
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      arrived(qf[c]);
+      arrived(of[c]);
+    }
   }
   const int64_t row = static_cast<int64_t>(bh) * p.tq64 + min(i, p.tq64 - 1);
-  const float base0 = p.base[row], delta = p.delta[row];
+  float base0 = p.base[row], delta = p.delta[row];
+  arrived(base0);
+  arrived(delta);
   f32x16 dq[D / 32];
 #pragma unroll
   for (int t = 0; t < D / 32; ++t)
