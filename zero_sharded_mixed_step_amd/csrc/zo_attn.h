@@ -26,6 +26,7 @@ namespace zo {
 constexpr int kAttnThreads = 256;
 constexpr int kWaves = 4;
 constexpr int kTile = 64;  // rows of a staged tile
+constexpr int kUnits = 256;  // compute units of the card
 
 // A staged tile is 64 rows of D bf16 without gaps (the direct loads to shared
 // memory write 64 lanes' 16 bytes one after another), and the 16-byte pieces of
@@ -40,6 +41,10 @@ __device__ __forceinline__ constexpr int swizzle(int r) {
 }
 template <int D>
 constexpr int kTileBytes = kTile * D * 2;
+
+// Of a tile of 128 keys: the tiles of 64 queries that see any of it, first and one past
+// the last, and a bit for each key that is seen.
+constexpr int kTileWords = 6;
 
 struct Strides3 {
   int64_t b, t, h;
@@ -64,6 +69,7 @@ struct AttnParams {
   float* base;      // [B][Hq][tq64]  -lse * log2(e), plus cap * log2(e); -inf: no keys
   float* delta;     // [B][Hq][tq64]  do . o
   int *qlo, *qhi;   // [B][tq64]      the keys a query sees; 0, 0 for none
+  int* tile;        // [B][key tiles][kTileWords] of what sees a tile of 128 keys
   float* dpart;     // [B][Hq][query tiles][bias_entries]: ds by distance
   float* dsum;      // [Hq][bias_entries]
   float* kvpart;    // [2][parts][B][Hk][Tk][D]: dk and dv of parts of a group's heads
@@ -199,6 +205,14 @@ __device__ __forceinline__ void lds_load16(uint32_t to, const void* from) {
                : "memory");
 #endif
 }
+__device__ __forceinline__ void lds_load4(uint32_t to, u32x4 buffer, uint32_t lane_offset) {
+#ifdef __HIP_DEVICE_COMPILE__
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(
+                   uniform(to)),
+               "v"(lane_offset), "s"(buffer)
+               : "memory");
+#endif
+}
 __device__ __forceinline__ void lds_load4(uint32_t to, const void* from) {
 #ifdef __HIP_DEVICE_COMPILE__
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, off" ::"s"(uniform(to)), "v"(from)
@@ -206,11 +220,11 @@ __device__ __forceinline__ void lds_load4(uint32_t to, const void* from) {
 #endif
 }
 
-// A descriptor of the memory from `base` on, for 32-bit offsets.
-__device__ __forceinline__ u32x4 buffer_at(const void* base) {
+// A descriptor of the memory from `base` on, for 32-bit offsets; beyond `bytes` reads are 0.
+__device__ __forceinline__ u32x4 buffer_at(const void* base, uint32_t bytes = 0xFFFFFFFFu) {
   const uint64_t a = reinterpret_cast<uint64_t>(base);
   return u32x4{uniform(static_cast<uint32_t>(a)), uniform(static_cast<uint32_t>(a >> 32) & 0xFFFFu),
-               0xFFFFFFFFu, 0x00020000u};
+               uniform(bytes), 0x00020000u};
 }
 
 // Loads of tiles of 64 rows of D columns.  A lane's offsets from a tile's
@@ -239,6 +253,19 @@ struct TileLoad {
       const int r = piece / (D / 8), c = (piece % (D / 8)) ^ swizzle<D>(r);
       off[u] = static_cast<uint32_t>(r) * static_cast<uint32_t>(s) * 2u + c * 16u;
     }
+  }
+
+  // For near rows, without a branch: rows from `last` on become 0, and all of them do
+  // without `on`.
+  __device__ __forceinline__ void start_near(uint32_t tile, int row0, bool on, int wave) const {
+    const int n = max(min(last - row0, kTile), 0);       // (64 rows of 16 MiB stay below 2^30)
+    const uint32_t bytes = ((n - 1) * static_cast<uint32_t>(stride) + D) * 2u *
+                           static_cast<uint32_t>(on & (n > 0));
+    const u32x4 from = buffer_at(base + row0 * stride, bytes);
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u)
+      lds_load16(tile + wave * (kLoads * 1024) + u * 1024, from,
+                 off[u % kOffs], static_cast<uint32_t>((u / kOffs) * 16 * stride));
   }
 
   __device__ __forceinline__ void start(uint32_t tile, int row0, int wave, int lane) const {
@@ -452,11 +479,13 @@ __device__ __forceinline__ int tile_of_rank(int y, int n, int* scratch, int tid,
 constexpr int kMinRanked = 16, kMaxRanked = 255;   // (a few tiles are not worth the ranking)
 
 // The same for a tile of 128 queries: its cost is the span of keys that four of its
-// queries see.  Without ranges, or where all workgroups run at once anyway (two to a
-// compute unit), the last tile first: the order of a causal mask.
-__device__ __forceinline__ int query_tile(const AttnParams& p, int b, int* scratch, int tid) {
+// queries see.  Without ranges, or where all workgroups run `at_once` anyway, the last
+// tile first: the order of a causal mask.
+__device__ __forceinline__ int query_tile(const AttnParams& p, int b, int* scratch, int tid,
+                                          int at_once) {
   const int n = gridDim.y, y = blockIdx.y;
-  if (!p.ranges || n < kMinRanked || n > kMaxRanked || gridDim.x * n <= 512) return n - 1 - y;
+  if (!p.ranges || n < kMinRanked || n > kMaxRanked || static_cast<int>(gridDim.x) * n <= at_once)
+    return n - 1 - y;
   return tile_of_rank(y, n, scratch, tid, [&](int t) {
     int lo = 0x7FFFFFFF, hi = 0;
 #pragma unroll

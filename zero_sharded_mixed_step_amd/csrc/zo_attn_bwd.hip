@@ -9,13 +9,72 @@
 #include "zo_attn.h"
 #include "zo_internal.h"
 
+#include <type_traits>
+
 namespace zo {
 
-// 64 queries of one (batch, head): 4 threads to a row.
-__global__ __launch_bounds__(256) void attn_bwd_prepare_kernel(const AttnParams p, int D) {
+// The bits 0 .. n - 1 (n from below 0 to above 64).
+__device__ __forceinline__ uint64_t bits_below(int n) {
+  return n <= 0 ? 0 : n >= 64 ? ~uint64_t(0) : (uint64_t(1) << n) - 1;
+}
+
+// What sees a tile of 128 keys (p.tile), by a workgroup.
+__device__ __forceinline__ void key_tile_words(const AttnParams& p, int b, int t, int tid) {
+  __shared__ int words[kWaves][kTileWords];
+  const int j0 = 128 * t, wave = tid >> 6;
+  int qa = 0x7FFFFFFF, qb = 0;
+  uint64_t seen_lo = 0, seen_hi = 0;
+  for (int i0 = tid; i0 < p.Tq; i0 += 8 * kAttnThreads) {  // 8 loads under way at a time
+    int2 r[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r[k] = key_range(p, b, i0 + k * kAttnThreads);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int lo = max(r[k].x - j0, 0), hi = min(r[k].y - j0, 128);
+      if (lo < hi) {
+        const int t = (i0 + k * kAttnThreads) / kTile;
+        qa = min(qa, t);
+        qb = max(qb, t + 1);
+        seen_lo |= bits_below(hi) & ~bits_below(lo);
+        seen_hi |= bits_below(hi - 64) & ~bits_below(lo - 64);
+      }
+    }
+  }
+  const uint32_t mine[4] = {static_cast<uint32_t>(seen_lo), static_cast<uint32_t>(seen_lo >> 32),
+                            static_cast<uint32_t>(seen_hi), static_cast<uint32_t>(seen_hi >> 32)};
+  qa = join_lanes<64>(qa, MinOp());
+  qb = join_lanes<64>(qb, MaxOp());
+  uint32_t all[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) all[w] = join_lanes<64>(mine[w], OrOp());
+  if ((tid & 63) == 0) {
+    words[wave][0] = qa;
+    words[wave][1] = qb;
+    for (int w = 0; w < 4; ++w) words[wave][2 + w] = all[w];
+  }
+  __syncthreads();
+  if (tid < kTileWords) {
+    int x = words[0][tid];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) {
+      const int y = words[w][tid];
+      x = tid == 0 ? min(x, y) : tid == 1 ? max(x, y) : x | y;
+    }
+    p.tile[(static_cast<int64_t>(b) * ((p.Tk + 127) / 128) + t) * kTileWords + tid] = x;
+  }
+}
+
+// 64 queries of one (batch, head): 4 threads to a row.  The workgroups before those of
+// the queries, `before` a head, take tiles of 128 keys, the heads of a batch row in turn.
+__global__ __launch_bounds__(256) void attn_bwd_prepare_kernel(const AttnParams p, int D, int before) {
   const int bh = blockIdx.x, b = bh / p.Hq, h = bh % p.Hq;
   const int tid = threadIdx.x, sub = tid & 3;
-  const int i = blockIdx.y * 64 + (tid >> 2);
+  if (static_cast<int>(blockIdx.y) < before) {
+    const int t = blockIdx.y * p.Hq + h;
+    if (128 * t < p.Tk) key_tile_words(p, b, t, tid);
+    return;
+  }
+  const int i = (blockIdx.y - before) * 64 + (tid >> 2);
   float sum = 0.f;
   const int2 r = key_range(p, b, i);
   if (r.y > r.x) {
@@ -62,11 +121,6 @@ __device__ __forceinline__ void grad_score(float x, float base, float dp, float 
 }
 
 // ---------------------------------------------------------------- dk, dv ---
-
-// The bits 0 .. n - 1 (n from below 0 to above 64).
-__device__ __forceinline__ uint64_t bits_below(int n) {
-  return n <= 0 ? 0 : n >= 64 ? ~uint64_t(0) : (uint64_t(1) << n) - 1;
-}
 
 // The registers of one wave a SIMD for 96 columns and more: k, v, dk and dv alone take
 // 144 or 192 of the 256 that two waves leave each.
@@ -159,8 +213,10 @@ struct DkvTile {
         if (!FULL) {
           const f32x4 lo = quad(2, at), hi = quad(3, at);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (j < __float_as_int(lo[e]) || j >= __float_as_int(hi[e])) base4[e] = -kInf;  // p = 0
+          for (int e = 0; e < 4; ++e) {
+            const bool out = (j < __float_as_int(lo[e])) | (j >= __float_as_int(hi[e]));
+            base4[e] = out ? -kInf : base4[e];         // p = 0
+          }
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -175,36 +231,52 @@ struct DkvTile {
     }
   }
   // (FIRST reads, then matrix instructions with what fits beside each)
-  template <int FIRST, int READS>
+  template <int FIRST, int READS, int BESIDE>
   static __device__ __forceinline__ void interleave() {
     __builtin_amdgcn_sched_group_barrier(0x100, FIRST, 0);
 #pragma unroll
     for (int n = 0; n < 2 * kC; ++n) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
       __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
-      __builtin_amdgcn_sched_group_barrier(0x402, 20, 0);
+      __builtin_amdgcn_sched_group_barrier(0x402, BESIDE, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
   }
 
-  // Every query of the tile sees all of the wave's keys.
-  __device__ __forceinline__ void full() const {
+  // Holds the operands' making where it stands: it would be moved down to their use.
+  static __device__ __forceinline__ void here(Block& k) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      arrived(k.pf[u]);
+      arrived(k.xf[u]);
+    }
+  }
+  // FULL: every query of the tile sees all of the wave's keys.  The next tile is staged
+  // in three places.
+  template <bool FULL, typename S0, typename S1, typename S2>
+  __device__ __forceinline__ void overlapped(S0 stage0, S1 stage1, S2 stage2) const {
     Block a, b;
     rows(a, 0);
     __builtin_amdgcn_sched_barrier(0);
+    stage0();
     multiply(a);
     __builtin_amdgcn_sched_barrier(0);
     rows(b, 1);
     multiply(b);
-    scores<true>(a, 0);
-    interleave<4, 2>();
+    scores<FULL>(a, 0);
+    here(a);
+    if (!FULL) arrived(b.x), arrived(b.dp);
+    interleave<FULL ? 4 : 8, FULL ? 2 : 3, FULL ? 20 : 26>();
+    stage1();
     cols(a, 0);
     add(a);
-    scores<true>(b, 1);
-    interleave<8, 3>();
+    scores<FULL>(b, 1);
+    here(b);
+    interleave<FULL ? 8 : 16, FULL ? 3 : 4, FULL ? 20 : 26>();
+    stage2();
     cols(b, 1);
     add(b);
-    interleave<8, 2>();
+    interleave<8, 2, 20>();
   }
   __device__ __forceinline__ void any() const {
 #pragma unroll
@@ -222,21 +294,15 @@ struct DkvTile {
   }
 };
 
-// Which tile of 128 keys a workgroup takes: the most often seen first (see query_tile),
-// by 256 queries spread over the row.
-__device__ __forceinline__ int key_tile(const AttnParams& p, int b, int* scratch, int tid) {
+// Which tile of 128 keys a workgroup takes: the most often seen first (see query_tile).
+__device__ __forceinline__ int key_tile(const AttnParams& p, int b, int* scratch, int tid, int at_once) {
   const int n = gridDim.y, y = blockIdx.y;
-  if (!p.ranges || n < kMinRanked || n > kMaxRanked || gridDim.x * n <= 512) return y;
-  int* part = scratch + kMaxRanked + 1;                // [kWaves][n]
-  const int64_t i = static_cast<int64_t>(b) * p.tq64 + static_cast<int64_t>(tid) * p.Tq / 256;
-  const int lo = p.qlo[i], hi = p.qhi[i];
-  for (int t = 0; t < n; ++t) {
-    const int seen = __popcll(__ballot(lo < 128 * t + 128 && hi > 128 * t));
-    if ((tid & 63) == 0) part[(tid >> 6) * n + t] = seen;
-  }
-  __syncthreads();
+  if (!p.ranges || p.Tq == 0 || n < kMinRanked || n > kMaxRanked ||
+      static_cast<int>(gridDim.x) * n <= at_once)
+    return y;
   return tile_of_rank(y, n, scratch, tid, [&](int t) {
-    return part[t] + part[n + t] + part[2 * n + t] + part[3 * n + t];
+    const int* words = p.tile + (static_cast<int64_t>(b) * n + t) * kTileWords;
+    return max(words[1] - words[0], 0);
   });
 }
 
@@ -250,9 +316,7 @@ __global__ __launch_bounds__(kAttnThreads, kDkvAlone<D> ? 1 : 2) void attn_dkv_k
   extern __shared__ __align__(1024) char smem[];       // [kBufs] tiles of q, of do
   const uint32_t tiles = lds_address(smem);
   char* stats = smem + kTiles * kTileBytes<D>;         // [kBufs] kStat
-  int* span = reinterpret_cast<int*>(stats + kBufs * kStat);             // [kWaves][2]
-  uint32_t* seen_by = reinterpret_cast<uint32_t*>(span + 2 * kWaves);       // [kWaves][4]
-  float* bias = reinterpret_cast<float*>(seen_by + 4 * kWaves);
+  float* bias = reinterpret_cast<float*>(stats + kBufs * kStat);
 
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -260,7 +324,8 @@ __global__ __launch_bounds__(kAttnThreads, kDkvAlone<D> ? 1 : 2) void attn_dkv_k
   const int part = bx % p.parts, bk = bx / p.parts, b = bk / p.Hk, hk = bk % p.Hk;
   BiasStage bs;                                        // (a bias goes with one head a workgroup)
   if constexpr (BIAS) bs.buckets(p, tid);
-  const int j0 = key_tile(p, b, reinterpret_cast<int*>(smem), tid) * 128;   // its first key
+  const int j0 = key_tile(p, b, reinterpret_cast<int*>(smem), tid,
+                          kDkvAlone<D> ? kUnits : 2 * kUnits) * 128;   // its first key
   const int jw = j0 + wave * 32, j = jw + (lane & 31);
   const int* qlo = p.qlo + static_cast<int64_t>(b) * p.tq64;
   const int* qhi = p.qhi + static_cast<int64_t>(b) * p.tq64;
@@ -269,70 +334,39 @@ __global__ __launch_bounds__(kAttnThreads, kDkvAlone<D> ? 1 : 2) void attn_dkv_k
   const int heads = p.group / p.parts, h0 = hk * p.group + part * heads;
 
   if constexpr (BIAS) bs.values(p, h0);
-  // the tiles of queries that see any of the keys lie in [qa, qb); and the keys seen
-  int qa = 0x7FFFFFFF, qb = 0;
-  uint64_t seen_lo = 0, seen_hi = 0;
-  for (int i0 = tid; i0 < p.tq64; i0 += 4 * kAttnThreads) {
-    int lo[4], hi[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = i0 + k * kAttnThreads;
-      lo[k] = i < p.tq64 ? max(qlo[i] - j0, 0) : 0;
-      hi[k] = i < p.tq64 ? min(qhi[i] - j0, 128) : 0;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (lo[k] < hi[k]) {
-        const int t = (i0 + k * kAttnThreads) / kTile;
-        qa = min(qa, t);
-        qb = max(qb, t + 1);
-        seen_lo |= bits_below(hi[k]) & ~bits_below(lo[k]);
-        seen_hi |= bits_below(hi[k] - 64) & ~bits_below(lo[k] - 64);
-      }
+  const int* words = p.tile + (static_cast<int64_t>(b) * gridDim.y + j0 / 128) * kTileWords;
+  int qa = 0, qb = 0;
+  uint32_t wave_sees = 0;
+  if (p.Tq > 0) {                                      // (without queries there is no workspace)
+    qb = uniform(words[1]);
+    qa = uniform(min(words[0], qb));
+    wave_sees = uniform(words[2 + wave]);
   }
-  qa = join_lanes<64>(qa, MinOp());
-  qb = join_lanes<64>(qb, MaxOp());
-  if (lane == 0) {
-    span[2 * wave] = qa;
-    span[2 * wave + 1] = qb;
-  }
-  const uint32_t mine[4] = {static_cast<uint32_t>(seen_lo), static_cast<uint32_t>(seen_lo >> 32),
-                            static_cast<uint32_t>(seen_hi), static_cast<uint32_t>(seen_hi >> 32)};
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const uint32_t x = join_lanes<64>(mine[w], OrOp());
-    if (lane == 0) seen_by[4 * wave + w] = x;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    qa = min(qa, span[2 * w]);
-    qb = max(qb, span[2 * w + 1]);
-  }
-  qb = __builtin_amdgcn_readfirstlane(qb);
-  qa = __builtin_amdgcn_readfirstlane(min(qa, qb));
   const int turns = (qb - qa) * heads;
 
   TileLoad<D> ql(p.q + b * p.qs.b + h0 * p.qs.h, p.qs.t, 0, p.Tq, wave, lane);
   TileLoad<D> ol(p.d_o + b * p.dos.b + h0 * p.dos.h, p.dos.t, 0, p.Tq, wave, lane);
-  int head = 0, qi = qa;                               // of the next tile to stage
+  int qi = qa;                                         // the next tile to stage
+  // of the tile's words a wave loads an array of its own
+  const int64_t first_head = (static_cast<int64_t>(b) * p.Hq + h0) * p.tq64;
+  const uint32_t* words_at = wave == 0   ? reinterpret_cast<const uint32_t*>(p.base + first_head)
+                             : wave == 1 ? reinterpret_cast<const uint32_t*>(p.delta + first_head)
+                             : wave == 2 ? reinterpret_cast<const uint32_t*>(qlo)
+                                         : reinterpret_cast<const uint32_t*>(qhi);
+  const int words_step = wave < 2 ? p.tq64 : 0;
+  const auto stage_words = [&](int buf, bool on) {
+    lds_load4(tiles + kTiles * kTileBytes<D> + buf * kStat + wave * kTile * 4,
+              buffer_at(words_at + qi * kTile, static_cast<uint32_t>(on) * kTile * 4), lane * 4);
+    const bool end = qi + 1 == qb;
+    qi = end ? qa : qi + 1;
+    words_at += end ? words_step : 0;
+    ql.base += end ? p.qs.h : 0;
+    ol.base += end ? p.dos.h : 0;
+  };
   const auto stage = [&](int buf) {
-    const int64_t bh = static_cast<int64_t>(b) * p.Hq + h0 + head;
     ql.start(tiles + buf * kTileBytes<D>, qi * kTile, wave, lane);
     ol.start(tiles + (kBufs + buf) * kTileBytes<D>, qi * kTile, wave, lane);
-    const uint32_t to = tiles + kTiles * kTileBytes<D> + buf * kStat + wave * kTile * 4;
-    const int i0 = qi * kTile;
-    const void* from = wave == 0   ? static_cast<const void*>(p.base + bh * p.tq64 + i0)
-                       : wave == 1 ? static_cast<const void*>(p.delta + bh * p.tq64 + i0)
-                       : wave == 2 ? static_cast<const void*>(qlo + i0)
-                                   : static_cast<const void*>(qhi + i0);
-    lds_load4(to, static_cast<const uint32_t*>(from) + lane);
-    if (++qi == qb) {
-      qi = qa;
-      ++head;
-      ql.base += p.qs.h;
-      ol.base += p.dos.h;
-    }
+    stage_words(buf, true);
   };
 #pragma unroll
   for (int k = 0; k < kBufs - 1; ++k)
@@ -343,8 +377,7 @@ __global__ __launch_bounds__(kAttnThreads, kDkvAlone<D> ? 1 : 2) void attn_dkv_k
     const bf16* k = p.k + b * p.ks.b + jj * p.ks.t + hk * p.ks.h;
     const bf16* v = p.v + b * p.vs.b + jj * p.vs.t + hk * p.vs.h;
     // (a key that no query sees may hold anything)
-    const uint32_t any = seen_by[wave] | seen_by[4 + wave] | seen_by[8 + wave] | seen_by[12 + wave];
-    const bool seen = (any >> (lane & 31)) & 1;
+    const bool seen = (wave_sees >> (lane & 31)) & 1;
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) {
       kf[c] = vf[c] = bf16x8{};
@@ -370,9 +403,12 @@ __global__ __launch_bounds__(kAttnThreads, kDkvAlone<D> ? 1 : 2) void attn_dkv_k
   int n = 0, buf = 0, i0 = qa * kTile;                 // of the tile at hand
   const auto stat_of = [&] { return reinterpret_cast<const float*>(stats + buf * kStat); };
   const auto word = [&](int k) { return reinterpret_cast<const int*>(stat_of())[k * kTile + lane]; };
-  const auto turn = [&](auto work) {
+  // (A tile's loads, issued in one go by four waves, hold each of them up for most of
+  // the 500 cycles that the 32 KiB of 128 columns take to pass: `work` that issues them
+  // by itself does so in three places.)
+  const auto turn = [&](auto work, bool by_itself = false) {
     const bool more = n + kBufs - 1 < turns;
-    if (more) stage((buf + kBufs - 1) % kBufs);
+    if (more && !by_itself) stage((buf + kBufs - 1) % kBufs);
     // a query that sees nothing (padding) may hold anything: cleared, since a weight of 0
     // does not stop a NaN
     const uint64_t seeing = __ballot(word(3) > word(2));
@@ -400,11 +436,24 @@ __global__ __launch_bounds__(kAttnThreads, kDkvAlone<D> ? 1 : 2) void attn_dkv_k
     return Tile{p, f, bias, kf, vf, dk, dv, j, jw, i0, lane, at.in(tiles + buf * kTileBytes<D>), quads,
                 words};
   };
+  const bool near = ql.near && ol.near;
+  const auto overlapped = [&](auto is_full) {
+    return [&, is_full] {
+      const bool more = n + kBufs - 1 < turns;
+      const int to = (buf + kBufs - 1) % kBufs;
+      tile().template overlapped<decltype(is_full)::value>(
+          [&] { ql.start_near(tiles + to * kTileBytes<D>, qi * kTile, more, wave); },
+          [&] { ol.start_near(tiles + (kBufs + to) * kTileBytes<D>, qi * kTile, more, wave); },
+          [&] { stage_words(to, more); });
+    };
+  };
   while (n < turns) {
     while (n < turns && !seen()) turn([] {});
-    if constexpr (Tile::kOverlap)
-      while (n < turns && full()) turn([&] { tile().full(); });
-    while (n < turns && seen() && !(Tile::kOverlap && full())) turn([&] { tile().any(); });
+    if constexpr (Tile::kOverlap) {
+      while (n < turns && near && full()) turn(overlapped(std::true_type()), true);
+      while (n < turns && near && seen() && !full()) turn(overlapped(std::false_type()), true);
+    }
+    while (n < turns && !(Tile::kOverlap && near) && seen()) turn([&] { tile().any(); });
   }
 
   if (j >= p.Tk) return;
@@ -602,7 +651,7 @@ __global__ __launch_bounds__(kAttnThreads, (kDqAlone<D, BIAS> ? 1 : 2)) void att
   const int hk = h / p.group;
   BiasStage bs;
   if constexpr (BIAS) bs.buckets(p, tid);
-  const int tile = query_tile(p, b, reinterpret_cast<int*>(ranges), tid);
+  const int tile = query_tile(p, b, reinterpret_cast<int*>(ranges), tid, kDqAlone<D, BIAS> ? kUnits : 2 * kUnits);
   const int i0 = tile * 128 + wave * 32;
   const int i = i0 + (lane & 31);
   const ScoreFactors f(p, CAP);
@@ -831,7 +880,7 @@ hipError_t run_bwd(const AttnParams& p, hipStream_t s) {
   hipError_t e = hipSuccess;
   if (p.B > 0 && p.Tk > 0) {
     e = launch_lds(attn_dkv_kernel<D, CAP, BIAS>, dim3(p.B * p.Hk * p.parts, (p.Tk + 127) / 128),
-                   dkv_bufs * (2 * kTileBytes<D> + 4 * kTile * 4) + 2 * kWaves * 4 + 16 * kWaves + n * 4, p, s);
+                   dkv_bufs * (2 * kTileBytes<D> + 4 * kTile * 4) + n * 4, p, s);
     if (e != hipSuccess) return e;
     if (p.parts > 1) {
       const int64_t pieces = static_cast<int64_t>(p.B) * p.Hk * p.Tk * D / 8;
@@ -876,6 +925,8 @@ size_t lay_out(AttnParams& p, int D, size_t entries, char* base) {
   p.delta = reinterpret_cast<float*>(take(rows * p.Hq * 4));
   p.qlo = reinterpret_cast<int*>(take(rows * 4));
   p.qhi = reinterpret_cast<int*>(take(rows * 4));
+  p.tile = reinterpret_cast<int*>(
+      take(p.Tq > 0 ? static_cast<size_t>(p.B) * ((p.Tk + 127) / 128) * kTileWords * sizeof(int) : 0));
   p.dpart = reinterpret_cast<float*>(
       take(static_cast<size_t>(p.B) * p.Hq * ((p.Tq + 127) / 128) * entries * 4));
   p.dsum = reinterpret_cast<float*>(take(p.Hq * entries * 4));
@@ -904,7 +955,9 @@ hipError_t launch_attn_bwd(const zero_attn_args& a, hipStream_t s) {
   p.parts = choose_parts(a.B, a.Tk, a.Hq, a.Hk, a.bias_table != nullptr);
   lay_out(p, a.D, a.bias_table ? bias_entries(p.reach) : 0, static_cast<char*>(a.workspace));
   if (a.B > 0 && a.Tq > 0) {
-    attn_bwd_prepare_kernel<<<dim3(a.B * a.Hq, p.tq64 / 64), 256, 0, s>>>(p, a.D);
+    const int before = ((a.Tk + 127) / 128 + a.Hq - 1) / a.Hq;
+    attn_bwd_prepare_kernel<<<dim3(a.B * a.Hq, p.tq64 / 64 + before), 256, 0, s>>>(p, a.D,
+                                                                                        before);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
