@@ -109,9 +109,12 @@ size_t zero_qk_norm_rope_workspace_bytes(int64_t T, int D);
  *   ranges[b][i] = {lo, hi} if given (clipped to [0, Tk]; lo >= hi: no key),
  *   else [0, i + 1 + off) if causal, else [0, Tk).
  *   o_i = sum_j softmax_j(s) v_j,   lse_i = log sum_j exp(s_ij).
- * A query that sees no key gives o = 0, lse = -inf and takes no part in any
- * gradient.  Keys that no query sees, whatever they hold, change nothing but
- * where a tile of keys that holds them is needed by others (see below).
+ * A query that sees no key gives o = 0, lse = -inf and gradients of 0, and takes
+ * no part in any other; a key that no query sees has gradients of 0.  Both may hold
+ * anything, NaN and infinities too: they are read as 0.  Masked scores are selected
+ * away, not multiplied.  What a key holds that some query sees counts for the
+ * queries near it, as in the formula with a weight of 0: a NaN in it may reach any
+ * query whose tile (128 queries) needs the key.
  *
  * Backward, from the forward's o and lse:
  *   p = exp(s - lse), dp_ij = do_i . v_j, ds = p (dp - do_i . o_i),
@@ -122,9 +125,7 @@ size_t zero_qk_norm_rope_workspace_bytes(int64_t T, int D);
  *
  * q, k, v, o and their gradients are bf16; p and dx are rounded to bf16 for
  * the matrix products (their sums stay binary32).  D is 32, 64, 96 or 128;
- * Hq is a multiple of Hk.  Masked keys inside a visible tile get the weight
- * 0, by selection for p; their v is multiplied by it, so a NaN or infinity in
- * the v of a masked key of such a tile is cleared first.
+ * Hq is a multiple of Hk.
  * Bases and strides are multiples of 16 bytes.
  *
  * bias_buckets has 2 * reach + 1 entries (entries outside [0, n_buckets) are
