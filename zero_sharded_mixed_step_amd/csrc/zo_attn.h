@@ -457,6 +457,15 @@ __device__ __forceinline__ uint64_t seen_keys(const int2* ranges, int k0, uint32
   return flags[0] | static_cast<uint64_t>(flags[1]) << 32;
 }
 
+// A workgroup's place in its kernel's grid, or in its part of a grid that two share.
+struct Place {
+  int x, y, nx, ny;
+};
+__device__ __forceinline__ Place place() {
+  return {static_cast<int>(blockIdx.x), static_cast<int>(blockIdx.y), static_cast<int>(gridDim.x),
+          static_cast<int>(gridDim.y)};
+}
+
 // Which tile the workgroup at place y of its batch row's launch order takes:
 // the one of rank y by decreasing cost (ties by index), so that the longest start first
 // and the last to start are short; documents give a tile's cost no order that its index
@@ -481,11 +490,10 @@ constexpr int kMinRanked = 16, kMaxRanked = 255;   // (a few tiles are not worth
 // The same for a tile of 128 queries: its cost is the span of keys that four of its
 // queries see.  Without ranges, or where all workgroups run `at_once` anyway, the last
 // tile first: the order of a causal mask.
-__device__ __forceinline__ int query_tile(const AttnParams& p, int b, int* scratch, int tid,
-                                          int at_once) {
-  const int n = gridDim.y, y = blockIdx.y;
-  if (!p.ranges || n < kMinRanked || n > kMaxRanked || static_cast<int>(gridDim.x) * n <= at_once)
-    return n - 1 - y;
+__device__ __forceinline__ int query_tile(const AttnParams& p, const Place& w, int b, int* scratch,
+                                          int tid, int at_once) {
+  const int n = w.ny, y = w.y;
+  if (!p.ranges || n < kMinRanked || n > kMaxRanked || w.nx * n <= at_once) return n - 1 - y;
   return tile_of_rank(y, n, scratch, tid, [&](int t) {
     int lo = 0x7FFFFFFF, hi = 0;
 #pragma unroll

@@ -214,7 +214,8 @@ struct DkvTile {
           const f32x4 lo = quad(2, at), hi = quad(3, at);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const bool out = (j < __float_as_int(lo[e])) | (j >= __float_as_int(hi[e]));
+            const int out = static_cast<int>(j < __float_as_int(lo[e])) |
+                            static_cast<int>(j >= __float_as_int(hi[e]));
             base4[e] = out ? -kInf : base4[e];         // p = 0
           }
         }
@@ -295,11 +296,10 @@ struct DkvTile {
 };
 
 // Which tile of 128 keys a workgroup takes: the most often seen first (see query_tile).
-__device__ __forceinline__ int key_tile(const AttnParams& p, int b, int* scratch, int tid, int at_once) {
-  const int n = gridDim.y, y = blockIdx.y;
-  if (!p.ranges || p.Tq == 0 || n < kMinRanked || n > kMaxRanked ||
-      static_cast<int>(gridDim.x) * n <= at_once)
-    return y;
+__device__ __forceinline__ int key_tile(const AttnParams& p, const Place& w, int b, int* scratch,
+                                        int tid, int at_once) {
+  const int n = w.ny, y = w.y;
+  if (!p.ranges || p.Tq == 0 || n < kMinRanked || n > kMaxRanked || w.nx * n <= at_once) return y;
   return tile_of_rank(y, n, scratch, tid, [&](int t) {
     const int* words = p.tile + (static_cast<int64_t>(b) * n + t) * kTileWords;
     return max(words[1] - words[0], 0);
@@ -309,22 +309,22 @@ __device__ __forceinline__ int key_tile(const AttnParams& p, int b, int* scratch
 // A workgroup owns 128 keys of one key head, 32 to a wave, and walks tiles of
 // 64 queries of the query heads that share it, or of a part of them.
 template <int D, bool CAP, bool BIAS>
-__global__ __launch_bounds__(kAttnThreads, kDkvAlone<D> ? 1 : 2) void attn_dkv_kernel(const AttnParams p) {
+__device__ __forceinline__ void attn_dkv(const AttnParams& p, const Place& w, char* smem) {
   constexpr int kBufs = kBuffers<D, kDkvAlone<D>>, kTiles = 2 * kBufs;
   constexpr int kAhead = (kBufs - 2) * (2 * TileLoad<D>::kLoads + 1);
   constexpr int kStat = 4 * kTile * 4;                 // base, delta, lo, hi of a tile
-  extern __shared__ __align__(1024) char smem[];       // [kBufs] tiles of q, of do
+  // smem: [kBufs] tiles of q, of do
   const uint32_t tiles = lds_address(smem);
   char* stats = smem + kTiles * kTileBytes<D>;         // [kBufs] kStat
   float* bias = reinterpret_cast<float*>(stats + kBufs * kStat);
 
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int bx = head_of_group(blockIdx.x, gridDim.x);
+  const int bx = head_of_group(w.x, w.nx);
   const int part = bx % p.parts, bk = bx / p.parts, b = bk / p.Hk, hk = bk % p.Hk;
   BiasStage bs;                                        // (a bias goes with one head a workgroup)
   if constexpr (BIAS) bs.buckets(p, tid);
-  const int j0 = key_tile(p, b, reinterpret_cast<int*>(smem), tid,
+  const int j0 = key_tile(p, w, b, reinterpret_cast<int*>(smem), tid,
                           kDkvAlone<D> ? kUnits : 2 * kUnits) * 128;   // its first key
   const int jw = j0 + wave * 32, j = jw + (lane & 31);
   const int* qlo = p.qlo + static_cast<int64_t>(b) * p.tq64;
@@ -334,7 +334,7 @@ __global__ __launch_bounds__(kAttnThreads, kDkvAlone<D> ? 1 : 2) void attn_dkv_k
   const int heads = p.group / p.parts, h0 = hk * p.group + part * heads;
 
   if constexpr (BIAS) bs.values(p, h0);
-  const int* words = p.tile + (static_cast<int64_t>(b) * gridDim.y + j0 / 128) * kTileWords;
+  const int* words = p.tile + (static_cast<int64_t>(b) * w.ny + j0 / 128) * kTileWords;
   int qa = 0, qb = 0;
   uint32_t wave_sees = 0;
   if (p.Tq > 0) {                                      // (without queries there is no workspace)
@@ -438,7 +438,7 @@ __global__ __launch_bounds__(kAttnThreads, kDkvAlone<D> ? 1 : 2) void attn_dkv_k
   };
   const bool near = ql.near && ol.near;
   const auto overlapped = [&](auto is_full) {
-    return [&, is_full] {
+    return [&] {
       const bool more = n + kBufs - 1 < turns;
       const int to = (buf + kBufs - 1) % kBufs;
       tile().template overlapped<decltype(is_full)::value>(
@@ -492,6 +492,12 @@ __global__ __launch_bounds__(kAttnThreads, kDkvAlone<D> ? 1 : 2) void attn_dkv_k
       *reinterpret_cast<bf16x4*>(ok + 32 * t + result_row(r, lane)) = x;
       *reinterpret_cast<bf16x4*>(ov + 32 * t + result_row(r, lane)) = y;
     }
+}
+
+template <int D, bool CAP, bool BIAS>
+__global__ __launch_bounds__(kAttnThreads, kDkvAlone<D> ? 1 : 2) void attn_dkv_kernel(const AttnParams p) {
+  extern __shared__ __align__(1024) char smem[];
+  attn_dkv<D, CAP, BIAS>(p, place(), smem);
 }
 
 // dk and dv from the parts, in the order of the heads: 8 values to a thread.
@@ -631,11 +637,10 @@ template <int D, bool BIAS>
 constexpr bool kDqAlone = D > 96 && BIAS;
 
 template <int D, bool CAP, bool BIAS>
-__global__ __launch_bounds__(kAttnThreads, (kDqAlone<D, BIAS> ? 1 : 2)) void attn_dq_kernel(
-    const AttnParams p) {
+__device__ __forceinline__ void attn_dq(const AttnParams& p, const Place& w, char* smem) {
   constexpr int kBufs = kBuffers<D, kDqAlone<D, BIAS>>, kTiles = 2 * kBufs;
   constexpr int kAhead = (kBufs - 2) * 2 * TileLoad<D>::kLoads;
-  extern __shared__ __align__(1024) char smem[];       // [kBufs] tiles of k, of v
+  // smem: [kBufs] tiles of k, of v
   const uint32_t tiles = lds_address(smem);
   int2* ranges = reinterpret_cast<int2*>(smem + kTiles * kTileBytes<D>);  // [128]
   int* hull = reinterpret_cast<int*>(ranges + 128);                  // [kWaves][2]
@@ -647,11 +652,11 @@ __global__ __launch_bounds__(kAttnThreads, (kDqAlone<D, BIAS> ? 1 : 2)) void att
 
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int bh = head_of_group(blockIdx.x, gridDim.x), b = bh / p.Hq, h = bh % p.Hq;
+  const int bh = head_of_group(w.x, w.nx), b = bh / p.Hq, h = bh % p.Hq;
   const int hk = h / p.group;
   BiasStage bs;
   if constexpr (BIAS) bs.buckets(p, tid);
-  const int tile = query_tile(p, b, reinterpret_cast<int*>(ranges), tid, kDqAlone<D, BIAS> ? kUnits : 2 * kUnits);
+  const int tile = query_tile(p, w, b, reinterpret_cast<int*>(ranges), tid, kDqAlone<D, BIAS> ? kUnits : 2 * kUnits);
   const int i0 = tile * 128 + wave * 32;
   const int i = i0 + (lane & 31);
   const ScoreFactors f(p, CAP);
@@ -774,7 +779,7 @@ __global__ __launch_bounds__(kAttnThreads, (kDqAlone<D, BIAS> ? 1 : 2)) void att
       past[2 * wave + 1] = ends[1];
     }
     __syncthreads();
-    float* out = p.dpart + (static_cast<int64_t>(bh) * gridDim.y + tile) * entries;
+    float* out = p.dpart + (static_cast<int64_t>(bh) * w.ny + tile) * entries;
     for (int d = tid; d < entries; d += kAttnThreads) {
       float x = 0.f;
 #pragma unroll
@@ -784,6 +789,25 @@ __global__ __launch_bounds__(kAttnThreads, (kDqAlone<D, BIAS> ? 1 : 2)) void att
       out[d] = x;
     }
   }
+}
+
+template <int D, bool CAP, bool BIAS>
+__global__ __launch_bounds__(kAttnThreads, (kDqAlone<D, BIAS> ? 1 : 2)) void attn_dq_kernel(
+    const AttnParams p) {
+  extern __shared__ __align__(1024) char smem[];
+  attn_dq<D, CAP, BIAS>(p, place(), smem);
+}
+
+// Both in one launch, where both run two workgroups to a compute unit: the second's
+// workgroups fill the places that the last of the first leave.  `kv` and `q`: the two grids.
+template <int D, bool CAP, bool BIAS>
+__global__ __launch_bounds__(kAttnThreads, 2) void attn_grads_kernel(const AttnParams p, int2 kv, int2 q) {
+  extern __shared__ __align__(1024) char smem[];
+  const int id = blockIdx.x, behind = id - kv.x * kv.y;
+  if (behind < 0)
+    attn_dkv<D, CAP, BIAS>(p, Place{id % kv.x, id / kv.x, kv.x, kv.y}, smem);
+  else
+    attn_dq<D, CAP, BIAS>(p, Place{behind % q.x, behind / q.x, q.x, q.y}, smem);
 }
 
 // The sums by distance over all batch rows and query tiles: 64 distances of a head
@@ -862,39 +886,44 @@ int choose_parts(int B, int Tk, int Hq, int Hk, bool bias) {
   return parts;
 }
 
-template <typename F>
-hipError_t launch_lds(F fn, dim3 grid, size_t lds, const AttnParams& p, hipStream_t s) {
+template <typename... A>
+hipError_t launch_lds(void (*fn)(A...), dim3 grid, size_t lds, hipStream_t s, A... args) {
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
                                            hipFuncAttributeMaxDynamicSharedMemorySize,
                                            static_cast<int>(lds));
   if (e != hipSuccess) return e;
-  fn<<<grid, kAttnThreads, lds, s>>>(p);
+  fn<<<grid, kAttnThreads, lds, s>>>(args...);
   return hipGetLastError();
 }
 
 template <int D, bool CAP, bool BIAS>
 hipError_t run_bwd(const AttnParams& p, hipStream_t s) {
   const size_t n = BIAS ? bias_entries(p.reach) : 0;
-  const int tiles = (p.Tq + 127) / 128;
   const size_t dkv_bufs = kBuffers<D, kDkvAlone<D>>, dq_bufs = kBuffers<D, kDqAlone<D, BIAS>>;
+  const size_t kv_lds = dkv_bufs * (2 * kTileBytes<D> + 4 * kTile * 4) + n * 4;
+  const size_t q_lds = dq_bufs * 2 * kTileBytes<D> + 128 * 8 + 4 * kWaves * 4 +
+                       (BIAS ? n + kWaves * (kDiagWords + n) : 0) * sizeof(float);
+  const int tiles = (p.Tq + 127) / 128;
+  const int2 kv = make_int2(p.B * p.Hk * p.parts, (p.Tk + 127) / 128);
+  const int2 q = make_int2(p.B * p.Hq, tiles);
   hipError_t e = hipSuccess;
-  if (p.B > 0 && p.Tk > 0) {
-    e = launch_lds(attn_dkv_kernel<D, CAP, BIAS>, dim3(p.B * p.Hk * p.parts, (p.Tk + 127) / 128),
-                   dkv_bufs * (2 * kTileBytes<D> + 4 * kTile * 4) + n * 4, p, s);
+  const int64_t both = static_cast<int64_t>(kv.x) * kv.y + static_cast<int64_t>(q.x) * q.y;
+  if (both == 0) return e;
+  if (!kDkvAlone<D> && both < (1 << 23)) {             // (256 threads each, below 2^31)
+    e = launch_lds(attn_grads_kernel<D <= 64 ? D : 64, CAP, BIAS>, dim3(static_cast<unsigned>(both)),
+                   kv_lds > q_lds ? kv_lds : q_lds, s, p, kv, q);
+  } else {
+    if (kv.x > 0 && kv.y > 0) e = launch_lds(attn_dkv_kernel<D, CAP, BIAS>, dim3(kv.x, kv.y), kv_lds, s, p);
     if (e != hipSuccess) return e;
-    if (p.parts > 1) {
-      const int64_t pieces = static_cast<int64_t>(p.B) * p.Hk * p.Tk * D / 8;
-      attn_dkv_join_kernel<<<static_cast<unsigned>((pieces + 255) / 256), 256, 0, s>>>(p, D);
-      e = hipGetLastError();
-      if (e != hipSuccess) return e;
-    }
+    if (q.x > 0 && q.y > 0) e = launch_lds(attn_dq_kernel<D, CAP, BIAS>, dim3(q.x, q.y), q_lds, s, p);
   }
-  if (p.B > 0 && p.Tq > 0)
-    e = launch_lds(attn_dq_kernel<D, CAP, BIAS>, dim3(p.B * p.Hq, tiles),
-                   dq_bufs * 2 * kTileBytes<D> + 128 * 8 + 4 * kWaves * 4 +
-                       (BIAS ? n + kWaves * (kDiagWords + n) : 0) * sizeof(float),
-                   p, s);
   if (e != hipSuccess) return e;
+  if (p.parts > 1 && kv.y > 0) {
+    const int64_t pieces = static_cast<int64_t>(p.B) * p.Hk * p.Tk * D / 8;
+    attn_dkv_join_kernel<<<static_cast<unsigned>((pieces + 255) / 256), 256, 0, s>>>(p, D);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   if (BIAS && p.dtable) {
     attn_dsum_kernel<<<dim3(p.Hq, static_cast<unsigned>((n + 63) / 64)), 1024, 0, s>>>(p, tiles);
     e = hipGetLastError();

@@ -122,7 +122,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnPar
   const int hk = h / p.group;
   BiasStage bs;
   if constexpr (BIAS) bs.buckets(p, tid);
-  const int tile = query_tile(p, b, reinterpret_cast<int*>(ranges), tid, 2 * kUnits);
+  const int tile = query_tile(p, place(), b, reinterpret_cast<int*>(ranges), tid, 2 * kUnits);
   const int i0 = tile * kRows + wave * 32;
   const int i = i0 + (lane & 31);
   const ScoreFactors f(p, CAP);
