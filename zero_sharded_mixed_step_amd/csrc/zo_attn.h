@@ -287,9 +287,9 @@ struct TileLoad {
   }
 };
 
-// Tiles of a pair of tensors under way or in use.  With three, a tile's loads have two
-// turns to arrive: a turn alone (1 to 2 us) does not cover the way to memory.
-// Where two workgroups share a compute unit, three of 128 columns do not fit.
+// Tiles of a pair of tensors under way or in use in the backward kernels.  With three, a
+// tile's loads have two turns to arrive: 274 us instead of 279 with two (4096 keys, 16 heads
+// of 64).  Where two workgroups share a compute unit, three of 128 columns do not fit.
 template <int D, bool ALONE>
 constexpr int kBuffers = D <= 96 || ALONE ? 3 : 2;
 
@@ -402,7 +402,7 @@ __device__ __forceinline__ bf16x8 signed_frag(bf16x8 f, bool flip) {
 
 // Workgroup index along x to (batch, head): the 8 dies take workgroups in turn, so
 // eighths of the heads in a row go to one die, whose cache then serves the query
-// heads of a key head together.
+// heads of a key head together (457 us instead of 459, backward, 4001 keys, 32 on 8 heads).
 __device__ __forceinline__ int head_of_group(int x, int n) {
   return n % 8 == 0 ? (x % 8) * (n / 8) + x / 8 : x;
 }
@@ -485,7 +485,9 @@ __device__ __forceinline__ int tile_of_rank(int y, int n, int* scratch, int tid,
   __syncthreads();
   return t;
 }
-constexpr int kMinRanked = 16, kMaxRanked = 255;   // (a few tiles are not worth the ranking)
+// (Ranked, 137 us instead of 154 forward and 457 instead of 476 backward: 4096 and 4001 keys
+// in two documents.  Eight tiles, 1024 keys: the same.  256 threads rank 255 tiles.)
+constexpr int kMinRanked = 16, kMaxRanked = 255;
 
 // The same for a tile of 128 queries: its cost is the span of keys that four of its
 // queries see.  Without ranges, or where all workgroups run `at_once` anyway, the last
