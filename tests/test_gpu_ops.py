@@ -305,6 +305,45 @@ def test_attention_offsets_past_32_bits(zs, torch):
         R.check(name, got, *want[name])
 
 
+@pytest.mark.parametrize("D", [96, 128])
+def test_attention_far_query_rows(zs, torch, D):
+    """Rows of q and do, and keys and values, 16 MiB apart: further than a staged
+    tile's 32-bit offsets go."""
+    bf = torch.bfloat16
+    T, stride = 70, 1 << 23
+    q, k, v, do = _attn_inputs(torch, 1, T, T, 1, 1, D, seed=D)
+    big = torch.empty(T * stride, dtype=bf, device="cuda")            # 1.2 GB
+    far = [big[4096 * n:].as_strided((1, T, 1, D), (T * stride, stride, D, 1)) for n in range(4)]
+    for x, y in zip(far, (q, k, v, do)):
+        x.copy_(y)
+    near = _dev(q, k, v, do)
+    ws = _ws(zs, torch, q, k, None, True)
+    results = []
+    for a in (far, near):
+        o, lse = torch.empty_like(near[0]), torch.empty(1, 1, T, device="cuda")
+        zs.zero_attn_fwd(*a[:3], o, lse, causal=True)
+        g = [torch.empty_like(x) for x in near[:3]]
+        zs.zero_attn_bwd(*a[:3], o, lse, a[3], *g, causal=True, workspace=ws)
+        results.append((o, lse, *g))
+    # the same sums in the same order, whichever way a tile was fetched
+    assert all(torch.equal(x, y) for x, y in zip(*results))
+
+
+@pytest.mark.parametrize("T,H,D,cap", [(517, 2, 128, 30.0), (517, 2, 96, 0.0), (2060, 16, 128, 0.0)])
+def test_attention_many_tiles_of_documents(zs, torch, T, H, D, cap):
+    """Several tiles each way: whole and partly masked tiles in turn, documents that
+    begin inside a tile, and (17 tiles of 16 heads) tiles taken by cost."""
+    q, k, v, do = _attn_inputs(torch, 1, T, T, H, H, D, seed=T + D)
+    doc = torch.zeros((1, T), dtype=torch.int32)
+    prefix = torch.zeros((1, T), dtype=torch.int32)
+    cuts = [0, T // 3 + 5, T // 3 + 40, T - 9]
+    for n, (lo, hi) in enumerate(zip(cuts, cuts[1:])):
+        doc[0, lo:hi] = n
+        prefix[0, lo:hi] = (hi - lo) // 2
+    doc[0, cuts[-1]:] = -1
+    _attn_both(zs, torch, q, k, v, do, ranges=R.doc_ranges(doc, prefix), cap=cap)
+
+
 def test_attention_gradient_by_differences(zs, torch):
     """dtable, and dq, dk, dv along random directions, against central
     differences of the 64-bit forward (1e-4 steps: their error is below 1e-6
