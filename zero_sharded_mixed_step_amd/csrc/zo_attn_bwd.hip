@@ -131,11 +131,12 @@ __device__ __forceinline__ void grad_score(float x, float base, float dp, float 
 
 // ---------------------------------------------------------------- dk, dv ---
 
-// The registers of one wave a SIMD for 96 columns and more: k, v, dk and dv alone take
-// 144 or 192 of the 256 that two waves leave each.  (At 64, 275 us with two waves and
-// 333 with one: 4096 keys, 16 heads.)
-template <int D>
-constexpr bool kDkvAlone = D > 64;
+// The registers of one wave a SIMD for 128 columns, and for 96 with a bias: k, v, dk and
+// dv alone take 192 or 144 of the 256 that two waves leave each, and the rest does not fit.
+// (Where it does, two waves: 368 us instead of 433 at 96 columns, 275 instead of 333 at
+// 64; 4096 keys, 16 heads.)
+template <int D, bool BIAS>
+constexpr bool kDkvAlone = D > 96 || (D > 64 && BIAS);
 
 // One tile of 64 queries, do's behind q's, for a wave's 32 keys: two blocks of 32
 // queries, of 4 D / 16 matrix instructions and 16 scores a lane each.  A wave that has
@@ -144,8 +145,8 @@ constexpr bool kDkvAlone = D > 64;
 // second's are.
 template <int D, bool CAP, bool BIAS>
 struct DkvTile {
-  static constexpr bool kOverlap = kDkvAlone<D>;
-  static constexpr int kG = kBuffers<D, kDkvAlone<D>> * kTileBytes<D>;  // from q's tile to do's
+  static constexpr bool kOverlap = kDkvAlone<D, BIAS>;
+  static constexpr int kG = kBuffers<D, kDkvAlone<D, BIAS>> * kTileBytes<D>;  // from q's tile to do's
   static constexpr int kC = D / 16, kT = D / 32;
   const AttnParams& p;
   const ScoreFactors& f;
@@ -320,7 +321,7 @@ __device__ __forceinline__ int key_tile(const AttnParams& p, const Place& w, int
 // 64 queries of the query heads that share it, or of a part of them.
 template <int D, bool CAP, bool BIAS>
 __device__ __forceinline__ void attn_dkv(const AttnParams& p, const Place& w, char* smem) {
-  constexpr int kBufs = kBuffers<D, kDkvAlone<D>>, kTiles = 2 * kBufs;
+  constexpr int kBufs = kBuffers<D, kDkvAlone<D, BIAS>>, kTiles = 2 * kBufs;
   constexpr int kAhead = (kBufs - 2) * (2 * TileLoad<D>::kLoads + 1);
   constexpr int kStat = 4 * kTile * 4;                 // base, delta, lo, hi of a tile
   // smem: [kBufs] tiles of q, of do
@@ -335,7 +336,7 @@ __device__ __forceinline__ void attn_dkv(const AttnParams& p, const Place& w, ch
   BiasStage bs;                                        // (a bias goes with one head a workgroup)
   if constexpr (BIAS) bs.buckets(p, tid);
   const int j0 = key_tile(p, w, b, reinterpret_cast<int*>(smem), tid,
-                          kDkvAlone<D> ? kUnits : 2 * kUnits) * 128;   // its first key
+                          kDkvAlone<D, BIAS> ? kUnits : 2 * kUnits) * 128;   // its first key
   const int jw = j0 + wave * 32, j = jw + (lane & 31);
   const int* qlo = p.qlo + static_cast<int64_t>(b) * p.tq64;
   const int* qhi = p.qhi + static_cast<int64_t>(b) * p.tq64;
@@ -505,7 +506,7 @@ __device__ __forceinline__ void attn_dkv(const AttnParams& p, const Place& w, ch
 }
 
 template <int D, bool CAP, bool BIAS>
-__global__ __launch_bounds__(kAttnThreads, kDkvAlone<D> ? 1 : 2) void attn_dkv_kernel(const AttnParams p) {
+__global__ __launch_bounds__(kAttnThreads, (kDkvAlone<D, BIAS> ? 1 : 2)) void attn_dkv_kernel(const AttnParams p) {
   extern __shared__ __align__(1024) char smem[];
   attn_dkv<D, CAP, BIAS>(p, place(), smem);
 }
@@ -910,7 +911,7 @@ hipError_t launch_lds(void (*fn)(A...), dim3 grid, size_t lds, hipStream_t s, A.
 template <int D, bool CAP, bool BIAS>
 hipError_t run_bwd(const AttnParams& p, hipStream_t s) {
   const size_t n = BIAS ? bias_entries(p.reach) : 0;
-  const size_t dkv_bufs = kBuffers<D, kDkvAlone<D>>, dq_bufs = kBuffers<D, kDqAlone<D, BIAS>>;
+  const size_t dkv_bufs = kBuffers<D, kDkvAlone<D, BIAS>>, dq_bufs = kBuffers<D, kDqAlone<D, BIAS>>;
   const size_t kv_lds = dkv_bufs * (2 * kTileBytes<D> + 4 * kTile * 4) + n * 4;
   const size_t q_lds = dq_bufs * 2 * kTileBytes<D> + 128 * 8 + 4 * kWaves * 4 +
                        (BIAS ? n + kWaves * (kDiagWords + n) : 0) * sizeof(float);
@@ -920,10 +921,14 @@ hipError_t run_bwd(const AttnParams& p, hipStream_t s) {
   hipError_t e = hipSuccess;
   const int64_t both = static_cast<int64_t>(kv.x) * kv.y + static_cast<int64_t>(q.x) * q.y;
   if (both == 0) return e;
-  if (!kDkvAlone<D> && both < (1 << 23)) {             // (256 threads each, below 2^31)
-    e = launch_lds(attn_grads_kernel<D <= 64 ? D : 64, CAP, BIAS>, dim3(static_cast<unsigned>(both)),
-                   kv_lds > q_lds ? kv_lds : q_lds, s, p, kv, q);
-  } else {
+  bool one = false;
+  if constexpr (!kDkvAlone<D, BIAS> && !kDqAlone<D, BIAS>) {
+    one = both < (1 << 23);                            // (256 threads each, below 2^31)
+    if (one)
+      e = launch_lds(attn_grads_kernel<D, CAP, BIAS>, dim3(static_cast<unsigned>(both)),
+                     kv_lds > q_lds ? kv_lds : q_lds, s, p, kv, q);
+  }
+  if (!one) {
     if (kv.x > 0 && kv.y > 0) e = launch_lds(attn_dkv_kernel<D, CAP, BIAS>, dim3(kv.x, kv.y), kv_lds, s, p);
     if (e != hipSuccess) return e;
     if (q.x > 0 && q.y > 0) e = launch_lds(attn_dq_kernel<D, CAP, BIAS>, dim3(q.x, q.y), q_lds, s, p);
