@@ -19,28 +19,13 @@
 #pragma once
 
 #include "zo_device.h"
+#include "zo_tile.h"
 #include "zero_ops.h"
 
 namespace zo {
 
 constexpr int kAttnThreads = 256;
-constexpr int kWaves = 4;
-constexpr int kTile = 64;  // rows of a staged tile
 constexpr int kUnits = 256;  // compute units of the card
-
-// A staged tile is 64 rows of D bf16 without gaps (the direct loads to shared
-// memory write 64 lanes' 16 bytes one after another), and the 16-byte pieces of
-// row r are stored at piece ^ swizzle(r).  The 8 rows of consecutive lanes'
-// 16-byte reads, and the 4 rows of a transposing read, then fall on different
-// banks: with 256-byte rows all start on the same bank and the 4 x 32 bytes of a
-// transposing read need 4 different pairs of pieces; 128-byte rows alternate between
-// two halves of the banks, 64- and 192-byte rows repeat after 4.
-template <int D>
-__device__ __forceinline__ constexpr int swizzle(int r) {
-  return D == 128 ? (r & 7) << 1 : D == 64 ? r & 6 : (r >> 2) & 1;
-}
-template <int D>
-constexpr int kTileBytes = kTile * D * 2;
 
 // Of a tile of 128 keys: the tiles of 64 queries that see any of it, first and one past
 // the last, and a bit for each key that is seen.
@@ -190,12 +175,23 @@ __device__ __forceinline__ bf16x8 to_frag(const float* x) {
 // only wait they need.  (m0, which nothing else here uses, takes the address.  The wait
 // states cover its write, and scalar registers that a vector instruction wrote just
 // before: inside the text no one else inserts them.)
-__device__ __forceinline__ void lds_load16(uint32_t to, u32x4 buffer, uint32_t lane_offset,
-                                           uint32_t offset) {
+// The form with a scalar offset is for rows that are all there; the one without is also
+// for descriptors that end before the tile does: what is beyond is then told by the lane's
+// offset alone.
+__device__ __forceinline__ void lds_load16_whole(uint32_t to, u32x4 buffer, uint32_t lane_offset,
+                                                 uint32_t offset) {
 #ifdef __HIP_DEVICE_COMPILE__
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(
                    uniform(to)),
                "v"(lane_offset), "s"(buffer), "s"(uniform(offset))
+               : "memory");
+#endif
+}
+__device__ __forceinline__ void lds_load16(uint32_t to, u32x4 buffer, uint32_t lane_offset) {
+#ifdef __HIP_DEVICE_COMPILE__
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(
+                   uniform(to)),
+               "v"(lane_offset), "s"(buffer)
                : "memory");
 #endif
 }
@@ -235,37 +231,30 @@ __device__ __forceinline__ u32x4 buffer_at(const void* base, uint32_t bytes = 0x
 // and rows too far apart for the offsets go the same way.
 template <int D>
 struct TileLoad {
-  static constexpr int kLoads = D / 32;                // of the workgroup's D / 8, 64 pieces each
-  // (8 rows further the swizzle is the same: loads that start there share a lane offset)
-  static constexpr int kOffs = D == 128 ? 2 : D == 64 ? 1 : kLoads;
+  using Map = TileMap<D>;
+  static constexpr int kLoads = Map::kLoads;
   const bf16* base;
   int64_t stride;
   int first, last;
   bool near;
-  uint32_t off[kOffs];
+  uint32_t off[Map::kOffs];
 
   __device__ __forceinline__ TileLoad(const bf16* b, int64_t s, int from, int to, int wave, int lane)
       : base(b), stride(s), first(from), last(to) {
-    near = s >= 0 && s < (1 << 23);
+    near = Map::near(s);
 #pragma unroll
-    for (int u = 0; u < kOffs; ++u) {
-      const int piece = (wave * kLoads + u) * 64 + lane;
-      const int r = piece / (D / 8), c = (piece % (D / 8)) ^ swizzle<D>(r);
-      off[u] = static_cast<uint32_t>(r) * static_cast<uint32_t>(s) * 2u + c * 16u;
-    }
+    for (int u = 0; u < Map::kOffs; ++u) off[u] = Map::first_offset(wave, u, lane, s);
   }
 
   // For near rows, without a branch: rows from `last` on become 0, and all of them do
-  // without `on`.
+  // without `on`.  Each run of loads has a descriptor of its own, which ends where the rows do.
   __device__ __forceinline__ void start_near(uint32_t tile, int row0, bool on, int wave) const {
-    const int n = max(min(last - row0, kTile), 0);       // (64 rows of 16 MiB stay below 2^30)
-    const uint32_t bytes = ((n - 1) * static_cast<uint32_t>(stride) + D) * 2u *
-                           static_cast<uint32_t>(on & (n > 0));
-    const u32x4 from = buffer_at(base + row0 * stride, bytes);
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u)
-      lds_load16(tile + wave * (kLoads * 1024) + u * 1024, from,
-                 off[u % kOffs], static_cast<uint32_t>((u / kOffs) * 16 * stride));
+    for (int u = 0; u < kLoads; ++u) {
+      const int row = row0 + Map::rows_on(u);
+      const u32x4 from = buffer_at(base + row * stride, Map::bytes(last - row, stride, on));
+      lds_load16(tile + wave * (kLoads * 1024) + u * 1024, from, off[u % Map::kOffs]);
+    }
   }
 
   __device__ __forceinline__ void start(uint32_t tile, int row0, int wave, int lane) const {
@@ -274,13 +263,12 @@ struct TileLoad {
       const u32x4 from = buffer_at(base + row0 * stride);
 #pragma unroll
       for (int u = 0; u < kLoads; ++u)
-        lds_load16(to + u * 1024, from, off[u % kOffs],
-                   static_cast<uint32_t>((u / kOffs) * 16 * stride));
+        lds_load16_whole(to + u * 1024, from, off[u % Map::kOffs],
+                         static_cast<uint32_t>(Map::rows_on(u) * 2 * stride));
     } else {
 #pragma unroll 1
       for (int u = 0; u < kLoads; ++u) {
-        const int piece = (wave * kLoads + u) * 64 + lane;
-        const int r = piece / (D / 8), c = (piece % (D / 8)) ^ swizzle<D>(r);
+        const int r = Map::row(wave, u, lane), c = Map::column(wave, u, lane);
         lds_load16(to + u * 1024, base + min(max(row0 + r, first), last - 1) * stride + c * 8);
       }
     }
