@@ -1,0 +1,171 @@
+"""The training operators at the ends of what they accept: large and tiny caps, empty
+batches, rows that a teacher is sure of, infinities in masked places, and the paths
+that only larger shapes take."""
+import math
+
+import pytest
+
+import ops_ref as R
+import ops_range_ref as X
+from gpu_util import gpu_or_skip
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def zs():
+    gpu_or_skip()
+    import zero_sharded_mixed_step_amd as zs
+    zs.ops_lib()
+    return zs
+
+
+@pytest.fixture(scope="module")
+def torch():
+    return gpu_or_skip()
+
+
+def _gen(torch, seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def _rand(torch, g, shape, dtype, scale=1.0):
+    return (torch.randn(shape, generator=g) * scale).to(dtype)
+
+
+def _attn_inputs(torch, B, Tq, Tk, Hq, Hk, D, seed, qscale=2.0):
+    g = _gen(torch, seed)
+    bf = torch.bfloat16
+    return [_rand(torch, g, (B, Tq, Hq, D), bf, qscale), _rand(torch, g, (B, Tk, Hk, D), bf),
+            _rand(torch, g, (B, Tk, Hk, D), bf), _rand(torch, g, (B, Tq, Hq, D), bf)]
+
+
+def _attn(zs, torch, q, k, v, do, table=None, **kw):
+    """o, lse and the gradients {name: tensor} of one call of each direction."""
+    B, Tq, Hq, D = q.shape
+    n = 0 if table is None else table.shape[0]
+    ws = [torch.full((max(16, zs.zero_attn_workspace_bytes(B, Tq, k.shape[1], Hq, k.shape[2], D, n, b)),),
+                     0x7F, dtype=torch.uint8, device="cuda") for b in (False, True)]
+    o = torch.full_like(q, math.nan)
+    lse = torch.full((B, Hq, Tq), math.nan, dtype=torch.float32, device="cuda")
+    zs.zero_attn_fwd(q, k, v, o, lse, bias_table=table, workspace=ws[0], **kw)
+    g = {name: torch.full_like(x, math.nan) for name, x in (("dv", v), ("dk", k), ("dq", q))}
+    if table is not None:
+        g["dtable"] = torch.full_like(table, math.nan)
+    zs.zero_attn_bwd(q, k, v, o, lse, do, g["dq"], g["dk"], g["dv"], dbias_table=g.get("dtable"),
+                     bias_table=table, workspace=ws[1], **kw)
+    return o, lse, g
+
+
+def _attn_check(zs, torch, q, k, v, do, *, scale=None, cap=0.0, ranges=None, causal=False, table=None,
+                buckets=None, ref=X.Attention):
+    """Both directions against the 64-bit formula."""
+    scale = q.shape[-1] ** -0.5 if scale is None else scale
+    seen = R.visible(q.shape[0], q.shape[1], k.shape[1], ranges, causal)
+    want = ref(q, k, v, scale=scale, cap=cap, seen=seen, table=table, buckets=buckets)
+    dev = lambda t: None if t is None else t.cuda()
+    o, lse, g = _attn(zs, torch, *(dev(t) for t in (q, k, v, do)), dev(table), scale=scale, cap=cap,
+                      ranges=dev(ranges), causal=causal, bias_buckets=dev(buckets))
+    want_o, bound_o, want_l, bound_l = want.forward()
+    R.check("lse", lse, want_l, bound_l)
+    R.check("o", o, want_o, bound_o)
+    grads = want.backward(o.cpu(), do)
+    for name, got in g.items():
+        R.check(name, got, *grads[name])
+
+
+# ----------------------------------------------- masked places, sure masks ---
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("value", ["lowest", "-inf"])
+def test_attention_backward_of_masking_biases(zs, torch, D, value):
+    """A bias of the type's lowest value, or -inf, at distances beside others that are
+    seen: both directions are those of a mask."""
+    T = 150
+    q, k, v, do = _attn_inputs(torch, 1, T, T, 2, 2, D, seed=D + 2)
+    low = torch.finfo(torch.bfloat16).min if value == "lowest" else -math.inf
+    table = _rand(torch, _gen(torch, 6), (4, 2), torch.bfloat16)
+    buckets = torch.tensor([3, 3, 1, 0, 2, 3, 3], dtype=torch.int32)           # 3: 2 and further
+    dist = torch.arange(T)[None] - torch.arange(T)[:, None]
+    seen = ((dist <= 1) & (dist >= -1))[None]
+    want = X.Attention(q, k, v, scale=D ** -0.5, seen=seen, table=table, buckets=buckets)
+    table[3] = low
+    o, lse, got = _attn(zs, torch, q.cuda(), k.cuda(), v.cuda(), do.cuda(), table.cuda(),
+                        scale=D ** -0.5, bias_buckets=buckets.cuda())
+    want_o, bound_o, want_l, bound_l = want.forward()
+    R.check("lse", lse, want_l, bound_l)
+    R.check("o", o, want_o, bound_o)
+    grads = want.backward(o.cpu(), do)
+    for name in ("dv", "dk", "dq"):
+        R.check(name, got[name], *grads[name])
+    val, bound = grads["dtable"]
+    R.check("dtable", got["dtable"][:3], val[:3], bound[:3])
+    assert bool((got["dtable"][3] == 0).all())
+
+
+# ------------------------------------------- paths that larger shapes take ---
+
+@pytest.mark.parametrize("B,T,Hq,Hk,D,cap", [
+    (4, 1100, 32, 8, 128, 30.0),      # 288 groups of keys: two parts of two heads each
+    (8, 1100, 16, 8, 128, 0.0),       # 576: one part of two heads
+    (4, 1100, 32, 8, 64, 0.0),        # the same in one launch with the queries' kernel
+    (8, 1100, 16, 8, 32, 0.0),
+    (8, 1100, 16, 8, 96, 0.0)])
+def test_attention_backward_of_several_heads_a_workgroup(zs, torch, B, T, Hq, Hk, D, cap):
+    """Key heads that a workgroup walks for more than one query head, in documents that
+    begin inside tiles.  (One batch row against the formula, the others are its copies.)"""
+    q, k, v, do = _attn_inputs(torch, 1, T, T, Hq, Hk, D, seed=T + D)
+    doc = torch.zeros((1, T), dtype=torch.int32)
+    cuts = [0, 300, 411, 900, T - 9]
+    for n, (lo, hi) in enumerate(zip(cuts, cuts[1:])):
+        doc[0, lo:hi] = n
+    doc[0, cuts[-1]:] = -1
+    ranges = R.doc_ranges(doc)
+    all_ = [x.expand(B, *x.shape[1:]).contiguous().cuda() for x in (q, k, v, do)]
+    o, lse, got = _attn(zs, torch, *all_, cap=cap,
+                        ranges=ranges.expand(B, T, 2).contiguous().cuda())
+    for name, x in [("o", o), ("lse", lse)] + list(got.items()):
+        assert all(torch.equal(x[0], x[b]) for b in range(1, B)), name
+    # the formula a few key heads at a time (64 bits on the host)
+    G = Hq // Hk
+    seen = R.visible(1, T, T, ranges)
+    for hk in (0, Hk - 1):
+        one = [q[:, :, hk * G:(hk + 1) * G], k[:, :, hk:hk + 1], v[:, :, hk:hk + 1],
+               do[:, :, hk * G:(hk + 1) * G]]
+        ref = X.Attention(*one[:3], scale=D ** -0.5, cap=cap, seen=seen)
+        want_o, bound_o, _, _ = ref.forward()
+        oh = o[:1, :, hk * G:(hk + 1) * G].cpu()
+        R.check("o", oh, want_o, bound_o)
+        grads = ref.backward(oh, one[3])
+        R.check("dq", got["dq"][:1, :, hk * G:(hk + 1) * G], *grads["dq"])
+        R.check("dk", got["dk"][:1, :, hk:hk + 1], *grads["dk"])
+        R.check("dv", got["dv"][:1, :, hk:hk + 1], *grads["dv"])
+
+
+@pytest.mark.parametrize("D,Hq,Hk", [(64, 2, 2), (64, 4, 1), (32, 2, 1), (96, 2, 2), (128, 4, 2)])
+def test_attention_cap_and_bias(zs, torch, D, Hq, Hk):
+    q, k, v, do = _attn_inputs(torch, 2, 210, 210, Hq, Hk, D, seed=D + Hq)
+    table = _rand(torch, _gen(torch, 3), (16, Hq), torch.bfloat16)
+    _attn_check(zs, torch, q, k, v, do, causal=True, cap=10.0, table=table,
+                buckets=zs.relpos_buckets(16, 40))
+
+
+def test_distill_backward_of_many_rows(zs, torch):
+    """More rows than one launch takes."""
+    N, V, K = 65535 + 70, 24, 3
+    g = _gen(torch, 5)
+    z = _rand(torch, g, (N, V), torch.float32, 2.0)
+    t = z + torch.randn(N, V, generator=g)
+    val, idx = torch.topk(t, K, dim=1)
+    idx, tlse = idx.to(torch.int32), torch.logsumexp(t.double(), 1).float()
+    w = torch.rand(N, generator=g) + 0.5
+    want = R.distill(z, idx, val, 1.0, tlse, w, 0.5)
+    loss, stats = torch.empty(N, device="cuda"), torch.empty(N, 2, device="cuda")
+    kw = dict(teacher_lse=tlse.cuda(), row_weight=w.cuda(), grad_scale=0.5)
+    zs.zero_distill_fwd(z.cuda(), idx.cuda(), val.cuda(), loss, stats, **kw)
+    R.check("loss", loss, *want["loss"])
+    dz = torch.full((N, V), math.nan, device="cuda")
+    zs.zero_distill_bwd(z.cuda(), idx.cuda(), val.cuda(), stats, dz, **kw)
+    R.check("dz", dz, *want["dz"])
