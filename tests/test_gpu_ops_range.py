@@ -76,6 +76,28 @@ def _attn_check(zs, torch, q, k, v, do, *, scale=None, cap=0.0, ranges=None, cau
         R.check(name, got, *grads[name])
 
 
+# ----------------------------------------------------------- empty batches ---
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,Tq,Tk", [(0, 5, 5), (2, 0, 0), (0, 0, 0), (2, 0, 5), (2, 5, 0)])
+def test_attention_bias_gradient_of_an_empty_batch(zs, torch, B, Tq, Tk, dtype):
+    """The sum over nothing is 0, and is written."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    bf = torch.bfloat16
+    q = torch.ones(B, Tq, 4, 64, device="cuda", dtype=bf)
+    k = torch.ones(B, Tk, 2, 64, device="cuda", dtype=bf)
+    o, lse = torch.zeros_like(q), torch.full((B, 4, Tq), -math.inf, device="cuda")
+    table = torch.ones(8, 4, device="cuda", dtype=dt)
+    dtable = torch.full_like(table, math.nan)
+    gq, gk, gv = (torch.full_like(x, math.nan) for x in (q, k, k))
+    ws = torch.full((max(16, zs.zero_attn_workspace_bytes(B, Tq, Tk, 4, 2, 64, 8, True)),), 0x7F,
+                    dtype=torch.uint8, device="cuda")
+    zs.zero_attn_bwd(q, k, k, o, lse, q, gq, gk, gv, dbias_table=dtable, bias_table=table,
+                     bias_buckets=zs.relpos_buckets(8, 20, device="cuda"), workspace=ws)
+    assert bool((dtable == 0).all())
+    assert all(bool((x == 0).all()) for x in (gq, gk, gv))
+
+
 # ----------------------------------------------- masked places, sure masks ---
 
 @pytest.mark.parametrize("D", [64, 128])

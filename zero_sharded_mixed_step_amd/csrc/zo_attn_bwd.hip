@@ -920,10 +920,9 @@ hipError_t run_bwd(const AttnParams& p, hipStream_t s) {
   const int2 q = make_int2(p.B * p.Hq, tiles);
   hipError_t e = hipSuccess;
   const int64_t both = static_cast<int64_t>(kv.x) * kv.y + static_cast<int64_t>(q.x) * q.y;
-  if (both == 0) return e;
   bool one = false;
   if constexpr (!kDkvAlone<D, BIAS> && !kDqAlone<D, BIAS>) {
-    one = both < (1 << 23);                            // (256 threads each, below 2^31)
+    one = both > 0 && both < (1 << 23);                // (256 threads each, below 2^31)
     if (one)
       e = launch_lds(attn_grads_kernel<D, CAP, BIAS>, dim3(static_cast<unsigned>(both)),
                      kv_lds > q_lds ? kv_lds : q_lds, s, p, kv, q);
@@ -934,13 +933,13 @@ hipError_t run_bwd(const AttnParams& p, hipStream_t s) {
     if (q.x > 0 && q.y > 0) e = launch_lds(attn_dq_kernel<D, CAP, BIAS>, dim3(q.x, q.y), q_lds, s, p);
   }
   if (e != hipSuccess) return e;
-  if (p.parts > 1 && kv.y > 0) {
+  if (p.parts > 1 && kv.x > 0 && kv.y > 0) {
     const int64_t pieces = static_cast<int64_t>(p.B) * p.Hk * p.Tk * D / 8;
     attn_dkv_join_kernel<<<static_cast<unsigned>((pieces + 255) / 256), 256, 0, s>>>(p, D);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (BIAS && p.dtable) {
+  if (BIAS && p.dtable) {                              // (the sum over an empty batch is 0)
     attn_dsum_kernel<<<dim3(p.Hq, static_cast<unsigned>((n + 63) / 64)), 1024, 0, s>>>(p, tiles);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
