@@ -102,7 +102,7 @@ size_t zero_qk_norm_rope_workspace_bytes(int64_t T, int D);
  *
  * For query i and key j of one batch row and head, with off = Tk - Tq:
  *   x = scale * q_i . k_j
- *   c = cap * tanh(x / cap)  if cap > 0, else x
+ *   c = cap * tanh(x / cap)  if cap > 0, else x       (cap <= 1e30)
  *   s = c + bias_table[bias_buckets[clamp(j - i - off, -reach, reach)
  *                                   + reach]][h]   (if bias_table is given)
  * and s = -inf for keys outside the query's interval [lo, hi):

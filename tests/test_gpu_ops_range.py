@@ -76,6 +76,34 @@ def _attn_check(zs, torch, q, k, v, do, *, scale=None, cap=0.0, ranges=None, cau
         R.check(name, got, *grads[name])
 
 
+# -------------------------------------------------------------------- caps ---
+
+@pytest.mark.parametrize("cap", [50.0, 64.0, 65.0, 1e3, 1e5, 1e6, 1e9, 1e30])
+@pytest.mark.parametrize("D,bias", [(64, False), (64, True), (128, False), (128, True), (96, True),
+                                    (32, False)])
+def test_attention_caps_of_any_size(zs, torch, D, bias, cap):
+    """A cap far above the scores leaves them as they are."""
+    q, k, v, do = _attn_inputs(torch, 1, 140, 140, 4, 2, D, seed=D)
+    table = buckets = None
+    if bias:
+        table = _rand(torch, _gen(torch, 3), (8, 4), torch.float32)
+        buckets = zs.relpos_buckets(8, 20)
+    _attn_check(zs, torch, q, k, v, do, causal=True, cap=cap, table=table, buckets=buckets)
+
+
+@pytest.mark.parametrize("cap", [100.0, 2000.0])
+def test_attention_caps_beside_large_scores(zs, torch, cap):
+    """Scores on both sides of the place where the tanh's two forms meet, and past the cap."""
+    q, k, v, do = _attn_inputs(torch, 1, 150, 150, 2, 2, 64, seed=12, qscale=60.0)
+    _attn_check(zs, torch, q, k, v, do, causal=True, cap=cap)
+
+
+def test_attention_split_keys_large_cap(zs, torch):
+    q, k, v, do = _attn_inputs(torch, 1, 3, 2500, 2, 2, 64, seed=8)
+    assert zs.zero_attn_workspace_bytes(1, 3, 2500, 2, 2, 64) > 0
+    _attn_check(zs, torch, q, k, v, do, causal=True, cap=1e6)
+
+
 # ----------------------------------------------------------- empty batches ---
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

@@ -51,7 +51,7 @@ struct AttnParams {
   Strides3 qs, ks, vs, os, dos, dqs, dks, dvs;
   // workspace
   int tq64;         // Tq up to a multiple of 64: the rows below are padded to it
-  float* base;      // [B][Hq][tq64]  -lse * log2(e), plus cap * log2(e); -inf: no keys
+  float* base;      // [B][Hq][tq64]  -lse * log2(e), plus cap * log2(e) if kByU; -inf: no keys
   float* delta;     // [B][Hq][tq64]  do . o
   int *qlo, *qhi;   // [B][tq64]      the keys a query sees; 0, 0 for none
   int* tile;        // [B][key tiles][kTileWords] of what sees a tile of 128 keys
@@ -360,19 +360,44 @@ __device__ __forceinline__ int bias_side(int lowest, int highest, int reach) {
   return highest <= -reach ? -1 : lowest >= reach ? 1 : 0;
 }
 
+// How a score is capped.  cap tanh(y) = cap - 2 cap u with u = 1 / (exp(2 y) + 1), which
+// is off by two steps (exponential, sum, reciprocal): the score is off by up to cap 2^-22,
+// however small it is itself.  Up to kUCap that is 1.5e-5, a 250th of the rounding of p to
+// bf16.  A larger cap takes small y by the tanh's series instead, which costs (us, 4096 keys,
+// 32 on 8 heads, by u and by the series): forward 141 and 176 at 128 columns, 98 and 119 at
+// 64; backward 480 and 759, 276 and 503.
+constexpr float kUCap = 64.f;
+enum CapForm { kNoCap = 0, kByU = 1, kAnyCap = 2 };
+__host__ __device__ constexpr int cap_form(float cap) {
+  return cap > 0.f ? (cap <= kUCap ? kByU : kAnyCap) : kNoCap;
+}
+
 // Factors of the scores.  Without a cap a score in units of log2 is x * a.
-// With one, cap tanh(y) = cap - 2 cap u, u = 1 / (exp(2 y) + 1): exp(2 y) is
-// exp2(x * a) and the score c2 - 2 c2 u.  A negative scale is taken to q, so a > 0:
+// With one, exp(2 y) is exp2(x * a) and the score c2 - 2 c2 u, or, of kAnyCap for small y,
+// x * s times the series.  A negative scale is taken to q, so a > 0:
 // the largest score is that of the largest x, and of the smallest u.  (A scale
 // of 0 becomes one that vanishes beside any score.)
 struct ScoreFactors {
-  float a, c2;
+  float a, c2, s;
   bool flip;
-  __device__ __forceinline__ ScoreFactors(const AttnParams& p, bool cap) {
-    const float s = fmaxf(fabsf(p.scale), 1e-30f) * kLog2e;
+  __device__ __forceinline__ ScoreFactors(const AttnParams& p, int cap) {
+    s = fmaxf(fabsf(p.scale), 1e-30f) * kLog2e;
     a = cap ? fmaxf(2.f * s / p.cap, 1e-30f) : s;
     c2 = cap ? p.cap * kLog2e : 0.f;
     flip = p.scale < 0.f;
+  }
+  __device__ __forceinline__ float u_of(float x) const { return rcp_hw(exp2_hw(x * a) + 1.f); }
+  // The capped score of kAnyCap, in units of log2: tanh(y) / y = 1 - y^2 / 3 + 2 y^4 / 15 -
+  // 17 y^6 / 315 + 62 y^8 / 2835 - 1382 y^10 / 155925 + .., whose next term is below 2^-26
+  // for y < 0.35; beyond, u's error is below 12 steps of the score.
+  __device__ __forceinline__ float any_cap(float x, float u) const {
+    const float y = x * a * (0.5f * kLn2), w = y * y;
+    float t = __builtin_fmaf(w, -1382.f / 155925.f, 62.f / 2835.f);
+    t = __builtin_fmaf(w, t, -17.f / 315.f);
+    t = __builtin_fmaf(w, t, 2.f / 15.f);
+    t = __builtin_fmaf(w, t, -1.f / 3.f);
+    t = __builtin_fmaf(w, t, 1.f);
+    return w < 0.35f * 0.35f ? x * s * t : __builtin_fmaf(u, -2.f * c2, c2);
   }
 };
 

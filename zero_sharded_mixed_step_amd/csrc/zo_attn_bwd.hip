@@ -102,7 +102,8 @@ __global__ __launch_bounds__(256) void attn_bwd_prepare_kernel(const AttnParams 
     p.delta[row] = sum;
     float lse = -kInf;
     if (r.y > r.x) lse = p.lse[static_cast<int64_t>(bh) * p.Tq + i];
-    p.base[row] = lse != -kInf ? (p.cap > 0.f ? p.cap * kLog2e : 0.f) - lse * kLog2e : -kInf;
+    p.base[row] =
+        lse != -kInf ? (cap_form(p.cap) == kByU ? p.cap * kLog2e : 0.f) - lse * kLog2e : -kInf;
     if (h == 0) {
       p.qlo[static_cast<int64_t>(b) * p.tq64 + i] = r.x;
       p.qhi[static_cast<int64_t>(b) * p.tq64 + i] = r.y;
@@ -111,15 +112,15 @@ __global__ __launch_bounds__(256) void attn_bwd_prepare_kernel(const AttnParams 
 }
 
 // One score's p, ds and dx, from the raw product x, dp, and base = bias - lse (in log2,
-// plus c2 with a cap).  With a cap, u = (1 - tanh) / 2 and dx is a quarter of ds (1 -
-// tanh^2) = 4 ds u (1 - u): the 4 goes into the gradients' final scale.
-template <bool CAP>
+// plus c2 with a cap up to kUCap).  With a cap, u = (1 - tanh) / 2 and dx is a quarter of ds
+// (1 - tanh^2) = 4 ds u (1 - u): the 4 goes into the gradients' final scale.
+template <int CAP>
 __device__ __forceinline__ void grad_score(float x, float base, float dp, float delta,
                                            const ScoreFactors& f, float& pr, float& ds,
                                            float& dx) {
-  if constexpr (CAP) {
-    const float u = rcp_hw(exp2_hw(x * f.a) + 1.f);
-    pr = exp2_hw(__builtin_fmaf(u, -2.f * f.c2, base));
+  if constexpr (CAP != kNoCap) {
+    const float u = f.u_of(x);
+    pr = exp2_hw(CAP == kByU ? __builtin_fmaf(u, -2.f * f.c2, base) : f.any_cap(x, u) + base);
     ds = pr * (dp - delta);
     dx = ds * __builtin_fmaf(-u, u, u);
   } else {
@@ -135,18 +136,20 @@ __device__ __forceinline__ void grad_score(float x, float base, float dp, float 
 // dv alone take 192 or 144 of the 256 that two waves leave each, and the rest does not fit.
 // (Where it does, two waves: 368 us instead of 433 at 96 columns, 275 instead of 333 at
 // 64; 4096 keys, 16 heads.)
-template <int D, bool BIAS>
-constexpr bool kDkvAlone = D > 96 || (D > 64 && BIAS);
+// A large cap's series has no place beside another wave either: 64 to 128 columns went to
+// scratch.
+template <int D, int CAP, bool BIAS>
+constexpr bool kDkvAlone = D > 96 || (D > 64 && BIAS) || CAP == kAnyCap;
 
 // One tile of 64 queries, do's behind q's, for a wave's 32 keys: two blocks of 32
 // queries, of 4 D / 16 matrix instructions and 16 scores a lane each.  A wave that has
 // its SIMD for itself overlaps the two by itself: the second block's scores are
 // multiplied while the first's are worked on, and the first's gradients while the
 // second's are.
-template <int D, bool CAP, bool BIAS>
+template <int D, int CAP, bool BIAS>
 struct DkvTile {
-  static constexpr bool kOverlap = kDkvAlone<D, BIAS>;
-  static constexpr int kG = kBuffers<D, kDkvAlone<D, BIAS>> * kTileBytes<D>;  // from q's tile to do's
+  static constexpr bool kOverlap = kDkvAlone<D, CAP, BIAS>;
+  static constexpr int kG = kBuffers<D, kDkvAlone<D, CAP, BIAS>> * kTileBytes<D>;  // from q's tile to do's
   static constexpr int kC = D / 16, kT = D / 32;
   const AttnParams& p;
   const ScoreFactors& f;
@@ -319,9 +322,9 @@ __device__ __forceinline__ int key_tile(const AttnParams& p, const Place& w, int
 
 // A workgroup owns 128 keys of one key head, 32 to a wave, and walks tiles of
 // 64 queries of the query heads that share it, or of a part of them.
-template <int D, bool CAP, bool BIAS>
+template <int D, int CAP, bool BIAS>
 __device__ __forceinline__ void attn_dkv(const AttnParams& p, const Place& w, char* smem) {
-  constexpr int kBufs = kBuffers<D, kDkvAlone<D, BIAS>>, kTiles = 2 * kBufs;
+  constexpr int kBufs = kBuffers<D, kDkvAlone<D, CAP, BIAS>>, kTiles = 2 * kBufs;
   constexpr int kAhead = (kBufs - 2) * (2 * TileLoad<D>::kLoads + 1);
   constexpr int kStat = 4 * kTile * 4;                 // base, delta, lo, hi of a tile
   // smem: [kBufs] tiles of q, of do
@@ -336,7 +339,7 @@ __device__ __forceinline__ void attn_dkv(const AttnParams& p, const Place& w, ch
   BiasStage bs;                                        // (a bias goes with one head a workgroup)
   if constexpr (BIAS) bs.buckets(p, tid);
   const int j0 = key_tile(p, w, b, reinterpret_cast<int*>(smem), tid,
-                          kDkvAlone<D, BIAS> ? kUnits : 2 * kUnits) * 128;   // its first key
+                          kDkvAlone<D, CAP, BIAS> ? kUnits : 2 * kUnits) * 128;   // its first key
   const int jw = j0 + wave * 32, j = jw + (lane & 31);
   const int* qlo = p.qlo + static_cast<int64_t>(b) * p.tq64;
   const int* qhi = p.qhi + static_cast<int64_t>(b) * p.tq64;
@@ -505,8 +508,8 @@ __device__ __forceinline__ void attn_dkv(const AttnParams& p, const Place& w, ch
     }
 }
 
-template <int D, bool CAP, bool BIAS>
-__global__ __launch_bounds__(kAttnThreads, (kDkvAlone<D, BIAS> ? 1 : 2)) void attn_dkv_kernel(const AttnParams p) {
+template <int D, int CAP, bool BIAS>
+__global__ __launch_bounds__(kAttnThreads, (kDkvAlone<D, CAP, BIAS> ? 1 : 2)) void attn_dkv_kernel(const AttnParams p) {
   extern __shared__ __align__(1024) char smem[];
   attn_dkv<D, CAP, BIAS>(p, place(), smem);
 }
@@ -577,7 +580,7 @@ __device__ __forceinline__ void add_diagonals(const float (&ds)[16], uint32_t mi
 
 // One tile of 64 keys for a wave's 32 queries.  `mine`: the wave's sums of ds by
 // distance, in shared memory; `ends`: of the distances past the reach.
-template <int D, bool CAP, bool BIAS>
+template <int D, int CAP, bool BIAS>
 __device__ __forceinline__ void attn_dq_tile(const AttnParams& p, const FragAt<D>& kt,
                                              const FragAt<D>& vt, const bf16x8 (&qf)[D / 16],
                                              const bf16x8 (&of)[D / 16], f32x16 (&dq)[D / 32],
@@ -644,12 +647,12 @@ __device__ __forceinline__ void attn_dq_tile(const AttnParams& p, const FragAt<D
 // 64 keys.  With the bias, sums of ds by distance are kept per wave in shared
 // memory; blocks that lie past the reach share a bucket and are summed in two
 // registers instead.
-template <int D, bool BIAS>
-constexpr bool kDqAlone = D > 96 && BIAS;
+template <int D, int CAP, bool BIAS>
+constexpr bool kDqAlone = (D > 96 && BIAS) || CAP == kAnyCap;
 
-template <int D, bool CAP, bool BIAS>
+template <int D, int CAP, bool BIAS>
 __device__ __forceinline__ void attn_dq(const AttnParams& p, const Place& w, char* smem) {
-  constexpr int kBufs = kBuffers<D, kDqAlone<D, BIAS>>, kTiles = 2 * kBufs;
+  constexpr int kBufs = kBuffers<D, kDqAlone<D, CAP, BIAS>>, kTiles = 2 * kBufs;
   constexpr int kAhead = (kBufs - 2) * 2 * TileLoad<D>::kLoads;
   // smem: [kBufs] tiles of k, of v
   const uint32_t tiles = lds_address(smem);
@@ -667,7 +670,7 @@ __device__ __forceinline__ void attn_dq(const AttnParams& p, const Place& w, cha
   const int hk = h / p.group;
   BiasStage bs;
   if constexpr (BIAS) bs.buckets(p, tid);
-  const int tile = query_tile(p, w, b, reinterpret_cast<int*>(ranges), tid, kDqAlone<D, BIAS> ? kUnits : 2 * kUnits);
+  const int tile = query_tile(p, w, b, reinterpret_cast<int*>(ranges), tid, kDqAlone<D, CAP, BIAS> ? kUnits : 2 * kUnits);
   const int i0 = tile * 128 + wave * 32;
   const int i = i0 + (lane & 31);
   const ScoreFactors f(p, CAP);
@@ -802,8 +805,8 @@ __device__ __forceinline__ void attn_dq(const AttnParams& p, const Place& w, cha
   }
 }
 
-template <int D, bool CAP, bool BIAS>
-__global__ __launch_bounds__(kAttnThreads, (kDqAlone<D, BIAS> ? 1 : 2)) void attn_dq_kernel(
+template <int D, int CAP, bool BIAS>
+__global__ __launch_bounds__(kAttnThreads, (kDqAlone<D, CAP, BIAS> ? 1 : 2)) void attn_dq_kernel(
     const AttnParams p) {
   extern __shared__ __align__(1024) char smem[];
   attn_dq<D, CAP, BIAS>(p, place(), smem);
@@ -812,7 +815,7 @@ __global__ __launch_bounds__(kAttnThreads, (kDqAlone<D, BIAS> ? 1 : 2)) void att
 // Both in one launch, where both run two workgroups to a compute unit: the second's
 // workgroups fill the places that the last of the first leave (118 us instead of 121:
 // 8 x 1024 tokens, 12 heads of 64, bias).  `kv` and `q`: the two grids.
-template <int D, bool CAP, bool BIAS>
+template <int D, int CAP, bool BIAS>
 __global__ __launch_bounds__(kAttnThreads, 2) void attn_grads_kernel(const AttnParams p, int2 kv, int2 q) {
   extern __shared__ __align__(1024) char smem[];
   const int id = blockIdx.x, behind = id - kv.x * kv.y;
@@ -908,10 +911,10 @@ hipError_t launch_lds(void (*fn)(A...), dim3 grid, size_t lds, hipStream_t s, A.
   return hipGetLastError();
 }
 
-template <int D, bool CAP, bool BIAS>
+template <int D, int CAP, bool BIAS>
 hipError_t run_bwd(const AttnParams& p, hipStream_t s) {
   const size_t n = BIAS ? bias_entries(p.reach) : 0;
-  const size_t dkv_bufs = kBuffers<D, kDkvAlone<D, BIAS>>, dq_bufs = kBuffers<D, kDqAlone<D, BIAS>>;
+  const size_t dkv_bufs = kBuffers<D, kDkvAlone<D, CAP, BIAS>>, dq_bufs = kBuffers<D, kDqAlone<D, CAP, BIAS>>;
   const size_t kv_lds = dkv_bufs * (2 * kTileBytes<D> + 4 * kTile * 4) + n * 4;
   const size_t q_lds = dq_bufs * 2 * kTileBytes<D> + 128 * 8 + 4 * kWaves * 4 +
                        (BIAS ? n + kWaves * (kDiagWords + n) : 0) * sizeof(float);
@@ -921,7 +924,7 @@ hipError_t run_bwd(const AttnParams& p, hipStream_t s) {
   hipError_t e = hipSuccess;
   const int64_t both = static_cast<int64_t>(kv.x) * kv.y + static_cast<int64_t>(q.x) * q.y;
   bool one = false;
-  if constexpr (!kDkvAlone<D, BIAS> && !kDqAlone<D, BIAS>) {
+  if constexpr (!kDkvAlone<D, CAP, BIAS> && !kDqAlone<D, CAP, BIAS>) {
     one = both > 0 && both < (1 << 23);                // (256 threads each, below 2^31)
     if (one)
       e = launch_lds(attn_grads_kernel<D, CAP, BIAS>, dim3(static_cast<unsigned>(both)),
@@ -949,11 +952,18 @@ hipError_t run_bwd(const AttnParams& p, hipStream_t s) {
   return e;
 }
 
+template <int D, int CAP>
+hipError_t pick_bwd(const AttnParams& p, hipStream_t s) {
+  return p.table ? run_bwd<D, CAP, true>(p, s) : run_bwd<D, CAP, false>(p, s);
+}
+
 template <int D>
 hipError_t pick_bwd(const AttnParams& p, hipStream_t s) {
-  if (p.cap > 0.f)
-    return p.table ? run_bwd<D, true, true>(p, s) : run_bwd<D, true, false>(p, s);
-  return p.table ? run_bwd<D, false, true>(p, s) : run_bwd<D, false, false>(p, s);
+  switch (cap_form(p.cap)) {
+    case kNoCap: return pick_bwd<D, kNoCap>(p, s);
+    case kByU: return pick_bwd<D, kByU>(p, s);
+    default: return pick_bwd<D, kAnyCap>(p, s);
+  }
 }
 
 // The workspace, in order; returns its size.

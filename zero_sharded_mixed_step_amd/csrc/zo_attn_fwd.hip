@@ -22,13 +22,14 @@
 namespace zo {
 
 // One tile of 64 keys for a wave's 32 queries.
-template <int D, bool CAP, bool BIAS>
+template <int D, int CAP, bool BIAS>
 __device__ __forceinline__ void attn_fwd_tile(const AttnParams& p, const FragAt<D>& kt,
                                               const FragAt<D>& vt, const bf16x8 (&qf)[D / 16],
                                               f32x16 (&acc)[D / 32], float& m, float& l, int2 rng,
                                               int k0, int i0, const ScoreFactors& f,
                                               const float* bias, int lane) {
-  float s[2][16];                        // x, or u with a cap, or with a bias the score
+  // x; with a cap up to kUCap u; with a larger one, or a bias, the score
+  float s[2][16];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     f32x16 x;
@@ -37,9 +38,17 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnParams& p, const FragAt<
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) x = mfma(frag_rows<D>(kt, t, c), qf[c], x);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) s[t][r] = CAP ? rcp_hw(exp2_hw(x[r] * f.a) + 1.f) : x[r];
+    for (int r = 0; r < 16; ++r) {
+      s[t][r] = CAP != kNoCap ? f.u_of(x[r]) : x[r];
+      if constexpr (CAP == kAnyCap) s[t][r] = f.any_cap(x[r], s[t][r]);
+    }
   }
   if constexpr (BIAS) {
+    const auto add_bias = [&](float x, float c) {
+      return CAP == kByU     ? __builtin_fmaf(x, -2.f * f.c2, f.c2 + c)
+             : CAP == kNoCap ? __builtin_fmaf(x, f.a, c)
+                             : x + c;
+    };
     const int d0 = k0 - (i0 + p.off);    // distances span d0 - 31 .. d0 + 63
     const int side = bias_side(d0 - 31, d0 + kTile - 1, p.reach);
     if (side != 0) {
@@ -48,8 +57,7 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnParams& p, const FragAt<
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          s[t][r] = CAP ? __builtin_fmaf(s[t][r], -2.f * f.c2, f.c2 + c)
-                        : __builtin_fmaf(s[t][r], f.a, c);
+          s[t][r] = add_bias(s[t][r], c);
     } else {
       const float* row = bias + d0 - (lane & 31) + 4 * (lane >> 5) + bias_span(p.reach);
 #pragma unroll
@@ -57,12 +65,12 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnParams& p, const FragAt<
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const float c = row[32 * t + 8 * (r >> 2) + (r & 3)];
-          s[t][r] = CAP ? __builtin_fmaf(s[t][r], -2.f * f.c2, f.c2 + c)
-                        : __builtin_fmaf(s[t][r], f.a, c);
+          s[t][r] = add_bias(s[t][r], c);
         }
     }
   }
-  constexpr bool kU = CAP && !BIAS;      // s holds u: the smallest is the largest score
+  constexpr bool kU = CAP == kByU && !BIAS;   // s holds u: the smallest is the largest score
+  constexpr bool kScore = BIAS || CAP == kAnyCap;
   if (!__all(rng.x <= k0 && rng.y >= k0 + kTile)) {    // not every query sees every key
     const uint32_t n = rng.y - rng.x;
     const int from = k0 + 4 * (lane >> 5) - rng.x;
@@ -81,7 +89,7 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnParams& p, const FragAt<
     for (int r = 0; r < 16; ++r) mx = kU ? fminf(mx, s[t][r]) : fmaxf(mx, s[t][r]);
   if constexpr (kU)
     mx = __builtin_fmaf(mx, -2.f * f.c2, f.c2);
-  else if constexpr (!BIAS)
+  else if constexpr (!kScore)
     mx *= f.a;
   mx = max_halves(mx);
   // The reference of the exponentials moves only when it is 2^8 too low: p, its
@@ -102,7 +110,7 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnParams& p, const FragAt<
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float x = s[g >> 1][8 * (g & 1) + j];
-      if constexpr (BIAS)
+      if constexpr (kScore)
         e[j] = exp2_hw(x - m);
       else
         e[j] = exp2_hw(__builtin_fmaf(x, kU ? -2.f * f.c2 : f.a, shift));
@@ -116,7 +124,7 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnParams& p, const FragAt<
   }
 }
 
-template <int D, bool CAP, bool BIAS, bool SPLIT>
+template <int D, int CAP, bool BIAS, bool SPLIT>
 __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnParams p) {
   constexpr int kRows = 32 * kWaves, kBufs = 2, kTiles = 2 * kBufs;
   constexpr int kAhead = (kBufs - 2) * 2 * TileLoad<D>::kLoads;   // loads of later tiles than the next
@@ -322,7 +330,7 @@ Split choose_split(int B, int Tq, int Tk, int Hq) {
   return {(tiles + each - 1) / each, each};
 }
 
-template <int D, bool CAP, bool BIAS>
+template <int D, int CAP, bool BIAS>
 hipError_t run_fwd(const AttnParams& p, hipStream_t s) {
   const size_t lds = 2 * 2 * kTileBytes<D> + 128 * sizeof(int2) + 2 * kWaves * sizeof(int) +
                      (BIAS ? bias_entries(p.reach) * sizeof(float) : 0);
@@ -349,11 +357,18 @@ hipError_t run_fwd(const AttnParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <int D, int CAP>
+hipError_t pick_fwd(const AttnParams& p, hipStream_t s) {
+  return p.table ? run_fwd<D, CAP, true>(p, s) : run_fwd<D, CAP, false>(p, s);
+}
+
 template <int D>
 hipError_t pick_fwd(const AttnParams& p, hipStream_t s) {
-  if (p.cap > 0.f)
-    return p.table ? run_fwd<D, true, true>(p, s) : run_fwd<D, true, false>(p, s);
-  return p.table ? run_fwd<D, false, true>(p, s) : run_fwd<D, false, false>(p, s);
+  switch (cap_form(p.cap)) {
+    case kNoCap: return pick_fwd<D, kNoCap>(p, s);
+    case kByU: return pick_fwd<D, kByU>(p, s);
+    default: return pick_fwd<D, kAnyCap>(p, s);
+  }
 }
 
 }  // namespace
