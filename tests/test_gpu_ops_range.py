@@ -104,6 +104,33 @@ def test_attention_split_keys_large_cap(zs, torch):
     _attn_check(zs, torch, q, k, v, do, causal=True, cap=1e6)
 
 
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("cap", [1e-10, 1e-40])
+def test_attention_tiny_caps(zs, torch, cap, bias):
+    """Scores that a cap takes to nothing: the softmax of the bias alone; a score of
+    exactly 0 stays one."""
+    q, k, v, do = _attn_inputs(torch, 1, 70, 70, 2, 2, 64, seed=4)
+    q[:, 5] = 0
+    table = buckets = None
+    if bias:
+        table = _rand(torch, _gen(torch, 3), (8, 2), torch.float32)
+        buckets = zs.relpos_buckets(8, 20)
+    dev = lambda t: None if t is None else t.cuda()
+    o, lse, g = _attn(zs, torch, *(dev(t) for t in (q, k, v, do)), dev(table), scale=0.125, cap=cap,
+                      causal=True, bias_buckets=dev(buckets))
+    seen = R.visible(1, 70, 70, causal=True)
+    want = X.Attention(torch.zeros_like(q), k, v, scale=0.125, seen=seen, table=table, buckets=buckets)
+    want_o, bound_o, want_l, bound_l = want.forward()
+    R.check("lse", lse, want_l, bound_l)
+    R.check("o", o, want_o, bound_o)
+    grads = want.backward(o.cpu(), do)
+    R.check("dv", g["dv"], *grads["dv"])
+    if bias:
+        R.check("dtable", g["dtable"], *grads["dtable"])
+    for name in ("dq", "dk"):
+        assert bool(torch.isfinite(g[name]).all()), name
+
+
 # ----------------------------------------------------------- empty batches ---
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

@@ -376,13 +376,14 @@ __host__ __device__ constexpr int cap_form(float cap) {
 // With one, exp(2 y) is exp2(x * a) and the score c2 - 2 c2 u, or, of kAnyCap for small y,
 // x * s times the series.  A negative scale is taken to q, so a > 0:
 // the largest score is that of the largest x, and of the smallest u.  (A scale
-// of 0 becomes one that vanishes beside any score.)
+// of 0 becomes one that vanishes beside any score; the factor of a tiny cap stays finite,
+// so that a score of 0 is one.)
 struct ScoreFactors {
   float a, c2, s;
   bool flip;
   __device__ __forceinline__ ScoreFactors(const AttnParams& p, int cap) {
     s = fmaxf(fabsf(p.scale), 1e-30f) * kLog2e;
-    a = cap ? fmaxf(2.f * s / p.cap, 1e-30f) : s;
+    a = cap ? fminf(fmaxf(2.f * s / p.cap, 1e-30f), 1e30f) : s;
     c2 = cap ? p.cap * kLog2e : 0.f;
     flip = p.scale < 0.f;
   }
