@@ -177,7 +177,8 @@ int zero_attn_ranges(const int32_t *doc, const int32_t *prefix, int B, int T, in
  *   of a tail that is compared with the student's mass outside the entries,
  *   qT = 1 - sum_k q_k (summed over the outside entries, not by difference):
  *   loss[n] = tau^2 w [ sum_k p_k (log p_k - log q_k) + pT (log pT - log qT) ]
- *   stats[n] = { log sum_j exp(z_j / tau),  c },  c = 1 - pT / qT  (1 without a tail)
+ *   stats[n] = { log sum_j exp(z_j / tau),  c },  c = 1 - pT / qT  (1 without a tail),
+ *              or, where c < -2^24, log(pT / qT) in its place (c itself is never above 1)
  *   dlogits  = grad_scale tau w (q_j - p_j) at the entries, grad_scale tau w c q_j
  *              elsewhere
  * with w = row_weight[n] (1 if NULL).  0 log 0 = 0.  Entries with idx outside

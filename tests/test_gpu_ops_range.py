@@ -246,3 +246,52 @@ def test_distill_backward_of_many_rows(zs, torch):
     dz = torch.full((N, V), math.nan, device="cuda")
     zs.zero_distill_bwd(z.cuda(), idx.cuda(), val.cuda(), stats, dz, **kw)
     R.check("dz", dz, *want["dz"])
+
+
+# --------------------------------------------- rows a model is sure of, tails ---
+
+def _distill_check(zs, torch, z, idx, val, tau, tlse, w=None, grad_scale=0.25):
+    """Loss, statistics and gradient, in one pass, from the statistics, and in place."""
+    want = X.distill(z, idx, val, tau, tlse, w, grad_scale)
+    dev = lambda t: None if t is None else t.cuda()
+    N = z.shape[0]
+    zd, di, dv = z.cuda(), idx.cuda(), val.cuda()
+    loss, stats = torch.full((N,), math.nan, device="cuda"), torch.full((N, 2), math.nan, device="cuda")
+    kw = dict(temperature=tau, teacher_lse=dev(tlse), row_weight=dev(w), grad_scale=grad_scale)
+    dz = torch.full_like(zd, math.nan)
+    zs.zero_distill_fwd(zd, di, dv, loss, stats, dlogits=dz, **kw)
+    R.check("loss", loss, *want["loss"])
+    R.check("stats", stats, *want["stats"])
+    R.check("dz", dz, *want["dz"])
+    alone, stats2 = torch.full_like(loss, math.nan), torch.full_like(stats, math.nan)
+    zs.zero_distill_fwd(zd, di, dv, alone, stats2, **kw)
+    assert torch.equal(alone, loss) and torch.equal(stats2, stats)
+    back = torch.full_like(zd, math.nan)
+    zs.zero_distill_bwd(zd, di, dv, stats, back, **kw)
+    R.check("dz from stats", back, *want["dz"])
+    place = zd.clone()
+    zs.zero_distill_bwd(place, di, dv, stats, place, **kw)
+    assert torch.equal(place, back)
+    zs.zero_distill_fwd(zd, di, dv, alone, stats2, dlogits=zd, **kw)
+    assert torch.equal(zd, dz)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,tau", [(40, 1.0), (1000, 2.0), (20011, 1.0), (140003, 1.0)])
+@pytest.mark.parametrize("gap", [10, 14, 60, 95, 110, 300])
+def test_distill_tail_of_a_sure_student(zs, torch, gap, V, tau, dtype):
+    """The teacher's entries lead every other logit by `gap` temperatures, and the teacher
+    leaves a hundredth to the tail: the outside's sum is far below the row's."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    N, K = 5, 8
+    g = _gen(torch, V + gap)
+    z = torch.randn(N, V, generator=g)
+    idx = torch.stack([torch.randperm(V, generator=g)[:K] for _ in range(N)]).to(torch.int32)
+    lead = torch.randn(N, K, generator=g) + gap * tau
+    lead[0] -= gap * tau                                  # an ordinary row among them
+    z.scatter_(1, idx.long(), lead)
+    z[1, ::3] = torch.where(z[1, ::3] > gap * tau / 2, z[1, ::3], -math.inf)   # a masked vocabulary
+    z = z.to(dt)
+    val = torch.randn(N, K, generator=g).to(dt)
+    tlse = (torch.logsumexp(val.double() / tau, 1) - math.log(0.99)).float()
+    _distill_check(zs, torch, z, idx, val, tau, tlse, torch.rand(N, generator=g) + 0.5)
