@@ -278,7 +278,7 @@ def _distill_check(zs, torch, z, idx, val, tau, tlse, w=None, grad_scale=0.25):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("V,tau", [(40, 1.0), (1000, 2.0), (20011, 1.0), (140003, 1.0)])
-@pytest.mark.parametrize("gap", [10, 14, 60, 95, 110, 300])
+@pytest.mark.parametrize("gap", [10, 14, 60, 95, 110, 300, 10000])
 def test_distill_tail_of_a_sure_student(zs, torch, gap, V, tau, dtype):
     """The teacher's entries lead every other logit by `gap` temperatures, and the teacher
     leaves a hundredth to the tail: the outside's sum is far below the row's."""
@@ -295,3 +295,25 @@ def test_distill_tail_of_a_sure_student(zs, torch, gap, V, tau, dtype):
     val = torch.randn(N, K, generator=g).to(dt)
     tlse = (torch.logsumexp(val.double() / tau, 1) - math.log(0.99)).float()
     _distill_check(zs, torch, z, idx, val, tau, tlse, torch.rand(N, generator=g) + 0.5)
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("V", [900, 20011])
+@pytest.mark.parametrize("offset", [1e3, 1e4, -1e4])
+def test_distill_logits_far_from_zero(zs, torch, offset, V, tail):
+    """Only differences of logits count: far from 0 the loss is as near to the formula."""
+    N, K = 6, 12
+    g = _gen(torch, V)
+    z = torch.randn(N, V, generator=g) * 2
+    t = z + torch.randn(N, V, generator=g)
+    val, idx = torch.topk(t, K, dim=1)
+    tlse = torch.logsumexp(t.double() / 1.3, 1).float() if tail else None
+    z = z + offset
+    want = X.distill(z, idx.to(torch.int32), val, 1.3, tlse)
+    loss, stats = torch.empty(N, device="cuda"), torch.empty(N, 2, device="cuda")
+    dz = torch.empty(N, V, device="cuda")
+    zs.zero_distill_fwd(z.cuda(), idx.to(torch.int32).cuda(), val.cuda(), loss, stats, dlogits=dz,
+                        temperature=1.3, teacher_lse=None if tlse is None else tlse.cuda())
+    R.check("loss", loss, *want["loss"])
+    R.check("stats", stats, *want["stats"])
+    R.check("dz", dz, *want["dz"])

@@ -308,7 +308,7 @@ __global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void distill_fwd_kernel(
   if constexpr (CH > 0) keep_packed(held);
 
   // exp((z - m) / tau) = 2^(z k2 - m2), with m2 the rounded m k2: the same in
-  // every term, and what the logarithm of the sum is put together with again
+  // every term, and put right in the logarithm of the sum (see base_of)
   const float m2 = m * k2;
   const auto power = [&](float z) { return exp2_hw(__builtin_fmaf(z, k2, -m2)); };
   const auto marks = [&](int c) {        // of the chunk's elements, the teacher's
@@ -350,7 +350,7 @@ __global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void distill_fwd_kernel(
   // the outside alone, about its own maximum: below the row's its powers, and c, would
   // leave binary32.  (Uniform, and rare: an ordinary row takes one comparison.)
   double mass = 0.0, coef = 1.0, out_mass = outside;
-  float m_out2 = m2;
+  float m_out = m, m_out2 = m2;
   bool sure = false;
   if (p.tail) {
     mass = t.sums[0] < 1.0 ? 1.0 - t.sums[0] : 0.0;
@@ -385,7 +385,8 @@ __global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void distill_fwd_kernel(
     if (lane == 0) sh.top[wave] = mo;
     __syncthreads();
     mo = join_lanes<kW>(sh.top[lane % kW], MaxOp());
-    m_out2 = mo == -kInf ? 0.f : mo * k2;
+    m_out = mo == -kInf ? 0.f : mo;
+    m_out2 = m_out * k2;
     float part_out = 0.f;
     if constexpr (CH > 0) {
 #pragma unroll
@@ -429,12 +430,16 @@ __global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void distill_fwd_kernel(
   // the logarithms come last: in binary64 they take registers that the held row
   // leaves only now
   if (tid == 0) {
-    const double base = static_cast<double>(m2) * 0.6931471805599453;
-    const double lse = base + log(total);
+    // of powers 2^(z k2 - x2) about x: x / tau, less what x2 and k2 were rounded by (k2's
+    // rounding alone moves a sum about 0 by 6e-4 at x / tau = 1e4)
+    const auto base_of = [&](float x, float x2) {
+      return static_cast<double>(x) * p.inv_tau +
+             (static_cast<double>(x2) - static_cast<double>(x) * k2) * 0.6931471805599453;
+    };
+    const double lse = base_of(m, m2) + log(total);
     double loss = t.sums[1] + t.sums[0] * lse;
     if (mass > 0.0) {
-      const double base_out = static_cast<double>(m_out2) * 0.6931471805599453;
-      const double ratio = log(mass) - (base_out + log(out_mass)) + lse;       // of pT / qT
+      const double ratio = log(mass) - (base_of(m_out, m_out2) + log(out_mass)) + lse;   // of pT / qT
       loss += mass * ratio;
       if (sure) coef = ratio;
     }
