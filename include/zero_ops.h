@@ -175,7 +175,9 @@ int zero_attn_ranges(const int32_t *doc, const int32_t *prefix, int B, int T, in
  *   given (the log of the sum of exp(t / tau) over the teacher's whole row),
  *   p_k = exp(t_k / tau - teacher_lse), and what is left of 1 is the mass pT
  *   of a tail that is compared with the student's mass outside the entries,
- *   qT = 1 - sum_k q_k (summed over the outside entries, not by difference):
+ *   qT = 1 - sum_k q_k (summed over the outside entries, not by difference; pT is 0 where
+ *   the entries are all of [0, V), and where qT is 0 and pT no more than the rounding of
+ *   teacher_lse, (1 + |teacher_lse|) 2^-23):
  *   loss[n] = tau^2 w [ sum_k p_k (log p_k - log q_k) + pT (log pT - log qT) ]
  *   stats[n] = { log sum_j exp(z_j / tau),  c },  c = 1 - pT / qT  (1 without a tail),
  *              or, where c < -2^24, log(pT / qT) in its place (c itself is never above 1)

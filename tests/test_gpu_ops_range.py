@@ -297,6 +297,36 @@ def test_distill_tail_of_a_sure_student(zs, torch, gap, V, tau, dtype):
     _distill_check(zs, torch, z, idx, val, tau, tlse, torch.rand(N, generator=g) + 0.5)
 
 
+@pytest.mark.parametrize("V,K", [(1, 1), (5, 5), (6, 9), (300, 300)])
+def test_distill_entries_of_the_whole_vocabulary(zs, torch, V, K):
+    """No token is left for a tail, whatever teacher_lse's rounding leaves of 1."""
+    N = 40
+    g = _gen(torch, V)
+    z = torch.randn(N, V, generator=g) * 2
+    idx = torch.stack([torch.randperm(V, generator=g) for _ in range(N)]).to(torch.int32)
+    idx = torch.nn.functional.pad(idx, (0, K - V), value=-1)
+    val = torch.randn(N, K, generator=g) + 9
+    tlse = torch.logsumexp(val[:, :V].double(), 1).float()
+    _distill_check(zs, torch, z, idx, val, 1.0, tlse)
+
+
+def test_distill_entries_of_all_that_is_allowed(zs, torch):
+    """The vocabulary outside the entries is masked for teacher and student: what
+    teacher_lse's rounding leaves of 1 is no tail; a real one makes the loss infinite."""
+    N, V, K = 40, 500, 30
+    g = _gen(torch, 3)
+    idx = torch.stack([torch.randperm(V, generator=g)[:K] for _ in range(N)]).to(torch.int32)
+    z = torch.full((N, V), -math.inf)
+    z.scatter_(1, idx.long(), torch.randn(N, K, generator=g) * 2)
+    val = torch.randn(N, K, generator=g) + 9
+    tlse = torch.logsumexp(val.double(), 1).float()
+    assert bool((torch.exp(val.double() - tlse.double()[:, None]).sum(1) < 1).any())
+    _distill_check(zs, torch, z, idx, val, 1.0, tlse)
+    loss, stats = torch.empty(N, device="cuda"), torch.empty(N, 2, device="cuda")
+    zs.zero_distill_fwd(z.cuda(), idx.cuda(), val.cuda(), loss, stats, teacher_lse=(tlse + 0.1).cuda())
+    assert bool((loss == math.inf).all())
+
+
 @pytest.mark.parametrize("tail", [False, True])
 @pytest.mark.parametrize("V", [900, 20011])
 @pytest.mark.parametrize("offset", [1e3, 1e4, -1e4])

@@ -152,14 +152,14 @@ struct Teacher {
   float* p;
   float* z;
   int* idx;
-  double* sums;  // mass: sum of p; cross: sum of p (log p - z / tau); any entry
+  double* sums;  // mass: sum of p; cross: sum of p (log p - z / tau); how many entries
 };
 
 template <typename E>
 __device__ __forceinline__ void load_teacher(const DistillParams& p, int64_t n, const E* z,
                                              int64_t from, int64_t to, int lane, const Teacher& t) {
   float mx = -kInf;
-  int any = 0;
+  int entries = 0;
   for (int k = lane; k < p.K; k += 64) {
     const int i = p.idx[n * p.K + k];
     const bool ok = i >= 0 && i < p.V;
@@ -167,7 +167,7 @@ __device__ __forceinline__ void load_teacher(const DistillParams& p, int64_t n, 
     t.z[k] = ok && i >= from && i < to ? static_cast<float>(z[i]) : 0.f;
     const float v = ok ? value<E>(p.val, n * p.K + k) : -kInf;
     t.p[k] = v;
-    any |= ok;
+    entries += ok;
     mx = MaxOp()(mx, v);
   }
   double base;
@@ -194,11 +194,11 @@ __device__ __forceinline__ void load_teacher(const DistillParams& p, int64_t n, 
   }
   mass = join_lanes<64>(mass, AddOp());
   cross = join_lanes<64>(cross, AddOp());
-  any = __any(any) != 0;
+  entries = join_lanes<64>(entries, AddOp());
   if (lane == 0) {
     t.sums[0] = mass;
     t.sums[1] = cross;
-    t.sums[2] = any ? 1.0 : 0.0;
+    t.sums[2] = entries;
   }
 }
 
@@ -353,7 +353,8 @@ __global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void distill_fwd_kernel(
   float m_out = m, m_out2 = m2;
   bool sure = false;
   if (p.tail) {
-    mass = t.sums[0] < 1.0 ? 1.0 - t.sums[0] : 0.0;
+    // (no token is left for a tail where the entries are the whole vocabulary)
+    mass = t.sums[0] < 1.0 && t.sums[2] < static_cast<double>(p.V) ? 1.0 - t.sums[0] : 0.0;
     if (mass > 0.0) coef = 1.0 - mass * (total / outside);
     sure = coef < -kMostC;
   }
@@ -399,6 +400,14 @@ __global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void distill_fwd_kernel(
     if (lane == 0) sh.sum[wave] = wave_out;
     __syncthreads();
     out_mass = join_lanes<kW>(sh.sum[lane % kW], AddOp());
+    if (out_mass == 0.0 && mass <= (1.0 + fabs(static_cast<double>(p.tlse[n]))) * 0x1p-23) {
+      // the student's vocabulary ends with the entries, and so does the teacher's but for
+      // its logarithm's rounding
+      sure = false;
+      mass = 0.0;
+      coef = 1.0;
+      m_out2 = m2;
+    }
   }
   // a row without weight, or with nothing to be compared with: statistics only
   const bool live = w != 0.f && (t.sums[2] != 0.0 || p.tail);
