@@ -155,6 +155,64 @@ def test_attention_bias_gradient_of_an_empty_batch(zs, torch, B, Tq, Tk, dtype):
 
 # ----------------------------------------------- masked places, sure masks ---
 
+@pytest.mark.parametrize("D", [64, 96, 128])
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_attention_infinite_bias_in_masked_places(zs, torch, D, cap):
+    """A causal mask leaves no key ahead of its query: what the bias says there, +inf or NaN,
+    has no part in either direction."""
+    T = 200
+    q, k, v, do = _attn_inputs(torch, 1, T, T, 2, 2, D, seed=D)
+    g = _gen(torch, 6)
+    table = _rand(torch, g, (4, 2), torch.float32)
+    buckets = torch.tensor([1, 1, 2, 2, 0, 3, 3, 3, 3], dtype=torch.int32)     # 3: ahead
+    clean = table.clone()
+    clean[3] = 0
+    seen = R.visible(1, T, T, causal=True)
+    want = X.Attention(q, k, v, scale=D ** -0.5, cap=cap, seen=seen, table=clean, buckets=buckets)
+    for value in (math.inf, -math.inf, math.nan):
+        table[3] = value
+        o, lse, got = _attn(zs, torch, q.cuda(), k.cuda(), v.cuda(), do.cuda(), table.cuda(),
+                            scale=D ** -0.5, cap=cap, causal=True, bias_buckets=buckets.cuda())
+        want_o, bound_o, want_l, bound_l = want.forward()
+        R.check("lse", lse, want_l, bound_l)
+        R.check("o", o, want_o, bound_o)
+        grads = want.backward(o.cpu(), do)
+        for name in ("dv", "dk", "dq", "dtable"):
+            R.check(name, got[name], *grads[name])
+
+
+@pytest.mark.parametrize("D", [64, 96, 128])
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_attention_products_past_binary32_in_masked_places(zs, torch, D, cap):
+    """Documents whose products overflow with each other's rows, but not with their
+    own: q . k, do . v of masked pairs."""
+    T, cut = 190, 70
+    q, k, v, do = _attn_inputs(torch, 1, T, T, 2, 2, D, seed=D + 1)
+    big = 2.0 ** 66
+    # document 0: small q and do, large k and v; document 1 the other way round
+    for x, y in ((q, k), (do, v)):
+        x[:, :cut] /= big
+        y[:, :cut] *= big
+        x[:, cut:] *= big
+        y[:, cut:] /= big
+    doc = torch.zeros((1, T), dtype=torch.int32)
+    doc[:, cut:] = 1
+    ranges = R.doc_ranges(doc)
+    seen = R.visible(1, T, T, ranges)
+    o, lse, got = _attn(zs, torch, q.cuda(), k.cuda(), v.cuda(), do.cuda(), scale=D ** -0.5, cap=cap,
+                        ranges=ranges.cuda())
+    # (bounds a document at a time: theirs are of unlike size)
+    for lo, hi in ((0, cut), (cut, T)):
+        one = [x[:, lo:hi] for x in (q, k, v, do)]
+        part = X.Attention(*one[:3], scale=D ** -0.5, cap=cap, seen=seen[:, lo:hi, lo:hi])
+        want_o, bound_o, want_l, bound_l = part.forward()
+        R.check("lse", lse[:, :, lo:hi], want_l, bound_l)
+        R.check("o", o[:, lo:hi], want_o, bound_o)
+        grads = part.backward(o.cpu()[:, lo:hi], one[3])
+        for name in ("dv", "dk", "dq"):
+            R.check(name, got[name][:, lo:hi], *grads[name])
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("value", ["lowest", "-inf"])
 def test_attention_backward_of_masking_biases(zs, torch, D, value):

@@ -111,21 +111,21 @@ __global__ __launch_bounds__(256) void attn_bwd_prepare_kernel(const AttnParams 
   }
 }
 
-// One score's p, ds and dx, from the raw product x, dp, and base = bias - lse (in log2,
+// One score's p, ds and dx, from the raw product x, dp - delta, and base = bias - lse (in log2,
 // plus c2 with a cap up to kUCap).  With a cap, u = (1 - tanh) / 2 and dx is a quarter of ds
 // (1 - tanh^2) = 4 ds u (1 - u): the 4 goes into the gradients' final scale.
 template <int CAP>
-__device__ __forceinline__ void grad_score(float x, float base, float dp, float delta,
+__device__ __forceinline__ void grad_score(float x, float base, float dp_delta,
                                            const ScoreFactors& f, float& pr, float& ds,
                                            float& dx) {
   if constexpr (CAP != kNoCap) {
     const float u = f.u_of(x);
     pr = exp2_hw(CAP == kByU ? __builtin_fmaf(u, -2.f * f.c2, base) : f.any_cap(x, u) + base);
-    ds = pr * (dp - delta);
+    ds = pr * dp_delta;
     dx = ds * __builtin_fmaf(-u, u, u);
   } else {
     pr = exp2_hw(__builtin_fmaf(x, f.a, base));
-    ds = pr * (dp - delta);
+    ds = pr * dp_delta;
     dx = ds;
   }
 }
@@ -222,23 +222,27 @@ struct DkvTile {
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         const int at = 32 * s + 16 * u + 8 * g;
-        f32x4 base4 = quad(0, at);
-        const f32x4 del = quad(1, at);
+        const f32x4 base4 = quad(0, at), del = quad(1, at);
+        bool out[4] = {};
         if (!FULL) {
           const f32x4 lo = quad(2, at), hi = quad(3, at);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int out = static_cast<int>(j < __float_as_int(lo[e])) |
-                            static_cast<int>(j >= __float_as_int(hi[e]));
-            base4[e] = out ? -kInf : base4[e];         // p = 0
-          }
+          for (int e = 0; e < 4; ++e)
+            out[e] = static_cast<int>(j < __float_as_int(lo[e])) |
+                     static_cast<int>(j >= __float_as_int(hi[e]));
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int n = 4 * g + e, r = 8 * u + n;
           float base = base4[e], ds;
           if constexpr (BIAS) base += side != 0 ? end : row[-(16 * u + 8 * g + e)];
-          grad_score<CAP>(k.x[r], base, k.dp[r], del[e], f, pr[n], ds, dx[n]);
+          float x = k.x[r], dp_delta = k.dp[r] - del[e];
+          if (!FULL) {                                 // p = 0, whatever these are
+            base = out[e] ? -kInf : base;
+            x = out[e] ? 0.f : x;
+            dp_delta = out[e] ? 0.f : dp_delta;
+          }
+          grad_score<CAP>(x, base, dp_delta, f, pr[n], ds, dx[n]);
         }
       }
       k.pf[u] = to_frag(pr);
@@ -612,14 +616,16 @@ __device__ __forceinline__ void attn_dq_tile(const AttnParams& p, const FragAt<D
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const uint32_t j = first + 8 * (r >> 2) + (r & 3);
-        base[r] = j < n ? base[r] : -kInf;               // p = 0
+        base[r] = j < n ? base[r] : -kInf;               // p = 0, whatever x and dp are
+        x[r] = j < n ? x[r] : 0.f;
+        dp[r] = j < n ? dp[r] : delta;
       }
     }
     float dx[16], ds[16];
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       float pr;
-      grad_score<CAP>(x[r], base[r], dp[r], delta, f, pr, ds[r], dx[r]);
+      grad_score<CAP>(x[r], base[r], dp[r] - delta, f, pr, ds[r], dx[r]);
     }
     float all = 0.f;
     if constexpr (BIAS) {
