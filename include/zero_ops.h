@@ -121,7 +121,10 @@ size_t zero_qk_norm_rope_workspace_bytes(int64_t T, int D);
  *   dbias_table[bucket][h] = sum of ds over batch, queries and keys,
  *   dx = ds (1 - (c/cap)^2), dq_i = scale sum_j dx k_j,
  *   dk_j = scale sum_i dx q_i, dv_j = sum_i p do_i,
- * dk and dv summed over the Hq / Hk query heads that share a key head.
+ * dk and dv summed over the Hq / Hk query heads that share a key head.  A query whose lse is
+ * below -2^24 (every key that it sees has a bias of -1e9, say, or of the type's lowest value) takes
+ * no part, as one that sees no key: its lse has no place for the log of the sum, and without it
+ * p cannot be formed.  (Forward, its softmax is that of its scores in binary32.)
  *
  * q, k, v, o and their gradients are bf16; p and dx are rounded to bf16 for
  * the matrix products (their sums stay binary32).  D is 32, 64, 96 or 128;

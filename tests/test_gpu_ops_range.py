@@ -240,6 +240,37 @@ def test_attention_backward_of_masking_biases(zs, torch, D, value):
     assert bool((got["dtable"][3] == 0).all())
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("value", ["lowest", -1e9, -1e20])
+def test_attention_rows_with_no_normaliser_left(zs, torch, D, value):
+    """Queries of which every key has a bias of the type's lowest value or -1e9: their lse
+    has no room for the log of a sum, and the backward pass takes them as queries
+    that see nothing.  The others' gradients are as without them."""
+    T = 150
+    q, k, v, do = _attn_inputs(torch, 1, T, T, 2, 2, D, seed=D + 3)
+    low = torch.finfo(torch.bfloat16).min if value == "lowest" else value
+    table = _rand(torch, _gen(torch, 6), (3, 2), torch.bfloat16)
+    table[0] = low
+    buckets = torch.tensor([1, 2, 0, 1, 1], dtype=torch.int32)                 # 0: the query's own key
+    seen = R.visible(1, T, T, causal=True)
+    o, lse, got = _attn(zs, torch, q.cuda(), k.cuda(), v.cuda(), do.cuda(), table.cuda(),
+                        scale=D ** -0.5, causal=True, bias_buckets=buckets.cuda())
+    # the first query sees its own key alone; the others see what is behind them
+    R.check("first", o[:, :1], v[:, :1].double(), R.BF * v[:, :1].double().abs())
+    strict = seen & ~torch.eye(T, dtype=torch.bool)[None]
+    want = X.Attention(q, k, v, scale=D ** -0.5, seen=strict, table=torch.where(
+        torch.arange(3)[:, None] == 0, 0.0, table.float()), buckets=buckets)
+    want_o, bound_o, want_l, bound_l = want.forward()
+    R.check("o", o[:, 1:], want_o[:, 1:], bound_o[:, 1:])
+    R.check("lse", lse[:, :, 1:], want_l[:, :, 1:], bound_l[:, :, 1:])
+    grads = want.backward(o.cpu(), do)
+    for name in ("dv", "dk", "dq"):
+        R.check(name, got[name], *grads[name])
+    val, bound = grads["dtable"]
+    R.check("dtable", got["dtable"][1:], val[1:], bound[1:])
+    assert bool((got["dtable"][0] == 0).all())
+
+
 # ------------------------------------------- paths that larger shapes take ---
 
 @pytest.mark.parametrize("B,T,Hq,Hk,D,cap", [

@@ -27,6 +27,10 @@ __device__ __forceinline__ uint64_t bits_below(int n) {
   return n <= 0 ? 0 : n >= 64 ? ~uint64_t(0) : (uint64_t(1) << n) - 1;
 }
 
+// A row's lse from which on down the row takes no part: every key that it sees has a bias
+// that masks it.
+constexpr float kLseLost = -16777216.f;
+
 // What sees a tile of 128 keys (p.tile), by a workgroup.
 __device__ __forceinline__ void key_tile_words(const AttnParams& p, int b, int t, int tid) {
   __shared__ int words[kWaves][kTileWords];
@@ -102,8 +106,10 @@ __global__ __launch_bounds__(256) void attn_bwd_prepare_kernel(const AttnParams 
     p.delta[row] = sum;
     float lse = -kInf;
     if (r.y > r.x) lse = p.lse[static_cast<int64_t>(bh) * p.Tq + i];
-    p.base[row] =
-        lse != -kInf ? (cap_form(p.cap) == kByU ? p.cap * kLog2e : 0.f) - lse * kLog2e : -kInf;
+    // (below kLseLost binary32 has no place for the log of a sum beside the scores: exp(s - lse)
+    // would be any power of 2^64)
+    p.base[row] = lse < kLseLost ? -kInf
+                                 : (cap_form(p.cap) == kByU ? p.cap * kLog2e : 0.f) - lse * kLog2e;
     if (h == 0) {
       p.qlo[static_cast<int64_t>(b) * p.tq64 + i] = r.x;
       p.qhi[static_cast<int64_t>(b) * p.tq64 + i] = r.y;
