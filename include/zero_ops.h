@@ -14,7 +14,8 @@
  *
  * Conventions, as in zero_step.h:
  *   - Status codes are those of zero_step.h.  Every argument is checked
- *     before anything is launched; no C++ exception escapes.
+ *     before anything is launched; no C++ exception escapes.  Numbers that
+ *     binary32 does not hold (scale, eps, grad_scale) are ZERO_EINVAL.
  *   - `stream` is a hipStream_t.  All work is enqueued on it, on the device
  *     that is current; nothing is allocated, copied to the host or
  *     synchronised, and no state outlives a call, so every call can be
@@ -194,7 +195,7 @@ int zero_attn_ranges(const int32_t *doc, const int32_t *prefix, int B, int T, in
  * zero_distill_fwd writes loss and stats, and dlogits too if given (one read
  * of the logits for all three); zero_distill_bwd writes dlogits from stats.
  * dlogits may be the logits themselves (same stride).  dtype is that of
- * logits, t and dlogits. K <= ZERO_DISTILL_MAX_K, V <= ZERO_DISTILL_MAX_V;
+ * logits, t and dlogits. 1e-30 <= tau <= 1e30, K <= ZERO_DISTILL_MAX_K, V <= ZERO_DISTILL_MAX_V;
  * logits and t may start at any element. */
 typedef struct zero_distill_args {
   size_t struct_bytes;          /* sizeof(zero_distill_args) */

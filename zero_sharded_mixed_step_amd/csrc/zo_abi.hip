@@ -3,6 +3,7 @@
 // exception crosses this boundary.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -39,14 +40,15 @@ int check_rows(const void* p, const int64_t* stride, int n, int elem_bytes) {
     if (rc_ != ZERO_OK) return rc_; \
   } while (0)
 
-bool positive_finite(double x) { return std::isfinite(x) && x > 0.0; }
+// Numbers that the kernels take in binary32.
+bool fits_f32(double x) { return std::fabs(x) <= FLT_MAX; }
 
 // ------------------------------------------------------------------- norm ---
 
 int check_norm(const zero_qk_norm_rope_args* a, bool fwd) {
   if (a == nullptr || a->struct_bytes != sizeof(*a)) return ZERO_EINVAL;
   if (a->dtype != ZERO_BF16 && a->dtype != ZERO_F32) return ZERO_EINVAL;
-  if (a->T < 0 || a->Hq < 0 || a->Hk < 0 || !(a->eps >= 0.0) || !std::isfinite(a->eps))
+  if (a->T < 0 || a->Hq < 0 || a->Hk < 0 || !(a->eps >= 0.0) || !fits_f32(a->eps))
     return ZERO_EINVAL;
   if (a->D < 8 || a->D > 256 || a->D % 8 != 0) return ZERO_ESIZE;
   if (a->rot_dim < 0 || a->rot_dim > a->D || a->rot_dim % (a->interleaved ? 8 : 16) != 0)
@@ -104,7 +106,7 @@ int check_attn(const zero_attn_args* a, bool fwd) {
   if (a == nullptr || a->struct_bytes != sizeof(*a)) return ZERO_EINVAL;
   ZO_CHECK(check_attn_sizes(a->B, a->Tq, a->Tk, a->Hq, a->Hk, a->D));
   if (!fwd && a->Tk > kMaxLen) return ZERO_ESIZE;
-  if (!std::isfinite(a->scale) || !std::isfinite(a->cap) || a->cap < 0.0) return ZERO_EINVAL;
+  if (!fits_f32(a->scale) || !std::isfinite(a->cap) || a->cap < 0.0) return ZERO_EINVAL;
   if (a->cap != 0.0 && !(static_cast<float>(a->cap) > 0.f && a->cap <= 1e30)) return ZERO_EINVAL;
   if (a->bias_table != nullptr) {
     if (a->bias_buckets == nullptr || a->n_buckets < 1 || a->reach < 0) return ZERO_EINVAL;
@@ -157,8 +159,7 @@ int check_distill(const zero_distill_args* a, bool fwd) {
   if (a->N < 0 || a->V < 1 || a->K < 1) return ZERO_EINVAL;
   if (a->N > kMaxRows || a->V > ZERO_DISTILL_MAX_V || a->K > ZERO_DISTILL_MAX_K)
     return ZERO_ESIZE;
-  if (!positive_finite(a->temperature) || !positive_finite(1.0 / a->temperature) ||
-      !std::isfinite(a->grad_scale))
+  if (!(a->temperature >= 1e-30 && a->temperature <= 1e30) || !fits_f32(a->grad_scale))
     return ZERO_EINVAL;
   if (a->N == 0) return ZERO_OK;
   if (!a->logits || !a->teacher_idx || !a->teacher_val || !a->stats) return ZERO_EINVAL;
