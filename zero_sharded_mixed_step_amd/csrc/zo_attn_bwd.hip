@@ -243,7 +243,10 @@ struct DkvTile {
           float base = base4[e], ds;
           if constexpr (BIAS) base += side != 0 ? end : row[-(16 * u + 8 * g + e)];
           float x = k.x[r], dp_delta = k.dp[r] - del[e];
-          if (!FULL) {                                 // p = 0, whatever these are
+          // p = 0, whatever score and dp are.  (Three selections before the exponentials and not
+          // two behind them, for which the comparisons' results would wait in registers: 465 us
+          // instead of 479, 4001 keys, 32 on 8 heads of 128, cap, prefixes.)
+          if (!FULL) {
             base = out[e] ? -kInf : base;
             x = out[e] ? 0.f : x;
             dp_delta = out[e] ? 0.f : dp_delta;
@@ -826,11 +829,13 @@ __global__ __launch_bounds__(kAttnThreads, (kDqAlone<D, CAP, BIAS> ? 1 : 2)) voi
 
 // Both in one launch, where both run two workgroups to a compute unit: the second's
 // workgroups fill the places that the last of the first leave (118 us instead of 121:
-// 8 x 1024 tokens, 12 heads of 64, bias).  `kv` and `q`: the two grids.
+// 8 x 1024 tokens, 12 heads of 64, bias).  `kv` and `q`: the two grids, of which the launch
+// takes the workgroups from `first` on.
 template <int D, int CAP, bool BIAS>
-__global__ __launch_bounds__(kAttnThreads, 2) void attn_grads_kernel(const AttnParams p, int2 kv, int2 q) {
+__global__ __launch_bounds__(kAttnThreads, 2) void attn_grads_kernel(const AttnParams p, int2 kv, int2 q,
+                                                                    int first) {
   extern __shared__ __align__(1024) char smem[];
-  const int id = blockIdx.x, behind = id - kv.x * kv.y;
+  const int id = first + blockIdx.x, behind = id - kv.x * kv.y;
   if (behind < 0)
     attn_dkv<D, CAP, BIAS>(p, Place{id % kv.x, id / kv.x, kv.x, kv.y}, smem);
   else
@@ -934,18 +939,18 @@ hipError_t run_bwd(const AttnParams& p, hipStream_t s) {
   const int2 kv = make_int2(p.B * p.Hk * p.parts, (p.Tk + 127) / 128);
   const int2 q = make_int2(p.B * p.Hq, tiles);
   hipError_t e = hipSuccess;
-  const int64_t both = static_cast<int64_t>(kv.x) * kv.y + static_cast<int64_t>(q.x) * q.y;
-  bool one = false;
-  if constexpr (!kDkvAlone<D, CAP, BIAS> && !kDqAlone<D, CAP, BIAS>) {
-    one = both > 0 && both < (1 << 23);                // (256 threads each, below 2^31)
-    if (one)
-      e = launch_lds(attn_grads_kernel<D, CAP, BIAS>, dim3(static_cast<unsigned>(both)),
-                     kv_lds > q_lds ? kv_lds : q_lds, s, p, kv, q);
-  }
-  if (!one) {
+  if constexpr (kDkvAlone<D, CAP, BIAS> || kDqAlone<D, CAP, BIAS>) {
     if (kv.x > 0 && kv.y > 0) e = launch_lds(attn_dkv_kernel<D, CAP, BIAS>, dim3(kv.x, kv.y), kv_lds, s, p);
     if (e != hipSuccess) return e;
     if (q.x > 0 && q.y > 0) e = launch_lds(attn_dq_kernel<D, CAP, BIAS>, dim3(q.x, q.y), q_lds, s, p);
+  } else {
+    const int64_t both = static_cast<int64_t>(kv.x) * kv.y + static_cast<int64_t>(q.x) * q.y;
+    constexpr int64_t kMost = 1 << 23;                 // (256 threads each, below 2^32)
+    if (both > 0x7FFFFFFF) return hipErrorInvalidConfiguration;      // (hundreds of GiB of rows)
+    for (int64_t first = 0; first < both && e == hipSuccess; first += kMost)
+      e = launch_lds(attn_grads_kernel<D, CAP, BIAS>,
+                     dim3(static_cast<unsigned>(both - first < kMost ? both - first : kMost)),
+                     kv_lds > q_lds ? kv_lds : q_lds, s, p, kv, q, static_cast<int>(first));
   }
   if (e != hipSuccess) return e;
   if (p.parts > 1 && kv.x > 0 && kv.y > 0) {
