@@ -27,7 +27,8 @@
  *   - Sums, softmax statistics and norms are binary32 or wider; each output
  *     element is rounded once.  Every sum has a fixed order and no atomics are
  *     used, so the same call gives the same bits every time on one device.
- *   - Outputs must not overlap inputs unless stated.
+ *   - Outputs must not overlap inputs unless stated (where the same address
+ *     is allowed, other strides are ZERO_EINVAL).
  */
 #ifndef ZERO_OPS_H
 #define ZERO_OPS_H

@@ -46,3 +46,20 @@ def test_numbers_past_binary32(lib):  # noqa: F811
                        dict(temperature=1e300), dict(grad_scale=1e39), dict(grad_scale=-1e300),
                        dict(grad_scale=math.nan)):
             assert _distill().call(fn, **change) == EINVAL, change
+
+
+def test_in_place_with_other_strides(lib):  # noqa: F811
+    """An output that is its input has to be laid out as it is: with other strides rows
+    would be written before they are read."""
+    same, wide = [128, 64], [256, 64]
+    f, b = lib.zero_qk_norm_rope_fwd, lib.zero_qk_norm_rope_bwd
+    for fn, x, y in ((f, "q", "yq"), (f, "k", "yk"), (b, "dyq", "dq"), (b, "dyk", "dk")):
+        for strides in ((wide, same), (same, wide)):
+            a = _norm(Hk=2, **{x: FAKE, y: FAKE, x + "_stride": strides[0], y + "_stride": strides[1]})
+            assert a.call(fn) == EINVAL, (x, y)
+        a = _norm(Hk=2, **{x: FAKE, y: FAKE, x + "_stride": [512, 64], y + "_stride": [512, 128]})
+        assert a.call(fn) == EINVAL, (x, y)
+    for fn in (lib.zero_distill_fwd, lib.zero_distill_bwd):
+        for strides in ((128, 100), (100, 128)):
+            assert _distill(dlogits=FAKE, logits_stride=strides[0],
+                            dlogits_stride=strides[1]).call(fn) == EINVAL

@@ -34,6 +34,12 @@ int check_rows(const void* p, const int64_t* stride, int n, int elem_bytes) {
   return ZERO_OK;
 }
 
+// An output y that is its input x: rows have to be written where they were read.
+int check_in_place(const void* x, const int64_t* xs, const void* y, const int64_t* ys, int64_t T,
+                   int64_t H) {
+  return x == y && ((T > 1 && xs[0] != ys[0]) || (H > 1 && xs[1] != ys[1])) ? ZERO_EINVAL : ZERO_OK;
+}
+
 #define ZO_CHECK(expr)              \
   do {                              \
     const int rc_ = (expr);         \
@@ -64,10 +70,12 @@ int check_norm(const zero_qk_norm_rope_args* a, bool fwd) {
     if (a->T > 0 && a->Hq > 0) {
       ZO_CHECK(check_rows(a->q, a->q_stride, 2, eb));
       ZO_CHECK(check_rows(a->yq, a->yq_stride, 2, eb));
+      ZO_CHECK(check_in_place(a->q, a->q_stride, a->yq, a->yq_stride, a->T, a->Hq));
     }
     if (a->T > 0 && a->Hk > 0) {
       ZO_CHECK(check_rows(a->k, a->k_stride, 2, eb));
       ZO_CHECK(check_rows(a->yk, a->yk_stride, 2, eb));
+      ZO_CHECK(check_in_place(a->k, a->k_stride, a->yk, a->yk_stride, a->T, a->Hk));
     }
     return ZERO_OK;
   }
@@ -75,11 +83,13 @@ int check_norm(const zero_qk_norm_rope_args* a, bool fwd) {
     ZO_CHECK(check_rows(a->q, a->q_stride, 2, eb));
     ZO_CHECK(check_rows(a->dyq, a->dyq_stride, 2, eb));
     ZO_CHECK(check_rows(a->dq, a->dq_stride, 2, eb));
+    ZO_CHECK(check_in_place(a->dyq, a->dyq_stride, a->dq, a->dq_stride, a->T, a->Hq));
   }
   if (a->T > 0 && a->Hk > 0) {
     ZO_CHECK(check_rows(a->k, a->k_stride, 2, eb));
     ZO_CHECK(check_rows(a->dyk, a->dyk_stride, 2, eb));
     ZO_CHECK(check_rows(a->dk, a->dk_stride, 2, eb));
+    ZO_CHECK(check_in_place(a->dyk, a->dyk_stride, a->dk, a->dk_stride, a->T, a->Hk));
   }
   if ((a->dwq && !a->wq) || (a->dwk && !a->wk)) return ZERO_EINVAL;
   if ((a->dwq && !aligned(a->dwq, eb)) || (a->dwk && !aligned(a->dwk, eb))) return ZERO_EALIGN;
@@ -170,6 +180,8 @@ int check_distill(const zero_distill_args* a, bool fwd) {
       !aligned(a->teacher_lse, 4) || !aligned(a->row_weight, 4))
     return ZERO_EALIGN;
   if (a->dlogits && a->dlogits_stride < a->V && a->N > 1) return ZERO_EINVAL;
+  if (a->dlogits == a->logits && a->dlogits_stride != a->logits_stride && a->N > 1)
+    return ZERO_EINVAL;
   return ZERO_OK;
 }
 
@@ -184,7 +196,7 @@ const char* zero_ops_strerror(int status) {
     case ZERO_OK: return "ok";
     case ZERO_EINVAL:
       return "invalid argument (null pointer, struct size, dtype, head counts, scale, cap, "
-             "temperature, bias map or missing workspace)";
+             "temperature, bias map, in place with other strides or missing workspace)";
     case ZERO_EALIGN:
       return "pointer or stride misaligned (head rows and workspaces need 16 bytes, ranges 8, "
              "other arrays their element)";
