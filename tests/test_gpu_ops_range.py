@@ -318,6 +318,30 @@ def test_attention_cap_and_bias(zs, torch, D, Hq, Hk):
                 buckets=zs.relpos_buckets(16, 40))
 
 
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (0.0, True), (8.0, False), (500.0, True)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_scales_of_any_sign(zs, torch, D, cap, bias):
+    """A negative scale, which is a positive one of -q (whose bounds count the scale's
+    size), and one of 0 (the softmax of the bias alone)."""
+    q, k, v, do = _attn_inputs(torch, 1, 130, 130, 4, 2, D, seed=D + 5)
+    table = buckets = None
+    if bias:
+        table = _rand(torch, _gen(torch, 3), (8, 4), torch.float32)
+        buckets = zs.relpos_buckets(8, 20, bidirectional=True)
+    dev = lambda t: None if t is None else t.cuda()
+    o, lse, g = _attn(zs, torch, *(dev(t) for t in (q, k, v, do)), dev(table), scale=-D ** -0.5, cap=cap,
+                      bias_buckets=dev(buckets))
+    want = X.Attention(-q, k, v, scale=D ** -0.5, cap=cap, seen=R.visible(1, 130, 130), table=table,
+                       buckets=buckets)
+    want_o, bound_o, want_l, bound_l = want.forward()
+    R.check("lse", lse, want_l, bound_l)
+    R.check("o", o, want_o, bound_o)
+    grads = want.backward(o.cpu(), do)
+    for name, got in g.items():
+        R.check(name, -got if name == "dq" else got, *grads[name])
+    _attn_check(zs, torch, q, k, v, do, scale=0.0, cap=cap, table=table, buckets=buckets)
+
+
 def test_distill_backward_of_many_rows(zs, torch):
     """More rows than one launch takes."""
     N, V, K = 65535 + 70, 24, 3
@@ -436,3 +460,15 @@ def test_distill_logits_far_from_zero(zs, torch, offset, V, tail):
     R.check("loss", loss, *want["loss"])
     R.check("stats", stats, *want["stats"])
     R.check("dz", dz, *want["dz"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_distill_longest_row_with_most_entries(zs, torch, dtype):
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    N, V, K = 2, zs._ops_binding.DISTILL_MAX_V, zs._ops_binding.DISTILL_MAX_K
+    g = _gen(torch, 9)
+    z = (torch.randn(N, V, generator=g) * 2).to(dt)
+    t = z.float() + torch.randn(N, V, generator=g)
+    val, idx = torch.topk(t, K, dim=1)
+    tlse = torch.logsumexp(t.double(), 1).float()
+    _distill_check(zs, torch, z, idx.to(torch.int32), val.to(dt), 1.0, tlse)
