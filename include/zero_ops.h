@@ -25,8 +25,9 @@
  *   - Strides are in elements; the innermost dimension (the head's D values,
  *     a row's V logits) is contiguous.  Addressing is 64-bit.
  *   - Sums, softmax statistics and norms are binary32 or wider; each output
- *     element is rounded once.  Every sum has a fixed order and no atomics are
- *     used, so the same call gives the same bits every time on one device.
+ *     element is rounded once.  Every sum has a fixed order (the only atomics
+ *     set bits in shared memory), so the same call gives the same bits every
+ *     time on one device.
  *   - Outputs must not overlap inputs unless stated (where the same address
  *     is allowed, other strides are ZERO_EINVAL).
  */
@@ -116,7 +117,8 @@ size_t zero_qk_norm_rope_workspace_bytes(int64_t T, int D);
  * anything, NaN and infinities too: they are read as 0.  Masked scores are selected
  * away, not multiplied.  What a key holds that some query sees counts for the
  * queries near it, as in the formula with a weight of 0: a NaN in it may reach any
- * query whose tile (128 queries) needs the key.
+ * query whose tile (128 queries) needs the key, and backward a NaN in a query that sees
+ * some key any key whose tile (128 keys) needs the query.
  *
  * Backward, from the forward's o and lse:
  *   p = exp(s - lse), dp_ij = do_i . v_j, ds = p (dp - do_i . o_i),
@@ -129,7 +131,8 @@ size_t zero_qk_norm_rope_workspace_bytes(int64_t T, int D);
  * p cannot be formed.  (Forward, its softmax is that of its scores in binary32.)
  *
  * q, k, v, o and their gradients are bf16; p and dx are rounded to bf16 for
- * the matrix products (their sums stay binary32).  D is 32, 64, 96 or 128;
+ * the matrix products (their sums stay binary32).  Scores and lse are binary32: p is off by
+ * some |lse| 2^-22 of itself.  D is 32, 64, 96 or 128;
  * Hq is a multiple of Hk.
  * Bases and strides are multiples of 16 bytes.
  *

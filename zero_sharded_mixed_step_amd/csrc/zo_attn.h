@@ -159,7 +159,10 @@ __device__ __forceinline__ int result_row(int r, int lane) {
   return 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
 }
 
-// Eight registers of a score result as an operand fragment.
+// Eight registers of a score result as an operand fragment: p or dx, rounded to bf16.  A
+// binary32 product would take sixteen times as long on the matrix units; with bf16 an output
+// is up to 1.4 times as far from the exact one as its own rounding to bf16 leaves it (2.0e-3
+// and 1.6e-3 of it, one token on 5003 keys).
 __device__ __forceinline__ bf16x8 to_frag(const float* x) {
   bf16x8 f;
 #pragma unroll
@@ -277,7 +280,11 @@ struct TileLoad {
 
 // Tiles of a pair of tensors under way or in use in the backward kernels.  With three, a
 // tile's loads have two turns to arrive: 274 us instead of 279 with two (4096 keys, 16 heads
-// of 64).  Where two workgroups share a compute unit, three of 128 columns do not fit.
+// of 64, no bias).  Where two workgroups share a compute unit, three of 128 columns do not fit.
+// The rule goes by columns alone.  A bias adds its tables: at 96 columns the queries' kernel
+// then has room for one workgroup a unit (354 us, where two tiles and two workgroups took 340:
+// 4096 keys, 16 heads, causal, reach 128), and so has the joint launch at 64 columns from a
+// reach of 256 on (364 us at 512, 209 at 128).
 template <int D, bool ALONE>
 constexpr int kBuffers = D <= 96 || ALONE ? 3 : 2;
 
@@ -499,7 +506,7 @@ __device__ __forceinline__ int tile_of_rank(int y, int n, int* scratch, int tid,
   __syncthreads();
   return t;
 }
-// (Ranked, 137 us instead of 154 forward and 457 instead of 476 backward: 4096 and 4001 keys
+// (Ranked, 134 us instead of 154 forward and 457 instead of 476 backward: 4096 and 4001 keys
 // in two documents.  Eight tiles, 1024 keys: the same.  256 threads rank 255 tiles.)
 constexpr int kMinRanked = 16, kMaxRanked = 255;
 

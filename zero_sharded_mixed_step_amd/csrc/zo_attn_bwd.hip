@@ -8,13 +8,13 @@
 // ranges, clipped, in the workspace, all padded to whole tiles of 64 queries, and
 // which tiles of queries see a tile of keys.
 //
-// What bounds it is the score work's issue beside the products (per score an
-// exponential, with a cap one more and a reciprocal, at a quarter of the rate of other
-// instructions) and shared memory, of which every matrix instruction reads an operand.
-// Measured, counting 5 products: 660 TFLOP/s at 128 columns and 630 at 64 (4096 keys, 16
-// heads, no mask), 414 with a cap, 32 heads on 8 and documents of 1325 and 2671
-// tokens (457 us: keys 315, queries 175, the rest 27 in the kernels' own times, which a
-// profiler stretches).
+// Measured, counting 5 products: 670 TFLOP/s at 128 columns, 705 at 96 and 620 at 64 (4096 keys,
+// 16 heads, no mask), 405 with a cap, 32 heads on 8 of 128 and documents of 1325 and 2671
+// tokens (465 us).  No unit is near full there: in the keys' kernel the matrix units are busy 22 %
+// of the time, vector issue is about a third of the busy time, waves wait 30 % of it, and units
+// are idle 22 % (512 uneven workgroups on 256).  What costs is work that follows on itself: a
+// block's products, its scores (an exponential each, with a cap one more and a reciprocal, at a
+// quarter of the rate of other instructions), the gradients' products.
 #include "zo_attn.h"
 #include "zo_internal.h"
 
@@ -140,7 +140,7 @@ __device__ __forceinline__ void grad_score(float x, float base, float dp_delta,
 
 // The registers of one wave a SIMD for 128 columns, and for 96 with a bias: k, v, dk and
 // dv alone take 192 or 144 of the 256 that two waves leave each, and the rest does not fit.
-// (Where it does, two waves: 368 us instead of 433 at 96 columns, 275 instead of 333 at
+// (Where it does, two waves: 358 us instead of 425 at 96 columns, 275 instead of 333 at
 // 64; 4096 keys, 16 heads.)
 // A large cap's series has no place beside another wave either: 64 to 128 columns went to
 // scratch.

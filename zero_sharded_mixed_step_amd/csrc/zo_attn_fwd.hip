@@ -11,11 +11,14 @@
 // in any row, which binary32 has room for.
 //
 // Two waves a SIMD, of two workgroups, overlap one's products with the other's score work,
-// which bounds it: an exponential a score, and with a cap one more and a reciprocal,
-// at a quarter of the rate of other instructions.  Measured on 4096 queries and keys, 32
-// heads, no mask: 940 to 990 TFLOP/s at 128 columns (810
-// capped), 840 at 64.  Splitting
-// the keys for a single token (choose_split), 4 x 12 heads on 5003 keys: 19 us, 3.2 TB/s of k and v.
+// which takes more issue than the products: an exponential a score, and with a cap one more and
+// a reciprocal, at a quarter of the rate of other instructions.  Measured on 4096 queries and
+// keys, 32 heads, no mask: 940 to 990 TFLOP/s at 128 columns (770 to 810 capped), 890 to 920 at
+// 96, 815 to 840 at 64 (the card's clock differs from day to day).  Documents and few heads add
+// idle units: counted at 4096 keys in two documents, 32 on 8 heads, cap, units are busy 81 % of
+// the kernel, at 8 x 1024 tokens, 12 heads of 64, bias, 52 %.
+// Splitting the keys for a single token (choose_split), 4 x 12 heads on 5003 keys: 19 us, 3.2
+// TB/s of k and v.
 #include "zo_attn.h"
 #include "zo_internal.h"
 
@@ -127,7 +130,6 @@ __device__ __forceinline__ void attn_fwd_tile(const AttnParams& p, const FragAt<
 template <int D, int CAP, bool BIAS, bool SPLIT>
 __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnParams p) {
   constexpr int kRows = 32 * kWaves, kBufs = 2, kTiles = 2 * kBufs;
-  constexpr int kAhead = (kBufs - 2) * 2 * TileLoad<D>::kLoads;   // loads of later tiles than the next
   extern __shared__ __align__(1024) char smem[];      // [kBufs] tiles of K, of V
   const uint32_t tiles = lds_address(smem);
   int2* ranges = reinterpret_cast<int2*>(smem + kTiles * kTileBytes<D>);  // [kRows]
@@ -206,8 +208,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_fwd_kernel(const AttnPar
       __syncthreads();
     }
     work();
+    // (One wait in two places: where the compiler has a single one it moves work across it, 287
+    // us instead of 277 at 4096 keys, 32 heads of 128, no mask.)
     if (ahead < kend)
-      wait_tile<kAhead>();
+      wait_tile();
     else
       wait_tile();
     k0 += kTile;

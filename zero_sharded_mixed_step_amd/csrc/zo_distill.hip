@@ -17,7 +17,8 @@
 // no difference of large numbers, and about its own maximum where it is far below the row's.
 //
 // Measured: 8192 x 50257 bf16 with the gradient 312 us, 5.3 TB/s of logits read and
-// gradient written; the backward alone, 1024 x 131072 fp32, 169 us, 6.4 TB/s.
+// gradient written, the loss alone 206 us, 4.0 TB/s; the backward alone, 1024 x 131072 fp32,
+// 168 us, 6.4 TB/s, 2048 x 50257 bf16 76 us, 5.4.
 #include "zo_device.h"
 #include "zo_internal.h"
 
