@@ -15,8 +15,8 @@
 // a reciprocal, at a quarter of the rate of other instructions.  Measured on 4096 queries and
 // keys, 32 heads, no mask: 940 to 990 TFLOP/s at 128 columns (770 to 810 capped), 890 to 920 at
 // 96, 815 to 840 at 64 (the card's clock differs from day to day).  Documents and few heads add
-// idle units: counted at 4096 keys in two documents, 32 on 8 heads, cap, units are busy 81 % of
-// the kernel, at 8 x 1024 tokens, 12 heads of 64, bias, 52 %.
+// idle units: counted at 4096 keys in two documents, 32 on 8 heads, cap, units are busy 79 % of
+// the kernel, at 8 x 1024 tokens, 12 heads of 64, bias, 51 %.
 // Splitting the keys for a single token (choose_split), 4 x 12 heads on 5003 keys: 19 us, 3.2
 // TB/s of k and v.
 #include "zo_attn.h"
