@@ -361,6 +361,33 @@ def test_distill_backward_of_many_rows(zs, torch):
     R.check("dz", dz, *want["dz"])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+@pytest.mark.parametrize("size", [1e-36, 1e-25, 1e-20, 1e-16, 1e16, 1e20, 1e30])
+def test_norm_of_values_of_any_size(zs, torch, size, D, dtype):
+    """Rows whose mean square is past binary32's ends, beside ordinary ones: without eps,
+    the norm is the same at every size."""
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = _gen(torch, D)
+    T, H = 7, 3
+    x = torch.randn(T, H, D, generator=g)
+    x[1::2] *= size
+    x = x.to(dt)
+    dy = torch.randn(T, H, D, generator=g)
+    dy[1::2] *= min(1.0, size)                            # (dx = dy / size stays in range)
+    dy, w = dy.to(dt), _rand(torch, g, (D,), dt)
+    pos, freq = torch.randint(0, 1000, (T,), generator=g, dtype=torch.int32), zs.rope_inv_freq(D)
+    kw = dict(wq=w.cuda(), eps=0.0, pos=pos.cuda(), inv_freq=freq.cuda())
+    y, dx = torch.full_like(x, math.nan).cuda(), torch.full_like(x, math.nan).cuda()
+    zs.zero_qk_norm_rope_fwd(x.cuda(), None, y, None, **kw)
+    R.check("y", y, *R.norm_forward(x, w, 0.0, pos, freq, False))
+    zs.zero_qk_norm_rope_bwd(x.cuda(), None, dy.cuda(), None, dx, None, **kw)
+    want, bound = R.norm_backward(x, w, dy, 0.0, pos, freq, False)["dx"]
+    # (gradients near the smallest numbers are off by those' steps)
+    tiny = 2.0 ** -126 * (R.half_step(dt) if dt == torch.float32 else 2.0 ** -7)
+    R.check("dx", dx, want, bound + tiny)
+
+
 # --------------------------------------------- rows a model is sure of, tails ---
 
 def _distill_check(zs, torch, z, idx, val, tau, tlse, w=None, grad_scale=0.25):

@@ -175,6 +175,20 @@ __device__ __forceinline__ float sum_row(float x) {
   return join_lanes<G>(x, AddOp());
 }
 
+// Whether a row's mean square plus eps is near the ends of binary32 (the reciprocal root takes
+// no subnormal numbers): of values below 1e-15 with an eps below 1e-30, or above 1e15.
+__device__ __forceinline__ bool far_mean(float v) { return !(v >= 1e-30f && v <= 1e30f); }
+
+// 1 / sqrt(mean(x^2) + eps) of such a row, from x times a power of 2.
+template <int G>
+__device__ __forceinline__ float far_inverse_rms(const float x[8], float v, float inv_d, float eps) {
+  const float s = v < 1.f ? 0x1p100f : 0x1p-100f;
+  float sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(x[j] * s, x[j] * s, sum);
+  return s * __builtin_amdgcn_rsqf(__builtin_fmaf(sum_row<G>(sum), inv_d, eps * s * s));
+}
+
 template <typename E>
 __device__ __forceinline__ void load_weight(const void* w, int at, bool active, float out[8]) {
 #pragma unroll
@@ -219,7 +233,12 @@ __global__ __launch_bounds__(kNormThreads) void norm_fwd_kernel(const NormParams
 #pragma unroll
         for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(x[j], x[j], sq);
         sq = sum_row<G>(sq);
-        const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(sq, inv_d, p.eps));
+        const float ms = __builtin_fmaf(sq, inv_d, p.eps);
+        float r = __builtin_amdgcn_rsqf(ms);
+        if (__any(h < a.H && far_mean(ms))) {             // (by the wave)
+          const float fr = far_inverse_rms<G>(x, ms, inv_d, p.eps);
+          r = far_mean(ms) ? fr : r;
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j];
         turn.template apply<false, G>(x, y, lane);
@@ -277,8 +296,18 @@ __global__ __launch_bounds__(kNormThreads) void norm_bwd_kernel(const NormParams
         }
         sq = sum_row<G>(sq);
         ux = sum_row<G>(ux);
-        const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(sq, inv_d, p.eps));
-        const float k = ux * inv_d * r * r;               // mean(u xhat) r
+        const float ms = __builtin_fmaf(sq, inv_d, p.eps);
+        float r = __builtin_amdgcn_rsqf(ms);
+        float k = ux * inv_d * r * r;                     // mean(u xhat) r
+        if (__any(h < a.H && far_mean(ms))) {             // (by the wave)
+          const float fr = far_inverse_rms<G>(x, ms, inv_d, p.eps);
+          float t = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) t = __builtin_fmaf(u[j], x[j] * fr, t);
+          t = sum_row<G>(t);
+          r = far_mean(ms) ? fr : r;
+          k = far_mean(ms) ? t * inv_d * fr : k;
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           if (on) dw[j] = __builtin_fmaf(g[j], x[j] * r, dw[j]);
