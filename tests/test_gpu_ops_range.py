@@ -131,6 +131,26 @@ def test_attention_tiny_caps(zs, torch, cap, bias):
         assert bool(torch.isfinite(g[name]).all()), name
 
 
+def test_attention_sum_of_many_equal_weights(zs, torch):
+    """2^17 keys of one weight, 0.7 of the largest: sums whose roundings all go one way."""
+    T, Tq, H, D = 1 << 17, 129, 160, 32
+    bf = torch.bfloat16
+    q = torch.zeros(1, Tq, H, D, device="cuda", dtype=bf)
+    q[..., 0] = 1
+    k = torch.zeros(1, T, 1, D, device="cuda", dtype=bf)
+    k[0, 0, 0, 0] = 0.357
+    v = torch.ones(1, T, 1, D, device="cuda", dtype=bf)
+    o, lse = torch.empty_like(q), torch.empty(1, H, Tq, device="cuda")
+    assert zs.zero_attn_workspace_bytes(1, Tq, T, H, 1, D) == 0              # (not split)
+    zs.zero_attn_fwd(q, k, v, o, lse, scale=1.0)
+    want = math.log(math.exp(float(k[0, 0, 0, 0])) + T - 1)
+    # a lane takes 32 of a tile's 64 keys: 32 + 2048 sums, and the score's own roundings
+    bound = (32 + T / 64) * R.F32R + 32 * R.F32R + 4 * R.F32R * want
+    assert float((lse.double() - want).abs().max()) <= bound
+    # the products' sums: 4 of 16 keys a tile
+    assert float((o.double() - 1).abs().max()) <= 2 * R.BF + 4 * T / 64 * R.F32R
+
+
 # ----------------------------------------------------------- empty batches ---
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
