@@ -125,6 +125,16 @@ def prepare(case, seed):
             "clip": _prepare_clip}[case["op"]](case, g)
 
 
+def _package():
+    import zero_sharded_mixed_step_amd as zs
+    return zs
+
+
+def _scratch(nbytes):
+    """Scratch memory that a program keeps from step to step."""
+    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device="cuda")
+
+
 def _prepare_embed(case, g):
     N, V, C = case["N"], case["V"], case["C"]
     # tokens of a text: a few words make up much of it, most of the table is
@@ -142,7 +152,8 @@ def _prepare_embed(case, g):
     s["dout"] = _normal(g, (N, C), case["dtype"], 1e-2)
     s["base"] = None if case["base"] == "none" else _normal(g, (V, C), case["base"], 1e-2)
     s["dtable"] = torch.empty((V, C), dtype=DTYPES[case["grad"]], device="cuda")
-    s["ws"] = None
+    if own:
+        s["ws"] = _scratch(_package().zero_embed_workspace_bytes(N, C))
     return s
 
 
@@ -167,7 +178,8 @@ def _prepare_norm(case, g):
     s["dx"] = torch.empty_like(s["x"])
     for n, x in (("dy", "y"), ("dw1", "w1"), ("dw2", "w2"), ("dgate", "gate")):
         s[n] = None if s[x] is None else torch.empty_like(s[x])
-    s["ws"] = None
+    if own:
+        s["ws"] = _scratch(_package().zero_block_norm_workspace_bytes(T, C))
     return s
 
 
@@ -230,7 +242,11 @@ def _prepare_clip(case, g):
         at[dt] += k
     s["inv"] = 1.0 / case["loss_scale"]
     s["norm"] = torch.empty(1, dtype=torch.float32, device="cuda")
-    s["acc"] = s["ws"] = None
+    if own:
+        # the table of the tensors that a program makes once for its gradients
+        zs = _package()
+        s["tensors"] = zs.GradTable(s["grads"], s["outs"])
+        s["acc"], s["ws"] = zs.new_norm_acc(1), _scratch(zs.zero_grads_workspace_bytes())
     return s
 
 
@@ -379,24 +395,14 @@ def _clip_plain(s):
 
 # ------------------------------------------------------ through the package ---
 
-def _scratch(s, nbytes):
-    """Scratch memory, kept by the program from step to step."""
-    if s["ws"] is None:
-        s["ws"] = torch.empty(max(nbytes, 16), dtype=torch.uint8, device="cuda")
-    return s["ws"]
-
-
 def _run_own(s):
-    import zero_sharded_mixed_step_amd as zs
-    case = s["case"]
+    zs, case = _package(), s["case"]
     if case["op"] == "embed":
         if case["pass_"] == "fwd":
             zs.zero_embed_fwd(s["table"], s["ids"], s["out"], scale=case["scale"])
             return s["out"]
-        ws = _scratch(s, zs.zero_embed_workspace_bytes(case["N"], case["C"])) \
-            if s["ws"] is None else s["ws"]
         zs.zero_embed_bwd(s["ids"], s["dout"], s["dtable"], scale=case["scale"], base=s["base"],
-                          workspace=ws)
+                          workspace=s["ws"])
         return s["dtable"]
     if case["op"] == "norm":
         kw = dict(post_norm=case["post"], post_weight=s["w1"], gate=s["gate"], pre_weight=s["w2"],
@@ -405,11 +411,9 @@ def _run_own(s):
         if case["pass_"] == "fwd":
             zs.zero_block_norm_fwd(s["x"], s["y"], s["h"], s["z"], **kw)
             return {n: s[n] for n in ("h", "z") if s[n] is not None}
-        ws = _scratch(s, zs.zero_block_norm_workspace_bytes(case["T"], case["C"])) \
-            if s["ws"] is None else s["ws"]
         zs.zero_block_norm_bwd(s["y"], s["h"], s["dh"], s["dz"], s["dx"], s["dy"],
                                dpost_weight=s["dw1"], dgate=s["dgate"], dpre_weight=s["dw2"],
-                               workspace=ws, **kw)
+                               workspace=s["ws"], **kw)
         return {n: s[n] for n in ("dx", "dy", "dw1", "dgate", "dw2") if s[n] is not None}
     if case["op"] == "policy":
         kw = dict(row_weight=s["w"], temperature=case["tau"], grad_scale=s["gscale"])
@@ -420,12 +424,9 @@ def _run_own(s):
                            old_logp=s["old"], ref_logp=s["ref"], clip_low=case["lo"],
                            clip_high=case["hi"], kl_coef=case["kl"], **kw)
         return {n: s[n] for n in ("loss", "stats", "dz") if n in s}
-    if s["acc"] is None:
-        s["acc"] = zs.new_norm_acc(1)
-        _scratch(s, zs.zero_grads_workspace_bytes())
-    zs.zero_grads_norm(s["grads"], s["acc"], inv_scale=s["inv"], workspace=s["ws"])
-    zs.zero_grads_clip(s["grads"], s["outs"], s["acc"], max_norm=case["max_norm"],
-                       inv_scale=s["inv"], norm_out=s["norm"])
+    zs.zero_grads_norm(s["tensors"], s["acc"], inv_scale=s["inv"], workspace=s["ws"])
+    zs.zero_grads_clip(s["tensors"], s["acc"], max_norm=case["max_norm"], inv_scale=s["inv"],
+                       norm_out=s["norm"])
     return dict(s["out"], norm=s["norm"][0])
 
 
