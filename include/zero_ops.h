@@ -11,6 +11,14 @@
  *     zero_attn_ranges derives the intervals from document ids.
  *   - zero_distill_fwd/_bwd: the distillation loss against a teacher's top
  *     logits, with its gradient in the same pass or from saved statistics.
+ *   - zero_embed_fwd/_bwd: the embedding lookup with a factor, and the table's
+ *     gradient.
+ *   - zero_block_norm_fwd/_bwd: the norm of a block's output, its gate, the
+ *     residual sum and the next block's norm, in one pass.
+ *   - zero_policy_fwd/_bwd: the clipped policy loss with a KL term on the
+ *     student's own samples, with its gradient as the distillation loss's.
+ *   - zero_grads_norm, zero_grads_clip: the exact global norm of the gradients
+ *     of many tensors, and their unscaling and clipping.
  *
  * Conventions, as in zero_step.h:
  *   - Status codes are those of zero_step.h.  Every argument is checked
@@ -43,7 +51,7 @@
 extern "C" {
 #endif
 
-#define ZERO_OPS_ABI_VERSION 1
+#define ZERO_OPS_ABI_VERSION 2
 
 /* Largest reach of the distance bias, most buckets, most teacher entries of
  * a row, and longest row of logits. */
@@ -51,6 +59,13 @@ extern "C" {
 #define ZERO_ATTN_MAX_BUCKETS 256
 #define ZERO_DISTILL_MAX_K 1024
 #define ZERO_DISTILL_MAX_V (1 << 20)
+/* Longest row of an embedding table or a residual stream, most rows of a
+ * table, longest row of logits of the policy loss, most tensors of a
+ * gradient call. */
+#define ZERO_ROW_MAX_C (1 << 14)
+#define ZERO_EMBED_MAX_V (1 << 24)
+#define ZERO_POLICY_MAX_V (1 << 20)
+#define ZERO_GRADS_MAX_COUNT (1 << 16)
 
 int zero_ops_abi_version(void);
 const char *zero_ops_strerror(int status);
@@ -219,6 +234,182 @@ typedef struct zero_distill_args {
 
 int zero_distill_fwd(const zero_distill_args *args, void *stream);
 int zero_distill_bwd(const zero_distill_args *args, void *stream);
+
+/* ---- embedding -------------------------------------------------------------
+ *
+ *   out[n] = scale * table[ids[n]],
+ *   dtable[v] = base[v] + scale * sum of dout[n] over the n with ids[n] = v
+ * (base NULL: 0).  Ids outside [0, V), such as padding, give rows of zeros and
+ * have no part in the gradient.
+ *
+ * zero_embed_bwd writes all of dtable.  base may be dtable itself (same dtype
+ * and stride): the sums are then added, and rows that no id names are left as
+ * they are.  A row's sum is binary32, in the order of n: runs of at most 64
+ * terms, then the runs; base is added last, before the one rounding.
+ *
+ * dtype (ZERO_BF16 or ZERO_F32) is that of table, out and dout, grad_dtype that
+ * of dtable, base_dtype that of base.  C is a multiple of 8 up to
+ * ZERO_ROW_MAX_C; rows start on 16 bytes (ZERO_EALIGN).  N <= 2^21. */
+typedef struct zero_embed_args {
+  size_t struct_bytes;          /* sizeof(zero_embed_args) */
+  int64_t N, V;
+  int32_t C, dtype, grad_dtype, base_dtype;
+  double scale;
+  const int32_t *ids;           /* [N] */
+  const void *table;            /* [V][C], forward */
+  void *out;                    /* [N][C], forward */
+  const void *dout;             /* [N][C], backward from here on */
+  const void *base;             /* [V][C] or NULL */
+  void *dtable;                 /* [V][C] */
+  int64_t table_stride, out_stride, dout_stride, base_stride, dtable_stride;
+  void *workspace;              /* backward only */
+  size_t workspace_bytes;
+} zero_embed_args;
+
+int zero_embed_fwd(const zero_embed_args *args, void *stream);
+int zero_embed_bwd(const zero_embed_args *args, void *stream);
+size_t zero_embed_workspace_bytes(int64_t N, int C);
+
+/* ---- norms around a block --------------------------------------------------
+ *
+ * For each token, over its C values, with rms(v) = sqrt(mean(v^2) + eps):
+ *   u = y / rms(y) * (post_w + weight_offset)   if post_norm, else y
+ *   h = res_scale * x + branch_scale * gate * u         (gate 1 if NULL)
+ *   z = h / rms(h) * (pre_w + weight_offset)
+ * x is the residual stream, y a block's output, h the new residual stream and z
+ * the next block's input.  A weight that is NULL counts as 1 (without the
+ * offset).  y NULL: no block, h = res_scale * x.  h (forward) or z may be NULL:
+ * not wanted; z is formed from h before its rounding.  gate is [C] for all
+ * tokens (gate_tokens 0) or [T][C].
+ *
+ * Backward, from the forward's h, y, weights and gate, and the gradients dh (NULL:
+ * 0) and dz (NULL: 0; h and pre_w are then not read) that come in:
+ *   u2 = dz * (pre_w + weight_offset),  hh = h / rms(h)
+ *   gh = dh + (u2 - hh * mean(u2 * hh)) / rms(h),     dx = res_scale * gh
+ *   du = branch_scale * gate * gh,      dgate = branch_scale * gh * u
+ *   dy = du, or with post_norm, yy = y / rms(y), u1 = du * (post_w + weight_offset),
+ *   dy = (u1 - yy * mean(u1 * yy)) / rms(y)
+ *   dpost_w = sum over tokens of du * yy,  dpre_w = sum of dz * hh,
+ * dgate summed over the tokens too where they share the gate.  dx, dy and the
+ * weights' gradients may each be NULL: not wanted.
+ *
+ * dtype (ZERO_BF16 or ZERO_F32) is that of y, z, the weights, the gate and
+ * their gradients, res_dtype that of x, h, dh and dx: the same, or ZERO_F32.
+ * C is a multiple of 8 up to ZERO_ROW_MAX_C, T <= 2^21; rows start on 16 bytes:
+ * base addresses and strides (ZERO_EALIGN).  h may be x, and dx may be dh (same
+ * strides).  The workspace is for backward calls that want a gradient summed over
+ * the tokens. */
+typedef struct zero_block_norm_args {
+  size_t struct_bytes;          /* sizeof(zero_block_norm_args) */
+  int64_t T;
+  int32_t C, dtype, res_dtype, post_norm, gate_tokens, reserved;
+  double eps, weight_offset, res_scale, branch_scale;
+  const void *x;                /* [T][C], forward */
+  const void *y;                /* [T][C] or NULL */
+  const void *post_w;           /* [C] or NULL */
+  const void *gate;             /* [C] or [T][C] or NULL */
+  const void *pre_w;            /* [C] or NULL */
+  void *h;                      /* [T][C]: forward's output, backward's input */
+  void *z;                      /* [T][C], forward */
+  const void *dh, *dz;          /* backward from here on */
+  void *dx, *dy;
+  void *dpost_w, *dgate, *dpre_w;
+  int64_t x_stride, y_stride, gate_stride, h_stride, z_stride;
+  int64_t dh_stride, dz_stride, dx_stride, dy_stride, dgate_stride;
+  void *workspace;
+  size_t workspace_bytes;
+} zero_block_norm_args;
+
+int zero_block_norm_fwd(const zero_block_norm_args *args, void *stream);
+int zero_block_norm_bwd(const zero_block_norm_args *args, void *stream);
+size_t zero_block_norm_workspace_bytes(int64_t T, int C);
+
+/* ---- clipped policy loss --------------------------------------------------
+ *
+ * Row n has V student logits z and the sampled token a = action[n].  With
+ * lse = log sum_j exp(z_j / tau), q_j = exp(z_j / tau - lse) and the token's log
+ * probability lp = z_a / tau - lse:
+ *   r = exp(lp - old_logp[n])   (old_logp NULL: lp itself, r = 1)
+ *   s = min(r A, min(max(r, 1 - clip_low), 1 + clip_high) A),  A = advantage[n]
+ *   e = ref_logp[n] - lp,  kl = exp(e) - e - 1     (ref_logp NULL: kl = 0)
+ *   loss[n] = w (kl_coef kl - s),   w = row_weight[n] (1 if NULL)
+ *   g = -A r  (0 where A > 0 and r > 1 + clip_high, and where A < 0 and
+ *       r < 1 - clip_low)  + kl_coef (1 - exp(e)),  the derivative by lp
+ *   stats[n] = { lse, lp, g, kl }
+ *   dlogits_j = grad_scale w g / tau ([j = a] - q_j)
+ * A row whose action is outside [0, V), or whose logits are all -inf, is absent:
+ * loss 0, gradient 0, lp, g and kl 0 in its stats.  A row with w = 0 has loss 0 and
+ * gradient 0 whatever it holds (its stats are formed all the same).  A row with
+ * g = 0 has gradient 0.  g beyond binary32 counts as its largest number in the
+ * gradient.
+ *
+ * zero_policy_fwd writes loss and stats, and dlogits too if given (one read of
+ * the logits for all three); zero_policy_bwd writes dlogits from stats (lse, lp
+ * and g, whatever loss they came from).  dlogits may be the logits themselves
+ * (same stride).  dtype is that of logits and dlogits.  1e-30 <= tau <= 1e30,
+ * 0 <= clip_low <= 1, clip_high >= 0, N <= 2^21, V <= ZERO_POLICY_MAX_V; logits may start
+ * at any element. */
+typedef struct zero_policy_args {
+  size_t struct_bytes;          /* sizeof(zero_policy_args) */
+  int64_t N, V;
+  int32_t dtype, reserved;
+  double temperature, clip_low, clip_high, kl_coef, grad_scale;
+  const void *logits;           /* [N][V] */
+  const int32_t *action;        /* [N] */
+  const float *advantage;       /* [N], forward */
+  const float *old_logp;        /* [N] or NULL, forward */
+  const float *ref_logp;        /* [N] or NULL, forward */
+  const float *row_weight;      /* [N] or NULL */
+  float *loss;                  /* [N], forward */
+  float *stats;                 /* [N][4]: forward's output, backward's input */
+  void *dlogits;                /* [N][V] */
+  int64_t logits_stride, dlogits_stride;
+} zero_policy_args;
+
+int zero_policy_fwd(const zero_policy_args *args, void *stream);
+int zero_policy_bwd(const zero_policy_args *args, void *stream);
+
+/* ---- the global norm of many gradients, and clipping ---------------------
+ *
+ * The tensors are dense vectors of sizes[i] elements at grads[i], any element
+ * alignment, dtypes[i] ZERO_F32 or ZERO_BF16; the arrays of addresses, sizes and
+ * dtypes are HOST memory, read during the call only.
+ *
+ * zero_grads_norm: the norm state of g = grads * inv_scale (binary32) of all the
+ * tensors into `acc`, which is overwritten, or added to with `add`: bit for bit what
+ * zero_grad_norm adds for the tensors one by one, so it may be summed over ranks and
+ * given to zero_adamw_step.  At most 2^37 elements in an accumulator.
+ *
+ * zero_grads_clip: outs[i] = (grads[i] * inv_scale) * coef, rounded to out_dtypes[i],
+ * with the skip and the coefficient that zero_step_gate derives from the n_accs
+ * accumulators, max_norm and check_overflow; a skipped call writes no tensor.  outs[i]
+ * may be grads[i] (same dtype).  norm_out, coef_out and skipped_out (each may be
+ * NULL): the global norm, infinite where a value is not finite, the coefficient (0 where
+ * skipped) and 1 where skipped, else 0. */
+typedef struct zero_grads_args {
+  size_t struct_bytes;          /* sizeof(zero_grads_args) */
+  int64_t count;
+  const void *const *grads;     /* HOST [count] */
+  void *const *outs;            /* HOST [count], clip */
+  const int64_t *sizes;         /* HOST [count] */
+  const int32_t *dtypes;        /* HOST [count] */
+  const int32_t *out_dtypes;    /* HOST [count], clip */
+  double inv_scale;
+  zero_norm_acc *acc;           /* norm */
+  int32_t add;                  /* norm */
+  int32_t n_accs;               /* clip from here on */
+  const zero_norm_acc *accs;
+  double max_norm;
+  int32_t check_overflow, reserved;
+  float *norm_out, *coef_out;
+  int32_t *skipped_out;
+  void *workspace;              /* norm */
+  size_t workspace_bytes;
+} zero_grads_args;
+
+int zero_grads_norm(const zero_grads_args *args, void *stream);
+int zero_grads_clip(const zero_grads_args *args, void *stream);
+size_t zero_grads_workspace_bytes(void);
 
 #ifdef __cplusplus
 }

@@ -8,8 +8,9 @@ built.
 
 Beside it, libzero_ops.so (include/zero_ops.h, `_ops_binding`) holds the
 operators of a student model's training step whose gradients the step reduces:
-per-head norm with rotation, masked/capped/biased attention, and the
-distillation loss.
+embedding, per-head norm with rotation, masked/capped/biased attention, the norms
+around a block, the distillation and policy losses, and the gradients' global
+norm and clipping.
 """
 from ._binding import (ACC_DIGITS, ACC_WORDS, REDUCE_WORKSPACE_BYTES, ZERO_BF16,  # noqa: F401
                        ZERO_F32,
@@ -22,8 +23,11 @@ from ._binding import (ACC_DIGITS, ACC_WORDS, REDUCE_WORKSPACE_BYTES, ZERO_BF16,
                        zero_strerror,
                        zero_unfused_workspace_bytes)
 from .step import ShardStep, choose_path  # noqa: F401
-from ._ops_binding import (ZeroOpsError, ops_lib, relpos_buckets, rope_inv_freq,  # noqa: F401
-                           zero_attn_bwd, zero_attn_fwd, zero_attn_ranges,
-                           zero_attn_workspace_bytes, zero_distill_bwd, zero_distill_fwd,
-                           zero_ops_abi_version, zero_ops_strerror, zero_qk_norm_rope_bwd,
+from ._ops_binding import (GradTable, ZeroOpsError, ops_lib, relpos_buckets,  # noqa: F401
+                           rope_inv_freq, zero_attn_bwd, zero_attn_fwd, zero_attn_ranges,
+                           zero_attn_workspace_bytes, zero_block_norm_bwd, zero_block_norm_fwd,
+                           zero_block_norm_workspace_bytes, zero_distill_bwd, zero_distill_fwd,
+                           zero_embed_bwd, zero_embed_fwd, zero_embed_workspace_bytes,
+                           zero_grads_clip, zero_grads_norm, zero_grads_workspace_bytes,
+                           zero_policy_bwd, zero_policy_fwd, zero_ops_abi_version, zero_ops_strerror, zero_qk_norm_rope_bwd,
                            zero_qk_norm_rope_fwd, zero_qk_norm_rope_workspace_bytes)

@@ -16,16 +16,24 @@ import torch
 from . import build as _build
 from ._binding import ZERO_BF16, ZERO_F32, ZeroStepError, _stream
 
-OPS_ABI_VERSION = 1
+OPS_ABI_VERSION = 2
 ATTN_MAX_REACH = 512
 ATTN_MAX_BUCKETS = 256
 DISTILL_MAX_K = 1024
 DISTILL_MAX_V = 1 << 20
+ROW_MAX_C = 1 << 14
+EMBED_MAX_V = 1 << 24
+POLICY_MAX_V = 1 << 20
+GRADS_MAX_COUNT = 1 << 16
 
 # The argument structs of zero_ops.h, field by field (native alignment).
 _NORM_ARGS = struct.Struct("@Qq6id14Q16q2Q")
 _ATTN_ARGS = struct.Struct("@Q10i2d13Q24q2Q")
 _DISTILL_ARGS = struct.Struct("@Q2q2i2d8Q2q")
+_EMBED_ARGS = struct.Struct("@Q2q4id6Q5q2Q")
+_BLOCK_NORM_ARGS = struct.Struct("@Qq6i4d14Q10q2Q")
+_POLICY_ARGS = struct.Struct("@Q2q2i5d9Q2q")
+_GRADS_ARGS = struct.Struct("@Qq5QdQ2iQd2i5Q")
 
 _BF16 = torch.bfloat16
 _CODES = {torch.float32: ZERO_F32, torch.bfloat16: ZERO_BF16}
@@ -54,7 +62,10 @@ def ops_lib():
         L.zero_ops_strerror.argtypes = [i]
         L.zero_ops_strerror.restype = C.c_char_p
         for name in ("zero_qk_norm_rope_fwd", "zero_qk_norm_rope_bwd", "zero_attn_fwd",
-                     "zero_attn_bwd", "zero_distill_fwd", "zero_distill_bwd"):
+                     "zero_attn_bwd", "zero_distill_fwd", "zero_distill_bwd", "zero_embed_fwd",
+                     "zero_embed_bwd", "zero_block_norm_fwd", "zero_block_norm_bwd",
+                     "zero_policy_fwd", "zero_policy_bwd", "zero_grads_norm",
+                     "zero_grads_clip"):
             f = getattr(L, name)
             f.argtypes, f.restype = [C.c_char_p, vp], i
         L.zero_qk_norm_rope_workspace_bytes.argtypes = [i64, i]
@@ -63,6 +74,11 @@ def ops_lib():
         L.zero_attn_workspace_bytes.restype = C.c_size_t
         L.zero_attn_ranges.argtypes = [vp, vp, i, i, i, vp, vp]
         L.zero_attn_ranges.restype = i
+        for name in ("zero_embed_workspace_bytes", "zero_block_norm_workspace_bytes"):
+            f = getattr(L, name)
+            f.argtypes, f.restype = [i64, i], C.c_size_t
+        L.zero_grads_workspace_bytes.argtypes = []
+        L.zero_grads_workspace_bytes.restype = C.c_size_t
         if L.zero_ops_abi_version() != OPS_ABI_VERSION:
             raise RuntimeError(f"{_build.OPS_LIB} has ABI version {L.zero_ops_abi_version()}, the "
                                f"binding expects {OPS_ABI_VERSION}: rebuild it")
@@ -408,3 +424,322 @@ def zero_distill_bwd(logits, teacher_idx, teacher_val, stats, dlogits, *, temper
         raise TypeError("dlogits must be a CUDA (HIP) tensor")
     _distill_call("zero_distill_bwd", logits, teacher_idx, teacher_val, None, stats, dlogits,
                   temperature, teacher_lse, row_weight, grad_scale, stream)
+
+
+# -------------------------------------------------------------- embedding ---
+
+def _matrix(t, name, shape, dtype, dev):
+    """Address and row stride (0 where there is one row) of a matrix; 0, 0 for None."""
+    if t is None:
+        return 0, 0
+    p, st = _tensor(t, name, shape, dtype, dev)
+    return p, st[0] if shape[0] > 1 else 0
+
+
+def _given(t, name, shape, dtype, dev):
+    if t is None:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    return _matrix(t, name, shape, dtype, dev)
+
+
+def zero_embed_workspace_bytes(N: int, C: int) -> int:
+    return ops_lib().zero_embed_workspace_bytes(int(N), int(C))
+
+
+def zero_embed_fwd(table, ids, out, *, scale=1.0, stream=None) -> None:
+    """out (N, C) = scale * table[ids]: table (V, C), float32 or bfloat16, ids (N)
+    int32; ids outside [0, V) give rows of zeros."""
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table is a (V, C) tensor")
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 1:
+        raise ValueError("ids is an (N) tensor")
+    V, width = table.shape
+    N, dt = ids.shape[0], table.dtype
+    code = _CODES.get(dt)
+    if code is None:
+        raise TypeError(f"the table is float32 or bfloat16, not {dt}")
+    dev = _device()
+    table_, st = _matrix(table, "table", (V, width), dt, dev)
+    out_, so = _given(out, "out", (N, width), dt, dev)
+    args = _EMBED_ARGS.pack(_EMBED_ARGS.size, N, V, width, code, 0, 0, scale,
+                            _flat(ids, "ids", (N,), torch.int32, dev), table_, out_, 0, 0, 0, st, so,
+                            0, 0, 0, 0, 0)
+    _call("zero_embed_fwd", args, stream, dev)
+
+
+def zero_embed_bwd(ids, dout, dtable, *, scale=1.0, base=None, workspace=None,
+                   stream=None) -> None:
+    """The gradient of zero_embed_fwd by the table: dtable (V, C) = base + scale * the
+    sums of dout's (N, C) rows by id.  base (V, C) is 0 where None, and may be dtable:
+    the sums are then added to it.  dout, base and dtable are float32 or bfloat16 each;
+    workspace: zero_embed_workspace_bytes(N, C) bytes."""
+    if not isinstance(dtable, torch.Tensor) or dtable.dim() != 2:
+        raise ValueError("dtable is a (V, C) tensor")
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 1:
+        raise ValueError("ids is an (N) tensor")
+    if not isinstance(dout, torch.Tensor):
+        raise TypeError("dout must be a CUDA (HIP) tensor")
+    V, width = dtable.shape
+    N = ids.shape[0]
+    codes = [0 if x is None else _CODES.get(x.dtype) for x in (dout, dtable, base)]
+    if None in codes:
+        raise TypeError("dout, dtable and base are float32 or bfloat16")
+    dev = _device()
+    dout_, sd = _matrix(dout, "dout", (N, width), dout.dtype, dev)
+    dt_, st = _matrix(dtable, "dtable", (V, width), dtable.dtype, dev)
+    base_, sb = (0, 0) if base is None else _matrix(base, "base", (V, width), base.dtype, dev)
+    args = _EMBED_ARGS.pack(_EMBED_ARGS.size, N, V, width, *codes, scale,
+                            _flat(ids, "ids", (N,), torch.int32, dev), 0, 0, dout_, base_, dt_, 0, 0,
+                            sd, sb, st, *_workspace(workspace, dev))
+    _call("zero_embed_bwd", args, stream, dev)
+
+
+# ---------------------------------------------------- norms around a block ---
+
+def zero_block_norm_workspace_bytes(T: int, C: int) -> int:
+    return ops_lib().zero_block_norm_workspace_bytes(int(T), int(C))
+
+
+def _block_types(res, others, what):
+    """T, C and the codes of a call's tensors: `res` one of the residual stream, `others`
+    those of the block's type."""
+    T, width = res.shape
+    dt = next((x.dtype for x in others if x is not None), res.dtype)
+    if dt not in _CODES or res.dtype not in _CODES:
+        raise TypeError(f"{what}: float32 or bfloat16, not {dt} and {res.dtype}")
+    return T, width, dt, _CODES[dt], _CODES[res.dtype]
+
+
+def _gate(gate, T, width, dt, dev, name="gate"):
+    """Whether it is a gate of each token, its address and its stride."""
+    if gate is None:
+        return 0, 0, 0
+    if isinstance(gate, torch.Tensor) and gate.dim() == 2:
+        return 1, *_matrix(gate, name, (T, width), dt, dev)
+    return 0, _flat(gate, name, (width,), dt, dev), 0
+
+
+def zero_block_norm_fwd(x, y, h, z, *, post_norm=False, post_weight=None, gate=None,
+                        pre_weight=None, weight_offset=0.0, res_scale=1.0, branch_scale=1.0,
+                        eps=1e-6, stream=None) -> None:
+    """The residual sum around a block and the next block's norm, over rows of C values:
+    h = res_scale * x + branch_scale * gate * u with u = y, or, with post_norm,
+    y / rms(y) * (post_weight + weight_offset); z = h / rms(h) * (pre_weight +
+    weight_offset).  x and h are (T, C) of the residual stream's type, y and z (T, C) and the
+    weights (C) of the block's (the same, or x and h are float32); gate is (C) or (T, C).  y
+    None: no block; h or z None: not wanted; weights None: 1.  h may be x."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x is a (T, C) tensor")
+    T, width, dt, code, rcode = _block_types(x, (y, z, post_weight, gate, pre_weight), "x, y and z")
+    dev, rt = _device(), x.dtype
+    x_, sx = _matrix(x, "x", (T, width), rt, dev)
+    y_, sy = _matrix(y, "y", (T, width), dt, dev)
+    h_, sh = _matrix(h, "h", (T, width), rt, dev)
+    z_, sz = _matrix(z, "z", (T, width), dt, dev)
+    tokens, gate_, sg = _gate(gate, T, width, dt, dev)
+    args = _BLOCK_NORM_ARGS.pack(
+        _BLOCK_NORM_ARGS.size, T, width, code, rcode, 1 if post_norm else 0, tokens, 0, eps,
+        weight_offset, res_scale, branch_scale, x_, y_,
+        _flat(post_weight, "post_weight", (width,), dt, dev), gate_,
+        _flat(pre_weight, "pre_weight", (width,), dt, dev), h_, z_, 0, 0, 0, 0, 0, 0, 0,
+        sx, sy, sg, sh, sz, 0, 0, 0, 0, 0, 0, 0)
+    _call("zero_block_norm_fwd", args, stream, dev)
+
+
+def zero_block_norm_bwd(y, h, dh, dz, dx, dy, *, dpost_weight=None, dgate=None, dpre_weight=None,
+                        post_norm=False, post_weight=None, gate=None, pre_weight=None,
+                        weight_offset=0.0, res_scale=1.0, branch_scale=1.0, eps=1e-6,
+                        workspace=None, stream=None) -> None:
+    """Gradients of zero_block_norm_fwd from its y, h, weights and gate and the gradients dh
+    and dz that come in (None: 0; without dz, h may be None): dx, dy and, where given,
+    dpost_weight, dgate and dpre_weight, each of which may be None.  dx may be dh.  workspace:
+    zero_block_norm_workspace_bytes(T, C) bytes where a gradient is summed over the tokens."""
+    res = next((t for t in (dh, dx, h) if isinstance(t, torch.Tensor)), None)
+    if res is None or res.dim() != 2:
+        raise ValueError("dh, dx and h are (T, C) tensors, one of them given")
+    T, width, dt, code, rcode = _block_types(res, (y, dz, dy, post_weight, gate, pre_weight),
+                                             "the gradients")
+    dev, rt = _device(), res.dtype
+    y_, sy = _matrix(y, "y", (T, width), dt, dev)
+    h_, sh = _matrix(h, "h", (T, width), rt, dev)
+    dh_, sdh = _matrix(dh, "dh", (T, width), rt, dev)
+    dz_, sdz = _matrix(dz, "dz", (T, width), dt, dev)
+    dx_, sdx = _matrix(dx, "dx", (T, width), rt, dev)
+    dy_, sdy = _matrix(dy, "dy", (T, width), dt, dev)
+    tokens, gate_, sg = _gate(gate, T, width, dt, dev)
+    dgate_ = sdg = 0
+    if dgate is not None:
+        own, dgate_, sdg = _gate(dgate, T, width, dt, dev, "dgate")
+        if gate is None or own != tokens:
+            raise ValueError("dgate has the gate's shape")
+    args = _BLOCK_NORM_ARGS.pack(
+        _BLOCK_NORM_ARGS.size, T, width, code, rcode, 1 if post_norm else 0, tokens, 0, eps,
+        weight_offset, res_scale, branch_scale, 0, y_,
+        _flat(post_weight, "post_weight", (width,), dt, dev), gate_,
+        _flat(pre_weight, "pre_weight", (width,), dt, dev), h_, 0, dh_, dz_, dx_, dy_,
+        _flat(dpost_weight, "dpost_weight", (width,), dt, dev), dgate_,
+        _flat(dpre_weight, "dpre_weight", (width,), dt, dev),
+        0, sy, sg, sh, 0, sdh, sdz, sdx, sdy, sdg, *_workspace(workspace, dev))
+    _call("zero_block_norm_bwd", args, stream, dev)
+
+
+# ------------------------------------------------------------ policy loss ---
+
+def _policy_call(fn, z, action, adv, old, ref, weight, loss, stats, dz, temperature, low, high,
+                 kl_coef, grad_scale, stream):
+    if not isinstance(z, torch.Tensor) or z.dim() != 2:
+        raise ValueError("logits is an (N, V) tensor")
+    N, V = z.shape
+    code = _CODES.get(z.dtype)
+    if code is None:
+        raise TypeError(f"logits are float32 or bfloat16, not {z.dtype}")
+    dev, dt, f32 = _device(), z.dtype, torch.float32
+    z_, sz = _tensor(z, "logits", z.shape, dt, dev)
+    dz_, sdz = (0, (V, 1)) if dz is None else _tensor(dz, "dlogits", z.shape, dt, dev)
+    args = _POLICY_ARGS.pack(
+        _POLICY_ARGS.size, N, V, code, 0, temperature, low, high, kl_coef, grad_scale, z_,
+        _flat(action, "action", (N,), torch.int32, dev), _flat(adv, "advantage", (N,), f32, dev),
+        _flat(old, "old_logp", (N,), f32, dev), _flat(ref, "ref_logp", (N,), f32, dev),
+        _flat(weight, "row_weight", (N,), f32, dev), _flat(loss, "loss", (N,), f32, dev),
+        _flat(stats, "stats", (N, 4), f32, dev), dz_, sz[0], sdz[0])
+    _call(fn, args, stream, dev)
+
+
+def zero_policy_fwd(logits, action, advantage, loss, stats, *, dlogits=None, old_logp=None,
+                    ref_logp=None, row_weight=None, temperature=1.0, clip_low=0.2, clip_high=0.2,
+                    kl_coef=0.0, grad_scale=1.0, stream=None) -> None:
+    """The clipped policy loss of the sampled tokens action (N, int32) under logits
+    (N, V), with their advantage (N): loss (N) and stats (N, 4) = the row's logsumexp, the
+    token's log probability, the loss's derivative by it (before the row's weight) and the
+    KL term; all float32.  If given, dlogits (N, V) = the gradient of grad_scale *
+    sum(loss), in the same pass (it may be `logits`).  old_logp (N) are the log
+    probabilities when sampled (None: now), ref_logp (N) the reference policy's, whose KL
+    term counts kl_coef; row_weight (N) weights the rows (0: no part in it)."""
+    _policy_call("zero_policy_fwd", logits, action, advantage, old_logp, ref_logp, row_weight, loss,
+                 stats, dlogits, temperature, clip_low, clip_high, kl_coef, grad_scale, stream)
+
+
+def zero_policy_bwd(logits, action, stats, dlogits, *, row_weight=None, temperature=1.0,
+                    grad_scale=1.0, stream=None) -> None:
+    """dlogits of zero_policy_fwd from its saved stats; row_weight (times what the rows'
+    losses were weighted with afterwards) is the incoming gradient."""
+    if dlogits is None:
+        raise TypeError("dlogits must be a CUDA (HIP) tensor")
+    _policy_call("zero_policy_bwd", logits, action, None, None, None, row_weight, None, stats,
+                 dlogits, temperature, 0.0, 0.0, 0.0, grad_scale, stream)
+
+
+# ------------------------------------------- norm and clipping of gradients ---
+
+class GradTable:
+    """The gradients of a model as zero_grads_norm and zero_grads_clip take them: their
+    addresses, sizes and types, laid out once for tensors that keep their memory from step
+    to step.  `outs` are where the clipped gradients go (float32 or bfloat16 each); None: in
+    place.  The tensors are held, and a call raises if one of them has moved since."""
+
+    def __init__(self, grads, outs=None):
+        self.grads = list(grads)
+        self.outs = self.grads if outs is None else list(outs)
+        if len(self.outs) != len(self.grads):
+            raise ValueError("as many outs as grads")
+        if len(self.grads) > GRADS_MAX_COUNT:
+            raise ValueError(f"at most {GRADS_MAX_COUNT} tensors")
+        self.device = None
+        for g, o in zip(self.grads, self.outs):
+            for name, t in (("grads", g), ("outs", o)):
+                if not isinstance(t, torch.Tensor) or not t.is_cuda:
+                    raise TypeError(f"{name} are CUDA (HIP) tensors")
+                if t.dtype not in _CODES:
+                    raise TypeError(f"{name} are float32 or bfloat16, not {t.dtype}")
+                if not t.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous")
+                if self.device is None:
+                    self.device = t.get_device()
+                if t.get_device() != self.device:
+                    raise ValueError("the tensors are on one device")
+            if o.numel() != g.numel():
+                raise ValueError(f"an output of {o.numel()} elements for {g.numel()}")
+        n = len(self.grads)
+        self._at = self._addresses()
+        self._sizes = [t.numel() for t in self.grads]
+        flat = [(C.c_uint64 * n)(*self._at[:n]), (C.c_uint64 * n)(*self._at[-n:] if n else ()),
+                (C.c_int64 * n)(*self._sizes),
+                (C.c_int32 * n)(*(_CODES[t.dtype] for t in self.grads)),
+                (C.c_int32 * n)(*(_CODES[t.dtype] for t in self.outs))]
+        self._arrays = flat
+        self._ptrs = tuple(C.addressof(a) for a in flat)
+
+    def _addresses(self):
+        at = [t.data_ptr() for t in self.grads]
+        if self.outs is not self.grads:
+            at += [t.data_ptr() for t in self.outs]
+        return at
+
+    def _checked(self, dev):
+        if self._addresses() != self._at or [t.numel() for t in self.grads] != self._sizes:
+            raise ValueError("a tensor of the table has moved or changed its size: make a new table")
+        if self.grads and self.device != dev:
+            raise ValueError(f"the table is on cuda:{self.device}; the library launches on the "
+                             f"current device, cuda:{dev}")
+        return self._ptrs
+
+
+def zero_grads_workspace_bytes() -> int:
+    return ops_lib().zero_grads_workspace_bytes()
+
+
+def _accs(acc, name, dev):
+    """Address and number of norm accumulators (zero_step.h)."""
+    if acc is None:
+        return 0, 0
+    if not isinstance(acc, torch.Tensor) or not acc.is_cuda or not acc.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous CUDA (HIP) tensor")
+    if acc.get_device() != dev:
+        raise ValueError(f"{name} is on {acc.device}, not on the current device")
+    nbytes = acc.numel() * acc.element_size()
+    if nbytes == 0 or nbytes % 128:
+        raise ValueError(f"{name} holds accumulators of 128 bytes, not {nbytes} bytes")
+    return acc.data_ptr(), nbytes // 128
+
+
+def _scalar(t, name, dtype, dev):
+    if t is None:
+        return 0
+    if isinstance(t, torch.Tensor) and t.numel() != 1:
+        raise ValueError(f"{name} has one element")
+    return _flat(t, name, t.shape if isinstance(t, torch.Tensor) else (1,), dtype, dev)
+
+
+def zero_grads_norm(table, acc, *, inv_scale=1.0, add=False, workspace=None,
+                    stream=None) -> None:
+    """The norm state of grads * inv_scale of a GradTable's tensors into the accumulator acc
+    (new_norm_acc(1)), added to what it holds if `add`: as zero_grad_norm's of the tensors one
+    by one, so that it may be summed over ranks or given to zero_adamw_step.  workspace:
+    zero_grads_workspace_bytes() bytes."""
+    dev = _device()
+    grads, _, sizes, types, _ = table._checked(dev)
+    acc_, n = _accs(acc, "acc", dev)
+    if n > 1:
+        raise ValueError("acc is one accumulator")
+    args = _GRADS_ARGS.pack(_GRADS_ARGS.size, len(table.grads), grads, 0, sizes, types, 0, inv_scale,
+                            acc_, 1 if add else 0, 0, 0, 0.0, 0, 0, 0, 0, 0,
+                            *_workspace(workspace, dev))
+    _call("zero_grads_norm", args, stream, dev)
+
+
+def zero_grads_clip(table, accs, *, max_norm, inv_scale=1.0, check_overflow=False, norm_out=None,
+                    coef_out=None, skipped_out=None, stream=None) -> None:
+    """outs = grads * inv_scale * coef of a GradTable's tensors, with coef and the skip as
+    zero_step_gate gives them for the accumulators accs, max_norm (0: no clipping) and
+    check_overflow; a skipped call writes no tensor.  norm_out and coef_out (float32) and
+    skipped_out (int32), one element each, get the global norm, the coefficient and whether
+    it was skipped."""
+    dev, f32 = _device(), torch.float32
+    grads, outs, sizes, types, out_types = table._checked(dev)
+    accs_, n = _accs(accs, "accs", dev)
+    args = _GRADS_ARGS.pack(_GRADS_ARGS.size, len(table.grads), grads, outs, sizes, types, out_types,
+                            inv_scale, 0, 0, n, accs_, max_norm, 1 if check_overflow else 0, 0,
+                            _scalar(norm_out, "norm_out", f32, dev),
+                            _scalar(coef_out, "coef_out", f32, dev),
+                            _scalar(skipped_out, "skipped_out", torch.int32, dev), 0, 0)
+    _call("zero_grads_clip", args, stream, dev)

@@ -33,7 +33,8 @@ PATTERNS_SOURCES = [os.path.join(HERE, "csrc", "zs_patterns.hip")]
 OPS_LIB = os.path.join(HERE, "libzero_ops.so")
 OPS_SOURCES = [os.path.join(HERE, "csrc", f)
                for f in ("zo_abi.hip", "zo_norm.hip", "zo_attn_fwd.hip", "zo_attn_bwd.hip",
-                         "zo_distill.hip")]
+                         "zo_distill.hip", "zo_embed.hip", "zo_block_norm.hip", "zo_policy.hip",
+                         "zo_grads.hip")]
 
 
 def _compile(sources, out, defines, verbose):

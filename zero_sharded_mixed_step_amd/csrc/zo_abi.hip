@@ -185,6 +185,199 @@ int check_distill(const zero_distill_args* a, bool fwd) {
   return ZERO_OK;
 }
 
+// -------------------------------------------------------------- embedding ---
+
+bool known_dtype(int dtype) { return dtype == ZERO_BF16 || dtype == ZERO_F32; }
+int bytes_of(int dtype) { return dtype == ZERO_BF16 ? 2 : 4; }
+
+// A matrix of n rows: a row of one has a stride that nothing uses.
+int check_matrix(const void* p, int64_t stride, int64_t n, int dtype) {
+  const int64_t s = n > 1 ? stride : 0;
+  return check_rows(p, &s, 1, bytes_of(dtype));
+}
+
+// Rows of C values that do not overlap one another: of an output, or of a gradient.
+bool rows_apart(int64_t stride, int64_t n, int64_t C) {
+  return n <= 1 || stride >= C || stride <= -C;
+}
+
+int check_row_width(int C) {
+  return C < 8 || C > ZERO_ROW_MAX_C || C % 8 != 0 ? ZERO_ESIZE : ZERO_OK;
+}
+
+int check_embed(const zero_embed_args* a, bool fwd) {
+  if (a == nullptr || a->struct_bytes != sizeof(*a)) return ZERO_EINVAL;
+  if (!known_dtype(a->dtype)) return ZERO_EINVAL;
+  if (a->N < 0 || a->V < 1 || !fits_f32(a->scale)) return ZERO_EINVAL;
+  if (a->N > kMaxRows || a->V > ZERO_EMBED_MAX_V) return ZERO_ESIZE;
+  ZO_CHECK(check_row_width(a->C));
+  if (a->N > 0) {
+    if (a->ids == nullptr) return ZERO_EINVAL;
+    if (!aligned(a->ids, 4)) return ZERO_EALIGN;
+  }
+  if (fwd) {
+    if (a->N == 0) return ZERO_OK;
+    ZO_CHECK(check_matrix(a->table, a->table_stride, a->V, a->dtype));
+    ZO_CHECK(check_matrix(a->out, a->out_stride, a->N, a->dtype));
+    return rows_apart(a->out_stride, a->N, a->C) ? ZERO_OK : ZERO_EINVAL;
+  }
+  if (!known_dtype(a->grad_dtype) || (a->base && !known_dtype(a->base_dtype))) return ZERO_EINVAL;
+  ZO_CHECK(check_matrix(a->dtable, a->dtable_stride, a->V, a->grad_dtype));
+  if (!rows_apart(a->dtable_stride, a->V, a->C)) return ZERO_EINVAL;
+  if (a->base != nullptr) {
+    ZO_CHECK(check_matrix(a->base, a->base_stride, a->V, a->base_dtype));
+    if (a->base == a->dtable && (a->base_dtype != a->grad_dtype ||
+                                 (a->V > 1 && a->base_stride != a->dtable_stride)))
+      return ZERO_EINVAL;
+  }
+  if (a->N == 0) return ZERO_OK;
+  ZO_CHECK(check_matrix(a->dout, a->dout_stride, a->N, a->dtype));
+  if (a->workspace == nullptr) return ZERO_EINVAL;
+  if (!aligned(a->workspace, 16)) return ZERO_EALIGN;
+  return a->workspace_bytes < zo::embed_workspace(a->N, a->C) ? ZERO_ESIZE : ZERO_OK;
+}
+
+// ------------------------------------------------------ norms round a block ---
+
+int check_vector(const void* p) { return p && !aligned(p, 16) ? ZERO_EALIGN : ZERO_OK; }
+
+int check_block(const zero_block_norm_args* a, bool fwd) {
+  if (a == nullptr || a->struct_bytes != sizeof(*a)) return ZERO_EINVAL;
+  if (!known_dtype(a->dtype) || (a->res_dtype != a->dtype && a->res_dtype != ZERO_F32))
+    return ZERO_EINVAL;
+  if (a->T < 0 || !(a->eps >= 0.0) || !fits_f32(a->eps) || !fits_f32(a->weight_offset) ||
+      !fits_f32(a->res_scale) || !fits_f32(a->branch_scale))
+    return ZERO_EINVAL;
+  if (a->T > kMaxRows) return ZERO_ESIZE;
+  ZO_CHECK(check_row_width(a->C));
+  // a weight without its norm, a norm or a gate without its block (without rows their
+  // arrays may be NULL)
+  const bool rows = a->T > 0;
+  if ((a->post_w && !a->post_norm) || (rows && !a->y && (a->post_norm || a->gate)))
+    return ZERO_EINVAL;
+  ZO_CHECK(check_vector(a->post_w));
+  ZO_CHECK(check_vector(a->pre_w));
+  const int dt = a->dtype, rt = a->res_dtype;
+  if (a->gate != nullptr) {
+    if (a->gate_tokens && rows) ZO_CHECK(check_matrix(a->gate, a->gate_stride, a->T, dt));
+    else ZO_CHECK(check_vector(a->gate));
+  }
+  if (a->y != nullptr && rows) ZO_CHECK(check_matrix(a->y, a->y_stride, a->T, dt));
+  if (fwd) {
+    if (!rows) return ZERO_OK;
+    if ((!a->h && !a->z) || (a->pre_w && !a->z)) return ZERO_EINVAL;
+    ZO_CHECK(check_matrix(a->x, a->x_stride, a->T, rt));
+    if (a->h != nullptr) {
+      ZO_CHECK(check_matrix(a->h, a->h_stride, a->T, rt));
+      if (!rows_apart(a->h_stride, a->T, a->C)) return ZERO_EINVAL;
+      if (a->h == a->x && a->T > 1 && a->h_stride != a->x_stride) return ZERO_EINVAL;
+    }
+    if (a->z != nullptr) {
+      ZO_CHECK(check_matrix(a->z, a->z_stride, a->T, dt));
+      if (!rows_apart(a->z_stride, a->T, a->C)) return ZERO_EINVAL;
+    }
+    return ZERO_OK;
+  }
+  if ((a->dpost_w && !a->post_w) || (a->dpre_w && !a->pre_w)) return ZERO_EINVAL;
+  if (rows && ((a->dgate && !a->gate) || (a->dy && !a->y) || (a->dpre_w && !a->dz) ||
+               (!a->dh && !a->dz)))
+    return ZERO_EINVAL;
+  const uintptr_t eb = bytes_of(dt);
+  if ((a->dpost_w && !aligned(a->dpost_w, eb)) || (a->dpre_w && !aligned(a->dpre_w, eb)) ||
+      (a->dgate && !aligned(a->dgate, a->gate_tokens ? 16 : eb)))
+    return ZERO_EALIGN;
+  if (!rows) return ZERO_OK;
+  if (a->dz != nullptr) {
+    ZO_CHECK(check_matrix(a->dz, a->dz_stride, a->T, dt));
+    ZO_CHECK(check_matrix(a->h, a->h_stride, a->T, rt));
+  }
+  if (a->dh != nullptr) ZO_CHECK(check_matrix(a->dh, a->dh_stride, a->T, rt));
+  if (a->dx != nullptr) {
+    ZO_CHECK(check_matrix(a->dx, a->dx_stride, a->T, rt));
+    if (!rows_apart(a->dx_stride, a->T, a->C)) return ZERO_EINVAL;
+    if (a->dx == a->dh && a->T > 1 && a->dx_stride != a->dh_stride) return ZERO_EINVAL;
+  }
+  if (a->dy != nullptr) {
+    ZO_CHECK(check_matrix(a->dy, a->dy_stride, a->T, dt));
+    if (!rows_apart(a->dy_stride, a->T, a->C)) return ZERO_EINVAL;
+  }
+  if (a->dgate != nullptr && a->gate_tokens) {
+    ZO_CHECK(check_matrix(a->dgate, a->dgate_stride, a->T, dt));
+    if (!rows_apart(a->dgate_stride, a->T, a->C)) return ZERO_EINVAL;
+  }
+  if (a->dpost_w || a->dpre_w || (a->dgate && !a->gate_tokens)) {
+    if (a->workspace == nullptr) return ZERO_EINVAL;
+    if (!aligned(a->workspace, 16)) return ZERO_EALIGN;
+    if (a->workspace_bytes < zo::block_norm_workspace(a->T, a->C)) return ZERO_ESIZE;
+  }
+  return ZERO_OK;
+}
+
+// ------------------------------------------------------------ policy loss ---
+
+int check_policy(const zero_policy_args* a, bool fwd) {
+  if (a == nullptr || a->struct_bytes != sizeof(*a)) return ZERO_EINVAL;
+  if (!known_dtype(a->dtype)) return ZERO_EINVAL;
+  if (a->N < 0 || a->V < 1) return ZERO_EINVAL;
+  if (a->N > kMaxRows || a->V > ZERO_POLICY_MAX_V) return ZERO_ESIZE;
+  if (!(a->temperature >= 1e-30 && a->temperature <= 1e30) || !fits_f32(a->grad_scale))
+    return ZERO_EINVAL;
+  if (fwd && (!(a->clip_low >= 0.0 && a->clip_low <= 1.0) || !(a->clip_high >= 0.0) ||
+              !fits_f32(a->clip_high) || !fits_f32(a->kl_coef)))
+    return ZERO_EINVAL;
+  if (a->N == 0) return ZERO_OK;
+  if (!a->logits || !a->action || !a->stats) return ZERO_EINVAL;
+  if (fwd ? !a->advantage || !a->loss : !a->dlogits) return ZERO_EINVAL;
+  const uintptr_t eb = bytes_of(a->dtype);
+  if (!aligned(a->logits, eb) || !aligned(a->dlogits, eb) || !aligned(a->action, 4) ||
+      !aligned(a->stats, 4) || !aligned(a->row_weight, 4))
+    return ZERO_EALIGN;
+  if (fwd && (!aligned(a->advantage, 4) || !aligned(a->loss, 4) || !aligned(a->old_logp, 4) ||
+              !aligned(a->ref_logp, 4)))
+    return ZERO_EALIGN;
+  if (a->dlogits && a->dlogits_stride < a->V && a->N > 1) return ZERO_EINVAL;
+  if (a->dlogits == a->logits && a->dlogits_stride != a->logits_stride && a->N > 1)
+    return ZERO_EINVAL;
+  return ZERO_OK;
+}
+
+// ------------------------------------------- norm and clipping of gradients ---
+
+constexpr int64_t kMaxElements = int64_t(1) << 37;   // of a norm accumulator
+
+int check_grads(const zero_grads_args* a, bool norm) {
+  if (a == nullptr || a->struct_bytes != sizeof(*a)) return ZERO_EINVAL;
+  if (a->count < 0 || !fits_f32(a->inv_scale)) return ZERO_EINVAL;
+  if (a->count > ZERO_GRADS_MAX_COUNT) return ZERO_ESIZE;
+  if (a->count > 0 && (!a->grads || !a->sizes || !a->dtypes)) return ZERO_EINVAL;
+  if (!norm && a->count > 0 && (!a->outs || !a->out_dtypes)) return ZERO_EINVAL;
+  int64_t total = 0;
+  for (int64_t i = 0; i < a->count; ++i) {
+    if (a->sizes[i] < 0 || !known_dtype(a->dtypes[i])) return ZERO_EINVAL;
+    if (!norm && !known_dtype(a->out_dtypes[i])) return ZERO_EINVAL;
+    if (a->sizes[i] > kMaxElements - total) return ZERO_ESIZE;
+    total += a->sizes[i];
+    if (a->sizes[i] == 0) continue;
+    if (!a->grads[i] || (!norm && !a->outs[i])) return ZERO_EINVAL;
+    if (!aligned(a->grads[i], bytes_of(a->dtypes[i])) ||
+        (!norm && !aligned(a->outs[i], bytes_of(a->out_dtypes[i]))))
+      return ZERO_EALIGN;
+    if (!norm && a->outs[i] == a->grads[i] && a->dtypes[i] != a->out_dtypes[i])
+      return ZERO_EINVAL;
+  }
+  if (norm) {
+    if (!a->acc || !a->workspace) return ZERO_EINVAL;
+    if (!aligned(a->acc, 16) || !aligned(a->workspace, 16)) return ZERO_EALIGN;
+    return a->workspace_bytes < zo::grads_workspace() ? ZERO_ESIZE : ZERO_OK;
+  }
+  if (a->n_accs < 0 || (a->n_accs > 0 && !a->accs) || !std::isfinite(a->max_norm))
+    return ZERO_EINVAL;
+  if (!aligned(a->accs, 16) || !aligned(a->norm_out, 4) || !aligned(a->coef_out, 4) ||
+      !aligned(a->skipped_out, 4))
+    return ZERO_EALIGN;
+  return ZERO_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -196,13 +389,14 @@ const char* zero_ops_strerror(int status) {
     case ZERO_OK: return "ok";
     case ZERO_EINVAL:
       return "invalid argument (null pointer, struct size, dtype, head counts, scale, cap, "
-             "temperature, bias map, in place with other strides or missing workspace)";
+             "temperature, clipping, bias map, weight or gradient without its input, rows that "
+             "overlap, in place with other strides or dtypes, or missing workspace)";
     case ZERO_EALIGN:
-      return "pointer or stride misaligned (head rows and workspaces need 16 bytes, ranges 8, "
-             "other arrays their element)";
+      return "pointer or stride misaligned (rows, their weights, accumulators and workspaces need "
+             "16 bytes, ranges 8, other arrays their element)";
     case ZERO_ESIZE:
-      return "size not supported (head dimension, rotation, lengths, reach, buckets, K, V) or "
-             "workspace too small";
+      return "size not supported (head dimension, rotation, lengths, width, reach, buckets, K, V, "
+             "count) or workspace too small";
     case ZERO_EHIP: return "HIP runtime error at launch";
     default: return "unknown status";
   }
@@ -293,5 +487,91 @@ int zero_distill_bwd(const zero_distill_args* a, void* stream) {
     return ZERO_EHIP;
   }
 }
+
+int zero_embed_fwd(const zero_embed_args* a, void* stream) {
+  try {
+    ZO_CHECK(check_embed(a, true));
+    if (a->N == 0) return ZERO_OK;
+    return status_of(zo::launch_embed_fwd(*a, as_stream(stream)));
+  } catch (...) {
+    return ZERO_EHIP;
+  }
+}
+
+int zero_embed_bwd(const zero_embed_args* a, void* stream) {
+  try {
+    ZO_CHECK(check_embed(a, false));
+    return status_of(zo::launch_embed_bwd(*a, as_stream(stream)));
+  } catch (...) {
+    return ZERO_EHIP;
+  }
+}
+
+size_t zero_embed_workspace_bytes(int64_t N, int C) {
+  return N <= 0 || C < 0 || N > kMaxRows || C > ZERO_ROW_MAX_C ? 0 : zo::embed_workspace(N, C);
+}
+
+int zero_block_norm_fwd(const zero_block_norm_args* a, void* stream) {
+  try {
+    ZO_CHECK(check_block(a, true));
+    if (a->T == 0) return ZERO_OK;
+    return status_of(zo::launch_block_norm_fwd(*a, as_stream(stream)));
+  } catch (...) {
+    return ZERO_EHIP;
+  }
+}
+
+int zero_block_norm_bwd(const zero_block_norm_args* a, void* stream) {
+  try {
+    ZO_CHECK(check_block(a, false));
+    return status_of(zo::launch_block_norm_bwd(*a, as_stream(stream)));
+  } catch (...) {
+    return ZERO_EHIP;
+  }
+}
+
+size_t zero_block_norm_workspace_bytes(int64_t T, int C) {
+  return T <= 0 || C < 0 || C > ZERO_ROW_MAX_C ? 0 : zo::block_norm_workspace(T, C);
+}
+
+int zero_policy_fwd(const zero_policy_args* a, void* stream) {
+  try {
+    ZO_CHECK(check_policy(a, true));
+    if (a->N == 0) return ZERO_OK;
+    return status_of(zo::launch_policy(*a, true, as_stream(stream)));
+  } catch (...) {
+    return ZERO_EHIP;
+  }
+}
+
+int zero_policy_bwd(const zero_policy_args* a, void* stream) {
+  try {
+    ZO_CHECK(check_policy(a, false));
+    if (a->N == 0) return ZERO_OK;
+    return status_of(zo::launch_policy(*a, false, as_stream(stream)));
+  } catch (...) {
+    return ZERO_EHIP;
+  }
+}
+
+int zero_grads_norm(const zero_grads_args* a, void* stream) {
+  try {
+    ZO_CHECK(check_grads(a, true));
+    return status_of(zo::launch_grads_norm(*a, as_stream(stream)));
+  } catch (...) {
+    return ZERO_EHIP;
+  }
+}
+
+int zero_grads_clip(const zero_grads_args* a, void* stream) {
+  try {
+    ZO_CHECK(check_grads(a, false));
+    return status_of(zo::launch_grads_clip(*a, as_stream(stream)));
+  } catch (...) {
+    return ZERO_EHIP;
+  }
+}
+
+size_t zero_grads_workspace_bytes(void) { return zo::grads_workspace(); }
 
 }  // extern "C"

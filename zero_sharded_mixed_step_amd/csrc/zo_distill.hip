@@ -7,9 +7,7 @@
 // row-wide sum, so a row is cut into pieces over workgroups.
 //
 // Rows may start at any element (an odd vocabulary makes every other row of a
-// bf16 matrix misaligned): a row is taken as 16-byte chunks counted from the
-// aligned address at or below its start, and its first and last chunk are
-// loaded and stored element by element.
+// bf16 matrix misaligned): zo_rows.h takes them as 16-byte chunks.
 //
 // The teacher's K entries and everything of them is formed in binary64: the
 // tail's mass is a difference from 1.  The entries' positions are marked in a
@@ -21,6 +19,7 @@
 // 168 us, 6.4 TB/s, 2048 x 50257 bf16 76 us, 5.4.
 #include "zo_device.h"
 #include "zo_internal.h"
+#include "zo_rows.h"
 
 namespace zo {
 
@@ -43,107 +42,6 @@ struct DistillParams {
   int64_t z_stride, dz_stride;
   int seg;  // backward: chunks of a piece
 };
-
-template <typename E>
-struct Chunk;
-template <>
-struct Chunk<bf16> {
-  static constexpr int kN = 8;
-  u32x4 r;
-  __device__ __forceinline__ float get(int e) const {
-    return e & 1 ? __uint_as_float(r[e >> 1] & 0xFFFF0000u) : bf16_bits_to_f32(r[e >> 1]);
-  }
-  __device__ __forceinline__ void fill_lowest() {  // -inf
-    r = u32x4{0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u};
-  }
-  __device__ __forceinline__ void put_raw(int e, bf16 x) {
-    union {
-      bf16 b;
-      uint16_t u;
-    } c;
-    c.b = x;
-    const uint32_t bits = c.u;
-    r[e >> 1] = e & 1 ? (r[e >> 1] & 0x0000FFFFu) | (bits << 16) : (r[e >> 1] & 0xFFFF0000u) | bits;
-  }
-};
-template <>
-struct Chunk<float> {
-  static constexpr int kN = 4;
-  f32x4 r;
-  __device__ __forceinline__ float get(int e) const { return r[e]; }
-  __device__ __forceinline__ void fill_lowest() { r = f32x4{-kInf, -kInf, -kInf, -kInf}; }
-  __device__ __forceinline__ void put_raw(int e, float x) { r[e] = x; }
-};
-
-template <typename E>
-__device__ __forceinline__ float value(const void* p, int64_t at) {
-  return static_cast<float>(static_cast<const E*>(p)[at]);
-}
-
-// A row as aligned chunks: chunk c holds elements c * kN - shift .. + kN - 1.
-template <typename E>
-struct Row {
-  static constexpr int kN = Chunk<E>::kN;
-  E* p;       // element 0
-  int shift;
-  int64_t V;
-  __device__ __forceinline__ Row(const void* base, int64_t at, int64_t v)
-      : p(const_cast<E*>(static_cast<const E*>(base)) + at), V(v) {
-    shift = static_cast<int>((reinterpret_cast<uintptr_t>(p) / sizeof(E)) % kN);
-  }
-  __device__ __forceinline__ int chunks() const {
-    return static_cast<int>((V + shift + kN - 1) / kN);
-  }
-  __device__ __forceinline__ bool whole(int c) const {
-    const int64_t e0 = static_cast<int64_t>(c) * kN - shift;
-    return e0 >= 0 && e0 + kN <= V;
-  }
-  __device__ __forceinline__ Chunk<E> load(int c) const {
-    Chunk<E> x;
-    const int64_t e0 = static_cast<int64_t>(c) * kN - shift;
-    if (whole(c)) {
-      x.r = *reinterpret_cast<const decltype(x.r)*>(p + e0);
-    } else {
-      x.fill_lowest();
-#pragma unroll
-      for (int e = 0; e < kN; ++e)
-        if (e0 + e >= 0 && e0 + e < V) x.put_raw(e, p[e0 + e]);
-    }
-    return x;
-  }
-  // y as this row's elements that chunk c of a row shifted by `from` holds
-  __device__ __forceinline__ void store(int c, int from, const float y[kN]) const {
-    const int64_t e0 = static_cast<int64_t>(c) * kN - from;
-    if (from == shift && e0 >= 0 && e0 + kN <= V) {
-      Chunk<E> x;
-      if constexpr (sizeof(E) == 2) {
-        union {
-          bf16x8 b;
-          u32x4 u;
-        } v;
-#pragma unroll
-        for (int e = 0; e < kN; ++e) v.b[e] = static_cast<bf16>(y[e]);
-        x.r = v.u;
-      } else {
-#pragma unroll
-        for (int e = 0; e < kN; ++e) x.r[e] = y[e];
-      }
-      *reinterpret_cast<decltype(x.r)*>(p + e0) = x.r;
-    } else {
-#pragma unroll
-      for (int e = 0; e < kN; ++e)
-        if (e0 + e >= 0 && e0 + e < V) p[e0 + e] = static_cast<E>(y[e]);
-    }
-  }
-};
-
-// Between the passes over a held row: its values are unpacked again in the next
-// pass, not carried over as twice the registers.
-template <typename E, int CH>
-__device__ __forceinline__ void keep_packed(Chunk<E> (&held)[CH]) {
-#pragma unroll
-  for (int c = 0; c < CH; ++c) asm volatile("" : "+v"(held[c].r));
-}
 
 // The teacher's side of a row, in shared memory: p[k], the student's logit
 // z[k] (of entries in [from, to)) and idx[k], -1 for an absent entry; and what

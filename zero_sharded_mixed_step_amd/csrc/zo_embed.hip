@@ -1,0 +1,423 @@
+// zo_embed.hip -- the embedding lookup with a factor, and the table's gradient.
+//
+// Both move rows and compute next to nothing: bound by memory.  Forward, a wave
+// copies a piece of a token's row.
+//
+// Backward, sum over the tokens of a row in a fixed order: the tokens are sorted by
+// id (equal ids by place), the sorted list is cut into chunks of P places, a wave sums
+// the rows of a chunk for 512 columns, one run of equal ids after another, and what a
+// chunk's first and last run share with its neighbours goes through the workspace and is
+// joined chunk by chunk.  The work of a wave does not depend on how often an id occurs.
+// Waves beside those write the rows that no id names.
+//
+// Sorting needs each place's rank, the number of (id, place) pairs below its own.  It is
+// counted: within a tile of 2048 places by comparing with all of them (two instructions a
+// comparison, spread over the card), and over the other tiles by searching their sorted
+// lists.  No pass depends on the ids' distribution, and there are one or two launches.
+#include "zo_device.h"
+#include "zo_internal.h"
+#include "zo_rows.h"
+
+namespace zo {
+
+constexpr int kRankTile = 2048;               // places that are ranked by comparison
+constexpr int kRankWaves = 16;                // waves that share a tile's comparisons
+constexpr int kSlice = 512;                   // columns of a wave: 8 a lane
+constexpr int kEmbedThreads = 256, kEmbedWaves = kEmbedThreads / 64;
+constexpr int kFillRows = 8;                  // table rows of a wave that writes what no id names
+
+struct EmbedParams {
+  int64_t N, V;
+  int C, slices, P, chunks;
+  float scale;
+  const int32_t* ids;
+  const void* table;
+  void* out;
+  const void* dout;
+  const void* base;
+  void* dtable;
+  int64_t table_s, out_s, dout_s, base_s, dtable_s;
+  int32_t *key, *place;                       // sorted
+  int32_t *tile_key, *tile_place;             // sorted within tiles
+  float* part;                                // [chunks][2][C]: a chunk's first and last run
+  int64_t sum_units;
+  bool fill;
+};
+
+// ---------------------------------------------------------------- forward ---
+
+template <typename E>
+__global__ __launch_bounds__(kEmbedThreads) void embed_fwd_kernel(const EmbedParams p) {
+  constexpr int kU = 4;
+  const int lane = threadIdx.x & 63;
+  const int64_t unit =
+      static_cast<int64_t>(blockIdx.x) * kEmbedWaves + uniform(threadIdx.x >> 6);
+  const int64_t n = unit / p.slices;
+  if (n >= p.N) return;
+  const int c0 = static_cast<int>(unit % p.slices) * kSlice * kU + 8 * lane;
+  const int32_t id = p.ids[n];
+  const bool on = id >= 0 && id < p.V;
+  Vec8<E> raw[kU];
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    raw[u] = Vec8<E>{};
+    if (on && c0 + u * kSlice < p.C) raw[u].load(p.table, id * p.table_s + c0 + u * kSlice);
+  }
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    float x[8];
+    raw[u].get(x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] *= p.scale;
+    if (!on) {                                // (a factor that is not finite, too)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = 0.f;
+    }
+    if (c0 + u * kSlice < p.C) Vec8<E>::store(p.out, n * p.out_s + c0 + u * kSlice, x);
+  }
+}
+
+// ------------------------------------------------------------------- sort ---
+
+// The id of place n, those outside the table behind all others.
+__device__ __forceinline__ int32_t key_of(const EmbedParams& p, int64_t n) {
+  const int32_t id = p.ids[n];
+  return id >= 0 && id < p.V ? id : static_cast<int32_t>(p.V);
+}
+
+// Ranks 64 places of a tile, one a lane: each of the 16 waves compares them with 128 of it.
+__global__ __launch_bounds__(64 * kRankWaves) void embed_rank_kernel(const EmbedParams p,
+                                                                    int32_t* key,
+                                                                    int32_t* place) {
+  __shared__ int below[kRankWaves][64];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * 64 + lane;
+  const int64_t tile = n / kRankTile * kRankTile;
+  constexpr int kShare = kRankTile / kRankWaves;
+  const int32_t mine = n < p.N ? key_of(p, n) : 0;
+  const int32_t own = static_cast<int32_t>(n - tile);
+  int rank = 0;
+#pragma unroll
+  for (int h = 0; h < kShare / 64; ++h) {
+    const int first = wave * kShare + h * 64;
+    const int64_t m = tile + first + lane;
+    const int32_t other = m < p.N ? key_of(p, m) : INT32_MAX;
+#pragma unroll 16
+    for (int i = 0; i < 64; ++i) {
+      const int32_t k = __builtin_amdgcn_readlane(other, i);
+      rank += k < mine + (first + i < own ? 1 : 0);
+    }
+  }
+  below[wave][lane] = rank;
+  __syncthreads();
+  if (wave == 0 && n < p.N) {
+    rank = 0;
+#pragma unroll
+    for (int w = 0; w < kRankWaves; ++w) rank += below[w][lane];
+    key[tile + rank] = mine;
+    place[tile + rank] = static_cast<int32_t>(n);
+  }
+}
+
+// How many keys of the sorted list are below `mine` (with `equal`: or equal to it).
+__device__ __forceinline__ int count_below(const int32_t* list, int n, int32_t mine, bool equal) {
+  const int32_t limit = mine + (equal ? 1 : 0);
+  int at = 0;
+#pragma unroll
+  for (int step = kRankTile; step > 0; step >>= 1) {
+    const int next = at + step;
+    if (next <= n && list[next - 1] < limit) at = next;
+  }
+  return at;
+}
+
+// Joins the sorted tiles: a place's rank is its rank in its tile and, of the other
+// tiles, what is below it (of tiles before its own also what is equal).
+__global__ __launch_bounds__(64 * kRankWaves) void embed_merge_kernel(const EmbedParams p) {
+  __shared__ int below[kRankWaves][64];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 64 + lane;
+  const int own = static_cast<int>(static_cast<int64_t>(blockIdx.x) * 64 / kRankTile);
+  const int tiles = static_cast<int>((p.N + kRankTile - 1) / kRankTile);
+  const int32_t mine = at < p.N ? p.tile_key[at] : 0;
+  int rank = 0;
+  for (int t = wave; t < tiles; t += kRankWaves) {
+    if (t == own) continue;
+    const int64_t first = static_cast<int64_t>(t) * kRankTile;
+    const int n = static_cast<int>(p.N - first < kRankTile ? p.N - first : kRankTile);
+    rank += count_below(p.tile_key + first, n, mine, t < own);
+  }
+  below[wave][lane] = rank;
+  __syncthreads();
+  if (wave == 0 && at < p.N) {
+    int64_t to = at - static_cast<int64_t>(own) * kRankTile;
+#pragma unroll
+    for (int w = 0; w < kRankWaves; ++w) to += below[w][lane];
+    p.key[to] = mine;
+    p.place[to] = p.tile_place[at];
+  }
+}
+
+// --------------------------------------------------------------- backward ---
+
+template <typename B>
+__device__ __forceinline__ void base_row(const EmbedParams& p, int64_t v, int c, float x[8]) {
+  Vec8<B> r;
+  r.load(p.base, v * p.base_s + c);
+  r.get(x);
+}
+
+// dtable[v] = base[v] + scale * sum, 8 columns.
+template <typename G, typename B>
+__device__ __forceinline__ void store_row(const EmbedParams& p, int64_t v, int c,
+                                          const float sum[8]) {
+  float y[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y[j] = sum[j] * p.scale;
+  if (p.base != nullptr) {
+    float b[8];
+    base_row<B>(p, v, c, b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = __builtin_fmaf(sum[j], p.scale, b[j]);
+  }
+  Vec8<G>::store(p.dtable, v * p.dtable_s + c, y);
+}
+
+__device__ __forceinline__ void store_part(const EmbedParams& p, int64_t chunk, int which, int c,
+                                           const float sum[8]) {
+  Vec8<float>::store(p.part, (chunk * 2 + which) * p.C + c, sum);
+}
+
+// A wave's chunk of sorted places, for 512 columns.
+template <typename E, typename G, typename B>
+__device__ __forceinline__ void sum_chunk(const EmbedParams& p, int64_t unit, int lane) {
+  constexpr int kAtOnce = 8;                  // rows under way
+  const int64_t chunk = unit / p.slices, first = chunk * p.P;
+  const int c = static_cast<int>(unit % p.slices) * kSlice + 8 * lane;
+  const bool on = c < p.C;
+  const int32_t none = static_cast<int32_t>(p.V);
+  const bool in = lane < p.P && first + lane < p.N;
+  const int32_t key = in ? p.key[first + lane] : none;
+  const int32_t place = in ? p.place[first + lane] : 0;
+  const int32_t before = first > 0 ? p.key[first - 1] : -1;
+  const int32_t after = first + p.P < p.N ? p.key[first + p.P] : none;
+  const int count = __popcll(__ballot(key < none));        // (sorted: the first lanes)
+  if (count == 0) return;
+  float sum[8] = {};
+  int32_t run = __builtin_amdgcn_readlane(key, 0);
+  bool shared = run == before;                // the run began in an earlier chunk
+  for (int i0 = 0; i0 < count; i0 += kAtOnce) {
+    Vec8<E> raw[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      raw[u] = Vec8<E>{};
+      if (i0 + u < count && on) {
+        const int64_t n = __builtin_amdgcn_readlane(place, i0 + u);
+        raw[u].load(p.dout, n * p.dout_s + c);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      if (i0 + u >= count) break;
+      const int32_t k = __builtin_amdgcn_readlane(key, i0 + u);
+      float x[8];
+      raw[u].get(x);
+      if (k != run) {
+        if (on) {
+          if (shared) store_part(p, chunk, 0, c, sum);
+          else store_row<G, B>(p, run, c, sum);
+        }
+        run = k;
+        shared = false;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] = x[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += x[j];
+      }
+    }
+  }
+  if (!on) return;
+  if (shared) store_part(p, chunk, 0, c, sum);
+  else if (run == after) store_part(p, chunk, 1, c, sum);
+  else store_row<G, B>(p, run, c, sum);
+}
+
+// Rows of the table that no id names: base, or zeros.
+template <typename G, typename B>
+__device__ __forceinline__ void fill_rows(const EmbedParams& p, int64_t unit, int lane) {
+  const int64_t v0 = unit * kFillRows;
+  const int64_t v = v0 + lane;
+  bool absent = lane < kFillRows && v < p.V;
+  if (absent) {
+    int64_t at = 0;                           // how many keys are below v
+    for (int64_t step = int64_t(1) << 21; step > 0; step >>= 1)
+      if (at + step <= p.N && p.key[at + step - 1] < v) at += step;
+    absent = at >= p.N || p.key[at] != v;
+  }
+  uint64_t rows = __ballot(absent);
+  while (rows != 0) {
+    const int64_t row = v0 + __builtin_ctzll(rows);
+    rows &= rows - 1;
+    for (int c = 8 * lane; c < p.C; c += kSlice) {
+      float x[8] = {};
+      if (p.base != nullptr) base_row<B>(p, row, c, x);
+      Vec8<G>::store(p.dtable, row * p.dtable_s + c, x);
+    }
+  }
+}
+
+template <typename E, typename G, typename B>
+__global__ __launch_bounds__(kEmbedThreads) void embed_sum_kernel(const EmbedParams p) {
+  const int lane = threadIdx.x & 63;
+  const int64_t unit =
+      static_cast<int64_t>(blockIdx.x) * kEmbedWaves + uniform(threadIdx.x >> 6);
+  if (unit < p.sum_units) sum_chunk<E, G, B>(p, unit, lane);
+  else if (p.fill && (unit - p.sum_units) * kFillRows < p.V)
+    fill_rows<G, B>(p, unit - p.sum_units, lane);
+}
+
+// The runs that go over a chunk's end, by the chunk that they begin in: its last part
+// and the first parts of the chunks after it, in order, every fourth by a wave.
+template <typename G, typename B>
+__global__ __launch_bounds__(kEmbedThreads) void embed_join_kernel(const EmbedParams p) {
+  __shared__ float fold[kEmbedWaves][kSlice];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int64_t chunk = blockIdx.x, first = chunk * p.P;
+  if (first + p.P >= p.N) return;
+  const int32_t run = p.key[first + p.P - 1];
+  if (run >= p.V || p.key[first + p.P] != run || (first > 0 && p.key[first - 1] == run)) return;
+  int64_t more = 0;                           // chunks after this one that begin with the run
+  for (;;) {
+    const int64_t at = (chunk + 1 + more + lane) * p.P;
+    const uint64_t same = __ballot(at < p.N && p.key[at] == run);
+    const int n = ~same == 0 ? 64 : __builtin_ctzll(~same);
+    more += n;
+    if (n < 64) break;
+  }
+  for (int s = 0; s < p.slices; ++s) {
+    const int c = s * kSlice + 8 * lane;
+    const bool on = c < p.C;
+    float sum[8] = {};
+#pragma unroll 4
+    for (int64_t q = wave; q <= more; q += kEmbedWaves) {
+      if (on) {
+        Vec8<float> r;
+        r.load(p.part, ((chunk + q) * 2 + (q == 0 ? 1 : 0)) * p.C + c);
+        float x[8];
+        r.get(x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += x[j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) fold[wave][8 * lane + j] = sum[j];
+    __syncthreads();
+    if (wave == 0 && on) {
+#pragma unroll
+      for (int w = 1; w < kEmbedWaves; ++w)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += fold[w][8 * lane + j];
+      store_row<G, B>(p, run, c, sum);
+    }
+    __syncthreads();
+  }
+}
+
+namespace {
+
+// Places of a chunk: enough chunks to fill the card, no more than a wave's lanes.
+int chunk_places(int64_t N) {
+  const int64_t p = (N + 1023) / 1024;
+  return static_cast<int>(p < 4 ? 4 : p > 64 ? 64 : p);
+}
+
+int64_t chunks_of(int64_t N) { return (N + chunk_places(N) - 1) / chunk_places(N); }
+
+size_t rounded(size_t n) { return (n + 15) & ~size_t(15); }
+
+template <typename E, typename G, typename B>
+hipError_t run_sums(const EmbedParams& p, hipStream_t s) {
+  const int64_t units = p.sum_units + (p.fill ? (p.V + kFillRows - 1) / kFillRows : 0);
+  const unsigned grid = static_cast<unsigned>((units + kEmbedWaves - 1) / kEmbedWaves);
+  if (grid == 0) return hipSuccess;
+  embed_sum_kernel<E, G, B><<<grid, kEmbedThreads, 0, s>>>(p);
+  if (p.chunks > 1) embed_join_kernel<G, B><<<p.chunks, kEmbedThreads, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+template <typename E, typename G>
+hipError_t pick_base(const EmbedParams& p, int base_dtype, hipStream_t s) {
+  return base_dtype == ZERO_BF16 ? run_sums<E, G, bf16>(p, s) : run_sums<E, G, float>(p, s);
+}
+
+template <typename E>
+hipError_t pick_grad(const EmbedParams& p, const zero_embed_args& a, hipStream_t s) {
+  return a.grad_dtype == ZERO_BF16 ? pick_base<E, bf16>(p, a.base_dtype, s)
+                                   : pick_base<E, float>(p, a.base_dtype, s);
+}
+
+}  // namespace
+
+size_t embed_workspace(int64_t N, int C) {
+  return 4 * rounded(N * sizeof(int32_t)) +
+         static_cast<size_t>(chunks_of(N)) * 2 * C * sizeof(float);
+}
+
+hipError_t launch_embed_fwd(const zero_embed_args& a, hipStream_t s) {
+  EmbedParams p = {};
+  p.N = a.N;
+  p.V = a.V;
+  p.C = a.C;
+  p.scale = static_cast<float>(a.scale);
+  p.ids = a.ids;
+  p.table = a.table;
+  p.out = a.out;
+  p.table_s = a.table_stride;
+  p.out_s = a.out_stride;
+  p.slices = (a.C + 4 * kSlice - 1) / (4 * kSlice);
+  const unsigned grid =
+      static_cast<unsigned>((p.N * p.slices + kEmbedWaves - 1) / kEmbedWaves);
+  if (a.dtype == ZERO_BF16) embed_fwd_kernel<bf16><<<grid, kEmbedThreads, 0, s>>>(p);
+  else embed_fwd_kernel<float><<<grid, kEmbedThreads, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+hipError_t launch_embed_bwd(const zero_embed_args& a, hipStream_t s) {
+  EmbedParams p = {};
+  p.N = a.N;
+  p.V = a.V;
+  p.C = a.C;
+  p.scale = static_cast<float>(a.scale);
+  p.ids = a.ids;
+  p.dout = a.dout;
+  p.base = a.base;
+  p.dtable = a.dtable;
+  p.dout_s = a.dout_stride;
+  p.base_s = a.base_stride;
+  p.dtable_s = a.dtable_stride;
+  p.slices = (a.C + kSlice - 1) / kSlice;
+  p.P = chunk_places(a.N);
+  p.chunks = static_cast<int>(chunks_of(a.N));
+  p.sum_units = static_cast<int64_t>(p.chunks) * p.slices;
+  p.fill = a.base != a.dtable;
+  char* ws = static_cast<char*>(a.workspace);
+  const size_t list = rounded(a.N * sizeof(int32_t));
+  p.key = reinterpret_cast<int32_t*>(ws);
+  p.place = reinterpret_cast<int32_t*>(ws + list);
+  p.tile_key = reinterpret_cast<int32_t*>(ws + 2 * list);
+  p.tile_place = reinterpret_cast<int32_t*>(ws + 3 * list);
+  p.part = reinterpret_cast<float*>(ws + 4 * list);
+  if (a.N > 0) {
+    const unsigned grid = static_cast<unsigned>((a.N + 63) / 64);
+    const bool tiles = a.N > kRankTile;
+    embed_rank_kernel<<<grid, 64 * kRankWaves, 0, s>>>(p, tiles ? p.tile_key : p.key,
+                                                      tiles ? p.tile_place : p.place);
+    if (tiles) embed_merge_kernel<<<grid, 64 * kRankWaves, 0, s>>>(p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return a.dtype == ZERO_BF16 ? pick_grad<bf16>(p, a, s) : pick_grad<float>(p, a, s);
+}
+
+}  // namespace zo

@@ -23,4 +23,18 @@ size_t attn_bwd_workspace(int B, int Tq, int Tk, int Hq, int Hk, int D, int n_bu
 
 hipError_t launch_distill(const zero_distill_args& a, bool forward, hipStream_t s);
 
+hipError_t launch_embed_fwd(const zero_embed_args& a, hipStream_t s);
+hipError_t launch_embed_bwd(const zero_embed_args& a, hipStream_t s);
+size_t embed_workspace(int64_t N, int C);
+
+hipError_t launch_block_norm_fwd(const zero_block_norm_args& a, hipStream_t s);
+hipError_t launch_block_norm_bwd(const zero_block_norm_args& a, hipStream_t s);
+size_t block_norm_workspace(int64_t T, int C);
+
+hipError_t launch_policy(const zero_policy_args& a, bool forward, hipStream_t s);
+
+hipError_t launch_grads_norm(const zero_grads_args& a, hipStream_t s);
+hipError_t launch_grads_clip(const zero_grads_args& a, hipStream_t s);
+size_t grads_workspace();
+
 }  // namespace zo

@@ -12,6 +12,7 @@
 // backward of 8192 tokens 60 us, 4.2 TB/s.
 #include "zo_device.h"
 #include "zo_internal.h"
+#include "zo_rows.h"
 
 namespace zo {
 
@@ -37,50 +38,6 @@ struct NormParams {
   int D, rot, interleaved;
   float eps;
   float* part;  // backward: [2][groups][D]
-};
-
-template <typename E>
-struct Vec8;
-template <>
-struct Vec8<bf16> {
-  u32x4 r;
-  __device__ __forceinline__ void load(const void* p, int64_t at) {
-    r = *reinterpret_cast<const u32x4*>(static_cast<const bf16*>(p) + at);
-  }
-  __device__ __forceinline__ void get(float x[8]) const {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[2 * j] = bf16_bits_to_f32(r[j]);
-      x[2 * j + 1] = __uint_as_float(r[j] & 0xFFFF0000u);
-    }
-  }
-  __device__ __forceinline__ static void store(void* p, int64_t at, const float x[8]) {
-    bf16x8 v;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = static_cast<bf16>(x[j]);
-    *reinterpret_cast<bf16x8*>(static_cast<bf16*>(p) + at) = v;
-  }
-};
-template <>
-struct Vec8<float> {
-  f32x4 a, b;
-  __device__ __forceinline__ void load(const void* p, int64_t at) {
-    const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + at);
-    a = q[0];
-    b = q[1];
-  }
-  __device__ __forceinline__ void get(float x[8]) const {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[j] = a[j];
-      x[4 + j] = b[j];
-    }
-  }
-  __device__ __forceinline__ static void store(void* p, int64_t at, const float x[8]) {
-    f32x4* q = reinterpret_cast<f32x4*>(static_cast<float*>(p) + at);
-    q[0] = f32x4{x[0], x[1], x[2], x[3]};
-    q[1] = f32x4{x[4], x[5], x[6], x[7]};
-  }
 };
 
 // The value of the lane half a group of G away.
@@ -174,10 +131,6 @@ template <int G>
 __device__ __forceinline__ float sum_row(float x) {
   return join_lanes<G>(x, AddOp());
 }
-
-// Whether a row's mean square plus eps is near the ends of binary32 (the reciprocal root takes
-// no subnormal numbers): of values below 1e-15 with an eps below 1e-30, or above 1e15.
-__device__ __forceinline__ bool far_mean(float v) { return !(v >= 1e-30f && v <= 1e30f); }
 
 // 1 / sqrt(mean(x^2) + eps) of such a row, from x times a power of 2.
 template <int G>

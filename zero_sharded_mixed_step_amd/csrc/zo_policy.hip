@@ -1,0 +1,385 @@
+// zo_policy.hip -- the clipped policy loss with a KL term, on sampled tokens.
+//
+// Bound by memory, as the distillation loss: the logits are read once and their
+// gradient is written once.  A workgroup owns a row and keeps it in registers (packed
+// as it came) between the maximum, the sum and the gradient, or, when the row is too long
+// for that, reads it again.  The backward pass needs no row-wide sum, so a row is cut
+// into pieces over workgroups.
+//
+// The sampled token is left out of the sum and added to it in binary64: with rest the sum of
+// the others' powers and own its own, lp = -log(1 + rest / own) and 1 - q_a = rest /
+// total keep their digits however sure the student is of the token.  What follows from lp
+// (ratio, clipping, KL term) is some binary64 operations a row.
+#include "zo_device.h"
+#include "zo_internal.h"
+#include "zo_rows.h"
+
+namespace zo {
+
+struct PolicyParams {
+  int64_t N, V;
+  double inv_tau, low, high, kl_coef, grad_scale;   // low, high: the ratio's borders
+  const void* z;
+  const int32_t* action;
+  const float *adv, *old_lp, *ref_lp, *weight;
+  float *loss, *stats;
+  void* dz;
+  int64_t z_stride, dz_stride;
+  int seg;                                          // backward: chunks of a piece
+};
+
+// The row's coefficient in the gradient, grad_scale w g / tau, within binary32: where it
+// is past its ends a probability of 0 must still give 0.
+__device__ __forceinline__ float coefficient(const PolicyParams& p, float w, double g) {
+  const double c = p.grad_scale * static_cast<double>(w) * p.inv_tau *
+                   (g > -kLowest ? -static_cast<double>(kLowest)
+                                 : g < kLowest ? static_cast<double>(kLowest) : g);
+  return c > -static_cast<double>(kLowest) ? -kLowest
+         : c < static_cast<double>(kLowest) ? kLowest : static_cast<float>(c);
+}
+
+// Logarithm and exponential of the row's numbers in binary64 with some 1e-12 of relative error,
+// by their series: one thread works on them while the row waits, and the library's, whose
+// last digits nobody needs here, take several times the steps.
+//
+// log(1 + x), -0.3 < x < 0.42, with the relative error kept for small x: 2 artanh(v)
+// with v = x / (2 + x), |v| < 0.175.
+__device__ __forceinline__ double log_near(double x) {
+  const double v = x / (2.0 + x), q = v * v;
+  double s = 1.0 / 15;
+  s = __builtin_fma(s, q, 1.0 / 13);
+  s = __builtin_fma(s, q, 1.0 / 11);
+  s = __builtin_fma(s, q, 1.0 / 9);
+  s = __builtin_fma(s, q, 1.0 / 7);
+  s = __builtin_fma(s, q, 1.0 / 5);
+  s = __builtin_fma(s, q, 1.0 / 3);
+  return __builtin_fma(s * q, 2.0 * v, 2.0 * v);
+}
+
+// log x, 2^-1000 < x < 2^1000.
+__device__ __forceinline__ double log_of(double x) {
+  const double m = __builtin_amdgcn_frexp_mant(x);
+  const bool low = m < 0.70710678118654752;
+  const double f = low ? m + m : m;            // in [0.7, 1.42)
+  const int k = __builtin_amdgcn_frexp_exp(x) - (low ? 1 : 0);
+  return __builtin_fma(static_cast<double>(k), 0.69314718055994531, log_near(f - 1.0));
+}
+
+// e^x - 1 - x for x = k log 2 + t: (2^k (1 + t + w) - 1) - x with w = e^t - 1 - t by
+// Taylor, |t| < 0.35, and w itself where k is 0.  Also gives e^x.
+__device__ __forceinline__ double exp_series(double x, double& beyond) {
+  if (!(x > -745.0)) {                         // (a NaN too)
+    const double e = x <= -745.0 ? 0.0 : x;
+    beyond = e - 1.0 - x;
+    return e;
+  }
+  if (x > 710.0) {
+    beyond = __builtin_huge_val();
+    return beyond;
+  }
+  const double k = __builtin_rint(x * 1.4426950408889634);
+  const double t = __builtin_fma(-k, 1.9082149292705877e-10,
+                                 __builtin_fma(-k, 0.69314718036912382, x));
+  double w = 1.0 / 39916800;                   // 1 / 11!
+  w = __builtin_fma(w, t, 1.0 / 3628800);
+  w = __builtin_fma(w, t, 1.0 / 362880);
+  w = __builtin_fma(w, t, 1.0 / 40320);
+  w = __builtin_fma(w, t, 1.0 / 5040);
+  w = __builtin_fma(w, t, 1.0 / 720);
+  w = __builtin_fma(w, t, 1.0 / 120);
+  w = __builtin_fma(w, t, 1.0 / 24);
+  w = __builtin_fma(w, t, 1.0 / 6);
+  w = __builtin_fma(w, t, 0.5);
+  w = w * t * t;
+  const double e = __builtin_amdgcn_ldexp(1.0 + (t + w), static_cast<int>(k));
+  beyond = k == 0.0 ? w : e - 1.0 - x;
+  return e;
+}
+
+struct PolicyRow {
+  double loss, g, kl;
+};
+
+// Loss (before the row's weight), its derivative by lp, and the KL term.
+__device__ __forceinline__ PolicyRow policy_row(const PolicyParams& p, int64_t n, double lp) {
+  const double A = p.adv[n];
+  double none;
+  const double r =
+      p.old_lp != nullptr ? exp_series(lp - static_cast<double>(p.old_lp[n]), none) : 1.0;
+  const double bound = r < p.low ? p.low : r > p.high ? p.high : r;   // (a NaN stays)
+  PolicyRow o;
+  const double free_ = r * A, held = bound * A;
+  o.loss = -(held < free_ ? held : free_);
+  const bool clipped = (A > 0.0 && r > p.high) || (A < 0.0 && r < p.low);
+  o.g = clipped ? 0.0 : -free_;
+  o.kl = 0.0;
+  if (p.ref_lp != nullptr) {
+    const double e = static_cast<double>(p.ref_lp[n]) - lp;
+    exp_series(e, o.kl);
+    o.loss += p.kl_coef * o.kl;
+    o.g -= p.kl_coef * (o.kl + e);
+  }
+  return o;
+}
+
+// Forward: loss and statistics, and the gradient if asked for.  CH > 0: the
+// row stays in registers, CH chunks to a thread; CH = 0: it is read again.
+template <typename E, int NT, int CH>
+__global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void policy_fwd_kernel(const PolicyParams p) {
+  constexpr int kN = Chunk<E>::kN, kW = NT / 64;
+  constexpr int kHeld = CH > 0 ? CH : 1;
+  __shared__ float tops[kW];
+  __shared__ double sums[kW];
+  __shared__ float row[2];                     // the gradient's coefficient, and 1 / total
+  // two of the chunks that the first wave holds, while one of its lanes works on the row's
+  // numbers: with 8 there are no registers for both
+  constexpr bool kStash = CH == 8;
+  __shared__ decltype(Chunk<E>::r) stash[kStash ? 2 * 64 : 1];
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int64_t n = blockIdx.x;
+  const Row<E> in(p.z, n * p.z_stride, p.V), out(p.dz, n * p.dz_stride, p.V);
+  const int chunks = in.chunks();
+  const int32_t action = static_cast<int32_t>(uniform(p.action[n]));
+  const bool named = action >= 0 && action < p.V;
+  const int own_chunk = named ? (action + in.shift) / kN : -1, own_e = (action + in.shift) % kN;
+  float own_z = 0.f;
+  if (named) own_z = static_cast<float>(in.p[action]);
+  const float k2 = static_cast<float>(p.inv_tau * 1.4426950408889634);
+  Chunk<E> held[kHeld];
+  if constexpr (CH > 0) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      held[c].fill_lowest();
+      if (tid + c * NT < chunks) held[c] = in.load(tid + c * NT);
+    }
+  }
+  float m = -kInf, sum = 0.f;
+  const auto chunk_max = [&](const Chunk<E>& x, float a) {
+#pragma unroll
+    for (int e = 0; e < kN; ++e) a = fmaxf(a, x.get(e));
+    return a;
+  };
+  if constexpr (CH > 0) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) m = chunk_max(held[c], m);
+  } else {
+    for (int c = tid; c < chunks; c += NT) m = chunk_max(in.load(c), m);
+  }
+  m = join_lanes<64>(m, MaxOp());
+  if (lane == 0) tops[wave] = m;
+  __syncthreads();
+  m = join_lanes<kW>(tops[lane % kW], MaxOp());
+  const bool empty = m == -kInf;
+  if (empty) m = 0.f;                          // nothing but -inf: a sum of 0, not of NaN
+  if constexpr (CH > 0) keep_packed(held);
+  // exp((z - m) / tau) = 2^(z k2 - m2), with m2 the rounded m k2: the same in
+  // every term, and put right in the logarithm of the sum (see base)
+  const float m2 = m * k2;
+  const auto power = [&](float z) { return exp2_hw(__builtin_fmaf(z, k2, -m2)); };
+  const auto chunk_sum = [&](const Chunk<E>& x, int c) {
+    float s = 0.f;
+    if (c == own_chunk) {
+#pragma unroll
+      for (int e = 0; e < kN; ++e) s += e == own_e ? 0.f : power(x.get(e));
+    } else {
+#pragma unroll
+      for (int e = 0; e < kN; ++e) s += power(x.get(e));
+    }
+    sum += s;
+  };
+  if constexpr (CH > 0) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      if (tid + c * NT < chunks) chunk_sum(held[c], tid + c * NT);
+  } else {
+    for (int c = tid; c < chunks; c += NT) chunk_sum(in.load(c), c);
+  }
+  if constexpr (CH > 0) keep_packed(held);
+  const double part = join_lanes<64>(static_cast<double>(sum), AddOp());
+  if (lane == 0) sums[wave] = part;
+  __syncthreads();
+  const double rest = join_lanes<kW>(sums[lane % kW], AddOp());
+  const auto row_numbers = [&] {
+    const float w = p.weight ? p.weight[n] : 1.f;
+    // x / tau less the powers' base: what m2 and k2 were rounded by comes back here
+    const double base = static_cast<double>(m) * p.inv_tau +
+                        (static_cast<double>(m2) - static_cast<double>(m) * k2) * 0.6931471805599453;
+    const double x = static_cast<double>(own_z) * p.inv_tau - base;
+    double none;
+    const double own = named ? exp_series(x, none) : 0.0, total = rest + own;
+    PolicyRow o{0.0, 0.0, 0.0};
+    double lse = -__builtin_huge_val(), lp = 0.0, others = 1.0;
+    const bool live = named && !empty;
+    // (the largest logit's power is about 1, so the total is no less; where the token has
+    // most of it, lp = -log(1 + rest / own))
+    if (!empty) lse = base + log_of(total);
+    if (live) {
+      const double q = rest / own;
+      lp = q < 0.4 ? -log_near(q) : x - (lse - base);
+      others = rest / total;
+      o = policy_row(p, n, lp);
+    }
+    p.loss[n] = live && w != 0.f ? static_cast<float>(o.loss * static_cast<double>(w)) : 0.f;
+    float* stats = p.stats + 4 * n;
+    stats[0] = static_cast<float>(lse);
+    stats[1] = static_cast<float>(lp);
+    stats[2] = static_cast<float>(o.g);
+    stats[3] = static_cast<float>(o.kl);
+    const float c = w != 0.f ? coefficient(p, w, o.g) : 0.f;
+    row[0] = c;
+    row[1] = static_cast<float>(1.0 / total);
+    if (p.dz != nullptr) tops[0] = c * static_cast<float>(others);   // the sampled token's gradient
+  };
+  if (wave == 0) {
+    if constexpr (kStash) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) stash[c * 64 + lane] = held[c].r;
+      asm volatile("" ::: "memory");
+    }
+    if (lane == 0) row_numbers();
+    if constexpr (kStash) {
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int c = 0; c < 2; ++c) held[c].r = stash[c * 64 + lane];
+    }
+  }
+  if (p.dz == nullptr) return;
+  __syncthreads();
+  const float c0 = row[0], own_grad = tops[0];
+  if (c0 == 0.f) {
+    const float zero[kN] = {};
+    for (int c = tid; c < chunks; c += NT) out.store(c, in.shift, zero);
+    return;
+  }
+  const float factor = -c0 * row[1];
+  const auto grad = [&](const Chunk<E>& x, int c) {
+    float y[kN];
+#pragma unroll
+    for (int e = 0; e < kN; ++e) y[e] = power(x.get(e)) * factor;
+    if (c == own_chunk) {
+#pragma unroll
+      for (int e = 0; e < kN; ++e) y[e] = e == own_e ? own_grad : y[e];
+    }
+    out.store(c, in.shift, y);
+  };
+  if constexpr (CH > 0) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      if (tid + c * NT < chunks) grad(held[c], tid + c * NT);
+  } else {
+    for (int c = tid; c < chunks; c += NT) grad(in.load(c), c);
+  }
+}
+
+// Backward from saved statistics: a piece of a row to a workgroup.
+template <typename E, int NT>
+__global__ __launch_bounds__(NT) void policy_bwd_kernel(const PolicyParams p) {
+  constexpr int kN = Chunk<E>::kN;
+  const int64_t n = blockIdx.y;
+  const Row<E> in(p.z, n * p.z_stride, p.V), out(p.dz, n * p.dz_stride, p.V);
+  const int c0 = blockIdx.x * p.seg, c1 = min(c0 + p.seg, in.chunks());
+  if (c0 >= c1) return;
+  const float w = p.weight ? p.weight[n] : 1.f;
+  const float lse = p.stats[4 * n], lp = p.stats[4 * n + 1], g = p.stats[4 * n + 2];
+  const int32_t action = static_cast<int32_t>(uniform(p.action[n]));
+  const bool named = action >= 0 && action < p.V;
+  const int own_chunk = named ? (action + in.shift) / kN : -1, own_e = (action + in.shift) % kN;
+  const float c = w != 0.f && named ? coefficient(p, w, g) : 0.f;
+  const bool live = c != 0.f;
+  const float inv_tau = static_cast<float>(p.inv_tau);
+  const auto prob = [&](float z) { return exp2_hw(__builtin_fmaf(z, inv_tau, -lse) * kLog2e); };
+  constexpr int kAtOnce = 4;                           // loads under way, a thread
+  for (int cc = c0 + threadIdx.x; cc < c1; cc += kAtOnce * NT) {
+    Chunk<E> x[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      x[k].fill_lowest();
+      if (live && cc + k * NT < c1) x[k] = in.load(cc + k * NT);
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int at = cc + k * NT;
+      if (at >= c1) continue;
+      float y[kN];
+#pragma unroll
+      for (int e = 0; e < kN; ++e) y[e] = live ? -c * prob(x[k].get(e)) : 0.f;
+      if (live && at == own_chunk) {
+        const float own = c * static_cast<float>(-expm1(static_cast<double>(lp)));
+#pragma unroll
+        for (int e = 0; e < kN; ++e) y[e] = e == own_e ? own : y[e];
+      }
+      out.store(at, in.shift, y);
+    }
+  }
+}
+
+namespace {
+
+template <typename E, int NT, int CH>
+hipError_t run_fwd(const PolicyParams& p, hipStream_t s) {
+  policy_fwd_kernel<E, NT, CH><<<static_cast<unsigned>(p.N), NT, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+// By the length of the row: held in registers where it fits, in the fewest that hold it,
+// and short rows by smaller workgroups.
+template <typename E>
+hipError_t pick_fwd(const PolicyParams& p, hipStream_t s) {
+  const int64_t chunks = (p.V + Chunk<E>::kN - 1) / Chunk<E>::kN + 1;
+  if (chunks <= 256 * 2) return run_fwd<E, 256, 2>(p, s);
+  if (chunks <= 256 * 4) return run_fwd<E, 256, 4>(p, s);
+  if (chunks <= 1024 * 2) return run_fwd<E, 1024, 2>(p, s);
+  if (chunks <= 1024 * 4) return run_fwd<E, 1024, 4>(p, s);
+  if (chunks <= 1024 * 8) return run_fwd<E, 1024, 8>(p, s);
+  if (chunks <= 1024 * 16) return run_fwd<E, 1024, 16>(p, s);
+  return run_fwd<E, 1024, 0>(p, s);
+}
+
+template <typename E>
+hipError_t run_bwd(const PolicyParams& p, hipStream_t s) {
+  constexpr int NT = 256;
+  const int chunks = static_cast<int>((p.V + Chunk<E>::kN - 1) / Chunk<E>::kN + 1);
+  for (int64_t n0 = 0; n0 < p.N; n0 += 65535) {
+    PolicyParams q = p;
+    const int64_t rows = p.N - n0 < 65535 ? p.N - n0 : 65535;
+    q.seg = NT * (Chunk<E>::kN == 4 ? 2 : 4);
+    q.z = static_cast<const E*>(p.z) + n0 * p.z_stride;
+    q.dz = static_cast<E*>(p.dz) + n0 * p.dz_stride;
+    q.action = p.action + n0;
+    q.weight = p.weight ? p.weight + n0 : nullptr;
+    q.stats = p.stats + 4 * n0;
+    policy_bwd_kernel<E, NT>
+        <<<dim3((chunks + q.seg - 1) / q.seg, static_cast<unsigned>(rows)), NT, 0, s>>>(q);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_policy(const zero_policy_args& a, bool forward, hipStream_t s) {
+  PolicyParams p = {};
+  p.N = a.N;
+  p.V = a.V;
+  p.inv_tau = 1.0 / a.temperature;
+  p.low = 1.0 - a.clip_low;
+  p.high = 1.0 + a.clip_high;
+  p.kl_coef = a.kl_coef;
+  p.grad_scale = a.grad_scale;
+  p.z = a.logits;
+  p.action = a.action;
+  p.adv = a.advantage;
+  p.old_lp = a.old_logp;
+  p.ref_lp = a.ref_logp;
+  p.weight = a.row_weight;
+  p.loss = a.loss;
+  p.stats = a.stats;
+  p.dz = a.dlogits;
+  p.z_stride = a.logits_stride;
+  p.dz_stride = a.dlogits_stride;
+  if (forward) return a.dtype == ZERO_BF16 ? pick_fwd<bf16>(p, s) : pick_fwd<float>(p, s);
+  return a.dtype == ZERO_BF16 ? run_bwd<bf16>(p, s) : run_bwd<float>(p, s);
+}
+
+}  // namespace zo
