@@ -636,7 +636,7 @@ def test_grads_clip_writes_nothing_else(zs, torch):
     assert bool((flat[~hit] == 7).all()) and not bool((flat[hit] == 7).any())
 
 
-@pytest.mark.parametrize("count", [1, 159, 160, 161, 255, 256, 257, 520])
+@pytest.mark.parametrize("count", [1, 159, 160, 161, 239, 240, 241, 255, 256, 257, 520])
 def test_grads_more_tensors_than_a_launch(zs, torch, count):
     sizes = [(i * 37) % 300 + 1 for i in range(count)]
     types = [(torch.bfloat16, torch.float32)[i % 3 == 0] for i in range(count)]
@@ -872,3 +872,39 @@ def test_long_rows_past_32_bits(zs, torch):
     q = math.exp(3) / (math.exp(3) + V - 1)
     assert float((stats[:, 1] - math.log(q)).abs().max()) < 1e-5
     assert float((dz[:, 5].float() + (1 - q)).abs().max()) < 2.0 ** -8
+
+
+def test_clip_coefficient_of_any_accumulator(zs, torch):
+    """The coefficient of zero_step_gate to the bit, and the norm, for sums from a single
+    unit of 2^-128 to the top digit, with carries pending, of one accumulator and of three."""
+    g = torch.Generator()
+    g.manual_seed(12)
+    coef, want = torch.empty(1, device="cuda"), torch.empty(1, device="cuda")
+    skip, norm = torch.empty(1, dtype=torch.int32, device="cuda"), torch.empty(1, device="cuda")
+    table = zs.GradTable([])
+    for case in range(120):
+        words = torch.zeros(3, 16, dtype=torch.int64)
+        n = 1 if case % 3 else 3
+        for a in range(n):
+            for k in range(13):
+                if case < 13 and k != case:
+                    continue
+                if torch.rand(1, generator=g) < (1.0 if case < 13 else 0.4):
+                    bits = int(torch.randint(1, 50, (1,), generator=g))
+                    words[a, k] = int(torch.randint(0, 1 << bits, (1,), generator=g)) + (case % 2)
+        if case == 14:                          # a tie: 2^53 + 1 units, and the next up
+            words.zero_()
+            words[0, 0], words[0, 1] = 1, 1 << 21
+        if case == 16:
+            words.zero_()
+            words[0, 0], words[0, 1] = 3, 1 << 21
+        accs = words[:n].cuda()
+        X = sum(x for x, _ in zs.read_norm_acc(accs))
+        true = math.sqrt(X / 2 ** 128) if X < 2 ** 1000 else 0.0
+        for max_norm in (true * 0.7 + 1e-300, 1e-6, 1.0):
+            zs.zero_step_gate(accs, max_norm, True, want, skip)
+            zs.zero_grads_clip(table, accs, max_norm=max_norm, check_overflow=True, norm_out=norm,
+                               coef_out=coef)
+            assert _same(coef, want), case
+        if true < 3.4e38:
+            assert abs(float(norm) - true) <= 2.0 ** -23 * true + 1e-45, case

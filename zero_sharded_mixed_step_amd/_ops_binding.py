@@ -670,13 +670,14 @@ class GradTable:
         self._ptrs = tuple(C.addressof(a) for a in flat)
 
     def _addresses(self):
-        at = [t.data_ptr() for t in self.grads]
+        at = list(map(torch.Tensor.data_ptr, self.grads))
         if self.outs is not self.grads:
-            at += [t.data_ptr() for t in self.outs]
+            at += map(torch.Tensor.data_ptr, self.outs)
         return at
 
     def _checked(self, dev):
-        if self._addresses() != self._at or [t.numel() for t in self.grads] != self._sizes:
+        if self._addresses() != self._at \
+                or list(map(torch.Tensor.numel, self.grads)) != self._sizes:
             raise ValueError("a tensor of the table has moved or changed its size: make a new table")
         if self.grads and self.device != dev:
             raise ValueError(f"the table is on cuda:{self.device}; the library launches on the "

@@ -22,30 +22,32 @@ using zs::kVec;
 constexpr int kGradThreads = 256;
 constexpr int kGradTile = 8192;               // elements of a tile: 4 chunks of 8 a thread
 constexpr int kTileChunks = kGradTile / kVec / kGradThreads;
-constexpr int kNormGroups = 1024;             // workgroups of the norm at most
+constexpr int kNormGroups = 1024;             // workgroups at most
+constexpr uint32_t kClipGroups = 2048;
 constexpr int kWords = kDigits + 1;           // digits, then the non-finite count
 static_assert(kTileChunks == 4, "a quad's lanes convert a group each");
 
-// Tensors of one launch.  first[i] is tensor i's first tile; its last tile holds tail[i]
-// elements.
+// Tensors of one launch.  first[i] is tensor i's first tile; info[i] holds the elements of
+// its last tile, and kBf16In and kBf16Out.  (Words, as scalar loads have no smaller: a byte
+// would come by a vector load, whose wait waits for the tile's loads too.)
+constexpr uint32_t kTail = 0xFFFF, kBf16In = 1u << 16, kBf16Out = 1u << 17;
 template <int N>
 struct TensorTable {
   int count;
   uint32_t first[N + 1];
-  uint16_t tail[N];
-  uint8_t type[N];                            // bit 0: bf16 gradients, bit 1: bf16 outputs
+  uint32_t info[N];
   const void* grad[N];
 
-  // The tensor of a tile, from tensor `at` on.
-  __device__ __forceinline__ int find(uint32_t tile, int at) const {
-    int step = 1;
+  // The tensor of a tile.
+  __device__ __forceinline__ int find(uint32_t tile) const {
+    int at = 0, step = 1;
     while (step < N) step <<= 1;
     for (; step > 0; step >>= 1)
       if (at + step < count && first[at + step] <= tile) at += step;
     return at;
   }
 };
-constexpr int kNormTensors = 256, kClipTensors = 160;
+constexpr int kNormTensors = 240, kClipTensors = 160;
 
 struct GradNormParams {
   TensorTable<kNormTensors> t;
@@ -69,52 +71,113 @@ struct GradClipParams {
 static_assert(sizeof(GradNormParams) <= 4096 && sizeof(GradClipParams) <= 4096,
               "kernel arguments");
 
-// Eight elements from any element on; those from `left` on read as +0.
+// What a thread holds of a tile: four chunks of eight elements.  The tensor's start may lie
+// at any element.
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
-struct Raw8 {
-  zs::u32x4 a, b;
-};
-__device__ __forceinline__ Raw8 load_any(const void* base, bool is_bf16, int64_t e0, int left) {
-  Raw8 r{};
-  if (is_bf16) {
-    const uint16_t* p = static_cast<const uint16_t*>(base) + e0;
-    if (left >= kVec) {
-      r.a = *reinterpret_cast<const u32x4_any*>(p);
-    } else {
+template <bool BF16>
+struct RawTile {
+  zs::u32x4 v[kTileChunks][BF16 ? 1 : 2];
+
+  // A thread's chunk u of a tile starts at element (u * 256 + thread) * 8.
+  __device__ __forceinline__ static int chunk_at(int u) {
+    return (u * kGradThreads + static_cast<int>(threadIdx.x)) * kVec;
+  }
+
+  __device__ __forceinline__ void load(const char* tile) {
 #pragma unroll
-      for (int j = 0; j < kVec; ++j)
-        if (j < left) r.a[j / 2] |= static_cast<uint32_t>(p[j]) << (16 * (j & 1));
-    }
-  } else {
-    const float* p = static_cast<const float*>(base) + e0;
-    if (left >= kVec) {
-      const f32x4_any x = *reinterpret_cast<const f32x4_any*>(p);
-      const f32x4_any y = *reinterpret_cast<const f32x4_any*>(p + 4);
+    for (int u = 0; u < kTileChunks; ++u) {
+      if constexpr (BF16) {
+        v[u][0] = reinterpret_cast<const u32x4_any*>(tile)[chunk_at(u) / kVec];
+      } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        r.a[j] = __float_as_uint(x[j]);
-        r.b[j] = __float_as_uint(y[j]);
+        for (int h = 0; h < 2; ++h)
+          v[u][h] = __builtin_bit_cast(
+              zs::u32x4, reinterpret_cast<const f32x4_any*>(tile)[chunk_at(u) / 4 + h]);
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kVec; ++j)
-        if (j < left) (j < 4 ? r.a : r.b)[j & 3] = __float_as_uint(p[j]);
     }
   }
-  return r;
-}
-__device__ __forceinline__ void widen(const Raw8& r, bool is_bf16, float x[kVec]) {
+
+  // Of a tile of n elements: those behind it are +0.
+  __device__ __forceinline__ void load_some(const char* tile, int n) {
 #pragma unroll
-  for (int j = 0; j < kVec; ++j) {
-    const uint32_t h = r.a[j / 2];
-    const float b = __uint_as_float(j & 1 ? h & 0xFFFF0000u : h << 16);
-    x[j] = is_bf16 ? b : __uint_as_float((j < 4 ? r.a : r.b)[j & 3]);
+    for (int u = 0; u < kTileChunks; ++u) {
+      const int c = chunk_at(u);
+#pragma unroll
+      for (int h = 0; h < (BF16 ? 1 : 2); ++h) v[u][h] = zs::u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        if (c + j >= n) continue;
+        if constexpr (BF16)
+          v[u][0][j / 2] |=
+              static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(tile)[c + j]) << (16 * (j & 1));
+        else
+          v[u][j / 4][j & 3] = reinterpret_cast<const uint32_t*>(tile)[c + j];
+      }
+    }
+  }
+
+  __device__ __forceinline__ void widen(int u, float scale, float x[kVec]) const {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      if constexpr (BF16) {
+        const uint32_t h = v[u][0][j / 2];
+        x[j] = __uint_as_float(j & 1 ? h & 0xFFFF0000u : h << 16) * scale;
+      } else {
+        x[j] = __uint_as_float(v[u][j / 4][j & 3]) * scale;
+      }
+    }
+  }
+};
+
+// Works on one tile: use(raw, tensor, info, first element, elements).
+template <bool BF16, typename Use>
+__device__ __forceinline__ void with_tile(const void* tensor, int i, uint32_t info, int64_t e0,
+                                          int n, Use use) {
+  const char* base = static_cast<const char*>(tensor) + e0 * (BF16 ? 2 : 4);
+  RawTile<BF16> raw;
+  if (n == kGradTile) raw.load(base);
+  else raw.load_some(base, n);
+  use(raw, i, info, e0, n);
+}
+
+// A workgroup's tiles, one of every gridDim.x; with BACK a tensor's last tile comes first.
+template <bool BACK, int N, typename Use>
+__device__ __forceinline__ void walk(const TensorTable<N>& t, uint32_t tiles, Use use) {
+  for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int i = t.find(tile);
+    const uint32_t info = t.info[i], first = t.first[i], last = t.first[i + 1] - 1;
+    const uint32_t inside = BACK ? last - tile : tile - first;
+    const int64_t e0 = static_cast<int64_t>(inside) * kGradTile;
+    const int n = inside == last - first ? static_cast<int>(info & kTail) : kGradTile;
+    if (info & kBf16In) with_tile<true>(t.grad[i], i, info, e0, n, use);
+    else with_tile<false>(t.grad[i], i, info, e0, n, use);
   }
 }
 
-// A thread's chunk u of a tile starts at element (u * 256 + thread) * 8.
+// The four group sums that a thread's quad has of a tile.  Squares of finite binary32
+// values sum to less than 2^261 in binary64, so only a value that is not finite makes the
+// chunk's sum infinite or NaN: they are looked for (zs::chunk_sumsq) only then.  Elements
+// behind the tensor's end are +0.
+template <bool BF16>
+__device__ __forceinline__ void tile_sums(const RawTile<BF16>& r, float scale,
+                                          double s4[kTileChunks], uint32_t& nonfinite) {
+#pragma unroll
+  for (int u = 0; u < kTileChunks; ++u) {
+    float g[kVec];
+    r.widen(u, scale, g);
+    double a = 0.0;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      const double x = static_cast<double>(g[j]);
+      a = __builtin_fma(x, x, a);
+    }
+    if (!__builtin_isfinite(a)) a = zs::chunk_sumsq(g, nonfinite);
+    s4[u] = zs::quad_group_sum(a);
+  }
+}
+
 __global__ __launch_bounds__(kGradThreads) void grads_norm_kernel(const GradNormParams p) {
   __shared__ uint64_t s_digit[kDigits][kGradThreads];
   __shared__ uint64_t s_part[kGradThreads / 64][kWords];
@@ -122,29 +185,9 @@ __global__ __launch_bounds__(kGradThreads) void grads_norm_kernel(const GradNorm
 #pragma unroll
   for (int k = 0; k < kDigits; ++k) s_digit[k][tid] = 0;
   uint32_t nonfinite = 0;
-  int at = 0;
-  for (uint32_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
-    at = p.t.find(tile, at);
-    const uint32_t inside = tile - p.t.first[at];
-    const int n = tile + 1 == p.t.first[at + 1] ? p.t.tail[at] : kGradTile;
-    const bool is_bf16 = p.t.type[at] & 1;
-    const int64_t e0 = static_cast<int64_t>(inside) * kGradTile;
-    Raw8 raw[kTileChunks];
-#pragma unroll
-    for (int u = 0; u < kTileChunks; ++u) {
-      const int c = (u * kGradThreads + tid) * kVec;
-      raw[u] = load_any(p.t.grad[at], is_bf16, e0 + c, n - c);
-    }
+  walk<false>(p.t, p.tiles, [&](const auto& raw, int, uint32_t, int64_t, int) {
     double s4[kTileChunks];
-#pragma unroll
-    for (int u = 0; u < kTileChunks; ++u) {
-      float g[kVec];
-      widen(raw[u], is_bf16, g);
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) g[j] *= p.inv_scale;
-      // (elements behind the tensor's end are +0: an inv_scale is finite)
-      s4[u] = zs::quad_group_sum(zs::chunk_sumsq(g, nonfinite));
-    }
+    tile_sums(raw, p.inv_scale, s4, nonfinite);
     // every lane of a quad holds the four group sums: lane q converts group q
     const double S = quad_lane == 0 ? s4[0] : quad_lane == 1 ? s4[1] : quad_lane == 2 ? s4[2] : s4[3];
     int base;
@@ -153,7 +196,7 @@ __global__ __launch_bounds__(kGradThreads) void grads_norm_kernel(const GradNorm
     if (p0 != 0) s_digit[base][tid] += p0;
     if (p1 != 0) s_digit[base + 1][tid] += p1;
     if (p2 != 0) s_digit[base + 2][tid] += p2;
-  }
+  });
   const int lane = tid & 63, wave = tid >> 6;
 #pragma unroll
   for (int k = 0; k < kWords; ++k) {
@@ -197,10 +240,14 @@ __global__ __launch_bounds__(kFoldThreads) void grads_fold_kernel(const uint64_t
 
 // -------------------------------------------------------------- clipping ---
 
-__device__ __forceinline__ void store_any(void* base, bool is_bf16, int64_t e0, int left,
-                                          const float x[kVec]) {
-  if (is_bf16) {
-    uint16_t* p = static_cast<uint16_t*>(base) + e0;
+// Past the caches: what the norm left in them of the gradients is read back from there,
+// which plain stores of the outputs would push out.  194 tensors of 301 MB, norm and
+// clipping: 175 us instead of 207; from the last tile to the first, so that the clipping
+// begins with what the norm read last, 168.
+template <bool BF16>
+__device__ __forceinline__ void store_chunk(void* base, int c, int left, const float x[kVec]) {
+  if constexpr (BF16) {
+    uint16_t* p = static_cast<uint16_t*>(base) + c;
     zs::u32x4 w;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -209,23 +256,75 @@ __device__ __forceinline__ void store_any(void* base, bool is_bf16, int64_t e0, 
              static_cast<uint32_t>(__builtin_bit_cast(uint16_t, hi)) << 16;
     }
     if (left >= kVec) {
-      *reinterpret_cast<u32x4_any*>(p) = w;
+      __builtin_nontemporal_store(static_cast<u32x4_any>(w), reinterpret_cast<u32x4_any*>(p));
     } else {
 #pragma unroll
       for (int j = 0; j < kVec; ++j)
         if (j < left) p[j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
     }
   } else {
-    float* p = static_cast<float*>(base) + e0;
+    float* p = static_cast<float*>(base) + c;
     if (left >= kVec) {
-      *reinterpret_cast<f32x4_any*>(p) = f32x4_any{x[0], x[1], x[2], x[3]};
-      *reinterpret_cast<f32x4_any*>(p + 4) = f32x4_any{x[4], x[5], x[6], x[7]};
+      f32x4_any* q = reinterpret_cast<f32x4_any*>(p);
+      __builtin_nontemporal_store(f32x4_any{x[0], x[1], x[2], x[3]}, q);
+      __builtin_nontemporal_store(f32x4_any{x[4], x[5], x[6], x[7]}, q + 1);
     } else {
 #pragma unroll
       for (int j = 0; j < kVec; ++j)
         if (j < left) p[j] = x[j];
     }
   }
+}
+
+template <bool OUT, bool IN>
+__device__ __forceinline__ void clip_tile(const RawTile<IN>& r, int n, float scale, float coef,
+                                          void* out) {
+#pragma unroll
+  for (int u = 0; u < kTileChunks; ++u) {
+    const int c = RawTile<IN>::chunk_at(u);
+    float g[kVec];
+    r.widen(u, scale, g);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) g[j] *= coef;
+    if (n == kGradTile) store_chunk<OUT>(out, c, kVec, g);
+    else store_chunk<OUT>(out, c, n - c, g);
+  }
+}
+
+// zs::fixed_to_double, operation for operation: RNE_binary64(X * 2^-128).  Its words are
+// chosen by comparisons, not by an index, so they stay in registers: every workgroup waits for
+// this number.
+__device__ __forceinline__ double fixed_value(const uint32_t w[zs::kSumWords]) {
+  constexpr int kN = zs::kSumWords;
+  int word = -1;
+  uint32_t high = 0;
+#pragma unroll
+  for (int k = 0; k < kN; ++k)
+    if (w[k] != 0u) {
+      word = k;
+      high = w[k];
+    }
+  if (word < 0) return 0.0;
+  const int top = 32 * word + (31 - __clz(static_cast<int>(high)));
+  if (top <= 52)
+    return __builtin_amdgcn_ldexp(static_cast<double>(static_cast<uint64_t>(w[1]) << 32 | w[0]),
+                                  -128);
+  const int s = top - 52, i = s >> 5, off = s & 31;    // lowest kept bit
+  const int half = (s - 1) >> 5, half_bit = (s - 1) & 31;
+  uint32_t w0 = 0, w1 = 0, w2 = 0, wh = 0, sticky = 0;
+#pragma unroll
+  for (int k = 0; k < kN; ++k) {
+    w0 = k == i ? w[k] : w0;
+    w1 = k == i + 1 ? w[k] : w1;
+    w2 = k == i + 2 ? w[k] : w2;
+    wh = k == half ? w[k] : wh;
+    sticky |= k < half ? w[k] : 0u;
+  }
+  sticky |= wh & ((1u << half_bit) - 1u);
+  const uint64_t lo = static_cast<uint64_t>(w1) << 32 | w0, hi = w2;
+  uint64_t mant = (off ? lo >> off | hi << (64 - off) : lo) & ((1ull << 53) - 1ull);
+  if (((wh >> half_bit) & 1u) && (sticky != 0u || (mant & 1ull))) ++mant;   // (2^53 is exact too)
+  return __builtin_amdgcn_ldexp(static_cast<double>(mant), s - 128);
 }
 
 // The step's gate (zs::evaluate_gate, operation for operation) with the norm that it comes
@@ -237,7 +336,7 @@ __device__ __forceinline__ zs::Gate gate_and_norm(const GradClipParams& p, doubl
   uint32_t w[zs::kSumWords];
   uint64_t nonfinite;
   zs::acc_total(p.accs, p.n_accs, w, nonfinite);
-  norm = nonfinite > 0 ? __builtin_huge_val() : __builtin_sqrt(zs::fixed_to_double(w));
+  norm = nonfinite > 0 ? __builtin_huge_val() : __builtin_sqrt(fixed_value(w));
   if (p.check_overflow && nonfinite > 0) {
     g.skip = 1;
   } else if (p.max_norm > 0.0) {
@@ -249,8 +348,7 @@ __device__ __forceinline__ zs::Gate gate_and_norm(const GradClipParams& p, doubl
 
 __global__ __launch_bounds__(kGradThreads) void grads_clip_kernel(const GradClipParams p) {
   __shared__ zs::Gate s_gate;
-  const int tid = threadIdx.x;
-  if (tid == 0) {
+  if (threadIdx.x == 0) {
     double norm;
     const zs::Gate g = gate_and_norm(p, norm);
     s_gate = g;
@@ -263,56 +361,40 @@ __global__ __launch_bounds__(kGradThreads) void grads_clip_kernel(const GradClip
   __syncthreads();
   if (s_gate.skip) return;
   const float coef = s_gate.coef;
-  int at = 0;
-  for (uint32_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
-    at = p.t.find(tile, at);
-    if (coef == 1.f && p.inv_scale == 1.f && p.out[at] == p.t.grad[at]) continue;
-    const uint32_t inside = tile - p.t.first[at];
-    const int n = tile + 1 == p.t.first[at + 1] ? p.t.tail[at] : kGradTile;
-    const bool in_bf16 = p.t.type[at] & 1, out_bf16 = p.t.type[at] & 2;
-    const int64_t e0 = static_cast<int64_t>(inside) * kGradTile;
-    Raw8 raw[kTileChunks];
-#pragma unroll
-    for (int u = 0; u < kTileChunks; ++u) {
-      const int c = (u * kGradThreads + tid) * kVec;
-      raw[u] = load_any(p.t.grad[at], in_bf16, e0 + c, n - c);
-    }
-#pragma unroll
-    for (int u = 0; u < kTileChunks; ++u) {
-      const int c = (u * kGradThreads + tid) * kVec;
-      float g[kVec];
-      widen(raw[u], in_bf16, g);
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) g[j] = g[j] * p.inv_scale * coef;
-      store_any(p.out[at], out_bf16, e0 + c, n - c, g);
-    }
-  }
+  walk<true>(p.t, p.tiles, [&](const auto& raw, int i, uint32_t info, int64_t e0, int n) {
+    if (coef == 1.f && p.inv_scale == 1.f && p.out[i] == p.t.grad[i]) return;
+    const bool out = info & kBf16Out;
+    char* to = static_cast<char*>(p.out[i]) + e0 * (out ? 2 : 4);
+    if (out) clip_tile<true>(raw, n, p.inv_scale, coef, to);
+    else clip_tile<false>(raw, n, p.inv_scale, coef, to);
+  });
 }
 
 namespace {
 
 uint32_t tiles_of(int64_t n) { return static_cast<uint32_t>((n + kGradTile - 1) / kGradTile); }
 
-// Puts tensors [from, ...) that have elements into the table, as many as fit it and as have
-// fewer than 2^31 tiles together; the next tensor to take.
+// Puts tensors that have elements into the table, from `from` on (with `out` from there
+// back), as many as fit it and as have fewer than 2^31 tiles together; the next tensor to take.
 template <int N>
 int64_t fill_table(const zero_grads_args& a, int64_t from, TensorTable<N>& t, void** out,
                    uint32_t& tiles) {
+  const int64_t step = out != nullptr ? -1 : 1;
   t.count = 0;
   tiles = 0;
-  for (; from < a.count; ++from) {
+  for (; from >= 0 && from < a.count; from += step) {
     const int64_t n = a.sizes[from];
     if (n == 0) continue;
     const uint32_t more = tiles_of(n);
     if (t.count == N || (t.count > 0 && tiles + static_cast<uint64_t>(more) > (1u << 31))) break;
     const int i = t.count++;
     t.first[i] = tiles;
-    t.tail[i] = static_cast<uint16_t>((n - 1) % kGradTile + 1);
+    t.info[i] = static_cast<uint32_t>((n - 1) % kGradTile + 1) |
+                (a.dtypes[from] == ZERO_BF16 ? kBf16In : 0u);
     t.grad[i] = a.grads[from];
-    t.type[i] = a.dtypes[from] == ZERO_BF16 ? 1 : 0;
     if (out != nullptr) {
       out[i] = a.outs[from];
-      t.type[i] |= a.out_dtypes[from] == ZERO_BF16 ? 2 : 0;
+      t.info[i] |= a.out_dtypes[from] == ZERO_BF16 ? kBf16Out : 0u;
     }
     tiles += more;
   }
@@ -355,10 +437,10 @@ hipError_t launch_grads_clip(const zero_grads_args& a, hipStream_t s) {
   p.coef_out = a.coef_out;
   p.skipped_out = a.skipped_out;
   p.lead = 1;
-  for (int64_t from = 0; p.lead || from < a.count;) {
+  for (int64_t from = a.count - 1; p.lead || from >= 0;) {
     from = fill_table(a, from, p.t, p.out, p.tiles);
     if (p.tiles == 0 && !p.lead) break;
-    const uint32_t grid = p.tiles < 1 ? 1 : p.tiles < 4096 ? p.tiles : 4096;
+    const uint32_t grid = p.tiles < 1 ? 1 : p.tiles < kClipGroups ? p.tiles : kClipGroups;
     grads_clip_kernel<<<grid, kGradThreads, 0, s>>>(p);
     p.lead = 0;
   }
