@@ -244,12 +244,14 @@ int zero_distill_bwd(const zero_distill_args *args, void *stream);
  *
  * zero_embed_bwd writes all of dtable.  base may be dtable itself (same dtype
  * and stride): the sums are then added, and rows that no id names are left as
- * they are.  A row's sum is binary32, in the order of n: runs of at most 64
- * terms, then the runs; base is added last, before the one rounding.
+ * they are.  A row's sum is binary32 in a fixed order: by the order of n, in
+ * pieces of at most 256 terms whose sums are then joined; base is added last, before the
+ * one rounding.
  *
  * dtype (ZERO_BF16 or ZERO_F32) is that of table, out and dout, grad_dtype that
  * of dtable, base_dtype that of base.  C is a multiple of 8 up to
- * ZERO_ROW_MAX_C; rows start on 16 bytes (ZERO_EALIGN).  N <= 2^21. */
+ * ZERO_ROW_MAX_C; rows start on 16 bytes (ZERO_EALIGN).  N <= 2^21.  Short calls need no
+ * workspace (0 bytes). */
 typedef struct zero_embed_args {
   size_t struct_bytes;          /* sizeof(zero_embed_args) */
   int64_t N, V;

@@ -88,9 +88,10 @@ def test_embed_argument_checks(lib):  # noqa: F811
         (dict(dtable=FAKE + 8), EALIGN), (dict(dtable_stride=60), EINVAL), (dict(dout=0), EINVAL),
         (dict(dout=FAKE + 4), EALIGN), (dict(dout_stride=65), EALIGN), (dict(base=FAKE + 8), EALIGN),
         (dict(base=FAKE), EINVAL), (dict(base=FAKE, base_dtype=0, base_stride=128), EINVAL),
-        (dict(workspace=0), EINVAL), (dict(workspace=FAKE + 8), EALIGN), (dict(workspace_bytes=64), ESIZE)])
+        (dict(N=300, workspace=0), EINVAL), (dict(N=300, workspace=FAKE + 8), EALIGN),
+        (dict(N=300, workspace_bytes=64), ESIZE)])
     w = lib.zero_embed_workspace_bytes
-    assert w(0, 64) == 0 and w(-1, 64) == 0 and w(8, 64) >= 4 * 32 + 2 * 2 * 64 * 4
+    assert w(0, 64) == 0 and w(-1, 64) == 0 and w(300, 64) >= 4 * 1200 + 2 * 75 * 64 * 4
     # (less than the gradient itself takes, beside the lists)
     assert w(1 << 20, 4096) < (1 << 20) * 4096 * 2 // 4
 

@@ -472,7 +472,7 @@ def zero_embed_bwd(ids, dout, dtable, *, scale=1.0, base=None, workspace=None,
     """The gradient of zero_embed_fwd by the table: dtable (V, C) = base + scale * the
     sums of dout's (N, C) rows by id.  base (V, C) is 0 where None, and may be dtable:
     the sums are then added to it.  dout, base and dtable are float32 or bfloat16 each;
-    workspace: zero_embed_workspace_bytes(N, C) bytes."""
+    workspace: zero_embed_workspace_bytes(N, C) bytes (0 for few tokens)."""
     if not isinstance(dtable, torch.Tensor) or dtable.dim() != 2:
         raise ValueError("dtable is a (V, C) tensor")
     if not isinstance(ids, torch.Tensor) or ids.dim() != 1:

@@ -232,9 +232,11 @@ int check_embed(const zero_embed_args* a, bool fwd) {
   }
   if (a->N == 0) return ZERO_OK;
   ZO_CHECK(check_matrix(a->dout, a->dout_stride, a->N, a->dtype));
+  const size_t need = zo::embed_workspace(a->N, a->C);
+  if (need == 0) return ZERO_OK;
   if (a->workspace == nullptr) return ZERO_EINVAL;
   if (!aligned(a->workspace, 16)) return ZERO_EALIGN;
-  return a->workspace_bytes < zo::embed_workspace(a->N, a->C) ? ZERO_ESIZE : ZERO_OK;
+  return a->workspace_bytes < need ? ZERO_ESIZE : ZERO_OK;
 }
 
 // ------------------------------------------------------ norms round a block ---

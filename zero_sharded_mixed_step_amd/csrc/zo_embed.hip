@@ -11,20 +11,29 @@
 // Waves beside those write the rows that no id names.
 //
 // Sorting needs each place's rank, the number of (id, place) pairs below its own.  It is
-// counted: within a tile of 2048 places by comparing with all of them (two instructions a
+// counted: within a tile of 1024 places by comparing with all of them (a few instructions a
 // comparison, spread over the card), and over the other tiles by searching their sorted
 // lists.  No pass depends on the ids' distribution, and there are one or two launches.
+// Up to 256 tokens need none of this: see embed_direct_kernel.
+//
+// Measured, bf16: forward of 16384 x 4096 41 us, 6.6 TB/s (rows met again come from the
+// caches); backward of the same into a table of 50257 rows with an fp32 base 265 us, 5.2 TB/s: ranks
+// 7, joining the tiles 5, sums and rows without a token 245, joining the runs 8; a table of
+// 50257 x 768 in fp32 for 61 tokens 29 us, 5.4 TB/s of zeros.
 #include "zo_device.h"
 #include "zo_internal.h"
 #include "zo_rows.h"
 
 namespace zo {
 
-constexpr int kRankTile = 2048;               // places that are ranked by comparison
+// Places that are ranked by comparison.  (16384 tokens: 6.7 us for the ranks and 4.8 for joining the
+// tiles, with 2048 10.2 and 4.9.)
+constexpr int kRankTile = 1024;
 constexpr int kRankWaves = 16;                // waves that share a tile's comparisons
 constexpr int kSlice = 512;                   // columns of a wave: 8 a lane
 constexpr int kEmbedThreads = 256, kEmbedWaves = kEmbedThreads / 64;
-constexpr int kFillRows = 8;                  // table rows of a wave that writes what no id names
+// Waves that join a run's parts.  (A run of 1000 tokens, 4096 columns: 21 us, with 8 waves 31.)
+constexpr int kJoinWaves = 16;
 
 struct EmbedParams {
   int64_t N, V;
@@ -40,8 +49,8 @@ struct EmbedParams {
   int32_t *key, *place;                       // sorted
   int32_t *tile_key, *tile_place;             // sorted within tiles
   float* part;                                // [chunks][2][C]: a chunk's first and last run
-  int64_t sum_units;
-  bool fill;
+  int64_t sum_units, fill_units;
+  int fill_rows;                              // table rows of a wave that writes what no id names; 0: none does
 };
 
 // ---------------------------------------------------------------- forward ---
@@ -85,14 +94,14 @@ __device__ __forceinline__ int32_t key_of(const EmbedParams& p, int64_t n) {
   return id >= 0 && id < p.V ? id : static_cast<int32_t>(p.V);
 }
 
-// Ranks 64 places of a tile, one a lane: each of the 16 waves compares them with 128 of it.
+// Ranks 64 places of a tile, one a lane: each of the 16 waves compares them with 64 of it.
 __global__ __launch_bounds__(64 * kRankWaves) void embed_rank_kernel(const EmbedParams p,
                                                                     int32_t* key,
                                                                     int32_t* place) {
   __shared__ int below[kRankWaves][64];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int64_t n = static_cast<int64_t>(blockIdx.x) * 64 + lane;
-  const int64_t tile = n / kRankTile * kRankTile;
+  const int64_t tile = static_cast<int64_t>(blockIdx.x) * 64 / kRankTile * kRankTile;
   constexpr int kShare = kRankTile / kRankWaves;
   const int32_t mine = n < p.N ? key_of(p, n) : 0;
   const int32_t own = static_cast<int32_t>(n - tile);
@@ -100,6 +109,7 @@ __global__ __launch_bounds__(64 * kRankWaves) void embed_rank_kernel(const Embed
 #pragma unroll
   for (int h = 0; h < kShare / 64; ++h) {
     const int first = wave * kShare + h * 64;
+    if (tile + first >= p.N) break;            // (uniform)
     const int64_t m = tile + first + lane;
     const int32_t other = m < p.N ? key_of(p, m) : INT32_MAX;
 #pragma unroll 16
@@ -243,28 +253,50 @@ __device__ __forceinline__ void sum_chunk(const EmbedParams& p, int64_t unit, in
   else store_row<G, B>(p, run, c, sum);
 }
 
-// Rows of the table that no id names: base, or zeros.
+// Rows v0 + i of the table for the bits i of `rows`: base, or zeros; four pieces of a row under way.
+template <typename G, typename B>
+__device__ __forceinline__ void write_base(const EmbedParams& p, int64_t v0, uint64_t rows,
+                                           int lane) {
+  constexpr int kU = 4;
+  while (rows != 0) {
+    const int64_t row = v0 + __builtin_ctzll(rows);
+    rows &= rows - 1;
+    if (p.base == nullptr) {
+      char* to = static_cast<char*>(p.dtable) + row * p.dtable_s * static_cast<int64_t>(sizeof(G));
+      for (int b = 16 * lane; b < p.C * static_cast<int>(sizeof(G)); b += 1024)
+        __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, reinterpret_cast<u32x4*>(to + b));
+      continue;
+    }
+    for (int c0 = 8 * lane; c0 < p.C; c0 += kSlice * kU) {
+      Vec8<B> raw[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        raw[u] = Vec8<B>{};
+        if (c0 + u * kSlice < p.C) raw[u].load_once(p.base, row * p.base_s + c0 + u * kSlice);
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        float x[8];
+        raw[u].get(x);
+        if (c0 + u * kSlice < p.C)
+          Vec8<G>::store_once(p.dtable, row * p.dtable_s + c0 + u * kSlice, x);
+      }
+    }
+  }
+}
+
+// Rows of the table that no id names.
 template <typename G, typename B>
 __device__ __forceinline__ void fill_rows(const EmbedParams& p, int64_t unit, int lane) {
-  const int64_t v0 = unit * kFillRows;
-  const int64_t v = v0 + lane;
-  bool absent = lane < kFillRows && v < p.V;
+  const int64_t v0 = unit * p.fill_rows, v = v0 + lane;
+  bool absent = lane < p.fill_rows && v < p.V;
   if (absent) {
     int64_t at = 0;                           // how many keys are below v
     for (int64_t step = int64_t(1) << 21; step > 0; step >>= 1)
       if (at + step <= p.N && p.key[at + step - 1] < v) at += step;
     absent = at >= p.N || p.key[at] != v;
   }
-  uint64_t rows = __ballot(absent);
-  while (rows != 0) {
-    const int64_t row = v0 + __builtin_ctzll(rows);
-    rows &= rows - 1;
-    for (int c = 8 * lane; c < p.C; c += kSlice) {
-      float x[8] = {};
-      if (p.base != nullptr) base_row<B>(p, row, c, x);
-      Vec8<G>::store(p.dtable, row * p.dtable_s + c, x);
-    }
-  }
+  write_base<G, B>(p, v0, __ballot(absent), lane);
 }
 
 template <typename E, typename G, typename B>
@@ -273,15 +305,91 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_sum_kernel(const EmbedPar
   const int64_t unit =
       static_cast<int64_t>(blockIdx.x) * kEmbedWaves + uniform(threadIdx.x >> 6);
   if (unit < p.sum_units) sum_chunk<E, G, B>(p, unit, lane);
-  else if (p.fill && (unit - p.sum_units) * kFillRows < p.V)
+  else if (unit - p.sum_units < p.fill_units)
     fill_rows<G, B>(p, unit - p.sum_units, lane);
 }
 
+// Up to 256 tokens: every wave has all of them in its lanes and finds an id's places by itself.
+// The wave of an id's first place sums its rows in order, and no sort, parts or join are needed:
+// one launch.  (200 tokens of 768 columns, added in place: 5 us, sorted 12; where they are all one
+// token 22, sorted 13.)
+constexpr int kDirectTokens = 256;
+
+template <typename E, typename G, typename B>
+__global__ __launch_bounds__(kEmbedThreads) void embed_direct_kernel(const EmbedParams p) {
+  constexpr int kK = kDirectTokens / 64, kAtOnce = 4;
+  const int lane = threadIdx.x & 63;
+  const int64_t unit =
+      static_cast<int64_t>(blockIdx.x) * kEmbedWaves + uniform(threadIdx.x >> 6);
+  int32_t key[kK];
+#pragma unroll
+  for (int k = 0; k < kK; ++k)
+    key[k] = 64 * k + lane < p.N ? key_of(p, 64 * k + lane) : static_cast<int32_t>(p.V);
+  if (unit >= p.sum_units) {
+    if (unit - p.sum_units >= p.fill_units) return;
+    const int64_t v0 = (unit - p.sum_units) * p.fill_rows;
+    const int here = static_cast<int>(min(p.V - v0, static_cast<int64_t>(p.fill_rows)));
+    uint64_t rows = 0;
+    for (int r = 0; r < here; ++r) {
+      bool named = false;
+#pragma unroll
+      for (int k = 0; k < kK; ++k) named |= key[k] == v0 + r;
+      if (!__any(named)) rows |= 1ull << r;
+    }
+    write_base<G, B>(p, v0, rows, lane);
+    return;
+  }
+  const int n = static_cast<int>(unit / p.slices);
+  const int c = static_cast<int>(unit % p.slices) * kSlice + 8 * lane;
+  const bool on = c < p.C;
+  int32_t run = 0;
+#pragma unroll
+  for (int k = 0; k < kK; ++k)
+    if (n / 64 == k) run = __builtin_amdgcn_readlane(key[k], n % 64);
+  if (run >= p.V) return;
+  uint64_t places[kK];
+  bool first = true;
+#pragma unroll
+  for (int k = 0; k < kK; ++k) {
+    places[k] = __ballot(key[k] == run);
+    const int before = n - 64 * k;             // places of these 64 that are before n
+    first &= before <= 0 || (places[k] & (before >= 64 ? ~0ull : (1ull << before) - 1)) == 0;
+  }
+  if (!first) return;
+  float sum[8] = {};
+#pragma unroll
+  for (int k = 0; k < kK; ++k) {
+    while (places[k] != 0) {
+      Vec8<E> raw[kAtOnce];
+      int count = 0;
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        raw[u] = Vec8<E>{};
+        if (places[k] == 0) continue;
+        const int64_t at = 64 * k + __builtin_ctzll(places[k]);
+        places[k] &= places[k] - 1;
+        ++count;
+        raw[u].load(p.dout, at * p.dout_s + (on ? c : 0));
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        if (u >= count) break;
+        float x[8];
+        raw[u].get(x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += x[j];
+      }
+    }
+  }
+  if (on) store_row<G, B>(p, run, c, sum);
+}
+
 // The runs that go over a chunk's end, by the chunk that they begin in: its last part
-// and the first parts of the chunks after it, in order, every fourth by a wave.
+// and the first parts of the chunks after it.  The workgroup's waves take a slice each, and
+// where there are more waves than slices, every so many of its parts.
 template <typename G, typename B>
-__global__ __launch_bounds__(kEmbedThreads) void embed_join_kernel(const EmbedParams p) {
-  __shared__ float fold[kEmbedWaves][kSlice];
+__global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(const EmbedParams p) {
+  __shared__ float fold[kJoinWaves][kSlice];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int64_t chunk = blockIdx.x, first = chunk * p.P;
   if (first + p.P >= p.N) return;
@@ -295,17 +403,26 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_join_kernel(const EmbedPa
     more += n;
     if (n < 64) break;
   }
-  for (int s = 0; s < p.slices; ++s) {
-    const int c = s * kSlice + 8 * lane;
-    const bool on = c < p.C;
+  const int shared = p.slices < kJoinWaves ? kJoinWaves / p.slices : 1;   // waves to a slice
+  const int at_once = p.slices < kJoinWaves ? p.slices : kJoinWaves;
+  const int mine = wave / at_once;            // (with waves left over: none of the parts)
+  for (int s0 = 0; s0 < p.slices; s0 += at_once) {
+    const int s = s0 + wave % at_once, c = s * kSlice + 8 * lane;
+    const bool on = c < p.C && mine < shared;
     float sum[8] = {};
-#pragma unroll 4
-    for (int64_t q = wave; q <= more; q += kEmbedWaves) {
-      if (on) {
-        Vec8<float> r;
-        r.load(p.part, ((chunk + q) * 2 + (q == 0 ? 1 : 0)) * p.C + c);
+    constexpr int kAtOnce = 8;                // parts under way
+    for (int64_t q0 = mine; q0 <= more; q0 += kAtOnce * shared) {
+      Vec8<float> raw[kAtOnce];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int64_t q = q0 + u * shared < more ? q0 + u * shared : more;
+        raw[u].load(p.part, ((chunk + q) * 2 + (q == 0 ? 1 : 0)) * p.C + (on ? c : 0));
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        if (q0 + u * shared > more) break;
         float x[8];
-        r.get(x);
+        raw[u].get(x);
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum[j] += x[j];
       }
@@ -313,9 +430,8 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_join_kernel(const EmbedPa
 #pragma unroll
     for (int j = 0; j < 8; ++j) fold[wave][8 * lane + j] = sum[j];
     __syncthreads();
-    if (wave == 0 && on) {
-#pragma unroll
-      for (int w = 1; w < kEmbedWaves; ++w)
+    if (mine == 0 && on) {
+      for (int w = wave + at_once; w < shared * at_once; w += at_once)
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum[j] += fold[w][8 * lane + j];
       store_row<G, B>(p, run, c, sum);
@@ -326,23 +442,38 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_join_kernel(const EmbedPa
 
 namespace {
 
-// Places of a chunk: enough chunks to fill the card, no more than a wave's lanes.
+// Places of a chunk, no more than a wave's lanes.  Longer chunks leave fewer runs and parts to
+// join, and 256 of them, by 8 slices, still fill the card (16384 x 4096, all 50257 rows / added in
+// place / one id for all tokens: 265 / 78 / 93 us; with 512 chunks 270 / 85 / 132, with 1024 279 /
+// 91 / 228).
 int chunk_places(int64_t N) {
-  const int64_t p = (N + 1023) / 1024;
+  const int64_t p = (N + 255) / 256;
   return static_cast<int>(p < 4 ? 4 : p > 64 ? 64 : p);
 }
 
 int64_t chunks_of(int64_t N) { return (N + chunk_places(N) - 1) / chunk_places(N); }
 
+// Rows of a wave that writes what no id names: one, so that the writes' front is compact (50257
+// rows of 4096: 293 us, two 302, eight 328), more of short ones, some 2048 columns.
+int fill_rows_of(int C) { return C >= 2048 ? 1 : C <= 32 ? 64 : 2048 / C; }
+
 size_t rounded(size_t n) { return (n + 15) & ~size_t(15); }
 
 template <typename E, typename G, typename B>
 hipError_t run_sums(const EmbedParams& p, hipStream_t s) {
-  const int64_t units = p.sum_units + (p.fill ? (p.V + kFillRows - 1) / kFillRows : 0);
+  if (p.N <= kDirectTokens) {
+    EmbedParams q = p;
+    q.sum_units = p.N * p.slices;
+    const int64_t units = q.sum_units + p.fill_units;
+    const unsigned grid = static_cast<unsigned>((units + kEmbedWaves - 1) / kEmbedWaves);
+    if (grid == 0) return hipSuccess;
+    embed_direct_kernel<E, G, B><<<grid, kEmbedThreads, 0, s>>>(q);
+    return hipGetLastError();
+  }
+  const int64_t units = p.sum_units + p.fill_units;
   const unsigned grid = static_cast<unsigned>((units + kEmbedWaves - 1) / kEmbedWaves);
-  if (grid == 0) return hipSuccess;
   embed_sum_kernel<E, G, B><<<grid, kEmbedThreads, 0, s>>>(p);
-  if (p.chunks > 1) embed_join_kernel<G, B><<<p.chunks, kEmbedThreads, 0, s>>>(p);
+  embed_join_kernel<G, B><<<p.chunks, 64 * kJoinWaves, 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -360,6 +491,7 @@ hipError_t pick_grad(const EmbedParams& p, const zero_embed_args& a, hipStream_t
 }  // namespace
 
 size_t embed_workspace(int64_t N, int C) {
+  if (N <= kDirectTokens) return 0;
   return 4 * rounded(N * sizeof(int32_t)) +
          static_cast<size_t>(chunks_of(N)) * 2 * C * sizeof(float);
 }
@@ -400,7 +532,10 @@ hipError_t launch_embed_bwd(const zero_embed_args& a, hipStream_t s) {
   p.P = chunk_places(a.N);
   p.chunks = static_cast<int>(chunks_of(a.N));
   p.sum_units = static_cast<int64_t>(p.chunks) * p.slices;
-  p.fill = a.base != a.dtable;
+  if (a.base != a.dtable) {
+    p.fill_rows = fill_rows_of(a.C);
+    p.fill_units = (a.V + p.fill_rows - 1) / p.fill_rows;
+  }
   char* ws = static_cast<char*>(a.workspace);
   const size_t list = rounded(a.N * sizeof(int32_t));
   p.key = reinterpret_cast<int32_t*>(ws);
@@ -408,7 +543,7 @@ hipError_t launch_embed_bwd(const zero_embed_args& a, hipStream_t s) {
   p.tile_key = reinterpret_cast<int32_t*>(ws + 2 * list);
   p.tile_place = reinterpret_cast<int32_t*>(ws + 3 * list);
   p.part = reinterpret_cast<float*>(ws + 4 * list);
-  if (a.N > 0) {
+  if (a.N > kDirectTokens) {
     const unsigned grid = static_cast<unsigned>((a.N + 63) / 64);
     const bool tiles = a.N > kRankTile;
     embed_rank_kernel<<<grid, 64 * kRankWaves, 0, s>>>(p, tiles ? p.tile_key : p.key,
