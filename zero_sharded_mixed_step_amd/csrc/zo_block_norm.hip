@@ -2,10 +2,16 @@
 // and the next block's norm in one pass, forward and backward.
 //
 // Bound by memory: every row is read once, kept in registers across its norms'
-// sums, and written once.  A row belongs to a wave where it has at most 1024 values (no
-// barrier), to a workgroup beyond.  Backward, workgroups walk the rows and keep the
-// sums of the weights' and the gate's gradients for their own columns in registers; each
-// leaves them in a row of the workspace, which a second kernel folds in order.
+// sums, and written once.  Forward, a row belongs to a wave where it has at most 1024 values (no
+// barrier), to a workgroup beyond.  Backward, where a value takes some 30 operations
+// and the sums over the tokens 16 registers a piece, the rows are spread over more threads;
+// workgroups walk the rows and leave their sums in a row of the workspace, which a second kernel
+// folds in order.
+//
+// Measured, bf16 with both norms and a gate by channel: forward of 16384 x 4096 98 us, 5.5 TB/s
+// (x and y read past the caches; through them 102); backward of 8192 x 4096 84 us, 4.8 TB/s, the
+// fold 5 of them (loads through the caches 90; four barriers a row and the gate's sums of their own,
+// twice the instructions: 104).  4097 x 1000, fp32 stream and a gate by token: backward 26 us.
 #include "zo_device.h"
 #include "zo_internal.h"
 #include "zo_rows.h"
@@ -13,7 +19,8 @@
 namespace zo {
 
 // Workgroups of the backward pass at most, each of which leaves a row of parts for
-// every gradient that is summed over the tokens.
+// every gradient that is summed over the tokens.  (8192 x 4096: 84 us; 768 96, 1024 95: the parts
+// grow, and not all run at once.)
 constexpr int kBlockBwdGroups = 512;
 
 struct BlockParams {
@@ -86,10 +93,11 @@ __device__ __forceinline__ char* row_of(void* base, int64_t t, int64_t stride) {
   return const_cast<char*>(row_of<T>(static_cast<const void*>(base), t, stride));
 }
 
-template <typename E>
+template <typename E, bool ONCE = false>
 __device__ __forceinline__ void load8(const void* p, int64_t at, float x[8]) {
   Vec8<E> v;
-  v.load(p, at);
+  if constexpr (ONCE) v.load_once(p, at);
+  else v.load(p, at);
   v.get(x);
 }
 
@@ -139,8 +147,8 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_fwd_kernel(con
 #pragma unroll
     for (int j = 0; j < 8; ++j) h[k][j] = y[k][j] = 0.f;
     if (on[k]) {
-      load8<R>(row_of<R>(p.x, t, p.x_s), c, h[k]);
-      if (p.y != nullptr) load8<E>(row_of<E>(p.y, t, p.y_s), c, y[k]);
+      load8<R, true>(row_of<R>(p.x, t, p.x_s), c, h[k]);
+      if (p.y != nullptr) load8<E, true>(row_of<E>(p.y, t, p.y_s), c, y[k]);
     }
   }
   if (p.y != nullptr) {
@@ -181,118 +189,222 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_fwd_kernel(con
   }
 }
 
-// Several sums over a row's threads at once: one barrier for all of them.
+// A row behind a buffer descriptor: loads past its end, or of an array that is not there, give 0
+// without a branch.  (Past the caches: read once.)
+template <typename T>
+struct BufferRow {
+  __amdgpu_buffer_rsrc_t r;
+  __device__ __forceinline__ BufferRow(const void* base, int64_t t, int64_t stride, int C, bool on) {
+    const char* at = row_of<T>(base, on ? t : 0, stride);
+    r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), 0,
+                                          on ? C * static_cast<int>(sizeof(T)) : 0, 0x00020000);
+  }
+  __device__ __forceinline__ void load(int c, Vec8<T>& v) const {
+    constexpr int kPast = 2;
+    const int b = c * static_cast<int>(sizeof(T));
+    if constexpr (sizeof(T) == 2) {
+      v.r = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, b, 0, kPast));
+    } else {
+      v.a = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, b, 0, kPast));
+      v.b = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, b + 16, 0, kPast));
+    }
+  }
+};
+
+// What a thread's loads of a row fetch, CH pieces of each array.
+template <typename E, typename R, int NT, int CH>
+struct RawRow {
+  Vec8<R> dh[CH], h[CH];
+  Vec8<E> dz[CH], y[CH];
+};
+
+// Sums of up to four values over a row's threads at once.  Halves, then quarters of the wave
+// take a value each by swaps between two registers, so a wave's 64 lanes are joined for
+// all of them in 3 swaps and 7 additions; one barrier, and the sums are in scalar registers.
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float x) {
+  return x + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), CTRL, 0xF, 0xF, true));
+}
+template <int G>
+__device__ __forceinline__ float sum_lanes(float x) {      // of G consecutive lanes, G <= 16
+  if constexpr (G >= 2) x = add_dpp<0xB1>(x);
+  if constexpr (G >= 4) x = add_dpp<0x4E>(x);
+  if constexpr (G >= 8) x = add_dpp<0x141>(x);
+  if constexpr (G >= 16) x = add_dpp<0x140>(x);
+  return x;
+}
+__device__ __forceinline__ float add_halves(float a, float b) {    // a's in the low 32 lanes
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float add_quarters(float a, float b) {  // a's in the even 16 lanes
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
 template <int NT, int N>
 __device__ __forceinline__ void row_sums(float* s, int& turn, float (&x)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = join_lanes<64>(x[i], AddOp());
+  static_assert(N >= 1 && N <= 4);
+  const int lane = threadIdx.x & 63;
+  // lanes 0..15: x[0], 16..31: x[2], 32..47: x[1], 48..63: x[3]
+  float v = add_halves(x[0], N > 1 ? x[N > 1 ? 1 : 0] : x[0]);
+  const float w = N > 2 ? add_halves(x[N > 2 ? 2 : 0], N > 3 ? x[N > 3 ? 3 : 0] : x[N > 2 ? 2 : 0]) : v;
+  v = sum_lanes<16>(add_quarters(v, w));
   if constexpr (NT > 64) {
     constexpr int kW = NT / 64;
-    float* at = s + turn * (3 * kW);
+    float* at = s + turn * (4 * kW);
     turn ^= 1;
-    const int lane = threadIdx.x & 63;
-    if (lane == 0) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) at[i * kW + (threadIdx.x >> 6)] = x[i];
-    }
+    if ((lane & 15) == 0) at[(lane >> 4) * kW + (threadIdx.x % NT >> 6)] = v;
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = join_lanes<kW>(at[i * kW + lane % kW], AddOp());
+    v = sum_lanes<kW>(at[(lane >> 4) * kW + lane % kW]);
   }
+  constexpr int kAt[4] = {0, 32, 16, 48};
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    x[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), kAt[i]));
 }
 
-// What the row's first sums leave of a norm: r = 1 / sqrt(ms) and mean(u v) r, of values
-// scaled by s where ms is past binary32's ends.
-template <int NT, int CH, typename U, typename V>
-__device__ __forceinline__ void far_norm(float* s, int& turn, float ms, float inv_c, float eps,
-                                         float& r, float& m, U u, V v) {
+// r = 1 / sqrt(mean(v^2) + eps) and mean(u v) r of a row whose mean square ms is past
+// binary32's ends, of v times a power of 2.  Rare: every wave reads the whole row again, and
+// needs no barrier for it.  part(c, u, v) gives the values of column c.
+template <typename Part>
+__device__ __forceinline__ void far_norm(int C, float ms, float inv_c, float eps, float& r, float& m,
+                                         Part part) {
   const float f = ms < 1.f ? 0x1p100f : 0x1p-100f;
-  float x[2] = {0.f, 0.f};
-#pragma unroll
-  for (int k = 0; k < CH; ++k) {
-    float a[8], b[8];
-    u(k, a);
-    v(k, b);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      x[0] = __builtin_fmaf(b[j] * f, b[j] * f, x[0]);
-      x[1] = __builtin_fmaf(a[j], b[j] * f, x[1]);
-    }
+  float vv = 0.f, uv = 0.f;
+#pragma unroll 1
+  for (int c = threadIdx.x & 63; c < C; c += 64) {
+    float u, v;
+    part(c, u, v);
+    vv = __builtin_fmaf(v * f, v * f, vv);
+    uv = __builtin_fmaf(u, v * f, uv);
   }
-  row_sums<NT, 2>(s, turn, x);
-  const float rf = __builtin_amdgcn_rsqf(__builtin_fmaf(x[0], inv_c, eps * f * f));
+  vv = join_lanes<64>(vv, AddOp());
+  uv = join_lanes<64>(uv, AddOp());
+  const float rf = __builtin_amdgcn_rsqf(__builtin_fmaf(vv, inv_c, eps * f * f));
   r = f * rf;
-  m = x[1] * inv_c * rf;
+  m = uv * inv_c * rf;
 }
+
+// Threads of a workgroup: four rows of up to 1024 values, or one.
+template <int NT>
+constexpr int kBwdThreads = NT <= 128 ? 4 * NT : NT;
 
 // Two barriers a row: h's and y's squares and u2 . h are summed first, u1 . y when
 // gh is known.  What a row's loads fetched stays packed in registers, and is widened
-// again for each use.
+// again for each use; the columns' weights are widened once.
+//
+// The gate's gradient and the first weight's come from one sum where the tokens share the
+// gate: t = sum of gh yy gives branch_scale (post_w + offset) t and branch_scale gate t.
 template <typename E, typename R, int NT, int CH>
-__global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_bwd_kernel(const BlockParams p) {
-  constexpr int kRows = NT < 256 ? 256 / NT : 1;
-  __shared__ float s[6 * NT / 64];
-  __shared__ float fold[kRows > 1 ? kRows : 1][kRows > 1 ? NT * CH * 8 : 1];
+__global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const BlockParams p) {
+  constexpr int kRows = kBwdThreads<NT> / NT;
+  __shared__ float s[NT > 64 ? kRows : 1][NT > 64 ? 8 * (NT / 64) : 1];
+  __shared__ float fold[kRows > 1 ? kRows : 1][kRows > 1 ? NT * 8 : 1];
   // 16 waves to a unit leave each 128 registers: two pieces of the longest rows are not
-  // held from use to use but read again, and worked on one after the other; u1 waits in
-  // shared memory.
+  // held from use to use but read again, and worked on one after the other, their weights too;
+  // u1 and pre_w's sums wait in shared memory.
   constexpr bool kHold = NT < 1024 || CH == 1;
   constexpr int kHeld = kHold ? CH : 1;
   __shared__ f32x4 kept[kHold ? 1 : 2 * CH][kHold ? 1 : NT];
+  __shared__ f32x4 kept_w2[kHold ? 1 : 2 * CH][kHold ? 1 : NT];
+  const auto put = [&](auto& at, int k, const float x[8]) {
+    at[2 * k][threadIdx.x] = f32x4{x[0], x[1], x[2], x[3]};
+    at[2 * k + 1][threadIdx.x] = f32x4{x[4], x[5], x[6], x[7]};
+  };
+  const auto take = [&](auto& at, int k, float x[8]) {
+    const f32x4 a = at[2 * k][threadIdx.x], b = at[2 * k + 1][threadIdx.x];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[j] = a[j];
+      x[4 + j] = b[j];
+    }
+  };
   const auto apart = [] {
     if constexpr (!kHold) __builtin_amdgcn_sched_barrier(0);
   };
   int turn = 0;
   const int tid = threadIdx.x % NT, row = uniform(threadIdx.x / NT);
   const float inv_c = 1.f / static_cast<float>(p.C);
-  float dw1[CH][8], dg[CH][8], dw2[CH][8];
+  const bool use_y = p.y != nullptr && (p.post || p.gate != nullptr), use_z = p.dz != nullptr;
+  const bool tokens = p.gate != nullptr && p.gate_tokens;
+  // post_w and pre_w with the offset, and the gate times branch_scale; 0 behind the row's end
+  const auto weights = [&](int k, float w1[8], float w2[8], float g[8]) {
+    const int c = 8 * (tid + k * NT);
 #pragma unroll
-  for (int k = 0; k < CH; ++k)
+    for (int j = 0; j < 8; ++j) w1[j] = w2[j] = g[j] = 0.f;
+    if (c < p.C) {
+      weight8<E>(row_of<E>(p.post_w, 0, 0), p.has_post_w, p.offset, c, w1);
+      weight8<E>(row_of<E>(p.pre_w, 0, 0), p.has_pre_w, p.offset, c, w2);
+      if (tokens) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw1[k][j] = dg[k][j] = dw2[k][j] = 0.f;
-  const bool use_y = p.y != nullptr && (p.post || p.gate != nullptr);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRows + row; t < p.T; t += step) {
-    const char *at_dh = row_of<R>(p.dh, t, p.dh_s), *at_h = row_of<R>(p.h, t, p.h_s);
-    const char *at_dz = row_of<E>(p.dz, t, p.dz_s), *at_y = row_of<E>(p.y, t, p.y_s);
-    const char* gate = row_of<E>(p.gate, p.gate_tokens ? t : 0, p.gate_s);
-    const char *post_w = row_of<E>(p.post_w, 0, 0), *pre_w = row_of<E>(p.pre_w, 0, 0);
-    Vec8<R> raw_dh[kHeld], raw_h[kHeld];
-    Vec8<E> raw_dz[kHeld], raw_y[kHeld];
-    const auto fetch = [&](auto& raw, bool wanted, const char* at, int k) {
-      const int c = 8 * (tid + k * NT);
-      raw = {};
-      if (wanted && c < p.C) raw.load(at, c);
-    };
-    const auto widen = [&](auto& raws, bool wanted, const char* at, int k, float x[8]) {
-      if constexpr (!kHold) fetch(raws[0], wanted, at, k);
-      raws[kHold ? k : 0].get(x);
-    };
-    const bool use_z = p.dz != nullptr;
-    const auto dh_of = [&](int k, float x[8]) { widen(raw_dh, p.dh != nullptr, at_dh, k, x); };
-    const auto h_of = [&](int k, float x[8]) { widen(raw_h, use_z, at_h, k, x); };
-    const auto dz_of = [&](int k, float x[8]) { widen(raw_dz, use_z, at_dz, k, x); };
-    const auto y_of = [&](int k, float x[8]) { widen(raw_y, use_y, at_y, k, x); };
-    float sums[3] = {0.f, 0.f, 0.f};             // h^2, u2 h, y^2
-    const auto u2_of = [&](int k, float x[8]) {
-      float w[8];
-      const int c = 8 * (tid + k * NT);
-      dz_of(k, x);
-      if (c < p.C && p.has_pre_w) {
-        load8<E>(pre_w, c, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] *= w[j] + p.offset;
+        for (int j = 0; j < 8; ++j) g[j] = p.branch_scale;
+      } else {
+        gate8<E>(p, row_of<E>(p.gate, 0, 0), c, g);
       }
-    };
+    }
+  };
+  // of a piece: w2, and w1 times the gate (or branch_scale, where every token has its own)
+  float held_w2[kHeld][8], held_gw[kHeld][8];
+  const auto columns = [&](int k, float w2[8], float gw[8]) {
+    float w1[8];
+    weights(k, w1, w2, gw);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) gw[j] *= w1[j];
+  };
+  float sum_t[CH][8], sum_w2[kHeld][8];          // of gh yy (by a token's gate), of dz hh
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    if constexpr (kHold) columns(k, held_w2[k], held_gw[k]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum_t[k][j] = sum_w2[kHold ? k : 0][j] = 0.f;
+    if constexpr (!kHold) put(kept_w2, k, sum_w2[0]);
+  }
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows; t0 < p.T; t0 += step) {
+    // (rows behind the last one: nothing is loaded or stored, but the barriers are met)
+    const int64_t t = t0 + row < p.T ? t0 + row : t0;
+    const int C = t0 + row < p.T ? p.C : 0;
+    RawRow<E, R, NT, kHeld> raw;
+    const BufferRow<R> at_h(p.h, t, p.h_s, C, use_z), at_dh(p.dh, t, p.dh_s, C, p.dh != nullptr);
+    const BufferRow<E> at_dz(p.dz, t, p.dz_s, C, use_z), at_y(p.y, t, p.y_s, C, use_y);
+    const char* gate = row_of<E>(p.gate, tokens ? t : 0, p.gate_s);
     if constexpr (kHold) {
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
-        fetch(raw_h[k], use_z, at_h, k);
-        fetch(raw_dz[k], use_z, at_dz, k);
-        fetch(raw_y[k], use_y, at_y, k);
-        fetch(raw_dh[k], p.dh != nullptr, at_dh, k);
+        const int c = 8 * (tid + k * NT);
+        at_h.load(c, raw.h[k]);
+        at_dz.load(c, raw.dz[k]);
+        at_y.load(c, raw.y[k]);
+        at_dh.load(c, raw.dh[k]);
       }
     }
+    const auto widen = [&](auto& raws, const auto& at, int k, float x[8]) {
+      if constexpr (!kHold) at.load(8 * (tid + k * NT), raws[0]);
+      raws[kHold ? k : 0].get(x);
+    };
+    const auto dh_of = [&](int k, float x[8]) { widen(raw.dh, at_dh, k, x); };
+    const auto h_of = [&](int k, float x[8]) { widen(raw.h, at_h, k, x); };
+    const auto dz_of = [&](int k, float x[8]) { widen(raw.dz, at_dz, k, x); };
+    const auto y_of = [&](int k, float x[8]) { widen(raw.y, at_y, k, x); };
+    const auto columns_of = [&](int k, float w2[8], float gw[8]) {
+      if constexpr (kHold) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          w2[j] = held_w2[k][j];
+          gw[j] = held_gw[k][j];
+        }
+      } else {
+        columns(k, w2, gw);
+      }
+    };
+    const auto u2_of = [&](int k, float x[8]) {
+      float w2[8], gw[8];
+      columns_of(k, w2, gw);
+      dz_of(k, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] *= w2[j];
+    };
+    float sums[3] = {0.f, 0.f, 0.f};             // h^2, u2 h, y^2
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       float h[8], u[8], y[8];
@@ -307,127 +419,139 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_bwd_kernel(con
       }
       apart();
     }
-    row_sums<NT, 3>(s, turn, sums);
+    row_sums<NT, 3>(s[NT > 64 ? row : 0], turn, sums);
     const float ms2 = __builtin_fmaf(sums[0], inv_c, p.eps);
     const float ms1 = __builtin_fmaf(sums[2], inv_c, p.eps);
     float r2 = __builtin_amdgcn_rsqf(ms2), r1 = __builtin_amdgcn_rsqf(ms1);
     float m2 = sums[1] * inv_c * r2;             // mean(u2 hh)
-    if (use_z && far_mean(ms2))
-      far_norm<NT, CH>(s, turn, ms2, inv_c, p.eps, r2, m2, u2_of, h_of);
+    if (!use_z) {
+      r2 = m2 = 0.f;
+    } else if (far_mean(ms2)) {
+      far_norm(C, ms2, inv_c, p.eps, r2, m2, [&](int c, float& u, float& v) {
+        u = value<E>(row_of<E>(p.dz, t, p.dz_s), c) *
+            (p.has_pre_w ? value<E>(p.pre_w, c) + p.offset : 1.f);
+        v = value<R>(row_of<R>(p.h, t, p.h_s), c);
+      });
+    }
     if (!p.post) {
       r1 = 1.f;
     } else if (far_mean(ms1)) {
       float none;
-      far_norm<NT, CH>(s, turn, ms1, inv_c, p.eps, r1, none, y_of, y_of);
+      far_norm(C, ms1, inv_c, p.eps, r1, none, [&](int c, float& u, float& v) {
+        u = 0.f;
+        v = value<E>(row_of<E>(p.y, t, p.y_s), c);
+      });
     }
+    if (C == 0) r1 = r2 = m2 = 0.f;              // (with an eps of 0 they were infinite)
+    const float a2 = -r2 * m2;
     float u1[kHeld][8], dot[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       const int c = 8 * (tid + k * NT);
-      float gh[8];
+      float gh[8], h[8], z[8], w2[8], gw[8];
       dh_of(k, gh);
-      if (use_z) {
-        float h[8], u[8], z[8];
-        h_of(k, h);
-        u2_of(k, u);
-        dz_of(k, z);
+      h_of(k, h);
+      dz_of(k, z);
+      columns_of(k, w2, gw);
+      float* dw2 = sum_w2[kHold ? k : 0];
+      if constexpr (!kHold) take(kept_w2, k, dw2);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float hh = h[j] * r2;
-          dw2[k][j] = __builtin_fmaf(z[j], hh, dw2[k][j]);
-          gh[j] = __builtin_fmaf(r2, __builtin_fmaf(-m2, hh, u[j]), gh[j]);
-        }
+      for (int j = 0; j < 8; ++j) {
+        const float hh = h[j] * r2;
+        dw2[j] = __builtin_fmaf(z[j], hh, dw2[j]);
+        gh[j] = __builtin_fmaf(a2, hh, __builtin_fmaf(r2, z[j] * w2[j], gh[j]));
       }
-      if (c < p.C && p.dx != nullptr) {
+      if constexpr (!kHold) put(kept_w2, k, dw2);
+      if (c < C && p.dx != nullptr) {
         float x[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = gh[j] * p.res_scale;
         Vec8<R>::store(row_of<R>(p.dx, t, p.dx_s), c, x);
       }
       float* u = u1[kHold ? k : 0];
+      float y[8];
+      y_of(k, y);
+      if (tokens) {
+        float g[8], d[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] = 0.f;
-      if (c < p.C && p.y != nullptr) {
-        float y[8], w[8], g[8];
-        y_of(k, y);
-        weight8<E>(post_w, p.has_post_w, p.offset, c, w);
-        gate8<E>(p, gate, c, g);
-        if (p.gate != nullptr) {
-          float d[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            d[j] = p.branch_scale * gh[j] * (y[j] * r1 * w[j]);
-            dg[k][j] += d[j];
-          }
-          if (p.dgate != nullptr) Vec8<E>::store(row_of<E>(p.dgate, t, p.dgate_s), c, d);
-        }
+        for (int j = 0; j < 8; ++j) g[j] = 0.f;
+        if (c < C) load8<E>(gate, c, g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float yy = y[j] * r1, du = gh[j] * g[j];
-          dw1[k][j] = __builtin_fmaf(du, yy, dw1[k][j]);
-          u[j] = du * w[j];
+          const float yy = y[j] * r1, v = gh[j] * gw[j];
+          d[j] = v * yy;
+          u[j] = v * g[j];
+          sum_t[k][j] = __builtin_fmaf(gh[j] * g[j], yy, sum_t[k][j]);
+          dot[0] = __builtin_fmaf(u[j], yy, dot[0]);
+        }
+        if (c < C && p.dgate != nullptr)
+          Vec8<E>::store(row_of<E>(p.dgate, t, p.dgate_s), c, d);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float yy = y[j] * r1;
+          u[j] = gh[j] * gw[j];
+          sum_t[k][j] = __builtin_fmaf(gh[j], yy, sum_t[k][j]);
           dot[0] = __builtin_fmaf(u[j], yy, dot[0]);
         }
       }
-      if constexpr (!kHold) {
-        kept[2 * k][tid] = f32x4{u[0], u[1], u[2], u[3]};
-        kept[2 * k + 1][tid] = f32x4{u[4], u[5], u[6], u[7]};
-      }
+      if constexpr (!kHold) put(kept, k, u);
       apart();
     }
     if (p.dy == nullptr) continue;
-    float m1 = 0.f;                              // mean(u1 yy)
+    float a1 = 0.f;                              // -r1 mean(u1 yy)
     if (p.post) {
-      row_sums<NT, 1>(s, turn, dot);
-      m1 = dot[0] * inv_c;
+      row_sums<NT, 1>(s[NT > 64 ? row : 0], turn, dot);
+      a1 = -r1 * (dot[0] * inv_c);
     }
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       const int c = 8 * (tid + k * NT);
-      if (c >= p.C) continue;
+      if (c >= C) continue;
       float* u = u1[kHold ? k : 0];
-      if constexpr (!kHold) {
-        const f32x4 a = kept[2 * k][tid], b = kept[2 * k + 1][tid];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          u[j] = a[j];
-          u[4 + j] = b[j];
-        }
-      }
+      if constexpr (!kHold) take(kept, k, u);
       if (p.post) {
         float y[8];
         y_of(k, y);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] = r1 * __builtin_fmaf(-m1, y[j] * r1, u[j]);
+        for (int j = 0; j < 8; ++j) u[j] = __builtin_fmaf(a1, y[j] * r1, r1 * u[j]);
       }
       Vec8<E>::store(row_of<E>(p.dy, t, p.dy_s), c, u);
     }
   }
   if (p.part == nullptr) return;
+  // the parts of post_w's, the gate's and pre_w's gradient
 #pragma unroll
-  for (int q = 0; q < 3; ++q) {
-    if (!p.want[q]) continue;
-    float* out = p.part + (static_cast<int64_t>(q) * gridDim.x + blockIdx.x) * p.C;
+  for (int k = 0; k < CH; ++k) {
+    const int c = 8 * (tid + k * NT);
+    float w1[8], w2[8], g[8];
+    weights(k, w1, w2, g);
+    float* dw2 = sum_w2[kHold ? k : 0];
+    if constexpr (!kHold) take(kept_w2, k, dw2);
 #pragma unroll
-    for (int k = 0; k < CH; ++k) {
-      const int c = 8 * (tid + k * NT);
-      const float* x = q == 0 ? dw1[k] : q == 1 ? dg[k] : dw2[k];
+    for (int q = 0; q < 3; ++q) {
+      if (!p.want[q]) continue;
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        x[j] = q == 0 ? sum_t[k][j] * g[j]
+               : q == 1 ? sum_t[k][j] * (p.branch_scale * w1[j]) : dw2[j];
+      float* out = p.part + (static_cast<int64_t>(q) * gridDim.x + blockIdx.x) * p.C;
       if constexpr (kRows == 1) {
         if (c < p.C) Vec8<float>::store(out, c, x);
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) fold[row][c + j] = x[j];
-      }
-    }
-    if constexpr (kRows > 1) {
-      __syncthreads();
-      for (int c = threadIdx.x; c < p.C; c += 256) {
-        float x = 0.f;
+        for (int j = 0; j < 8; ++j) fold[row][8 * tid + j] = x[j];
+        __syncthreads();
+        for (int i = threadIdx.x; i < NT * 8; i += kBwdThreads<NT>) {
+          const int at = 8 * k * NT + i;
+          float v = 0.f;
 #pragma unroll
-        for (int v = 0; v < kRows; ++v) x += fold[v][c];
-        out[c] = x;
+          for (int r = 0; r < kRows; ++r) v += fold[r][i];
+          if (at < p.C) out[at] = v;
+        }
+        __syncthreads();
       }
-      __syncthreads();
     }
   }
 }
@@ -506,7 +630,7 @@ int bwd_groups(int64_t T, int C) {
 template <typename E, typename R, int NT, int CH>
 void run_bwd(const BlockParams& p, hipStream_t s) {
   block_norm_bwd_kernel<E, R, NT, CH>
-      <<<bwd_groups(p.T, p.C), NT < 256 ? 256 : NT, 0, s>>>(p);
+      <<<bwd_groups(p.T, p.C), kBwdThreads<NT>, 0, s>>>(p);
 }
 
 template <typename E, typename R, int NT, int CH>
@@ -516,8 +640,9 @@ void run_fwd(const BlockParams& p, hipStream_t s) {
       <<<static_cast<unsigned>((p.T + kRows - 1) / kRows), kThreads, 0, s>>>(p);
 }
 
-// By the row's length: forward the fewest threads that hold it with 16 values each;
-// backward, where 24 sums a piece of 8 values stay in registers too, with 8 each.
+// By the row's length: forward the fewest threads that hold it with 16 values each (16384 x 4096: 98
+// us, 8 values each 101, 32 each 107), backward with 8 (8192 x 4096: 84, 16 each 88; 4097 x 1000: 26,
+// a wave with 16 each 28).
 template <typename E, typename R>
 hipError_t pick_block(const BlockParams& p, bool fwd, hipStream_t s) {
   if (p.T == 0) return hipSuccess;
@@ -530,7 +655,7 @@ hipError_t pick_block(const BlockParams& p, bool fwd, hipStream_t s) {
     else run_fwd<E, R, 1024, 2>(p, s);
   } else {
     if (p.C <= 512) run_bwd<E, R, 64, 1>(p, s);
-    else if (p.C <= 1024) run_bwd<E, R, 64, 2>(p, s);
+    else if (p.C <= 1024) run_bwd<E, R, 128, 1>(p, s);
     else if (p.C <= 2048) run_bwd<E, R, 256, 1>(p, s);
     else if (p.C <= 4096) run_bwd<E, R, 512, 1>(p, s);
     else if (p.C <= 8192) run_bwd<E, R, 1024, 1>(p, s);

@@ -10,6 +10,11 @@
 // the others' powers and own its own, lp = -log(1 + rest / own) and 1 - q_a = rest /
 // total keep their digits however sure the student is of the token.  What follows from lp
 // (ratio, clipping, KL term) is some binary64 operations a row.
+//
+// Measured: 8192 x 50257 bf16 with the gradient 314 us, 5.2 TB/s of logits read and gradient
+// written (350 with the library's logarithms and exponentials in binary64, which one thread
+// works on while the row waits); the backward alone, 1024 x 131072 fp32, 162 us, 6.6 TB/s (172 with
+// loads through the caches).
 #include "zo_device.h"
 #include "zo_internal.h"
 #include "zo_rows.h"
@@ -294,7 +299,7 @@ __global__ __launch_bounds__(NT) void policy_bwd_kernel(const PolicyParams p) {
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
       x[k].fill_lowest();
-      if (live && cc + k * NT < c1) x[k] = in.load(cc + k * NT);
+      if (live && cc + k * NT < c1) x[k] = in.template load<true>(cc + k * NT);
     }
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
@@ -321,8 +326,8 @@ hipError_t run_fwd(const PolicyParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-// By the length of the row: held in registers where it fits, in the fewest that hold it,
-// and short rows by smaller workgroups.
+// By the length of the row, as the distillation loss, whose rows are taken the same way: held in
+// registers where it fits, in the fewest that hold it, and short rows by smaller workgroups.
 template <typename E>
 hipError_t pick_fwd(const PolicyParams& p, hipStream_t s) {
   const int64_t chunks = (p.V + Chunk<E>::kN - 1) / Chunk<E>::kN + 1;
@@ -342,7 +347,7 @@ hipError_t run_bwd(const PolicyParams& p, hipStream_t s) {
   for (int64_t n0 = 0; n0 < p.N; n0 += 65535) {
     PolicyParams q = p;
     const int64_t rows = p.N - n0 < 65535 ? p.N - n0 : 65535;
-    q.seg = NT * (Chunk<E>::kN == 4 ? 2 : 4);
+    q.seg = NT * (Chunk<E>::kN == 4 ? 2 : 4);    // (the distillation loss's pieces)
     q.z = static_cast<const E*>(p.z) + n0 * p.z_stride;
     q.dz = static_cast<E*>(p.dz) + n0 * p.dz_stride;
     q.action = p.action + n0;

@@ -131,11 +131,15 @@ struct Row {
     const int64_t e0 = static_cast<int64_t>(c) * kN - shift;
     return e0 >= 0 && e0 + kN <= V;
   }
+  // (ONCE: past the caches)
+  template <bool ONCE = false>
   __device__ __forceinline__ Chunk<E> load(int c) const {
     Chunk<E> x;
     const int64_t e0 = static_cast<int64_t>(c) * kN - shift;
     if (whole(c)) {
-      x.r = *reinterpret_cast<const decltype(x.r)*>(p + e0);
+      const auto* at = reinterpret_cast<const decltype(x.r)*>(p + e0);
+      if constexpr (ONCE) x.r = __builtin_nontemporal_load(at);
+      else x.r = *at;
     } else {
       x.fill_lowest();
 #pragma unroll
