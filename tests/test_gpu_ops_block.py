@@ -142,6 +142,19 @@ def test_embed_backward_types(zs, torch, N, V, C, types):
     _embed_bwd(zs, torch, ids, dout, V, -0.37, base, gt)
 
 
+@pytest.mark.parametrize("base", [None, "bf16", "f32"])
+@pytest.mark.parametrize("N", [5, 400])
+@pytest.mark.parametrize("V,C", [(20011, 8), (300007, 8), (9001, 104), (4099, 1528), (33, 8200)])
+def test_embed_backward_rows_without_tokens(zs, torch, V, C, N, base):
+    """Several table rows to a wave, one, and parts of one; the shortest pieces."""
+    g = _gen(torch, V)
+    ids = _ids(torch, "zipf", N, V, g)
+    ids[N // 2] = V - 1
+    b = None if base is None else _rand(torch, g, (V, C), _types(torch, base)[0])
+    for grad in (torch.bfloat16, torch.float32):
+        _embed_bwd(zs, torch, ids, _rand(torch, g, (N, C), torch.bfloat16), V, 1.0, b, grad)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("N", [0, 1, 70, 3000])
 def test_embed_backward_adds_in_place(zs, torch, N, dtype):

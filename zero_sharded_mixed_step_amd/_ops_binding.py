@@ -635,7 +635,8 @@ class GradTable:
     """The gradients of a model as zero_grads_norm and zero_grads_clip take them: their
     addresses, sizes and types, laid out once for tensors that keep their memory from step
     to step.  `outs` are where the clipped gradients go (float32 or bfloat16 each); None: in
-    place.  The tensors are held, and a call raises if one of them has moved since."""
+    place.  The tensors and their memory are held, with the sizes that they have here, and a
+    call raises if one of them has moved since."""
 
     def __init__(self, grads, outs=None):
         self.grads = list(grads)
@@ -661,9 +662,10 @@ class GradTable:
                 raise ValueError(f"an output of {o.numel()} elements for {g.numel()}")
         n = len(self.grads)
         self._at = self._addresses()
-        self._sizes = [t.numel() for t in self.grads]
+        # (a tensor that is given other memory leaves what the addresses name in place)
+        self._memory = [t.untyped_storage() for t in self.grads + self.outs]
         flat = [(C.c_uint64 * n)(*self._at[:n]), (C.c_uint64 * n)(*self._at[-n:] if n else ()),
-                (C.c_int64 * n)(*self._sizes),
+                (C.c_int64 * n)(*(t.numel() for t in self.grads)),
                 (C.c_int32 * n)(*(_CODES[t.dtype] for t in self.grads)),
                 (C.c_int32 * n)(*(_CODES[t.dtype] for t in self.outs))]
         self._arrays = flat
@@ -676,9 +678,8 @@ class GradTable:
         return at
 
     def _checked(self, dev):
-        if self._addresses() != self._at \
-                or list(map(torch.Tensor.numel, self.grads)) != self._sizes:
-            raise ValueError("a tensor of the table has moved or changed its size: make a new table")
+        if self._addresses() != self._at:
+            raise ValueError("a tensor of the table has moved: make a new table")
         if self.grads and self.device != dev:
             raise ValueError(f"the table is on cuda:{self.device}; the library launches on the "
                              f"current device, cuda:{dev}")

@@ -17,9 +17,11 @@
 // Up to 256 tokens need none of this: see embed_direct_kernel.
 //
 // Measured, bf16: forward of 16384 x 4096 41 us, 6.6 TB/s (rows met again come from the
-// caches); backward of the same into a table of 50257 rows with an fp32 base 265 us, 5.2 TB/s: ranks
-// 7, joining the tiles 5, sums and rows without a token 245, joining the runs 8; a table of
+// caches); backward of the same into a table of 50257 rows with an fp32 base 260 us, 5.3 TB/s: ranks
+// 7, joining the tiles 5, sums and rows without a token 240, joining the runs 8; a table of
 // 50257 x 768 in fp32 for 61 tokens 29 us, 5.4 TB/s of zeros.
+#include <algorithm>
+
 #include "zo_device.h"
 #include "zo_internal.h"
 #include "zo_rows.h"
@@ -30,6 +32,7 @@ namespace zo {
 // tiles, with 2048 10.2 and 4.9.)
 constexpr int kRankTile = 1024;
 constexpr int kRankWaves = 16;                // waves that share a tile's comparisons
+constexpr int kFillColumns = 4096;            // columns of a wave that writes what no id names
 constexpr int kSlice = 512;                   // columns of a wave: 8 a lane
 constexpr int kEmbedThreads = 256, kEmbedWaves = kEmbedThreads / 64;
 // Waves that join a run's parts.  (A run of 1000 tokens, 4096 columns: 21 us, with 8 waves 31.)
@@ -50,6 +53,7 @@ struct EmbedParams {
   int32_t *tile_key, *tile_place;             // sorted within tiles
   float* part;                                // [chunks][2][C]: a chunk's first and last run
   int64_t sum_units, fill_units;
+  int fill_parts;                             // parts of a table row that waves take
   int fill_rows;                              // table rows of a wave that writes what no id names; 0: none does
 };
 
@@ -253,33 +257,58 @@ __device__ __forceinline__ void sum_chunk(const EmbedParams& p, int64_t unit, in
   else store_row<G, B>(p, run, c, sum);
 }
 
-// Rows v0 + i of the table for the bits i of `rows`: base, or zeros; four pieces of a row under way.
+// N columns as they are in memory, past the caches: one access of 16 bytes or fewer, so that a
+// wave's accesses leave no gaps.  (13357 rows of 7896, base and gradient in fp32: 174 us; two
+// accesses of 16 bytes with gaps 286.)
+template <typename T, int N>
+using Piece = T __attribute__((ext_vector_type(N)));
+template <typename T, int N>
+__device__ __forceinline__ Piece<T, N> load_piece(const T* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const Piece<T, N>*>(p));
+}
+template <typename T, typename From>
+__device__ __forceinline__ void store_piece(T* p, From x) {
+  constexpr int kN = sizeof(From) / sizeof(x[0]);
+  __builtin_nontemporal_store(__builtin_convertvector(x, Piece<T, kN>),
+                              reinterpret_cast<Piece<T, kN>*>(p));
+}
+
+// A wave's share of the table: rows v0 + i, i < count, for the bits i of `rows`, and of long rows a
+// part: base, or zeros.  The lanes take the rows' pieces one after another over
+// all the rows, four to a lane under way.
 template <typename G, typename B>
-__device__ __forceinline__ void write_base(const EmbedParams& p, int64_t v0, uint64_t rows,
-                                           int lane) {
+__device__ __forceinline__ void write_base(const EmbedParams& p, int64_t unit, int count,
+                                           uint64_t rows, int lane) {
   constexpr int kU = 4;
-  while (rows != 0) {
-    const int64_t row = v0 + __builtin_ctzll(rows);
-    rows &= rows - 1;
-    if (p.base == nullptr) {
-      char* to = static_cast<char*>(p.dtable) + row * p.dtable_s * static_cast<int64_t>(sizeof(G));
-      for (int b = 16 * lane; b < p.C * static_cast<int>(sizeof(G)); b += 1024)
-        __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, reinterpret_cast<u32x4*>(to + b));
-      continue;
+  const int64_t v0 = unit / p.fill_parts * p.fill_rows;
+  const int c0 = static_cast<int>(unit % p.fill_parts) * kFillColumns;
+  const int columns = min(p.C - c0, kFillColumns);
+  const bool zeros = p.base == nullptr;
+  constexpr int kWide = sizeof(G) == 2 && sizeof(B) == 2 ? 8 : 4;                  // columns of a piece
+  const int pieces = zeros ? columns * static_cast<int>(sizeof(G)) / 16 : columns / kWide;   // of a row
+  for (int i0 = lane; i0 < count * pieces; i0 += 64 * kU) {
+    Piece<B, kWide> raw[kU];
+    int row[kU], piece[kU];
+    bool on[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int i = i0 + 64 * u;
+      row[u] = count == 1 ? 0 : i / pieces;
+      piece[u] = i - row[u] * pieces;
+      on[u] = i < count * pieces && ((rows >> row[u]) & 1) != 0;
+      raw[u] = {};
+      if (on[u] && !zeros)
+        raw[u] = load_piece<B, kWide>(static_cast<const B*>(p.base) + (v0 + row[u]) * p.base_s + c0 +
+                                      kWide * piece[u]);
     }
-    for (int c0 = 8 * lane; c0 < p.C; c0 += kSlice * kU) {
-      Vec8<B> raw[kU];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        raw[u] = Vec8<B>{};
-        if (c0 + u * kSlice < p.C) raw[u].load_once(p.base, row * p.base_s + c0 + u * kSlice);
-      }
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        float x[8];
-        raw[u].get(x);
-        if (c0 + u * kSlice < p.C)
-          Vec8<G>::store_once(p.dtable, row * p.dtable_s + c0 + u * kSlice, x);
+    for (int u = 0; u < kU; ++u) {
+      if (!on[u]) continue;
+      G* to = static_cast<G*>(p.dtable) + (v0 + row[u]) * p.dtable_s + c0;
+      if (zeros) {
+        __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, reinterpret_cast<u32x4*>(to) + piece[u]);
+      } else {
+        store_piece<G>(to + kWide * piece[u], raw[u]);
       }
     }
   }
@@ -288,7 +317,7 @@ __device__ __forceinline__ void write_base(const EmbedParams& p, int64_t v0, uin
 // Rows of the table that no id names.
 template <typename G, typename B>
 __device__ __forceinline__ void fill_rows(const EmbedParams& p, int64_t unit, int lane) {
-  const int64_t v0 = unit * p.fill_rows, v = v0 + lane;
+  const int64_t v0 = unit / p.fill_parts * p.fill_rows, v = v0 + lane;
   bool absent = lane < p.fill_rows && v < p.V;
   if (absent) {
     int64_t at = 0;                           // how many keys are below v
@@ -296,7 +325,8 @@ __device__ __forceinline__ void fill_rows(const EmbedParams& p, int64_t unit, in
       if (at + step <= p.N && p.key[at + step - 1] < v) at += step;
     absent = at >= p.N || p.key[at] != v;
   }
-  write_base<G, B>(p, v0, __ballot(absent), lane);
+  const int here = static_cast<int>(min(p.V - v0, static_cast<int64_t>(p.fill_rows)));
+  write_base<G, B>(p, unit, here, __ballot(absent), lane);
 }
 
 template <typename E, typename G, typename B>
@@ -327,7 +357,7 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_direct_kernel(const Embed
     key[k] = 64 * k + lane < p.N ? key_of(p, 64 * k + lane) : static_cast<int32_t>(p.V);
   if (unit >= p.sum_units) {
     if (unit - p.sum_units >= p.fill_units) return;
-    const int64_t v0 = (unit - p.sum_units) * p.fill_rows;
+    const int64_t v0 = (unit - p.sum_units) / p.fill_parts * p.fill_rows;
     const int here = static_cast<int>(min(p.V - v0, static_cast<int64_t>(p.fill_rows)));
     uint64_t rows = 0;
     for (int r = 0; r < here; ++r) {
@@ -336,7 +366,7 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_direct_kernel(const Embed
       for (int k = 0; k < kK; ++k) named |= key[k] == v0 + r;
       if (!__any(named)) rows |= 1ull << r;
     }
-    write_base<G, B>(p, v0, rows, lane);
+    write_base<G, B>(p, unit - p.sum_units, here, rows, lane);
     return;
   }
   const int n = static_cast<int>(unit / p.slices);
@@ -453,9 +483,16 @@ int chunk_places(int64_t N) {
 
 int64_t chunks_of(int64_t N) { return (N + chunk_places(N) - 1) / chunk_places(N); }
 
-// Rows of a wave that writes what no id names: one, so that the writes' front is compact (50257
-// rows of 4096: 293 us, two 302, eight 328), more of short ones, some 2048 columns.
-int fill_rows_of(int C) { return C >= 2048 ? 1 : C <= 32 ? 64 : 2048 / C; }
+// Rows of a wave that writes what no id names: one, or up to 4096 columns of it, so that the writes'
+// front is compact (50257 rows of 4096 with a base: 260 us; two rows 302 and eight 328 where one took
+// 293; 2048 columns 269; 13357 rows of 7896 for 20 tokens: 174, whole rows 184).  More of rows that are
+// shorter than the search for the tokens' rows is long, some 1536 columns (50257 rows of 1024: 48 us, two
+// rows 54; of 768: two 44, one 47; 200000 of 64: 32 rows 20, one 89), or without a search half of it
+// (50257 of 768: one 28.9, two 30.4); of a small table no more than leave 4096 waves.
+int fill_rows_of(int64_t N, int64_t V, int C) {
+  const int64_t rows = std::min<int64_t>((N <= kDirectTokens ? 768 : 1536) / C, V / 4096);
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rows, 64)));
+}
 
 size_t rounded(size_t n) { return (n + 15) & ~size_t(15); }
 
@@ -533,8 +570,9 @@ hipError_t launch_embed_bwd(const zero_embed_args& a, hipStream_t s) {
   p.chunks = static_cast<int>(chunks_of(a.N));
   p.sum_units = static_cast<int64_t>(p.chunks) * p.slices;
   if (a.base != a.dtable) {
-    p.fill_rows = fill_rows_of(a.C);
-    p.fill_units = (a.V + p.fill_rows - 1) / p.fill_rows;
+    p.fill_rows = fill_rows_of(a.N, a.V, a.C);
+    p.fill_parts = (a.C + kFillColumns - 1) / kFillColumns;
+    p.fill_units = (a.V + p.fill_rows - 1) / p.fill_rows * p.fill_parts;
   }
   char* ws = static_cast<char*>(a.workspace);
   const size_t list = rounded(a.N * sizeof(int32_t));
