@@ -515,6 +515,13 @@ def test_policy_strides_and_absent_rows(zs, torch, dtype):
                                row_weight=d[4], kl_coef=0.1)
         R.check("dz", dv, *want["dz"])
         assert bool((dwide[:, :5] == 7).all()) and bool((dwide[:, 5 + V:] == 7).all())
+    # a NaN beside nothing but -inf is not an absent row, wherever it stands
+    for at in (0, int(act[8])):
+        z2 = torch.full((1, V), -math.inf, dtype=dt)
+        z2[0, at] = math.nan
+        l2, s2 = torch.empty(1, device="cuda"), torch.empty(1, 4, device="cuda")
+        zs.zero_policy_fwd(z2.cuda(), d[0][8:9], d[1][8:9], l2, s2)
+        assert math.isnan(float(l2)) and math.isnan(float(s2[0, 0]))
     R.check("loss", loss, *want["loss"])
     keep = [n for n in range(N) if n != 5]
     R.check("stats", stats[keep], want["stats"][0][keep], want["stats"][1][keep])
@@ -757,6 +764,14 @@ def test_grad_table_notices_what_moved(zs, torch):
         zs.GradTable([t], [t[:50]])
     with pytest.raises(TypeError):
         zs.GradTable([t.half()])
+    # the same tensor twice, neighbours that overlap, an output on another's gradient
+    u = torch.randn(200, device="cuda")
+    for grads, outs in (([t, t], None), ([u[:100], u[99:]], None), ([u[:100], u[100:]], [u[100:], t]),
+                        ([t, u[:100]], [u[50:150], u[:100]])):
+        with pytest.raises(ValueError):
+            zs.GradTable(grads, outs)
+    zs.GradTable([t, t], [u[:100], u[100:]])           # read twice, written apart
+    zs.GradTable([u[:100], u[100:]])
 
 
 # ------------------------------------------- streams, graphs, repeatability ---

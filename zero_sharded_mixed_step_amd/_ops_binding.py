@@ -660,6 +660,7 @@ class GradTable:
                     raise ValueError("the tensors are on one device")
             if o.numel() != g.numel():
                 raise ValueError(f"an output of {o.numel()} elements for {g.numel()}")
+        self._refuse_overlaps()
         n = len(self.grads)
         self._at = self._addresses()
         # (a tensor that is given other memory leaves what the addresses name in place)
@@ -670,6 +671,20 @@ class GradTable:
                 (C.c_int32 * n)(*(_CODES[t.dtype] for t in self.outs))]
         self._arrays = flat
         self._ptrs = tuple(C.addressof(a) for a in flat)
+
+    def _refuse_overlaps(self):
+        """An output lies on no other tensor but its own gradient."""
+        spans = []
+        for g, o in zip(self.grads, self.outs):
+            for t, written in ((g, False), (o, True)):
+                if t.numel() and (written or g.data_ptr() != o.data_ptr()):
+                    at = t.data_ptr()
+                    spans.append((at, at + t.numel() * t.element_size(), written))
+        ends = {False: 0, True: 0}                 # of what was read, of what was written
+        for at, end, written in sorted(spans):
+            if at < ends[True] or (written and at < ends[False]):
+                raise ValueError("outputs overlap one another or other gradients")
+            ends[written] = max(ends[written], end)
 
     def _addresses(self):
         at = list(map(torch.Tensor.data_ptr, self.grads))

@@ -109,8 +109,8 @@ struct PolicyRow {
 __device__ __forceinline__ PolicyRow policy_row(const PolicyParams& p, int64_t n, double lp) {
   const double A = p.adv[n];
   double none;
-  const double r =
-      p.old_lp != nullptr ? exp_series(lp - static_cast<double>(p.old_lp[n]), none) : 1.0;
+  const double r = p.old_lp != nullptr ? exp_series(lp - static_cast<double>(p.old_lp[n]), none)
+                   : lp != lp          ? lp : 1.0;
   const double bound = r < p.low ? p.low : r > p.high ? p.high : r;   // (a NaN stays)
   PolicyRow o;
   const double free_ = r * A, held = bound * A;
@@ -174,8 +174,8 @@ __global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void policy_fwd_kernel(const P
   if (lane == 0) tops[wave] = m;
   __syncthreads();
   m = join_lanes<kW>(tops[lane % kW], MaxOp());
-  const bool empty = m == -kInf;
-  if (empty) m = 0.f;                          // nothing but -inf: a sum of 0, not of NaN
+  const bool low = m == -kInf;
+  if (low) m = 0.f;                            // nothing but -inf: a sum of 0, not of NaN
   if constexpr (CH > 0) keep_packed(held);
   // exp((z - m) / tau) = 2^(z k2 - m2), with m2 the rounded m k2: the same in
   // every term, and put right in the logarithm of the sum (see base)
@@ -214,6 +214,7 @@ __global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void policy_fwd_kernel(const P
     const double own = named ? exp_series(x, none) : 0.0, total = rest + own;
     PolicyRow o{0.0, 0.0, 0.0};
     double lse = -__builtin_huge_val(), lp = 0.0, others = 1.0;
+    const bool empty = low && total == 0.0;    // (a NaN has no part in a maximum, but in the sum)
     const bool live = named && !empty;
     // (the largest logit's power is about 1, so the total is no less; where the token has
     // most of it, lp = -log(1 + rest / own))
