@@ -528,6 +528,51 @@ def test_policy_strides_and_absent_rows(zs, torch, dtype):
     assert bool((dv[2:6] == 0).all()) and bool((loss[2:7] == 0).all())
 
 
+@pytest.mark.parametrize("V", [300, 33333])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_policy_rows_far_from_0(zs, torch, dtype, V):
+    """Rows of the type's lowest value alone, or with -inf; logits that agree where binary32 holds
+    no logarithm of a sum beside them: as the same rows next to 0."""
+    dt, = _types(torch, dtype)
+    g = _gen(torch, 21)
+    lowest = torch.finfo(dt).min
+    place = torch.arange(V)
+    # (what the row is, the same row with its largest value at 0)
+    rows = [(torch.full((V,), lowest), torch.zeros(V)),
+            (torch.where(place % 3 == 0, -math.inf, lowest), torch.where(place % 3 == 0, -math.inf, 0.0)),
+            (torch.full((V,), -1e30), torch.zeros(V)),
+            (torch.where(place % 5 == 2, 1e35, torch.randn(V, generator=g)),
+             torch.where(place % 5 == 2, 0.0, -math.inf)),
+            (torch.where(place == 7, lowest, -1e38), torch.where(place == 7, -math.inf, 0.0))]
+    tau = 1.0
+    if dt == torch.float32:                     # (differences of some temperatures beside 2^23 of them)
+        k = torch.randint(-12, 1, (V,), generator=g).float()
+        k[5] = 0.0
+        rows.append((2.0 ** 23 + k, k))
+        rows.append((-2.0 ** 23 + k, k))
+    z, near = (torch.stack([r[i] for r in rows]).to(dt) for i in (0, 1))
+    N = len(rows)
+    act = torch.tensor([3, 7, 299, 2, 11, 5, 6][:N], dtype=torch.int32)
+    adv = torch.tensor([1.0, -0.5, 2.0, 0.7, -1.0, 1.5, -2.0][:N])
+    lp = torch.log_softmax(near.double(), 1).gather(1, act.long()[:, None])[:, 0]
+    old, ref = (lp - 0.1).float(), (lp + 0.3).float()
+    want = B.policy(near, act, adv, tau=tau, old=old, ref=ref, kl_coef=0.2, grad_scale=0.5)
+    d = [t.cuda() for t in (z, act, adv, old, ref)]
+    loss, stats = torch.empty(N, device="cuda"), torch.empty(N, 4, device="cuda")
+    dz, back, inplace = torch.empty_like(d[0]), torch.empty_like(d[0]), d[0].clone()
+    zs.zero_policy_fwd(*d[:3], loss, stats, dlogits=dz, old_logp=d[3], ref_logp=d[4], kl_coef=0.2,
+                       grad_scale=0.5, temperature=tau)
+    zs.zero_policy_bwd(d[0], d[1], stats, back, grad_scale=0.5, temperature=tau)
+    zs.zero_policy_bwd(inplace, d[1], stats, inplace, grad_scale=0.5, temperature=tau)
+    R.check("loss", loss, *want["loss"])
+    R.check("stats", stats[:, 1:], want["stats"][0][:, 1:], want["stats"][1][:, 1:])
+    lse = z.double().max(1).values / tau + want["stats"][0][:, 0]
+    R.check("lse", stats[:, 0], lse, want["stats"][1][:, 0] + 2 ** -23 * lse.abs())
+    R.check("dz", dz, *want["dz"])
+    R.check("dz of the backward", back, *want["dz"])
+    assert _same(back, inplace)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_policy_ends_of_the_range(zs, torch, dtype):
     """Sure tokens (1 - q far below a rounding of 1), tokens of no probability, logits far

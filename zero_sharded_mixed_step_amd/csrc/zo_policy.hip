@@ -178,10 +178,13 @@ __global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void policy_fwd_kernel(const P
   if (low) m = 0.f;                            // nothing but -inf: a sum of 0, not of NaN
   if constexpr (CH > 0) keep_packed(held);
   // exp((z - m) / tau) = 2^(z k2 - m2), with m2 the rounded m k2: the same in
-  // every term, and put right in the logarithm of the sum (see base)
-  const float m2 = m * k2;
+  // every term, and put right in the logarithm of the sum (see base).  Where the rounding would
+  // outweigh the powers (or m k2 is past binary32), from the difference z - m: such a row is read again.
+  const bool far = !(fabsf(m) * k2 <= 0x1p20f);
+  const float m2 = far ? 0.f : m * k2;
   const auto power = [&](float z) { return exp2_hw(__builtin_fmaf(z, k2, -m2)); };
-  const auto chunk_sum = [&](const Chunk<E>& x, int c) {
+  const auto power_far = [&](float z) { return exp2_hw((z - m) * k2); };
+  const auto chunk_sum = [&](const Chunk<E>& x, int c, const auto& power) {
     float s = 0.f;
     if (c == own_chunk) {
 #pragma unroll
@@ -192,12 +195,15 @@ __global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void policy_fwd_kernel(const P
     }
     sum += s;
   };
-  if constexpr (CH > 0) {
+  if (far) {
+#pragma unroll 1
+    for (int c = tid; c < chunks; c += NT) chunk_sum(in.load(c), c, power_far);
+  } else if constexpr (CH > 0) {
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-      if (tid + c * NT < chunks) chunk_sum(held[c], tid + c * NT);
+      if (tid + c * NT < chunks) chunk_sum(held[c], tid + c * NT, power);
   } else {
-    for (int c = tid; c < chunks; c += NT) chunk_sum(in.load(c), c);
+    for (int c = tid; c < chunks; c += NT) chunk_sum(in.load(c), c, power);
   }
   if constexpr (CH > 0) keep_packed(held);
   const double part = join_lanes<64>(static_cast<double>(sum), AddOp());
@@ -208,20 +214,24 @@ __global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void policy_fwd_kernel(const P
     const float w = p.weight ? p.weight[n] : 1.f;
     // x / tau less the powers' base: what m2 and k2 were rounded by comes back here
     const double base = static_cast<double>(m) * p.inv_tau +
-                        (static_cast<double>(m2) - static_cast<double>(m) * k2) * 0.6931471805599453;
+                        (far ? 0.0 : static_cast<double>(m2) - static_cast<double>(m) * k2) *
+                            0.6931471805599453;
     const double x = static_cast<double>(own_z) * p.inv_tau - base;
     double none;
     const double own = named ? exp_series(x, none) : 0.0, total = rest + own;
     PolicyRow o{0.0, 0.0, 0.0};
-    double lse = -__builtin_huge_val(), lp = 0.0, others = 1.0;
+    double lse = -__builtin_huge_val(), lp = 0.0, others = 1.0, log_total = 0.0;
     const bool empty = low && total == 0.0;    // (a NaN has no part in a maximum, but in the sum)
     const bool live = named && !empty;
     // (the largest logit's power is about 1, so the total is no less; where the token has
     // most of it, lp = -log(1 + rest / own))
-    if (!empty) lse = base + log_of(total);
+    if (!empty) {
+      log_total = log_of(total);
+      lse = base + log_total;
+    }
     if (live) {
       const double q = rest / own;
-      lp = q < 0.4 ? -log_near(q) : x - (lse - base);
+      lp = q < 0.4 ? -log_near(q) : x - log_total;
       others = rest / total;
       o = policy_row(p, n, lp);
     }
@@ -258,7 +268,7 @@ __global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void policy_fwd_kernel(const P
     return;
   }
   const float factor = -c0 * row[1];
-  const auto grad = [&](const Chunk<E>& x, int c) {
+  const auto grad = [&](const Chunk<E>& x, int c, const auto& power) {
     float y[kN];
 #pragma unroll
     for (int e = 0; e < kN; ++e) y[e] = power(x.get(e)) * factor;
@@ -268,22 +278,28 @@ __global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void policy_fwd_kernel(const P
     }
     out.store(c, in.shift, y);
   };
-  if constexpr (CH > 0) {
+  if (far) {
+#pragma unroll 1
+    for (int c = tid; c < chunks; c += NT) grad(in.load(c), c, power_far);
+  } else if constexpr (CH > 0) {
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-      if (tid + c * NT < chunks) grad(held[c], tid + c * NT);
+      if (tid + c * NT < chunks) grad(held[c], tid + c * NT, power);
   } else {
-    for (int c = tid; c < chunks; c += NT) grad(in.load(c), c);
+    for (int c = tid; c < chunks; c += NT) grad(in.load(c), c, power);
   }
 }
 
-// Backward from saved statistics: a piece of a row to a workgroup.
+// Backward from saved statistics: a piece of a row to a workgroup.  q_j = exp(z_j / tau - lse), or
+// exp((z_j - z_a) / tau + lp) where lse is so large that its rounding shows: then one workgroup has the
+// whole row, as the gradient may be written over z_a.
 template <typename E, int NT>
 __global__ __launch_bounds__(NT) void policy_bwd_kernel(const PolicyParams p) {
   constexpr int kN = Chunk<E>::kN;
   const int64_t n = blockIdx.y;
   const Row<E> in(p.z, n * p.z_stride, p.V), out(p.dz, n * p.dz_stride, p.V);
-  const int c0 = blockIdx.x * p.seg, c1 = min(c0 + p.seg, in.chunks());
+  const int c0 = blockIdx.x * p.seg;
+  int c1 = min(c0 + p.seg, in.chunks());
   if (c0 >= c1) return;
   const float w = p.weight ? p.weight[n] : 1.f;
   const float lse = p.stats[4 * n], lp = p.stats[4 * n + 1], g = p.stats[4 * n + 2];
@@ -293,7 +309,15 @@ __global__ __launch_bounds__(NT) void policy_bwd_kernel(const PolicyParams p) {
   const float c = w != 0.f && named ? coefficient(p, w, g) : 0.f;
   const bool live = c != 0.f;
   const float inv_tau = static_cast<float>(p.inv_tau);
-  const auto prob = [&](float z) { return exp2_hw(__builtin_fmaf(z, inv_tau, -lse) * kLog2e); };
+  float shift = 0.f, base = lse;
+  if (live && fabsf(lse) > 0x1p16f && fabsf(lp) < fabsf(lse)) {
+    if (blockIdx.x > 0) return;
+    c1 = in.chunks();
+    shift = static_cast<float>(in.p[action]);
+    base = -lp;
+    __syncthreads();
+  }
+  const auto prob = [&](float z) { return exp2_hw(__builtin_fmaf(z - shift, inv_tau, -base) * kLog2e); };
   constexpr int kAtOnce = 4;                           // loads under way, a thread
   for (int cc = c0 + threadIdx.x; cc < c1; cc += kAtOnce * NT) {
     Chunk<E> x[kAtOnce];
