@@ -455,7 +455,7 @@ def _policy_all(zs, torch, z, act, adv, old, ref, w, *, tau=1.0, lo=0.2, hi=0.2,
     return loss, stats, dz
 
 
-# rows of every kernel: 256 threads with 2 and 4 chunks, 1024 with 2, 4, 8 and 16, read again
+# rows of every kernel: in registers, in shared memory too, and partly read again
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("V", [1, 2, 7, 500, 1031, 2047, 4001, 8185, 12001, 16400, 33333, 65540,
                                131071, 200003])
@@ -464,6 +464,23 @@ def test_policy_lengths(zs, torch, V, dtype):
     N = 7 if V < 50000 else 3
     s = _policy_inputs(torch, N, V, dt, V, tau=0.8)
     _policy_all(zs, torch, *s, tau=0.8, kl=0.1, gs=0.25)
+
+
+@pytest.mark.parametrize("V,dtype", [(4088, "bf16"), (4090, "bf16"), (8200, "bf16"), (16370, "bf16"),
+                                     (32761, "bf16"), (65521, "bf16"), (65529, "bf16"), (103921, "bf16"),
+                                     (103937, "bf16"), (2045, "f32"), (32765, "f32"), (51973, "f32"),
+                                     (262147, "f32")])
+def test_policy_lengths_next_to_the_kernels(zs, torch, V, dtype):
+    """The last row of one form and the first of the next; the sampled token in what is kept in
+    shared memory or read again; rows that rise to their end, so that every piece has a new maximum."""
+    dt, = _types(torch, dtype)
+    z, act, adv, old, ref, w = _policy_inputs(torch, 3, V, dt, V)
+    z[1] = (z[1].float() + torch.linspace(0, 40, V)).to(dt)
+    z[2] = (z[2].float() - torch.linspace(0, 40, V)).to(dt)
+    z[2, V // 2:] = -math.inf
+    act = torch.tensor([V - 1, V - 2, 5], dtype=torch.int32)
+    lp = torch.log_softmax(z.double(), 1).gather(1, act.long()[:, None])[:, 0]
+    _policy_all(zs, torch, z, act, adv, (lp + 0.05).float(), (lp - 0.2).float(), w, kl=0.1)
 
 
 @pytest.mark.parametrize("tau,lo,hi", [(1.0, 0.2, 0.28), (0.5, 0.0, 0.0), (3.0, 1.0, 5.0)])

@@ -2,19 +2,22 @@
 //
 // Bound by memory, as the distillation loss: the logits are read once and their
 // gradient is written once.  A workgroup owns a row and keeps it in registers (packed
-// as it came) between the maximum, the sum and the gradient, or, when the row is too long
-// for that, reads it again.  The backward pass needs no row-wide sum, so a row is cut
-// into pieces over workgroups.
+// as it came) between the maximum, the sum and the gradient; of a row too long for that the
+// rest is kept in shared memory, and what is beyond that too is read twice, for its maximum and sum
+// and for its gradient.  The backward pass needs no row-wide sum, so a row is cut into pieces over
+// workgroups.
 //
 // The sampled token is left out of the sum and added to it in binary64: with rest the sum of
 // the others' powers and own its own, lp = -log(1 + rest / own) and 1 - q_a = rest /
 // total keep their digits however sure the student is of the token.  What follows from lp
 // (ratio, clipping, KL term) is some binary64 operations a row.
 //
-// Measured: 8192 x 50257 bf16 with the gradient 314 us, 5.2 TB/s of logits read and gradient
+// Measured: 8192 x 50257 bf16 with the gradient 318 us, 5.2 TB/s of logits read and gradient
 // written (350 with the library's logarithms and exponentials in binary64, which one thread
 // works on while the row waits); the backward alone, 1024 x 131072 fp32, 162 us, 6.6 TB/s (172 with
 // loads through the caches).
+#include <algorithm>
+
 #include "zo_device.h"
 #include "zo_internal.h"
 #include "zo_rows.h"
@@ -31,6 +34,7 @@ struct PolicyParams {
   void* dz;
   int64_t z_stride, dz_stride;
   int seg;                                          // backward: chunks of a piece
+  int kept;                                         // forward: chunks in shared memory
 };
 
 // The row's coefficient in the gradient, grad_scale w g / tau, within binary32: where it
@@ -101,6 +105,14 @@ __device__ __forceinline__ double exp_series(double x, double& beyond) {
   return e;
 }
 
+// The lanes' 16 bytes straight to shared memory, lane l's to to[l].
+template <typename T>
+__device__ __forceinline__ void load_to_lds(T* to, const void* from) {
+  __builtin_amdgcn_global_load_lds(
+      (const __attribute__((address_space(1))) void*)from,
+      (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+
 struct PolicyRow {
   double loss, g, kl;
 };
@@ -127,19 +139,22 @@ __device__ __forceinline__ PolicyRow policy_row(const PolicyParams& p, int64_t n
   return o;
 }
 
-// Forward: loss and statistics, and the gradient if asked for.  CH > 0: the
-// row stays in registers, CH chunks to a thread; CH = 0: it is read again.
-template <typename E, int NT, int CH>
+// Forward: loss and statistics, and the gradient if asked for.  The row stays in registers, CH
+// chunks to a thread.  LONG: what is beyond them stays in shared memory, p.kept chunks, and what is
+// beyond those is read once for its maximum and sum together and again for the gradient.
+template <typename E, int NT, int CH, bool LONG>
 __global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void policy_fwd_kernel(const PolicyParams p) {
   constexpr int kN = Chunk<E>::kN, kW = NT / 64;
-  constexpr int kHeld = CH > 0 ? CH : 1;
+  using Raw = decltype(Chunk<E>::r);
+  extern __shared__ __align__(16) char beyond[];
+  Raw* const kept = reinterpret_cast<Raw*>(beyond);
   __shared__ float tops[kW];
   __shared__ double sums[kW];
   __shared__ float row[2];                     // the gradient's coefficient, and 1 / total
   // two of the chunks that the first wave holds, while one of its lanes works on the row's
   // numbers: with 8 there are no registers for both
   constexpr bool kStash = CH == 8;
-  __shared__ decltype(Chunk<E>::r) stash[kStash ? 2 * 64 : 1];
+  __shared__ Raw stash[kStash ? 2 * 64 : 1];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int64_t n = blockIdx.x;
   const Row<E> in(p.z, n * p.z_stride, p.V), out(p.dz, n * p.dz_stride, p.V);
@@ -150,40 +165,23 @@ __global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void policy_fwd_kernel(const P
   float own_z = 0.f;
   if (named) own_z = static_cast<float>(in.p[action]);
   const float k2 = static_cast<float>(p.inv_tau * 1.4426950408889634);
-  Chunk<E> held[kHeld];
-  if constexpr (CH > 0) {
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      held[c].fill_lowest();
-      if (tid + c * NT < chunks) held[c] = in.load(tid + c * NT);
+  const int kept_end = LONG ? min(chunks, CH * NT + p.kept) : 0;
+  if constexpr (LONG) {
+    for (int c0 = CH * NT + wave * 64; c0 < kept_end; c0 += NT) {
+      const int c = c0 + lane;
+      if (c >= kept_end) continue;
+      if (in.whole(c))
+        load_to_lds(kept + (c0 - CH * NT), in.p + static_cast<int64_t>(c) * kN - in.shift);
+      else
+        kept[c - CH * NT] = in.load(c).r;
     }
   }
-  float m = -kInf, sum = 0.f;
   const auto chunk_max = [&](const Chunk<E>& x, float a) {
 #pragma unroll
     for (int e = 0; e < kN; ++e) a = fmaxf(a, x.get(e));
     return a;
   };
-  if constexpr (CH > 0) {
-#pragma unroll
-    for (int c = 0; c < CH; ++c) m = chunk_max(held[c], m);
-  } else {
-    for (int c = tid; c < chunks; c += NT) m = chunk_max(in.load(c), m);
-  }
-  m = join_lanes<64>(m, MaxOp());
-  if (lane == 0) tops[wave] = m;
-  __syncthreads();
-  m = join_lanes<kW>(tops[lane % kW], MaxOp());
-  const bool low = m == -kInf;
-  if (low) m = 0.f;                            // nothing but -inf: a sum of 0, not of NaN
-  if constexpr (CH > 0) keep_packed(held);
-  // exp((z - m) / tau) = 2^(z k2 - m2), with m2 the rounded m k2: the same in
-  // every term, and put right in the logarithm of the sum (see base).  Where the rounding would
-  // outweigh the powers (or m k2 is past binary32), from the difference z - m: such a row is read again.
-  const bool far = !(fabsf(m) * k2 <= 0x1p20f);
-  const float m2 = far ? 0.f : m * k2;
-  const auto power = [&](float z) { return exp2_hw(__builtin_fmaf(z, k2, -m2)); };
-  const auto power_far = [&](float z) { return exp2_hw((z - m) * k2); };
+  // the powers of a chunk but for the sampled token's
   const auto chunk_sum = [&](const Chunk<E>& x, int c, const auto& power) {
     float s = 0.f;
     if (c == own_chunk) {
@@ -193,19 +191,81 @@ __global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void policy_fwd_kernel(const P
 #pragma unroll
       for (int e = 0; e < kN; ++e) s += power(x.get(e));
     }
-    sum += s;
+    return s;
   };
+  // exp((z - m) / tau) = 2^(z k2 - m2), with m2 the rounded m k2: the same in every term, and put
+  // right in the logarithm of the sum (see base)
+  float rest_m = -kInf, rest_m2 = 0.f, rest_sum = 0.f;
+  if constexpr (LONG) {
+    constexpr int kAtOnce = 4;
+    for (int c = kept_end + tid; c < chunks; c += kAtOnce * NT) {
+      Chunk<E> x[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        x[k].fill_lowest();
+        if (c + k * NT < chunks) x[k] = in.load(c + k * NT);
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const float top = chunk_max(x[k], -kInf);
+        if (top > rest_m) {
+          const float m2 = top * k2;
+          if (rest_sum > 0.f) rest_sum *= exp2_hw(rest_m2 - m2);
+          rest_m = top;
+          rest_m2 = m2;
+        }
+        rest_sum += chunk_sum(x[k], c + k * NT,
+                              [&](float z) { return exp2_hw(__builtin_fmaf(z, k2, -rest_m2)); });
+      }
+    }
+  }
+  Chunk<E> held[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    held[c].fill_lowest();
+    if (tid + c * NT < chunks) held[c] = in.load(tid + c * NT);
+  }
+  float m = rest_m, sum = 0.f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) m = chunk_max(held[c], m);
+  const auto each_kept = [&](const auto& f) {    // (a lane reads what its own wave has put there)
+    if constexpr (LONG) {
+#pragma unroll 1
+      for (int c = CH * NT + tid; c < kept_end; c += NT) {
+        Chunk<E> x;
+        x.r = kept[c - CH * NT];
+        f(x, c);
+      }
+    }
+  };
+  if constexpr (LONG) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    each_kept([&](const Chunk<E>& x, int) { m = chunk_max(x, m); });
+  }
+  m = join_lanes<64>(m, MaxOp());
+  if (lane == 0) tops[wave] = m;
+  __syncthreads();
+  m = join_lanes<kW>(tops[lane % kW], MaxOp());
+  const bool low = m == -kInf;
+  if (low) m = 0.f;                            // nothing but -inf: a sum of 0, not of NaN
+  keep_packed(held);
+  // Where the rounding of m2 would outweigh the powers (or m k2 is past binary32), they are formed
+  // from the difference z - m: such a row is read again.
+  const bool far = !(fabsf(m) * k2 <= 0x1p20f);
+  const float m2 = far ? 0.f : m * k2;
+  const auto power = [&](float z) { return exp2_hw(__builtin_fmaf(z, k2, -m2)); };
+  const auto power_far = [&](float z) { return exp2_hw((z - m) * k2); };
   if (far) {
 #pragma unroll 1
-    for (int c = tid; c < chunks; c += NT) chunk_sum(in.load(c), c, power_far);
-  } else if constexpr (CH > 0) {
+    for (int c = tid; c < chunks; c += NT) sum += chunk_sum(in.load(c), c, power_far);
+  } else {
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-      if (tid + c * NT < chunks) chunk_sum(held[c], tid + c * NT, power);
-  } else {
-    for (int c = tid; c < chunks; c += NT) chunk_sum(in.load(c), c, power);
+      if (tid + c * NT < chunks) sum += chunk_sum(held[c], tid + c * NT, power);
+    each_kept([&](const Chunk<E>& x, int c) { sum += chunk_sum(x, c, power); });
+    if constexpr (LONG) sum += rest_sum > 0.f ? rest_sum * exp2_hw(rest_m2 - m2) : rest_sum;
   }
-  if constexpr (CH > 0) keep_packed(held);
+  keep_packed(held);
   const double part = join_lanes<64>(static_cast<double>(sum), AddOp());
   if (lane == 0) sums[wave] = part;
   __syncthreads();
@@ -281,12 +341,25 @@ __global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void policy_fwd_kernel(const P
   if (far) {
 #pragma unroll 1
     for (int c = tid; c < chunks; c += NT) grad(in.load(c), c, power_far);
-  } else if constexpr (CH > 0) {
+    return;
+  }
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
-      if (tid + c * NT < chunks) grad(held[c], tid + c * NT, power);
-  } else {
-    for (int c = tid; c < chunks; c += NT) grad(in.load(c), c, power);
+  for (int c = 0; c < CH; ++c)
+    if (tid + c * NT < chunks) grad(held[c], tid + c * NT, power);
+  each_kept([&](const Chunk<E>& x, int c) { grad(x, c, power); });
+  if constexpr (LONG) {
+    constexpr int kAtOnce = 4;
+    for (int c = kept_end + tid; c < chunks; c += kAtOnce * NT) {
+      Chunk<E> x[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        x[k].fill_lowest();
+        if (c + k * NT < chunks) x[k] = in.load(c + k * NT);
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+        if (c + k * NT < chunks) grad(x[k], c + k * NT, power);
+    }
   }
 }
 
@@ -347,22 +420,41 @@ namespace {
 
 template <typename E, int NT, int CH>
 hipError_t run_fwd(const PolicyParams& p, hipStream_t s) {
-  policy_fwd_kernel<E, NT, CH><<<static_cast<unsigned>(p.N), NT, 0, s>>>(p);
+  policy_fwd_kernel<E, NT, CH, false><<<static_cast<unsigned>(p.N), NT, 0, s>>>(p);
   return hipGetLastError();
 }
 
-// By the length of the row, as the distillation loss, whose rows are taken the same way: held in
-// registers where it fits, in the fewest that hold it, and short rows by smaller workgroups.
+// Rows beyond 8192 chunks.  Two workgroups fill a unit's registers, and what they keep in
+// shared memory its 160 KiB (4096 x 80000 bf16: 256 us, one with 16 chunks a thread 309; 2048 x 128000:
+// 222, 247; 9000 kept, so that one workgroup runs on a unit: 256, 256).  2048 x 200000: 382 us; 1024 x
+// 131072 fp32 270 us, where everything read in three passes took 515 and 360.
+template <typename E>
+hipError_t run_fwd_long(const PolicyParams& q, int64_t chunks, hipStream_t s) {
+  constexpr int NT = 1024, CH = 8, kKept = 4800;
+  PolicyParams p = q;
+  p.kept = static_cast<int>(std::min<int64_t>(chunks - NT * CH, kKept));
+  const int lds = p.kept * 16;
+  const auto fn = policy_fwd_kernel<E, NT, CH, true>;
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (e != hipSuccess) return e;
+  fn<<<static_cast<unsigned>(p.N), NT, lds, s>>>(p);
+  return hipGetLastError();
+}
+
+// By the length of the row: 8 chunks a thread, in the fewest threads that hold it, so that all
+// rows under way fill the card's registers (bf16 with the gradient: 16384 x 4001 65 us, 256
+// threads with 2 chunks each 81; 4096 x 8200 33, 1024 with 2 45; 4096 x 20000 67, 1024 with 4 76).
+// Rows of fewer than 4096 bf16 or 2048 fp32 values, 128 threads with 4.
 template <typename E>
 hipError_t pick_fwd(const PolicyParams& p, hipStream_t s) {
   const int64_t chunks = (p.V + Chunk<E>::kN - 1) / Chunk<E>::kN + 1;
-  if (chunks <= 256 * 2) return run_fwd<E, 256, 2>(p, s);
-  if (chunks <= 256 * 4) return run_fwd<E, 256, 4>(p, s);
-  if (chunks <= 1024 * 2) return run_fwd<E, 1024, 2>(p, s);
-  if (chunks <= 1024 * 4) return run_fwd<E, 1024, 4>(p, s);
+  if (chunks <= 128 * 4) return run_fwd<E, 128, 4>(p, s);
+  if (chunks <= 128 * 8) return run_fwd<E, 128, 8>(p, s);
+  if (chunks <= 256 * 8) return run_fwd<E, 256, 8>(p, s);
+  if (chunks <= 512 * 8) return run_fwd<E, 512, 8>(p, s);
   if (chunks <= 1024 * 8) return run_fwd<E, 1024, 8>(p, s);
-  if (chunks <= 1024 * 16) return run_fwd<E, 1024, 16>(p, s);
-  return run_fwd<E, 1024, 0>(p, s);
+  return run_fwd_long<E>(p, chunks, s);
 }
 
 template <typename E>
