@@ -331,6 +331,25 @@ def test_block_norm_many_rows(zs, torch, C, T):
     _block_both(zs, torch, s, post=True, branch=0.5)
 
 
+@pytest.mark.parametrize("gate", ["channel", "token"])
+@pytest.mark.parametrize("C,types", [(1288, ("bf16", "f32")), (2048, ("bf16", "bf16")), (5128, ("f32", "f32")),
+                                     (8192, ("bf16", "bf16")), (9000, ("bf16", "f32"))], ids=str)
+def test_block_norm_backward_walks(zs, torch, C, types, gate):
+    """Three rows and more to a workgroup, two rows side by side and the next row's loads ahead of
+    this one's end among them; over its own input, and without the branch's gradient."""
+    dt, rt = _types(torch, *types)
+    T = 2051 if C <= 2048 else 774
+    s = _block_inputs(torch, T, C, dt, rt, C, True, gate)
+    h, _, got = _block_both(zs, torch, s, post=True, offset=0.5, branch=0.3)
+    d = {n: None if t is None else t.cuda() for n, t in s.items()}
+    kw = dict(post_norm=True, post_weight=d["w1"], gate=d["gate"], pre_weight=d["w2"], weight_offset=0.5,
+              branch_scale=0.3)
+    ws, _ = _ws(torch, zs.zero_block_norm_workspace_bytes(T, C))
+    dw2 = torch.empty_like(d["w2"])
+    zs.zero_block_norm_bwd(d["y"], h, d["dh"], d["dz"], d["dh"], None, dpre_weight=dw2, workspace=ws, **kw)
+    assert _same(d["dh"], got["dx"].contiguous()) and _same(dw2, got["dw2"])
+
+
 @pytest.mark.parametrize("C", [64, 1000, 4096, 16384])
 @pytest.mark.parametrize("scale,eps", [(1e25, 1e-6), (1e-20, 0.0), (1e15, 1e-6), (3e-16, 1e-32)])
 def test_block_norm_far_rows(zs, torch, C, scale, eps):

@@ -11,7 +11,10 @@
 // Measured, bf16 with both norms and a gate by channel: forward of 16384 x 4096 98 us, 5.5 TB/s
 // (x and y read past the caches; through them 102); backward of 8192 x 4096 84 us, 4.8 TB/s, the
 // fold 5 of them (loads through the caches 90; four barriers a row and the gate's sums of their own,
-// twice the instructions: 104).  4097 x 1000, fp32 stream and a gate by token: backward 26 us.
+// twice the instructions: 104).  4097 x 1000, fp32 stream and a gate by token: backward 26 us.  8192 x
+// 8192 backward 152 us, 5.3 TB/s; 4096 x 16384, where less is held, 190 us, 4.2 TB/s.
+#include <algorithm>
+
 #include "zo_device.h"
 #include "zo_internal.h"
 #include "zo_rows.h"
@@ -20,8 +23,10 @@ namespace zo {
 
 // Workgroups of the backward pass at most, each of which leaves a row of parts for
 // every gradient that is summed over the tokens.  (8192 x 4096: 84 us; 768 96, 1024 95: the parts
-// grow, and not all run at once.)
-constexpr int kBlockBwdGroups = 512;
+// grow, and not all run at once.)  One of 1024 threads fills a unit: 8192 x 8192 152 us with 256 of
+// them, 162 with 512.  Fewer where each would have less than four rows: 500 x 4096 19 us, 23 with a
+// row each.
+constexpr int kBlockBwdGroups = 512, kBlockBwdLarge = 256, kBlockBwdFew = 256;
 
 struct BlockParams {
   int64_t T;
@@ -285,9 +290,10 @@ __device__ __forceinline__ void far_norm(int C, float ms, float inv_c, float eps
   m = uv * inv_c * rf;
 }
 
-// Threads of a workgroup: four rows of up to 1024 values, or one.
+// Threads of a workgroup: four rows of up to 1024 values, two of up to 2048 (16384 x 2048: 73 us,
+// with one 78), or one.
 template <int NT>
-constexpr int kBwdThreads = NT <= 128 ? 4 * NT : NT;
+constexpr int kBwdThreads = NT <= 128 ? 4 * NT : NT == 256 ? 512 : NT;
 
 // Two barriers a row: h's and y's squares and u2 . h are summed first, u1 . y when
 // gh is known.  What a row's loads fetched stays packed in registers, and is widened
@@ -300,9 +306,9 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
   constexpr int kRows = kBwdThreads<NT> / NT;
   __shared__ float s[NT > 64 ? kRows : 1][NT > 64 ? 8 * (NT / 64) : 1];
   __shared__ float fold[kRows > 1 ? kRows : 1][kRows > 1 ? NT * 8 : 1];
-  // 16 waves to a unit leave each 128 registers: two pieces of the longest rows are not
-  // held from use to use but read again, and worked on one after the other, their weights too;
-  // u1 and pre_w's sums wait in shared memory.
+  // 16 waves to a unit leave each 128 registers: of the longest rows' two pieces dz, dh and the
+  // weights are not held but read at each use, one piece after the other (y read again too: 225 us at
+  // 4096 x 16384 for 190), and u1 and pre_w's sums wait in shared memory.
   constexpr bool kHold = NT < 1024 || CH == 1;
   constexpr int kHeld = kHold ? CH : 1;
   __shared__ f32x4 kept[kHold ? 1 : 2 * CH][kHold ? 1 : NT];
@@ -359,33 +365,46 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
     for (int j = 0; j < 8; ++j) sum_t[k][j] = sum_w2[kHold ? k : 0][j] = 0.f;
     if constexpr (!kHold) put(kept_w2, k, sum_w2[0]);
   }
+  // A workgroup that has its unit to itself fetches the next row before it ends this one (8192 x
+  // 8192: 162 us instead of 171; where two share a unit it gains nothing, 82 for 79 at 4096).
+  constexpr bool kAhead = NT == 1024;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows; t0 < p.T; t0 += step) {
-    // (rows behind the last one: nothing is loaded or stored, but the barriers are met)
-    const int64_t t = t0 + row < p.T ? t0 + row : t0;
-    const int C = t0 + row < p.T ? p.C : 0;
-    RawRow<E, R, NT, kHeld> raw;
+  const auto row_at = [&](int64_t t0) { return t0 + row < p.T ? t0 + row : p.T - 1; };
+  // (rows behind the last one: nothing is loaded or stored, but the barriers are met)
+  const auto length = [&](int64_t t0) { return t0 + row < p.T ? p.C : 0; };
+  RawRow<E, R, NT, CH> raw;
+  const auto fetch = [&](int64_t t0, Vec8<E> (&y)[CH]) {
+    const int64_t t = row_at(t0);
+    const int C = length(t0);
     const BufferRow<R> at_h(p.h, t, p.h_s, C, use_z), at_dh(p.dh, t, p.dh_s, C, p.dh != nullptr);
     const BufferRow<E> at_dz(p.dz, t, p.dz_s, C, use_z), at_y(p.y, t, p.y_s, C, use_y);
-    const char* gate = row_of<E>(p.gate, tokens ? t : 0, p.gate_s);
-    if constexpr (kHold) {
 #pragma unroll
-      for (int k = 0; k < CH; ++k) {
-        const int c = 8 * (tid + k * NT);
-        at_h.load(c, raw.h[k]);
-        at_dz.load(c, raw.dz[k]);
-        at_y.load(c, raw.y[k]);
-        at_dh.load(c, raw.dh[k]);
-      }
+    for (int k = 0; k < CH; ++k) {
+      const int c = 8 * (tid + k * NT);
+      at_h.load(c, raw.h[k]);
+      if constexpr (kHold) at_dz.load(c, raw.dz[k]);
+      at_y.load(c, y[k]);
+      if constexpr (kHold) at_dh.load(c, raw.dh[k]);
     }
-    const auto widen = [&](auto& raws, const auto& at, int k, float x[8]) {
-      if constexpr (!kHold) at.load(8 * (tid + k * NT), raws[0]);
-      raws[kHold ? k : 0].get(x);
+  };
+  if constexpr (kAhead) fetch(static_cast<int64_t>(blockIdx.x) * kRows, raw.y);
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows; t0 < p.T; t0 += step) {
+    const int64_t t = row_at(t0);
+    const int C = length(t0);
+    const char* gate = row_of<E>(p.gate, tokens ? t : 0, p.gate_s);
+    if constexpr (!kAhead) fetch(t0, raw.y);
+    const auto h_of = [&](int k, float x[8]) { raw.h[k].get(x); };
+    const auto y_of = [&](int k, float x[8]) { raw.y[k].get(x); };
+    const auto dh_of = [&](int k, float x[8]) {
+      if constexpr (!kHold)
+        BufferRow<R>(p.dh, t, p.dh_s, C, p.dh != nullptr).load(8 * (tid + k * NT), raw.dh[0]);
+      raw.dh[kHold ? k : 0].get(x);
     };
-    const auto dh_of = [&](int k, float x[8]) { widen(raw.dh, at_dh, k, x); };
-    const auto h_of = [&](int k, float x[8]) { widen(raw.h, at_h, k, x); };
-    const auto dz_of = [&](int k, float x[8]) { widen(raw.dz, at_dz, k, x); };
-    const auto y_of = [&](int k, float x[8]) { widen(raw.y, at_y, k, x); };
+    const auto dz_of = [&](int k, float x[8]) {
+      if constexpr (!kHold)
+        BufferRow<E>(p.dz, t, p.dz_s, C, use_z).load(8 * (tid + k * NT), raw.dz[0]);
+      raw.dz[kHold ? k : 0].get(x);
+    };
     const auto columns_of = [&](int k, float w2[8], float gw[8]) {
       if constexpr (kHold) {
 #pragma unroll
@@ -498,16 +517,17 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
       if constexpr (!kHold) put(kept, k, u);
       apart();
     }
-    if (p.dy == nullptr) continue;
+    Vec8<E> next_y[CH];
+    if constexpr (kAhead) fetch(t0 + step, next_y);
     float a1 = 0.f;                              // -r1 mean(u1 yy)
-    if (p.post) {
+    if (p.dy != nullptr && p.post) {
       row_sums<NT, 1>(s[NT > 64 ? row : 0], turn, dot);
       a1 = -r1 * (dot[0] * inv_c);
     }
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       const int c = 8 * (tid + k * NT);
-      if (c >= C) continue;
+      if (c >= C || p.dy == nullptr) continue;
       float* u = u1[kHold ? k : 0];
       if constexpr (!kHold) take(kept, k, u);
       if (p.post) {
@@ -517,6 +537,10 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
         for (int j = 0; j < 8; ++j) u[j] = __builtin_fmaf(a1, y[j] * r1, r1 * u[j]);
       }
       Vec8<E>::store(row_of<E>(p.dy, t, p.dy_s), c, u);
+    }
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int k = 0; k < CH; ++k) raw.y[k] = next_y[k];
     }
   }
   if (p.part == nullptr) return;
@@ -620,11 +644,13 @@ BlockParams block_params(const zero_block_norm_args& a) {
   return p;
 }
 
-int rows_of(int C) { return C <= 1024 ? 4 : 1; }
+int rows_of(int C) { return C <= 1024 ? 4 : C <= 2048 ? 2 : 1; }
 
 int bwd_groups(int64_t T, int C) {
   const int64_t n = (T + rows_of(C) - 1) / rows_of(C);
-  return static_cast<int>(n < kBlockBwdGroups ? n : kBlockBwdGroups);
+  const int64_t wanted = std::max<int64_t>(T / 4, std::min<int64_t>(n, kBlockBwdFew));
+  return static_cast<int>(
+      std::min({wanted, n, static_cast<int64_t>(C > 4096 ? kBlockBwdLarge : kBlockBwdGroups)}));
 }
 
 template <typename E, typename R, int NT, int CH>
