@@ -130,6 +130,24 @@ def test_embed_backward_tokens(zs, torch, N, kind):
     assert bool((got.cpu()[absent] == 0).all())
 
 
+@pytest.mark.parametrize("kind", ["zipf", "same", "few", "down"])
+@pytest.mark.parametrize("N", [16384, 16385, 40003, 262144, 262145, 2 ** 21])
+def test_embed_backward_many_tokens(zs, torch, N, kind):
+    """Lists that are joined in one, two and three passes, the last ones short; runs over more
+    chunks than a wave has lanes, and than it finds in two steps."""
+    g = _gen(torch, N)
+    V, C = 5003, 8
+    ids = _ids(torch, kind, N, V, g)
+    # whole numbers, whose sums binary32 holds exactly
+    dout = torch.randint(-4, 5, (N, C), generator=g).to(torch.bfloat16)
+    want = torch.zeros(V + 1, C, dtype=torch.float64)
+    want.index_add_(0, torch.where((ids >= 0) & (ids < V), ids, V).long(), dout.double())
+    ws, behind = _ws(torch, zs.zero_embed_workspace_bytes(N, C))
+    got = torch.full((V, C), math.nan, device="cuda")
+    zs.zero_embed_bwd(ids.cuda(), dout.cuda(), got, workspace=ws)
+    assert torch.equal(got.cpu().double(), want[:V]) and bool((behind == 0xFF).all())
+
+
 @pytest.mark.parametrize("types", [("bf16", "bf16", None), ("bf16", "f32", "bf16"), ("f32", "f32", "f32"),
                                    ("bf16", "bf16", "f32"), ("f32", "bf16", "bf16")], ids=str)
 @pytest.mark.parametrize("N,V,C", [(1, 1, 8), (37, 12, 520), (500, 90, 1000), (2100, 70, 1544)])

@@ -12,8 +12,9 @@
 //
 // Sorting needs each place's rank, the number of (id, place) pairs below its own.  It is
 // counted: within a tile of 1024 places by comparing with all of them (a few instructions a
-// comparison, spread over the card), and over the other tiles by searching their sorted
-// lists.  No pass depends on the ids' distribution, and there are one or two launches.
+// comparison, spread over the card), and over the other tiles by searching their sorted lists, 16
+// lists at a time.  No pass depends on the ids' distribution, and there are one launch for 1024
+// tokens, two for 16384, three for 262144.
 // Up to 256 tokens need none of this: see embed_direct_kernel.
 //
 // Measured, bf16: forward of 16384 x 4096 41 us, 6.6 TB/s (rows met again come from the
@@ -32,10 +33,14 @@ namespace zo {
 // tiles, with 2048 10.2 and 4.9.)
 constexpr int kRankTile = 1024;
 constexpr int kRankWaves = 16;                // waves that share a tile's comparisons
+// Sorted lists that are joined at a time.  (262144 tokens of 768 columns: 275 us, two passes of 36 of
+// them; with 32 lists 288 in all, with 64 324; all 256 lists in one pass take 235 alone.)
+constexpr int kMergeLists = 16;
 constexpr int kFillColumns = 4096;            // columns of a wave that writes what no id names
 constexpr int kSlice = 512;                   // columns of a wave: 8 a lane
 constexpr int kEmbedThreads = 256, kEmbedWaves = kEmbedThreads / 64;
-// Waves that join a run's parts.  (A run of 1000 tokens, 4096 columns: 21 us, with 8 waves 31.)
+// Waves that join 512 columns of a run's parts.  (262144 tokens of 768 columns, 43000 of them in one
+// run: 36 us, with 8 waves 44, with 4 70.)
 constexpr int kJoinWaves = 16;
 
 struct EmbedParams {
@@ -133,42 +138,46 @@ __global__ __launch_bounds__(64 * kRankWaves) void embed_rank_kernel(const Embed
   }
 }
 
-// How many keys of the sorted list are below `mine` (with `equal`: or equal to it).
-__device__ __forceinline__ int count_below(const int32_t* list, int n, int32_t mine, bool equal) {
+// How many keys of the sorted list of n <= `size` (a power of 2) are below `mine` (with `equal`:
+// or equal to it).
+__device__ __forceinline__ int count_below(const int32_t* list, int n, int size, int32_t mine,
+                                           bool equal) {
   const int32_t limit = mine + (equal ? 1 : 0);
   int at = 0;
-#pragma unroll
-  for (int step = kRankTile; step > 0; step >>= 1) {
+  for (int step = size; step > 0; step >>= 1) {
     const int next = at + step;
     if (next <= n && list[next - 1] < limit) at = next;
   }
   return at;
 }
 
-// Joins the sorted tiles: a place's rank is its rank in its tile and, of the other
-// tiles, what is below it (of tiles before its own also what is equal).
-__global__ __launch_bounds__(64 * kRankWaves) void embed_merge_kernel(const EmbedParams p) {
+// Joins every kMergeLists sorted lists of 1 << log2_len places: a place's rank is its rank in its
+// list and, of the others, what is below it (of lists before its own also what is equal).
+__global__ __launch_bounds__(64 * kRankWaves) void embed_merge_kernel(
+    int64_t N, int log2_len, const int32_t* list_key, const int32_t* list_place, int32_t* key,
+    int32_t* place) {
   __shared__ int below[kRankWaves][64];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 64 + lane;
-  const int own = static_cast<int>(static_cast<int64_t>(blockIdx.x) * 64 / kRankTile);
-  const int tiles = static_cast<int>((p.N + kRankTile - 1) / kRankTile);
-  const int32_t mine = at < p.N ? p.tile_key[at] : 0;
+  const int own = static_cast<int>(static_cast<int64_t>(blockIdx.x) * 64 >> log2_len);
+  const int group = own / kMergeLists * kMergeLists;
+  const int lists = static_cast<int>((N + (int64_t(1) << log2_len) - 1) >> log2_len);
+  const int32_t mine = at < N ? list_key[at] : 0;
   int rank = 0;
-  for (int t = wave; t < tiles; t += kRankWaves) {
+  for (int t = group + wave; t < min(lists, group + kMergeLists); t += kRankWaves) {
     if (t == own) continue;
-    const int64_t first = static_cast<int64_t>(t) * kRankTile;
-    const int n = static_cast<int>(p.N - first < kRankTile ? p.N - first : kRankTile);
-    rank += count_below(p.tile_key + first, n, mine, t < own);
+    const int64_t first = static_cast<int64_t>(t) << log2_len;
+    const int n = static_cast<int>(min(N - first, int64_t(1) << log2_len));
+    rank += count_below(list_key + first, n, 1 << log2_len, mine, t < own);
   }
   below[wave][lane] = rank;
   __syncthreads();
-  if (wave == 0 && at < p.N) {
-    int64_t to = at - static_cast<int64_t>(own) * kRankTile;
+  if (wave == 0 && at < N) {
+    int64_t to = at - (static_cast<int64_t>(own - group) << log2_len);
 #pragma unroll
     for (int w = 0; w < kRankWaves; ++w) to += below[w][lane];
-    p.key[to] = mine;
-    p.place[to] = p.tile_place[at];
+    key[to] = mine;
+    place[to] = list_place[at];
   }
 }
 
@@ -415,8 +424,8 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_direct_kernel(const Embed
 }
 
 // The runs that go over a chunk's end, by the chunk that they begin in: its last part
-// and the first parts of the chunks after it.  The workgroup's waves take a slice each, and
-// where there are more waves than slices, every so many of its parts.
+// and the first parts of the chunks after it.  A workgroup has a slice of a run, and a wave every
+// 16th of its parts.
 template <typename G, typename B>
 __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(const EmbedParams p) {
   __shared__ float fold[kJoinWaves][kSlice];
@@ -426,56 +435,51 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(const Embed
   const int32_t run = p.key[first + p.P - 1];
   if (run >= p.V || p.key[first + p.P] != run || (first > 0 && p.key[first - 1] == run)) return;
   int64_t more = 0;                           // chunks after this one that begin with the run
-  for (;;) {
-    const int64_t at = (chunk + 1 + more + lane) * p.P;
+  const auto count = [&](int64_t step) {      // adds every step-th, until one does not
+    const int64_t at = (chunk + more + (lane + 1) * step) * p.P;
     const uint64_t same = __ballot(at < p.N && p.key[at] == run);
     const int n = ~same == 0 ? 64 : __builtin_ctzll(~same);
-    more += n;
-    if (n < 64) break;
-  }
-  const int shared = p.slices < kJoinWaves ? kJoinWaves / p.slices : 1;   // waves to a slice
-  const int at_once = p.slices < kJoinWaves ? p.slices : kJoinWaves;
-  const int mine = wave / at_once;            // (with waves left over: none of the parts)
-  for (int s0 = 0; s0 < p.slices; s0 += at_once) {
-    const int s = s0 + wave % at_once, c = s * kSlice + 8 * lane;
-    const bool on = c < p.C && mine < shared;
-    float sum[8] = {};
-    constexpr int kAtOnce = 8;                // parts under way
-    for (int64_t q0 = mine; q0 <= more; q0 += kAtOnce * shared) {
-      Vec8<float> raw[kAtOnce];
+    more += n * step;
+    return n == 64;
+  };
+  if (count(1))
+    for (int64_t step = 4096; step > 0; step >>= 6) count(step);
+  const int c = blockIdx.y * kSlice + 8 * lane;
+  const bool on = c < p.C;
+  float sum[8] = {};
+  constexpr int kAtOnce = 8;                  // parts under way
+  for (int64_t q0 = wave; q0 <= more; q0 += kAtOnce * kJoinWaves) {
+    Vec8<float> raw[kAtOnce];
 #pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) {
-        const int64_t q = q0 + u * shared < more ? q0 + u * shared : more;
-        raw[u].load(p.part, ((chunk + q) * 2 + (q == 0 ? 1 : 0)) * p.C + (on ? c : 0));
-      }
-#pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) {
-        if (q0 + u * shared > more) break;
-        float x[8];
-        raw[u].get(x);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] += x[j];
-      }
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int64_t q = min(q0 + u * kJoinWaves, more);
+      raw[u].load(p.part, ((chunk + q) * 2 + (q == 0 ? 1 : 0)) * p.C + (on ? c : 0));
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) fold[wave][8 * lane + j] = sum[j];
-    __syncthreads();
-    if (mine == 0 && on) {
-      for (int w = wave + at_once; w < shared * at_once; w += at_once)
+    for (int u = 0; u < kAtOnce; ++u) {
+      if (q0 + u * kJoinWaves > more) break;
+      float x[8];
+      raw[u].get(x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] += fold[w][8 * lane + j];
-      store_row<G, B>(p, run, c, sum);
+      for (int j = 0; j < 8; ++j) sum[j] += x[j];
     }
-    __syncthreads();
   }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) fold[wave][8 * lane + j] = sum[j];
+  __syncthreads();
+  if (wave > 0 || !on) return;
+  for (int w = 1; w < kJoinWaves && w <= more; ++w)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] += fold[w][8 * lane + j];
+  store_row<G, B>(p, run, c, sum);
 }
 
 namespace {
 
 // Places of a chunk, no more than a wave's lanes.  Longer chunks leave fewer runs and parts to
 // join, and 256 of them, by 8 slices, still fill the card (16384 x 4096, all 50257 rows / added in
-// place / one id for all tokens: 265 / 78 / 93 us; with 512 chunks 270 / 85 / 132, with 1024 279 /
-// 91 / 228).
+// place / one id for all tokens: 274 / 101 / 54 us; with 512 chunks 277 / 101 / 65, with 1024 284 /
+// 110 / 91).
 int chunk_places(int64_t N) {
   const int64_t p = (N + 255) / 256;
   return static_cast<int>(p < 4 ? 4 : p > 64 ? 64 : p);
@@ -510,7 +514,8 @@ hipError_t run_sums(const EmbedParams& p, hipStream_t s) {
   const int64_t units = p.sum_units + p.fill_units;
   const unsigned grid = static_cast<unsigned>((units + kEmbedWaves - 1) / kEmbedWaves);
   embed_sum_kernel<E, G, B><<<grid, kEmbedThreads, 0, s>>>(p);
-  embed_join_kernel<G, B><<<p.chunks, 64 * kJoinWaves, 0, s>>>(p);
+  embed_join_kernel<G, B>
+      <<<dim3(p.chunks, p.slices), 64 * kJoinWaves, 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -583,10 +588,17 @@ hipError_t launch_embed_bwd(const zero_embed_args& a, hipStream_t s) {
   p.part = reinterpret_cast<float*>(ws + 4 * list);
   if (a.N > kDirectTokens) {
     const unsigned grid = static_cast<unsigned>((a.N + 63) / 64);
-    const bool tiles = a.N > kRankTile;
-    embed_rank_kernel<<<grid, 64 * kRankWaves, 0, s>>>(p, tiles ? p.tile_key : p.key,
-                                                      tiles ? p.tile_place : p.place);
-    if (tiles) embed_merge_kernel<<<grid, 64 * kRankWaves, 0, s>>>(p);
+    // the lists go to and fro between two places, the last ones to p.key
+    int passes = 0;
+    for (int64_t n = kRankTile; n < a.N; n *= kMergeLists) ++passes;
+    int32_t* const lists[2][2] = {{p.key, p.place}, {p.tile_key, p.tile_place}};
+    embed_rank_kernel<<<grid, 64 * kRankWaves, 0, s>>>(p, lists[passes % 2][0], lists[passes % 2][1]);
+    for (int64_t n = kRankTile; n < a.N; n *= kMergeLists, --passes) {
+      int32_t* const* from = lists[passes % 2];
+      int32_t* const* to = lists[(passes + 1) % 2];
+      embed_merge_kernel<<<grid, 64 * kRankWaves, 0, s>>>(a.N, __builtin_ctzll(n), from[0], from[1],
+                                                         to[0], to[1]);
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
