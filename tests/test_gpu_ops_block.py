@@ -774,6 +774,23 @@ def test_grads_more_tensors_than_a_launch(zs, torch, count):
         assert _same(a, b)
 
 
+@pytest.mark.parametrize("n", [8188, 8192, 8195, 24576, 40001])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_grads_clip_types_of_whole_tiles(zs, torch, n, offset):
+    """Every pair of types, whole tiles and cut ones, beside each other in one call."""
+    pairs = [(a, b) for a in (torch.bfloat16, torch.float32) for b in (torch.bfloat16, torch.float32)]
+    grads = _tensors(torch, [n] * 4, [a for a, _ in pairs], 21, offset=offset)
+    outs = _tensors(torch, [n] * 4, [b for _, b in pairs], 22, offset=1 - offset)
+    acc = zs.new_norm_acc(1)
+    ws, _ = _ws(torch, zs.zero_grads_workspace_bytes())
+    table, coef = zs.GradTable(grads, outs), torch.empty(1, device="cuda")
+    zs.zero_grads_norm(table, acc, inv_scale=0.3, workspace=ws)
+    zs.zero_grads_clip(table, acc, max_norm=2.0, inv_scale=0.3, coef_out=coef)
+    inv = float(torch.tensor(0.3))
+    for a, b in zip(outs, _clipped(torch, grads, outs, inv, float(coef))):
+        assert _same(a, b)
+
+
 def test_grads_many_tiles(zs, torch):
     """More tiles than workgroups, in both calls, over several tensors."""
     sizes = [8192 * 700 + 5, 8192 * 4100, 11, 8192 * 900 + 8191]

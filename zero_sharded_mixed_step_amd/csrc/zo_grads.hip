@@ -75,28 +75,35 @@ struct GradClipParams {
 static_assert(sizeof(GradNormParams) <= 4096 && sizeof(GradClipParams) <= 4096,
               "kernel arguments");
 
-// What a thread holds of a tile: four chunks of eight elements.  The tensor's start may lie
-// at any element.
+// What a thread holds of a tile: chunks of W elements.  The tensor's start may lie at any
+// element.
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
-template <bool BF16>
+template <bool BF16, int W>
 struct RawTile {
-  zs::u32x4 v[kTileChunks][BF16 ? 1 : 2];
+  static constexpr int kWidth = W, kChunks = kGradTile / W / kGradThreads;
+  static constexpr int kWide = BF16 ? 8 : 4;         // elements of 16 bytes
+  static constexpr int kPieces = (W + kWide - 1) / kWide;
+  zs::u32x4 v[kChunks][kPieces];                     // (8 bytes in the first two words)
 
-  // A thread's chunk u of a tile starts at element (u * 256 + thread) * 8.
+  // A thread's chunk u of a tile starts at element (u * 256 + thread) * W.
   __device__ __forceinline__ static int chunk_at(int u) {
-    return (u * kGradThreads + static_cast<int>(threadIdx.x)) * kVec;
+    return (u * kGradThreads + static_cast<int>(threadIdx.x)) * W;
   }
 
   __device__ __forceinline__ void load(const char* tile) {
 #pragma unroll
-    for (int u = 0; u < kTileChunks; ++u) {
-      if constexpr (BF16) {
-        v[u][0] = reinterpret_cast<const u32x4_any*>(tile)[chunk_at(u) / kVec];
+    for (int u = 0; u < kChunks; ++u) {
+      if constexpr (BF16 && W == 8) {
+        v[u][0] = reinterpret_cast<const u32x4_any*>(tile)[chunk_at(u) / 8];
+      } else if constexpr (BF16) {
+        const u32x2_any x = reinterpret_cast<const u32x2_any*>(tile)[chunk_at(u) / 4];
+        v[u][0] = zs::u32x4{x[0], x[1], 0, 0};
       } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < kPieces; ++h)
           v[u][h] = __builtin_bit_cast(
               zs::u32x4, reinterpret_cast<const f32x4_any*>(tile)[chunk_at(u) / 4 + h]);
       }
@@ -106,12 +113,12 @@ struct RawTile {
   // Of a tile of n elements: those behind it are +0.
   __device__ __forceinline__ void load_some(const char* tile, int n) {
 #pragma unroll
-    for (int u = 0; u < kTileChunks; ++u) {
+    for (int u = 0; u < kChunks; ++u) {
       const int c = chunk_at(u);
 #pragma unroll
-      for (int h = 0; h < (BF16 ? 1 : 2); ++h) v[u][h] = zs::u32x4{0, 0, 0, 0};
+      for (int h = 0; h < kPieces; ++h) v[u][h] = zs::u32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) {
+      for (int j = 0; j < W; ++j) {
         if (c + j >= n) continue;
         if constexpr (BF16)
           v[u][0][j / 2] |=
@@ -122,9 +129,9 @@ struct RawTile {
     }
   }
 
-  __device__ __forceinline__ void widen(int u, float scale, float x[kVec]) const {
+  __device__ __forceinline__ void widen(int u, float scale, float x[W]) const {
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
+    for (int j = 0; j < W; ++j) {
       if constexpr (BF16) {
         const uint32_t h = v[u][0][j / 2];
         x[j] = __uint_as_float(j & 1 ? h & 0xFFFF0000u : h << 16) * scale;
@@ -136,27 +143,38 @@ struct RawTile {
 };
 
 // Works on one tile: use(raw, tensor, info, first element, elements).
-template <bool BF16, typename Use>
+template <bool BF16, int W, typename Use>
 __device__ __forceinline__ void with_tile(const void* tensor, int i, uint32_t info, int64_t e0,
                                           int n, Use use) {
   const char* base = static_cast<const char*>(tensor) + e0 * (BF16 ? 2 : 4);
-  RawTile<BF16> raw;
+  RawTile<BF16, W> raw;
   if (n == kGradTile) raw.load(base);
   else raw.load_some(base, n);
   use(raw, i, info, e0, n);
 }
 
-// A workgroup's tiles, one of every gridDim.x; with BACK a tensor's last tile comes first.
-template <bool BACK, int N, typename Use>
+// A workgroup's tiles, one of every gridDim.x; with CLIP a tensor's last tile comes first, and
+// chunks are of 4 elements where either side is fp32: 16 bytes, so that a wave's accesses leave no
+// gaps (60 tensors of 4096 x 4096, fp32: 1540 us, in chunks of 8 1900; bf16 to fp32 1160, 1540).
+template <bool CLIP, int N, typename Use>
 __device__ __forceinline__ void walk(const TensorTable<N>& t, uint32_t tiles, Use use) {
   for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int i = t.find(tile);
     const uint32_t info = t.info[i], first = t.first[i], last = t.first[i + 1] - 1;
-    const uint32_t inside = BACK ? last - tile : tile - first;
+    const uint32_t inside = CLIP ? last - tile : tile - first;
     const int64_t e0 = static_cast<int64_t>(inside) * kGradTile;
     const int n = inside == last - first ? static_cast<int>(info & kTail) : kGradTile;
-    if (info & kBf16In) with_tile<true>(t.grad[i], i, info, e0, n, use);
-    else with_tile<false>(t.grad[i], i, info, e0, n, use);
+    if (!(info & kBf16In)) {
+      with_tile<false, CLIP ? 4 : 8>(t.grad[i], i, info, e0, n, use);
+      continue;
+    }
+    if constexpr (CLIP) {
+      if (!(info & kBf16Out)) {
+        with_tile<true, 4>(t.grad[i], i, info, e0, n, use);
+        continue;
+      }
+    }
+    with_tile<true, 8>(t.grad[i], i, info, e0, n, use);
   }
 }
 
@@ -165,7 +183,7 @@ __device__ __forceinline__ void walk(const TensorTable<N>& t, uint32_t tiles, Us
 // chunk's sum infinite or NaN: they are looked for (zs::chunk_sumsq) only then.  Elements
 // behind the tensor's end are +0.
 template <bool BF16>
-__device__ __forceinline__ void tile_sums(const RawTile<BF16>& r, float scale,
+__device__ __forceinline__ void tile_sums(const RawTile<BF16, kVec>& r, float scale,
                                           double s4[kTileChunks], uint32_t& nonfinite) {
 #pragma unroll
   for (int u = 0; u < kTileChunks; ++u) {
@@ -248,50 +266,52 @@ __global__ __launch_bounds__(kFoldThreads) void grads_fold_kernel(const uint64_t
 // which plain stores of the outputs would push out.  194 tensors of 301 MB, norm and
 // clipping: 175 us instead of 207; from the last tile to the first, so that the clipping
 // begins with what the norm read last, 168.
-template <bool BF16>
-__device__ __forceinline__ void store_chunk(void* base, int c, int left, const float x[kVec]) {
+template <bool BF16, int W>
+__device__ __forceinline__ void store_chunk(void* base, int c, int left, const float x[W]) {
   if constexpr (BF16) {
     uint16_t* p = static_cast<uint16_t*>(base) + c;
-    zs::u32x4 w;
+    uint32_t w[W / 2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < W / 2; ++j) {
       const __bf16 lo = static_cast<__bf16>(x[2 * j]), hi = static_cast<__bf16>(x[2 * j + 1]);
       w[j] = static_cast<uint32_t>(__builtin_bit_cast(uint16_t, lo)) |
              static_cast<uint32_t>(__builtin_bit_cast(uint16_t, hi)) << 16;
     }
-    if (left >= kVec) {
-      __builtin_nontemporal_store(static_cast<u32x4_any>(w), reinterpret_cast<u32x4_any*>(p));
+    if (left >= W) {
+      if constexpr (W == 8)
+        __builtin_nontemporal_store(u32x4_any{w[0], w[1], w[2], w[3]}, reinterpret_cast<u32x4_any*>(p));
+      else
+        __builtin_nontemporal_store(u32x2_any{w[0], w[1]}, reinterpret_cast<u32x2_any*>(p));
     } else {
 #pragma unroll
-      for (int j = 0; j < kVec; ++j)
+      for (int j = 0; j < W; ++j)
         if (j < left) p[j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
     }
   } else {
+    static_assert(W == 4);
     float* p = static_cast<float*>(base) + c;
-    if (left >= kVec) {
-      f32x4_any* q = reinterpret_cast<f32x4_any*>(p);
-      __builtin_nontemporal_store(f32x4_any{x[0], x[1], x[2], x[3]}, q);
-      __builtin_nontemporal_store(f32x4_any{x[4], x[5], x[6], x[7]}, q + 1);
+    if (left >= W) {
+      __builtin_nontemporal_store(f32x4_any{x[0], x[1], x[2], x[3]}, reinterpret_cast<f32x4_any*>(p));
     } else {
 #pragma unroll
-      for (int j = 0; j < kVec; ++j)
+      for (int j = 0; j < W; ++j)
         if (j < left) p[j] = x[j];
     }
   }
 }
 
-template <bool OUT, bool IN>
-__device__ __forceinline__ void clip_tile(const RawTile<IN>& r, int n, float scale, float coef,
+template <bool OUT, bool IN, int W>
+__device__ __forceinline__ void clip_tile(const RawTile<IN, W>& r, int n, float scale, float coef,
                                           void* out) {
 #pragma unroll
-  for (int u = 0; u < kTileChunks; ++u) {
-    const int c = RawTile<IN>::chunk_at(u);
-    float g[kVec];
+  for (int u = 0; u < RawTile<IN, W>::kChunks; ++u) {
+    const int c = RawTile<IN, W>::chunk_at(u);
+    float g[W];
     r.widen(u, scale, g);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) g[j] *= coef;
-    if (n == kGradTile) store_chunk<OUT>(out, c, kVec, g);
-    else store_chunk<OUT>(out, c, n - c, g);
+    for (int j = 0; j < W; ++j) g[j] *= coef;
+    if (n == kGradTile) store_chunk<OUT, W>(out, c, W, g);
+    else store_chunk<OUT, W>(out, c, n - c, g);
   }
 }
 
@@ -350,7 +370,9 @@ __device__ __forceinline__ zs::Gate gate_and_norm(const GradClipParams& p, doubl
   return g;
 }
 
-__global__ __launch_bounds__(kGradThreads) void grads_clip_kernel(const GradClipParams p) {
+// (At least four workgroups to a unit: with the registers that the compiler takes by itself three,
+// and 194 tensors of 301 MB take 169 us for both passes, not 165.)
+__global__ __launch_bounds__(kGradThreads, 4) void grads_clip_kernel(const GradClipParams p) {
   __shared__ zs::Gate s_gate;
   if (threadIdx.x == 0) {
     double norm;
@@ -369,8 +391,13 @@ __global__ __launch_bounds__(kGradThreads) void grads_clip_kernel(const GradClip
     if (coef == 1.f && p.inv_scale == 1.f && p.out[i] == p.t.grad[i]) return;
     const bool out = info & kBf16Out;
     char* to = static_cast<char*>(p.out[i]) + e0 * (out ? 2 : 4);
-    if (out) clip_tile<true>(raw, n, p.inv_scale, coef, to);
-    else clip_tile<false>(raw, n, p.inv_scale, coef, to);
+    constexpr int kW = std::remove_reference_t<decltype(raw)>::kWidth;
+    if constexpr (kW == 8) {
+      clip_tile<true>(raw, n, p.inv_scale, coef, to);
+    } else {
+      if (out) clip_tile<true>(raw, n, p.inv_scale, coef, to);
+      else clip_tile<false>(raw, n, p.inv_scale, coef, to);
+    }
   });
 }
 
