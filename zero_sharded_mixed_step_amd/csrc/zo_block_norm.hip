@@ -11,8 +11,8 @@
 // Measured, bf16 with both norms and a gate by channel: forward of 16384 x 4096 98 us, 5.5 TB/s
 // (x and y read past the caches; through them 102); backward of 8192 x 4096 84 us, 4.8 TB/s, the
 // fold 5 of them (loads through the caches 90; four barriers a row and the gate's sums of their own,
-// twice the instructions: 104).  4097 x 1000, fp32 stream and a gate by token: backward 26 us.  8192 x
-// 8192 backward 152 us, 5.3 TB/s; 4096 x 16384, where less is held, 190 us, 4.2 TB/s.
+// twice the instructions: 104).  4097 x 1000, fp32 stream and a gate by token: backward 25 us.  8192 x
+// 8192 backward 153 us, 5.3 TB/s; 4096 x 16384, where less is held, 192 us, 4.2 TB/s.
 #include <algorithm>
 
 #include "zo_device.h"
@@ -98,19 +98,78 @@ __device__ __forceinline__ char* row_of(void* base, int64_t t, int64_t stride) {
   return const_cast<char*>(row_of<T>(static_cast<const void*>(base), t, stride));
 }
 
-template <typename E, bool ONCE = false>
-__device__ __forceinline__ void load8(const void* p, int64_t at, float x[8]) {
-  Vec8<E> v;
-  if constexpr (ONCE) v.load_once(p, at);
-  else v.load(p, at);
-  v.get(x);
+// A piece's columns: 8 from c on, or, SPLIT, 4 from c on and 4 that are kHalf further, so that
+// a wave's accesses of 16 bytes leave no gaps where values have 4 bytes (fp32, 8192 x 4096: forward 98
+// us, 8 in a row 111; backward 152, 168).
+constexpr int kHalf = 256;
+template <typename E, typename R>
+constexpr bool kSplit = sizeof(E) == 4 || sizeof(R) == 4;
+template <bool SPLIT, int NT>
+__device__ __forceinline__ int column(int tid, int k) {
+  return SPLIT ? 8 * ((tid & ~63) + k * NT) + 4 * (tid & 63) : 8 * (tid + k * NT);
+}
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// Four columns.
+template <bool ONCE>
+__device__ __forceinline__ void load4(const float* p, float x[4]) {
+  const f32x4* q = reinterpret_cast<const f32x4*>(p);
+  const f32x4 v = ONCE ? __builtin_nontemporal_load(q) : *q;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x[j] = v[j];
+}
+template <bool ONCE>
+__device__ __forceinline__ void load4(const bf16* p, float x[4]) {
+  const u32x2* q = reinterpret_cast<const u32x2*>(p);
+  const u32x2 v = ONCE ? __builtin_nontemporal_load(q) : *q;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    x[2 * j] = bf16_bits_to_f32(v[j]);
+    x[2 * j + 1] = __uint_as_float(v[j] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void store4(float* p, const float x[4]) {
+  *reinterpret_cast<f32x4*>(p) = f32x4{x[0], x[1], x[2], x[3]};
+}
+__device__ __forceinline__ void store4(bf16* p, const float x[4]) {
+  bf16x4 v;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = static_cast<bf16>(x[j]);
+  *reinterpret_cast<bf16x4*>(p) = v;
+}
+
+// A piece of a row of C columns; 0 behind its end.  (ONCE: past the caches.)
+template <typename T, bool SPLIT, bool ONCE = false>
+__device__ __forceinline__ void load8(const void* p, int c, int C, float x[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = 0.f;
+  if constexpr (SPLIT) {
+    if (c < C) load4<ONCE>(static_cast<const T*>(p) + c, x);
+    if (c + kHalf < C) load4<ONCE>(static_cast<const T*>(p) + c + kHalf, x + 4);
+  } else if (c < C) {
+    Vec8<T> v;
+    if constexpr (ONCE) v.load_once(p, c);
+    else v.load(p, c);
+    v.get(x);
+  }
+}
+template <typename T, bool SPLIT>
+__device__ __forceinline__ void store8(void* p, int c, int C, const float x[8]) {
+  if constexpr (SPLIT) {
+    if (c < C) store4(static_cast<T*>(p) + c, x);
+    if (c + kHalf < C) store4(static_cast<T*>(p) + c + kHalf, x + 4);
+  } else if (c < C) {
+    Vec8<T>::store(p, c, x);
+  }
 }
 
 // A weight plus its offset, or 1 where there is none.
-template <typename E>
-__device__ __forceinline__ void weight8(const void* w, int has, float offset, int at, float x[8]) {
+template <typename E, bool SPLIT>
+__device__ __forceinline__ void weight8(const void* w, int has, float offset, int c, int C,
+                                        float x[8]) {
   if (has) {
-    load8<E>(w, at, x);
+    load8<E, SPLIT>(w, c, C, x);
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] += offset;
   } else {
@@ -120,10 +179,10 @@ __device__ __forceinline__ void weight8(const void* w, int has, float offset, in
 }
 
 // branch_scale times the gate, `gate` its row or NULL.
-template <typename E>
-__device__ __forceinline__ void gate8(const BlockParams& p, const char* gate, int at, float g[8]) {
+template <typename E, bool SPLIT>
+__device__ __forceinline__ void gate8(const BlockParams& p, const char* gate, int c, float g[8]) {
   if (p.gate != nullptr) {
-    load8<E>(gate, at, g);
+    load8<E, SPLIT>(gate, c, p.C, g);
 #pragma unroll
     for (int j = 0; j < 8; ++j) g[j] *= p.branch_scale;
   } else {
@@ -136,6 +195,7 @@ __device__ __forceinline__ void gate8(const BlockParams& p, const char* gate, in
 template <typename E, typename R, int NT, int CH>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_fwd_kernel(const BlockParams p) {
   constexpr int kRows = NT < 256 ? 256 / NT : 1;
+  constexpr bool S = kSplit<E, R>;
   __shared__ float s[2 * NT / 64];
   RowSum<NT> sum{s, 0};
   const int tid = threadIdx.x % NT;
@@ -147,24 +207,24 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_fwd_kernel(con
   bool on[CH];
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
-    const int c = 8 * (tid + k * NT);
+    const int c = column<S, NT>(tid, k);
     on[k] = c < p.C;
 #pragma unroll
     for (int j = 0; j < 8; ++j) h[k][j] = y[k][j] = 0.f;
     if (on[k]) {
-      load8<R, true>(row_of<R>(p.x, t, p.x_s), c, h[k]);
-      if (p.y != nullptr) load8<E, true>(row_of<E>(p.y, t, p.y_s), c, y[k]);
+      load8<R, S, true>(row_of<R>(p.x, t, p.x_s), c, p.C, h[k]);
+      if (p.y != nullptr) load8<E, S, true>(row_of<E>(p.y, t, p.y_s), c, p.C, y[k]);
     }
   }
   if (p.y != nullptr) {
     const float r = p.post ? inverse_rms<NT, CH>(sum, y, inv_c, p.eps) : 1.f;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int c = 8 * (tid + k * NT);
+      const int c = column<S, NT>(tid, k);
       if (!on[k]) continue;
       float w[8], g[8];
-      weight8<E>(p.post_w, p.has_post_w, p.offset, c, w);
-      gate8<E>(p, gate, c, g);
+      weight8<E, S>(p.post_w, p.has_post_w, p.offset, c, p.C, w);
+      gate8<E, S>(p, gate, c, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         h[k][j] = __builtin_fmaf(g[j], y[k][j] * r * w[j], h[k][j] * p.res_scale);
@@ -178,24 +238,24 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_fwd_kernel(con
   if (p.h != nullptr) {
 #pragma unroll
     for (int k = 0; k < CH; ++k)
-      if (on[k]) Vec8<R>::store(row_of<R>(p.h, t, p.h_s), 8 * (tid + k * NT), h[k]);
+      if (on[k]) store8<R, S>(row_of<R>(p.h, t, p.h_s), column<S, NT>(tid, k), p.C, h[k]);
   }
   if (p.z == nullptr) return;
   const float r = inverse_rms<NT, CH>(sum, h, inv_c, p.eps);
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
-    const int c = 8 * (tid + k * NT);
+    const int c = column<S, NT>(tid, k);
     if (!on[k]) continue;
     float w[8];
-    weight8<E>(p.pre_w, p.has_pre_w, p.offset, c, w);
+    weight8<E, S>(p.pre_w, p.has_pre_w, p.offset, c, p.C, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) h[k][j] = h[k][j] * r * w[j];
-    Vec8<E>::store(row_of<E>(p.z, t, p.z_s), c, h[k]);
+    store8<E, S>(row_of<E>(p.z, t, p.z_s), c, p.C, h[k]);
   }
 }
 
 // A row behind a buffer descriptor: loads past its end, or of an array that is not there, give 0
-// without a branch.  (Past the caches: read once.)
+// without a branch.  (ONCE: past the caches.)
 template <typename T>
 struct BufferRow {
   __amdgpu_buffer_rsrc_t r;
@@ -204,14 +264,21 @@ struct BufferRow {
     r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), 0,
                                           on ? C * static_cast<int>(sizeof(T)) : 0, 0x00020000);
   }
+  template <bool SPLIT, bool ONCE>
   __device__ __forceinline__ void load(int c, Vec8<T>& v) const {
-    constexpr int kPast = 2;
+    constexpr int kPast = ONCE ? 2 : 0;
     const int b = c * static_cast<int>(sizeof(T));
-    if constexpr (sizeof(T) == 2) {
-      v.r = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, b, 0, kPast));
-    } else {
+    if constexpr (sizeof(T) == 4) {
+      constexpr int kNext = SPLIT ? 4 * kHalf : 16;
       v.a = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, b, 0, kPast));
-      v.b = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, b + 16, 0, kPast));
+      v.b = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, b + kNext, 0, kPast));
+    } else if constexpr (SPLIT) {
+      const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, b, 0, kPast));
+      const u32x2 hi =
+          __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, b + 2 * kHalf, 0, kPast));
+      v.r = u32x4{lo[0], lo[1], hi[0], hi[1]};
+    } else {
+      v.r = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, b, 0, kPast));
     }
   }
 };
@@ -308,8 +375,8 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
   __shared__ float fold[kRows > 1 ? kRows : 1][kRows > 1 ? NT * 8 : 1];
   // 16 waves to a unit leave each 128 registers: of the longest rows' two pieces dz, dh and the
   // weights are not held but read at each use, one piece after the other (y read again too: 225 us at
-  // 4096 x 16384 for 190), and u1 and pre_w's sums wait in shared memory.
-  constexpr bool kHold = NT < 1024 || CH == 1;
+  // 4096 x 16384 for 192), and u1 and pre_w's sums wait in shared memory.
+  constexpr bool kHold = NT < 1024 || CH == 1, S = kSplit<E, R> && kHold;
   constexpr int kHeld = kHold ? CH : 1;
   __shared__ f32x4 kept[kHold ? 1 : 2 * CH][kHold ? 1 : NT];
   __shared__ f32x4 kept_w2[kHold ? 1 : 2 * CH][kHold ? 1 : NT];
@@ -335,17 +402,17 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
   const bool tokens = p.gate != nullptr && p.gate_tokens;
   // post_w and pre_w with the offset, and the gate times branch_scale; 0 behind the row's end
   const auto weights = [&](int k, float w1[8], float w2[8], float g[8]) {
-    const int c = 8 * (tid + k * NT);
+    const int c = column<S, NT>(tid, k);
 #pragma unroll
     for (int j = 0; j < 8; ++j) w1[j] = w2[j] = g[j] = 0.f;
     if (c < p.C) {
-      weight8<E>(row_of<E>(p.post_w, 0, 0), p.has_post_w, p.offset, c, w1);
-      weight8<E>(row_of<E>(p.pre_w, 0, 0), p.has_pre_w, p.offset, c, w2);
+      weight8<E, S>(row_of<E>(p.post_w, 0, 0), p.has_post_w, p.offset, c, p.C, w1);
+      weight8<E, S>(row_of<E>(p.pre_w, 0, 0), p.has_pre_w, p.offset, c, p.C, w2);
       if (tokens) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) g[j] = p.branch_scale;
       } else {
-        gate8<E>(p, row_of<E>(p.gate, 0, 0), c, g);
+        gate8<E, S>(p, row_of<E>(p.gate, 0, 0), c, g);
       }
     }
   };
@@ -380,11 +447,11 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
     const BufferRow<E> at_dz(p.dz, t, p.dz_s, C, use_z), at_y(p.y, t, p.y_s, C, use_y);
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int c = 8 * (tid + k * NT);
-      at_h.load(c, raw.h[k]);
-      if constexpr (kHold) at_dz.load(c, raw.dz[k]);
-      at_y.load(c, y[k]);
-      if constexpr (kHold) at_dh.load(c, raw.dh[k]);
+      const int c = column<S, NT>(tid, k);
+      at_h.template load<S, kHold>(c, raw.h[k]);
+      if constexpr (kHold) at_dz.template load<S, kHold>(c, raw.dz[k]);
+      at_y.template load<S, kHold>(c, y[k]);
+      if constexpr (kHold) at_dh.template load<S, kHold>(c, raw.dh[k]);
     }
   };
   if constexpr (kAhead) fetch(static_cast<int64_t>(blockIdx.x) * kRows, raw.y);
@@ -397,12 +464,13 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
     const auto y_of = [&](int k, float x[8]) { raw.y[k].get(x); };
     const auto dh_of = [&](int k, float x[8]) {
       if constexpr (!kHold)
-        BufferRow<R>(p.dh, t, p.dh_s, C, p.dh != nullptr).load(8 * (tid + k * NT), raw.dh[0]);
+        BufferRow<R>(p.dh, t, p.dh_s, C, p.dh != nullptr)
+            .template load<S, kHold>(column<S, NT>(tid, k), raw.dh[0]);
       raw.dh[kHold ? k : 0].get(x);
     };
     const auto dz_of = [&](int k, float x[8]) {
       if constexpr (!kHold)
-        BufferRow<E>(p.dz, t, p.dz_s, C, use_z).load(8 * (tid + k * NT), raw.dz[0]);
+        BufferRow<E>(p.dz, t, p.dz_s, C, use_z).template load<S, kHold>(column<S, NT>(tid, k), raw.dz[0]);
       raw.dz[kHold ? k : 0].get(x);
     };
     const auto columns_of = [&](int k, float w2[8], float gw[8]) {
@@ -466,7 +534,7 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
     float u1[kHeld][8], dot[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int c = 8 * (tid + k * NT);
+      const int c = column<S, NT>(tid, k);
       float gh[8], h[8], z[8], w2[8], gw[8];
       dh_of(k, gh);
       h_of(k, h);
@@ -485,16 +553,14 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
         float x[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = gh[j] * p.res_scale;
-        Vec8<R>::store(row_of<R>(p.dx, t, p.dx_s), c, x);
+        store8<R, S>(row_of<R>(p.dx, t, p.dx_s), c, C, x);
       }
       float* u = u1[kHold ? k : 0];
       float y[8];
       y_of(k, y);
       if (tokens) {
         float g[8], d[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = 0.f;
-        if (c < C) load8<E>(gate, c, g);
+        load8<E, S>(gate, c, C, g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float yy = y[j] * r1, v = gh[j] * gw[j];
@@ -504,7 +570,7 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
           dot[0] = __builtin_fmaf(u[j], yy, dot[0]);
         }
         if (c < C && p.dgate != nullptr)
-          Vec8<E>::store(row_of<E>(p.dgate, t, p.dgate_s), c, d);
+          store8<E, S>(row_of<E>(p.dgate, t, p.dgate_s), c, C, d);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -526,7 +592,7 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
     }
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int c = 8 * (tid + k * NT);
+      const int c = column<S, NT>(tid, k);
       if (c >= C || p.dy == nullptr) continue;
       float* u = u1[kHold ? k : 0];
       if constexpr (!kHold) take(kept, k, u);
@@ -536,7 +602,7 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
 #pragma unroll
         for (int j = 0; j < 8; ++j) u[j] = __builtin_fmaf(a1, y[j] * r1, r1 * u[j]);
       }
-      Vec8<E>::store(row_of<E>(p.dy, t, p.dy_s), c, u);
+      store8<E, S>(row_of<E>(p.dy, t, p.dy_s), c, C, u);
     }
     if constexpr (kAhead) {
 #pragma unroll
@@ -547,7 +613,7 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
   // the parts of post_w's, the gate's and pre_w's gradient
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
-    const int c = 8 * (tid + k * NT);
+    const int c = column<S, NT>(tid, k);
     float w1[8], w2[8], g[8];
     weights(k, w1, w2, g);
     float* dw2 = sum_w2[kHold ? k : 0];
@@ -562,10 +628,11 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
                : q == 1 ? sum_t[k][j] * (p.branch_scale * w1[j]) : dw2[j];
       float* out = p.part + (static_cast<int64_t>(q) * gridDim.x + blockIdx.x) * p.C;
       if constexpr (kRows == 1) {
-        if (c < p.C) Vec8<float>::store(out, c, x);
+        store8<float, S>(out, c, p.C, x);
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) fold[row][8 * tid + j] = x[j];
+        for (int j = 0; j < 8; ++j)
+          fold[row][column<S, NT>(tid, 0) + j + (S && j >= 4 ? kHalf - 4 : 0)] = x[j];
         __syncthreads();
         for (int i = threadIdx.x; i < NT * 8; i += kBwdThreads<NT>) {
           const int at = 8 * k * NT + i;
