@@ -520,6 +520,39 @@ def test_policy_lengths_next_to_the_kernels(zs, torch, V, dtype):
     _policy_all(zs, torch, z, act, adv, (lp + 0.05).float(), (lp - 0.2).float(), w, kl=0.1)
 
 
+@pytest.mark.parametrize("V,dtype", [(2001, "bf16"), (50257, "bf16"), (90001, "bf16"), (131072, "f32"),
+                                     (200003, "bf16")])
+def test_policy_masked_stretches(zs, torch, V, dtype):
+    """Stretches of the vocabulary at the type's lowest value or -inf: the end, the middle, all but a
+    few tokens, whichever pass or piece of the row they fall into."""
+    dt, = _types(torch, dtype)
+    lowest = torch.finfo(dt).min
+    g = _gen(torch, V)
+    z = _rand(torch, g, (6, V), dt, 2.0)
+    act = torch.tensor([1, V // 3, V - 1, 7, V // 2, 0], dtype=torch.int32)
+    z[0, V // 2:] = lowest
+    z[1, V // 2:] = -math.inf
+    z[2, :V - 5] = lowest
+    z[3, 9:] = torch.where(torch.arange(V - 9) % 2 == 0, lowest, -math.inf).to(dt)
+    z[4, : V // 2 - 3] = lowest
+    z[4, V // 2 + 3:] = -math.inf
+    z[5, 1:] = lowest                           # one token alone
+    # (the same rows for the oracle: 64 bits need no lowest value, and its bounds take none)
+    same = torch.where(z == lowest, -math.inf, z.float()).to(dt)
+    lp = torch.log_softmax(same.double(), 1).gather(1, act.long()[:, None])[:, 0]
+    adv = torch.tensor([1.0, -0.5, 2.0, -1.0, 0.3, 1.0])
+    old, ref = (lp - 0.05).float(), (lp + 0.2).float()
+    want = B.policy(same, act, adv, old=old, ref=ref, kl_coef=0.1)
+    d = [t.cuda() for t in (z, act, adv, old, ref)]
+    loss, stats, dz = torch.empty(6, device="cuda"), torch.empty(6, 4, device="cuda"), torch.empty_like(d[0])
+    zs.zero_policy_fwd(*d[:3], loss, stats, dlogits=dz, old_logp=d[3], ref_logp=d[4], kl_coef=0.1)
+    R.check("loss", loss, *want["loss"])
+    R.check("stats", stats, *want["stats"])
+    R.check("dz", dz, *want["dz"])
+    zs.zero_policy_bwd(d[0], d[1], stats, dz)
+    R.check("dz of the backward", dz, *want["dz"])
+
+
 @pytest.mark.parametrize("tau,lo,hi", [(1.0, 0.2, 0.28), (0.5, 0.0, 0.0), (3.0, 1.0, 5.0)])
 @pytest.mark.parametrize("forms", ["old", "ref", "both", "neither"])
 def test_policy_forms(zs, torch, forms, tau, lo, hi):

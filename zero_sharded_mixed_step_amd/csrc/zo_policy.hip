@@ -139,6 +139,9 @@ __device__ __forceinline__ PolicyRow policy_row(const PolicyParams& p, int64_t n
   return o;
 }
 
+// Where logits over tau log 2 are so far from 0, a row is formed from differences.
+constexpr float kFar = 0x1p20f;
+
 // Forward: loss and statistics, and the gradient if asked for.  The row stays in registers, CH
 // chunks to a thread.  LONG: what is beyond them stays in shared memory, p.kept chunks, and what is
 // beyond those is read once for its maximum and sum together and again for the gradient.
@@ -209,10 +212,14 @@ __global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void policy_fwd_kernel(const P
       for (int k = 0; k < kAtOnce; ++k) {
         const float top = chunk_max(x[k], -kInf);
         if (top > rest_m) {
+          // (not of a chunk that is masked by the lowest value alone, whose product may be past
+          // binary32; the row of one that is so far above 0 is read again, see far)
           const float m2 = top * k2;
-          if (rest_sum > 0.f) rest_sum *= exp2_hw(rest_m2 - m2);
+          if (fabsf(m2) <= 2.f * kFar) {
+            if (rest_sum > 0.f) rest_sum *= exp2_hw(rest_m2 - m2);
+            rest_m2 = m2;
+          }
           rest_m = top;
-          rest_m2 = m2;
         }
         rest_sum += chunk_sum(x[k], c + k * NT,
                               [&](float z) { return exp2_hw(__builtin_fmaf(z, k2, -rest_m2)); });
@@ -251,7 +258,7 @@ __global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void policy_fwd_kernel(const P
   keep_packed(held);
   // Where the rounding of m2 would outweigh the powers (or m k2 is past binary32), they are formed
   // from the difference z - m: such a row is read again.
-  const bool far = !(fabsf(m) * k2 <= 0x1p20f);
+  const bool far = !(fabsf(m) * k2 <= kFar);
   const float m2 = far ? 0.f : m * k2;
   const auto power = [&](float z) { return exp2_hw(__builtin_fmaf(z, k2, -m2)); };
   const auto power_far = [&](float z) { return exp2_hw((z - m) * k2); };
@@ -433,12 +440,11 @@ hipError_t run_fwd_long(const PolicyParams& q, int64_t chunks, hipStream_t s) {
   constexpr int NT = 1024, CH = 8, kKept = 4800;
   PolicyParams p = q;
   p.kept = static_cast<int>(std::min<int64_t>(chunks - NT * CH, kKept));
-  const int lds = p.kept * 16;
   const auto fn = policy_fwd_kernel<E, NT, CH, true>;
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, kKept * 16);
   if (e != hipSuccess) return e;
-  fn<<<static_cast<unsigned>(p.N), NT, lds, s>>>(p);
+  fn<<<static_cast<unsigned>(p.N), NT, p.kept * 16, s>>>(p);
   return hipGetLastError();
 }
 
