@@ -348,9 +348,10 @@ size_t zero_block_norm_workspace_bytes(int64_t T, int C);
  * zero_policy_fwd writes loss and stats, and dlogits too if given (one read of
  * the logits for all three); zero_policy_bwd writes dlogits from stats (lse, lp
  * and g, whatever loss they came from).  dlogits may be the logits themselves
- * (same stride).  dtype is that of logits and dlogits.  1e-30 <= tau <= 1e30 (and z_j / tau
- * within binary32, or the row's results are NaN), 0 <= clip_low <= 1, clip_high >= 0, N <= 2^21, V <= ZERO_POLICY_MAX_V; logits may start
- * at any element. */
+ * (same stride).  dtype is that of logits and dlogits.  1e-30 <= tau <= 1e30 (and
+ * z_j / tau within binary32, or the row's results are NaN), 0 <= clip_low <= 1,
+ * clip_high >= 0, N <= 2^21, V <= ZERO_POLICY_MAX_V; logits may start at any
+ * element. */
 typedef struct zero_policy_args {
   size_t struct_bytes;          /* sizeof(zero_policy_args) */
   int64_t N, V;
@@ -385,9 +386,9 @@ int zero_policy_bwd(const zero_policy_args *args, void *stream);
  * zero_grads_clip: outs[i] = (grads[i] * inv_scale) * coef, rounded to out_dtypes[i],
  * with the skip and the coefficient that zero_step_gate derives from the n_accs
  * accumulators, max_norm and check_overflow; a skipped call writes no tensor.  outs[i]
- * may be grads[i] (same dtype), and overlaps no other tensor.  norm_out, coef_out and skipped_out (each may be
- * NULL): the global norm, infinite where a value is not finite, the coefficient (0 where
- * skipped) and 1 where skipped, else 0. */
+ * may be grads[i] (same dtype), and overlaps no other tensor.  norm_out, coef_out and
+ * skipped_out (each may be NULL): the global norm, infinite where a value is not finite,
+ * the coefficient (0 where skipped) and 1 where skipped, else 0. */
 typedef struct zero_grads_args {
   size_t struct_bytes;          /* sizeof(zero_grads_args) */
   int64_t count;

@@ -1006,6 +1006,47 @@ def test_block_ops_repeat_bitwise_on_streams_and_in_graphs(zs, torch, N):
         assert same()
 
 
+def test_large_forms_in_a_graph(zs, torch):
+    """Long rows of logits, wide rows backward and tokens whose lists are joined in two passes, which
+    take other kernels than the pass above: replayed with eager calls between."""
+    g = _gen(torch, 31)
+    V, N, width, tokens = 90001, 3, 9000, 20000
+    z = _rand(torch, g, (N, V), torch.bfloat16, 2.0).cuda()
+    act = torch.tensor([5, V - 1, 70000], dtype=torch.int32).cuda()
+    adv = torch.tensor([1.0, -0.5, 2.0]).cuda()
+    loss, stats, dz = torch.empty(N, device="cuda"), torch.empty(N, 4, device="cuda"), torch.empty_like(z)
+    rows = [_rand(torch, g, (600, width), torch.bfloat16).cuda() for _ in range(4)]
+    w = _rand(torch, g, (width,), torch.bfloat16).cuda()
+    dx, dy, dw = torch.empty_like(rows[0]), torch.empty_like(rows[0]), torch.empty_like(w)
+    ws = torch.empty(zs.zero_block_norm_workspace_bytes(600, width), dtype=torch.uint8, device="cuda")
+    ids = torch.randint(0, 500, (tokens,), generator=g, dtype=torch.int32).cuda()
+    dout = _rand(torch, g, (tokens, 64), torch.bfloat16).cuda()
+    dtable = torch.empty(500, 64, device="cuda")
+    ews = torch.empty(zs.zero_embed_workspace_bytes(tokens, 64), dtype=torch.uint8, device="cuda")
+
+    def run():
+        zs.zero_policy_fwd(z, act, adv, loss, stats, dlogits=dz)
+        zs.zero_block_norm_bwd(*rows, dx, dy, dpost_weight=dw, post_norm=True, post_weight=w, workspace=ws)
+        zs.zero_embed_bwd(ids, dout, dtable, workspace=ews)
+
+    outs = (loss, stats, dz, dx, dy, dw, dtable)
+    run()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in outs]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(4):
+        for t in (*outs, ws, ews):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(_same(a, b) for a, b in zip(outs, want))
+        run()
+        torch.cuda.synchronize()
+        assert all(_same(a, b) for a, b in zip(outs, want))
+
+
 def test_block_ops_with_other_memory_between_streams(zs, torch):
     """A call on a stream of its own, given as an argument."""
     s = _state(zs, torch, 100)

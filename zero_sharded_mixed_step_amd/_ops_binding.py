@@ -107,14 +107,13 @@ def _call(fn, args, stream, dev):
         s = torch._C._cuda_getCurrentRawStream(dev)
     else:
         s = _stream(stream)
-    status = getattr(ops_lib(), fn)(args, s)
+    status = getattr(_lib or ops_lib(), fn)(args, s)
     if status != 0:
         raise ZeroOpsError(status, fn)
 
 
-def _tensor(t, name, shape, dtype, dev):
-    """Address and strides of a tensor on device `dev` with the given shape
-    and dtype, whose last dimension is contiguous."""
+def _refuse(t, name, shape, dtype, dev):
+    """Says what is wrong with a tensor that is not on device `dev`, of `dtype` and `shape`."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     if t.get_device() != dev:
@@ -122,22 +121,34 @@ def _tensor(t, name, shape, dtype, dev):
                          f"device, cuda:{dev}")
     if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, the call needs {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, the call needs {tuple(shape)}")
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, the call needs {tuple(shape)}")
+
+
+# (These three look at each tensor with as few calls as say all: some 0.5 us a tensor, of
+# which a small call has time for few.)
+
+def _tensor(t, name, shape, dtype, dev, Tensor=torch.Tensor):
+    """Address and strides of a tensor on device `dev` with the given shape
+    and dtype, whose last dimension is contiguous."""
+    if not isinstance(t, Tensor) or t.get_device() != dev or dev < 0 or \
+            t.dtype is not dtype or t.shape != shape:
+        _refuse(t, name, shape, dtype, dev)
     st = t.stride()
     if st and st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     return t.data_ptr(), st
 
 
-def _flat(t, name, shape, dtype, dev):
+def _flat(t, name, shape, dtype, dev, Tensor=torch.Tensor):
     """Address of a contiguous tensor; 0 for None."""
     if t is None:
         return 0
-    p, _ = _tensor(t, name, shape, dtype, dev)
+    if not isinstance(t, Tensor) or t.get_device() != dev or dev < 0 or \
+            t.dtype is not dtype or t.shape != shape:
+        _refuse(t, name, shape, dtype, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return p
+    return t.data_ptr()
 
 
 def _used(shape, strides):
@@ -428,12 +439,17 @@ def zero_distill_bwd(logits, teacher_idx, teacher_val, stats, dlogits, *, temper
 
 # -------------------------------------------------------------- embedding ---
 
-def _matrix(t, name, shape, dtype, dev):
+def _matrix(t, name, shape, dtype, dev, Tensor=torch.Tensor):
     """Address and row stride (0 where there is one row) of a matrix; 0, 0 for None."""
     if t is None:
         return 0, 0
-    p, st = _tensor(t, name, shape, dtype, dev)
-    return p, st[0] if shape[0] > 1 else 0
+    if not isinstance(t, Tensor) or t.get_device() != dev or dev < 0 or \
+            t.dtype is not dtype or t.shape != shape:
+        _refuse(t, name, shape, dtype, dev)
+    row, last = t.stride()
+    if last != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr(), row if shape[0] > 1 else 0
 
 
 def _given(t, name, shape, dtype, dev):
@@ -504,10 +520,15 @@ def _block_types(res, others, what):
     """T, C and the codes of a call's tensors: `res` one of the residual stream, `others`
     those of the block's type."""
     T, width = res.shape
-    dt = next((x.dtype for x in others if x is not None), res.dtype)
-    if dt not in _CODES or res.dtype not in _CODES:
-        raise TypeError(f"{what}: float32 or bfloat16, not {dt} and {res.dtype}")
-    return T, width, dt, _CODES[dt], _CODES[res.dtype]
+    dt = rt = res.dtype
+    for x in others:
+        if x is not None:
+            dt = x.dtype
+            break
+    code, rcode = _CODES.get(dt), _CODES.get(rt)
+    if code is None or rcode is None:
+        raise TypeError(f"{what}: float32 or bfloat16, not {dt} and {rt}")
+    return T, width, dt, code, rcode
 
 
 def _gate(gate, T, width, dt, dev, name="gate"):
@@ -554,8 +575,8 @@ def zero_block_norm_bwd(y, h, dh, dz, dx, dy, *, dpost_weight=None, dgate=None, 
     and dz that come in (None: 0; without dz, h may be None): dx, dy and, where given,
     dpost_weight, dgate and dpre_weight, each of which may be None.  dx may be dh.  workspace:
     zero_block_norm_workspace_bytes(T, C) bytes where a gradient is summed over the tokens."""
-    res = next((t for t in (dh, dx, h) if isinstance(t, torch.Tensor)), None)
-    if res is None or res.dim() != 2:
+    res = dh if dh is not None else dx if dx is not None else h
+    if not isinstance(res, torch.Tensor) or res.dim() != 2:
         raise ValueError("dh, dx and h are (T, C) tensors, one of them given")
     T, width, dt, code, rcode = _block_types(res, (y, dz, dy, post_weight, gate, pre_weight),
                                              "the gradients")
