@@ -12,7 +12,11 @@
 // total keep their digits however sure the student is of the token.  What follows from lp
 // (ratio, clipping, KL term) is some binary64 operations a row.
 //
-// Measured: 8192 x 50257 bf16 with the gradient 318 us, 5.2 TB/s of logits read and gradient
+// The forward's gradient is written past the caches: alone the kernel takes 4 to 20 % less (8192 x 50257
+// bf16: 310 us, through them 322; 2048 x 50257: 72, 93), and with the gradient's reader behind it as long
+// as before (587 and 587, 162 and 161).
+//
+// Measured: 8192 x 50257 bf16 with the gradient 310 us, 5.3 TB/s of logits read and gradient
 // written (350 with the library's logarithms and exponentials in binary64, which one thread
 // works on while the row waits); the backward alone, 1024 x 131072 fp32, 162 us, 6.6 TB/s (172 with
 // loads through the caches).
@@ -331,7 +335,7 @@ __global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void policy_fwd_kernel(const P
   const float c0 = row[0], own_grad = tops[0];
   if (c0 == 0.f) {
     const float zero[kN] = {};
-    for (int c = tid; c < chunks; c += NT) out.store(c, in.shift, zero);
+    for (int c = tid; c < chunks; c += NT) out.template store<true>(c, in.shift, zero);
     return;
   }
   const float factor = -c0 * row[1];
@@ -343,7 +347,7 @@ __global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void policy_fwd_kernel(const P
 #pragma unroll
       for (int e = 0; e < kN; ++e) y[e] = e == own_e ? own_grad : y[e];
     }
-    out.store(c, in.shift, y);
+    out.template store<true>(c, in.shift, y);
   };
   if (far) {
 #pragma unroll 1
@@ -432,9 +436,10 @@ hipError_t run_fwd(const PolicyParams& p, hipStream_t s) {
 }
 
 // Rows beyond 8192 chunks.  Two workgroups fill a unit's registers, and what they keep in
-// shared memory its 160 KiB (4096 x 80000 bf16: 256 us, one with 16 chunks a thread 309; 2048 x 128000:
-// 222, 247; 9000 kept, so that one workgroup runs on a unit: 256, 256).  2048 x 200000: 382 us; 1024 x
-// 131072 fp32 270 us, where everything read in three passes took 515 and 360.
+// shared memory its 160 KiB (written through the caches, 4096 x 80000 bf16: 256 us, one with 16 chunks a
+// thread 309; 2048 x 128000: 222, 247; 9000 kept, so that one workgroup runs on a unit: 256, 256; 2048 x
+// 200000: 382 us and 1024 x 131072 fp32 270 us, everything read in three passes 515 and 360.  Past them:
+// 233, 201, 328 and 222).
 template <typename E>
 hipError_t run_fwd_long(const PolicyParams& q, int64_t chunks, hipStream_t s) {
   constexpr int NT = 1024, CH = 8, kKept = 4800;
@@ -449,8 +454,9 @@ hipError_t run_fwd_long(const PolicyParams& q, int64_t chunks, hipStream_t s) {
 }
 
 // By the length of the row: 8 chunks a thread, in the fewest threads that hold it, so that all
-// rows under way fill the card's registers (bf16 with the gradient: 16384 x 4001 65 us, 256
-// threads with 2 chunks each 81; 4096 x 8200 33, 1024 with 2 45; 4096 x 20000 67, 1024 with 4 76).
+// rows under way fill the card's registers (bf16 with the gradient, still written through the caches:
+// 16384 x 4001 65 us, 256 threads with 2 chunks each 81; 4096 x 8200 33, 1024 with 2 45; 4096 x 20000
+// 67, 1024 with 4 76).
 // Rows of fewer than 4096 bf16 or 2048 fp32 values, 128 threads with 4.
 template <typename E>
 hipError_t pick_fwd(const PolicyParams& p, hipStream_t s) {

@@ -149,6 +149,7 @@ struct Row {
     return x;
   }
   // y as this row's elements that chunk c of a row shifted by `from` holds
+  template <bool ONCE = false>
   __device__ __forceinline__ void store(int c, int from, const float y[kN]) const {
     const int64_t e0 = static_cast<int64_t>(c) * kN - from;
     if (from == shift && e0 >= 0 && e0 + kN <= V) {
@@ -165,7 +166,9 @@ struct Row {
 #pragma unroll
         for (int e = 0; e < kN; ++e) x.r[e] = y[e];
       }
-      *reinterpret_cast<decltype(x.r)*>(p + e0) = x.r;
+      auto* at = reinterpret_cast<decltype(x.r)*>(p + e0);
+      if constexpr (ONCE) __builtin_nontemporal_store(x.r, at);
+      else *at = x.r;
     } else {
 #pragma unroll
       for (int e = 0; e < kN; ++e)
