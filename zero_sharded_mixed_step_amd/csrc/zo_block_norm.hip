@@ -101,67 +101,11 @@ __device__ __forceinline__ char* row_of(void* base, int64_t t, int64_t stride) {
 // A piece's columns: 8 from c on, or, SPLIT, 4 from c on and 4 that are kHalf further, so that
 // a wave's accesses of 16 bytes leave no gaps where values have 4 bytes (fp32, 8192 x 4096: forward 98
 // us, 8 in a row 111; backward 152, 168).
-constexpr int kHalf = 256;
 template <typename E, typename R>
 constexpr bool kSplit = sizeof(E) == 4 || sizeof(R) == 4;
 template <bool SPLIT, int NT>
 __device__ __forceinline__ int column(int tid, int k) {
   return SPLIT ? 8 * ((tid & ~63) + k * NT) + 4 * (tid & 63) : 8 * (tid + k * NT);
-}
-
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-// Four columns.
-template <bool ONCE>
-__device__ __forceinline__ void load4(const float* p, float x[4]) {
-  const f32x4* q = reinterpret_cast<const f32x4*>(p);
-  const f32x4 v = ONCE ? __builtin_nontemporal_load(q) : *q;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) x[j] = v[j];
-}
-template <bool ONCE>
-__device__ __forceinline__ void load4(const bf16* p, float x[4]) {
-  const u32x2* q = reinterpret_cast<const u32x2*>(p);
-  const u32x2 v = ONCE ? __builtin_nontemporal_load(q) : *q;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    x[2 * j] = bf16_bits_to_f32(v[j]);
-    x[2 * j + 1] = __uint_as_float(v[j] & 0xFFFF0000u);
-  }
-}
-__device__ __forceinline__ void store4(float* p, const float x[4]) {
-  *reinterpret_cast<f32x4*>(p) = f32x4{x[0], x[1], x[2], x[3]};
-}
-__device__ __forceinline__ void store4(bf16* p, const float x[4]) {
-  bf16x4 v;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = static_cast<bf16>(x[j]);
-  *reinterpret_cast<bf16x4*>(p) = v;
-}
-
-// A piece of a row of C columns; 0 behind its end.  (ONCE: past the caches.)
-template <typename T, bool SPLIT, bool ONCE = false>
-__device__ __forceinline__ void load8(const void* p, int c, int C, float x[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) x[j] = 0.f;
-  if constexpr (SPLIT) {
-    if (c < C) load4<ONCE>(static_cast<const T*>(p) + c, x);
-    if (c + kHalf < C) load4<ONCE>(static_cast<const T*>(p) + c + kHalf, x + 4);
-  } else if (c < C) {
-    Vec8<T> v;
-    if constexpr (ONCE) v.load_once(p, c);
-    else v.load(p, c);
-    v.get(x);
-  }
-}
-template <typename T, bool SPLIT>
-__device__ __forceinline__ void store8(void* p, int c, int C, const float x[8]) {
-  if constexpr (SPLIT) {
-    if (c < C) store4(static_cast<T*>(p) + c, x);
-    if (c + kHalf < C) store4(static_cast<T*>(p) + c + kHalf, x + 4);
-  } else if (c < C) {
-    Vec8<T>::store(p, c, x);
-  }
 }
 
 // A weight plus its offset, or 1 where there is none.

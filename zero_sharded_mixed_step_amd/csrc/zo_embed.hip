@@ -62,24 +62,35 @@ struct EmbedParams {
   int fill_rows;                              // table rows of a wave that writes what no id names; 0: none does
 };
 
+// A wave's columns: 8 of a slice to a lane, 4 and 4 of its halves where one of their
+// two types is fp32.
+template <typename E, typename G>
+constexpr bool kSplit = sizeof(E) == 4 || sizeof(G) == 4;
+template <bool S>
+__device__ __forceinline__ int column(int64_t slice, int lane) {
+  return static_cast<int>(slice) * kSlice + (S ? 4 : 8) * lane;
+}
+
 // ---------------------------------------------------------------- forward ---
 
 template <typename E>
 __global__ __launch_bounds__(kEmbedThreads) void embed_fwd_kernel(const EmbedParams p) {
   constexpr int kU = 4;
+  constexpr bool S = kSplit<E, E>;
   const int lane = threadIdx.x & 63;
   const int64_t unit =
       static_cast<int64_t>(blockIdx.x) * kEmbedWaves + uniform(threadIdx.x >> 6);
   const int64_t n = unit / p.slices;
   if (n >= p.N) return;
-  const int c0 = static_cast<int>(unit % p.slices) * kSlice * kU + 8 * lane;
+  const int c0 = column<S>(unit % p.slices * kU, lane);
   const int32_t id = p.ids[n];
   const bool on = id >= 0 && id < p.V;
   Vec8<E> raw[kU];
 #pragma unroll
   for (int u = 0; u < kU; ++u) {
     raw[u] = Vec8<E>{};
-    if (on && c0 + u * kSlice < p.C) raw[u].load(p.table, id * p.table_s + c0 + u * kSlice);
+    if (on)
+      load_raw8<S, false>(static_cast<const E*>(p.table) + id * p.table_s, c0 + u * kSlice, p.C, raw[u]);
   }
 #pragma unroll
   for (int u = 0; u < kU; ++u) {
@@ -91,7 +102,7 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_fwd_kernel(const EmbedPar
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = 0.f;
     }
-    if (c0 + u * kSlice < p.C) Vec8<E>::store(p.out, n * p.out_s + c0 + u * kSlice, x);
+    store8<E, S>(static_cast<E*>(p.out) + n * p.out_s, c0 + u * kSlice, p.C, x);
   }
 }
 
@@ -183,15 +194,9 @@ __global__ __launch_bounds__(64 * kRankWaves) void embed_merge_kernel(
 
 // --------------------------------------------------------------- backward ---
 
-template <typename B>
-__device__ __forceinline__ void base_row(const EmbedParams& p, int64_t v, int c, float x[8]) {
-  Vec8<B> r;
-  r.load(p.base, v * p.base_s + c);
-  r.get(x);
-}
-
-// dtable[v] = base[v] + scale * sum, 8 columns.
-template <typename G, typename B>
+// dtable[v] = base[v] + scale * sum, a piece of 8 columns, past the caches.  (16384 x 4096 into bf16:
+// 107 us, through them 125.)
+template <typename G, typename B, bool S>
 __device__ __forceinline__ void store_row(const EmbedParams& p, int64_t v, int c,
                                           const float sum[8]) {
   float y[8];
@@ -199,24 +204,26 @@ __device__ __forceinline__ void store_row(const EmbedParams& p, int64_t v, int c
   for (int j = 0; j < 8; ++j) y[j] = sum[j] * p.scale;
   if (p.base != nullptr) {
     float b[8];
-    base_row<B>(p, v, c, b);
+    load8<B, S>(static_cast<const B*>(p.base) + v * p.base_s, c, p.C, b);
 #pragma unroll
     for (int j = 0; j < 8; ++j) y[j] = __builtin_fmaf(sum[j], p.scale, b[j]);
   }
-  Vec8<G>::store(p.dtable, v * p.dtable_s + c, y);
+  store8<G, S, true>(static_cast<G*>(p.dtable) + v * p.dtable_s, c, p.C, y);
 }
 
+template <bool S>
 __device__ __forceinline__ void store_part(const EmbedParams& p, int64_t chunk, int which, int c,
                                            const float sum[8]) {
-  Vec8<float>::store(p.part, (chunk * 2 + which) * p.C + c, sum);
+  store8<float, S>(p.part + (chunk * 2 + which) * p.C, c, p.C, sum);
 }
 
 // A wave's chunk of sorted places, for 512 columns.
 template <typename E, typename G, typename B>
 __device__ __forceinline__ void sum_chunk(const EmbedParams& p, int64_t unit, int lane) {
   constexpr int kAtOnce = 8;                  // rows under way
+  constexpr bool S = kSplit<E, G>;
   const int64_t chunk = unit / p.slices, first = chunk * p.P;
-  const int c = static_cast<int>(unit % p.slices) * kSlice + 8 * lane;
+  const int c = column<S>(unit % p.slices, lane);
   const bool on = c < p.C;
   const int32_t none = static_cast<int32_t>(p.V);
   const bool in = lane < p.P && first + lane < p.N;
@@ -234,9 +241,9 @@ __device__ __forceinline__ void sum_chunk(const EmbedParams& p, int64_t unit, in
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
       raw[u] = Vec8<E>{};
-      if (i0 + u < count && on) {
+      if (i0 + u < count) {
         const int64_t n = __builtin_amdgcn_readlane(place, i0 + u);
-        raw[u].load(p.dout, n * p.dout_s + c);
+        load_raw8<S, false>(static_cast<const E*>(p.dout) + n * p.dout_s, c, p.C, raw[u]);
       }
     }
 #pragma unroll
@@ -247,8 +254,8 @@ __device__ __forceinline__ void sum_chunk(const EmbedParams& p, int64_t unit, in
       raw[u].get(x);
       if (k != run) {
         if (on) {
-          if (shared) store_part(p, chunk, 0, c, sum);
-          else store_row<G, B>(p, run, c, sum);
+          if (shared) store_part<S>(p, chunk, 0, c, sum);
+          else store_row<G, B, S>(p, run, c, sum);
         }
         run = k;
         shared = false;
@@ -261,9 +268,9 @@ __device__ __forceinline__ void sum_chunk(const EmbedParams& p, int64_t unit, in
     }
   }
   if (!on) return;
-  if (shared) store_part(p, chunk, 0, c, sum);
-  else if (run == after) store_part(p, chunk, 1, c, sum);
-  else store_row<G, B>(p, run, c, sum);
+  if (shared) store_part<S>(p, chunk, 0, c, sum);
+  else if (run == after) store_part<S>(p, chunk, 1, c, sum);
+  else store_row<G, B, S>(p, run, c, sum);
 }
 
 // N columns as they are in memory, past the caches: one access of 16 bytes or fewer, so that a
@@ -357,6 +364,7 @@ constexpr int kDirectTokens = 256;
 template <typename E, typename G, typename B>
 __global__ __launch_bounds__(kEmbedThreads) void embed_direct_kernel(const EmbedParams p) {
   constexpr int kK = kDirectTokens / 64, kAtOnce = 4;
+  constexpr bool S = kSplit<E, G>;
   const int lane = threadIdx.x & 63;
   const int64_t unit =
       static_cast<int64_t>(blockIdx.x) * kEmbedWaves + uniform(threadIdx.x >> 6);
@@ -379,7 +387,7 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_direct_kernel(const Embed
     return;
   }
   const int n = static_cast<int>(unit / p.slices);
-  const int c = static_cast<int>(unit % p.slices) * kSlice + 8 * lane;
+  const int c = column<S>(unit % p.slices, lane);
   const bool on = c < p.C;
   int32_t run = 0;
 #pragma unroll
@@ -408,7 +416,7 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_direct_kernel(const Embed
         const int64_t at = 64 * k + __builtin_ctzll(places[k]);
         places[k] &= places[k] - 1;
         ++count;
-        raw[u].load(p.dout, at * p.dout_s + (on ? c : 0));
+        load_raw8<S, false>(static_cast<const E*>(p.dout) + at * p.dout_s, c, p.C, raw[u]);
       }
 #pragma unroll
       for (int u = 0; u < kAtOnce; ++u) {
@@ -420,7 +428,7 @@ __global__ __launch_bounds__(kEmbedThreads) void embed_direct_kernel(const Embed
       }
     }
   }
-  if (on) store_row<G, B>(p, run, c, sum);
+  if (on) store_row<G, B, S>(p, run, c, sum);
 }
 
 // The runs that go over a chunk's end, by the chunk that they begin in: its last part
@@ -444,7 +452,8 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(const Embed
   };
   if (count(1))
     for (int64_t step = 4096; step > 0; step >>= 6) count(step);
-  const int c = blockIdx.y * kSlice + 8 * lane;
+  constexpr bool S = true;                    // (the parts are fp32)
+  const int c = column<S>(blockIdx.y, lane);
   const bool on = c < p.C;
   float sum[8] = {};
   constexpr int kAtOnce = 8;                  // parts under way
@@ -453,7 +462,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(const Embed
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
       const int64_t q = min(q0 + u * kJoinWaves, more);
-      raw[u].load(p.part, ((chunk + q) * 2 + (q == 0 ? 1 : 0)) * p.C + (on ? c : 0));
+      load_raw8<S, false>(p.part + ((chunk + q) * 2 + (q == 0 ? 1 : 0)) * p.C, c, p.C, raw[u]);
     }
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
@@ -471,7 +480,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(const Embed
   for (int w = 1; w < kJoinWaves && w <= more; ++w)
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum[j] += fold[w][8 * lane + j];
-  store_row<G, B>(p, run, c, sum);
+  store_row<G, B, S>(p, run, c, sum);
 }
 
 namespace {

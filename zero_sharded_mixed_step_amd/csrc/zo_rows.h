@@ -73,6 +73,75 @@ struct Vec8<float> {
   }
 };
 
+// Eight columns of a row of C from c on, or, SPLIT, four and four that are kHalf further, so that a
+// wave's accesses of 16 bytes leave no gaps where values have 4 bytes.  0 behind the row's end.
+// (ONCE: past the caches.)
+constexpr int kHalf = 256;
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+template <bool ONCE, typename V>
+__device__ __forceinline__ V load_as(const void* p) {
+  if constexpr (ONCE) return __builtin_nontemporal_load(static_cast<const V*>(p));
+  else return *static_cast<const V*>(p);
+}
+template <bool SPLIT, bool ONCE>
+__device__ __forceinline__ void load_raw8(const bf16* p, int c, int C, Vec8<bf16>& v) {
+  v.r = u32x4{0, 0, 0, 0};
+  if constexpr (SPLIT) {
+    if (c < C) {
+      const u32x2 x = load_as<ONCE, u32x2>(p + c);
+      v.r[0] = x[0];
+      v.r[1] = x[1];
+    }
+    if (c + kHalf < C) {
+      const u32x2 x = load_as<ONCE, u32x2>(p + c + kHalf);
+      v.r[2] = x[0];
+      v.r[3] = x[1];
+    }
+  } else if (c < C) {
+    v.r = load_as<ONCE, u32x4>(p + c);
+  }
+}
+template <bool SPLIT, bool ONCE>
+__device__ __forceinline__ void load_raw8(const float* p, int c, int C, Vec8<float>& v) {
+  v.a = v.b = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (c < C) v.a = load_as<ONCE, f32x4>(p + c);
+  if ((SPLIT ? c + kHalf : c) < C) v.b = load_as<ONCE, f32x4>(p + c + (SPLIT ? kHalf : 4));
+}
+template <typename T, bool SPLIT, bool ONCE = false>
+__device__ __forceinline__ void load8(const void* p, int c, int C, float x[8]) {
+  Vec8<T> v;
+  load_raw8<SPLIT, ONCE>(static_cast<const T*>(p), c, C, v);
+  v.get(x);
+}
+
+template <bool ONCE, typename V>
+__device__ __forceinline__ void store_as(void* p, V v) {
+  if constexpr (ONCE) __builtin_nontemporal_store(v, static_cast<V*>(p));
+  else *static_cast<V*>(p) = v;
+}
+template <bool ONCE>
+__device__ __forceinline__ void store4(float* p, const float x[4]) {
+  store_as<ONCE>(p, f32x4{x[0], x[1], x[2], x[3]});
+}
+template <bool ONCE>
+__device__ __forceinline__ void store4(bf16* p, const float x[4]) {
+  bf16x4 v;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = static_cast<bf16>(x[j]);
+  store_as<ONCE>(p, v);
+}
+template <typename T, bool SPLIT, bool ONCE = false>
+__device__ __forceinline__ void store8(void* p, int c, int C, const float x[8]) {
+  T* const at = static_cast<T*>(p) + c;
+  if constexpr (SPLIT) {
+    if (c < C) store4<ONCE>(at, x);
+    if (c + kHalf < C) store4<ONCE>(at + kHalf, x + 4);
+  } else if (c < C) {
+    if constexpr (ONCE) Vec8<T>::store_once(at, 0, x);
+    else Vec8<T>::store(at, 0, x);
+  }
+}
+
 // Whether a row's mean square plus eps is near the ends of binary32 (the reciprocal root takes
 // no subnormal numbers): of values below 1e-15 with an eps below 1e-30, or above 1e15.
 __device__ __forceinline__ bool far_mean(float v) { return !(v >= 1e-30f && v <= 1e30f); }
