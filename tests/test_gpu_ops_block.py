@@ -368,6 +368,27 @@ def test_block_norm_backward_walks(zs, torch, C, types, gate):
     assert _same(d["dh"], got["dx"].contiguous()) and _same(dw2, got["dw2"])
 
 
+@pytest.mark.parametrize("C,types", [(1024, ("bf16", "bf16")), (2056, ("f32", "f32")), (4096, ("bf16", "f32")),
+                                     (8192, ("bf16", "bf16")), (16384, ("bf16", "f32"))], ids=str)
+def test_block_norm_outputs_past_the_caches(zs, torch, C, types):
+    """Outputs of more than 192 MiB: the rows of the same call on 256 of them, to the bit."""
+    dt, rt = _types(torch, *types)
+    T = -(-(200 << 20) // (C * ((torch.finfo(dt).bits + torch.finfo(rt).bits) // 8)))
+    s = {n: None if t is None else t.cuda()
+         for n, t in _block_inputs(torch, 256, C, dt, rt, C, True, "channel").items()}
+    some = torch.arange(T, device="cuda") % 251
+    big = {n: s[n][some].contiguous() for n in ("x", "y", "dh", "dz")}
+    kw = dict(post_norm=True, post_weight=s["w1"], gate=s["gate"], pre_weight=s["w2"], res_scale=0.9)
+    out = []
+    for d in (s, big):
+        h, z, dx, dy = (torch.full_like(d[n], math.nan) for n in ("x", "y", "x", "y"))
+        zs.zero_block_norm_fwd(d["x"], d["y"], h, z, **kw)
+        zs.zero_block_norm_bwd(d["y"], h, d["dh"], d["dz"], dx, dy, **kw)
+        out.append((h, z, dx, dy))
+    for a, b in zip(*out):
+        assert _same(a[some], b)
+
+
 @pytest.mark.parametrize("C", [64, 1000, 4096, 16384])
 @pytest.mark.parametrize("scale,eps", [(1e25, 1e-6), (1e-20, 0.0), (1e15, 1e-6), (3e-16, 1e-32)])
 def test_block_norm_far_rows(zs, torch, C, scale, eps):

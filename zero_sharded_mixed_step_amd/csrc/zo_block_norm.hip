@@ -8,8 +8,8 @@
 // workgroups walk the rows and leave their sums in a row of the workspace, which a second kernel
 // folds in order.
 //
-// Measured, bf16 with both norms and a gate by channel: forward of 16384 x 4096 98 us, 5.5 TB/s
-// (x and y read past the caches; through them 102); backward of 8192 x 4096 84 us, 4.8 TB/s, the
+// Measured, bf16 with both norms and a gate by channel: forward of 16384 x 4096 94 us, 5.7 TB/s
+// (all past the caches; written through them 98, read too 102); backward of 8192 x 4096 84 us, 4.8 TB/s, the
 // fold 5 of them (loads through the caches 90; four barriers a row and the gate's sums of their own,
 // twice the instructions: 104).  4097 x 1000, fp32 stream and a gate by token: backward 25 us.  8192 x
 // 8192 backward 153 us, 5.3 TB/s; 4096 x 16384, where less is held, 192 us, 4.2 TB/s.
@@ -136,7 +136,7 @@ __device__ __forceinline__ void gate8(const BlockParams& p, const char* gate, in
 }
 
 // NT threads to a row, CH pieces of 8 values to a thread.
-template <typename E, typename R, int NT, int CH>
+template <typename E, typename R, int NT, int CH, bool PAST>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_fwd_kernel(const BlockParams p) {
   constexpr int kRows = NT < 256 ? 256 / NT : 1;
   constexpr bool S = kSplit<E, R>;
@@ -182,7 +182,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_fwd_kernel(con
   if (p.h != nullptr) {
 #pragma unroll
     for (int k = 0; k < CH; ++k)
-      if (on[k]) store8<R, S>(row_of<R>(p.h, t, p.h_s), column<S, NT>(tid, k), p.C, h[k]);
+      if (on[k]) store8<R, S, PAST>(row_of<R>(p.h, t, p.h_s), column<S, NT>(tid, k), p.C, h[k]);
   }
   if (p.z == nullptr) return;
   const float r = inverse_rms<NT, CH>(sum, h, inv_c, p.eps);
@@ -194,7 +194,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_fwd_kernel(con
     weight8<E, S>(p.pre_w, p.has_pre_w, p.offset, c, p.C, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) h[k][j] = h[k][j] * r * w[j];
-    store8<E, S>(row_of<E>(p.z, t, p.z_s), c, p.C, h[k]);
+    store8<E, S, PAST>(row_of<E>(p.z, t, p.z_s), c, p.C, h[k]);
   }
 }
 
@@ -312,7 +312,7 @@ constexpr int kBwdThreads = NT <= 128 ? 4 * NT : NT == 256 ? 512 : NT;
 //
 // The gate's gradient and the first weight's come from one sum where the tokens share the
 // gate: t = sum of gh yy gives branch_scale (post_w + offset) t and branch_scale gate t.
-template <typename E, typename R, int NT, int CH>
+template <typename E, typename R, int NT, int CH, bool PAST>
 __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const BlockParams p) {
   constexpr int kRows = kBwdThreads<NT> / NT;
   __shared__ float s[NT > 64 ? kRows : 1][NT > 64 ? 8 * (NT / 64) : 1];
@@ -497,7 +497,7 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
         float x[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = gh[j] * p.res_scale;
-        store8<R, S>(row_of<R>(p.dx, t, p.dx_s), c, C, x);
+        store8<R, S, PAST>(row_of<R>(p.dx, t, p.dx_s), c, C, x);
       }
       float* u = u1[kHold ? k : 0];
       float y[8];
@@ -514,7 +514,7 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
           dot[0] = __builtin_fmaf(u[j], yy, dot[0]);
         }
         if (c < C && p.dgate != nullptr)
-          store8<E, S>(row_of<E>(p.dgate, t, p.dgate_s), c, C, d);
+          store8<E, S, PAST>(row_of<E>(p.dgate, t, p.dgate_s), c, C, d);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -546,7 +546,7 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
 #pragma unroll
         for (int j = 0; j < 8; ++j) u[j] = __builtin_fmaf(a1, y[j] * r1, r1 * u[j]);
       }
-      store8<E, S>(row_of<E>(p.dy, t, p.dy_s), c, C, u);
+      store8<E, S, PAST>(row_of<E>(p.dy, t, p.dy_s), c, C, u);
     }
     if constexpr (kAhead) {
 #pragma unroll
@@ -664,17 +664,26 @@ int bwd_groups(int64_t T, int C) {
       std::min({wanted, n, static_cast<int64_t>(C > 4096 ? kBlockBwdLarge : kBlockBwdGroups)}));
 }
 
+// From here on outputs go past the caches, which do not hold them until they are read.  (T x 4096 bf16,
+// us, with both outputs' readers behind it: T = 16384 forward 171 instead of 191, backward 229 instead of 243;
+// 12288, 192 MiB, 131 and 131, 174 and 179; 8192 92 instead of 86, 122 instead of 113.)
+constexpr int64_t kPastBytes = int64_t(192) << 20;
+
 template <typename E, typename R, int NT, int CH>
 void run_bwd(const BlockParams& p, hipStream_t s) {
-  block_norm_bwd_kernel<E, R, NT, CH>
-      <<<bwd_groups(p.T, p.C), kBwdThreads<NT>, 0, s>>>(p);
+  const int64_t bytes = (p.dx ? sizeof(R) : 0) + (p.dy ? sizeof(E) : 0);
+  const auto fn = p.T * p.C * bytes >= kPastBytes ? block_norm_bwd_kernel<E, R, NT, CH, true>
+                                                  : block_norm_bwd_kernel<E, R, NT, CH, false>;
+  fn<<<bwd_groups(p.T, p.C), kBwdThreads<NT>, 0, s>>>(p);
 }
 
 template <typename E, typename R, int NT, int CH>
 void run_fwd(const BlockParams& p, hipStream_t s) {
   constexpr int kThreads = NT < 256 ? 256 : NT, kRows = kThreads / NT;
-  block_norm_fwd_kernel<E, R, NT, CH>
-      <<<static_cast<unsigned>((p.T + kRows - 1) / kRows), kThreads, 0, s>>>(p);
+  const int64_t bytes = (p.h ? sizeof(R) : 0) + (p.z ? sizeof(E) : 0);
+  const auto fn = p.T * p.C * bytes >= kPastBytes ? block_norm_fwd_kernel<E, R, NT, CH, true>
+                                                  : block_norm_fwd_kernel<E, R, NT, CH, false>;
+  fn<<<static_cast<unsigned>((p.T + kRows - 1) / kRows), kThreads, 0, s>>>(p);
 }
 
 // By the row's length: forward the fewest threads that hold it with 16 values each (16384 x 4096: 98
