@@ -657,7 +657,7 @@ class GradTable:
     addresses, sizes and types, laid out once for tensors that keep their memory from step
     to step.  `outs` are where the clipped gradients go (float32 or bfloat16 each); None: in
     place.  The tensors and their memory are held, with the sizes that they have here, and a
-    call raises if one of them has moved since."""
+    call raises if one that it reads or writes has moved since."""
 
     def __init__(self, grads, outs=None):
         self.grads = list(grads)
@@ -683,10 +683,12 @@ class GradTable:
                 raise ValueError(f"an output of {o.numel()} elements for {g.numel()}")
         self._refuse_overlaps()
         n = len(self.grads)
-        self._at = self._addresses()
+        self._grads_at = self._out_at = list(map(torch.Tensor.data_ptr, self.grads))
+        if self.outs is not self.grads:
+            self._out_at = list(map(torch.Tensor.data_ptr, self.outs))
         # (a tensor that is given other memory leaves what the addresses name in place)
         self._memory = [t.untyped_storage() for t in self.grads + self.outs]
-        flat = [(C.c_uint64 * n)(*self._at[:n]), (C.c_uint64 * n)(*self._at[-n:] if n else ()),
+        flat = [(C.c_uint64 * n)(*self._grads_at), (C.c_uint64 * n)(*self._out_at),
                 (C.c_int64 * n)(*(t.numel() for t in self.grads)),
                 (C.c_int32 * n)(*(_CODES[t.dtype] for t in self.grads)),
                 (C.c_int32 * n)(*(_CODES[t.dtype] for t in self.outs))]
@@ -707,14 +709,12 @@ class GradTable:
                 raise ValueError("outputs overlap one another or other gradients")
             ends[written] = max(ends[written], end)
 
-    def _addresses(self):
-        at = list(map(torch.Tensor.data_ptr, self.grads))
-        if self.outs is not self.grads:
-            at += map(torch.Tensor.data_ptr, self.outs)
-        return at
-
-    def _checked(self, dev):
-        if self._addresses() != self._at:
+    def _checked(self, dev, written):
+        """The table's arrays, after a look at where its tensors are now (the outputs too if they are
+        `written`: 40 ns a tensor, most of what a call on hundreds of small ones costs)."""
+        at = torch.Tensor.data_ptr
+        if list(map(at, self.grads)) != self._grads_at or (
+                written and self.outs is not self.grads and list(map(at, self.outs)) != self._out_at):
             raise ValueError("a tensor of the table has moved: make a new table")
         if self.grads and self.device != dev:
             raise ValueError(f"the table is on cuda:{self.device}; the library launches on the "
@@ -755,7 +755,7 @@ def zero_grads_norm(table, acc, *, inv_scale=1.0, add=False, workspace=None,
     by one, so that it may be summed over ranks or given to zero_adamw_step.  workspace:
     zero_grads_workspace_bytes() bytes."""
     dev = _device()
-    grads, _, sizes, types, _ = table._checked(dev)
+    grads, _, sizes, types, _ = table._checked(dev, False)
     acc_, n = _accs(acc, "acc", dev)
     if n > 1:
         raise ValueError("acc is one accumulator")
@@ -773,7 +773,7 @@ def zero_grads_clip(table, accs, *, max_norm, inv_scale=1.0, check_overflow=Fals
     skipped_out (int32), one element each, get the global norm, the coefficient and whether
     it was skipped."""
     dev, f32 = _device(), torch.float32
-    grads, outs, sizes, types, out_types = table._checked(dev)
+    grads, outs, sizes, types, out_types = table._checked(dev, True)
     accs_, n = _accs(accs, "accs", dev)
     args = _GRADS_ARGS.pack(_GRADS_ARGS.size, len(table.grads), grads, outs, sizes, types, out_types,
                             inv_scale, 0, 0, n, accs_, max_norm, 1 if check_overflow else 0, 0,
