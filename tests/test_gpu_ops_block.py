@@ -148,6 +148,26 @@ def test_embed_backward_many_tokens(zs, torch, N, kind):
     assert torch.equal(got.cpu().double(), want[:V]) and bool((behind == 0xFF).all())
 
 
+@pytest.mark.parametrize("kind", ["zipf", "same", "few", "down", "beside", "none"])
+@pytest.mark.parametrize("N", [257, 4097, 70001])
+@pytest.mark.parametrize("V,C", [(20011, 8), (300007, 8), (9001, 2048), (8209, 4104)])
+def test_embed_backward_runs_in_large_tables(zs, torch, V, C, N, kind):
+    """Runs that fill the keys a wave looks at for the rows that no id names, with a row beside them."""
+    if N * C > 1 << 24:
+        N = 4097
+    g = _gen(torch, V + N)
+    ids = _ids(torch, kind if kind != "beside" else "same", N, V, g)
+    if kind == "beside":
+        ids[3], ids[4] = V // 2 - 1, V // 2 + 2
+    dout = torch.randint(-4, 5, (N, C), generator=g).to(torch.bfloat16)
+    want = torch.zeros(V + 1, C, dtype=torch.float64)
+    want.index_add_(0, torch.where((ids >= 0) & (ids < V), ids, V).long(), dout.double())
+    ws, _ = _ws(torch, zs.zero_embed_workspace_bytes(N, C))
+    got = torch.full((V, C), math.nan, device="cuda")
+    zs.zero_embed_bwd(ids.cuda(), dout.cuda(), got, workspace=ws)
+    assert torch.equal(got.cpu().double(), want[:V])
+
+
 @pytest.mark.parametrize("types", [("bf16", "bf16", None), ("bf16", "f32", "bf16"), ("f32", "f32", "f32"),
                                    ("bf16", "bf16", "f32"), ("f32", "bf16", "bf16")], ids=str)
 @pytest.mark.parametrize("N,V,C", [(1, 1, 8), (37, 12, 520), (500, 90, 1000), (2100, 70, 1544)])
@@ -926,6 +946,11 @@ def test_grad_table_notices_what_moved(zs, torch):
     t.data = torch.randn(100, device="cuda")
     with pytest.raises(ValueError):
         zs.zero_grads_norm(table, acc, workspace=ws)
+    with pytest.raises(ValueError):
+        zs.zero_grads_clip(table, acc, max_norm=1.0)
+    g, o = torch.randn(100, device="cuda"), torch.randn(100, device="cuda")
+    table = zs.GradTable([g], [o])
+    o.data = torch.randn(100, device="cuda")
     with pytest.raises(ValueError):
         zs.zero_grads_clip(table, acc, max_norm=1.0)
     with pytest.raises(ValueError):

@@ -58,6 +58,7 @@ struct EmbedParams {
   int32_t *tile_key, *tile_place;             // sorted within tiles
   float* part;                                // [chunks][2][C]: a chunk's first and last run
   int64_t sum_units, fill_units;
+  int64_t search_step;                        // 64 times it are at least N; 0: see fill_rows
   int fill_parts;                             // parts of a table row that waves take
   int fill_rows;                              // table rows of a wave that writes what no id names; 0: none does
 };
@@ -356,19 +357,39 @@ __device__ __forceinline__ void write_base(const EmbedParams& p, int64_t unit, i
   }
 }
 
-// Rows of the table that no id names.
+// Rows of the table that no id names.  The lanes look together for the keys below the first row, 64
+// times fewer places a step; the 64 keys from there on say which rows are named, but where runs fill
+// them.  Then, and for long rows, whose writes hide the steps of a search that asks for less, every lane
+// looks for its own row.  (16384 tokens, 50257 rows in bf16: of 2048 columns 54 us, each lane for itself
+// 65; of 4096 105, 102.)
 template <typename G, typename B>
 __device__ __forceinline__ void fill_rows(const EmbedParams& p, int64_t unit, int lane) {
-  const int64_t v0 = unit / p.fill_parts * p.fill_rows, v = v0 + lane;
-  bool absent = lane < p.fill_rows && v < p.V;
-  if (absent) {
-    int64_t at = 0;                           // how many keys are below v
-    for (int64_t step = int64_t(1) << 21; step > 0; step >>= 1)
-      if (at + step <= p.N && p.key[at + step - 1] < v) at += step;
-    absent = at >= p.N || p.key[at] != v;
-  }
+  const int64_t v0 = unit / p.fill_parts * p.fill_rows;
   const int here = static_cast<int>(min(p.V - v0, static_cast<int64_t>(p.fill_rows)));
-  write_base<G, B>(p, unit, here, __ballot(absent), lane);
+  int64_t at = 0;                             // how many keys are below v0, or the lane's row
+  uint64_t absent = 0;
+  bool found = p.search_step > 0;
+  if (found) {
+    for (int64_t step = p.search_step; step > 0; step >>= 6) {
+      const int64_t i = at + (lane + 1) * step - 1;
+      at += step * __popcll(__ballot(i < p.N && p.key[i] < v0));
+    }
+    const int64_t key = at + lane < p.N ? p.key[at + lane] : p.V;
+    for (int r = 0; r < here; ++r)
+      if (!__any(key == v0 + r)) absent |= 1ull << r;
+    found = __any(key >= v0 + here);
+  }
+  if (!found) {
+    bool none = lane < here;
+    if (none) {
+      const int64_t v = v0 + lane;
+      for (int64_t step = int64_t(1) << 21; step > 0; step >>= 1)
+        if (at + step <= p.N && p.key[at + step - 1] < v) at += step;
+      none = at >= p.N || p.key[at] != v;
+    }
+    absent = __ballot(none);
+  }
+  write_base<G, B>(p, unit, here, absent, lane);
 }
 
 template <typename E, typename G, typename B>
@@ -524,12 +545,11 @@ int64_t chunks_of(int64_t N) { return (N + chunk_places(N) - 1) / chunk_places(N
 
 // Rows of a wave that writes what no id names: one, or up to 4096 columns of it, so that the writes'
 // front is compact (50257 rows of 4096 with a base: 260 us; two rows 302 and eight 328 where one took
-// 293; 2048 columns 269; 13357 rows of 7896 for 20 tokens: 174, whole rows 184).  More of rows that are
-// shorter than the search for the tokens' rows is long, some 1536 columns (50257 rows of 1024: 48 us, two
-// rows 54; of 768: two 44, one 47; 200000 of 64: 32 rows 20, one 89), or without a search half of it
-// (50257 of 768: one 28.9, two 30.4); of a small table no more than leave 4096 waves.
-int fill_rows_of(int64_t N, int64_t V, int C) {
-  const int64_t rows = std::min<int64_t>((N <= kDirectTokens ? 768 : 1536) / C, V / 4096);
+// 293; 2048 columns 269; 13357 rows of 7896 for 20 tokens: 174, whole rows 184).  Of shorter rows as many
+// as are 4 KiB of the gradient (16384 tokens, 50257 rows of 768 in fp32: one 42 us, two 45; in bf16
+// two 34, one 39; of 1024 in bf16 two 37, one 40), of a small table no more than leave 4096 waves.
+int fill_rows_of(int64_t V, int C, int grad_dtype) {
+  const int64_t rows = std::min<int64_t>(4096 / (C * (grad_dtype == ZERO_BF16 ? 2 : 4)), V / 4096);
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rows, 64)));
 }
 
@@ -610,9 +630,11 @@ hipError_t launch_embed_bwd(const zero_embed_args& a, hipStream_t s) {
   p.chunks = static_cast<int>(chunks_of(a.N));
   p.sum_units = static_cast<int64_t>(p.chunks) * p.slices;
   if (a.base != a.dtable) {
-    p.fill_rows = fill_rows_of(a.N, a.V, a.C);
+    p.fill_rows = fill_rows_of(a.V, a.C, a.grad_dtype);
     p.fill_parts = (a.C + kFillColumns - 1) / kFillColumns;
     p.fill_units = (a.V + p.fill_rows - 1) / p.fill_rows * p.fill_parts;
+    if (a.C < kFillColumns)
+      for (p.search_step = 1; p.search_step * 64 < a.N;) p.search_step *= 64;
   }
   char* ws = static_cast<char*>(a.workspace);
   const size_t list = rounded(a.N * sizeof(int32_t));
