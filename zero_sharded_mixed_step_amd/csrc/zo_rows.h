@@ -16,11 +16,6 @@ struct Vec8<bf16> {
   __device__ __forceinline__ void load(const void* p, int64_t at) {
     r = *reinterpret_cast<const u32x4*>(static_cast<const bf16*>(p) + at);
   }
-  // (read, or below written, once: past the caches)
-  __device__ __forceinline__ void load_once(const void* p, int64_t at) {
-    r = __builtin_nontemporal_load(
-        reinterpret_cast<const u32x4*>(static_cast<const bf16*>(p) + at));
-  }
   __device__ __forceinline__ void get(float x[8]) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -34,6 +29,7 @@ struct Vec8<bf16> {
     for (int j = 0; j < 8; ++j) v[j] = static_cast<bf16>(x[j]);
     *reinterpret_cast<bf16x8*>(static_cast<bf16*>(p) + at) = v;
   }
+  // (past the caches)
   __device__ __forceinline__ static void store_once(void* p, int64_t at, const float x[8]) {
     bf16x8 v;
 #pragma unroll
@@ -48,11 +44,6 @@ struct Vec8<float> {
     const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + at);
     a = q[0];
     b = q[1];
-  }
-  __device__ __forceinline__ void load_once(const void* p, int64_t at) {
-    const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + at);
-    a = __builtin_nontemporal_load(q);
-    b = __builtin_nontemporal_load(q + 1);
   }
   __device__ __forceinline__ void get(float x[8]) const {
 #pragma unroll
