@@ -36,8 +36,11 @@
  *     element is rounded once.  Every sum has a fixed order (the only atomics
  *     set bits in shared memory), so the same call gives the same bits every
  *     time on one device.
- *   - Outputs must not overlap inputs unless stated (where the same address
- *     is allowed, other strides are ZERO_EINVAL).
+ *   - Outputs must not overlap inputs, one another or the workspace unless
+ *     stated (where the same address is allowed, other strides are
+ *     ZERO_EINVAL).  From the embedding on such calls are ZERO_EINVAL; arrays
+ *     whose rows lie between one another's, as columns of one buffer do, are
+ *     apart.
  */
 #ifndef ZERO_OPS_H
 #define ZERO_OPS_H
@@ -386,7 +389,9 @@ int zero_policy_bwd(const zero_policy_args *args, void *stream);
  * zero_grads_clip: outs[i] = (grads[i] * inv_scale) * coef, rounded to out_dtypes[i],
  * with the skip and the coefficient that zero_step_gate derives from the n_accs
  * accumulators, max_norm and check_overflow; a skipped call writes no tensor.  outs[i]
- * may be grads[i] (same dtype), and overlaps no other tensor.  norm_out, coef_out and
+ * may be grads[i] (same dtype), and overlaps no other tensor: looked for at each call, in
+ * the order of the addresses, unless outs_apart is 1, by which the caller says that it has
+ * seen to it (0.03 us a tensor on the host).  norm_out, coef_out and
  * skipped_out (each may be NULL): the global norm, infinite where a value is not finite,
  * the coefficient (0 where skipped) and 1 where skipped, else 0. */
 typedef struct zero_grads_args {
@@ -403,7 +408,7 @@ typedef struct zero_grads_args {
   int32_t n_accs;               /* clip from here on */
   const zero_norm_acc *accs;
   double max_norm;
-  int32_t check_overflow, reserved;
+  int32_t check_overflow, outs_apart;
   float *norm_out, *coef_out;
   int32_t *skipped_out;
   void *workspace;              /* norm */

@@ -776,7 +776,7 @@ def zero_grads_clip(table, accs, *, max_norm, inv_scale=1.0, check_overflow=Fals
     grads, outs, sizes, types, out_types = table._checked(dev, True)
     accs_, n = _accs(accs, "accs", dev)
     args = _GRADS_ARGS.pack(_GRADS_ARGS.size, len(table.grads), grads, outs, sizes, types, out_types,
-                            inv_scale, 0, 0, n, accs_, max_norm, 1 if check_overflow else 0, 0,
+                            inv_scale, 0, 0, n, accs_, max_norm, 1 if check_overflow else 0, 1,
                             _scalar(norm_out, "norm_out", f32, dev),
                             _scalar(coef_out, "coef_out", f32, dev),
                             _scalar(skipped_out, "skipped_out", torch.int32, dev), 0, 0)

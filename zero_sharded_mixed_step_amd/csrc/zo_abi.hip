@@ -3,14 +3,20 @@
 // exception crosses this boundary.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
+#include <utility>
+#include <vector>
 
 #include "zero_ops.h"
 #include "zo_internal.h"
+#include "zo_spans.h"
 
 namespace {
+
+using zo::Span;
 
 hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
 
@@ -205,6 +211,24 @@ int check_row_width(int C) {
   return C < 8 || C > ZERO_ROW_MAX_C || C % 8 != 0 ? ZERO_ESIZE : ZERO_OK;
 }
 
+// Whether what a call writes meets nothing else of it; `need` bytes of its workspace are used.
+bool embed_apart(const zero_embed_args* a, bool fwd, size_t need) {
+  const int eb = bytes_of(a->dtype);
+  zo::Arrays<2, 3> m;
+  if (a->N > 0) m.reads(Span(a->ids, a->N * 4));
+  if (fwd) {
+    m.writes(Span(a->out, a->N, a->out_stride, a->C, eb));
+    m.reads(Span(a->table, a->V, a->table_stride, a->C, eb));
+    return m.apart();
+  }
+  m.writes(Span(a->dtable, a->V, a->dtable_stride, a->C, bytes_of(a->grad_dtype)));
+  if (need > 0) m.writes(Span(a->workspace, static_cast<int64_t>(need)));
+  if (a->N > 0) m.reads(Span(a->dout, a->N, a->dout_stride, a->C, eb));
+  if (a->base != a->dtable)
+    m.reads(Span(a->base, a->V, a->base_stride, a->C, bytes_of(a->base_dtype)));
+  return m.apart();
+}
+
 int check_embed(const zero_embed_args* a, bool fwd) {
   if (a == nullptr || a->struct_bytes != sizeof(*a)) return ZERO_EINVAL;
   if (!known_dtype(a->dtype)) return ZERO_EINVAL;
@@ -219,7 +243,7 @@ int check_embed(const zero_embed_args* a, bool fwd) {
     if (a->N == 0) return ZERO_OK;
     ZO_CHECK(check_matrix(a->table, a->table_stride, a->V, a->dtype));
     ZO_CHECK(check_matrix(a->out, a->out_stride, a->N, a->dtype));
-    return rows_apart(a->out_stride, a->N, a->C) ? ZERO_OK : ZERO_EINVAL;
+    return rows_apart(a->out_stride, a->N, a->C) && embed_apart(a, true, 0) ? ZERO_OK : ZERO_EINVAL;
   }
   if (!known_dtype(a->grad_dtype) || (a->base && !known_dtype(a->base_dtype))) return ZERO_EINVAL;
   ZO_CHECK(check_matrix(a->dtable, a->dtable_stride, a->V, a->grad_dtype));
@@ -230,18 +254,56 @@ int check_embed(const zero_embed_args* a, bool fwd) {
                                  (a->V > 1 && a->base_stride != a->dtable_stride)))
       return ZERO_EINVAL;
   }
-  if (a->N == 0) return ZERO_OK;
-  ZO_CHECK(check_matrix(a->dout, a->dout_stride, a->N, a->dtype));
-  const size_t need = zo::embed_workspace(a->N, a->C);
-  if (need == 0) return ZERO_OK;
-  if (a->workspace == nullptr) return ZERO_EINVAL;
-  if (!aligned(a->workspace, 16)) return ZERO_EALIGN;
-  return a->workspace_bytes < need ? ZERO_ESIZE : ZERO_OK;
+  size_t need = 0;
+  if (a->N > 0) {
+    ZO_CHECK(check_matrix(a->dout, a->dout_stride, a->N, a->dtype));
+    need = zo::embed_workspace(a->N, a->C);
+    if (need > 0) {
+      if (a->workspace == nullptr) return ZERO_EINVAL;
+      if (!aligned(a->workspace, 16)) return ZERO_EALIGN;
+      if (a->workspace_bytes < need) return ZERO_ESIZE;
+    }
+  }
+  return embed_apart(a, false, need) ? ZERO_OK : ZERO_EINVAL;
 }
 
 // ------------------------------------------------------ norms round a block ---
 
 int check_vector(const void* p) { return p && !aligned(p, 16) ? ZERO_EALIGN : ZERO_OK; }
+
+// (Of calls that have rows.)
+bool block_apart(const zero_block_norm_args* a, bool fwd, bool parts) {
+  const int eb = bytes_of(a->dtype), rb = bytes_of(a->res_dtype);
+  const auto rows = [&](const void* p, int64_t stride, int bytes) {
+    return Span(p, a->T, stride, a->C, bytes);
+  };
+  const auto vector = [&](const void* p) { return Span(p, static_cast<int64_t>(a->C) * eb); };
+  const auto gate = [&](const void* p, int64_t stride) {
+    return a->gate_tokens ? rows(p, stride, eb) : vector(p);
+  };
+  zo::Arrays<6, 7> m;
+  m.reads(rows(a->y, a->y_stride, eb));
+  m.reads(vector(a->post_w));
+  m.reads(gate(a->gate, a->gate_stride));
+  if (fwd || a->dz != nullptr) m.reads(vector(a->pre_w));
+  if (fwd) {
+    m.writes(rows(a->h, a->h_stride, rb));
+    m.writes(rows(a->z, a->z_stride, eb));
+    if (a->x != a->h) m.reads(rows(a->x, a->x_stride, rb));
+    return m.apart();
+  }
+  m.writes(rows(a->dx, a->dx_stride, rb));
+  m.writes(rows(a->dy, a->dy_stride, eb));
+  m.writes(vector(a->dpost_w));
+  m.writes(gate(a->dgate, a->dgate_stride));
+  m.writes(vector(a->dpre_w));
+  if (parts)
+    m.writes(Span(a->workspace, static_cast<int64_t>(zo::block_norm_workspace(a->T, a->C))));
+  if (a->dh != a->dx) m.reads(rows(a->dh, a->dh_stride, rb));
+  m.reads(rows(a->dz, a->dz_stride, eb));
+  if (a->dz != nullptr) m.reads(rows(a->h, a->h_stride, rb));
+  return m.apart();
+}
 
 int check_block(const zero_block_norm_args* a, bool fwd) {
   if (a == nullptr || a->struct_bytes != sizeof(*a)) return ZERO_EINVAL;
@@ -278,7 +340,7 @@ int check_block(const zero_block_norm_args* a, bool fwd) {
       ZO_CHECK(check_matrix(a->z, a->z_stride, a->T, dt));
       if (!rows_apart(a->z_stride, a->T, a->C)) return ZERO_EINVAL;
     }
-    return ZERO_OK;
+    return block_apart(a, true, false) ? ZERO_OK : ZERO_EINVAL;
   }
   if ((a->dpost_w && !a->post_w) || (a->dpre_w && !a->pre_w)) return ZERO_EINVAL;
   if (rows && ((a->dgate && !a->gate) || (a->dy && !a->y) || (a->dpre_w && !a->dz) ||
@@ -307,15 +369,36 @@ int check_block(const zero_block_norm_args* a, bool fwd) {
     ZO_CHECK(check_matrix(a->dgate, a->dgate_stride, a->T, dt));
     if (!rows_apart(a->dgate_stride, a->T, a->C)) return ZERO_EINVAL;
   }
-  if (a->dpost_w || a->dpre_w || (a->dgate && !a->gate_tokens)) {
+  const bool parts = a->dpost_w || a->dpre_w || (a->dgate && !a->gate_tokens);
+  if (parts) {
     if (a->workspace == nullptr) return ZERO_EINVAL;
     if (!aligned(a->workspace, 16)) return ZERO_EALIGN;
     if (a->workspace_bytes < zo::block_norm_workspace(a->T, a->C)) return ZERO_ESIZE;
   }
-  return ZERO_OK;
+  return block_apart(a, false, parts) ? ZERO_OK : ZERO_EINVAL;
 }
 
 // ------------------------------------------------------------ policy loss ---
+
+bool policy_apart(const zero_policy_args* a, bool fwd) {
+  const int eb = bytes_of(a->dtype);
+  const auto numbers = [&](const void* p, int of_a_row) { return Span(p, a->N * of_a_row * 4); };
+  zo::Arrays<3, 6> m;
+  m.writes(Span(a->dlogits, a->N, a->dlogits_stride, a->V, eb));
+  if (a->logits != a->dlogits) m.reads(Span(a->logits, a->N, a->logits_stride, a->V, eb));
+  m.reads(numbers(a->action, 1));
+  m.reads(numbers(a->row_weight, 1));
+  if (fwd) {
+    m.writes(numbers(a->loss, 1));
+    m.writes(numbers(a->stats, 4));
+    m.reads(numbers(a->advantage, 1));
+    m.reads(numbers(a->old_logp, 1));
+    m.reads(numbers(a->ref_logp, 1));
+  } else {
+    m.reads(numbers(a->stats, 4));
+  }
+  return m.apart();
+}
 
 int check_policy(const zero_policy_args* a, bool fwd) {
   if (a == nullptr || a->struct_bytes != sizeof(*a)) return ZERO_EINVAL;
@@ -340,12 +423,75 @@ int check_policy(const zero_policy_args* a, bool fwd) {
   if (a->dlogits && a->dlogits_stride < a->V && a->N > 1) return ZERO_EINVAL;
   if (a->dlogits == a->logits && a->dlogits_stride != a->logits_stride && a->N > 1)
     return ZERO_EINVAL;
-  return ZERO_OK;
+  return policy_apart(a, fwd) ? ZERO_OK : ZERO_EINVAL;
 }
 
 // ------------------------------------------- norm and clipping of gradients ---
 
 constexpr int64_t kMaxElements = int64_t(1) << 37;   // of a norm accumulator
+
+struct Bytes {
+  uintptr_t at = 0, end = 0;
+  Bytes() = default;
+  Bytes(const void* p, int64_t n)
+      : at(reinterpret_cast<uintptr_t>(p)), end(at + static_cast<uintptr_t>(n)) {}
+  // (at least one byte of both: an empty one meets none)
+  bool meets(const Bytes& b) const { return std::max(at, b.at) < std::min(end, b.end); }
+};
+
+// Whether what a call writes beside the tensors (`small`, some of which may be empty) meets no tensor,
+// nor the accumulators that it reads, and outputs do not meet these.
+bool small_apart(const zero_grads_args* a, bool clip, const Bytes (&small)[3], const Bytes& accs) {
+  Bytes around;                               // all of them: most tensors lie outside
+  around.at = UINTPTR_MAX;
+  const auto extend = [&](const Bytes& b) {
+    if (b.at == b.end) return;
+    around.at = std::min(around.at, b.at);
+    around.end = std::max(around.end, b.end);
+  };
+  extend(accs);
+  for (int i = 0; i < 3; ++i) {
+    extend(small[i]);
+    if (small[i].meets(accs)) return false;
+    for (int j = 0; j < i; ++j)
+      if (small[i].meets(small[j])) return false;
+  }
+  const auto meets_small = [&](const Bytes& t) {
+    return t.meets(small[0]) || t.meets(small[1]) || t.meets(small[2]);
+  };
+  for (int64_t i = 0; i < a->count; ++i) {
+    const Bytes g(a->grads[i], a->sizes[i] * bytes_of(a->dtypes[i]));
+    if (g.at < around.end && around.at < g.end && meets_small(g)) return false;
+    if (!clip) continue;
+    const Bytes out(a->outs[i], a->sizes[i] * bytes_of(a->out_dtypes[i]));
+    if (out.at < around.end && around.at < out.end && (meets_small(out) || out.meets(accs)))
+      return false;
+  }
+  return true;
+}
+
+// Whether every output lies on no tensor but its own gradient, by their addresses in order.
+bool outs_apart(const zero_grads_args* a) {
+  struct Piece : Bytes {
+    bool written;
+  };
+  std::vector<Piece> pieces;
+  pieces.reserve(2 * a->count);
+  for (int64_t i = 0; i < a->count; ++i) {
+    if (a->sizes[i] == 0) continue;
+    if (a->outs[i] != a->grads[i])
+      pieces.push_back({Bytes(a->grads[i], a->sizes[i] * bytes_of(a->dtypes[i])), false});
+    pieces.push_back({Bytes(a->outs[i], a->sizes[i] * bytes_of(a->out_dtypes[i])), true});
+  }
+  std::sort(pieces.begin(), pieces.end(),
+            [](const Piece& x, const Piece& y) { return x.at < y.at; });
+  uintptr_t read = 0, written = 0;            // ends of what came before
+  for (const Piece& x : pieces) {
+    if (x.at < written || (x.written && x.at < read)) return false;
+    (x.written ? written : read) = std::max(x.written ? written : read, x.end);
+  }
+  return true;
+}
 
 int check_grads(const zero_grads_args* a, bool norm) {
   if (a == nullptr || a->struct_bytes != sizeof(*a)) return ZERO_EINVAL;
@@ -370,14 +516,25 @@ int check_grads(const zero_grads_args* a, bool norm) {
   if (norm) {
     if (!a->acc || !a->workspace) return ZERO_EINVAL;
     if (!aligned(a->acc, 16) || !aligned(a->workspace, 16)) return ZERO_EALIGN;
-    return a->workspace_bytes < zo::grads_workspace() ? ZERO_ESIZE : ZERO_OK;
+    if (a->workspace_bytes < zo::grads_workspace()) return ZERO_ESIZE;
+    if (total == 0) return ZERO_OK;            // (the workspace is not used)
+    return small_apart(a, false,
+                       {Bytes(a->acc, sizeof(*a->acc)),
+                        Bytes(a->workspace, static_cast<int64_t>(zo::grads_workspace())), Bytes()},
+                       Bytes())
+               ? ZERO_OK
+               : ZERO_EINVAL;
   }
   if (a->n_accs < 0 || (a->n_accs > 0 && !a->accs) || !std::isfinite(a->max_norm))
     return ZERO_EINVAL;
   if (!aligned(a->accs, 16) || !aligned(a->norm_out, 4) || !aligned(a->coef_out, 4) ||
       !aligned(a->skipped_out, 4))
     return ZERO_EALIGN;
-  return ZERO_OK;
+  if (!small_apart(a, true, {Bytes(a->norm_out, a->norm_out ? 4 : 0), Bytes(a->coef_out, a->coef_out ? 4 : 0),
+                             Bytes(a->skipped_out, a->skipped_out ? 4 : 0)},
+                   Bytes(a->accs, static_cast<int64_t>(sizeof(*a->accs)) * a->n_accs)))
+    return ZERO_EINVAL;
+  return a->outs_apart == 1 || outs_apart(a) ? ZERO_OK : ZERO_EINVAL;
 }
 
 }  // namespace
