@@ -51,3 +51,56 @@ def test_columns_of_one_buffer(zs, torch, T, C):
             to.copy_(of)
         for a, b in zip(run(*v), want):
             assert _same(a, b)
+
+
+def _ends(torch, g, T, C, dtype, size):
+    """Rows 0 and 2 of about `size`, the others ordinary."""
+    x = torch.randn(T, C, generator=g).clamp(-2, 2)
+    x[0::2] *= size
+    return x.to(dtype)
+
+
+@pytest.mark.parametrize("C", [64, 1000, 2048, 4096, 8192, 16384])
+@pytest.mark.parametrize("types", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")], ids=str)
+@pytest.mark.parametrize("size", [2.0 ** -126, 2.0 ** -128, 2.0 ** -130, 2.0 ** -140, 1.2e38])
+def test_block_norm_rows_at_the_ends(zs, torch, C, types, size):
+    """Rows whose inverse root is past binary32's ends, from subnormal values to the largest: normed as
+    any other, and so are their gradients.  (Bounds: every row's own; the powers of 2 round nothing.)"""
+    dt, rt = _types(torch, *types)
+    if size < 2.0 ** -133 and (dt, rt) != (torch.float32, torch.float32):
+        size = 2.0 ** -131                     # (bf16's smallest number is 2^-133)
+    T, g = 3, _gen(torch, C)
+    small = size < 1.0
+    ws, behind = _ws(torch, zs.zero_block_norm_workspace_bytes(T, C))
+    w1, w2, gate_c = (_rand(torch, g, (C,), dt, 0.5) for _ in range(3))
+    dz = _rand(torch, g, (T, C), dt, 2.0 ** -60 if small else 1.0)
+    dh = _rand(torch, g, (T, C), rt, 2.0 ** 60 if small else 1.0)
+
+    def both(x, y, post, gate, branch, dh):
+        ref = B.Block(x, y, post=post, w1=w1 if post else None, gate=gate, w2=w2, branch=branch, eps=0.0, dt=dt)
+        d = [None if t is None else t.cuda() for t in (x, y, w1 if post else None, gate, w2, dh, dz)]
+        kw = dict(post_norm=post, post_weight=d[2], gate=d[3], pre_weight=d[4], branch_scale=branch, eps=0.0)
+        h = torch.full((T, C), math.nan, dtype=rt, device="cuda")
+        z = torch.full((T, C), math.nan, dtype=dt, device="cuda")
+        zs.zero_block_norm_fwd(d[0], d[1], h, z, **kw)
+        want = ref.forward(True)
+        R.check("h", h, *want["h"])
+        R.check("z", z, *want["z"])
+        assert bool(torch.isfinite(z).all())
+        got = dict(dx=torch.full_like(h, math.nan), dw2=torch.full_like(d[4], math.nan))
+        if y is not None:
+            got.update(dy=torch.full_like(z, math.nan), dw1=torch.full_like(d[4], math.nan),
+                       dgate=torch.full_like(d[3], math.nan))
+        zs.zero_block_norm_bwd(d[1], h, d[5], d[6], got["dx"], got.get("dy"), dpost_weight=got.get("dw1"),
+                               dgate=got.get("dgate"), dpre_weight=got["dw2"], workspace=ws, **kw)
+        want = ref.backward(h.cpu(), dh, dz)
+        for n, t in got.items():
+            assert bool(torch.isfinite(t).all()), n
+            R.check(n, t, *want[n])
+
+    # the stream itself is at the end; then a block's output that is normed into an ordinary stream
+    both(_ends(torch, g, T, C, rt, size), None, False, None, 1.0, dh)
+    for gate in (gate_c, _rand(torch, g, (T, C), dt, 0.5)):
+        both(_rand(torch, g, (T, C), rt), _ends(torch, g, T, C, dt, size), True, gate,
+             2.0 ** -60 if small else 1.0, _rand(torch, g, (T, C), rt))
+    assert bool((behind == 0xFF).all())

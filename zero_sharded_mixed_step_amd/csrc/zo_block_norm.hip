@@ -62,7 +62,7 @@ struct RowSum {
 };
 
 // 1 / sqrt(mean(v^2) + eps), and where that mean is past binary32's ends, of v times a
-// power of 2.  The same in all threads of the row.
+// power of 2 (see far_root).  The same in all threads of the row.
 template <int NT, int CH>
 __device__ __forceinline__ float inverse_rms(RowSum<NT>& sum, const float (&v)[CH][8], float inv_c,
                                              float eps) {
@@ -73,14 +73,14 @@ __device__ __forceinline__ float inverse_rms(RowSum<NT>& sum, const float (&v)[C
     for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(v[k][j], v[k][j], sq);
   const float ms = __builtin_fmaf(sum(sq), inv_c, eps);
   float r = __builtin_amdgcn_rsqf(ms);
-  if (far_mean(ms)) {
+  if (__builtin_expect(far_mean(ms), 0)) {
     const float s = ms < 1.f ? 0x1p100f : 0x1p-100f;
     sq = 0.f;
 #pragma unroll
     for (int k = 0; k < CH; ++k)
 #pragma unroll
       for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(v[k][j] * s, v[k][j] * s, sq);
-    r = s * __builtin_amdgcn_rsqf(__builtin_fmaf(sum(sq), inv_c, eps * s * s));
+    r = far_root(__builtin_fmaf(sum(sq), inv_c, eps * s * s), s);
   }
   return r;
 }
@@ -135,6 +135,18 @@ __device__ __forceinline__ void gate8(const BlockParams& p, const char* gate, in
   }
 }
 
+// A row whose root stands apart from its power takes that.
+template <int CH>
+__device__ __forceinline__ float with_power(float (&v)[CH][8], float r) {
+  if (__builtin_expect(power_apart(r), 0)) {
+#pragma unroll
+    for (int k = 0; k < CH; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[k][j] *= far_power(r);
+  }
+  return fabsf(r);
+}
+
 // NT threads to a row, CH pieces of 8 values to a thread.
 template <typename E, typename R, int NT, int CH, bool PAST>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_fwd_kernel(const BlockParams p) {
@@ -161,7 +173,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_fwd_kernel(con
     }
   }
   if (p.y != nullptr) {
-    const float r = p.post ? inverse_rms<NT, CH>(sum, y, inv_c, p.eps) : 1.f;
+    const float r = p.post ? with_power(y, inverse_rms<NT, CH>(sum, y, inv_c, p.eps)) : 1.f;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       const int c = column<S, NT>(tid, k);
@@ -185,7 +197,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void block_norm_fwd_kernel(con
       if (on[k]) store8<R, S, PAST>(row_of<R>(p.h, t, p.h_s), column<S, NT>(tid, k), p.C, h[k]);
   }
   if (p.z == nullptr) return;
-  const float r = inverse_rms<NT, CH>(sum, h, inv_c, p.eps);
+  const float r = with_power(h, inverse_rms<NT, CH>(sum, h, inv_c, p.eps));
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
     const int c = column<S, NT>(tid, k);
@@ -279,26 +291,26 @@ __device__ __forceinline__ void row_sums(float* s, int& turn, float (&x)[N]) {
     x[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), kAt[i]));
 }
 
-// r = 1 / sqrt(mean(v^2) + eps) and mean(u v) r of a row whose mean square ms is past
-// binary32's ends, of v times a power of 2.  Rare: every wave reads the whole row again, and
+// r = 1 / sqrt(mean(v^2) + eps), as far_root gives it, and m = mean(u v) of normed v, of a row whose
+// mean square ms is past binary32's ends.  Rare: every wave reads the whole row again, and
 // needs no barrier for it.  part(c, u, v) gives the values of column c.
 template <typename Part>
 __device__ __forceinline__ void far_norm(int C, float ms, float inv_c, float eps, float& r, float& m,
                                          Part part) {
-  const float f = ms < 1.f ? 0x1p100f : 0x1p-100f;
+  const float s = ms < 1.f ? 0x1p100f : 0x1p-100f;
   float vv = 0.f, uv = 0.f;
 #pragma unroll 1
   for (int c = threadIdx.x & 63; c < C; c += 64) {
     float u, v;
     part(c, u, v);
-    vv = __builtin_fmaf(v * f, v * f, vv);
-    uv = __builtin_fmaf(u, v * f, uv);
+    vv = __builtin_fmaf(v * s, v * s, vv);
+    uv = __builtin_fmaf(u, v * s, uv);
   }
   vv = join_lanes<64>(vv, AddOp());
   uv = join_lanes<64>(uv, AddOp());
-  const float rf = __builtin_amdgcn_rsqf(__builtin_fmaf(vv, inv_c, eps * f * f));
-  r = f * rf;
-  m = uv * inv_c * rf;
+  const float mean = __builtin_fmaf(vv, inv_c, eps * s * s);
+  r = far_root(mean, s);
+  m = uv * inv_c * __builtin_amdgcn_rsqf(mean);
 }
 
 // Threads of a workgroup: four rows of up to 1024 values, two of up to 2048 (16384 x 2048: 73 us,
@@ -457,7 +469,7 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
     float m2 = sums[1] * inv_c * r2;             // mean(u2 hh)
     if (!use_z) {
       r2 = m2 = 0.f;
-    } else if (far_mean(ms2)) {
+    } else if (__builtin_expect(far_mean(ms2), 0)) {
       far_norm(C, ms2, inv_c, p.eps, r2, m2, [&](int c, float& u, float& v) {
         u = value<E>(row_of<E>(p.dz, t, p.dz_s), c) *
             (p.has_pre_w ? value<E>(p.pre_w, c) + p.offset : 1.f);
@@ -466,7 +478,7 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
     }
     if (!p.post) {
       r1 = 1.f;
-    } else if (far_mean(ms1)) {
+    } else if (__builtin_expect(far_mean(ms1), 0)) {
       float none;
       far_norm(C, ms1, inv_c, p.eps, r1, none, [&](int c, float& u, float& v) {
         u = 0.f;
@@ -474,7 +486,8 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
       });
     }
     if (C == 0) r1 = r2 = m2 = 0.f;              // (with an eps of 0 they were infinite)
-    const float a2 = -r2 * m2;
+    const bool apart1 = power_apart(r1), apart2 = power_apart(r2);
+    const float a2 = -fabsf(r2) * (m2 * far_power(r2));
     float u1[kHeld][8], dot[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
@@ -487,10 +500,19 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
       float* dw2 = sum_w2[kHold ? k : 0];
       if constexpr (!kHold) take(kept_w2, k, dw2);
 #pragma unroll
+      for (int j = 0; j < 8; ++j) w2[j] *= z[j];
+      if (__builtin_expect(apart2, 0)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          h[j] *= far_power(r2);
+          w2[j] *= far_power(r2);
+        }
+      }
+#pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float hh = h[j] * r2;
+        const float hh = h[j] * fabsf(r2);
         dw2[j] = __builtin_fmaf(z[j], hh, dw2[j]);
-        gh[j] = __builtin_fmaf(a2, hh, __builtin_fmaf(r2, z[j] * w2[j], gh[j]));
+        gh[j] = __builtin_fmaf(a2, hh, __builtin_fmaf(fabsf(r2), w2[j], gh[j]));
       }
       if constexpr (!kHold) put(kept_w2, k, dw2);
       if (c < C && p.dx != nullptr) {
@@ -499,15 +521,21 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
         for (int j = 0; j < 8; ++j) x[j] = gh[j] * p.res_scale;
         store8<R, S, PAST>(row_of<R>(p.dx, t, p.dx_s), c, C, x);
       }
+      // (where the longest rows' types differ no register is left to wait with it: read again)
+      if constexpr (!kHold && sizeof(E) != sizeof(R)) columns_of(k, w2, gw);
       float* u = u1[kHold ? k : 0];
       float y[8];
       y_of(k, y);
+      if (__builtin_expect(apart1, 0)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] *= far_power(r1);
+      }
       if (tokens) {
         float g[8], d[8];
         load8<E, S>(gate, c, C, g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float yy = y[j] * r1, v = gh[j] * gw[j];
+          const float yy = y[j] * fabsf(r1), v = gh[j] * gw[j];
           d[j] = v * yy;
           u[j] = v * g[j];
           sum_t[k][j] = __builtin_fmaf(gh[j] * g[j], yy, sum_t[k][j]);
@@ -518,7 +546,7 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float yy = y[j] * r1;
+          const float yy = y[j] * fabsf(r1);
           u[j] = gh[j] * gw[j];
           sum_t[k][j] = __builtin_fmaf(gh[j], yy, sum_t[k][j]);
           dot[0] = __builtin_fmaf(u[j], yy, dot[0]);
@@ -532,7 +560,7 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
     float a1 = 0.f;                              // -r1 mean(u1 yy)
     if (p.dy != nullptr && p.post) {
       row_sums<NT, 1>(s[NT > 64 ? row : 0], turn, dot);
-      a1 = -r1 * (dot[0] * inv_c);
+      a1 = -fabsf(r1) * (dot[0] * inv_c * far_power(r1));
     }
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
@@ -543,8 +571,15 @@ __global__ __launch_bounds__(kBwdThreads<NT>) void block_norm_bwd_kernel(const B
       if (p.post) {
         float y[8];
         y_of(k, y);
+        if (__builtin_expect(apart1, 0)) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] = __builtin_fmaf(a1, y[j] * r1, r1 * u[j]);
+          for (int j = 0; j < 8; ++j) {
+            y[j] *= far_power(r1);
+            u[j] *= far_power(r1);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = __builtin_fmaf(a1, y[j] * fabsf(r1), fabsf(r1) * u[j]);
       }
       store8<E, S, PAST>(row_of<E>(p.dy, t, p.dy_s), c, C, u);
     }

@@ -137,6 +137,20 @@ __device__ __forceinline__ void store8(void* p, int c, int C, const float x[8]) 
 // no subnormal numbers): of values below 1e-15 with an eps below 1e-30, or above 1e15.
 __device__ __forceinline__ bool far_mean(float v) { return !(v >= 1e-30f && v <= 1e30f); }
 
+// 1 / sqrt of such a row's mean from `mean`, that of its values times `power` (2^100 or 2^-100).  Where
+// it is no normal number (values below 2^-127 or above 2^126) power and root stay apart, as infinity
+// times 0 would be no number: minus the root, and the values take far_power of it.
+__device__ __forceinline__ float far_root(float mean, float power) {
+  const float root = __builtin_amdgcn_rsqf(mean), r = root * power;
+  return r >= 0x1p-126f && r < kInf ? r : -root;
+}
+__device__ __forceinline__ bool power_apart(float r) {               // (of a value that all lanes have)
+  return static_cast<int32_t>(uniform(__float_as_uint(r))) < 0;
+}
+__device__ __forceinline__ float far_power(float r) {
+  return r >= 0.f ? 1.f : r < -1.f ? 0x1p100f : 0x1p-100f;
+}
+
 template <typename E>
 struct Chunk;
 template <>
