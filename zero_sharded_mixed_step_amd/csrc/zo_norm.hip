@@ -132,14 +132,15 @@ __device__ __forceinline__ float sum_row(float x) {
   return join_lanes<G>(x, AddOp());
 }
 
-// 1 / sqrt(mean(x^2) + eps) of such a row, from x times a power of 2.
+// 1 / sqrt(mean(x^2) + eps) of such a row, from x times a power of 2 (see far_root: less than 0 where
+// x has to take the power itself).
 template <int G>
 __device__ __forceinline__ float far_inverse_rms(const float x[8], float v, float inv_d, float eps) {
   const float s = v < 1.f ? 0x1p100f : 0x1p-100f;
   float sum = 0.f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(x[j] * s, x[j] * s, sum);
-  return s * __builtin_amdgcn_rsqf(__builtin_fmaf(sum_row<G>(sum), inv_d, eps * s * s));
+  return far_root(__builtin_fmaf(sum_row<G>(sum), inv_d, eps * s * s), s);
 }
 
 template <typename E>
@@ -191,6 +192,11 @@ __global__ __launch_bounds__(kNormThreads) void norm_fwd_kernel(const NormParams
         if (__any(h < a.H && far_mean(ms))) {             // (by the wave)
           const float fr = far_inverse_rms<G>(x, ms, inv_d, p.eps);
           r = far_mean(ms) ? fr : r;
+        }
+        if (__any(r < 0.f)) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] *= far_power(r);
+          r = fabsf(r);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j];
@@ -256,10 +262,18 @@ __global__ __launch_bounds__(kNormThreads) void norm_bwd_kernel(const NormParams
           const float fr = far_inverse_rms<G>(x, ms, inv_d, p.eps);
           float t = 0.f;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) t = __builtin_fmaf(u[j], x[j] * fr, t);
+          for (int j = 0; j < 8; ++j) t = __builtin_fmaf(u[j], x[j] * far_power(fr) * fabsf(fr), t);
           t = sum_row<G>(t);
           r = far_mean(ms) ? fr : r;
-          k = far_mean(ms) ? t * inv_d * fr : k;
+          k = far_mean(ms) ? t * inv_d * far_power(fr) * fabsf(fr) : k;
+        }
+        if (__any(r < 0.f)) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            x[j] *= far_power(r);
+            u[j] *= far_power(r);
+          }
+          r = fabsf(r);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
