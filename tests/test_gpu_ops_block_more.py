@@ -104,3 +104,55 @@ def test_block_norm_rows_at_the_ends(zs, torch, C, types, size):
         both(_rand(torch, g, (T, C), rt), _ends(torch, g, T, C, dt, size), True, gate,
              2.0 ** -60 if small else 1.0, _rand(torch, g, (T, C), rt))
     assert bool((behind == 0xFF).all())
+
+
+# |lse| up to which the backward's probabilities are formed from it, beyond from the token's logit
+FAR_LSE = {"f32": 32.0, "bf16": 2048.0}
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V,tau", [(300, 1.0), (20011, 0.7)])
+@pytest.mark.parametrize("centre", [0.0, 20.0, -25.0, 45.0, 1000.0, -3000.0, 30000.0, -60000.0, 65000.0, 4e6])
+def test_policy_gradients_keep_their_digits_far_from_0(zs, torch, dtype, V, tau, centre):
+    """A row's gradient depends on differences of its logits alone: the forward's is as good wherever the
+    row lies, the backward's but for the rounding of the statistic that it is formed from."""
+    dt, = _types(torch, dtype)
+    g, N, F = _gen(torch, V + int(abs(centre))), 8, R.F32R
+    z = ((torch.randn(N, V, generator=g) * 2 + centre) * tau).to(dt)
+    act = torch.randint(0, V, (N,), generator=g, dtype=torch.int32)
+    act[:2] = z[:2].float().argmax(1).to(torch.int32)
+    z[2, act[2]] = (centre - 40.0) * tau                       # a token of little probability
+    adv = torch.tensor([1.0, -0.5, 2.0, 0.7, -1.0, 1.5, -2.0, 0.3])
+    x = z.double() / tau
+    lse = torch.logsumexp(x, 1)
+    lp = x.gather(1, act.long()[:, None])[:, 0] - lse
+    old, ref = (lp - 0.05).float(), (lp + 0.3).float()
+    kw = dict(tau=tau, old=old, ref=ref, kl_coef=0.1, grad_scale=0.5)
+    want = B.policy(z, act, adv, **kw)
+    assert want["near"] == 0
+    d = [t.cuda() for t in (z, act, adv, old, ref)]
+    loss, stats = torch.empty(N, device="cuda"), torch.empty(N, 4, device="cuda")
+    dz, back, place = torch.empty_like(d[0]), torch.empty_like(d[0]), d[0].clone()
+    bkw = dict(grad_scale=0.5, temperature=tau)
+    zs.zero_policy_fwd(*d[:3], loss, stats, dlogits=dz, old_logp=d[3], ref_logp=d[4], kl_coef=0.1, **bkw)
+    zs.zero_policy_bwd(d[0], d[1], stats, back, **bkw)
+    zs.zero_policy_bwd(place, d[1], stats, place, **bkw)
+    assert _same(back, place)
+    # Errors of q, relative: of the row's sum (as in ops_block_ref); of an exponent, which is below
+    # `span` and takes three roundings and those of 1 / tau and log2 e; of the power and three products.
+    span = (x.max(1, keepdim=True).values - x).clamp(max=100.0)
+    e = (V / 256 + 64) * F + 4 * F * span.max(1, keepdim=True).values
+    q, one = torch.exp(x - lse[:, None]), torch.zeros_like(x).scatter_(1, act.long()[:, None], 1.0)
+    val, g_row, g_off = want["dz"][0], want["stats"][0][:, 2:3].abs(), want["stats"][1][:, 2:3]
+
+    def bound(eq):
+        off = g_row * (q * eq + one * (1 - q) * 6 * (e + F)) + g_off * (one - q).abs()
+        return R.half_step(dt) * val.abs() + 1.02 * 0.5 / tau * off + B.TINY
+
+    R.check("dz", dz, val, bound(F * (6 * span + 16) + e))
+    # Backward besides: lse's or lp's own rounding, and of the exponent's parts that are as large
+    # (z / tau, or the difference from the token's logit, twice).
+    far = (lse.abs() > FAR_LSE[dtype]) & (lp.abs() < lse.abs())
+    large = torch.where(far, lp.abs(), lse.abs())[:, None]
+    arg = (x - lse[:, None]).abs().clamp(max=200.0)
+    R.check("dz of the backward", back, val, bound(F * (3 * large + 6 * arg + 16) + e))

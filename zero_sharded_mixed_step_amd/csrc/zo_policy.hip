@@ -37,7 +37,7 @@ struct PolicyParams {
   float *loss, *stats;
   void* dz;
   int64_t z_stride, dz_stride;
-  int seg;                                          // backward: chunks of a piece
+  int seg, in_place;                                // backward: chunks of a piece
   int kept;                                         // forward: chunks in shared memory
 };
 
@@ -375,8 +375,13 @@ __global__ __launch_bounds__(NT, CH <= 8 ? 8 : 4) void policy_fwd_kernel(const P
 }
 
 // Backward from saved statistics: a piece of a row to a workgroup.  q_j = exp(z_j / tau - lse), or
-// exp((z_j - z_a) / tau + lp) where lse is so large that its rounding shows: then one workgroup has the
-// whole row, as the gradient may be written over z_a.
+// exp((z_j - z_a) / tau + lp) where lse is so large that its rounding and those of z_j / tau, some
+// 2^-24 of it each, would show beside the gradient's own: 2^-19 of an fp32 q at 32 (where its own exponential
+// is off by as much), an eighth of a rounding to bf16 at 2048.  In place one workgroup then has the
+// whole row, as the gradient is written over z_a (1024 x 131072 fp32 about 100, so that all rows are such: 277
+// us, about 0 188; to another place 168 and 168).
+template <typename E>
+constexpr float kFarLse = sizeof(E) == 4 ? 0x1p5f : 0x1p11f;
 template <typename E, int NT>
 __global__ __launch_bounds__(NT) void policy_bwd_kernel(const PolicyParams p) {
   constexpr int kN = Chunk<E>::kN;
@@ -394,12 +399,14 @@ __global__ __launch_bounds__(NT) void policy_bwd_kernel(const PolicyParams p) {
   const bool live = c != 0.f;
   const float inv_tau = static_cast<float>(p.inv_tau);
   float shift = 0.f, base = lse;
-  if (live && fabsf(lse) > 0x1p16f && fabsf(lp) < fabsf(lse)) {
-    if (blockIdx.x > 0) return;
-    c1 = in.chunks();
+  if (live && fabsf(lse) > kFarLse<E> && fabsf(lp) < fabsf(lse)) {
+    if (p.in_place) {
+      if (blockIdx.x > 0) return;
+      c1 = in.chunks();
+    }
     shift = static_cast<float>(in.p[action]);
     base = -lp;
-    __syncthreads();
+    if (p.in_place) __syncthreads();
   }
   const auto prob = [&](float z) { return exp2_hw(__builtin_fmaf(z - shift, inv_tau, -base) * kLog2e); };
   constexpr int kAtOnce = 4;                           // loads under way, a thread
@@ -512,6 +519,7 @@ hipError_t launch_policy(const zero_policy_args& a, bool forward, hipStream_t s)
   p.dz = a.dlogits;
   p.z_stride = a.logits_stride;
   p.dz_stride = a.dlogits_stride;
+  p.in_place = a.logits == a.dlogits;
   if (forward) return a.dtype == ZERO_BF16 ? pick_fwd<bf16>(p, s) : pick_fwd<float>(p, s);
   return a.dtype == ZERO_BF16 ? run_bwd<bf16>(p, s) : run_bwd<float>(p, s);
 }
