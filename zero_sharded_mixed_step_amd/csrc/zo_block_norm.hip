@@ -701,7 +701,9 @@ int bwd_groups(int64_t T, int C) {
 
 // From here on outputs go past the caches, which do not hold them until they are read.  (T x 4096 bf16,
 // us, with both outputs' readers behind it: T = 16384 forward 171 instead of 191, backward 229 instead of 243;
-// 12288, 192 MiB, 131 and 131, 174 and 179; 8192 92 instead of 86, 122 instead of 113.)
+// 12288, 192 MiB, 131 and 131, 174 and 179; 8192 92 instead of 86, 122 instead of 113.  The gradient of a
+// gate by token does not count: with its reader too, backward at 8192, 10240 and 11264, 192 to 264 MiB of all three,
+// past them 234, 280 and 304, through them 204, 269 and 298.)
 constexpr int64_t kPastBytes = int64_t(192) << 20;
 
 template <typename E, typename R, int NT, int CH>
