@@ -15,6 +15,11 @@ loss and a KL term to the initial student.  The gradients of all parameters are
 views of one vector; their global norm and clipping (zero_grads_norm, zero_grads_clip)
 write the bf16 replica that `ShardStep` reduces.  Plain matrix products are torch's.
 
+One rank trains here, whose gradient is the whole one.  With several, every rank's gradient goes to
+the step unclipped: the norm to clip by is that of the reduced gradient, whose shards' accumulators
+add up (zero_grad_norm of each rank's shard, or zero_grads_norm of its pieces), and the
+step clips by it itself.
+
   python examples/policy_student.py [--steps 40]
 """
 import argparse
@@ -181,8 +186,9 @@ def sample(student, param, ref, tokens, generator):
                 weight=torch.full((n,), 1.0 / n, device="cuda")), float(reward.mean())
 
 
-def train(steps=40, updates=4, B=8, T=64, log=print):
-    """Rollouts of `updates` updates each; the mean rewards."""
+def train(steps=40, updates=4, B=8, T=64, log=print, state=None):
+    """Rollouts of `updates` updates each; the mean rewards.  `state`, a dict, gets the student, its
+    step and the norm of the last gradient."""
     student = Student(B, T)
     step = zs.ShardStep(student.n, 1, BF, lr=2e-2, beta2=0.95)
     step.master.copy_(student.initial(1))
@@ -207,6 +213,8 @@ def train(steps=40, updates=4, B=8, T=64, log=print):
         rewards.append(reward)
         if s % 10 == 0 or s == steps - 1:
             log("step %3d  reward %.4f  gradient norm %.4f" % (s, reward, float(norm)))
+    if state is not None:
+        state.update(student=student, step=step, norm=norm)
     return rewards
 
 

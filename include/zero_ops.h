@@ -384,8 +384,10 @@ int zero_policy_bwd(const zero_policy_args *args, void *stream);
  *
  * zero_grads_norm: the norm state of g = grads * inv_scale (binary32) of all the
  * tensors into `acc`, which is overwritten, or added to with `add`: bit for bit what
- * zero_grad_norm adds for the tensors one by one, so it may be summed over ranks and
- * given to zero_adamw_step.  At most 2^37 elements in an accumulator.
+ * zero_grad_norm adds for the tensors one by one, so it may be given to zero_adamw_step,
+ * and summed over ranks that each hold a part of one gradient: its shards after the
+ * reduction (the sum over ranks' gradients before it is not the reduced gradient's norm).
+ * At most 2^37 elements in an accumulator.
  *
  * zero_grads_clip: outs[i] = (grads[i] * inv_scale) * coef, rounded to out_dtypes[i],
  * with the skip and the coefficient that zero_step_gate derives from the n_accs

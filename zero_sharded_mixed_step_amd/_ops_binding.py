@@ -752,7 +752,8 @@ def zero_grads_norm(table, acc, *, inv_scale=1.0, add=False, workspace=None,
                     stream=None) -> None:
     """The norm state of grads * inv_scale of a GradTable's tensors into the accumulator acc
     (new_norm_acc(1)), added to what it holds if `add`: as zero_grad_norm's of the tensors one
-    by one, so that it may be summed over ranks or given to zero_adamw_step.  workspace:
+    by one, so that it may be given to zero_adamw_step, or summed over ranks that each hold a
+    shard of the reduced gradient.  workspace:
     zero_grads_workspace_bytes() bytes."""
     dev = _device()
     grads, _, sizes, types, _ = table._checked(dev, False)
