@@ -156,3 +156,56 @@ def test_policy_gradients_keep_their_digits_far_from_0(zs, torch, dtype, V, tau,
     large = torch.where(far, lp.abs(), lse.abs())[:, None]
     arg = (x - lse[:, None]).abs().clamp(max=200.0)
     R.check("dz of the backward", back, val, bound(F * (3 * large + 6 * arg + 16) + e))
+
+
+@pytest.mark.parametrize("C", [64, 1000, 4096])
+@pytest.mark.parametrize("T", [20011, 262144])
+def test_block_norm_sums_of_one_sign(zs, torch, T, C):
+    """Weights' and gate's gradients whose terms all have one sign.  A thread adds the rows of its
+    workgroup that it walks, of 256 workgroups at least and up to four rows of each at a time; then come
+    four rows' parts, 32 workgroups' in order and 16 waves'."""
+    T = min(T, (1 << 25) // C)
+    F, f32 = R.F32R, torch.float32
+    g = torch.Generator(device="cuda")
+    g.manual_seed(C)
+    r = lambda *s: torch.rand(*s, generator=g, device="cuda") + 0.25
+    y, h, dh, dz, w, gate = r(T, C), r(T, C), r(T, C), r(T, C), r(C), r(C)
+    dw1, dgate, dw2 = (torch.full((C,), math.nan, device="cuda") for _ in range(3))
+    ws = torch.empty(zs.zero_block_norm_workspace_bytes(T, C), dtype=torch.uint8, device="cuda")
+    kw = dict(post_norm=True, post_weight=w, gate=gate, eps=0.0, workspace=ws)
+    zs.zero_block_norm_bwd(y, None, dh, None, None, None, dpost_weight=dw1, dgate=dgate, **kw)
+    zs.zero_block_norm_bwd(None, h, None, dz, dh, None, pre_weight=w, dpre_weight=dw2, eps=0.0, workspace=ws)
+    # (in pieces: 64-bit copies of everything would be 16 times as large)
+    t = torch.zeros(C, dtype=torch.float64, device="cuda")
+    s = t.clone()
+    g.manual_seed(C)
+    y, h, dh = r(T, C), r(T, C), r(T, C)
+    for i in range(0, T, 16384):
+        a, b = y[i:i + 16384].double(), h[i:i + 16384].double()
+        t += (dh[i:i + 16384].double() * a / a.square().mean(1, keepdim=True).sqrt()).sum(0)
+        s += (dz[i:i + 16384].double() * b / b.square().mean(1, keepdim=True).sqrt()).sum(0)
+    chain = T / (256 * (4 if C <= 1024 else 1)) + 1 + 4 + 32 + 16
+    for name, got, want in (("dw1", dw1, t * gate.double()), ("dgate", dgate, t * w.double()), ("dw2", dw2, s)):
+        off = float(((got.double() - want) / want).abs().max())
+        assert off <= (chain + 10) * F + B.E_ROOT, (name, off / F, chain)
+
+
+@pytest.mark.parametrize("grad", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [300, 16390, 1 << 17, 1 << 20])
+def test_embed_sums_of_one_sign(zs, torch, N, grad):
+    """All tokens one row, all terms of one sign: 64 places of a chunk in order at most, every 16th
+    of the chunks', the 16 waves'."""
+    gt, = _types(torch, grad)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(N)
+    C = 24
+    d = torch.rand(N, C, generator=g, device="cuda") + 0.25
+    ids = torch.full((N,), 2, dtype=torch.int32, device="cuda")
+    got = torch.full((5, C), math.nan, dtype=gt, device="cuda")
+    zs.zero_embed_bwd(ids, d, got, workspace=_ws(torch, zs.zero_embed_workspace_bytes(N, C))[0])
+    want = d.double().sum(0)
+    places = max(4, min(64, (N + 255) // 256))
+    chain = places + N / places / 16 + 1 + 16
+    off = float(((got[2].double() - want) / want).abs().max())
+    assert off <= (chain + 3) * R.F32R + R.half_step(gt), (off / R.F32R, chain)
+    assert bool((got[[0, 1, 3, 4]] == 0).all())
