@@ -354,8 +354,9 @@ size_t zero_block_norm_workspace_bytes(int64_t T, int C);
  * above 32 (2048 for ZERO_BF16) and lp nearer to 0, lp's.  dlogits may be the logits themselves
  * (same stride; in place the backward gives such a row to one workgroup).  dtype is that of logits and dlogits.  1e-30 <= tau <= 1e30 (and
  * z_j / tau within binary32, or the row's results are NaN), 0 <= clip_low <= 1,
- * clip_high >= 0, N <= 2^21, V <= ZERO_POLICY_MAX_V; logits may start at any
- * element. */
+ * clip_high >= 0, N <= 2^21, V <= ZERO_POLICY_MAX_V; logits and dlogits may start at any
+ * element (a row of dlogits that starts elsewhere between 16 bytes than the row of
+ * logits is stored element by element, in about twice the time). */
 typedef struct zero_policy_args {
   size_t struct_bytes;          /* sizeof(zero_policy_args) */
   int64_t N, V;

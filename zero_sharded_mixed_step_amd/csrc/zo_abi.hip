@@ -548,8 +548,8 @@ const char* zero_ops_strerror(int status) {
     case ZERO_OK: return "ok";
     case ZERO_EINVAL:
       return "invalid argument (null pointer, struct size, dtype, head counts, scale, cap, "
-             "temperature, clipping, bias map, weight or gradient without its input, rows that "
-             "overlap, in place with other strides or dtypes, or missing workspace)";
+             "temperature, clipping, bias map, weight or gradient without its input, rows or "
+             "arrays that overlap, in place with other strides or dtypes, or missing workspace)";
     case ZERO_EALIGN:
       return "pointer or stride misaligned (rows, their weights, accumulators and workspaces need "
              "16 bytes, ranges 8, other arrays their element)";

@@ -8,9 +8,9 @@
 // workgroups walk the rows and leave their sums in a row of the workspace, which a second kernel
 // folds in order.
 //
-// Measured, bf16 with both norms and a gate by channel: forward of 16384 x 4096 94 us, 5.7 TB/s
-// (all past the caches; written through them 98, read too 102); backward of 8192 x 4096 84 us, 4.8 TB/s, the
-// fold 5 of them (loads through the caches 90; four barriers a row and the gate's sums of their own,
+// Measured, bf16 with both norms and a gate by channel: forward of 16384 x 4096 91 to 94 us, 5.7 to
+// 5.9 TB/s (all past the caches; written through them 98, read too 102); backward of 8192 x 4096 84 us, 4.8 TB/s,
+// the fold 5 of them (loads through the caches 90; four barriers a row and the gate's sums of their own,
 // twice the instructions: 104).  4097 x 1000, fp32 stream and a gate by token: backward 25 us.  8192 x
 // 8192 backward 153 us, 5.3 TB/s; 4096 x 16384, where less is held, 192 us, 4.2 TB/s.
 #include <algorithm>

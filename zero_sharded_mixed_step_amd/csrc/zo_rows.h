@@ -222,7 +222,9 @@ struct Row {
     }
     return x;
   }
-  // y as this row's elements that chunk c of a row shifted by `from` holds
+  // y as this row's elements that chunk c of a row shifted by `from` holds: one by one where this row
+  // is shifted otherwise (a gradient whose rows start elsewhere between 16 bytes than the logits':
+  // 8192 x 50257 bf16 626 us for 313)
   template <bool ONCE = false>
   __device__ __forceinline__ void store(int c, int from, const float y[kN]) const {
     const int64_t e0 = static_cast<int64_t>(c) * kN - from;
