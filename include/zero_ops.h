@@ -352,7 +352,8 @@ size_t zero_block_norm_workspace_bytes(int64_t T, int C);
  * the logits for all three); zero_policy_bwd writes dlogits from stats (lse, lp
  * and g, whatever loss they came from).  Its q_j carry lse's rounding, or, where |lse| is
  * above 32 (2048 for ZERO_BF16) and lp nearer to 0, lp's.  dlogits may be the logits themselves
- * (same stride; in place the backward gives such a row to one workgroup).  dtype is that of logits and dlogits.  1e-30 <= tau <= 1e30 (and
+ * (same stride; in place the backward gives such a row to one workgroup).  dtype is
+ * that of logits and dlogits.  1e-30 <= tau <= 1e30 (and
  * z_j / tau within binary32, or the row's results are NaN), 0 <= clip_low <= 1,
  * clip_high >= 0, N <= 2^21, V <= ZERO_POLICY_MAX_V; logits and dlogits may start at any
  * element (a row of dlogits that starts elsewhere between 16 bytes than the row of

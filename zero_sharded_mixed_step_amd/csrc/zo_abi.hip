@@ -7,7 +7,6 @@
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
-#include <utility>
 #include <vector>
 
 #include "zero_ops.h"

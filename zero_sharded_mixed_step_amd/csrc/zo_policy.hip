@@ -16,9 +16,10 @@
 // bf16: 310 us, through them 322; 2048 x 50257: 72, 93), and with the gradient's reader behind it as long
 // as before (587 and 587, 162 and 161).
 //
-// Measured: 8192 x 50257 bf16, the loss alone 187 us, 4.4 TB/s, with the gradient 312 us, 5.3 TB/s of logits
-// read and gradient written, where the gradient starts elsewhere between 16 bytes than the logits 626 (350 with the library's logarithms and exponentials in binary64, which one thread
-// works on while the row waits); the backward alone, 1024 x 131072 fp32, 162 us, 6.6 TB/s (172 with
+// Measured: 8192 x 50257 bf16, the loss alone 187 us, 4.4 TB/s, with the gradient 312 us, 5.3 TB/s of
+// logits read and gradient written (350 with the library's logarithms and exponentials in binary64,
+// which one thread works on while the row waits; 626 where the gradient's rows start elsewhere between 16
+// bytes than the logits'); the backward alone, 1024 x 131072 fp32, 160 to 164 us, 6.6 TB/s (172 with
 // loads through the caches).
 #include <algorithm>
 
